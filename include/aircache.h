@@ -519,6 +519,237 @@ typedef struct aircache_quant_problem {
 
 AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t* status, void* stream);
 
+/* -------------------------------------------------------------- paged cache */
+
+/*
+ * One layer's cache of a running batch, kept in pages of `page_rows` rows so
+ * that sequences can grow and shrink without moving: row i of sequence s lies
+ * in page table[s][i / page_rows] at row i % page_rows.  (The KV-cache tutorial
+ * page's append K_{1:t} = [K_{1:t-1}; k_t], and the compressed rows of
+ * aircache_compact, with the rows' storage split.)  Three entry points work on
+ * it: aircache_rotate appends rows, aircache_paged_decode attends over them
+ * and adds the weight that each row gets to its mass, aircache_evict drops the
+ * rows of least mass.
+ *
+ *   k, v    [num_pages][page_rows][h_kv][head_dim], element strides
+ *           stride_page, stride_row, stride_head (the same for k and v; a
+ *           fused [num_pages][2][page_rows].. buffer works through them);
+ *           bf16, or int8 codes with one fp32 scale per row and KV head
+ *           (row = scale * code, scale >= 0).
+ *   table   device int32 [num_seqs], rows table_stride apart, max_pages used.
+ *           Only the entries of a sequence's own rows are read.
+ *   lens    device int32 [num_seqs]: rows of each sequence.
+ *   k_scale, v_scale, mass (fp32), order (int32): [num_pages][h_kv][page_rows], dense.
+ *   mass    optional: attention weight a row has been given so far by its KV
+ *           head's query heads.
+ *   order   optional: the number of tokens appended to the sequence before the
+ *           row's own (0 for its first).  Eviction moves rows, so a row's place
+ *           says nothing about its age; this does.
+ * Attention does not depend on the order of the rows, and keys are stored
+ * rotated, so no other operation needs their positions.
+ *
+ * Two sequences may share pages (a common prefix) as long as only
+ * aircache_paged_decode without mass_out reads them; a page that a call writes
+ * to (appended rows, mass, eviction) belongs to one sequence.
+ * Requirements (else AIRCACHE_ERR_INVALID_ARG): 0 <= num_seqs <= 65535,
+ * head_dim 64 or 128, kv_dtype AIRCACHE_BF16 or AIRCACHE_INT8 (with both
+ * scales), page_rows a multiple of 16 in 16..4096, max_pages >= 1 with
+ * max_pages * page_rows <= 2^31 - 2^16, 1 <= num_pages <= 2^31 - 1, table_stride >=
+ * max_pages; k and v 16-byte aligned, strides positive multiples of 16 bytes.
+ * Device-side, a length outside [0, max_pages * page_rows] or a page outside
+ * [0, num_pages) sets AIRCACHE_ERR_DEVICE_BOUNDS; nothing is then read or
+ * written through it (each entry point says what becomes of the sequence).
+ */
+typedef struct aircache_pages {
+    int32_t num_seqs;
+    int32_t h_kv;
+    int32_t head_dim;
+    int32_t kv_dtype;
+    int32_t page_rows;
+    int32_t max_pages;
+    int64_t num_pages;
+    void* k;
+    void* v;
+    int64_t stride_page;
+    int64_t stride_row;
+    int64_t stride_head;
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* lens;
+    float* k_scale;  /* AIRCACHE_INT8 only */
+    float* v_scale;
+    float* mass;     /* optional */
+    int32_t* order;  /* optional */
+} aircache_pages;
+
+/*
+ * Norms of queries and keys for each head, the rotation by position and the
+ * append to the cache, in one pass over a batch's projections: the step before
+ * aircache_prefill, aircache_compress, aircache_decode and
+ * aircache_paged_decode, whose queries and keys are post-rotation.  For token t
+ * and each query or key head x of it:
+ *   x' = x / sqrt(mean(x^2) + eps) * weight          (with a weight; else x' = x)
+ *   the first rotary_dim elements are turned in pairs (a, b) by the angle
+ *   position * inv_freq[i]:  (a cos - b sin, b cos + a sin), the rest stay;
+ *   pair i is (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved.
+ * Everything is fp32 and is rounded once, to bf16 or to the int8 code.
+ *
+ * turns [rotary_dim/2][2] fp32: inv_freq[i] / (2 pi) as a sum hi + lo of two
+ * floats, so that the angle of a far position keeps its bits (the product with
+ * the position is formed exactly and reduced to a part of a turn before it is
+ * rounded).  positions int32 [axes][num_tokens]; with axes == 3 (the time, row
+ * and column of an image's tokens) the first section0 frequencies go by axis
+ * 0, the next section1 by axis 1 and the rest by axis 2.  Without positions a
+ * token's position is its order (see below).
+ *
+ * Tokens cu_tokens[s] .. cu_tokens[s+1]-1 belong to sequence s; tokens at or
+ * behind cu_tokens[num_seqs] are padding, whose outputs are left as they are.
+ * With a cache (pages != NULL), lens[s] counts the rows of s AFTER the append:
+ * the n tokens of s become its rows lens[s]-n .. lens[s]-1, with mass 0 (if
+ * the cache has mass) and order seen[s]-n .. seen[s]-1 (if it has order), where
+ * seen[s] is the number of tokens appended to s so far, these n among them.  int8 caches get s = max |y| / 127 of the
+ * row's head in fp32 and codes round(y / s), half away from zero (0 for a row
+ * of zeros).  Without a cache cu_tokens may be NULL (no padding) and positions
+ * must be given.
+ * q_out may be q and k_out may be k (the same pointer and strides: in place).
+ *
+ * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; head_dim
+ * 64 or 128; at least one of q, k; q_out with q; k_out or pages with k; v
+ * exactly with pages; rotary_dim 0 or a multiple of 16 up to head_dim, turns
+ * when it is not 0; axes 1 or 3, sections >= 0 with a sum of rotary_dim/2 when
+ * axes is 3; eps >= 0; seen when pages has order or positions is NULL (with
+ * rotary_dim > 0); pointers 16-byte aligned, strides multiples of 8 elements.
+ * A token whose row or page is out of bounds sets AIRCACHE_ERR_DEVICE_BOUNDS
+ * in *status (optional device int32, not cleared by the call) and is not
+ * appended; its q_out and k_out are written.  One kernel.
+ */
+typedef struct aircache_rotate_problem {
+    int64_t num_tokens;   /* rows of q, k, v: 0..2^31-1 */
+    int32_t num_seqs;
+    int32_t h_q;
+    int32_t h_kv;
+    int32_t head_dim;
+    int32_t dtype;
+    int32_t rotary_dim;
+    int32_t interleaved;  /* 0 or 1 */
+    int32_t axes;
+    int32_t section0;
+    int32_t section1;
+    float eps;
+    int32_t reserved0;    /* 0 */
+    const void* q;        /* [num_tokens][h_q][head_dim] */
+    const void* k;        /* [num_tokens][h_kv][head_dim] */
+    const void* v;
+    int64_t q_stride_tok, q_stride_head;
+    int64_t k_stride_tok, k_stride_head;
+    int64_t v_stride_tok, v_stride_head;
+    void* q_out;
+    void* k_out;
+    int64_t qo_stride_tok, qo_stride_head;
+    int64_t ko_stride_tok, ko_stride_head;
+    const void* q_weight;  /* optional bf16 [head_dim] */
+    const void* k_weight;
+    const float* turns;
+    const int32_t* positions;
+    const int32_t* cu_tokens;  /* device [num_seqs + 1], non-decreasing, from 0 */
+    const int32_t* seen;       /* device [num_seqs] */
+    const aircache_pages* pages;  /* HOST; num_seqs, h_kv and head_dim as here */
+} aircache_rotate_problem;
+
+AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* status, void* stream);
+
+/*
+ * One decode step over a paged cache: for sequence s, query head h (KV head
+ * h / (h_q / h_kv)) and its rows j < lens[s]
+ *   out[s][h] = sum_j w_j v_j,  w_j = softmax_j(scale * q[s][h] . k_j)
+ *   lse[s][h] = log sum_j exp(scale * q[s][h] . k_j)        (optional)
+ *   mass_out[row j][KV head] = mass[..] + the sum of w_j over the KV head's
+ *   query heads                                              (optional)
+ * A sequence without rows gets out = 0 and lse = -inf.  out is bf16, lse fp32
+ * dense [num_seqs][h_q]; mass_out is pages->mass itself (in place) or another
+ * array of its shape, where only the slots of attended rows are written.
+ *
+ * The work is split by rows, not by sequences: every CTA takes the same number
+ * of 64-row tiles of the batch's (sequence, KV head) list, whatever the lengths,
+ * and the parts of one (sequence, KV head) are joined by the last of its CTAs,
+ * in a fixed order.  With mass_out a second kernel turns the logits, which the
+ * first leaves in the workspace, into weights.
+ *
+ * total_rows bounds the sum of lens; it sizes the grid and the workspace.  A
+ * larger sum sets AIRCACHE_ERR_CAPACITY and nothing is computed.  A sequence
+ * with a length or page out of bounds sets AIRCACHE_ERR_DEVICE_BOUNDS; a bad
+ * length counts as 0, a bad page's rows count as not there.
+ * Requirements: dtype AIRCACHE_BF16; h_q a multiple of h_kv (else
+ * AIRCACHE_ERR_INVALID_ARG) with at most 16 query heads to a KV head (else
+ * AIRCACHE_ERR_UNSUPPORTED); 1 <= total_rows <= 2^31 - 2^16; scale > 0 and finite; q 16-byte
+ * aligned and its strides multiples of 8; out 16-byte aligned, dense; mass_out
+ * only with pages->mass.
+ *
+ * The workspace is caller-owned, 256-byte aligned, ZEROED ONCE before its first
+ * use and left ready for the next call, as aircache_decode's; a device error
+ * stays recorded until the caller zeroes it.
+ */
+typedef struct aircache_paged_decode_problem {
+    const aircache_pages* pages;  /* HOST */
+    int32_t h_q;
+    int32_t dtype;
+    float scale;
+    int32_t reserved0;    /* 0 */
+    int64_t total_rows;
+    const void* q;        /* [num_seqs][h_q][head_dim] */
+    int64_t q_stride_seq;
+    int64_t q_stride_head;
+    void* out;            /* [num_seqs][h_q][head_dim] bf16, dense */
+    float* lse;           /* optional */
+    float* mass_out;      /* optional */
+} aircache_paged_decode_problem;
+
+AIRCACHE_API size_t aircache_paged_decode_workspace_size(const aircache_paged_decode_problem* p);
+AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size_t ws_bytes,
+                                       void* stream);
+
+/*
+ * Eviction by accumulated attention weight: of the n = lens[s] rows of sequence
+ * s, every KV head keeps keep[s] (all if n <= keep[s]): first its protected rows
+ * (order < sink, or order >= seen[s] - recent), then those of largest mass, ties to
+ * the lower row (a NaN counts as -inf).  Kept rows that lie at keep[s] or behind move, in ascending
+ * order, into the vacated rows below keep[s], in ascending order, and take
+ * their scales, mass and order along; every other row stays where it is, so as
+ * few bytes as possible move.  lens_out[s] = min(n, keep[s]); pages past
+ * ceil(lens_out[s] / page_rows) are the caller's again.
+ *
+ * mass_out and order_out are pages->mass and pages->order (in place) or other
+ * arrays of their shape, which then get the entries of all rows below
+ * lens_out[s] and nothing else.  lens is read by every KV head and lens_out
+ * must be another array (several layers are cut by the same lens before it
+ * takes lens_out's values).
+ *
+ * max_rows bounds lens; it sizes the workspace and the launch, and is at most
+ * AIRCACHE_MAX_EVICT_ROWS (else AIRCACHE_ERR_UNSUPPORTED).  A sequence with a
+ * length outside [0, max_rows], a page out of bounds, keep[s] < 0, or n > keep[s] < sink + recent
+ * sets AIRCACHE_ERR_DEVICE_BOUNDS and keeps its rows, mass and order
+ * (lens_out[s] = lens[s]).
+ * Requirements (else AIRCACHE_ERR_INVALID_ARG): mass; order when sink or recent
+ * is not 0, seen when recent is not 0; order_out exactly with order; sink, recent >= 0.  Workspace as
+ * for aircache_paged_decode.  One kernel.
+ */
+#define AIRCACHE_MAX_EVICT_ROWS 393216
+
+typedef struct aircache_evict_problem {
+    const aircache_pages* pages;  /* HOST */
+    const int32_t* keep;      /* device [num_seqs] */
+    const int32_t* seen;      /* device [num_seqs] */
+    int32_t* lens_out;        /* device [num_seqs] */
+    float* mass_out;
+    int32_t* order_out;
+    int32_t sink;
+    int32_t recent;
+    int64_t max_rows;
+} aircache_evict_problem;
+
+AIRCACHE_API size_t aircache_evict_workspace_size(const aircache_evict_problem* p);
+AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

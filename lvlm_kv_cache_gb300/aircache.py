@@ -106,6 +106,55 @@ class QuantProblemStruct(ctypes.Structure):
     ]
 
 
+class PagesStruct(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32), ("page_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("stride_page", ctypes.c_int64), ("stride_row", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+        ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("mass", ctypes.c_void_p), ("order", ctypes.c_void_p),
+    ]
+
+
+class RotateProblemStruct(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64), ("num_seqs", ctypes.c_int32), ("h_q", ctypes.c_int32),
+        ("h_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("axes", ctypes.c_int32),
+        ("section0", ctypes.c_int32), ("section1", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved0", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("q_stride_tok", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("k_stride_tok", ctypes.c_int64), ("k_stride_head", ctypes.c_int64),
+        ("v_stride_tok", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("qo_stride_tok", ctypes.c_int64), ("qo_stride_head", ctypes.c_int64),
+        ("ko_stride_tok", ctypes.c_int64), ("ko_stride_head", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+        ("pages", ctypes.POINTER(PagesStruct)),
+    ]
+
+
+class PagedDecodeProblemStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.POINTER(PagesStruct)), ("h_q", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("reserved0", ctypes.c_int32), ("total_rows", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("q_stride_seq", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("mass_out", ctypes.c_void_p),
+    ]
+
+
+class EvictProblemStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.POINTER(PagesStruct)), ("keep", ctypes.c_void_p), ("seen", ctypes.c_void_p),
+        ("lens_out", ctypes.c_void_p), ("mass_out", ctypes.c_void_p), ("order_out", ctypes.c_void_p),
+        ("sink", ctypes.c_int32), ("recent", ctypes.c_int32), ("max_rows", ctypes.c_int64),
+    ]
+
+
 def lib():
     """The loaded CUDA library (raises if it was not built)."""
     global _lib
@@ -160,6 +209,18 @@ def lib():
         L.aircache_decode_splits.restype = i32
         L.aircache_decode.argtypes = [DP, vp, sz, vp]
         L.aircache_decode.restype = i32
+        L.aircache_rotate.argtypes = [ctypes.POINTER(RotateProblemStruct), vp, vp]
+        L.aircache_rotate.restype = i32
+        PD = ctypes.POINTER(PagedDecodeProblemStruct)
+        L.aircache_paged_decode_workspace_size.argtypes = [PD]
+        L.aircache_paged_decode_workspace_size.restype = sz
+        L.aircache_paged_decode.argtypes = [PD, vp, sz, vp]
+        L.aircache_paged_decode.restype = i32
+        EV = ctypes.POINTER(EvictProblemStruct)
+        L.aircache_evict_workspace_size.argtypes = [EV]
+        L.aircache_evict_workspace_size.restype = sz
+        L.aircache_evict.argtypes = [EV, vp, sz, vp]
+        L.aircache_evict.restype = i32
         _lib = L
     return _lib
 
@@ -586,3 +647,308 @@ def row_index(prob: Problem, out, ws=None, stream=None, check=True):
         if st != OK:
             raise AirCacheError(st, "aircache_row_index (device)")
     return ri
+
+
+# ------------------------------------------------------------------ paged cache
+
+MAX_EVICT_ROWS = 393216
+
+
+def _same_device(*ts):
+    """Every given tensor lies on one CUDA device, which is returned."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("the tensors must be on a CUDA device")
+        if dev is not None and t.device != dev:
+            raise ValueError("the tensors must be on one device")
+        dev = t.device
+    return dev
+
+
+def _dense(t, dtype, shape, name):
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)}")
+
+
+def _run_paged(prob, ws, stream, call, where):
+    """`call(stream)` on the problem's device, whichever the current one is.
+    An empty batch (whose tensors have no storage) needs no call."""
+    if prob.empty:
+        return
+    if ws is not None and ws.device != prob.device:
+        raise ValueError("the workspace must be on the problem's device")
+    if torch.cuda.current_device() == prob.device.index:
+        _check(call(_stream(stream)), where)
+    else:
+        with torch.cuda.device(prob.device):
+            _check(call(_stream(stream)), where)
+
+
+class PagedCache:
+    """One layer's cache in pages (aircache_pages in the header).
+
+    k, v: [P, page_rows, H_kv, D] bf16 with equal strides, or int8 codes with
+    k_scale, v_scale [P, H_kv, page_rows] fp32; table: int32 [S, max_pages]
+    (rows may be strided); lens: int32 [S], the rows of each sequence; mass
+    fp32 and order int32 [P, H_kv, page_rows] are optional.  The tensors are
+    the caller's and are updated in place by the calls that write them."""
+
+    def __init__(self, k, v, table, lens, k_scale=None, v_scale=None, mass=None, order=None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v are [P, page_rows, H_kv, D] of one type and one layout, head_dim contiguous")
+        if k.dtype not in (torch.bfloat16, torch.int8):
+            raise TypeError("cached rows are bfloat16 or int8 codes")
+        P, page_rows, h_kv, d = (int(x) for x in k.shape)
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table is an int32 [S, max_pages] tensor with contiguous rows")
+        S, max_pages = (int(x) for x in table.shape)
+        _dense(lens, torch.int32, (S,), "lens")
+        q8 = k.dtype == torch.int8
+        if q8 != (k_scale is not None) or q8 != (v_scale is not None):
+            raise ValueError("int8 codes come with k_scale and v_scale, bf16 rows without")
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale"), (mass, "mass")):
+            _dense(t, torch.float32, (P, h_kv, page_rows), name)
+        _dense(order, torch.int32, (P, h_kv, page_rows), "order")
+        self.device = _same_device(k, v, table, lens, k_scale, v_scale, mass, order)
+        self.k, self.v, self.table, self.lens = k, v, table, lens
+        self.k_scale, self.v_scale, self.mass, self.order = k_scale, v_scale, mass, order
+        self.num_seqs, self.max_pages, self.num_pages, self.page_rows = S, max_pages, P, page_rows
+        self.h_kv, self.d = h_kv, d
+        adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = PagesStruct(
+            num_seqs=S, h_kv=h_kv, head_dim=d, kv_dtype=INT8 if q8 else BF16, page_rows=page_rows,
+            max_pages=max_pages, num_pages=P, k=adr(k), v=adr(v), stride_page=k.stride(0), stride_row=k.stride(1),
+            stride_head=k.stride(2), table=adr(table), table_stride=max(table.stride(0), max_pages), lens=adr(lens),
+            k_scale=adr(k_scale), v_scale=adr(v_scale), mass=adr(mass), order=adr(order))
+
+
+def rotation_table(inv_freq):
+    """The rotation's frequencies as aircache_rotate takes them: fp32
+    [n, 2], inv_freq / (2 pi) as a sum of two floats.  inv_freq: fp64 tensor or
+    sequence of n angular frequencies (radians per position)."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64)
+    turns = f / (2 * math.pi)
+    hi = turns.to(torch.float32)
+    return torch.stack((hi, (turns - hi.to(torch.float64)).to(torch.float32)), dim=-1).contiguous()
+
+
+class RotateProblem:
+    """Per-head norms, rotation and append of one layer's projections (see
+    aircache_rotate in the header).
+
+    q: [T, H_q, D], k and v: [T, H_kv, D] bf16 (any strides that are multiples
+    of 8 with D contiguous, such as views of one fused projection); q_out,
+    k_out: bf16 outputs (q_out is allocated when None; k_out when None and
+    there is no cache; in place: pass q, k).  cache: a PagedCache that the rows
+    are appended to.  cu_tokens, seen: int32 [S + 1], [S]; positions: int32 [T], or [3, T] with
+    sections (n0, n1, n2) frequencies to each axis.  turns: rotation_table's
+    output on the device (None: no rotation)."""
+
+    def __init__(self, q=None, k=None, v=None, q_out=None, k_out=None, cache=None, cu_tokens=None, seen=None,
+                 positions=None, sections=None, turns=None, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False):
+        if q is None and k is None:
+            raise ValueError("q or k must be given")
+        some = q if q is not None else k
+        T, d = int(some.shape[0]), int(some.shape[2])
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if k is not None and k_out is None and cache is None:
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        for t, like in ((q, None), (k, None), (v, k), (q_out, q), (k_out, k)):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or t.stride(2) != 1:
+                raise ValueError("q, k, v and their outputs are bf16 [T, heads, D] with head_dim contiguous")
+            if like is not None and t.shape != like.shape:
+                raise ValueError("v, q_out and k_out have the shapes of k, q and k")
+        if (q_out is not None and q is None) or (k_out is not None and k is None):
+            raise ValueError("an output needs its input")
+        for w in (q_weight, k_weight):
+            _dense(w, torch.bfloat16, (d,), "a norm's weight")
+        rot = 0
+        if turns is not None:
+            rot = 2 * int(turns.shape[0])
+            _dense(turns, torch.float32, (rot // 2, 2), "turns")
+        axes, n0, n1 = 1, 0, 0
+        if positions is not None:
+            if positions.dim() == 2:
+                axes = 3
+                if sections is None or len(sections) != 3 or sum(sections) != rot // 2 or min(sections) < 0:
+                    raise ValueError("positions of three axes need sections that add up to rotary_dim / 2")
+                n0, n1 = int(sections[0]), int(sections[1])
+            _dense(positions, torch.int32, (3, T) if axes == 3 else (T,), "positions")
+        S = cu_tokens.numel() - 1 if cu_tokens is not None else 0
+        _dense(cu_tokens, torch.int32, (S + 1,), "cu_tokens")
+        _dense(seen, torch.int32, (S,), "seen")
+        if cache is not None and (cu_tokens is None or cache.num_seqs != S or k is None or v is None
+                                  or cache.h_kv != k.shape[1] or cache.d != d):
+            raise ValueError("a cache needs k, v and cu_tokens of its sequences, KV heads and head_dim")
+        self.device = _same_device(q, k, v, q_out, k_out, cu_tokens, seen, positions, turns, q_weight, k_weight,
+                                   cache.k if cache is not None else None)
+        self.keep = (q, k, v, cu_tokens, seen, positions, turns, q_weight, k_weight, cache)
+        self.empty = T == 0 or (cu_tokens is not None and S == 0)
+        self.q_out, self.k_out = q_out, k_out
+        adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        st = lambda t, i: 0 if t is None else t.stride(i)  # noqa: E731
+        self.c = RotateProblemStruct(
+            num_tokens=T, num_seqs=S, h_q=0 if q is None else int(q.shape[1]), h_kv=0 if k is None else int(k.shape[1]),
+            head_dim=d, dtype=BF16, rotary_dim=rot, interleaved=1 if interleaved else 0, axes=axes, section0=n0,
+            section1=n1, eps=float(eps), reserved0=0, q=adr(q), k=adr(k), v=adr(v),
+            q_stride_tok=st(q, 0), q_stride_head=st(q, 1), k_stride_tok=st(k, 0), k_stride_head=st(k, 1),
+            v_stride_tok=st(v, 0), v_stride_head=st(v, 1), q_out=adr(q_out), k_out=adr(k_out),
+            qo_stride_tok=st(q_out, 0), qo_stride_head=st(q_out, 1), ko_stride_tok=st(k_out, 0),
+            ko_stride_head=st(k_out, 1), q_weight=adr(q_weight), k_weight=adr(k_weight), turns=adr(turns),
+            positions=adr(positions), cu_tokens=adr(cu_tokens), seen=adr(seen),
+            pages=ctypes.pointer(cache.c) if cache is not None else None)
+        self.ref = ctypes.byref(self.c)
+
+
+def aircache_rotate(prob: RotateProblem, status=None, stream=None):
+    _run_paged(prob, status, stream, lambda s: lib().aircache_rotate(prob.ref, _ptr(status), s), "aircache_rotate")
+
+
+def rotate(prob: RotateProblem, stream=None, check=True):
+    """One call; returns (q_out, k_out).  check=True reads the device status (synchronises)."""
+    st = torch.zeros(1, dtype=torch.int32, device=prob.device) if check else None
+    aircache_rotate(prob, st, stream)
+    if check:
+        code = aircache_get_error(st, stream)
+        if code != OK:
+            raise AirCacheError(code, "aircache_rotate (device)")
+    return prob.q_out, prob.k_out
+
+
+class PagedDecodeProblem:
+    """One decode step over a PagedCache (see aircache_paged_decode in the header).
+
+    q: [S, H_q, D] bf16; out: bf16 [S, H_q, D] (allocated when None); lse:
+    True (allocated) or an fp32 [S, H_q] tensor; scale: the logits' factor
+    (None: 1 / sqrt(D)); accumulate: add the weights to cache.mass in place, or
+    pass mass_out for another array; total_rows: a bound of the sum of
+    cache.lens (0: what the pages and the table can hold; give it when
+    sequences share pages)."""
+
+    def __init__(self, q, cache, out=None, lse=None, scale=None, accumulate=False, mass_out=None, total_rows=0):
+        if q.dim() != 3 or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+            raise ValueError("q is bf16 [S, H_q, D], head_dim contiguous")
+        S, h_q, d = (int(x) for x in q.shape)
+        if S != cache.num_seqs or d != cache.d:
+            raise ValueError("q must have the cache's sequences and head_dim")
+        if out is None:
+            out = torch.empty((S, h_q, d), dtype=torch.bfloat16, device=q.device)
+        if lse is True:
+            lse = torch.empty((S, h_q), dtype=torch.float32, device=q.device)
+        _dense(out, torch.bfloat16, (S, h_q, d), "out")
+        _dense(lse, torch.float32, (S, h_q), "lse")
+        if accumulate and mass_out is None:
+            mass_out = cache.mass
+        if (accumulate or mass_out is not None) and cache.mass is None:
+            raise ValueError("the cache has no mass to accumulate")
+        _dense(mass_out, torch.float32, (cache.num_pages, cache.h_kv, cache.page_rows), "mass_out")
+        if not total_rows:
+            total_rows = min(S * cache.max_pages, cache.num_pages) * cache.page_rows
+        self.device = _same_device(q, out, lse, mass_out, cache.k)
+        self.keep = (q, cache)
+        self.empty = S == 0
+        self.out, self.lse, self.mass_out = out, lse, mass_out
+        adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = PagedDecodeProblemStruct(
+            pages=ctypes.pointer(cache.c), h_q=h_q, dtype=BF16, scale=float(d ** -0.5 if scale is None else scale),
+            reserved0=0, total_rows=max(1, int(total_rows)), q=adr(q), q_stride_seq=q.stride(0),
+            q_stride_head=q.stride(1), out=adr(out), lse=adr(lse), mass_out=adr(mass_out))
+        self.ref = ctypes.byref(self.c)
+
+    def workspace_size(self) -> int:
+        if self.empty:
+            return 256
+        with torch.cuda.device(self.device):
+            n = lib().aircache_paged_decode_workspace_size(self.ref)
+        if n == 0:
+            raise AirCacheError(ERR_INVALID_ARG, "aircache_paged_decode_workspace_size")
+        return int(n)
+
+    def new_workspace(self) -> torch.Tensor:
+        """A zeroed workspace (zeroed once; every call leaves it ready for the next)."""
+        return torch.zeros(self.workspace_size(), dtype=torch.uint8, device=self.device)
+
+
+def aircache_paged_decode(prob: PagedDecodeProblem, ws, stream=None):
+    _run_paged(prob, ws, stream, lambda s: lib().aircache_paged_decode(prob.ref, _ptr(ws), ws.numel(), s),
+               "aircache_paged_decode")
+
+
+def paged_decode(prob: PagedDecodeProblem, ws=None, stream=None, check=True):
+    """One decode step; returns prob.out.  check=True reads the device error word (synchronises)."""
+    ws = prob.new_workspace() if ws is None else ws
+    aircache_paged_decode(prob, ws, stream)
+    if check:
+        st = aircache_get_error(ws, stream)
+        if st != OK:
+            raise AirCacheError(st, "aircache_paged_decode (device)")
+    return prob.out
+
+
+class EvictProblem:
+    """Eviction from a PagedCache by its mass (see aircache_evict in the header).
+
+    keep: int32 [S], rows each sequence keeps; lens_out: int32 [S], not
+    cache.lens itself; seen: int32 [S], tokens appended so far (needed with
+    recent); sink, recent: the first and the newest tokens, always kept;
+    mass_out, order_out: other arrays than the cache's (None: in place);
+    max_rows: a bound of cache.lens (0: the table's capacity)."""
+
+    def __init__(self, cache, keep, lens_out, seen=None, sink=0, recent=0, mass_out=None, order_out=None, max_rows=0):
+        S = cache.num_seqs
+        for t, name in ((keep, "keep"), (lens_out, "lens_out"), (seen, "seen")):
+            _dense(t, torch.int32, (S,), name)
+        if cache.mass is None:
+            raise ValueError("the cache has no mass to evict by")
+        mass_out = cache.mass if mass_out is None else mass_out
+        order_out = cache.order if order_out is None else order_out
+        shape = (cache.num_pages, cache.h_kv, cache.page_rows)
+        _dense(mass_out, torch.float32, shape, "mass_out")
+        _dense(order_out, torch.int32, shape, "order_out")
+        self.device = _same_device(cache.k, keep, lens_out, seen, mass_out, order_out)
+        self.keep_alive = (cache, keep, seen)
+        self.empty = S == 0
+        self.lens_out, self.mass_out, self.order_out = lens_out, mass_out, order_out
+        adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = EvictProblemStruct(
+            pages=ctypes.pointer(cache.c), keep=adr(keep), seen=adr(seen), lens_out=adr(lens_out),
+            mass_out=adr(mass_out), order_out=adr(order_out), sink=int(sink), recent=int(recent),
+            max_rows=int(max_rows) or cache.max_pages * cache.page_rows)
+        self.ref = ctypes.byref(self.c)
+
+    def workspace_size(self) -> int:
+        if self.empty:
+            return 256
+        with torch.cuda.device(self.device):
+            n = lib().aircache_evict_workspace_size(self.ref)
+        if n == 0:
+            raise AirCacheError(ERR_INVALID_ARG, "aircache_evict_workspace_size")
+        return int(n)
+
+    def new_workspace(self) -> torch.Tensor:
+        """A zeroed workspace (zeroed once; every call leaves it ready for the next)."""
+        return torch.zeros(self.workspace_size(), dtype=torch.uint8, device=self.device)
+
+
+def aircache_evict(prob: EvictProblem, ws, stream=None):
+    _run_paged(prob, ws, stream, lambda s: lib().aircache_evict(prob.ref, _ptr(ws), ws.numel(), s), "aircache_evict")
+
+
+def evict(prob: EvictProblem, ws=None, stream=None, check=True):
+    """One eviction; returns prob.lens_out.  check=True reads the device error word (synchronises)."""
+    ws = prob.new_workspace() if ws is None else ws
+    aircache_evict(prob, ws, stream)
+    if check:
+        st = aircache_get_error(ws, stream)
+        if st != OK:
+            raise AirCacheError(st, "aircache_evict (device)")
+    return prob.lens_out

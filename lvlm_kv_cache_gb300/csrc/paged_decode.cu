@@ -1,0 +1,855 @@
+// One decode step of attention over a paged cache (aircache_paged_decode).
+//
+//   x_j = scale q . k_j,  o = sum_j exp(x_j - m) v_j / l,  l = sum_j exp(x_j - m),
+//   mass_j += sum over the KV head's query heads of exp(x_j - m) / l.
+//
+// 4 g D operations for the 4 D bytes of a row's key and value (g query heads to a
+// KV head): bound by HBM.  The batch's rows form one list of 64-row tiles,
+// sequence by sequence and KV head by KV head, and every CTA takes an equal
+// run of it, so ragged lengths leave no CTA idle.  A producer warp looks the
+// pages up and copies each tile as four 16-row pieces (TMA; a page is a
+// multiple of 16 rows, so a piece never crosses one) into a ring of stages;
+// four consumer warps take one piece each: S = Q K^T and O += P V with
+// mma.sync (16 query heads by 16 rows; tcgen05's 128-row operand would be
+// seven eighths padding), an online softmax in base 2 between them.  A (sequence, KV
+// head) that several CTAs share is joined by the last of them to finish (an
+// atomic count, no waiting), in the order of the CTAs.
+//
+// int8 rows carry a scale each.  The key's multiplies the logit.  The value's
+// joins the weight before it is rounded to f16: the weights of O are
+// exp2(x_j + log2 s_j) against their own running maximum, and the sum l keeps its own.
+//
+// Weights are rounded to bf16 (int8 rows: f16) for the product with V, which
+// halves their registers and is what the matrix instruction takes; maximum,
+// sum, O and the joins are fp32, and out is rounded once, to bf16.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "pages.cuh"
+#include "rowmma.cuh"
+#include "tmap.cuh"
+
+namespace aircache {
+namespace {
+
+constexpr int kPdRows = 64;   // rows of a tile
+constexpr int kPdWarps = 4;   // consumer warps, 16 rows each
+constexpr int kPdThreads = (kPdWarps + 1) * 32;
+constexpr int kPdGroup = 16;  // query heads of a KV head, at most
+constexpr int kPdHeader = 256;  // workspace: error word, then the tile count of the last call
+
+template <int D, bool Q8>
+struct PdCfg {
+  static constexpr int kPiece = 16 * D * (Q8 ? 1 : 2);  // 16 rows of K or of V
+  static constexpr int kTile = kPdWarps * kPiece;
+  static constexpr int kStageBytes = 2 * kTile;
+  static constexpr int kStages = (Q8 ? 65536 : 98304) / kStageBytes;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kScratch = kPdGroup * D * 4;           // the warps' joined O
+  static constexpr int kScales = Q8 ? kStages * 2 * kPdRows * 4 : 0;
+  static constexpr int kMl = kPdWarps * kPdGroup * 3 * 4;     // (m, l, n) of each warp and head
+  static constexpr int kSmem = 1024 + kRing + kScratch + kScales + kMl + kStages * (8 + 8 + 4) + 256;
+  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+};
+
+// What the mass kernel needs of a tile: its place, and its pieces' pages (-1: not there).
+struct TileInfo {
+  int s, h, i, pad;
+  int page[4];
+};
+
+struct PdArgs {
+  Pages pages;
+  const __nv_bfloat16* q;
+  int64_t q_stride_seq, q_stride_head;
+  __nv_bfloat16* out;
+  float* lse;
+  float* mass_out;
+  int32_t* error;
+  int32_t* tiles;    // tile count, for the mass kernel
+  uint32_t* count;   // [S * h_kv] arrivals
+  float* lse2;       // [S * h_q] base 2
+  float4* part_ml;   // [2 CTAs][g]: m, l, n of O
+  float* part_o;     // [2 CTAs][g][D]
+  TileInfo* info;    // [tiles]
+  float* logits;     // [tiles][g][64], base 2
+  int64_t total_rows;
+  int h_q, group;
+  float scale_log2;
+};
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int a, int b, int c, int d, int e,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Rows of sequence s that count: 0 when its length is out of bounds.
+__device__ __forceinline__ int rows_of(const Pages& p, int s) {
+  const int n = p.lens[s];
+  return n >= 0 && n <= p.max_rows ? n : 0;
+}
+
+// A run of tiles of one (sequence, KV head): what a CTA does at a time.
+struct Run {
+  int s, h, len, tiles;  // the unit: its sequence, KV head, rows and tiles
+  int first, count;      // the CTA's tiles of it
+  int64_t at, left;      // list index of tile `first`; tiles of the CTA from there on
+};
+
+// Moves to the next unit that has tiles; false at the end of the CTA's share.
+__device__ __forceinline__ bool next_run(const Pages& p, Run& r) {
+  r.at += r.count;
+  r.left -= r.count;
+  if (r.left <= 0) return false;
+  if (++r.h == p.h_kv) {
+    r.h = 0;
+    do {  // tiles are left, so a sequence with rows follows
+      if (++r.s >= p.num_seqs) return false;
+      r.len = rows_of(p, r.s);
+    } while (r.len == 0);
+    r.tiles = (r.len + kPdRows - 1) / kPdRows;
+  }
+  r.first = 0;
+  r.count = (int)(r.left < r.tiles ? r.left : r.tiles);
+  return true;
+}
+
+// The batch's tile count and this CTA's first run, by all threads of the CTA
+// (n_thr of them): lengths are summed in parts of consecutive sequences.
+struct Share {
+  int64_t total, per;
+  Run run;
+};
+__device__ __forceinline__ Share make_share(const PdArgs& a, int n_thr, int64_t* scan, Run* found) {
+  const Pages& p = a.pages;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = n_thr / 32;
+  const int part = (p.num_seqs + n_thr - 1) / n_thr;
+  const int s0 = min(tid * part, p.num_seqs), s1 = min(s0 + part, p.num_seqs);
+  int64_t tiles = 0, rows = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int n = rows_of(p, s);
+    if (n != p.lens[s] && blockIdx.x == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+    tiles += (n + kPdRows - 1) / kPdRows;
+    rows += n;
+  }
+  int64_t incl = tiles;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += t;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, off);
+  if (lane == 31) scan[warp] = incl;
+  if (lane == 0) scan[8 + warp] = rows;
+  __syncthreads();
+  int64_t before = incl - tiles, total = 0, all = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+    all += scan[8 + w];
+  }
+  if (all > a.total_rows) {
+    if (blockIdx.x == 0 && tid == 0) set_error(a.error, AIRCACHE_ERR_CAPACITY);
+    total = -1;  // nothing is computed
+  }
+  Share sh;
+  sh.total = total * p.h_kv;
+  sh.per = (sh.total + gridDim.x - 1) / gridDim.x;
+  const int64_t t0 = sh.per * blockIdx.x;
+  if (t0 < sh.total && t0 >= before * p.h_kv && t0 < (before + tiles) * p.h_kv) {
+    int64_t b = before * p.h_kv;
+    for (int s = s0; s < s1; ++s) {
+      const int n = rows_of(p, s), t = (n + kPdRows - 1) / kPdRows;
+      if (t0 < b + (int64_t)t * p.h_kv) {
+        found->s = s;
+        found->h = (int)((t0 - b) / t);
+        found->len = n;
+        found->tiles = t;
+        found->first = (int)((t0 - b) % t);
+        found->at = t0;
+        found->left = (sh.total - t0 < sh.per ? sh.total - t0 : sh.per);
+        found->count = (int)(found->left < t - found->first ? found->left : t - found->first);
+        break;
+      }
+      b += (int64_t)t * p.h_kv;
+    }
+  }
+  __syncthreads();
+  sh.run = *found;
+  if (t0 >= sh.total) sh.run.left = sh.run.count = 0;
+  return sh;
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                  const __grid_constant__ CUtensorMap vmap,
+                                                                  const __grid_constant__ PdArgs a) {
+  using C = PdCfg<D, Q8>;
+  extern __shared__ uint8_t pd_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pd_raw) + 1023) & ~uintptr_t(1023));
+  float* scratch = reinterpret_cast<float*>(ring + C::kRing);               // [16][D], swizzled
+  float* scales = reinterpret_cast<float*>(ring + C::kRing + C::kScratch);  // [stages][K, V][64]
+  float* mlw = reinterpret_cast<float*>(ring + C::kRing + C::kScratch + C::kScales);  // [4][16][3]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(mlw) + C::kMl);
+  uint64_t* empty = full + C::kStages;
+  int64_t* scan = reinterpret_cast<int64_t*>(empty + C::kStages);  // [16]
+  Run* found = reinterpret_cast<Run*>(scan + 16);
+  uint32_t* pieces = reinterpret_cast<uint32_t*>(found + 1);       // [stages] which pieces of a tile are there
+  int* ctl = reinterpret_cast<int*>(pieces + C::kStages);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = a.group;
+  const Pages& p = a.pages;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kPdWarps);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kPdWarps && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  pdl_wait();
+  const Share sh = make_share(a, kPdThreads, scan, found);  // (its barriers publish the mbarriers too)
+  if (blockIdx.x == 0 && tid == 0) *a.tiles = (int)(sh.total > 0 ? sh.total : 0);
+  Run r = sh.run;
+
+  if (warp == kPdWarps) {
+    // ---- producer warp: lane j of 32 holds the page of the j-th 16-row piece
+    // ahead (8 tiles); 0-3 copy keys, 4-7 values, 8-15 the scales of int8 rows
+    int st = 0;
+    uint32_t phase = 0, filled = 0;
+    bool alive = true;
+    for (bool more = r.left > 0; more && alive; more = next_run(p, r)) {
+      const int32_t* table = p.table + (int64_t)r.s * p.table_stride;
+      int page = -1;
+      for (int i = 0; i < r.count; ++i) {
+        if ((i & 7) == 0) {
+          const int row = ((r.first + i) * 4 + lane) * 16;
+          page = -1;
+          if (row < r.len && row < (r.first + r.count) * kPdRows) {
+            page = table[row / p.page_rows];
+            if (!page_ok(p, page)) {
+              set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+              page = -1;
+            }
+          }
+        }
+        const int piece = lane & 3;
+        const int pg = __shfl_sync(0xffffffffu, page, (i & 7) * 4 + piece);
+        const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0) & 15u;
+        if (filled >= C::kStages) {
+          if (!mbar_wait(&empty[st], phase ^ 1)) {
+            set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+            alive = false;
+            break;
+          }
+        }
+        uint8_t* dst = ring + st * C::kStageBytes + piece * C::kPiece;
+        if (lane == 0) {
+          pieces[st] = mask;
+          fence_proxy_async_smem();  // the consumers' generic accesses of this stage come first
+          mbar_arrive_expect_tx(&full[st], __popc(mask) * (2 * C::kPiece + (Q8 ? 128 : 0)));
+        }
+        __syncwarp();
+        const int row = (((r.first + i) * 4 + piece) * 16) % p.page_rows;
+        if (pg >= 0 && lane < 8) {
+          fence_proxy_async_smem();
+          const uint32_t to = smem_u32(dst) + (lane >= 4 ? C::kTile : 0);
+          const CUtensorMap* map = lane >= 4 ? &vmap : &kmap;
+          if constexpr (Q8)
+            tma_load_4d(to, map, 0, row, r.h, pg, &full[st]);
+          else
+            tma_load_5d(to, map, 0, row, 0, r.h, pg, &full[st]);
+        }
+        if constexpr (Q8) {
+          if (pg >= 0 && lane >= 8 && lane < 16) {
+            fence_proxy_async_smem();
+            const int64_t slot = page_slot(p, pg, r.h, row);
+            bulk_g2s(scales + (st * 2 + (lane >= 12)) * kPdRows + piece * 16,
+                     (lane >= 12 ? p.v_scale : p.k_scale) + slot, 64, &full[st]);
+          }
+        }
+        if (a.mass_out) {
+          const int64_t t = r.at + i;
+          if (lane < 4) a.info[t].page[lane] = pg;
+          if (lane == 4) *reinterpret_cast<int4*>(&a.info[t]) = make_int4(r.s, r.h, r.first + i, 0);
+        }
+        ++filled;
+        if (++st == C::kStages) st = 0, phase ^= 1;
+      }
+    }
+    return;
+  }
+
+  // ---- consumers
+  const int hA = lane >> 2, cq = lane & 3;  // accumulator rows (heads) hA and hA + 8, columns 2cq, 2cq + 1
+  // sequences without rows: out = 0, lse = -inf
+  for (int s = blockIdx.x; s < p.num_seqs && sh.total >= 0; s += gridDim.x) {
+    if (rows_of(p, s) != 0) continue;
+    for (int i = tid; i < a.h_q * D / 8; i += kPdWarps * 32)
+      *reinterpret_cast<uint4*>(a.out + (int64_t)s * a.h_q * D + i * 8) = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < a.h_q && a.lse; i += kPdWarps * 32) a.lse[(int64_t)s * a.h_q + i] = -INFINITY;
+  }
+  int st = 0;
+  uint32_t phase = 0;
+  bool alive = true;
+  for (bool more = r.left > 0; more; more = next_run(p, r)) {
+    // ---- the group's queries as A fragments (rows at or past g: zeros)
+    uint32_t qa[D / 16][4];
+    {
+      const __nv_bfloat16* q0 = a.q + (int64_t)r.s * a.q_stride_seq + (int64_t)(r.h * g + hA) * a.q_stride_head;
+      const __nv_bfloat16* q1 = q0 + 8 * a.q_stride_head;
+      const bool in0 = hA < g, in1 = hA + 8 < g;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        if constexpr (Q8) {
+          // k-step kk of quad lane cq covers d = cq*D/4 + 4kk + 0..3, as the key codes are read below
+          const uint2 x = in0 ? *reinterpret_cast<const uint2*>(q0 + cq * (D / 4) + 4 * kk) : make_uint2(0, 0);
+          const uint2 y = in1 ? *reinterpret_cast<const uint2*>(q1 + cq * (D / 4) + 4 * kk) : make_uint2(0, 0);
+          qa[kk][0] = x.x;
+          qa[kk][1] = y.x;
+          qa[kk][2] = x.y;
+          qa[kk][3] = y.y;
+        } else {
+          const int d = 16 * kk + 2 * cq;
+          qa[kk][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + d) : 0u;
+          qa[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + d) : 0u;
+          qa[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + d + 8) : 0u;
+          qa[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) : 0u;
+        }
+      }
+    }
+    float kmult = a.scale_log2;
+    if constexpr (Q8) {
+      // Q enters the f16 product times the power of two that puts the group's
+      // largest |q| in [2^14, 2^15): exact, and undone in the logit's multiplier
+      float mx = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      float qscale = 1.f;
+      if (mx > 0.f && mx < INFINITY) {
+        int ex;
+        (void)frexpf(mx, &ex);
+        qscale = ldexpf(1.f, min(15 - ex, 120));
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
+          const __half2 hq = __floats2half2_rn(f.x * qscale, f.y * qscale);
+          qa[kk][j] = *reinterpret_cast<const uint32_t*>(&hq);
+        }
+      kmult /= qscale;
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+    float nA = -INFINITY, nB = -INFINITY;  // O's own reference (int8 rows; else unused)
+
+    for (int i = 0; i < r.count && alive; ++i) {
+      if (!mbar_wait(&full[st], phase)) {
+        if (lane == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+        alive = false;
+        break;
+      }
+      const int valid = (pieces[st] >> warp) & 1 ? min(16, r.len - (r.first + i) * kPdRows - 16 * warp) : 0;
+      if (valid > 0) {
+        uint8_t* kt = ring + st * C::kStageBytes + warp * C::kPiece;
+        uint8_t* vt = kt + C::kTile;
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        float ks[4] = {1.f, 1.f, 1.f, 1.f}, lv[4] = {0.f, 0.f, 0.f, 0.f};  // rows 2cq, 2cq+1, 2cq+8, 2cq+9
+        if constexpr (Q8) {
+          const float* sk = scales + st * 2 * kPdRows + 16 * warp;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = 2 * cq + (j & 1) + 8 * (j >> 1);
+            ks[j] = sk[row];
+            lv[j] = log2f(sk[kPdRows + row]);
+          }
+          uint32_t kq[2][D / 16];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              const uint4 x =
+                  *reinterpret_cast<const uint4*>(kt + swz8<D>((8 * t + hA) * D + cq * (D / 4) + 16 * w));
+              kq[t][4 * w] = x.x;
+              kq[t][4 * w + 1] = x.y;
+              kq[t][4 * w + 2] = x.z;
+              kq[t][4 * w + 3] = x.w;
+            }
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t x = kq[t][kk] ^ 0x80808080u;
+              mma16816<true>(sc[t], qa[kk], widen2_f16(x, 0x4140u), widen2_f16(x, 0x4342u));
+            }
+        } else {
+          if (valid < 16) {
+            // rows past the end may hold anything: zero their V so that weights of 0 add exactly 0
+            for (int c = lane; c < 16 * (D / 8); c += 32) {
+              const int rr = c / (D / 8), rest = c % (D / 8);
+              if (rr >= valid)
+                *reinterpret_cast<uint4*>(vt + (rest >> 3) * 2048 + rr * 128 + (rest & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+          }
+          const uint32_t kb = smem_u32(kt);
+          const int mi = lane >> 3, row = (lane & 7) + 8 * (mi >> 1);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t kf[4];
+            ldsm_x4(kf, swz(kb + (kk >> 2) * 2048, row, 2 * (kk & 3) + (mi & 1)));
+            mma16816<false>(sc[0], qa[kk], kf[0], kf[1]);
+            mma16816<false>(sc[1], qa[kk], kf[2], kf[3]);
+          }
+        }
+        // base-2 logits; rows at or past `valid` get weight 0
+        float tA = -INFINITY, tB = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool in = 8 * t + 2 * cq + e < valid;
+            const float mult = Q8 ? kmult * ks[2 * t + e] : kmult;
+            sc[t][e] = in ? sc[t][e] * mult : -INFINITY;
+            sc[t][2 + e] = in ? sc[t][2 + e] * mult : -INFINITY;
+            if (Q8) lv[2 * t + e] = in ? lv[2 * t + e] : -INFINITY;
+            tA = fmaxf(tA, sc[t][e]);
+            tB = fmaxf(tB, sc[t][2 + e]);
+          }
+        if (a.mass_out) {
+          float* lg = a.logits + (r.at + i) * g * kPdRows + 16 * warp + 2 * cq;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (hA < g) *reinterpret_cast<float2*>(lg + hA * kPdRows + 8 * t) = make_float2(sc[t][0], sc[t][1]);
+            if (hA + 8 < g)
+              *reinterpret_cast<float2*>(lg + (hA + 8) * kPdRows + 8 * t) = make_float2(sc[t][2], sc[t][3]);
+          }
+        }
+        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
+        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2));
+        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
+        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2));
+        const float xA = fmaxf(mA, tA), xB = fmaxf(mB, tB);
+        float fA = fast_exp2(mA - xA), fB = fast_exp2(mB - xB);
+        mA = xA;
+        mB = xB;
+        uint32_t pa[4];
+        float sA = 0.f, sB = 0.f;
+        if constexpr (Q8) {
+          lA *= fA;
+          lB *= fB;
+          float yA = -INFINITY, yB = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sA += fast_exp2(sc[t][e] - xA);
+              sB += fast_exp2(sc[t][2 + e] - xB);
+              sc[t][e] += lv[2 * t + e];
+              sc[t][2 + e] += lv[2 * t + e];
+              yA = fmaxf(yA, sc[t][e]);
+              yB = fmaxf(yB, sc[t][2 + e]);
+            }
+          lA += sA;
+          lB += sB;
+          yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
+          yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
+          yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
+          yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
+          yA = fmaxf(fmaxf(yA, nA), -1e30f);  // (finite: rows of zeros only keep weights of 0)
+          yB = fmaxf(fmaxf(yB, nB), -1e30f);
+          fA = fast_exp2(nA - yA);
+          fB = fast_exp2(nB - yB);
+          nA = yA;
+          nB = yB;
+          float x0, x1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            pa[2 * t] = pack_f16(kP16 * fast_exp2(sc[t][0] - yA), kP16 * fast_exp2(sc[t][1] - yA), x0, x1);
+            pa[2 * t + 1] = pack_f16(kP16 * fast_exp2(sc[t][2] - yB), kP16 * fast_exp2(sc[t][3] - yB), x0, x1);
+          }
+        } else {
+          // the sum takes the weights before they are rounded: lse and mass need it
+          float x0, x1;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float wA0 = fast_exp2(sc[t][0] - xA), wA1 = fast_exp2(sc[t][1] - xA);
+            const float wB0 = fast_exp2(sc[t][2] - xB), wB1 = fast_exp2(sc[t][3] - xB);
+            pa[2 * t] = pack_bf16(wA0, wA1, x0, x1);
+            sA += wA0 + wA1;
+            pa[2 * t + 1] = pack_bf16(wB0, wB1, x0, x1);
+            sB += wB0 + wB1;
+          }
+          lA = lA * fA + sA;
+          lB = lB * fB + sB;
+        }
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          o[t][0] *= fA;
+          o[t][1] *= fA;
+          o[t][2] *= fB;
+          o[t][3] *= fB;
+        }
+        if constexpr (Q8) {
+          // lane (hA, cq) takes rows 2cq, 2cq+1, 2cq+8, 2cq+9, value columns hA*(D/8) .. +D/8-1:
+          // n-tile t's column n is the value column n*(D/8) + t
+          uint32_t vw[4][D / 32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int off = swz8<D>((2 * cq + (j & 1) + 8 * (j >> 1)) * D + hA * (D / 8));
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + off);
+              vw[j][0] = x.x ^ 0x80808080u;
+              vw[j][1] = x.y ^ 0x80808080u;
+              vw[j][2] = x.z ^ 0x80808080u;
+              vw[j][3] = x.w ^ 0x80808080u;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(vt + off);
+              vw[j][0] = x.x ^ 0x80808080u;
+              vw[j][1] = x.y ^ 0x80808080u;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) {
+            const uint32_t sel = (uint32_t)(t & 3) | ((uint32_t)((t & 3) + 4) << 4);
+            const uint32_t b0 = widen2_f16(__byte_perm(vw[0][t >> 2], vw[1][t >> 2], sel), 0x4140u);
+            const uint32_t b1 = widen2_f16(__byte_perm(vw[2][t >> 2], vw[3][t >> 2], sel), 0x4140u);
+            mma16816<true>(o[t], pa, b0, b1);
+          }
+        } else {
+          const uint32_t vb = smem_u32(vt);
+          const int mi = lane >> 3, row = (lane & 7) + 8 * (mi & 1);
+#pragma unroll
+          for (int np = 0; np < D / 16; ++np) {
+            uint32_t vf[4];
+            ldsm_x4_trans(vf, swz(vb + (np >> 2) * 2048, row, 2 * (np & 3) + (mi >> 1)));
+            mma16816<false>(o[2 * np], pa, vf[0], vf[1]);
+            mma16816<false>(o[2 * np + 1], pa, vf[2], vf[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+      if (++st == C::kStages) st = 0, phase ^= 1;
+    }
+
+    // ---- join the four warps: (m, l, n) by all, then O in turns, each warp another quarter of the columns
+    lA += __shfl_xor_sync(0xffffffffu, lA, 1);
+    lA += __shfl_xor_sync(0xffffffffu, lA, 2);
+    lB += __shfl_xor_sync(0xffffffffu, lB, 1);
+    lB += __shfl_xor_sync(0xffffffffu, lB, 2);
+    if (!Q8) nA = mA, nB = mB;
+    named_bar_sync(1, kPdWarps * 32);  // the last run's scratch and mlw are read
+    if (cq == 0) {
+      float* w = mlw + (warp * kPdGroup + hA) * 3;
+      w[0] = mA, w[1] = lA, w[2] = nA;
+      w += 8 * 3;
+      w[0] = mB, w[1] = lB, w[2] = nB;
+    }
+    named_bar_sync(1, kPdWarps * 32);
+    auto joined = [&](int hh, float& m, float& l, float& n) {
+      m = n = -INFINITY;
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPdWarps; ++w) {
+        m = fmaxf(m, mlw[(w * kPdGroup + hh) * 3]);
+        n = fmaxf(n, mlw[(w * kPdGroup + hh) * 3 + 2]);
+      }
+#pragma unroll
+      for (int w = 0; w < kPdWarps; ++w) {
+        const float x = mlw[(w * kPdGroup + hh) * 3];
+        if (x != -INFINITY) l += mlw[(w * kPdGroup + hh) * 3 + 1] * fast_exp2(x - m);
+      }
+    };
+    {
+      float m, l, n;
+      joined(hA, m, l, n);
+      const float cA = nA == -INFINITY ? 0.f : fast_exp2(nA - n);
+      joined(hA + 8, m, l, n);
+      const float cB = nB == -INFINITY ? 0.f : fast_exp2(nB - n);
+      float2* sc2 = reinterpret_cast<float2*>(scratch);
+      for (int turn = 0; turn < 4; ++turn) {
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          if ((t / (D / 32)) != ((turn + warp) & 3)) continue;
+          const int col = (4 * t + cq) ^ ((hA & 3) << 2);  // float2 columns, spread over the banks
+          float2* x = sc2 + hA * (D / 2) + col;
+          float2* y = x + 8 * (D / 2);
+          float2 u = make_float2(o[t][0] * cA, o[t][1] * cA), v = make_float2(o[t][2] * cB, o[t][3] * cB);
+          if (turn) u.x += x->x, u.y += x->y, v.x += y->x, v.y += y->y;
+          *x = u;
+          *y = v;
+        }
+        named_bar_sync(1, kPdWarps * 32);
+      }
+    }
+    // int8 values: column d sits where n-tile d % (D/8) keeps its column d / (D/8)
+    auto joined_o = [&](int hh, int d) {
+      const int ds = Q8 ? 8 * (d % (D / 8)) + d / (D / 8) : d;
+      return scratch[hh * D + (((ds >> 1) ^ ((hh & 3) << 2)) << 1) + (ds & 1)];
+    };
+    const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
+    constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
+    auto finish = [&](int hh, float m, float l) {  // the head's log-sum-exp
+      if (a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (a.mass_out) a.lse2[head0 + hh] = l > 0.f ? m + log2f(l) : INFINITY;
+    };
+    if (r.count == r.tiles) {
+      for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
+        const int hh = c / (D / 4), d = c % (D / 4) * 4;
+        float m, l, n;
+        joined(hh, m, l, n);
+        const float f = l > 0.f ? kUndo * fast_exp2(n - m) / l : 0.f;
+        __nv_bfloat162 x[2] = {__floats2bfloat162_rn(joined_o(hh, d) * f, joined_o(hh, d + 1) * f),
+                               __floats2bfloat162_rn(joined_o(hh, d + 2) * f, joined_o(hh, d + 3) * f)};
+        *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
+        if (d == 0) finish(hh, m, l);
+      }
+      continue;
+    }
+    // ---- a part of a unit: the partial result, then the join by the unit's last CTA.
+    // CTA c's part goes to slot 2c when the unit began before c, to 2c + 1 when it began in c.
+    {
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (r.first == 0 ? 1 : 0);
+      for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
+        const int hh = c / (D / 4), d = c % (D / 4) * 4;
+        *reinterpret_cast<float4*>(a.part_o + (slot * g + hh) * D + d) =
+            make_float4(joined_o(hh, d), joined_o(hh, d + 1), joined_o(hh, d + 2), joined_o(hh, d + 3));
+        if (d == 0) {
+          float m, l, n;
+          joined(hh, m, l, n);
+          a.part_ml[slot * g + hh] = make_float4(m, l, n, 0.f);
+        }
+      }
+    }
+    const int64_t u0 = r.at - r.first;  // the unit's first tile
+    const int c0 = (int)(u0 / sh.per), c1 = (int)((u0 + r.tiles - 1) / sh.per), parts = c1 - c0 + 1;
+    __threadfence();
+    named_bar_sync(1, kPdWarps * 32);
+    uint32_t* count = a.count + (int64_t)r.s * p.h_kv + r.h;
+    if (tid == 0) ctl[0] = atomicAdd(count, 1u) == (uint32_t)(parts - 1);
+    named_bar_sync(1, kPdWarps * 32);
+    if (!ctl[0]) continue;
+    if (tid == 0) *count = 0;  // every call leaves the counters at zero
+    __threadfence();
+    for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
+      const int hh = c / (D / 4), d = c % (D / 4) * 4;
+      const int64_t first = 2 * (int64_t)c0 + 1;  // then 2 (c0 + j)
+      auto at = [&](int j) { return (j == 0 ? first : 2 * (int64_t)(c0 + j)) * g + hh; };
+      float m = -INFINITY, n = -INFINITY, l = 0.f;
+      for (int j = 0; j < parts; ++j) {
+        const float4 x = __ldcg(a.part_ml + at(j));
+        m = fmaxf(m, x.x);
+        n = fmaxf(n, x.z);
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < parts; ++j) {
+        const float4 x = __ldcg(a.part_ml + at(j));
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(j) * D + d));
+        if (x.x == -INFINITY) continue;
+        l += x.y * fast_exp2(x.x - m);
+        const float f = fast_exp2(x.z - n);
+        acc.x += f * y.x;
+        acc.y += f * y.y;
+        acc.z += f * y.z;
+        acc.w += f * y.w;
+      }
+      const float f = l > 0.f ? kUndo * fast_exp2(n - m) / l : 0.f;
+      __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
+      *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
+      if (d == 0) finish(hh, m, l);
+    }
+  }
+}
+
+// The rows' mass from the stored logits: a warp takes a tile, a lane two rows of it.
+__global__ void __launch_bounds__(256) paged_mass_kernel(const __grid_constant__ PdArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, g = a.group;
+  const int total = *a.tiles;
+  const Pages& p = a.pages;
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8) {
+    const int4 w = *reinterpret_cast<const int4*>(&a.info[t]);
+    const int page = a.info[t].page[lane >> 3];
+    const int row = w.z * kPdRows + 2 * lane;
+    const int len = p.lens[w.x];
+    if (page < 0 || row >= len) continue;
+    const int64_t slot = page_slot(p, page, w.y, row % p.page_rows);
+    const float* lg = a.logits + (int64_t)t * g * kPdRows + 2 * lane;
+    const float* lse = a.lse2 + (int64_t)w.x * a.h_q + w.y * g;
+    float x = 0.f, y = 0.f;
+    for (int hh = 0; hh < g; ++hh) {
+      const float2 v = *reinterpret_cast<const float2*>(lg + hh * kPdRows);
+      const float z = lse[hh];
+      x += fast_exp2(v.x - z);
+      y += fast_exp2(v.y - z);
+    }
+    a.mass_out[slot] = p.mass[slot] + x;
+    if (row + 1 < len) a.mass_out[slot + 1] = p.mass[slot + 1] + y;
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+struct PdPlan {
+  Pages pages;
+  bool q8;
+  int d, g, grid, sms;
+  int64_t tiles;  // bound of the tile list
+  size_t lse_off, ml_off, o_off, info_off, lg_off, total;
+};
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
+  if (!p) return AIRCACHE_ERR_INVALID_ARG;
+  const int rc = check_pages(p->pages, pl.pages);
+  if (rc != AIRCACHE_OK) return rc;
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  if (p->h_q <= 0 || p->h_q % p->pages->h_kv != 0 || p->reserved0 != 0 || p->dtype != AIRCACHE_BF16 ||
+      !(p->scale > 0.f) || !std::isfinite(p->scale) || p->total_rows < 1 || p->total_rows > 0x7fff0000LL || !p->q ||
+      !p->out || !al16(p->q) || !al16(p->out) || p->q_stride_seq < 0 || p->q_stride_head < 0 ||
+      p->q_stride_seq % 8 != 0 || p->q_stride_head % 8 != 0 || (p->mass_out && !p->pages->mass) ||
+      (reinterpret_cast<uintptr_t>(p->lse) & 3) != 0 || (reinterpret_cast<uintptr_t>(p->mass_out) & 3) != 0)
+    return AIRCACHE_ERR_INVALID_ARG;
+  pl.g = p->h_q / p->pages->h_kv;
+  if (pl.g > kPdGroup) return AIRCACHE_ERR_UNSUPPORTED;
+  pl.q8 = p->pages->kv_dtype == AIRCACHE_INT8;
+  pl.d = p->pages->head_dim;
+  int dev = 0;
+  pl.sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&pl.sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
+  pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
+  if (pl.tiles > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
+  pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2LL * pl.sms, pl.tiles));
+  pl.lse_off = kPdHeader + up256(sizeof(uint32_t) * (size_t)units);
+  pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
+  pl.o_off = pl.ml_off + up256(sizeof(float4) * 2 * (size_t)pl.grid * pl.g);
+  pl.info_off = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.g * pl.d);
+  pl.lg_off = pl.info_off + (p->mass_out ? up256(sizeof(TileInfo) * (size_t)pl.tiles) : 0);
+  pl.total = pl.lg_off + (p->mass_out ? up256(sizeof(float) * (size_t)pl.tiles * pl.g * kPdRows) : 0);
+  return AIRCACHE_OK;
+}
+
+// One box: 16 rows of one page and KV head, every 128-byte column slab of them.
+bool encode_pages(CUtensorMap* m, const void* base, const PdPlan& pl) {
+  auto enc = tma_encoder();
+  if (!enc) return false;
+  const Pages& p = pl.pages;
+  if (pl.q8) {
+    cuuint64_t dims[4] = {(cuuint64_t)pl.d, (cuuint64_t)p.page_rows, (cuuint64_t)p.h_kv, (cuuint64_t)p.num_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)p.stride_row, (cuuint64_t)p.stride_head, (cuuint64_t)p.stride_page};
+    cuuint32_t box[4] = {(cuuint32_t)pl.d, 16, 1, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, pl.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
+  cuuint64_t dims[5] = {64, (cuuint64_t)p.page_rows, (cuuint64_t)pl.d / 64, (cuuint64_t)p.h_kv,
+                        (cuuint64_t)p.num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)p.stride_row * 2, 128, (cuuint64_t)p.stride_head * 2,
+                           (cuuint64_t)p.stride_page * 2};
+  cuuint32_t box[5] = {64, 16, (cuuint32_t)pl.d / 64, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool Q8>
+int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
+  CUtensorMap km, vm;
+  if (!encode_pages(&km, pl.pages.k, pl) || !encode_pages(&vm, pl.pages.v, pl)) return AIRCACHE_ERR_UNSUPPORTED;
+  constexpr int smem = PdCfg<D, Q8>::kSmem;
+  if (allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<D, Q8>), smem) != cudaSuccess)
+    return AIRCACHE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.grid);
+  cfg.blockDim = dim3(kPdThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (a.mass_out) {
+    const int grid = (int)std::min<int64_t>((pl.tiles + 7) / 8, 8LL * pl.sms);
+    if (launch_pdl(paged_mass_kernel, dim3(grid), dim3(256), 0, s, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  }
+  return AIRCACHE_OK;
+}
+
+}  // namespace
+}  // namespace aircache
+
+using namespace aircache;
+
+extern "C" {
+
+size_t aircache_paged_decode_workspace_size(const aircache_paged_decode_problem* p) {
+  PdPlan pl;
+  return pd_plan(p, pl) == AIRCACHE_OK ? pl.total : 0;
+}
+
+int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size_t ws_bytes, void* stream) {
+  PdPlan pl;
+  const int rc = pd_plan(p, pl);
+  if (rc != AIRCACHE_OK) return rc;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) != 0) return AIRCACHE_ERR_INVALID_ARG;
+  if (ws_bytes < pl.total) return AIRCACHE_ERR_WORKSPACE;
+  if (p->pages->num_seqs == 0) return AIRCACHE_OK;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  PdArgs a;
+  a.pages = pl.pages;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.q_stride_seq = p->q_stride_seq;
+  a.q_stride_head = p->q_stride_head;
+  a.out = static_cast<__nv_bfloat16*>(p->out);
+  a.lse = p->lse;
+  a.mass_out = p->mass_out;
+  a.error = reinterpret_cast<int32_t*>(w);
+  a.tiles = reinterpret_cast<int32_t*>(w + 64);
+  a.count = reinterpret_cast<uint32_t*>(w + kPdHeader);
+  a.lse2 = reinterpret_cast<float*>(w + pl.lse_off);
+  a.part_ml = reinterpret_cast<float4*>(w + pl.ml_off);
+  a.part_o = reinterpret_cast<float*>(w + pl.o_off);
+  a.info = reinterpret_cast<TileInfo*>(w + pl.info_off);
+  a.logits = reinterpret_cast<float*>(w + pl.lg_off);
+  a.total_rows = p->total_rows;
+  a.h_q = p->h_q;
+  a.group = pl.g;
+  a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pl.q8) return pl.d == 128 ? launch_pd<128, true>(pl, a, s) : launch_pd<64, true>(pl, a, s);
+  return pl.d == 128 ? launch_pd<128, false>(pl, a, s) : launch_pd<64, false>(pl, a, s);
+}
+
+}  // extern "C"

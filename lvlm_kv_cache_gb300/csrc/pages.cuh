@@ -1,0 +1,76 @@
+// The paged cache as the kernels of rotate.cu, paged_decode.cu and evict.cu see
+// it, and the host checks they share.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace aircache {
+
+// Device-visible description of one layer's pages (host checks done).
+struct Pages {
+  uint8_t* k;
+  uint8_t* v;
+  int64_t stride_page, stride_row, stride_head;  // elements
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  float* k_scale;
+  float* v_scale;
+  float* mass;
+  int32_t* order;
+  int64_t num_pages;
+  int num_seqs, h_kv, page_rows, max_rows;  // max_rows: the table's capacity of one sequence
+};
+
+// The slot of (page, row) of KV head h in the scale, mass and order arrays.
+__device__ __forceinline__ int64_t page_slot(const Pages& p, int page, int h, int row) {
+  return ((int64_t)page * p.h_kv + h) * p.page_rows + row;
+}
+// Element offset of (page, row) of KV head h in k and v.
+__device__ __forceinline__ int64_t page_elem(const Pages& p, int page, int h, int row) {
+  return (int64_t)page * p.stride_page + (int64_t)row * p.stride_row + (int64_t)h * p.stride_head;
+}
+__device__ __forceinline__ bool page_ok(const Pages& p, int page) { return page >= 0 && page < p.num_pages; }
+
+// Host: AIRCACHE_OK and the device description, or why not.
+inline int check_pages(const aircache_pages* p, Pages& d) {
+  if (!p || p->num_seqs < 0 || p->num_seqs > 65535 || p->h_kv <= 0 || p->h_kv > 65535 ||
+      (p->head_dim != 64 && p->head_dim != 128) || (p->kv_dtype != AIRCACHE_BF16 && p->kv_dtype != AIRCACHE_INT8) ||
+      p->page_rows < 16 || p->page_rows > 4096 || p->page_rows % 16 != 0 || p->max_pages < 1 ||
+      (int64_t)p->max_pages * p->page_rows > 0x7fff0000LL || p->num_pages < 1 || p->num_pages > 0x7fffffffLL ||
+      p->table_stride < p->max_pages || !p->k || !p->v || !p->table || !p->lens)
+    return AIRCACHE_ERR_INVALID_ARG;
+  const bool q8 = p->kv_dtype == AIRCACHE_INT8;
+  const int64_t unit = q8 ? 16 : 8;
+  // the scale arrays are read in pieces of 16 floats: they start on 16 bytes too
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  if (!al16(p->k) || !al16(p->v) || p->stride_page <= 0 || p->stride_row <= 0 || p->stride_head <= 0 ||
+      p->stride_page % unit != 0 || p->stride_row % unit != 0 || p->stride_head % unit != 0 ||
+      (q8 && (!p->k_scale || !p->v_scale || !al16(p->k_scale) || !al16(p->v_scale))))
+    return AIRCACHE_ERR_INVALID_ARG;
+  auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
+  if (!al4(p->table) || !al4(p->lens) || !al4(p->mass) || !al4(p->order)) return AIRCACHE_ERR_INVALID_ARG;
+  d.k = static_cast<uint8_t*>(p->k);
+  d.v = static_cast<uint8_t*>(p->v);
+  d.stride_page = p->stride_page;
+  d.stride_row = p->stride_row;
+  d.stride_head = p->stride_head;
+  d.table = p->table;
+  d.table_stride = p->table_stride;
+  d.lens = p->lens;
+  d.k_scale = q8 ? p->k_scale : nullptr;
+  d.v_scale = q8 ? p->v_scale : nullptr;
+  d.mass = p->mass;
+  d.order = p->order;
+  d.num_pages = p->num_pages;
+  d.num_seqs = p->num_seqs;
+  d.h_kv = p->h_kv;
+  d.page_rows = p->page_rows;
+  d.max_rows = p->max_pages * p->page_rows;
+  return AIRCACHE_OK;
+}
+
+}  // namespace aircache

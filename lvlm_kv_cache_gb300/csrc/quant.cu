@@ -14,6 +14,7 @@
 // two could round differently).
 #include <cuda_bf16.h>
 
+#include "int8code.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
 
@@ -35,25 +36,6 @@ struct QuantArgs {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// clip(round(x / s)) with x / s correctly rounded, s > 0, |x| <= 127 s.
-// The quotient is first taken as t = x * (1/s) (both correctly rounded:
-// within 1.6e-5 of the exact quotient, and the correctly rounded quotient is
-// within 3.9e-6 of that).  Away from half-integers both round to the same
-// integer, and round-to-nearest-even (rint) equals round-half-away there; within
-// 4e-5 of a half-integer the correctly rounded division and roundf decide.
-// |t| < 127.5 always, so no clip is needed.
-__device__ __forceinline__ int code(float x, float s, float rs) {
-  const float t = x * rs;
-  const float rt = rintf(t);
-  if (fabsf(t - rt) > 0.5f - 4e-5f) return (int)roundf(__fdiv_rn(x, s));
-  return (int)rt;
-}
-
-// four codes -> one word, byte i = code i
-__device__ __forceinline__ uint32_t pack4(int c0, int c1, int c2, int c3) {
-  return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kQuantThreads) quant_kernel(const __grid_constant__ QuantArgs a) {

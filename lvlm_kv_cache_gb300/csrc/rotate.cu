@@ -1,0 +1,316 @@
+// Norms of queries and keys for each head, the rotation by position and the
+// append to the paged cache (aircache_rotate).
+//
+// Per token, head and element: x' = x rsqrt(mean x^2 + eps) w; the pairs
+// (a, b) of the first R elements become (a cos - b sin, b cos + a sin).  A few
+// operations per 4 bytes moved: bound by HBM, or by latency for a handful of
+// tokens.
+//
+// D/8 lanes take one head's row, 16 bytes a lane, so a warp works on 2 (D =
+// 128) or 4 (D = 64) rows at once; it walks over the query, key and value heads
+// of ONE token, so that the token's sines and cosines are formed once, in the
+// registers of the lanes that need them, and the slot in the cache is looked
+// up once.  Half-style partners sit R/16 lanes away (one shuffle); interleaved
+// ones in the same lane.
+//
+// The angle: position * (hi + lo) turns is reduced before it is rounded.  The
+// position splits into two parts of at most 20 bits (exact in fp32), each
+// product with hi is taken with its rounding error (one multiplication and one
+// fused multiply-add, an error-free product), whole turns are dropped, and
+// the rest goes to sincospif: to about 2^-24 turns up to position 2^24, and to
+// 2^-19 turns at the far end of int32, where lo's own last bit shows.
+#include "int8code.cuh"
+#include "pages.cuh"
+
+namespace aircache {
+namespace {
+
+constexpr int kRotWarps = 8;
+constexpr int kRotBatch = 4;  // rows a lane group has in flight
+
+struct RotArgs {
+  const __nv_bfloat16* src[3];  // q, k, v
+  int64_t src_tok[3], src_head[3];
+  __nv_bfloat16* out[2];  // q_out, k_out
+  int64_t out_tok[2], out_head[2];
+  const __nv_bfloat16* weight[2];
+  const float2* turns;
+  const int32_t* positions;
+  const int32_t* cu_tokens;
+  const int32_t* seen;
+  int32_t* status;
+  int64_t num_tokens;
+  Pages pages;
+  int num_seqs, h_q, h_kv, heads;  // heads: rows of one token that the call touches
+  int rot, axes, sec0, sec1, has_pages;
+  int per;  // heads of one token that one warp takes
+  float eps;
+};
+
+// Sequence of token t: the last s with cu[s] <= t; 32 candidates a step.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t, int lane) {
+  int lo = 0, len = n + 1;  // entries lo .. lo+len-1 may hold it
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = lane * step < len && cu[i] <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    if (c == 0) return -1;
+    lo += (c - 1) * step;
+    len = min(step, len - (c - 1) * step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float x[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float x[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t*>(&t);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// sin and cos of 2 pi * position * (hi + lo)
+__device__ __forceinline__ void turn(int pos, float2 f, float& sn, float& cs) {
+  const float a = (float)(pos & ~0xfff), b = (float)(pos & 0xfff);
+  const float p1 = __fmul_rn(a, f.x), p2 = __fmul_rn(b, f.x);
+  const float e1 = __fmaf_rn(a, f.x, -p1), e2 = __fmaf_rn(b, f.x, -p2);
+  const float rest = (e1 + e2) + __fmaf_rn(a, f.y, __fmul_rn(b, f.y));
+  float r = (p1 - rintf(p1)) + (p2 - rintf(p2));
+  r = (r - rintf(r)) + rest;
+  sincospif(2.f * r, &sn, &cs);
+}
+
+template <int D, bool Q8, bool INTER>
+__global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int kLanes = D / 8;           // lanes of one row
+  constexpr int kRows = 32 / kLanes;      // rows a warp has at once
+  constexpr int kAngles = INTER ? 4 : 8;  // of one lane
+  const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
+  const int64_t t = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
+  if (t >= a.num_tokens) return;
+  const int first = blockIdx.y * a.per, last = min(first + a.per, a.heads);
+
+  // ---- the token's sequence, order and slot
+  int s = 0, order = 0;
+  if (a.cu_tokens) {
+    s = find_seq(a.cu_tokens, a.num_seqs, (int)t, lane);
+    if (s < 0 || s >= a.num_seqs) return;  // padding
+    const int back = a.cu_tokens[s + 1] - (int)t;
+    if (a.seen) order = a.seen[s] - back;
+  }
+  int page = -1, row = 0;
+  if (a.has_pages) {
+    const int len = a.pages.lens[s], back = a.cu_tokens[s + 1] - (int)t;
+    const int i = len - back;
+    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
+      page = a.pages.table[s * a.pages.table_stride + i / a.pages.page_rows];
+      row = i % a.pages.page_rows;
+      if (!page_ok(a.pages, page)) page = -1;
+    }
+    if (page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
+  }
+
+  // ---- this lane's angles (elements 8l .. 8l+7)
+  float sn[kAngles], cs[kAngles];
+  const bool turned = 8 * l < a.rot;
+  const int half = a.rot / 2;
+  if (turned) {
+#pragma unroll
+    for (int e = 0; e < kAngles; ++e) {
+      const int i = INTER ? 4 * l + e : (8 * l + e < half ? 8 * l + e : 8 * l + e - half);
+      int pos = order;
+      if (a.positions) {
+        const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
+        pos = a.positions[axis * a.num_tokens + t];
+      }
+      turn(pos, a.turns[i], sn[e], cs[e]);
+    }
+  }
+  // the partner's lane: R/16 lanes up for the lower half, down for the upper one
+  const int partner = turned ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
+  const float sign = 8 * l < half ? -1.f : 1.f;
+
+  for (int j0 = first + grp; j0 - grp < last; j0 += kRows * kRotBatch) {
+    uint4 in[kRotBatch];
+    int what[kRotBatch], head[kRotBatch];
+#pragma unroll
+    for (int b = 0; b < kRotBatch; ++b) {
+      const int j = j0 + b * kRows;
+      what[b] = j < a.h_q ? 0 : j < a.h_q + a.h_kv ? 1 : 2;
+      head[b] = j - (what[b] == 0 ? 0 : what[b] == 1 ? a.h_q : a.h_q + a.h_kv);
+      in[b] = make_uint4(0, 0, 0, 0);
+      if (j < last)
+        in[b] = *reinterpret_cast<const uint4*>(a.src[what[b]] + t * a.src_tok[what[b]] +
+                                                head[b] * a.src_head[what[b]] + 8 * l);
+      else
+        what[b] = 3;
+    }
+#pragma unroll
+    for (int b = 0; b < kRotBatch; ++b) {
+      if (j0 - grp + b * kRows >= last) break;  // (uniform in the warp)
+      float x[8];
+      unpack8(in[b], x);
+      const __nv_bfloat16* w = what[b] < 2 ? a.weight[what[b]] : nullptr;
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+#pragma unroll
+      for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (w) {
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        float wf[8];
+        unpack8(*reinterpret_cast<const uint4*>(w + 8 * l), wf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= r * wf[e];
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x[e];
+      if constexpr (INTER) {
+        if (turned && what[b] < 2) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
+            y[2 * e + 1] = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_sync(0xffffffffu, x[e], partner);
+          if (turned && what[b] < 2) y[e] = x[e] * cs[e] + sign * o * sn[e];
+        }
+      }
+      const uint4 bits = what[b] == 2 ? in[b] : pack8(y);
+      if (what[b] < 2 && a.out[what[b]])
+        *reinterpret_cast<uint4*>(a.out[what[b]] + t * a.out_tok[what[b]] + head[b] * a.out_head[what[b]] + 8 * l) =
+            bits;
+      float sc = 0.f;
+      if constexpr (Q8) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        sc = __fdiv_rn(m, 127.f);
+      }
+      if (what[b] == 0 || what[b] == 3 || page < 0) continue;
+      uint8_t* base = what[b] == 1 ? a.pages.k : a.pages.v;
+      const int64_t at = page_elem(a.pages, page, head[b], row) + 8 * l;
+      const int64_t slot = page_slot(a.pages, page, head[b], row);
+      if constexpr (Q8) {
+        uint2 c = make_uint2(0u, 0u);
+        if (sc > 0.f) {
+          const float rs = __frcp_rn(sc);
+          c.x = pack4(code(y[0], sc, rs), code(y[1], sc, rs), code(y[2], sc, rs), code(y[3], sc, rs));
+          c.y = pack4(code(y[4], sc, rs), code(y[5], sc, rs), code(y[6], sc, rs), code(y[7], sc, rs));
+        }
+        *reinterpret_cast<uint2*>(base + at) = c;
+        if (l == 0) (what[b] == 1 ? a.pages.k_scale : a.pages.v_scale)[slot] = sc;
+      } else {
+        *reinterpret_cast<uint4*>(base + 2 * at) = bits;
+      }
+      if (l == 0 && what[b] == 1) {
+        if (a.pages.mass) a.pages.mass[slot] = 0.f;
+        if (a.pages.order) a.pages.order[slot] = order;
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace aircache
+
+using namespace aircache;
+
+extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status, void* stream) {
+  if (!p) return AIRCACHE_ERR_INVALID_ARG;
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  auto strides = [](int64_t tok, int64_t head) { return tok >= 0 && head >= 0 && tok % 8 == 0 && head % 8 == 0; };
+  if (p->dtype != AIRCACHE_BF16 || (p->head_dim != 64 && p->head_dim != 128) || p->num_tokens < 0 ||
+      p->num_tokens > 0x7fffffffLL || p->num_seqs < 0 || p->num_seqs > 65535 || p->reserved0 != 0 ||
+      (p->interleaved & ~1) != 0 || !(p->eps >= 0.f) || (!p->q && !p->k) || (!p->q) != (!p->q_out) ||
+      (p->q && p->h_q <= 0) || (p->k && p->h_kv <= 0) || p->h_q > 65535 || p->h_kv > 65535 ||
+      (p->k && !p->k_out && !p->pages) || (!p->k && (p->k_out || p->pages)) || (!p->v) != (!p->pages))
+    return AIRCACHE_ERR_INVALID_ARG;
+  if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 16 != 0 || (p->rotary_dim && !p->turns) ||
+      (p->axes != 1 && p->axes != 3) || (p->axes == 3 && (p->section0 < 0 || p->section1 < 0 ||
+       (int64_t)p->section0 + p->section1 > p->rotary_dim / 2 || !p->positions)))
+    return AIRCACHE_ERR_INVALID_ARG;
+  if (!al16(p->q) || !al16(p->k) || !al16(p->v) || !al16(p->q_out) || !al16(p->k_out) || !al16(p->q_weight) ||
+      !al16(p->k_weight) || !al16(p->turns) || (p->q && !strides(p->q_stride_tok, p->q_stride_head)) ||
+      (p->k && !strides(p->k_stride_tok, p->k_stride_head)) || (p->v && !strides(p->v_stride_tok, p->v_stride_head)) ||
+      (p->q_out && !strides(p->qo_stride_tok, p->qo_stride_head)) ||
+      (p->k_out && !strides(p->ko_stride_tok, p->ko_stride_head)))
+    return AIRCACHE_ERR_INVALID_ARG;
+  // in place means the same rows, not shifted ones
+  if ((p->q && p->q_out == p->q && (p->qo_stride_tok != p->q_stride_tok || p->qo_stride_head != p->q_stride_head)) ||
+      (p->k_out && p->k_out == p->k &&
+       (p->ko_stride_tok != p->k_stride_tok || p->ko_stride_head != p->k_stride_head)))
+    return AIRCACHE_ERR_INVALID_ARG;
+  RotArgs a = {};
+  bool q8 = false;
+  if (p->pages) {
+    const int rc = check_pages(p->pages, a.pages);
+    if (rc != AIRCACHE_OK) return rc;
+    if (p->pages->num_seqs != p->num_seqs || p->pages->h_kv != p->h_kv || p->pages->head_dim != p->head_dim ||
+        !p->cu_tokens || (p->pages->order && !p->seen))
+      return AIRCACHE_ERR_INVALID_ARG;
+    q8 = p->pages->kv_dtype == AIRCACHE_INT8;
+  }
+  if (p->rotary_dim && !p->positions && (!p->seen || !p->cu_tokens)) return AIRCACHE_ERR_INVALID_ARG;
+  if (p->num_tokens == 0 || (p->cu_tokens && p->num_seqs == 0)) return AIRCACHE_OK;
+  a.src[0] = static_cast<const __nv_bfloat16*>(p->q);
+  a.src[1] = static_cast<const __nv_bfloat16*>(p->k);
+  a.src[2] = static_cast<const __nv_bfloat16*>(p->v);
+  a.src_tok[0] = p->q_stride_tok, a.src_head[0] = p->q_stride_head;
+  a.src_tok[1] = p->k_stride_tok, a.src_head[1] = p->k_stride_head;
+  a.src_tok[2] = p->v_stride_tok, a.src_head[2] = p->v_stride_head;
+  a.out[0] = static_cast<__nv_bfloat16*>(p->q_out);
+  a.out[1] = static_cast<__nv_bfloat16*>(p->k_out);
+  a.out_tok[0] = p->qo_stride_tok, a.out_head[0] = p->qo_stride_head;
+  a.out_tok[1] = p->ko_stride_tok, a.out_head[1] = p->ko_stride_head;
+  a.weight[0] = static_cast<const __nv_bfloat16*>(p->q_weight);
+  a.weight[1] = static_cast<const __nv_bfloat16*>(p->k_weight);
+  a.turns = reinterpret_cast<const float2*>(p->turns);
+  a.positions = p->positions;
+  a.cu_tokens = p->cu_tokens;
+  a.seen = p->seen;
+  a.status = status;
+  a.num_tokens = p->num_tokens;
+  a.num_seqs = p->num_seqs;
+  a.h_q = p->q ? p->h_q : 0;
+  a.h_kv = p->k ? p->h_kv : 0;
+  a.heads = a.h_q + a.h_kv + (p->pages ? a.h_kv : 0);
+  a.rot = p->rotary_dim;
+  a.axes = p->axes;
+  a.sec0 = p->section0;
+  a.sec1 = p->section1;
+  a.has_pages = p->pages != nullptr;
+  a.per = a.heads;
+  a.eps = p->eps;
+  const dim3 grid((unsigned)((p->num_tokens + kRotWarps - 1) / kRotWarps), (a.heads + a.per - 1) / a.per);
+  const dim3 block(kRotWarps * 32);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void (*kernel)(RotArgs);
+  if (p->head_dim == 128)
+    kernel = q8 ? (p->interleaved ? rotate_kernel<128, true, true> : rotate_kernel<128, true, false>)
+                : (p->interleaved ? rotate_kernel<128, false, true> : rotate_kernel<128, false, false>);
+  else
+    kernel = q8 ? (p->interleaved ? rotate_kernel<64, true, true> : rotate_kernel<64, true, false>)
+                : (p->interleaved ? rotate_kernel<64, false, true> : rotate_kernel<64, false, false>);
+  return launch_pdl(kernel, grid, block, 0, s, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
+}
