@@ -555,8 +555,8 @@ AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t
  * head_dim 64 or 128, kv_dtype AIRCACHE_BF16 or AIRCACHE_INT8 (with both
  * scales), page_rows a multiple of 16 in 16..4096, max_pages >= 1 with
  * max_pages * page_rows <= 2^31 - 2^16, 1 <= num_pages <= 2^31 - 1, table_stride >=
- * max_pages; k and v 16-byte aligned, strides positive multiples of 16 bytes.
- * Device-side, a length outside [0, max_pages * page_rows] or a page outside
+ * max_pages; k, v, the scales, mass and order 16-byte aligned, strides positive
+ * multiples of 16 bytes.  Device-side, a length outside [0, max_pages * page_rows] or a page outside
  * [0, num_pages) sets AIRCACHE_ERR_DEVICE_BOUNDS; nothing is then read or
  * written through it (each entry point says what becomes of the sequence).
  */
@@ -731,7 +731,7 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  * (lens_out[s] = lens[s]).
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): mass; order when sink or recent
  * is not 0, seen when recent is not 0; order_out exactly with order; sink, recent >= 0.  Workspace as
- * for aircache_paged_decode.  One kernel.
+ * for aircache_paged_decode.  Two kernels: one selects, one moves.
  */
 #define AIRCACHE_MAX_EVICT_ROWS 393216
 

@@ -45,14 +45,14 @@ inline int check_pages(const aircache_pages* p, Pages& d) {
     return AIRCACHE_ERR_INVALID_ARG;
   const bool q8 = p->kv_dtype == AIRCACHE_INT8;
   const int64_t unit = q8 ? 16 : 8;
-  // the scale arrays are read in pieces of 16 floats: they start on 16 bytes too
+  // scales, mass and order are read in pieces of 4 and 16 values: they start on 16 bytes too
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
   if (!al16(p->k) || !al16(p->v) || p->stride_page <= 0 || p->stride_row <= 0 || p->stride_head <= 0 ||
       p->stride_page % unit != 0 || p->stride_row % unit != 0 || p->stride_head % unit != 0 ||
       (q8 && (!p->k_scale || !p->v_scale || !al16(p->k_scale) || !al16(p->v_scale))))
     return AIRCACHE_ERR_INVALID_ARG;
   auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
-  if (!al4(p->table) || !al4(p->lens) || !al4(p->mass) || !al4(p->order)) return AIRCACHE_ERR_INVALID_ARG;
+  if (!al4(p->table) || !al4(p->lens) || !al16(p->mass) || !al16(p->order)) return AIRCACHE_ERR_INVALID_ARG;
   d.k = static_cast<uint8_t*>(p->k);
   d.v = static_cast<uint8_t*>(p->v);
   d.stride_page = p->stride_page;
