@@ -719,8 +719,8 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  * ceil(lens_out[s] / page_rows) are the caller's again.
  *
  * mass_out and order_out are pages->mass and pages->order (in place) or other
- * arrays of their shape, which then get the entries of all rows below
- * lens_out[s] and nothing else.  lens is read by every KV head and lens_out
+ * arrays of their shape and alignment, which then get the entries of all rows below
+ * lens_out[s] and nothing else (of a sequence in error: some of its entries).  lens is read by every KV head and lens_out
  * must be another array (several layers are cut by the same lens before it
  * takes lens_out's values).
  *

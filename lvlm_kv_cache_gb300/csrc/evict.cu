@@ -9,10 +9,13 @@
 //
 // select: one thread-block cluster (or, for short sequences, one CTA) per
 // (sequence, KV head).  Each CTA holds the keys of a slice of the rows in
-// shared memory (the mass as an order-preserving integer); the threshold is
-// found by radix selection, four digits of 8 bits, adding up the CTAs'
-// histograms through distributed shared memory.  Its warps then walk over
-// consecutive rows and list vacated rows and movers in order.  Bound by the
+// shared memory (the mass as an order-preserving integer).  The threshold is
+// found by histograms of 256 equal parts of the range that is left, from the
+// keys' least to their largest, added up through distributed shared memory, and so on
+// within the threshold's part: spread over their bins however the masses are (digits
+// of fixed places would put most rows into a few bins and serialise their
+// atomics).  Its warps then walk over consecutive rows, four to a lane, and list vacated rows
+// and movers in order.  Bound by the
 // chain of barriers and scans: 8 bytes a row are read.
 // move: CTAs over all SMs copy the listed rows, 32 moves to a warp at a time.
 // Bound by HBM.
@@ -51,14 +54,15 @@ struct Before {
   uint32_t less, more;      // rows under the threshold below keep; rows over it at keep and behind
 };
 
+constexpr int kBinBits = 8, kBins = 1 << kBinBits;
+
 struct EvShared {
-  uint32_t hist[4][256];
-  uint32_t spread[256][8];  // the first digit's counts, eight copies: few values, many rows
-  uint32_t total[256];
+  uint32_t hist[4][kBins];
   Before warp[kEvWarps];
   Before sum;
-  uint32_t digit, above;
-  int bad;
+  uint32_t scan[kEvWarps], scan2[kEvWarps], scan3[kEvWarps];
+  uint32_t least, most, safe, bad;  // this CTA's least and largest key, protected rows, bad pages
+  uint32_t bin, above;
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -74,14 +78,17 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// CL: a cluster of gridDim.x CTAs per (sequence, KV head); else one CTA.
-template <bool CL>
+// R CTAs (a cluster) per (sequence, KV head).  What they tell each other is read
+// by one lane per CTA at once, or by loads that do not wait for one another: a
+// load from another CTA's shared memory takes several hundred cycles.
+template <int R>
 __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvArgs a) {
   extern __shared__ uint32_t ev_keys[];
   __shared__ EvShared sh;
   const Pages& p = a.pages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ranks = CL ? gridDim.x : 1, rank = CL ? blockIdx.x : 0;  // the cluster spans x
+  constexpr bool CL = R > 1;
+  const int rank = CL ? blockIdx.x : 0;  // the cluster spans x
   const int h = blockIdx.y, s = blockIdx.z;
   auto sync_all = [] {
     if (CL)
@@ -91,8 +98,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   };
   auto peer = [&](const uint32_t* x, int r) { return CL ? ld_cluster_u32(cluster_map(smem_u32(x), r)) : *x; };
   pdl_trigger();
-  for (int i = tid; i < 4 * 256; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
-  for (int i = tid; i < 8 * 256; i += kEvThreads) (&sh.spread[0][0])[i] = 0;
+  for (int i = tid; i < 4 * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
   if (tid == 0) sh.bad = 0;
   __syncthreads();
   pdl_wait();
@@ -103,23 +109,29 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   if (!sane && tid == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
   const int n = sane ? len : 0;
   const bool cut = sane && n > keep;
-  const int per = ((n + ranks - 1) / ranks + 15) & ~15;
+  const int per = ((n + R - 1) / R + 15) & ~15;
   const int lo = min(rank * per, n), mine = min(per, n - lo);  // this CTA's rows
   const int32_t* table = p.table + (int64_t)s * p.table_stride;
   const int32_t fresh = a.seen && a.recent ? a.seen[s] - a.recent : 0x7fffffff;  // order from which rows are recent
   const bool aged = a.sink | a.recent;
 
-  // ---- keys of the slice, and the first digit's counts.  Four rows a thread
+  // Where mass and order go to other arrays, every row below the new length is
+  // copied on the way; the moves overwrite the vacated ones
+  const bool copy_mass = a.mass_out != p.mass, copy_order = a.order_out && a.order_out != p.order;
+  const int new_len = cut ? keep : n;
+
+  // ---- keys of the slice, their range and the protected rows.  Four rows a thread
   // (a page holds a multiple of 16), four such groups in flight
   constexpr int kFlight = 4;
+  uint32_t least = kProtected, most = 0, safe = 0;
   for (int i0 = 4 * tid; i0 < mine; i0 += 4 * kFlight * kEvThreads) {
-    int page[kFlight];
+    int page[kFlight], at[kFlight];
     float4 m[kFlight];
     int4 o[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int i = i0 + 4 * f * kEvThreads;
-      page[f] = i < mine ? table[(lo + i) / p.page_rows] : 0;
+      const int i = i0 + 4 * f * kEvThreads, x = page_of(p, lo + i, at[f]);
+      page[f] = i < mine ? table[x] : 0;
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
@@ -128,9 +140,9 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       o[f] = make_int4(0, 0, 0, 0);
       if (i < mine) {
         if (page_ok(p, page[f])) {
-          const int64_t slot = page_slot(p, page[f], h, (lo + i) % p.page_rows);
+          const int64_t slot = page_slot(p, page[f], h, at[f]);
           m[f] = *reinterpret_cast<const float4*>(p.mass + slot);
-          if (aged) o[f] = *reinterpret_cast<const int4*>(p.order + slot);
+          if (aged || copy_order) o[f] = *reinterpret_cast<const int4*>(p.order + slot);
         } else {
           sh.bad = 1;
         }
@@ -142,74 +154,103 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       if (i >= mine) break;
       const float mm[4] = {m[f].x, m[f].y, m[f].z, m[f].w};
       const int oo[4] = {o[f].x, o[f].y, o[f].z, o[f].w};
+      const int keep_out = new_len - lo - i;  // of these four rows, how many lie below the new length
+      if ((copy_mass || copy_order) && keep_out > 0 && page_ok(p, page[f])) {
+        const int64_t slot = page_slot(p, page[f], h, at[f]);
+        if (keep_out >= 4) {
+          if (copy_mass) *reinterpret_cast<float4*>(a.mass_out + slot) = m[f];
+          if (copy_order) *reinterpret_cast<int4*>(a.order_out + slot) = o[f];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 3; ++j) {
+            if (copy_mass && j < keep_out) a.mass_out[slot + j] = mm[j];
+            if (copy_order && j < keep_out) a.order_out[slot + j] = oo[j];
+          }
+        }
+      }
       uint32_t key[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        key[j] = aged && (oo[j] < a.sink || oo[j] >= fresh) ? kProtected : mass_key(mm[j]);
-        if (cut && i + j < mine) atomicAdd(&sh.spread[key[j] >> 24][lane & 7], 1u);
+        const bool in = i + j < mine;
+        key[j] = !in || (aged && (oo[j] < a.sink || oo[j] >= fresh)) ? kProtected : mass_key(mm[j]);
+        least = min(least, key[j]);
+        most = max(most, key[j] + 1);  // (a protected row wraps to 0)
+        safe += in && key[j] == kProtected;
       }
       *reinterpret_cast<uint4*>(ev_keys + i) = make_uint4(key[0], key[1], key[2], key[3]);
     }
   }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  safe = __reduce_add_sync(0xffffffffu, safe);
+  if (lane == 0) sh.scan[warp] = least, sh.scan2[warp] = most, sh.scan3[warp] = safe;
   __syncthreads();
-  if (tid < 256) {
-    uint32_t c = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c += sh.spread[tid][j];
-    sh.hist[0][tid] = c;
+  if (warp == 0) {
+    const bool in = lane < kEvWarps;
+    least = __reduce_min_sync(0xffffffffu, in ? sh.scan[lane] : kProtected);
+    most = __reduce_max_sync(0xffffffffu, in ? sh.scan2[lane] : 0u);
+    safe = __reduce_add_sync(0xffffffffu, in ? sh.scan3[lane] : 0u);
+    if (lane == 0) sh.least = least, sh.most = most, sh.safe = safe;
   }
   sync_all();
-  bool bad = false;
-  for (int x = 0; x < ranks; ++x) bad |= peer(reinterpret_cast<const uint32_t*>(&sh.bad), x) != 0;
+  const int from = min(lane, R - 1);
+  least = __reduce_min_sync(0xffffffffu, peer(&sh.least, from));
+  most = __reduce_max_sync(0xffffffffu, peer(&sh.most, from));
+  safe = peer(&sh.safe, from);
+  safe = __reduce_add_sync(0xffffffffu, lane < R ? safe : 0u);
+  const bool bad = __reduce_max_sync(0xffffffffu, peer(&sh.bad, from)) != 0;
   if (bad && tid == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
   const bool go = cut && !bad;
 
-  // ---- the keep-th largest key, digit by digit
-  uint32_t prefix = 0, need = keep;  // need: rows still to take among those that share the prefix
-  if (go && keep > 0) {
-    for (int d = 0; d < 4; ++d) {
-      const int shift = 24 - 8 * d;
-      if (d > 0) {
-        for (int i = tid; i < mine; i += kEvThreads) {
-          const uint32_t key = ev_keys[i];
-          if ((key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[d][(key >> shift) & 255], 1u);
-        }
-        sync_all();
-      }
-      if (tid < 256) {
-        uint32_t c = 0;
+  // ---- the threshold, and how many of the rows at it stay (`need`).  Protected
+  // rows stay, unless there are more of them than places
+  uint32_t prefix = kProtected, need = keep;
+  if (go && safe < (uint32_t)keep) {
+    need = keep - safe;
+    prefix = least;  // where the range that is left begins
+    int shift = 32 - __clz(most - 1 - least);  // its keys: prefix .. prefix + 2^shift - 1
+    for (int d = 0; shift > 0; ++d) {
+      const uint32_t top = shift;
+      shift = max(0, shift - kBinBits);
+      // (no protected row, nor what fills the last group of four, lies in it)
+      const uint32_t left = min(top > 31 ? 0xffffffffu : (1u << top) - 1, kProtected - 1 - prefix);
+      for (int i = 4 * tid; i < mine; i += 4 * kEvThreads) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
+        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-        for (int x = 0; x < (CL ? kEvMaxCluster : 1); ++x)
-          if (x < ranks) c += peer(&sh.hist[d][tid], x);
-        sh.total[tid] = c;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t off = key[j] - prefix;  // (a key below the range wraps past it)
+          if (off <= left) atomicAdd(&sh.hist[d][off >> shift], 1u);
+        }
+      }
+      sync_all();
+      // from the largest bin down, a bin to each of the first threads
+      uint32_t c = 0;
+      if (tid < kBins) {
+        uint32_t v[R];
+#pragma unroll
+        for (int x = 0; x < R; ++x) v[x] = peer(&sh.hist[d][kBins - 1 - tid], x);
+#pragma unroll
+        for (int x = 0; x < R; ++x) c += v[x];
+      }
+      uint32_t incl = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += t;
+      }
+      if (lane == 31) sh.scan[warp] = incl;
+      __syncthreads();
+      uint32_t above = incl - c;
+#pragma unroll
+      for (int w = 0; w < kBins / 32; ++w)
+        if (w < warp) above += sh.scan[w];
+      if (tid < kBins && above < need && above + c >= need) {
+        sh.bin = kBins - 1 - tid;
+        sh.above = above;
       }
       __syncthreads();
-      if (warp == 0) {  // lane 0 has the largest digits
-        uint32_t c[8], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = sh.total[255 - 8 * lane - i];
-        uint32_t incl = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += t;
-        }
-        uint32_t above = incl - sum;
-        if (above < need && incl >= need) {
-          int digit = 0;
-          uint32_t over = 0;
-          bool found = false;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (!found && above + c[i] >= need) found = true, digit = 255 - 8 * lane - i, over = above;
-            above += c[i];
-          }
-          sh.digit = digit;
-          sh.above = over;
-        }
-      }
-      __syncthreads();
-      prefix |= sh.digit << shift;
+      prefix += sh.bin << shift;
       need -= sh.above;
     }
   }
@@ -217,19 +258,44 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   // ---- ranks.  Of the rows at the threshold the `need` lowest stay, so with T
   // ties, L lesser rows (below keep) and M greater rows (at keep and behind) before a row, L + T -
   // min(T, need) rows were vacated and M + min(T, need) - min(ties below keep, need) moved.
-  // A warp walks over consecutive rows
-  const int span = ((mine + kEvWarps - 1) / kEvWarps + 31) & ~31;
+  // A warp walks over consecutive rows, a lane over four of them at a time
+  const int span = ((mine + kEvWarps - 1) / kEvWarps + 127) & ~127;
   const int w0 = min(warp * span, mine), w1 = min(w0 + span, mine);
   if (go) {
     Before b = {0, 0, 0, 0};
-    for (int i = w0 + lane; i - lane < w1; i += 32) {
-      const uint32_t key = i < w1 ? ev_keys[i] : 0;
-      const bool in = i < w1, low = lo + i < keep;
-      b.ties += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
-      b.ties_low += __popc(__ballot_sync(0xffffffffu, in && low && key == prefix));
-      b.less += __popc(__ballot_sync(0xffffffffu, in && low && key < prefix));
-      b.more += __popc(__ballot_sync(0xffffffffu, in && !low && key > prefix));
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+      const int i = i0 + 4 * lane;
+      if (i0 + 128 <= w1 && (lo + i0 + 128 <= keep || lo + i0 >= keep)) {  // all below keep, or none
+        const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
+        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+        uint32_t tie = 0, over = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tie += key[j] == prefix;
+          over += key[j] > prefix;
+        }
+        b.ties += tie;
+        if (lo + i0 >= keep)
+          b.more += over;
+        else
+          b.ties_low += tie, b.less += 4 - tie - over;
+      } else if (i < w1) {
+        const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
+        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = i + j < w1, low = lo + i + j < keep, tie = in && key[j] == prefix;
+          b.ties += tie;
+          b.ties_low += tie && low;
+          b.less += in && low && key[j] < prefix;
+          b.more += in && !low && key[j] > prefix;
+        }
+      }
     }
+    b.ties = __reduce_add_sync(0xffffffffu, b.ties);
+    b.ties_low = __reduce_add_sync(0xffffffffu, b.ties_low);
+    b.less = __reduce_add_sync(0xffffffffu, b.less);
+    b.more = __reduce_add_sync(0xffffffffu, b.more);
     if (lane == 0) sh.warp[warp] = b;
     __syncthreads();
     if (tid == 0) {
@@ -245,36 +311,88 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
     }
     sync_all();
     Before at = {0, 0, 0, 0};  // before this warp's rows
-    uint32_t ties_low = 0, less = 0;
-    for (int x = 0; x < ranks; ++x) {
-      const uint32_t t = peer(&sh.sum.ties, x), tl = peer(&sh.sum.ties_low, x), l = peer(&sh.sum.less, x),
-                     m = peer(&sh.sum.more, x);
-      if (x < rank) at.ties += t, at.less += l, at.more += m;
-      ties_low += tl;
-      less += l;
-    }
+    const uint32_t t_ = peer(&sh.sum.ties, from), l_ = peer(&sh.sum.less, from), m_ = peer(&sh.sum.more, from),
+                   tl_ = peer(&sh.sum.ties_low, from);
+    at.ties = __reduce_add_sync(0xffffffffu, lane < rank ? t_ : 0u);
+    at.less = __reduce_add_sync(0xffffffffu, lane < rank ? l_ : 0u);
+    at.more = __reduce_add_sync(0xffffffffu, lane < rank ? m_ : 0u);
+    const uint32_t ties_low = __reduce_add_sync(0xffffffffu, lane < R ? tl_ : 0u);
+    const uint32_t less = __reduce_add_sync(0xffffffffu, lane < R ? l_ : 0u);
 #pragma unroll
     for (int w = 0; w < kEvWarps; ++w)
       if (w < warp) at.ties += sh.warp[w].ties, at.less += sh.warp[w].less, at.more += sh.warp[w].more;
-    if (keep == 0) at.more = 0;
     const uint32_t stay_low = min(ties_low, need);
     int32_t* list = a.lists + ((int64_t)s * p.h_kv + h) * 2 * a.half;
-    const uint32_t under = (1u << lane) - 1;
-    for (int i = w0 + lane; i - lane < w1 && keep > 0; i += 32) {
-      const uint32_t key = i < w1 ? ev_keys[i] : 0;
-      const bool in = i < w1, low = lo + i < keep;
-      const uint32_t tie = __ballot_sync(0xffffffffu, in && key == prefix);
-      const uint32_t lesser = __ballot_sync(0xffffffffu, in && low && key < prefix);
-      const uint32_t greater = __ballot_sync(0xffffffffu, in && !low && key > prefix);
-      const uint32_t t = at.ties + __popc(tie & under);  // ties before this row
-      const bool stays = key > prefix || (key == prefix && t < need);
-      if (in && low && !stays) list[at.less + __popc(lesser & under) + t - min(t, need)] = lo + i;
-      if (in && !low && stays)
-        list[a.half + at.more + __popc(greater & under) + min(t, need) - stay_low] = lo + i;
-      if (in) ev_keys[i] = stays;
-      at.ties += __popc(tie);
-      at.less += __popc(lesser);
-      at.more += __popc(greater);
+    // the warp's rows are compacted over its own keys, vacated rows (below keep,
+    // so they come first) before movers, and written out in whole lines
+    const uint32_t hole0 = at.less + at.ties - min(at.ties, need);
+    const uint32_t mover0 = at.more + min(at.ties + b.ties_low, need);
+    const uint32_t holes = b.less + b.ties_low - (min(at.ties + b.ties_low, need) - min(at.ties, need));
+    uint32_t* const packed = ev_keys + w0;
+    for (int i0 = w0; i0 < w1 && keep > 0; i0 += 128) {
+      const int i = i0 + 4 * lane;
+      const uint4 k4 = i < w1 ? *reinterpret_cast<const uint4*>(ev_keys + i) : make_uint4(0, 0, 0, 0);
+      const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+      const bool tied = key[0] == prefix || key[1] == prefix || key[2] == prefix || key[3] == prefix;
+      if (i0 + 128 <= w1 && (lo + i0 + 128 <= keep || lo + i0 >= keep) && !__any_sync(0xffffffffu, tied)) {
+        // 128 rows on one side of keep and off the threshold: only lesser or only greater rows count
+        const bool high = lo + i0 >= keep;
+        uint32_t is[4], c = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c += is[j] = (key[j] > prefix) == high;
+        uint32_t incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += t;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31), stay = min(at.ties, need);
+        uint32_t* to = packed + incl - c + (high ? holes + at.more + stay - mover0 : at.less + at.ties - stay - hole0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (is[j]) *to++ = lo + i + j;
+        if (high)
+          at.more += all;
+        else
+          at.less += all;
+        continue;
+      }
+      uint32_t c = 0;  // ties, lesser, greater rows of this lane: ten bits each
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = i + j < w1, low = lo + i + j < keep;
+        c += (in && key[j] == prefix) + ((uint32_t)(in && low && key[j] < prefix) << 10) +
+             ((uint32_t)(in && !low && key[j] > prefix) << 20);
+      }
+      uint32_t incl = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += t;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+      incl -= c;
+      __syncwarp();  // the keys of these rows are read, before earlier places are written
+      uint32_t t = at.ties + (incl & 1023), l = at.less + (incl >> 10 & 1023), m = at.more + (incl >> 20);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = i + j < w1, low = lo + i + j < keep;
+        const bool tie = key[j] == prefix, stays = key[j] > prefix || (tie && t < need);
+        if (in && low && !stays) packed[l + t - min(t, need) - hole0] = lo + i + j;
+        if (in && !low && stays) packed[holes + m + min(t, need) - mover0] = lo + i + j;
+        t += in && tie;
+        l += in && low && key[j] < prefix;
+        m += in && !low && key[j] > prefix;
+      }
+      at.ties += all & 1023;
+      at.less += all >> 10 & 1023;
+      at.more += all >> 20;
+    }
+    __syncwarp();
+    if (keep > 0) {
+      const uint32_t movers = at.more + min(at.ties, need) - mover0;
+      for (uint32_t e = lane; e < holes; e += 32) list[hole0 + e] = packed[e];
+      for (uint32_t e = lane; e < movers; e += 32) list[a.half + mover0 - stay_low + e] = packed[holes + e];
     }
     if (tid == 0 && rank == 0) a.moves[(int64_t)s * p.h_kv + h] = keep > 0 ? less + ties_low - stay_low : 0;
   } else if (tid == 0 && rank == 0) {
@@ -282,18 +400,6 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   }
   if (tid == 0 && rank == 0 && h == 0) a.lens_out[s] = go ? keep : len;
 
-  // ---- rows that stay where they are: mass and order, if these go to other arrays
-  const bool copy_mass = a.mass_out != p.mass, copy_order = a.order_out && a.order_out != p.order;
-  if ((copy_mass || copy_order) && sane && !bad) {
-    __syncthreads();
-    const int new_len = cut ? keep : n;
-    for (int i = tid; i < mine && lo + i < new_len; i += kEvThreads) {
-      if (go && !ev_keys[i]) continue;
-      const int64_t slot = page_slot(p, table[(lo + i) / p.page_rows], h, (lo + i) % p.page_rows);
-      if (copy_mass) a.mass_out[slot] = p.mass[slot];
-      if (copy_order) a.order_out[slot] = p.order[slot];
-    }
-  }
   if (CL) cluster_sync_all();  // shared memory stays readable until every rank is done
 }
 
@@ -319,8 +425,9 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const __grid_con
     const int cnt = min(32, moves - m0);
     if (lane < cnt) {
       const int to = list[m0 + lane], from = list[a.half + m0 + lane];
-      const int tp = table[to / p.page_rows], fp = table[from / p.page_rows];
-      const int tr = to % p.page_rows, fr = from % p.page_rows;
+      int tr, fr;
+      const int tx = page_of(p, to, tr), fx = page_of(p, from, fr);
+      const int tp = table[tx], fp = table[fx];
       const int64_t ds = page_slot(p, tp, h, tr), ss = page_slot(p, fp, h, fr);
       a.mass_out[ds] = p.mass[ss];
       if (a.order_out) a.order_out[ds] = p.order[ss];
@@ -363,7 +470,8 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   const int rc = check_pages(p->pages, pl.pages);
   if (rc != AIRCACHE_OK) return rc;
   if (!p->keep || !p->lens_out || p->lens_out == p->pages->lens || !p->pages->mass || !p->mass_out ||
-      (!p->order_out) != (!p->pages->order) || p->sink < 0 || p->recent < 0 ||
+      (!p->order_out) != (!p->pages->order) || (reinterpret_cast<uintptr_t>(p->mass_out) & 15) != 0 ||
+      (reinterpret_cast<uintptr_t>(p->order_out) & 15) != 0 || p->sink < 0 || p->recent < 0 ||
       ((p->sink || p->recent) && !p->pages->order) || (p->recent && !p->seen) || p->max_rows < 1)
     return AIRCACHE_ERR_INVALID_ARG;
   if (p->max_rows > AIRCACHE_MAX_EVICT_ROWS) return AIRCACHE_ERR_UNSUPPORTED;
@@ -375,7 +483,7 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   // but at least 2048 rows to a CTA (each rank costs every barrier and
   // histogram sum), and as many as the keys need room
   int ranks = 1;
-  while (ranks < kEvMaxCluster && (units * ranks * 2 <= 2 * pl.sms) && p->max_rows > 2048LL * ranks) ranks *= 2;
+  while (ranks < kEvMaxCluster && (units * ranks * 2 <= 2LL * pl.sms) && p->max_rows > 2048LL * ranks) ranks *= 2;
   while (p->max_rows > (int64_t)kEvSlice * ranks) ranks *= 2;
   pl.ranks = ranks;
   pl.row_bytes = p->pages->head_dim * (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2);
@@ -386,12 +494,12 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   return AIRCACHE_OK;
 }
 
-template <bool CL>
+template <int R>
 int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
-  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<CL>), (int)pl.smem) != cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<R>), (int)pl.smem) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.ranks, a.pages.h_kv, a.pages.num_seqs);
+  cfg.gridDim = dim3(R, a.pages.h_kv, a.pages.num_seqs);
   cfg.blockDim = dim3(kEvThreads);
   cfg.dynamicSmemBytes = pl.smem;
   cfg.stream = s;
@@ -399,12 +507,12 @@ int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = pl.ranks;
+  attr[1].val.clusterDim.x = R;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CL ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CL>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
+  cfg.numAttrs = R > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
 }
 
 template <int RB>
@@ -453,7 +561,10 @@ int aircache_evict(const aircache_evict_problem* p, void* ws, size_t ws_bytes, v
   a.sink = p->sink;
   a.recent = p->recent;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sel = pl.ranks > 1 ? launch_select<true>(pl, a, s) : launch_select<false>(pl, a, s);
+  const int sel = pl.ranks == 1   ? launch_select<1>(pl, a, s)
+                  : pl.ranks == 2 ? launch_select<2>(pl, a, s)
+                  : pl.ranks == 4 ? launch_select<4>(pl, a, s)
+                                  : launch_select<8>(pl, a, s);
   if (sel != AIRCACHE_OK) return sel;
   switch (pl.row_bytes) {
     case 256: return launch_move<16>(pl, a, s);

@@ -23,7 +23,17 @@ struct Pages {
   int32_t* order;
   int64_t num_pages;
   int num_seqs, h_kv, page_rows, max_rows;  // max_rows: the table's capacity of one sequence
+  uint32_t page_inv;                        // 2^32 / (page_rows / 16), rounded up (0: page_rows is 16)
 };
+
+// row / page_rows and row % page_rows for rows below 2^24: pages hold d = page_rows / 16
+// pieces of 16 rows, and piece * page_inv / 2^32 is off by less than 1 / d, since piece * d < 2^32.
+__device__ __forceinline__ int page_of(const Pages& p, int row, int& in_page) {
+  const uint32_t piece = (uint32_t)row >> 4;
+  const int page = (int)(p.page_inv ? __umulhi(piece, p.page_inv) : piece);
+  in_page = row - page * p.page_rows;
+  return page;
+}
 
 // The slot of (page, row) of KV head h in the scale, mass and order arrays.
 __device__ __forceinline__ int64_t page_slot(const Pages& p, int page, int h, int row) {
@@ -70,6 +80,8 @@ inline int check_pages(const aircache_pages* p, Pages& d) {
   d.h_kv = p->h_kv;
   d.page_rows = p->page_rows;
   d.max_rows = p->max_pages * p->page_rows;
+  const uint64_t pieces = p->page_rows / 16;
+  d.page_inv = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
   return AIRCACHE_OK;
 }
 
