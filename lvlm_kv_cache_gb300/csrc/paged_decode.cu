@@ -51,7 +51,7 @@ struct PdCfg {
   static constexpr int kScratch = kPdGroup * D * 4;           // the warps' joined O
   static constexpr int kScales = Q8 ? kStages * 2 * kPdRows * 4 : 0;
   static constexpr int kMl = kPdWarps * kPdGroup * 3 * 4;     // (m, l, n) of each warp and head
-  static constexpr int kSmem = 1024 + kRing + kScratch + kScales + kMl + kStages * (8 + 8 + 4) + 256;
+  static constexpr int kSmem = 1024 + kRing + kScratch + kScales + kMl + kStages * (8 + 8 + 4) + 448;
   static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
 };
 
@@ -96,95 +96,130 @@ __device__ __forceinline__ int rows_of(const Pages& p, int s) {
   return n >= 0 && n <= p.max_rows ? n : 0;
 }
 
-// A run of tiles of one (sequence, KV head): what a CTA does at a time.
+// How the batch's tiles are dealt out: the units (the sequences' KV heads) lie
+// one after the other on a line, each with its tiles and then `kPdEnd` places
+// without work, which stand for the time that a unit's end costs the CTAs it
+// falls to (merging the warps, writing, joining, the next queries).  CTA c
+// takes the places c * per .. c * per + per - 1, so the parts of a unit go to
+// consecutive CTAs and only its first and its last run can be a part.
+constexpr uint32_t kPdEnd = 4;
+
+// A run of tiles of one unit: what a CTA does at a time.
 struct Run {
-  int s, h, len, tiles;  // the unit: its sequence, KV head, rows and tiles
-  int first, count;      // the CTA's tiles of it
-  int64_t at, left;      // list index of tile `first`; tiles of the CTA from there on
+  int s, h, len;         // the unit: its sequence, KV head and rows,
+  uint32_t tiles, unit;  // tiles and its first place on the line;
+  uint32_t first, count; // the CTA's tiles of it,
+  uint32_t at;           // the batch's tiles before `first`
 };
 
-// Moves to the next unit that has tiles; false at the end of the CTA's share.
-__device__ __forceinline__ bool next_run(const Pages& p, Run& r) {
-  r.at += r.count;
-  r.left -= r.count;
-  if (r.left <= 0) return false;
+// The part of unit (s, h) at place `unit` that lies in the CTA's places lo .. hi-1.
+__device__ __forceinline__ void clip_run(Run& r, uint32_t lo, uint32_t hi) {
+  const uint32_t from = max(r.unit, lo), to = min(r.unit + r.tiles, hi);
+  r.first = from - r.unit;
+  r.count = to > from ? to - from : 0;
+}
+
+// Moves to the next unit that has tiles in the CTA's places; false if there is none.
+__device__ __forceinline__ bool next_run(const Pages& p, Run& r, uint32_t lo, uint32_t hi) {
+  r.at += r.tiles - r.first;
+  r.unit += r.tiles + kPdEnd;
+  if (r.unit >= hi) return false;
   if (++r.h == p.h_kv) {
     r.h = 0;
-    do {  // tiles are left, so a sequence with rows follows
+    do {
       if (++r.s >= p.num_seqs) return false;
       r.len = rows_of(p, r.s);
     } while (r.len == 0);
     r.tiles = (r.len + kPdRows - 1) / kPdRows;
   }
-  r.first = 0;
-  r.count = (int)(r.left < r.tiles ? r.left : r.tiles);
+  clip_run(r, lo, hi);
   return true;
 }
 
-// The batch's tile count and this CTA's first run, by all threads of the CTA
-// (n_thr of them): lengths are summed in parts of consecutive sequences.
 struct Share {
-  int64_t total, per;
+  int32_t tiles;  // of the batch; negative: too many, and nothing is computed
+  uint32_t per, lo, hi;
+  Run run;        // the CTA's first (count may be 0: the places behind a unit)
+};
+struct ShareScratch {
+  uint32_t places[8], tiles[8];
+  int64_t rows[8];
   Run run;
 };
-__device__ __forceinline__ Share make_share(const PdArgs& a, int n_thr, int64_t* scan, Run* found) {
+// By all threads of the CTA: lengths are summed by runs of consecutive sequences, one to a thread.
+__device__ __forceinline__ Share make_share(const PdArgs& a, ShareScratch* sc) {
   const Pages& p = a.pages;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = n_thr / 32;
-  const int part = (p.num_seqs + n_thr - 1) / n_thr;
-  const int s0 = min(tid * part, p.num_seqs), s1 = min(s0 + part, p.num_seqs);
-  int64_t tiles = 0, rows = 0;
+  constexpr int kWarps = kPdThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.num_seqs + kPdThreads - 1) / kPdThreads;
+  const int s0 = min(tid * each, p.num_seqs), s1 = min(s0 + each, p.num_seqs);
+  uint32_t tiles = 0, places = 0;
+  int64_t rows = 0;
   for (int s = s0; s < s1; ++s) {
     const int n = rows_of(p, s);
     if (n != p.lens[s] && blockIdx.x == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
-    tiles += (n + kPdRows - 1) / kPdRows;
+    const uint32_t t = (n + kPdRows - 1) / kPdRows;
+    tiles += t;
+    places += t ? t + kPdEnd : 0;
     rows += n;
   }
-  int64_t incl = tiles;
+  uint32_t incl_p = places, incl_t = tiles;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t t = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += t;
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl_p, off), y = __shfl_up_sync(0xffffffffu, incl_t, off);
+    if (lane >= off) incl_p += x, incl_t += y;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, off);
-  if (lane == 31) scan[warp] = incl;
-  if (lane == 0) scan[8 + warp] = rows;
+  if (lane == 31) sc->places[warp] = incl_p, sc->tiles[warp] = incl_t;
+  if (lane == 0) sc->rows[warp] = rows;
   __syncthreads();
-  int64_t before = incl - tiles, total = 0, all = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-    all += scan[8 + w];
-  }
-  if (all > a.total_rows) {
-    if (blockIdx.x == 0 && tid == 0) set_error(a.error, AIRCACHE_ERR_CAPACITY);
-    total = -1;  // nothing is computed
+  uint32_t before = incl_p - places, tiles_before = incl_t - tiles, total = 0, all_tiles = 0;
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sc->places[w], tiles_before += sc->tiles[w];
+    total += sc->places[w];
+    all_tiles += sc->tiles[w];
+    all += sc->rows[w];
   }
   Share sh;
-  sh.total = total * p.h_kv;
-  sh.per = (sh.total + gridDim.x - 1) / gridDim.x;
-  const int64_t t0 = sh.per * blockIdx.x;
-  if (t0 < sh.total && t0 >= before * p.h_kv && t0 < (before + tiles) * p.h_kv) {
-    int64_t b = before * p.h_kv;
+  if (all > a.total_rows) {  // (only then could the counts above have passed 32 bits)
+    if (blockIdx.x == 0 && tid == 0) set_error(a.error, AIRCACHE_ERR_CAPACITY);
+    sh.tiles = -1;
+    sh.per = sh.lo = sh.hi = 0;
+    return sh;
+  }
+  const uint32_t h_kv = p.h_kv;
+  total *= h_kv;
+  sh.tiles = (int32_t)(all_tiles * h_kv);
+  sh.per = max(1u, (total + gridDim.x - 1) / gridDim.x);
+  sh.lo = min(sh.per * blockIdx.x, total);
+  sh.hi = min(sh.lo + sh.per, total);
+  if (sh.lo < sh.hi && sh.lo >= before * h_kv && sh.lo < (before + places) * h_kv) {
+    uint32_t at = before * h_kv, t_at = tiles_before * h_kv;
     for (int s = s0; s < s1; ++s) {
-      const int n = rows_of(p, s), t = (n + kPdRows - 1) / kPdRows;
-      if (t0 < b + (int64_t)t * p.h_kv) {
-        found->s = s;
-        found->h = (int)((t0 - b) / t);
-        found->len = n;
-        found->tiles = t;
-        found->first = (int)((t0 - b) % t);
-        found->at = t0;
-        found->left = (sh.total - t0 < sh.per ? sh.total - t0 : sh.per);
-        found->count = (int)(found->left < t - found->first ? found->left : t - found->first);
+      const int n = rows_of(p, s);
+      const uint32_t t = (n + kPdRows - 1) / kPdRows, wide = t ? t + kPdEnd : 0;
+      if (sh.lo < at + wide * h_kv) {
+        Run r;
+        r.s = s;
+        r.h = (int)((sh.lo - at) / wide);
+        r.len = n;
+        r.tiles = t;
+        r.unit = at + r.h * wide;
+        clip_run(r, sh.lo, sh.hi);
+        if (r.count == 0) r.first = t;
+        r.at = t_at + r.h * t + r.first;
+        sc->run = r;
         break;
       }
-      b += (int64_t)t * p.h_kv;
+      at += wide * h_kv;
+      t_at += t * h_kv;
     }
   }
   __syncthreads();
-  sh.run = *found;
-  if (t0 >= sh.total) sh.run.left = sh.run.count = 0;
+  sh.run = sc->run;
   return sh;
 }
 
@@ -200,9 +235,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   float* mlw = reinterpret_cast<float*>(ring + C::kRing + C::kScratch + C::kScales);  // [4][16][3]
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(mlw) + C::kMl);
   uint64_t* empty = full + C::kStages;
-  int64_t* scan = reinterpret_cast<int64_t*>(empty + C::kStages);  // [16]
-  Run* found = reinterpret_cast<Run*>(scan + 16);
-  uint32_t* pieces = reinterpret_cast<uint32_t*>(found + 1);       // [stages] which pieces of a tile are there
+  ShareScratch* share = reinterpret_cast<ShareScratch*>(empty + C::kStages);
+  uint32_t* pieces = reinterpret_cast<uint32_t*>(share + 1);  // [stages] which pieces of a tile are there
   int* ctl = reinterpret_cast<int*>(pieces + C::kStages);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -221,8 +255,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   pdl_wait();
-  const Share sh = make_share(a, kPdThreads, scan, found);  // (its barriers publish the mbarriers too)
-  if (blockIdx.x == 0 && tid == 0) *a.tiles = (int)(sh.total > 0 ? sh.total : 0);
+  const Share sh = make_share(a, share);  // (its barriers publish the mbarriers too)
+  if (blockIdx.x == 0 && tid == 0) *a.tiles = max(sh.tiles, 0);
   Run r = sh.run;
 
   if (warp == kPdWarps) {
@@ -231,14 +265,14 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     int st = 0;
     uint32_t phase = 0, filled = 0;
     bool alive = true;
-    for (bool more = r.left > 0; more && alive; more = next_run(p, r)) {
+    for (bool more = sh.lo < sh.hi; more && alive; more = next_run(p, r, sh.lo, sh.hi)) {
       const int32_t* table = p.table + (int64_t)r.s * p.table_stride;
       int page = -1;
-      for (int i = 0; i < r.count; ++i) {
+      for (uint32_t i = 0; i < r.count; ++i) {
         if ((i & 7) == 0) {
-          const int row = ((r.first + i) * 4 + lane) * 16;
+          const int row = (int)((r.first + i) * 4 + lane) * 16;
           page = -1;
-          if (row < r.len && row < (r.first + r.count) * kPdRows) {
+          if (row < r.len && row < (int)((r.first + r.count) * kPdRows)) {
             page = table[row / p.page_rows];
             if (!page_ok(p, page)) {
               set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
@@ -263,7 +297,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           mbar_arrive_expect_tx(&full[st], __popc(mask) * (2 * C::kPiece + (Q8 ? 128 : 0)));
         }
         __syncwarp();
-        const int row = (((r.first + i) * 4 + piece) * 16) % p.page_rows;
+        const int row = (int)(((r.first + i) * 4 + piece) * 16) % p.page_rows;
         if (pg >= 0 && lane < 8) {
           fence_proxy_async_smem();
           const uint32_t to = smem_u32(dst) + (lane >= 4 ? C::kTile : 0);
@@ -282,7 +316,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           }
         }
         if (a.mass_out) {
-          const int64_t t = r.at + i;
+          const uint32_t t = r.at + i;
           if (lane < 4) a.info[t].page[lane] = pg;
           if (lane == 4) *reinterpret_cast<int4*>(&a.info[t]) = make_int4(r.s, r.h, r.first + i, 0);
         }
@@ -296,7 +330,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   // ---- consumers
   const int hA = lane >> 2, cq = lane & 3;  // accumulator rows (heads) hA and hA + 8, columns 2cq, 2cq + 1
   // sequences without rows: out = 0, lse = -inf
-  for (int s = blockIdx.x; s < p.num_seqs && sh.total >= 0; s += gridDim.x) {
+  for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
     for (int i = tid; i < a.h_q * D / 8; i += kPdWarps * 32)
       *reinterpret_cast<uint4*>(a.out + (int64_t)s * a.h_q * D + i * 8) = make_uint4(0, 0, 0, 0);
@@ -305,7 +339,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   int st = 0;
   uint32_t phase = 0;
   bool alive = true;
-  for (bool more = r.left > 0; more; more = next_run(p, r)) {
+  for (bool more = sh.lo < sh.hi; more; more = next_run(p, r, sh.lo, sh.hi)) {
+    if (r.count == 0) continue;
     // ---- the group's queries as A fragments (rows at or past g: zeros)
     uint32_t qa[D / 16][4];
     {
@@ -367,13 +402,13 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
     float nA = -INFINITY, nB = -INFINITY;  // O's own reference (int8 rows; else unused)
 
-    for (int i = 0; i < r.count && alive; ++i) {
+    for (uint32_t i = 0; i < r.count && alive; ++i) {
       if (!mbar_wait(&full[st], phase)) {
         if (lane == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
         alive = false;
         break;
       }
-      const int valid = (pieces[st] >> warp) & 1 ? min(16, r.len - (r.first + i) * kPdRows - 16 * warp) : 0;
+      const int valid = (pieces[st] >> warp) & 1 ? min(16, r.len - (int)(r.first + i) * kPdRows - 16 * warp) : 0;
       if (valid > 0) {
         uint8_t* kt = ring + st * C::kStageBytes + warp * C::kPiece;
         uint8_t* vt = kt + C::kTile;
@@ -442,7 +477,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
             tB = fmaxf(tB, sc[t][2 + e]);
           }
         if (a.mass_out) {
-          float* lg = a.logits + (r.at + i) * g * kPdRows + 16 * warp + 2 * cq;
+          float* lg = a.logits + (int64_t)(r.at + i) * g * kPdRows + 16 * warp + 2 * cq;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (hA < g) *reinterpret_cast<float2*>(lg + hA * kPdRows + 8 * t) = make_float2(sc[t][0], sc[t][1]);
@@ -633,9 +668,11 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       continue;
     }
     // ---- a part of a unit: the partial result, then the join by the unit's last CTA.
-    // CTA c's part goes to slot 2c when the unit began before c, to 2c + 1 when it began in c.
+    // CTA c's part goes to slot 2c when the unit began before c, to 2c + 1 when it began in c
+    const int c0 = (int)(r.unit / sh.per), parts = (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1;
+    auto slot_of = [&](int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
     {
-      const int64_t slot = 2 * (int64_t)blockIdx.x + (r.first == 0 ? 1 : 0);
+      const int64_t slot = slot_of(blockIdx.x - c0);
       for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
         const int hh = c / (D / 4), d = c % (D / 4) * 4;
         *reinterpret_cast<float4*>(a.part_o + (slot * g + hh) * D + d) =
@@ -647,8 +684,6 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         }
       }
     }
-    const int64_t u0 = r.at - r.first;  // the unit's first tile
-    const int c0 = (int)(u0 / sh.per), c1 = (int)((u0 + r.tiles - 1) / sh.per), parts = c1 - c0 + 1;
     __threadfence();
     named_bar_sync(1, kPdWarps * 32);
     uint32_t* count = a.count + (int64_t)r.s * p.h_kv + r.h;
@@ -659,26 +694,42 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     __threadfence();
     for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
       const int hh = c / (D / 4), d = c % (D / 4) * 4;
-      const int64_t first = 2 * (int64_t)c0 + 1;  // then 2 (c0 + j)
-      auto at = [&](int j) { return (j == 0 ? first : 2 * (int64_t)(c0 + j)) * g + hh; };
+      auto at = [&](int j) { return slot_of(j) * g + hh; };
+      // eight parts' loads in flight: the unit's last CTA is what the call waits for
+      constexpr int kFlight = 8;
       float m = -INFINITY, n = -INFINITY, l = 0.f;
-      for (int j = 0; j < parts; ++j) {
-        const float4 x = __ldcg(a.part_ml + at(j));
-        m = fmaxf(m, x.x);
-        n = fmaxf(n, x.z);
-      }
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int j = 0; j < parts; ++j) {
-        const float4 x = __ldcg(a.part_ml + at(j));
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(j) * D + d));
-        if (x.x == -INFINITY) continue;
-        l += x.y * fast_exp2(x.x - m);
-        const float f = fast_exp2(x.z - n);
-        acc.x += f * y.x;
-        acc.y += f * y.y;
-        acc.z += f * y.z;
-        acc.w += f * y.w;
+      for (int j0 = 0; j0 < parts; j0 += kFlight) {
+        float4 x[kFlight], y[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+          const int64_t j = at(min(j0 + f, parts - 1));
+          x[f] = __ldcg(a.part_ml + j);
+          y[f] = __ldcg(reinterpret_cast<const float4*>(a.part_o + j * D + d));
+        }
+        float m1 = m, n1 = n;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+          if (j0 + f >= parts) x[f].x = x[f].z = -INFINITY;  // (a part without rows has them so)
+          m1 = fmaxf(m1, x[f].x);
+          n1 = fmaxf(n1, x[f].z);
+        }
+        if (m1 == -INFINITY) continue;
+        l *= fast_exp2(m - m1);
+        float c = fast_exp2(n - n1);
+        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+          if (x[f].x == -INFINITY) continue;
+          l += x[f].y * fast_exp2(x[f].x - m1);
+          c = fast_exp2(x[f].z - n1);
+          acc.x += c * y[f].x;
+          acc.y += c * y[f].y;
+          acc.z += c * y[f].z;
+          acc.w += c * y[f].w;
+        }
+        m = m1;
+        n = n1;
       }
       const float f = l > 0.f ? kUndo * fast_exp2(n - m) / l : 0.f;
       __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
@@ -748,7 +799,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&pl.sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
-  if (pl.tiles > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
+  if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
   pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2LL * pl.sms, pl.tiles));
   pl.lse_off = kPdHeader + up256(sizeof(uint32_t) * (size_t)units);
   pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
