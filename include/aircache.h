@@ -671,9 +671,9 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  *
  * The work is split by rows, not by sequences: every CTA takes the same number
  * of 64-row tiles of the batch's (sequence, KV head) list, whatever the lengths,
- * and the parts of one (sequence, KV head) are joined by the last of its CTAs,
- * in a fixed order.  With mass_out a second kernel turns the logits, which the
- * first leaves in the workspace, into weights.
+ * and a second kernel joins the parts of each (sequence, KV head), in a fixed
+ * order.  With mass_out it also turns the logits, which the first then leaves in
+ * the workspace, into weights.
  *
  * total_rows bounds the sum of lens; it sizes the grid and the workspace.  A
  * larger sum sets AIRCACHE_ERR_CAPACITY and nothing is computed.  A sequence
@@ -682,7 +682,7 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  * Requirements: dtype AIRCACHE_BF16; h_q a multiple of h_kv (else
  * AIRCACHE_ERR_INVALID_ARG) with at most 16 query heads to a KV head (else
  * AIRCACHE_ERR_UNSUPPORTED); 1 <= total_rows <= 2^31 - 2^16; scale > 0 and finite; q 16-byte
- * aligned and its strides multiples of 8; out 16-byte aligned, dense; mass_out
+ * aligned and its strides multiples of 8; out and mass_out 16-byte aligned, dense; mass_out
  * only with pages->mass.
  *
  * The workspace is caller-owned, 256-byte aligned, ZEROED ONCE before its first

@@ -70,8 +70,8 @@ struct PdArgs {
   float* mass_out;
   int32_t* error;
   int32_t* tiles;    // tile count, for the mass kernel
-  uint32_t* count;   // [S * h_kv] arrivals
-  float* lse2;       // [S * h_q] base 2
+  int2* unit;        // [S * h_kv]: the first CTA that has a part of it, and how many have one
+  float* lse2;       // [S * h_q] base 2, of units that one CTA has whole
   float4* part_ml;   // [2 CTAs][g]: m, l, n of O
   float* part_o;     // [2 CTAs][g][D]
   TileInfo* info;    // [tiles]
@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   uint64_t* empty = full + C::kStages;
   ShareScratch* share = reinterpret_cast<ShareScratch*>(empty + C::kStages);
   uint32_t* pieces = reinterpret_cast<uint32_t*>(share + 1);  // [stages] which pieces of a tile are there
-  int* ctl = reinterpret_cast<int*>(pieces + C::kStages);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.group;
@@ -335,6 +334,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     for (int i = tid; i < a.h_q * D / 8; i += kPdWarps * 32)
       *reinterpret_cast<uint4*>(a.out + (int64_t)s * a.h_q * D + i * 8) = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < a.h_q && a.lse; i += kPdWarps * 32) a.lse[(int64_t)s * a.h_q + i] = -INFINITY;
+    for (int i = tid; i < p.h_kv; i += kPdWarps * 32) a.unit[s * p.h_kv + i] = make_int2(0, 0);
   }
   int st = 0;
   uint32_t phase = 0;
@@ -648,6 +648,10 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       const int ds = Q8 ? 8 * (d % (D / 8)) + d / (D / 8) : d;
       return scratch[hh * D + (((ds >> 1) ^ ((hh & 3) << 2)) << 1) + (ds & 1)];
     };
+    if (tid == 0 && r.first == 0) {
+      const int c0 = (int)(r.unit / sh.per);
+      a.unit[r.s * p.h_kv + r.h] = make_int2(c0, (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1);
+    }
     const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
     constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
     auto finish = [&](int hh, float m, float l) {  // the head's log-sum-exp
@@ -667,74 +671,80 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       }
       continue;
     }
-    // ---- a part of a unit: the partial result, then the join by the unit's last CTA.
-    // CTA c's part goes to slot 2c when the unit began before c, to 2c + 1 when it began in c
-    const int c0 = (int)(r.unit / sh.per), parts = (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1;
-    auto slot_of = [&](int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
-    {
-      const int64_t slot = slot_of(blockIdx.x - c0);
-      for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
-        const int hh = c / (D / 4), d = c % (D / 4) * 4;
-        *reinterpret_cast<float4*>(a.part_o + (slot * g + hh) * D + d) =
-            make_float4(joined_o(hh, d), joined_o(hh, d + 1), joined_o(hh, d + 2), joined_o(hh, d + 3));
-        if (d == 0) {
-          float m, l, n;
-          joined(hh, m, l, n);
-          a.part_ml[slot * g + hh] = make_float4(m, l, n, 0.f);
-        }
-      }
-    }
-    __threadfence();
-    named_bar_sync(1, kPdWarps * 32);
-    uint32_t* count = a.count + (int64_t)r.s * p.h_kv + r.h;
-    if (tid == 0) ctl[0] = atomicAdd(count, 1u) == (uint32_t)(parts - 1);
-    named_bar_sync(1, kPdWarps * 32);
-    if (!ctl[0]) continue;
-    if (tid == 0) *count = 0;  // every call leaves the counters at zero
-    __threadfence();
+    // ---- a part of a unit: the join kernel adds it to the others.  CTA c's part goes
+    // to slot 2c when the unit began before c, to 2c + 1 when it began in c
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (r.first == 0 ? 1 : 0);
     for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
       const int hh = c / (D / 4), d = c % (D / 4) * 4;
-      auto at = [&](int j) { return slot_of(j) * g + hh; };
-      // eight parts' loads in flight: the unit's last CTA is what the call waits for
-      constexpr int kFlight = 8;
+      *reinterpret_cast<float4*>(a.part_o + (slot * g + hh) * D + d) =
+          make_float4(joined_o(hh, d), joined_o(hh, d + 1), joined_o(hh, d + 2), joined_o(hh, d + 3));
+      if (d == 0) {
+        float m, l, n;
+        joined(hh, m, l, n);
+        a.part_ml[slot * g + hh] = make_float4(m, l, n, 0.f);
+      }
+    }
+  }
+}
+
+// Joins the parts of the units that several CTAs shared: a unit to a CTA, four columns a thread.
+constexpr int kPjThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PdArgs a, float undo) {
+  pdl_trigger();
+  pdl_wait();
+  const Pages& p = a.pages;
+  const int tid = threadIdx.x, lane = tid & 31, g = a.group;
+  const int units = p.num_seqs * p.h_kv;
+  auto slot_of = [](int c0, int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int2 un = a.unit[u];  // its first CTA, its parts
+    if (un.y < 2) continue;
+    const int64_t head0 = (int64_t)u * g;  // (s h_kv + h) g = s h_q + h g
+    for (int c = tid; c < g * (D / 4); c += kPjThreads) {
+      const int hh = c / (D / 4), d = c % (D / 4) * 4;
+      constexpr int kFlight = 8;  // parts whose loads are in flight
       float m = -INFINITY, n = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j0 = 0; j0 < parts; j0 += kFlight) {
+      for (int j0 = 0; j0 < un.y; j0 += kFlight) {
         float4 x[kFlight], y[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-          const int64_t j = at(min(j0 + f, parts - 1));
-          x[f] = __ldcg(a.part_ml + j);
-          y[f] = __ldcg(reinterpret_cast<const float4*>(a.part_o + j * D + d));
+          const int64_t j = slot_of(un.x, min(j0 + f, un.y - 1)) * g + hh;
+          x[f] = a.part_ml[j];
+          y[f] = *reinterpret_cast<const float4*>(a.part_o + j * D + d);
         }
         float m1 = m, n1 = n;
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-          if (j0 + f >= parts) x[f].x = x[f].z = -INFINITY;  // (a part without rows has them so)
+          if (j0 + f >= un.y) x[f].x = x[f].z = -INFINITY;  // (a part without rows has them so)
           m1 = fmaxf(m1, x[f].x);
           n1 = fmaxf(n1, x[f].z);
         }
         if (m1 == -INFINITY) continue;
         l *= fast_exp2(m - m1);
-        float c = fast_exp2(n - n1);
-        acc.x *= c, acc.y *= c, acc.z *= c, acc.w *= c;
+        float k = fast_exp2(n - n1);
+        acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
           if (x[f].x == -INFINITY) continue;
           l += x[f].y * fast_exp2(x[f].x - m1);
-          c = fast_exp2(x[f].z - n1);
-          acc.x += c * y[f].x;
-          acc.y += c * y[f].y;
-          acc.z += c * y[f].z;
-          acc.w += c * y[f].w;
+          k = fast_exp2(x[f].z - n1);
+          acc.x += k * y[f].x;
+          acc.y += k * y[f].y;
+          acc.z += k * y[f].z;
+          acc.w += k * y[f].w;
         }
         m = m1;
         n = n1;
       }
-      const float f = l > 0.f ? kUndo * fast_exp2(n - m) / l : 0.f;
+      const float f = l > 0.f ? undo * fast_exp2(n - m) / l : 0.f;
       __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
       *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
-      if (d == 0) finish(hh, m, l);
+      if (d == 0) {
+        if (a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.mass_out) a.lse2[head0 + hh] = l > 0.f ? m + log2f(l) : INFINITY;
+      }
     }
   }
 }
@@ -756,14 +766,19 @@ __global__ void __launch_bounds__(256) paged_mass_kernel(const __grid_constant__
     const float* lg = a.logits + (int64_t)t * g * kPdRows + 2 * lane;
     const float* lse = a.lse2 + (int64_t)w.x * a.h_q + w.y * g;
     float x = 0.f, y = 0.f;
+#pragma unroll 4
     for (int hh = 0; hh < g; ++hh) {
       const float2 v = *reinterpret_cast<const float2*>(lg + hh * kPdRows);
       const float z = lse[hh];
       x += fast_exp2(v.x - z);
       y += fast_exp2(v.y - z);
     }
-    a.mass_out[slot] = p.mass[slot] + x;
-    if (row + 1 < len) a.mass_out[slot + 1] = p.mass[slot + 1] + y;
+    if (row + 1 < len) {
+      const float2 v = *reinterpret_cast<const float2*>(p.mass + slot);
+      *reinterpret_cast<float2*>(a.mass_out + slot) = make_float2(v.x + x, v.y + y);
+    } else {
+      a.mass_out[slot] = p.mass[slot] + x;
+    }
   }
 }
 
@@ -788,7 +803,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
       !(p->scale > 0.f) || !std::isfinite(p->scale) || p->total_rows < 1 || p->total_rows > 0x7fff0000LL || !p->q ||
       !p->out || !al16(p->q) || !al16(p->out) || p->q_stride_seq < 0 || p->q_stride_head < 0 ||
       p->q_stride_seq % 8 != 0 || p->q_stride_head % 8 != 0 || (p->mass_out && !p->pages->mass) ||
-      (reinterpret_cast<uintptr_t>(p->lse) & 3) != 0 || (reinterpret_cast<uintptr_t>(p->mass_out) & 3) != 0)
+      (reinterpret_cast<uintptr_t>(p->lse) & 3) != 0 || !al16(p->mass_out))
     return AIRCACHE_ERR_INVALID_ARG;
   pl.g = p->h_q / p->pages->h_kv;
   if (pl.g > kPdGroup) return AIRCACHE_ERR_UNSUPPORTED;
@@ -801,7 +816,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
   if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
   pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2LL * pl.sms, pl.tiles));
-  pl.lse_off = kPdHeader + up256(sizeof(uint32_t) * (size_t)units);
+  pl.lse_off = kPdHeader + up256(sizeof(int2) * (size_t)units);
   pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
   pl.o_off = pl.ml_off + up256(sizeof(float4) * 2 * (size_t)pl.grid * pl.g);
   pl.info_off = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.g * pl.d);
@@ -851,6 +866,12 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  const int64_t units = (int64_t)pl.pages.num_seqs * pl.pages.h_kv;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, 3LL * pl.sms));
+  cfg.blockDim = dim3(kPjThreads);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, Q8 ? 1.f / kP16 : 1.f) != cudaSuccess)
+    return AIRCACHE_ERR_CUDA;
   if (a.mass_out) {
     const int grid = (int)std::min<int64_t>((pl.tiles + 7) / 8, 8LL * pl.sms);
     if (launch_pdl(paged_mass_kernel, dim3(grid), dim3(256), 0, s, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
@@ -888,7 +909,7 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   a.mass_out = p->mass_out;
   a.error = reinterpret_cast<int32_t*>(w);
   a.tiles = reinterpret_cast<int32_t*>(w + 64);
-  a.count = reinterpret_cast<uint32_t*>(w + kPdHeader);
+  a.unit = reinterpret_cast<int2*>(w + kPdHeader);
   a.lse2 = reinterpret_cast<float*>(w + pl.lse_off);
   a.part_ml = reinterpret_cast<float4*>(w + pl.ml_off);
   a.part_o = reinterpret_cast<float*>(w + pl.o_off);
