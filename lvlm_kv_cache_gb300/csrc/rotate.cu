@@ -6,12 +6,13 @@
 // operations per 4 bytes moved: bound by HBM, or by latency for a handful of
 // tokens.
 //
-// D/8 lanes take one head's row, 16 bytes a lane, so a warp works on 2 (D =
+// D/8 lanes take one head's row, eight elements a lane, so a warp works on 2 (D =
 // 128) or 4 (D = 64) rows at once; it walks over the query, key and value heads
 // of ONE token, so that the token's sines and cosines are formed once, in the
-// registers of the lanes that need them, and the slot in the cache is looked
-// up once.  Half-style partners sit R/16 lanes away (one shuffle); interleaved
-// ones in the same lane.
+// registers of the lanes that need them, multiplied by the norm's weights, and the slot in
+// the cache is looked up once.  Both elements of a pair lie in one lane (half
+// style: four elements and the four half a rotation further), so a row costs no
+// shuffles but the norm's.  With few tokens a token's heads go to several warps.
 //
 // The angle: position * (hi + lo) turns is reduced before it is rounded.  The
 // position splits into two parts of at most 20 bits (exact in fp32), each
@@ -19,6 +20,8 @@
 // fused multiply-add, an error-free product), whole turns are dropped, and
 // the rest goes to sincospif: to about 2^-24 turns up to position 2^24, and to
 // 2^-19 turns at the far end of int32, where lo's own last bit shows.
+#include <algorithm>
+
 #include "int8code.cuh"
 #include "pages.cuh"
 
@@ -43,7 +46,7 @@ struct RotArgs {
   Pages pages;
   int num_seqs, h_q, h_kv, heads;  // heads: rows of one token that the call touches
   int rot, axes, sec0, sec1, has_pages;
-  int per;  // heads of one token that one warp takes
+  int per, shares;  // heads of one token that one warp takes, and warps to a token
   float eps;
 };
 
@@ -91,115 +94,83 @@ __device__ __forceinline__ void turn(int pos, float2 f, float& sn, float& cs) {
   sincospif(2.f * r, &sn, &cs);
 }
 
-template <int D, bool Q8, bool INTER>
-__global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_constant__ RotArgs a) {
-  constexpr int kLanes = D / 8;           // lanes of one row
-  constexpr int kRows = 32 / kLanes;      // rows a warp has at once
-  constexpr int kAngles = INTER ? 4 : 8;  // of one lane
-  const int lane = threadIdx.x & 31, l = lane % kLanes, grp = lane / kLanes;
-  const int64_t t = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
-  pdl_trigger();
-  pdl_wait();
-  if (t >= a.num_tokens) return;
-  const int first = blockIdx.y * a.per, last = min(first + a.per, a.heads);
+// What a lane does to each row of its token.
+struct Lane {
+  int e0, e1;           // its elements: e0 .. e0+3 and e1 .. e1+3
+  float cs[4], sn[4];   // of its four pairs
+  bool turned;          // false: elements behind rotary_dim
+  int page, row, order; // the token's slot (page < 0: none)
+};
 
-  // ---- the token's sequence, order and slot
-  int s = 0, order = 0;
-  if (a.cu_tokens) {
-    s = find_seq(a.cu_tokens, a.num_seqs, (int)t, lane);
-    if (s < 0 || s >= a.num_seqs) return;  // padding
-    const int back = a.cu_tokens[s + 1] - (int)t;
-    if (a.seen) order = a.seen[s] - back;
-  }
-  int page = -1, row = 0;
-  if (a.has_pages) {
-    const int len = a.pages.lens[s], back = a.cu_tokens[s + 1] - (int)t;
-    const int i = len - back;
-    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
-      page = a.pages.table[s * a.pages.table_stride + i / a.pages.page_rows];
-      row = i % a.pages.page_rows;
-      if (!page_ok(a.pages, page)) page = -1;
-    }
-    if (page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
-  }
-
-  // ---- this lane's angles (elements 8l .. 8l+7)
-  float sn[kAngles], cs[kAngles];
-  const bool turned = 8 * l < a.rot;
-  const int half = a.rot / 2;
-  if (turned) {
+// Heads first .. last-1 of the token: KIND 0 queries, 1 keys, 2 values.
+template <int D, bool Q8, bool INTER, int KIND>
+__device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, int64_t t, int first, int last,
+                                              int lane) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int l = lane % kLanes, grp = lane / kLanes;
+  const __nv_bfloat16* src = a.src[KIND] + t * a.src_tok[KIND];
+  // pair (u, v) of elements: u' = u c0 - v s1, v' = v c1 + u s0 (the weights inside)
+  float c0[4], c1[4], s0[4], s1[4];
+  const __nv_bfloat16* weight = KIND < 2 ? a.weight[KIND < 2 ? KIND : 0] : nullptr;
+  if (KIND < 2) {
+    float w[8];
 #pragma unroll
-    for (int e = 0; e < kAngles; ++e) {
-      const int i = INTER ? 4 * l + e : (8 * l + e < half ? 8 * l + e : 8 * l + e - half);
-      int pos = order;
-      if (a.positions) {
-        const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
-        pos = a.positions[axis * a.num_tokens + t];
-      }
-      turn(pos, a.turns[i], sn[e], cs[e]);
+    for (int e = 0; e < 8; ++e) w[e] = weight ? __bfloat162float(weight[(e < 4 ? x.e0 : x.e1 - 4) + e]) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float wu = INTER ? w[2 * e] : w[e], wv = INTER ? w[2 * e + 1] : w[4 + e];
+      c0[e] = x.cs[e] * wu;
+      c1[e] = x.cs[e] * wv;
+      s0[e] = x.sn[e] * wu;
+      s1[e] = x.sn[e] * wv;
     }
   }
-  // the partner's lane: R/16 lanes up for the lower half, down for the upper one
-  const int partner = turned ? (8 * l < half ? lane + half / 8 : lane - half / 8) : lane;
-  const float sign = 8 * l < half ? -1.f : 1.f;
-
-  for (int j0 = first + grp; j0 - grp < last; j0 += kRows * kRotBatch) {
-    uint4 in[kRotBatch];
-    int what[kRotBatch], head[kRotBatch];
+  for (int j0 = first; j0 < last; j0 += kRows * kRotBatch) {
+    uint2 lo[kRotBatch], hi[kRotBatch];
 #pragma unroll
     for (int b = 0; b < kRotBatch; ++b) {
-      const int j = j0 + b * kRows;
-      what[b] = j < a.h_q ? 0 : j < a.h_q + a.h_kv ? 1 : 2;
-      head[b] = j - (what[b] == 0 ? 0 : what[b] == 1 ? a.h_q : a.h_q + a.h_kv);
-      in[b] = make_uint4(0, 0, 0, 0);
-      if (j < last)
-        in[b] = *reinterpret_cast<const uint4*>(a.src[what[b]] + t * a.src_tok[what[b]] +
-                                                head[b] * a.src_head[what[b]] + 8 * l);
-      else
-        what[b] = 3;
+      const int j = j0 + b * kRows + grp;
+      lo[b] = hi[b] = make_uint2(0u, 0u);
+      if (j < last) {
+        const __nv_bfloat16* from = src + j * a.src_head[KIND];
+        lo[b] = *reinterpret_cast<const uint2*>(from + x.e0);
+        hi[b] = *reinterpret_cast<const uint2*>(from + x.e1);
+      }
     }
 #pragma unroll
     for (int b = 0; b < kRotBatch; ++b) {
-      if (j0 - grp + b * kRows >= last) break;  // (uniform in the warp)
-      float x[8];
-      unpack8(in[b], x);
-      const __nv_bfloat16* w = what[b] < 2 ? a.weight[what[b]] : nullptr;
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (w) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float wf[8];
-        unpack8(*reinterpret_cast<const uint4*>(w + 8 * l), wf);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= r * wf[e];
-      }
+      if (j0 + b * kRows >= last) break;  // (uniform in the warp)
+      const int j = j0 + b * kRows + grp;
       float y[8];
+      unpack8(make_uint4(lo[b].x, lo[b].y, hi[b].x, hi[b].y), y);
+      if (KIND < 2) {
+        float r = 1.f;
+        if (weight) {
+          float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[e];
-      if constexpr (INTER) {
-        if (turned && what[b] < 2) {
+          for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
-            y[2 * e + 1] = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
+          for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+          r = rsqrtf(ss * (1.f / D) + a.eps);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float& yu = INTER ? y[2 * e] : y[e];
+          float& yv = INTER ? y[2 * e + 1] : y[4 + e];
+          const float u = yu * r, v = yv * r;
+          yu = u * c0[e];
+          yv = v * c1[e];
+          if (x.turned) {  // (not by a zero sine: an infinite neighbour would spoil the element)
+            yu -= v * s1[e];
+            yv += u * s0[e];
           }
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(0xffffffffu, x[e], partner);
-          if (turned && what[b] < 2) y[e] = x[e] * cs[e] + sign * o * sn[e];
-        }
+        const uint4 bits = pack8(y);
+        lo[b] = make_uint2(bits.x, bits.y);
+        hi[b] = make_uint2(bits.z, bits.w);
       }
-      const uint4 bits = what[b] == 2 ? in[b] : pack8(y);
-      if (what[b] < 2 && a.out[what[b]])
-        *reinterpret_cast<uint4*>(a.out[what[b]] + t * a.out_tok[what[b]] + head[b] * a.out_head[what[b]] + 8 * l) =
-            bits;
       float sc = 0.f;
-      if constexpr (Q8) {
+      if constexpr (Q8 && KIND > 0) {
         float m = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
@@ -207,28 +178,102 @@ __global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_con
         for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         sc = __fdiv_rn(m, 127.f);
       }
-      if (what[b] == 0 || what[b] == 3 || page < 0) continue;
-      uint8_t* base = what[b] == 1 ? a.pages.k : a.pages.v;
-      const int64_t at = page_elem(a.pages, page, head[b], row) + 8 * l;
-      const int64_t slot = page_slot(a.pages, page, head[b], row);
+      if (j >= last) continue;
+      if (KIND < 2 && a.out[KIND < 2 ? KIND : 0]) {
+        __nv_bfloat16* to = a.out[KIND < 2 ? KIND : 0] + t * a.out_tok[KIND < 2 ? KIND : 0] +
+                            j * a.out_head[KIND < 2 ? KIND : 0];
+        *reinterpret_cast<uint2*>(to + x.e0) = lo[b];
+        *reinterpret_cast<uint2*>(to + x.e1) = hi[b];
+      }
+      if (KIND == 0 || x.page < 0) continue;
+      uint8_t* base = KIND == 1 ? a.pages.k : a.pages.v;
+      const int64_t at = page_elem(a.pages, x.page, j, x.row);
       if constexpr (Q8) {
-        uint2 c = make_uint2(0u, 0u);
+        uint32_t p0 = 0u, p1 = 0u;
         if (sc > 0.f) {
           const float rs = __frcp_rn(sc);
-          c.x = pack4(code(y[0], sc, rs), code(y[1], sc, rs), code(y[2], sc, rs), code(y[3], sc, rs));
-          c.y = pack4(code(y[4], sc, rs), code(y[5], sc, rs), code(y[6], sc, rs), code(y[7], sc, rs));
+          p0 = pack4(code(y[0], sc, rs), code(y[1], sc, rs), code(y[2], sc, rs), code(y[3], sc, rs));
+          p1 = pack4(code(y[4], sc, rs), code(y[5], sc, rs), code(y[6], sc, rs), code(y[7], sc, rs));
         }
-        *reinterpret_cast<uint2*>(base + at) = c;
-        if (l == 0) (what[b] == 1 ? a.pages.k_scale : a.pages.v_scale)[slot] = sc;
+        *reinterpret_cast<uint32_t*>(base + at + x.e0) = p0;
+        *reinterpret_cast<uint32_t*>(base + at + x.e1) = p1;
       } else {
-        *reinterpret_cast<uint4*>(base + 2 * at) = bits;
+        *reinterpret_cast<uint2*>(base + 2 * (at + x.e0)) = lo[b];
+        *reinterpret_cast<uint2*>(base + 2 * (at + x.e1)) = hi[b];
       }
-      if (l == 0 && what[b] == 1) {
-        if (a.pages.mass) a.pages.mass[slot] = 0.f;
-        if (a.pages.order) a.pages.order[slot] = order;
+      if (l == 0 && (KIND == 1 || Q8)) {
+        const int64_t slot = page_slot(a.pages, x.page, j, x.row);
+        if (Q8) (KIND == 1 ? a.pages.k_scale : a.pages.v_scale)[slot] = sc;
+        if (KIND == 1 && a.pages.mass) a.pages.mass[slot] = 0.f;
+        if (KIND == 1 && a.pages.order) a.pages.order[slot] = x.order;
       }
     }
   }
+}
+
+template <int D, bool Q8, bool INTER>
+__global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int kLanes = D / 8;
+  const int lane = threadIdx.x & 31, l = lane % kLanes;
+  const int64_t w = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
+  const int64_t t = w / a.shares;  // neighbouring warps share a token's heads
+  pdl_trigger();
+  pdl_wait();
+  if (t >= a.num_tokens) return;
+  const int first = (int)(w % a.shares) * a.per, last = min(first + a.per, a.heads);
+  const int q_end = min(last, a.h_q), k_end = min(last, a.h_q + a.h_kv);
+
+  // ---- the token's sequence, order and slot
+  Lane x;
+  int s = 0, back = 0;
+  x.order = 0;
+  if (a.cu_tokens) {
+    s = find_seq(a.cu_tokens, a.num_seqs, (int)t, lane);
+    if (s < 0 || s >= a.num_seqs) return;  // padding
+    back = a.cu_tokens[s + 1] - (int)t;
+    if (a.seen) x.order = a.seen[s] - back;
+  }
+  x.page = -1;
+  x.row = 0;
+  if (a.has_pages && last > a.h_q) {
+    const int len = a.pages.lens[s], i = len - back;
+    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
+      x.page = a.pages.table[s * a.pages.table_stride + i / a.pages.page_rows];
+      x.row = i % a.pages.page_rows;
+      if (!page_ok(a.pages, x.page)) x.page = -1;
+    }
+    if (x.page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
+  }
+
+  // ---- this lane's elements and angles
+  const int pairs = a.rot / 8;  // lanes whose elements turn
+  x.turned = l < pairs;
+  if (INTER) {
+    x.e0 = 8 * l;
+    x.e1 = 8 * l + 4;
+  } else {
+    x.e0 = x.turned ? 4 * l : 8 * l;
+    x.e1 = x.turned ? a.rot / 2 + 4 * l : 8 * l + 4;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x.cs[e] = 1.f, x.sn[e] = 0.f;
+  if (x.turned && first < a.h_q + a.h_kv) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 4 * l + e;
+      int pos = x.order;
+      if (a.positions) {
+        const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
+        pos = a.positions[axis * a.num_tokens + t];
+      }
+      turn(pos, a.turns[i], x.sn[e], x.cs[e]);
+    }
+  }
+  if (first < q_end) rows_of_token<D, Q8, INTER, 0>(a, x, t, first, q_end, lane);
+  if (max(first, a.h_q) < k_end)
+    rows_of_token<D, Q8, INTER, 1>(a, x, t, max(first, a.h_q) - a.h_q, k_end - a.h_q, lane);
+  if (max(first, a.h_q + a.h_kv) < last)
+    rows_of_token<D, Q8, INTER, 2>(a, x, t, max(first, a.h_q + a.h_kv) - a.h_q - a.h_kv, last - a.h_q - a.h_kv, lane);
 }
 
 }  // namespace
@@ -300,9 +345,17 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   a.sec0 = p->section0;
   a.sec1 = p->section1;
   a.has_pages = p->pages != nullptr;
-  a.per = a.heads;
   a.eps = p->eps;
-  const dim3 grid((unsigned)((p->num_tokens + kRotWarps - 1) / kRotWarps), (a.heads + a.per - 1) / a.per);
+  // A warp takes a whole token where that makes enough warps for the GPU (16 to an
+  // SM); with fewer tokens it takes as few rows as it has at once
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int at_once = p->head_dim == 128 ? 2 : 4;
+  const int64_t want = std::max<int64_t>(1, 16LL * sms / p->num_tokens);
+  a.per = (int)std::max<int64_t>(at_once, (a.heads + want - 1) / want);
+  a.per = (a.per + at_once - 1) / at_once * at_once;
+  a.shares = (a.heads + a.per - 1) / a.per;
+  const dim3 grid((unsigned)((p->num_tokens * a.shares + kRotWarps - 1) / kRotWarps));
   const dim3 block(kRotWarps * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void (*kernel)(RotArgs);
