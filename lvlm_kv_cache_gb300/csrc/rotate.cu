@@ -28,8 +28,13 @@
 namespace aircache {
 namespace {
 
-constexpr int kRotWarps = 8;
-constexpr int kRotBatch = 4;  // rows a lane group has in flight
+constexpr int kRotWarps = 4;
+
+// NB: rows a lane group works on at a time, while as many load.  Two, with 32 warps
+// to an SM, where there are tokens enough (15,541 tokens of 28 + 4 heads of 128: 58 us, and
+// 64 with four); four, with 24 warps, where a warp has to keep its own loads in flight
+// (3,447 tokens of 32 + 32 heads of 64: 17.7 us, and 20.7 with two).
+constexpr int kRotFew = 24;  // warps to an SM
 
 struct RotArgs {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -102,20 +107,52 @@ struct Lane {
   int page, row, order; // the token's slot (page < 0: none)
 };
 
-// Heads first .. last-1 of the token: KIND 0 queries, 1 keys, 2 values.
-template <int D, bool Q8, bool INTER, int KIND>
-__device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, int64_t t, int first, int last,
-                                              int lane) {
+// The next rows of a token's queries, keys or values, a lane's eight elements of each.
+template <int NB>
+struct Batch {
+  uint2 lo[NB], hi[NB];
+};
+// WIDE: the eight elements are one 16-byte piece (interleaved pairs, and values, which do not turn).
+template <int D, bool WIDE, int NB>
+__device__ __forceinline__ void load_rows(Batch<NB>& r, const __nv_bfloat16* src, int64_t head_stride, int j0, int last,
+                                          int e0, int e1, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int j = j0 + b * kRows + lane / kLanes;
+    r.lo[b] = r.hi[b] = make_uint2(0u, 0u);
+    if (j < last) {
+      const __nv_bfloat16* from = src + j * head_stride;
+      if (WIDE) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from + 8 * (lane % kLanes));
+        r.lo[b] = make_uint2(v.x, v.y);
+        r.hi[b] = make_uint2(v.z, v.w);
+      } else {
+        r.lo[b] = *reinterpret_cast<const uint2*>(from + e0);
+        r.hi[b] = *reinterpret_cast<const uint2*>(from + e1);
+      }
+    }
+  }
+}
+
+// Heads first .. last-1 of the token: KIND 0 queries, 1 keys, 2 values.  `r` holds the first of them.
+template <int D, bool Q8, bool INTER, int KIND, int NB>
+__device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, int64_t t, int first, int last,
+                                              int lane, Batch<NB>& r) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr bool kWide = INTER || KIND == 2;
   const int l = lane % kLanes, grp = lane / kLanes;
   const __nv_bfloat16* src = a.src[KIND] + t * a.src_tok[KIND];
   // pair (u, v) of elements: u' = u c0 - v s1, v' = v c1 + u s0 (the weights inside)
   float c0[4], c1[4], s0[4], s1[4];
   const __nv_bfloat16* weight = KIND < 2 ? a.weight[KIND < 2 ? KIND : 0] : nullptr;
   if (KIND < 2) {
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = weight ? __bfloat162float(weight[(e < 4 ? x.e0 : x.e1 - 4) + e]) : 1.f;
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (weight) {
+      const uint2 wl = *reinterpret_cast<const uint2*>(weight + x.e0);
+      const uint2 wh = *reinterpret_cast<const uint2*>(weight + x.e1);
+      unpack8(make_uint4(wl.x, wl.y, wh.x, wh.y), w);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float wu = INTER ? w[2 * e] : w[e], wv = INTER ? w[2 * e + 1] : w[4 + e];
@@ -125,39 +162,33 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
       s1[e] = x.sn[e] * wv;
     }
   }
-  for (int j0 = first; j0 < last; j0 += kRows * kRotBatch) {
-    uint2 lo[kRotBatch], hi[kRotBatch];
+  for (int j0 = first; j0 < last; j0 += kRows * NB) {
+    // the next rows load while these are worked on
+    Batch<NB> next;
+    load_rows<D, kWide>(next, src, a.src_head[KIND], j0 + kRows * NB, last, x.e0, x.e1, lane);
+    uint2* const lo = r.lo;
+    uint2* const hi = r.hi;
 #pragma unroll
-    for (int b = 0; b < kRotBatch; ++b) {
-      const int j = j0 + b * kRows + grp;
-      lo[b] = hi[b] = make_uint2(0u, 0u);
-      if (j < last) {
-        const __nv_bfloat16* from = src + j * a.src_head[KIND];
-        lo[b] = *reinterpret_cast<const uint2*>(from + x.e0);
-        hi[b] = *reinterpret_cast<const uint2*>(from + x.e1);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < kRotBatch; ++b) {
+    for (int b = 0; b < NB; ++b) {
       if (j0 + b * kRows >= last) break;  // (uniform in the warp)
       const int j = j0 + b * kRows + grp;
       float y[8];
       unpack8(make_uint4(lo[b].x, lo[b].y, hi[b].x, hi[b].y), y);
       if (KIND < 2) {
-        float r = 1.f;
+        float rms = 1.f;
         if (weight) {
           float ss = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
 #pragma unroll
           for (int off = kLanes / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          r = rsqrtf(ss * (1.f / D) + a.eps);
+          rms = rsqrtf(ss * (1.f / D) + a.eps);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float& yu = INTER ? y[2 * e] : y[e];
           float& yv = INTER ? y[2 * e + 1] : y[4 + e];
-          const float u = yu * r, v = yv * r;
+          const float u = yu * rms, v = yv * rms;
           yu = u * c0[e];
           yv = v * c1[e];
           if (x.turned) {  // (not by a zero sine: an infinite neighbour would spoil the element)
@@ -182,8 +213,12 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
       if (KIND < 2 && a.out[KIND < 2 ? KIND : 0]) {
         __nv_bfloat16* to = a.out[KIND < 2 ? KIND : 0] + t * a.out_tok[KIND < 2 ? KIND : 0] +
                             j * a.out_head[KIND < 2 ? KIND : 0];
-        *reinterpret_cast<uint2*>(to + x.e0) = lo[b];
-        *reinterpret_cast<uint2*>(to + x.e1) = hi[b];
+        if (kWide) {
+          *reinterpret_cast<uint4*>(to + 8 * l) = make_uint4(lo[b].x, lo[b].y, hi[b].x, hi[b].y);
+        } else {
+          *reinterpret_cast<uint2*>(to + x.e0) = lo[b];
+          *reinterpret_cast<uint2*>(to + x.e1) = hi[b];
+        }
       }
       if (KIND == 0 || x.page < 0) continue;
       uint8_t* base = KIND == 1 ? a.pages.k : a.pages.v;
@@ -195,8 +230,14 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
           p0 = pack4(code(y[0], sc, rs), code(y[1], sc, rs), code(y[2], sc, rs), code(y[3], sc, rs));
           p1 = pack4(code(y[4], sc, rs), code(y[5], sc, rs), code(y[6], sc, rs), code(y[7], sc, rs));
         }
-        *reinterpret_cast<uint32_t*>(base + at + x.e0) = p0;
-        *reinterpret_cast<uint32_t*>(base + at + x.e1) = p1;
+        if (kWide) {
+          *reinterpret_cast<uint2*>(base + at + 8 * l) = make_uint2(p0, p1);
+        } else {
+          *reinterpret_cast<uint32_t*>(base + at + x.e0) = p0;
+          *reinterpret_cast<uint32_t*>(base + at + x.e1) = p1;
+        }
+      } else if (kWide) {
+        *reinterpret_cast<uint4*>(base + 2 * (at + 8 * l)) = make_uint4(lo[b].x, lo[b].y, hi[b].x, hi[b].y);
       } else {
         *reinterpret_cast<uint2*>(base + 2 * (at + x.e0)) = lo[b];
         *reinterpret_cast<uint2*>(base + 2 * (at + x.e1)) = hi[b];
@@ -208,11 +249,12 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
         if (KIND == 1 && a.pages.order) a.pages.order[slot] = x.order;
       }
     }
+    r = next;
   }
 }
 
-template <int D, bool Q8, bool INTER>
-__global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_constant__ RotArgs a) {
+template <int D, bool Q8, bool INTER, int NB>
+__global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRotWarps) rotate_kernel(const __grid_constant__ RotArgs a) {
   constexpr int kLanes = D / 8;
   const int lane = threadIdx.x & 31, l = lane % kLanes;
   const int64_t w = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
@@ -223,8 +265,28 @@ __global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_con
   const int first = (int)(w % a.shares) * a.per, last = min(first + a.per, a.heads);
   const int q_end = min(last, a.h_q), k_end = min(last, a.h_q + a.h_kv);
 
-  // ---- the token's sequence, order and slot
+  // ---- this lane's elements, and its first rows, which load while the rest is looked up
   Lane x;
+  const int pairs = a.rot / 8;  // lanes whose elements turn
+  x.turned = l < pairs;
+  if (INTER) {
+    x.e0 = 8 * l;
+    x.e1 = 8 * l + 4;
+  } else {
+    x.e0 = x.turned ? 4 * l : 8 * l;
+    x.e1 = x.turned ? a.rot / 2 + 4 * l : 8 * l + 4;
+  }
+  const int kind = first < a.h_q ? 0 : first < a.h_q + a.h_kv ? 1 : 2;
+  const int kind0 = kind == 0 ? 0 : kind == 1 ? a.h_q : a.h_q + a.h_kv;
+  Batch<NB> r;
+  const __nv_bfloat16* from = a.src[kind] + t * a.src_tok[kind];
+  const int from_end = (kind == 0 ? q_end : kind == 1 ? k_end : last) - kind0;
+  if (INTER || kind == 2)
+    load_rows<D, true>(r, from, a.src_head[kind], first - kind0, from_end, x.e0, x.e1, lane);
+  else
+    load_rows<D, false>(r, from, a.src_head[kind], first - kind0, from_end, x.e0, x.e1, lane);
+
+  // ---- the token's sequence, order and slot
   int s = 0, back = 0;
   x.order = 0;
   if (a.cu_tokens) {
@@ -245,16 +307,7 @@ __global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_con
     if (x.page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
   }
 
-  // ---- this lane's elements and angles
-  const int pairs = a.rot / 8;  // lanes whose elements turn
-  x.turned = l < pairs;
-  if (INTER) {
-    x.e0 = 8 * l;
-    x.e1 = 8 * l + 4;
-  } else {
-    x.e0 = x.turned ? 4 * l : 8 * l;
-    x.e1 = x.turned ? a.rot / 2 + 4 * l : 8 * l + 4;
-  }
+  // ---- its angles
 #pragma unroll
   for (int e = 0; e < 4; ++e) x.cs[e] = 1.f, x.sn[e] = 0.f;
   if (x.turned && first < a.h_q + a.h_kv) {
@@ -269,11 +322,26 @@ __global__ void __launch_bounds__(kRotWarps * 32) rotate_kernel(const __grid_con
       turn(pos, a.turns[i], x.sn[e], x.cs[e]);
     }
   }
-  if (first < q_end) rows_of_token<D, Q8, INTER, 0>(a, x, t, first, q_end, lane);
-  if (max(first, a.h_q) < k_end)
-    rows_of_token<D, Q8, INTER, 1>(a, x, t, max(first, a.h_q) - a.h_q, k_end - a.h_q, lane);
-  if (max(first, a.h_q + a.h_kv) < last)
-    rows_of_token<D, Q8, INTER, 2>(a, x, t, max(first, a.h_q + a.h_kv) - a.h_q - a.h_kv, last - a.h_q - a.h_kv, lane);
+  if (first < q_end) rows_of_token<D, Q8, INTER, 0>(a, x, t, first, q_end, lane, r);
+  if (max(first, a.h_q) < k_end) {
+    const int from = max(first, a.h_q) - a.h_q, to = k_end - a.h_q;
+    if (kind < 1) load_rows<D, INTER>(r, a.src[1] + t * a.src_tok[1], a.src_head[1], from, to, x.e0, x.e1, lane);
+    rows_of_token<D, Q8, INTER, 1>(a, x, t, from, to, lane, r);
+  }
+  if (max(first, a.h_q + a.h_kv) < last) {
+    const int from = max(first, a.h_q + a.h_kv) - a.h_q - a.h_kv, to = last - a.h_q - a.h_kv;
+    if (kind < 2) load_rows<D, true>(r, a.src[2] + t * a.src_tok[2], a.src_head[2], from, to, x.e0, x.e1, lane);
+    rows_of_token<D, Q8, INTER, 2>(a, x, t, from, to, lane, r);
+  }
+}
+
+template <int D>
+auto rotate_pick(bool q8, bool inter, bool few) -> void (*)(RotArgs) {
+  if (few)
+    return q8 ? (inter ? rotate_kernel<D, true, true, 4> : rotate_kernel<D, true, false, 4>)
+              : (inter ? rotate_kernel<D, false, true, 4> : rotate_kernel<D, false, false, 4>);
+  return q8 ? (inter ? rotate_kernel<D, true, true, 2> : rotate_kernel<D, true, false, 2>)
+            : (inter ? rotate_kernel<D, false, true, 2> : rotate_kernel<D, false, false, 2>);
 }
 
 }  // namespace
@@ -358,12 +426,8 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   const dim3 grid((unsigned)((p->num_tokens * a.shares + kRotWarps - 1) / kRotWarps));
   const dim3 block(kRotWarps * 32);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void (*kernel)(RotArgs);
-  if (p->head_dim == 128)
-    kernel = q8 ? (p->interleaved ? rotate_kernel<128, true, true> : rotate_kernel<128, true, false>)
-                : (p->interleaved ? rotate_kernel<128, false, true> : rotate_kernel<128, false, false>);
-  else
-    kernel = q8 ? (p->interleaved ? rotate_kernel<64, true, true> : rotate_kernel<64, true, false>)
-                : (p->interleaved ? rotate_kernel<64, false, true> : rotate_kernel<64, false, false>);
+  const bool few = p->num_tokens * a.shares <= (int64_t)kRotFew * sms;
+  void (*kernel)(RotArgs) = p->head_dim == 128 ? rotate_pick<128>(q8, p->interleaved != 0, few)
+                                               : rotate_pick<64>(q8, p->interleaved != 0, few);
   return launch_pdl(kernel, grid, block, 0, s, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
 }

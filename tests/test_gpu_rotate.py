@@ -62,6 +62,24 @@ def test_dense_matches_definition(A, d, rot, h_q, h_kv, inter, norm):
         check(ko, k, w[1], 1e-5, angle, inter)
 
 
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 64, True), (64, 64, False), (64, 64, True)])
+def test_many_tokens(A, d, rot, inter):
+    # more tokens than warps stay on the GPU at once: the kernel's form for long prompts
+    g = torch.Generator(device="cuda").manual_seed(6)
+    T = 5003
+    q = torch.randn((T, 3, d), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((T, 2, d), generator=g, device="cuda").to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn((2, d), generator=g, device="cuda")).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    f = freqs(rot)
+    prob = A.RotateProblem(q, k, positions=pos, turns=A.rotation_table(torch.tensor(f)).cuda(), q_weight=w[0],
+                           k_weight=w[1], interleaved=inter)
+    A.rotate(prob)
+    angle = pos.double().cpu().numpy()[:, None] * f
+    check(prob.q_out, q, w[0], 1e-6, angle, inter)
+    check(prob.k_out, k, w[1], 1e-6, angle, inter)
+
+
 def test_three_axes(A):
     T, d = 300, 128
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -134,7 +152,7 @@ def append_case(A, lens_new, lens_old, int8, page_rows, d=128, h_q=7, h_kv=3, pa
 @pytest.mark.parametrize("page_rows,d,new,old", [
     (16, 128, [1] * 9, [0, 1, 15, 16, 17, 40, 300, 31, 32]),
     (64, 64, [0, 70, 1, 0, 129, 3, 0], [5, 0, 63, 0, 1, 64, 9]),
-    (48, 128, [50], [0]), (256, 64, [1, 1], [255, 256]), (16, 128, [1] * 70, list(range(70)))])
+    (64, 128, [2200, 1, 1800], [0, 50, 7]), (48, 128, [50], [0]), (256, 64, [1, 1], [255, 256]), (16, 128, [1] * 70, list(range(70)))])
 def test_append(A, int8, page_rows, d, new, old):
     pad, dropped = 5, 1000
     cache, prob, (q, k, v, w, f, cu, seen) = append_case(A, new, old, int8, page_rows, d, pad=pad, dropped=dropped)
