@@ -9,9 +9,13 @@
 // run of it, so ragged lengths leave no CTA idle.  A producer warp looks the
 // pages up and copies each tile as four 16-row pieces (TMA; a page is a
 // multiple of 16 rows, so a piece never crosses one) into a ring of stages;
-// four consumer warps take one piece each: S = Q K^T and O += P V with
-// mma.sync (16 query heads by 16 rows; tcgen05's 128-row operand would be
-// seven eighths padding), an online softmax in base 2 between them.  A (sequence, KV
+// four consumer warps take one piece each: S = Q K^T (16 query heads by 16
+// rows) and O^T += V^T P^T (16 columns by 8 heads, so up to 8 query heads pad
+// nothing there) with mma.sync; tcgen05's 128-row operand would be seven eighths
+// padding or more.  S's accumulators are P^T's operand as they are.  Between them an online
+// softmax in base 2 whose reference moves only when a logit passes it by more
+// than a few powers of two (a vote of the warp): the weights are then at most
+// 2^8 (2 in f16), O is rarely rescaled, and no row maximum is formed otherwise.  A (sequence, KV
 // head) that several CTAs share is joined by the last of them to finish (an
 // atomic count, no waiting), in the order of the CTAs.
 //
@@ -27,6 +31,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pages.cuh"
 #include "rowmma.cuh"
@@ -41,19 +46,24 @@ constexpr int kPdThreads = (kPdWarps + 1) * 32;
 constexpr int kPdGroup = 16;  // query heads of a KV head, at most
 constexpr int kPdHeader = 256;  // workspace: error word, then the tile count of the last call
 
-template <int D, bool Q8>
+// HB: blocks of eight query heads.
+template <int D, bool Q8, int HB>
 struct PdCfg {
   static constexpr int kPiece = 16 * D * (Q8 ? 1 : 2);  // 16 rows of K or of V
   static constexpr int kTile = kPdWarps * kPiece;
   static constexpr int kStageBytes = 2 * kTile;
   static constexpr int kStages = (Q8 ? 65536 : 98304) / kStageBytes;
   static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kScratch = kPdGroup * D * 4;           // the warps' joined O
+  static constexpr int kCtas = HB == 1 ? 3 : 2;               // to an SM, for the registers
+  static constexpr int kScratch = 8 * HB * D * 4;             // the warps' joined O
   static constexpr int kScales = Q8 ? kStages * 2 * kPdRows * 4 : 0;
   static constexpr int kMl = kPdWarps * kPdGroup * 3 * 4;     // (m, l, n) of each warp and head
   static constexpr int kSmem = 1024 + kRing + kScratch + kScales + kMl + kStages * (8 + 8 + 4) + 448;
-  static_assert(kSmem <= 113 * 1024, "two CTAs per SM");
+  static_assert(kSmem <= (Q8 && HB == 1 ? 75 : 113) * 1024, "CTAs per SM, as ctas_per_sm() says");
 };
+// CTAs to an SM: two rings of 96 KB keep enough bytes in flight for bf16 rows.  int8 rows are bound
+// by the instructions that widen them: a third CTA gives them more warps to issue from.
+constexpr int ctas_per_sm(bool q8, int group) { return q8 && group <= 8 ? 3 : 2; }
 
 // What the mass kernel needs of a tile: its place, and its pieces' pages (-1: not there).
 struct TileInfo {
@@ -223,14 +233,14 @@ __device__ __forceinline__ Share make_share(const PdArgs& a, ShareScratch* sc) {
   return sh;
 }
 
-template <int D, bool Q8>
-__global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+template <int D, bool Q8, int HB>
+__global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap,
                                                                   const __grid_constant__ PdArgs a) {
-  using C = PdCfg<D, Q8>;
+  using C = PdCfg<D, Q8, HB>;
   extern __shared__ uint8_t pd_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pd_raw) + 1023) & ~uintptr_t(1023));
-  float* scratch = reinterpret_cast<float*>(ring + C::kRing);               // [16][D], swizzled
+  float* scratch = reinterpret_cast<float*>(ring + C::kRing);               // [8 HB][D], swizzled
   float* scales = reinterpret_cast<float*>(ring + C::kRing + C::kScratch);  // [stages][K, V][64]
   float* mlw = reinterpret_cast<float*>(ring + C::kRing + C::kScratch + C::kScales);  // [4][16][3]
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(mlw) + C::kMl);
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   }
 
   // ---- consumers
-  const int hA = lane >> 2, cq = lane & 3;  // accumulator rows (heads) hA and hA + 8, columns 2cq, 2cq + 1
+  const int hA = lane >> 2, cq = lane & 3;  // S: heads hA and hA + 8, rows 2cq, 2cq + 1 of each eight
   // sequences without rows: out = 0, lse = -inf
   for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
@@ -341,29 +351,26 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   bool alive = true;
   for (bool more = sh.lo < sh.hi; more; more = next_run(p, r, sh.lo, sh.hi)) {
     if (r.count == 0) continue;
-    // ---- the group's queries as A fragments (rows at or past g: zeros)
-    uint32_t qa[D / 16][4];
-    {
-      const __nv_bfloat16* q0 = a.q + (int64_t)r.s * a.q_stride_seq + (int64_t)(r.h * g + hA) * a.q_stride_head;
-      const __nv_bfloat16* q1 = q0 + 8 * a.q_stride_head;
-      const bool in0 = hA < g, in1 = hA + 8 < g;
+    // ---- the group's queries as A fragments (heads at or past g: zeros)
+    uint32_t qa[D / 16][2 * HB];
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      const bool in = hA + 8 * b < g;
+      const __nv_bfloat16* q = a.q + (int64_t)r.s * a.q_stride_seq + (int64_t)(r.h * g + hA + 8 * b) * a.q_stride_head;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        if constexpr (Q8) {
-          // k-step kk of quad lane cq covers d = cq*D/4 + 4kk + 0..3, as the key codes are read below
-          const uint2 x = in0 ? *reinterpret_cast<const uint2*>(q0 + cq * (D / 4) + 4 * kk) : make_uint2(0, 0);
-          const uint2 y = in1 ? *reinterpret_cast<const uint2*>(q1 + cq * (D / 4) + 4 * kk) : make_uint2(0, 0);
-          qa[kk][0] = x.x;
-          qa[kk][1] = y.x;
-          qa[kk][2] = x.y;
-          qa[kk][3] = y.y;
-        } else {
-          const int d = 16 * kk + 2 * cq;
-          qa[kk][0] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + d) : 0u;
-          qa[kk][1] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + d) : 0u;
-          qa[kk][2] = in0 ? *reinterpret_cast<const uint32_t*>(q0 + d + 8) : 0u;
-          qa[kk][3] = in1 ? *reinterpret_cast<const uint32_t*>(q1 + d + 8) : 0u;
+        uint2 x = make_uint2(0u, 0u);
+        if (in) {
+          if constexpr (Q8) {
+            // k-step kk of quad lane cq covers d = cq*D/4 + 4kk + 0..3, as the key codes are read below
+            x = *reinterpret_cast<const uint2*>(q + cq * (D / 4) + 4 * kk);
+          } else {
+            x.x = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * cq);
+            x.y = *reinterpret_cast<const uint32_t*>(q + 16 * kk + 2 * cq + 8);
+          }
         }
+        qa[kk][b] = x.x;
+        qa[kk][HB + b] = x.y;
       }
     }
     float kmult = a.scale_log2;
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2 * HB; ++j) {
           const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
           mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
@@ -389,18 +396,25 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 2 * HB; ++j) {
           const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
           const __half2 hq = __floats2half2_rn(f.x * qscale, f.y * qscale);
           qa[kk][j] = *reinterpret_cast<const uint32_t*>(&hq);
         }
       kmult /= qscale;
     }
-    float o[D / 8][4];
+    // o[t][b]: columns 16t + hA and + 8 (rows of the product), heads 8b + 2cq and + 1
+    float o[D / 16][HB][4];
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
-    float nA = -INFINITY, nB = -INFINITY;  // O's own reference (int8 rows; else unused)
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int b = 0; b < HB; ++b) o[t][b][0] = o[t][b][1] = o[t][b][2] = o[t][b][3] = 0.f;
+    // of head hA + 8b: the sum's reference and this lane's part of the sum; O's reference (the
+    // same, but for int8 rows)
+    float m[HB], l[HB], n[HB];
+#pragma unroll
+    for (int b = 0; b < HB; ++b) m[b] = -INFINITY, l[b] = 0.f, n[b] = Q8 ? -1e30f : -INFINITY;
+    constexpr float kSlack = 8.f, kSlack16 = 1.f;  // (f16 weights carry 2^14: 2^15 is the most they may reach)
 
     for (uint32_t i = 0; i < r.count && alive; ++i) {
       if (!mbar_wait(&full[st], phase)) {
@@ -414,13 +428,17 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         uint8_t* vt = kt + C::kTile;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         float ks[4] = {1.f, 1.f, 1.f, 1.f}, lv[4] = {0.f, 0.f, 0.f, 0.f};  // rows 2cq, 2cq+1, 2cq+8, 2cq+9
+        auto qk = [&](int t, int kk, uint32_t b0, uint32_t b1) {
+          const uint32_t af[4] = {qa[kk][0], HB == 2 ? qa[kk][1] : 0u, qa[kk][HB], HB == 2 ? qa[kk][3] : 0u};
+          mma16816<Q8>(sc[t], af, b0, b1);
+        };
         if constexpr (Q8) {
           const float* sk = scales + st * 2 * kPdRows + 16 * warp;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int row = 2 * cq + (j & 1) + 8 * (j >> 1);
-            ks[j] = sk[row];
-            lv[j] = log2f(sk[kPdRows + row]);
+            ks[j] = kmult * sk[row];
+            lv[j] = __log2f(sk[kPdRows + row]);
           }
           uint32_t kq[2][D / 16];
 #pragma unroll
@@ -439,7 +457,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const uint32_t x = kq[t][kk] ^ 0x80808080u;
-              mma16816<true>(sc[t], qa[kk], widen2_f16(x, 0x4140u), widen2_f16(x, 0x4342u));
+              qk(t, kk, widen2_f16(x, 0x4140u), widen2_f16(x, 0x4342u));
             }
         } else {
           if (valid < 16) {
@@ -458,101 +476,83 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t kf[4];
             ldsm_x4(kf, swz(kb + (kk >> 2) * 2048, row, 2 * (kk & 3) + (mi & 1)));
-            mma16816<false>(sc[0], qa[kk], kf[0], kf[1]);
-            mma16816<false>(sc[1], qa[kk], kf[2], kf[3]);
+            qk(0, kk, kf[0], kf[1]);
+            qk(1, kk, kf[2], kf[3]);
           }
         }
         // base-2 logits; rows at or past `valid` get weight 0
-        float tA = -INFINITY, tB = -INFINITY;
+        bool over = false;
+        float top[HB], ytop[HB];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int b = 0; b < HB; ++b) {
+          top[b] = ytop[b] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool in = 8 * t + 2 * cq + e < valid;
-            const float mult = Q8 ? kmult * ks[2 * t + e] : kmult;
-            sc[t][e] = in ? sc[t][e] * mult : -INFINITY;
-            sc[t][2 + e] = in ? sc[t][2 + e] * mult : -INFINITY;
-            if (Q8) lv[2 * t + e] = in ? lv[2 * t + e] : -INFINITY;
-            tA = fmaxf(tA, sc[t][e]);
-            tB = fmaxf(tB, sc[t][2 + e]);
+          for (int j = 0; j < 4; ++j) {
+            float& x = sc[j >> 1][2 * b + (j & 1)];
+            const bool in = 8 * (j >> 1) + 2 * cq + (j & 1) < valid;
+            x = in ? x * (Q8 ? ks[j] : kmult) : -INFINITY;
+            top[b] = fmaxf(top[b], x);
+            if (Q8) ytop[b] = fmaxf(ytop[b], in ? x + lv[j] : -INFINITY);
           }
+          over |= top[b] > m[b] + kSlack;
+          if (Q8) over |= ytop[b] > n[b] + kSlack16;
+        }
         if (a.mass_out) {
           float* lg = a.logits + (int64_t)(r.at + i) * g * kPdRows + 16 * warp + 2 * cq;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (hA < g) *reinterpret_cast<float2*>(lg + hA * kPdRows + 8 * t) = make_float2(sc[t][0], sc[t][1]);
-            if (hA + 8 < g)
-              *reinterpret_cast<float2*>(lg + (hA + 8) * kPdRows + 8 * t) = make_float2(sc[t][2], sc[t][3]);
-          }
+          for (int b = 0; b < HB; ++b)
+            if (hA + 8 * b < g)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                *reinterpret_cast<float2*>(lg + (hA + 8 * b) * kPdRows + 8 * t) =
+                    make_float2(sc[t][2 * b], sc[t][2 * b + 1]);
         }
-        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 1));
-        tA = fmaxf(tA, __shfl_xor_sync(0xffffffffu, tA, 2));
-        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 1));
-        tB = fmaxf(tB, __shfl_xor_sync(0xffffffffu, tB, 2));
-        const float xA = fmaxf(mA, tA), xB = fmaxf(mB, tB);
-        float fA = fast_exp2(mA - xA), fB = fast_exp2(mB - xB);
-        mA = xA;
-        mB = xB;
-        uint32_t pa[4];
-        float sA = 0.f, sB = 0.f;
-        if constexpr (Q8) {
-          lA *= fA;
-          lB *= fB;
-          float yA = -INFINITY, yB = -INFINITY;
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sA += fast_exp2(sc[t][e] - xA);
-              sB += fast_exp2(sc[t][2 + e] - xB);
-              sc[t][e] += lv[2 * t + e];
-              sc[t][2 + e] += lv[2 * t + e];
-              yA = fmaxf(yA, sc[t][e]);
-              yB = fmaxf(yB, sc[t][2 + e]);
+          for (int b = 0; b < HB; ++b) {
+            float x = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], 1));
+            x = fmaxf(m[b], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)));
+            float f = fast_exp2(m[b] - x);  // (from -inf: 0)
+            l[b] *= f;
+            m[b] = x;
+            if (Q8) {
+              float y = fmaxf(ytop[b], __shfl_xor_sync(0xffffffffu, ytop[b], 1));
+              y = fmaxf(n[b], fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2)));
+              f = fast_exp2(n[b] - y);
+              n[b] = y;
             }
-          lA += sA;
-          lB += sB;
-          yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
-          yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
-          yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
-          yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
-          yA = fmaxf(fmaxf(yA, nA), -1e30f);  // (finite: rows of zeros only keep weights of 0)
-          yB = fmaxf(fmaxf(yB, nB), -1e30f);
-          fA = fast_exp2(nA - yA);
-          fB = fast_exp2(nB - yB);
-          nA = yA;
-          nB = yB;
-          float x0, x1;
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * cq), f1 = __shfl_sync(0xffffffffu, f, 8 * cq + 4);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+              o[t][b][0] *= f0;
+              o[t][b][1] *= f1;
+              o[t][b][2] *= f0;
+              o[t][b][3] *= f1;
+            }
+          }
+        }
+        // the sum takes the weights before they are rounded: lse and mass need it
+        uint32_t pb[HB][2];
+#pragma unroll
+        for (int b = 0; b < HB; ++b)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            pa[2 * t] = pack_f16(kP16 * fast_exp2(sc[t][0] - yA), kP16 * fast_exp2(sc[t][1] - yA), x0, x1);
-            pa[2 * t + 1] = pack_f16(kP16 * fast_exp2(sc[t][2] - yB), kP16 * fast_exp2(sc[t][3] - yB), x0, x1);
+            const float x0 = sc[t][2 * b], x1 = sc[t][2 * b + 1];
+            const float w0 = fast_exp2(x0 - m[b]), w1 = fast_exp2(x1 - m[b]);
+            l[b] += w0 + w1;
+            if constexpr (Q8) {
+              // (a masked row's scale may be anything: its logit decides)
+              const float y0 = x0 == -INFINITY ? x0 : x0 + lv[2 * t], y1 = x1 == -INFINITY ? x1 : x1 + lv[2 * t + 1];
+              const __half2 h = __floats2half2_rn(kP16 * fast_exp2(y0 - n[b]), kP16 * fast_exp2(y1 - n[b]));
+              pb[b][t] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
+              pb[b][t] = *reinterpret_cast<const uint32_t*>(&h);
+            }
           }
-        } else {
-          // the sum takes the weights before they are rounded: lse and mass need it
-          float x0, x1;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float wA0 = fast_exp2(sc[t][0] - xA), wA1 = fast_exp2(sc[t][1] - xA);
-            const float wB0 = fast_exp2(sc[t][2] - xB), wB1 = fast_exp2(sc[t][3] - xB);
-            pa[2 * t] = pack_bf16(wA0, wA1, x0, x1);
-            sA += wA0 + wA1;
-            pa[2 * t + 1] = pack_bf16(wB0, wB1, x0, x1);
-            sB += wB0 + wB1;
-          }
-          lA = lA * fA + sA;
-          lB = lB * fB + sB;
-        }
-#pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          o[t][0] *= fA;
-          o[t][1] *= fA;
-          o[t][2] *= fB;
-          o[t][3] *= fB;
-        }
         if constexpr (Q8) {
           // lane (hA, cq) takes rows 2cq, 2cq+1, 2cq+8, 2cq+9, value columns hA*(D/8) .. +D/8-1:
-          // n-tile t's column n is the value column n*(D/8) + t
+          // product row hA of m-tile t is the value column hA*(D/8) + 2t, row hA + 8 the next one
           uint32_t vw[4][D / 32];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -570,21 +570,28 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
             }
           }
 #pragma unroll
-          for (int t = 0; t < D / 8; ++t) {
-            const uint32_t sel = (uint32_t)(t & 3) | ((uint32_t)((t & 3) + 4) << 4);
-            const uint32_t b0 = widen2_f16(__byte_perm(vw[0][t >> 2], vw[1][t >> 2], sel), 0x4140u);
-            const uint32_t b1 = widen2_f16(__byte_perm(vw[2][t >> 2], vw[3][t >> 2], sel), 0x4140u);
-            mma16816<true>(o[t], pa, b0, b1);
+          for (int w = 0; w < D / 32; ++w) {  // four columns: two rows' bytes interleaved, two columns to a word
+            const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+            const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+            const uint32_t va[4] = {widen2_f16(x0, 0x4140u), widen2_f16(x0, 0x4342u), widen2_f16(y0, 0x4140u),
+                                    widen2_f16(y0, 0x4342u)};
+            const uint32_t vb[4] = {widen2_f16(x1, 0x4140u), widen2_f16(x1, 0x4342u), widen2_f16(y1, 0x4140u),
+                                    widen2_f16(y1, 0x4342u)};
+#pragma unroll
+            for (int b = 0; b < HB; ++b) {
+              mma16816<true>(o[2 * w][b], va, pb[b][0], pb[b][1]);
+              mma16816<true>(o[2 * w + 1][b], vb, pb[b][0], pb[b][1]);
+            }
           }
         } else {
           const uint32_t vb = smem_u32(vt);
-          const int mi = lane >> 3, row = (lane & 7) + 8 * (mi & 1);
+          const int mi = lane >> 3, row = (lane & 7) + 8 * (mi >> 1);
 #pragma unroll
-          for (int np = 0; np < D / 16; ++np) {
+          for (int t = 0; t < D / 16; ++t) {
             uint32_t vf[4];
-            ldsm_x4_trans(vf, swz(vb + (np >> 2) * 2048, row, 2 * (np & 3) + (mi >> 1)));
-            mma16816<false>(o[2 * np], pa, vf[0], vf[1]);
-            mma16816<false>(o[2 * np + 1], pa, vf[2], vf[3]);
+            ldsm_x4_trans(vf, swz(vb + (t >> 2) * 2048, row, 2 * (t & 3) + (mi & 1)));
+#pragma unroll
+            for (int b = 0; b < HB; ++b) mma16816<false>(o[t][b], vf, pb[b][0], pb[b][1]);
           }
         }
       }
@@ -594,17 +601,18 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     }
 
     // ---- join the four warps: (m, l, n) by all, then O in turns, each warp another quarter of the columns
-    lA += __shfl_xor_sync(0xffffffffu, lA, 1);
-    lA += __shfl_xor_sync(0xffffffffu, lA, 2);
-    lB += __shfl_xor_sync(0xffffffffu, lB, 1);
-    lB += __shfl_xor_sync(0xffffffffu, lB, 2);
-    if (!Q8) nA = mA, nB = mB;
     named_bar_sync(1, kPdWarps * 32);  // the last run's scratch and mlw are read
-    if (cq == 0) {
-      float* w = mlw + (warp * kPdGroup + hA) * 3;
-      w[0] = mA, w[1] = lA, w[2] = nA;
-      w += 8 * 3;
-      w[0] = mB, w[1] = lB, w[2] = nB;
+    // (addresses from here on are formed at each run's end, not held in registers through its tiles)
+    int hA = lane >> 2, cq = lane & 3;
+    asm volatile("" : "+r"(hA), "+r"(cq));
+#pragma unroll
+    for (int b = 0; b < HB; ++b) {
+      float x = l[b] + __shfl_xor_sync(0xffffffffu, l[b], 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if (cq == 0) {
+        float* w = mlw + (warp * kPdGroup + hA + 8 * b) * 3;
+        w[0] = m[b], w[1] = x, w[2] = Q8 ? n[b] : m[b];
+      }
     }
     named_bar_sync(1, kPdWarps * 32);
     auto joined = [&](int hh, float& m, float& l, float& n) {
@@ -621,32 +629,48 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         if (x != -INFINITY) l += mlw[(w * kPdGroup + hh) * 3 + 1] * fast_exp2(x - m);
       }
     };
+    // head hh's column d lies at d ^ 8 (hh / 2 mod 4): a warp's stores then fall into 32 banks
+    auto place = [](int hh, int d) { return hh * D + (d ^ ((hh >> 1 & 3) << 3)); };
     {
-      float m, l, n;
-      joined(hA, m, l, n);
-      const float cA = nA == -INFINITY ? 0.f : fast_exp2(nA - n);
-      joined(hA + 8, m, l, n);
-      const float cB = nB == -INFINITY ? 0.f : fast_exp2(nB - n);
-      float2* sc2 = reinterpret_cast<float2*>(scratch);
-      for (int turn = 0; turn < 4; ++turn) {
+      float c[HB][2];
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          if ((t / (D / 32)) != ((turn + warp) & 3)) continue;
-          const int col = (4 * t + cq) ^ ((hA & 3) << 2);  // float2 columns, spread over the banks
-          float2* x = sc2 + hA * (D / 2) + col;
-          float2* y = x + 8 * (D / 2);
-          float2 u = make_float2(o[t][0] * cA, o[t][1] * cA), v = make_float2(o[t][2] * cB, o[t][3] * cB);
-          if (turn) u.x += x->x, u.y += x->y, v.x += y->x, v.y += y->y;
-          *x = u;
-          *y = v;
+      for (int b = 0; b < HB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int hh = 8 * b + 2 * cq + e;
+          float mm, ll, nn;
+          joined(hh, mm, ll, nn);
+          const float x = mlw[(warp * kPdGroup + hh) * 3 + 2];
+          c[b][e] = x == -INFINITY ? 0.f : fast_exp2(x - nn);
+        }
+      auto put = [&](auto q, bool first) {
+        constexpr int quarter = decltype(q)::value;
+#pragma unroll
+        for (int t = quarter * (D / 64); t < (quarter + 1) * (D / 64); ++t)
+#pragma unroll
+          for (int b = 0; b < HB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float* to = scratch + place(8 * b + 2 * cq + (j & 1), 16 * t + hA + 8 * (j >> 1));
+              const float x = o[t][b][j] * c[b][j & 1];
+              *to = first ? x : *to + x;
+            }
+      };
+#pragma unroll 1
+      for (int turn = 0; turn < 4; ++turn) {
+        switch ((turn + warp) & 3) {
+          case 0: put(std::integral_constant<int, 0>(), turn == 0); break;
+          case 1: put(std::integral_constant<int, 1>(), turn == 0); break;
+          case 2: put(std::integral_constant<int, 2>(), turn == 0); break;
+          default: put(std::integral_constant<int, 3>(), turn == 0); break;
         }
         named_bar_sync(1, kPdWarps * 32);
       }
     }
-    // int8 values: column d sits where n-tile d % (D/8) keeps its column d / (D/8)
+    // int8 values: where the value column d went
     auto joined_o = [&](int hh, int d) {
-      const int ds = Q8 ? 8 * (d % (D / 8)) + d / (D / 8) : d;
-      return scratch[hh * D + (((ds >> 1) ^ ((hh & 3) << 2)) << 1) + (ds & 1)];
+      const int rem = d % (D / 8);
+      return scratch[place(hh, Q8 ? 16 * (rem >> 1) + d / (D / 8) + 8 * (rem & 1) : d)];
     };
     if (tid == 0 && r.first == 0) {
       const int c0 = (int)(r.unit / sh.per);
@@ -694,7 +718,7 @@ __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_con
   pdl_trigger();
   pdl_wait();
   const Pages& p = a.pages;
-  const int tid = threadIdx.x, lane = tid & 31, g = a.group;
+  const int tid = threadIdx.x, g = a.group;
   const int units = p.num_seqs * p.h_kv;
   auto slot_of = [](int c0, int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
@@ -815,7 +839,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
   if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
-  pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2LL * pl.sms, pl.tiles));
+  pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)ctas_per_sm(pl.q8, pl.g) * pl.sms, pl.tiles));
   pl.lse_off = kPdHeader + up256(sizeof(int2) * (size_t)units);
   pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
   pl.o_off = pl.ml_off + up256(sizeof(float4) * 2 * (size_t)pl.grid * pl.g);
@@ -830,13 +854,19 @@ bool encode_pages(CUtensorMap* m, const void* base, const PdPlan& pl) {
   auto enc = tma_encoder();
   if (!enc) return false;
   const Pages& p = pl.pages;
+  // L2 fetches what one row of one KV head covers and no more: with 256 bytes promoted, 64-wide bf16
+  // heads (128 bytes) brought half of their neighbours along (669 MB for 452)
+  const int row = pl.d * (pl.q8 ? 1 : 2);
+  const CUtensorMapL2promotion promote = row == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : row == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                      : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   if (pl.q8) {
     cuuint64_t dims[4] = {(cuuint64_t)pl.d, (cuuint64_t)p.page_rows, (cuuint64_t)p.h_kv, (cuuint64_t)p.num_pages};
     cuuint64_t strides[3] = {(cuuint64_t)p.stride_row, (cuuint64_t)p.stride_head, (cuuint64_t)p.stride_page};
     cuuint32_t box[4] = {(cuuint32_t)pl.d, 16, 1, 1}, es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, pl.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
   cuuint64_t dims[5] = {64, (cuuint64_t)p.page_rows, (cuuint64_t)pl.d / 64, (cuuint64_t)p.h_kv,
                         (cuuint64_t)p.num_pages};
@@ -844,16 +874,16 @@ bool encode_pages(CUtensorMap* m, const void* base, const PdPlan& pl) {
                            (cuuint64_t)p.stride_page * 2};
   cuuint32_t box[5] = {64, 16, (cuuint32_t)pl.d / 64, 1, 1}, es[5] = {1, 1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promote,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int HB>
 int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!encode_pages(&km, pl.pages.k, pl) || !encode_pages(&vm, pl.pages.v, pl)) return AIRCACHE_ERR_UNSUPPORTED;
-  constexpr int smem = PdCfg<D, Q8>::kSmem;
-  if (allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<D, Q8>), smem) != cudaSuccess)
+  constexpr int smem = PdCfg<D, Q8, HB>::kSmem;
+  if (allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<D, Q8, HB>), smem) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid);
@@ -865,7 +895,7 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8, HB>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   const int64_t units = (int64_t)pl.pages.num_seqs * pl.pages.h_kv;
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, 3LL * pl.sms));
   cfg.blockDim = dim3(kPjThreads);
@@ -877,6 +907,11 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
     if (launch_pdl(paged_mass_kernel, dim3(grid), dim3(256), 0, s, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   }
   return AIRCACHE_OK;
+}
+
+template <int D, bool Q8>
+int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
+  return pl.g <= 8 ? launch_pd<D, Q8, 1>(pl, a, s) : launch_pd<D, Q8, 2>(pl, a, s);
 }
 
 }  // namespace
