@@ -91,12 +91,14 @@ struct PdArgs {
   float scale_log2;
 };
 
+// Keys and values pass through L2 once: they are to go first, so that the stored logits stay for the
+// mass (16 x 16k with mass: 107.5 us without the policy, 104.6 with; 64-wide heads: 80.6 and 76.5).
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int a, int b, int c, int d, int e,
-                                            uint64_t* bar) {
+                                            uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-      "%6}], [%7];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+      "{%2, %3, %4, %5, %6}], [%7], %8;\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 
@@ -271,6 +273,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   if (warp == kPdWarps) {
     // ---- producer warp: lane j of 32 holds the page of the j-th 16-row piece
     // ahead (8 tiles); 0-3 copy keys, 4-7 values, 8-15 the scales of int8 rows
+    const uint64_t policy = l2_evict_first_policy();
     int st = 0;
     uint32_t phase = 0, filled = 0;
     bool alive = true;
@@ -312,9 +315,9 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           const uint32_t to = smem_u32(dst) + (lane >= 4 ? C::kTile : 0);
           const CUtensorMap* map = lane >= 4 ? &vmap : &kmap;
           if constexpr (Q8)
-            tma_load_4d(to, map, 0, row, r.h, pg, &full[st]);
+            tma_load_4d_hint(to, map, 0, row, r.h, pg, &full[st], policy);
           else
-            tma_load_5d(to, map, 0, row, 0, r.h, pg, &full[st]);
+            tma_load_5d(to, map, 0, row, 0, r.h, pg, &full[st], policy);
         }
         if constexpr (Q8) {
           if (pg >= 0 && lane >= 8 && lane < 16) {
@@ -711,23 +714,28 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   }
 }
 
-// Joins the parts of the units that several CTAs shared: a unit to a CTA, four columns a thread.
-constexpr int kPjThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_constant__ PdArgs a, float undo) {
+// After the attention.  Joins the parts of the units that several CTAs shared: a
+// unit to a CTA, four columns a thread.  MASS: also turns the stored logits into
+// weights and adds them to the rows' mass: a warp takes a run of tiles, a lane two
+// rows of each; it forms its unit's log-sum-exps from the parts itself, which costs less
+// than a third launch that waits for the join (16 x 16k: 103 us, and 107 with that launch).
+constexpr int kPfThreads = 256;
+template <int D, bool MASS>
+__global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(const __grid_constant__ PdArgs a,
+                                                                                float undo) {
   pdl_trigger();
   pdl_wait();
   const Pages& p = a.pages;
-  const int tid = threadIdx.x, g = a.group;
+  const int tid = threadIdx.x, lane = tid & 31, g = a.group;
   const int units = p.num_seqs * p.h_kv;
   auto slot_of = [](int c0, int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int2 un = a.unit[u];  // its first CTA, its parts
     if (un.y < 2) continue;
     const int64_t head0 = (int64_t)u * g;  // (s h_kv + h) g = s h_q + h g
-    for (int c = tid; c < g * (D / 4); c += kPjThreads) {
+    for (int c = tid; c < g * (D / 4); c += kPfThreads) {
       const int hh = c / (D / 4), d = c % (D / 4) * 4;
-      constexpr int kFlight = 8;  // parts whose loads are in flight
+      constexpr int kFlight = MASS ? 4 : 8;  // parts whose loads are in flight
       float m = -INFINITY, n = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int j0 = 0; j0 < un.y; j0 += kFlight) {
@@ -765,44 +773,77 @@ __global__ void __launch_bounds__(kPjThreads) paged_join_kernel(const __grid_con
       const float f = l > 0.f ? undo * fast_exp2(n - m) / l : 0.f;
       __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
       *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
-      if (d == 0) {
-        if (a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        if (a.mass_out) a.lse2[head0 + hh] = l > 0.f ? m + log2f(l) : INFINITY;
-      }
+      if (d == 0 && a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
   }
-}
-
-// The rows' mass from the stored logits: a warp takes a tile, a lane two rows of it.
-__global__ void __launch_bounds__(256) paged_mass_kernel(const __grid_constant__ PdArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, g = a.group;
-  const int total = *a.tiles;
-  const Pages& p = a.pages;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8) {
-    const int4 w = *reinterpret_cast<const int4*>(&a.info[t]);
-    const int page = a.info[t].page[lane >> 3];
-    const int row = w.z * kPdRows + 2 * lane;
-    const int len = p.lens[w.x];
-    if (page < 0 || row >= len) continue;
-    const int64_t slot = page_slot(p, page, w.y, row % p.page_rows);
+  if (!MASS) return;
+  const int total = *a.tiles, warps = gridDim.x * (kPfThreads / 32);
+  const int each = (total + warps - 1) / warps, w = blockIdx.x * (kPfThreads / 32) + (tid >> 5);
+  const int t1 = min((w + 1) * each, total);
+  int now = -1;
+  float lse = INFINITY;  // lane hh: of query head hh of unit `now`
+  for (int t = w * each; t < t1; ++t) {
+    // (the logits' place goes by the tile alone: they load while the rest is looked up)
     const float* lg = a.logits + (int64_t)t * g * kPdRows + 2 * lane;
-    const float* lse = a.lse2 + (int64_t)w.x * a.h_q + w.y * g;
-    float x = 0.f, y = 0.f;
-#pragma unroll 4
-    for (int hh = 0; hh < g; ++hh) {
-      const float2 v = *reinterpret_cast<const float2*>(lg + hh * kPdRows);
-      const float z = lse[hh];
-      x += fast_exp2(v.x - z);
-      y += fast_exp2(v.y - z);
+    float2 v[8];
+#pragma unroll
+    for (int hh = 0; hh < 8; ++hh)
+      v[hh] = hh < g ? *reinterpret_cast<const float2*>(lg + hh * kPdRows) : make_float2(-INFINITY, -INFINITY);
+    const int4 x = *reinterpret_cast<const int4*>(&a.info[t]);
+    const int page = a.info[t].page[lane >> 3];
+    const int u = x.x * p.h_kv + x.y, row = x.z * kPdRows + 2 * lane, len = p.lens[x.x];
+    const bool in = page >= 0 && row < len;
+    const int64_t slot = in ? page_slot(p, page, x.y, row % p.page_rows) : 0;
+    float2 old = in ? *reinterpret_cast<const float2*>(p.mass + slot) : make_float2(0.f, 0.f);
+    if (u != now) {
+      now = u;
+      const int2 un = a.unit[u];
+      if (un.y < 2) {
+        if (lane < g) lse = a.lse2[(int64_t)u * g + lane];
+      } else {
+        // the heads side by side, 32 / width lanes to each, four parts of a lane in flight
+        const int width = g <= 8 ? 8 : 16, subs = 32 / width, hh = min(lane & (width - 1), g - 1);
+        float m = -INFINITY, l = 0.f;
+        for (int j0 = lane / width; j0 < un.y; j0 += 4 * subs) {
+          float2 ml[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            ml[f] = *reinterpret_cast<const float2*>(a.part_ml + slot_of(un.x, min(j0 + f * subs, un.y - 1)) * g + hh);
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            if (j0 + f * subs >= un.y || ml[f].x == -INFINITY) continue;
+            const float m1 = fmaxf(m, ml[f].x);
+            l = l * fast_exp2(m - m1) + ml[f].y * fast_exp2(ml[f].x - m1);
+            m = m1;
+          }
+        }
+        float m1 = m;
+        for (int off = width; off < 32; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
+        l = m == -INFINITY ? 0.f : l * fast_exp2(m - m1);
+        for (int off = width; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        lse = l > 0.f ? m1 + log2f(l) : INFINITY;
+      }
     }
-    if (row + 1 < len) {
-      const float2 v = *reinterpret_cast<const float2*>(p.mass + slot);
-      *reinterpret_cast<float2*>(a.mass_out + slot) = make_float2(v.x + x, v.y + y);
-    } else {
-      a.mass_out[slot] = p.mass[slot] + x;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int hh = 0; hh < 8; ++hh) {
+      const float z = __shfl_sync(0xffffffffu, lse, hh);
+      if (hh < g) {
+        sum.x += fast_exp2(v[hh].x - z);
+        sum.y += fast_exp2(v[hh].y - z);
+      }
     }
+    for (int hh = 8; hh < g; ++hh) {
+      const float z = __shfl_sync(0xffffffffu, lse, hh);
+      const float2 y = *reinterpret_cast<const float2*>(lg + hh * kPdRows);
+      sum.x += fast_exp2(y.x - z);
+      sum.y += fast_exp2(y.y - z);
+    }
+    if (!in) continue;
+    if (row + 1 < len)
+      *reinterpret_cast<float2*>(a.mass_out + slot) = make_float2(old.x + sum.x, old.y + sum.y);
+    else
+      a.mass_out[slot] = old.x + sum.x;
   }
 }
 
@@ -897,15 +938,14 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8, HB>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   const int64_t units = (int64_t)pl.pages.num_seqs * pl.pages.h_kv;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, 3LL * pl.sms));
-  cfg.blockDim = dim3(kPjThreads);
+  const int64_t work = a.mass_out ? std::max(units, (pl.tiles + kPfThreads / 32 - 1) / (kPfThreads / 32)) : units;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(work, (a.mass_out ? 4LL : 3LL) * pl.sms));
+  cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, a, Q8 ? 1.f / kP16 : 1.f) != cudaSuccess)
+  const float undo = Q8 ? 1.f / kP16 : 1.f;
+  if (cudaLaunchKernelEx(&cfg, a.mass_out ? paged_finish_kernel<D, true> : paged_finish_kernel<D, false>, a, undo) !=
+      cudaSuccess)
     return AIRCACHE_ERR_CUDA;
-  if (a.mass_out) {
-    const int grid = (int)std::min<int64_t>((pl.tiles + 7) / 8, 8LL * pl.sms);
-    if (launch_pdl(paged_mass_kernel, dim3(grid), dim3(256), 0, s, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  }
   return AIRCACHE_OK;
 }
 
