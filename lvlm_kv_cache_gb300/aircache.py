@@ -675,18 +675,22 @@ def _dense(t, dtype, shape, name):
         raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)}")
 
 
-def _run_paged(prob, ws, stream, call, where):
-    """`call(stream)` on the problem's device, whichever the current one is.
-    An empty batch (whose tensors have no storage) needs no call."""
-    if prob.empty:
-        return
+def _paged_stream(prob, ws, stream):
+    """The stream handle of a call on `prob` (by default the current stream of the problem's device)."""
     if ws is not None and ws.device != prob.device:
         raise ValueError("the workspace must be on the problem's device")
-    if torch.cuda.current_device() == prob.device.index:
-        _check(call(_stream(stream)), where)
+    return torch._C._cuda_getCurrentRawStream(prob.device.index) if stream is None else stream.cuda_stream
+
+
+def _run_paged(fn, where, prob, *args):
+    """fn(problem, *args) on the problem's device, whichever the current one is."""
+    if torch._C._cuda_getDevice() == prob.device.index:
+        st = fn(prob.ref, *args)
     else:
         with torch.cuda.device(prob.device):
-            _check(call(_stream(stream)), where)
+            st = fn(prob.ref, *args)
+    if st != OK:
+        raise AirCacheError(st, where)
 
 
 class PagedCache:
@@ -810,7 +814,10 @@ class RotateProblem:
 
 
 def aircache_rotate(prob: RotateProblem, status=None, stream=None):
-    _run_paged(prob, status, stream, lambda s: lib().aircache_rotate(prob.ref, _ptr(status), s), "aircache_rotate")
+    if prob.empty:  # (tensors without storage)
+        return
+    s = _paged_stream(prob, status, stream)
+    _run_paged(lib().aircache_rotate, "aircache_rotate", prob, None if status is None else status.data_ptr(), s)
 
 
 def rotate(prob: RotateProblem, stream=None, check=True):
@@ -879,8 +886,10 @@ class PagedDecodeProblem:
 
 
 def aircache_paged_decode(prob: PagedDecodeProblem, ws, stream=None):
-    _run_paged(prob, ws, stream, lambda s: lib().aircache_paged_decode(prob.ref, _ptr(ws), ws.numel(), s),
-               "aircache_paged_decode")
+    if prob.empty:
+        return
+    s = _paged_stream(prob, ws, stream)
+    _run_paged(lib().aircache_paged_decode, "aircache_paged_decode", prob, ws.data_ptr(), ws.numel(), s)
 
 
 def paged_decode(prob: PagedDecodeProblem, ws=None, stream=None, check=True):
@@ -940,7 +949,10 @@ class EvictProblem:
 
 
 def aircache_evict(prob: EvictProblem, ws, stream=None):
-    _run_paged(prob, ws, stream, lambda s: lib().aircache_evict(prob.ref, _ptr(ws), ws.numel(), s), "aircache_evict")
+    if prob.empty:
+        return
+    s = _paged_stream(prob, ws, stream)
+    _run_paged(lib().aircache_evict, "aircache_evict", prob, ws.data_ptr(), ws.numel(), s)
 
 
 def evict(prob: EvictProblem, ws=None, stream=None, check=True):

@@ -4,6 +4,7 @@
 // stream; nothing here allocates, frees or synchronises except
 // aircache_get_error.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -31,6 +32,17 @@ cudaError_t allow_smem(const void* func, int bytes) {
   e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.push_back(Entry{func, dev, bytes});
   return e;
+}
+
+int device_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed) > 0) return known[dev].load(std::memory_order_relaxed);
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 152;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 }  // namespace aircache

@@ -475,9 +475,7 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
       ((p->sink || p->recent) && !p->pages->order) || (p->recent && !p->seen) || p->max_rows < 1)
     return AIRCACHE_ERR_INVALID_ARG;
   if (p->max_rows > AIRCACHE_MAX_EVICT_ROWS) return AIRCACHE_ERR_UNSUPPORTED;
-  int dev = 0;
-  pl.sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&pl.sms, cudaDevAttrMultiProcessorCount, dev);
+  pl.sms = device_sms();
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
   // CTAs per (sequence, KV head): enough that the batch fills the SMs twice,
   // but at least 2048 rows to a CTA (each rank costs every barrier and

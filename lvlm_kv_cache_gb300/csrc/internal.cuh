@@ -223,6 +223,8 @@ cudaError_t launch_pdl(void (*kernel)(Arg), dim3 grid, dim3 block, size_t smem, 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) for `func` on the current
 // device, skipped when an earlier call already allowed at least `bytes`.
 cudaError_t allow_smem(const void* func, int bytes);
+// SMs of the current device (asked once per device; 152 where there is none).
+int device_sms();
 cudaError_t launch_offsets(const Dev& p, const Ws& w, int64_t out_capacity, cudaStream_t s);
 // aircache_budget_noalloc after host validation: stats, budgets and the
 // optional device status copy, with the module's fixed scratch.

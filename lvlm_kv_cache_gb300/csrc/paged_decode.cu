@@ -874,9 +874,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   if (pl.g > kPdGroup) return AIRCACHE_ERR_UNSUPPORTED;
   pl.q8 = p->pages->kv_dtype == AIRCACHE_INT8;
   pl.d = p->pages->head_dim;
-  int dev = 0;
-  pl.sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&pl.sms, cudaDevAttrMultiProcessorCount, dev);
+  pl.sms = device_sms();
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
   if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;

@@ -416,8 +416,7 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   a.eps = p->eps;
   // A warp takes a whole token where that makes enough warps for the GPU (16 to an
   // SM); with fewer tokens it takes as few rows as it has at once
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = device_sms();
   const int at_once = p->head_dim == 128 ? 2 : 4;
   const int64_t want = std::max<int64_t>(1, 16LL * sms / p->num_tokens);
   a.per = (int)std::max<int64_t>(at_once, (a.heads + want - 1) / want);
