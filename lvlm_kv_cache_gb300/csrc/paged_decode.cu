@@ -23,9 +23,10 @@
 // joins the weight before it is rounded to f16: the weights of O are
 // exp2(x_j + log2 s_j) against their own running maximum, and the sum l keeps its own.
 //
-// Weights are rounded to bf16 (int8 rows: f16) for the product with V, which
-// halves their registers and is what the matrix instruction takes; maximum,
-// sum, O and the joins are fp32, and out is rounded once, to bf16.
+// The product with V takes 16-bit weights: bf16 ones as a sum of two (what
+// rounding takes away goes through a second product, which costs no time beside
+// the bytes: 16 x 16k 103.6 us with and without), f16 ones (int8 rows) rounded
+// once, to 2^-12.  Maximum, sum, O and the joins are fp32, and out is rounded once, to bf16.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           }
         }
         // the sum takes the weights before they are rounded: lse and mass need it
-        uint32_t pb[HB][2];
+        uint32_t pb[HB][2], pl[HB][2];  // (pl: what rounding to bf16 takes from them)
 #pragma unroll
         for (int b = 0; b < HB; ++b)
 #pragma unroll
@@ -551,6 +552,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
             } else {
               const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
               pb[b][t] = *reinterpret_cast<const uint32_t*>(&h);
+              const __nv_bfloat162 r = __floats2bfloat162_rn(w0 - __low2float(h), w1 - __high2float(h));
+              pl[b][t] = *reinterpret_cast<const uint32_t*>(&r);
             }
           }
         if constexpr (Q8) {
@@ -594,7 +597,10 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
             uint32_t vf[4];
             ldsm_x4_trans(vf, swz(vb + (t >> 2) * 2048, row, 2 * (t & 3) + (mi & 1)));
 #pragma unroll
-            for (int b = 0; b < HB; ++b) mma16816<false>(o[t][b], vf, pb[b][0], pb[b][1]);
+            for (int b = 0; b < HB; ++b) {
+              mma16816<false>(o[t][b], vf, pb[b][0], pb[b][1]);
+              mma16816<false>(o[t][b], vf, pl[b][0], pl[b][1]);
+            }
           }
         }
       }

@@ -4,8 +4,8 @@ Tolerances.  A dot product in fp32 over D exact products is off by at most
 D 2^-24 sum |q_d k_d| scale =: dx (at the row where that is largest), and a
 weight by a relative 2 dx + 2^-20 (two exponentials of that error, the base-2
 exponential's own 2^-22, products).  lse: dx + 2^-20 (1 + |lse|).  out: each
-weight is also rounded to 16 bits (2^-8 bf16, less for f16) before it meets V, and
-out once more: (2^-8 + 2 dx + 2^-18) sum w |v| + 2^-8 |out|.  int8 rows: the
+weight also becomes a sum of two bf16 before it meets V (2^-8 of 2^-8), or one f16
+(2^-11), and out is rounded to bf16: (2^-16 or 2^-11, + 2 dx + 2^-18) sum w |v| + 2^-8 |out|.  int8 rows: the
 weight times the value's scale is held in f16, 2^14 to the largest of them, so a
 small one is also off by half of f16's least step, 2^-25 / 2^14 of the largest,
 which its code (at most 127) multiplies: n 127 2^-39 max w s on top.  mass: the
@@ -46,7 +46,8 @@ def verify(prob, cache_before, q, scale=None, skip_mass=False):
     out, lse, w, size, spread = O.decode(q.double().cpu().numpy(), c, scale)
     dx = d * 2.0 ** -24 * size
     got = prob.out.double().cpu().numpy()
-    tol = (HALF + 2 * dx[..., None] + 2.0 ** -18) * spread + HALF * np.abs(out) + 1e-30
+    weight = 2.0 ** -16 if c["v_scale"] is None else 2.0 ** -11
+    tol = (weight + 2 * dx[..., None] + 2.0 ** -18) * spread + HALF * np.abs(out) + 1e-30
     if c["v_scale"] is not None:
         top = O.largest_weighted_scale(q.double().cpu().numpy(), c, scale)
         tol += (c["lens"][:, None] * 127 * 2.0 ** -39 * top)[..., None]
