@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     float m[HB], l[HB], n[HB];
 #pragma unroll
     for (int b = 0; b < HB; ++b) m[b] = -INFINITY, l[b] = 0.f, n[b] = Q8 ? -1e30f : -INFINITY;
+    static_assert(kP16 == 16384.f, "2^14, as the weights' exponent takes it");
     constexpr float kSlack = 8.f, kSlack16 = 1.f;  // (f16 weights carry 2^14: 2^15 is the most they may reach)
 
     for (uint32_t i = 0; i < r.count && alive; ++i) {
@@ -442,27 +443,20 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           for (int j = 0; j < 4; ++j) {
             const int row = 2 * cq + (j & 1) + 8 * (j >> 1);
             ks[j] = kmult * sk[row];
-            lv[j] = __log2f(sk[kPdRows + row]);
+            lv[j] = row < valid ? __log2f(sk[kPdRows + row]) : 0.f;  // (past the end a scale may be anything)
           }
-          uint32_t kq[2][D / 16];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {  // (one eight of rows after the other: fewer registers at a time)
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
               const uint4 x =
                   *reinterpret_cast<const uint4*>(kt + swz8<D>((8 * t + hA) * D + cq * (D / 4) + 16 * w));
-              kq[t][4 * w] = x.x;
-              kq[t][4 * w + 1] = x.y;
-              kq[t][4 * w + 2] = x.z;
-              kq[t][4 * w + 3] = x.w;
-            }
+              const uint32_t k4[4] = {x.x ^ 0x80808080u, x.y ^ 0x80808080u, x.z ^ 0x80808080u, x.w ^ 0x80808080u};
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t x = kq[t][kk] ^ 0x80808080u;
-              qk(t, kk, widen2_f16(x, 0x4140u), widen2_f16(x, 0x4342u));
+              for (int e = 0; e < 4; ++e)
+                qk(t, 4 * w + e, widen2_f16(k4[e], 0x4140u), widen2_f16(k4[e], 0x4342u));
             }
+          }
         } else {
           if (valid < 16) {
             // rows past the end may hold anything: zero their V so that weights of 0 add exactly 0
@@ -496,7 +490,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
             const bool in = 8 * (j >> 1) + 2 * cq + (j & 1) < valid;
             x = in ? x * (Q8 ? ks[j] : kmult) : -INFINITY;
             top[b] = fmaxf(top[b], x);
-            if (Q8) ytop[b] = fmaxf(ytop[b], in ? x + lv[j] : -INFINITY);
+            if (Q8) ytop[b] = fmaxf(ytop[b], x + lv[j]);
           }
           over |= top[b] > m[b] + kSlack;
           if (Q8) over |= ytop[b] > n[b] + kSlack16;
@@ -545,9 +539,9 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
             const float w0 = fast_exp2(x0 - m[b]), w1 = fast_exp2(x1 - m[b]);
             l[b] += w0 + w1;
             if constexpr (Q8) {
-              // (a masked row's scale may be anything: its logit decides)
-              const float y0 = x0 == -INFINITY ? x0 : x0 + lv[2 * t], y1 = x1 == -INFINITY ? x1 : x1 + lv[2 * t + 1];
-              const __half2 h = __floats2half2_rn(kP16 * fast_exp2(y0 - n[b]), kP16 * fast_exp2(y1 - n[b]));
+              // (2^14 enters the exponent: kP16 exp2(y - n) = exp2(y - (n - 14)))
+              const __half2 h = __floats2half2_rn(fast_exp2(x0 + lv[2 * t] - (n[b] - 14.f)),
+                                                  fast_exp2(x1 + lv[2 * t + 1] - (n[b] - 14.f)));
               pb[b][t] = *reinterpret_cast<const uint32_t*>(&h);
             } else {
               const __nv_bfloat162 h = __floats2bfloat162_rn(w0, w1);
@@ -559,34 +553,31 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         if constexpr (Q8) {
           // lane (hA, cq) takes rows 2cq, 2cq+1, 2cq+8, 2cq+9, value columns hA*(D/8) .. +D/8-1:
           // product row hA of m-tile t is the value column hA*(D/8) + 2t, row hA + 8 the next one
-          uint32_t vw[4][D / 32];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int off = swz8<D>((2 * cq + (j & 1) + 8 * (j >> 1)) * D + hA * (D / 8));
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vt + off);
-              vw[j][0] = x.x ^ 0x80808080u;
-              vw[j][1] = x.y ^ 0x80808080u;
-              vw[j][2] = x.z ^ 0x80808080u;
-              vw[j][3] = x.w ^ 0x80808080u;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(vt + off);
-              vw[j][0] = x.x ^ 0x80808080u;
-              vw[j][1] = x.y ^ 0x80808080u;
+          for (int half = 0; half < D / 64; ++half) {  // eight columns of each row at a time
+            uint2 v8[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v8[j] = *reinterpret_cast<const uint2*>(
+                  vt + swz8<D>((2 * cq + (j & 1) + 8 * (j >> 1)) * D + hA * (D / 8)) + 8 * half);
+              v8[j].x ^= 0x80808080u;
+              v8[j].y ^= 0x80808080u;
             }
-          }
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w) {  // four columns: two rows' bytes interleaved, two columns to a word
-            const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-            const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            const uint32_t va[4] = {widen2_f16(x0, 0x4140u), widen2_f16(x0, 0x4342u), widen2_f16(y0, 0x4140u),
-                                    widen2_f16(y0, 0x4342u)};
-            const uint32_t vb[4] = {widen2_f16(x1, 0x4140u), widen2_f16(x1, 0x4342u), widen2_f16(y1, 0x4140u),
-                                    widen2_f16(y1, 0x4342u)};
+            for (int w = 0; w < 2; ++w) {  // four columns: two rows' bytes interleaved, two columns to a word
+              const uint32_t r0 = w ? v8[0].y : v8[0].x, r1 = w ? v8[1].y : v8[1].x;
+              const uint32_t r2 = w ? v8[2].y : v8[2].x, r3 = w ? v8[3].y : v8[3].x;
+              const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
+              const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
+              const uint32_t va[4] = {widen2_f16(x0, 0x4140u), widen2_f16(x0, 0x4342u), widen2_f16(y0, 0x4140u),
+                                      widen2_f16(y0, 0x4342u)};
+              const uint32_t vb[4] = {widen2_f16(x1, 0x4140u), widen2_f16(x1, 0x4342u), widen2_f16(y1, 0x4140u),
+                                      widen2_f16(y1, 0x4342u)};
 #pragma unroll
-            for (int b = 0; b < HB; ++b) {
-              mma16816<true>(o[2 * w][b], va, pb[b][0], pb[b][1]);
-              mma16816<true>(o[2 * w + 1][b], vb, pb[b][0], pb[b][1]);
+              for (int b = 0; b < HB; ++b) {
+                mma16816<true>(o[4 * half + 2 * w][b], va, pb[b][0], pb[b][1]);
+                mma16816<true>(o[4 * half + 2 * w + 1][b], vb, pb[b][0], pb[b][1]);
+              }
             }
           }
         } else {
