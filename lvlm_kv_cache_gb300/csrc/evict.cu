@@ -29,7 +29,7 @@ namespace {
 constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
-constexpr int kMvThreads = 256;
+constexpr int kMvThreads = 256, kMvCtas = 4;  // of the moves: threads of a CTA, CTAs to an SM
 constexpr int kEvSlice = AIRCACHE_MAX_EVICT_ROWS / kEvMaxCluster;  // keys of one CTA, at most
 constexpr int kEvHeader = 256;                                     // workspace: error word
 constexpr uint32_t kProtected = 0xffffffffu;
@@ -403,9 +403,13 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   if (CL) cluster_sync_all();  // shared memory stays readable until every rank is done
 }
 
-// RB: 16-byte pieces of a row of one KV head.
+// RB: 16-byte pieces of a row of one KV head.  What a warp waits for is hidden
+// by other warps, so few registers count for more than many loads of one warp
+// (16 x 16k to half: 73 us with eight row loads in flight and 24 warps to an SM,
+// 61 with four and 32), and nothing is stored before every load of the 32 moves' scales, mass
+// and order and the first rows' has been issued.
 template <int RB>
-__global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const __grid_constant__ EvArgs a) {
+__global__ void __launch_bounds__(kMvThreads, kMvCtas) evict_move_kernel(const __grid_constant__ EvArgs a) {
   pdl_trigger();
   pdl_wait();
   const Pages& p = a.pages;
@@ -421,24 +425,24 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const __grid_con
   const int size = p.k_scale ? 1 : 2;
   for (int m0 = 32 * (blockIdx.x * (kMvThreads / 32) + (threadIdx.x >> 5)); m0 < moves;
        m0 += 32 * gridDim.x * (kMvThreads / 32)) {
-    int64_t src = 0, dst = 0;
+    int64_t src = 0, dst = 0, ds = 0;
     const int cnt = min(32, moves - m0);
+    float mass = 0.f, ks = 0.f, vs = 0.f;
+    int32_t order = 0;
     if (lane < cnt) {
       const int to = list[m0 + lane], from = list[a.half + m0 + lane];
       int tr, fr;
       const int tx = page_of(p, to, tr), fx = page_of(p, from, fr);
       const int tp = table[tx], fp = table[fx];
-      const int64_t ds = page_slot(p, tp, h, tr), ss = page_slot(p, fp, h, fr);
-      a.mass_out[ds] = p.mass[ss];
-      if (a.order_out) a.order_out[ds] = p.order[ss];
-      if (p.k_scale) {
-        p.k_scale[ds] = p.k_scale[ss];
-        p.v_scale[ds] = p.v_scale[ss];
-      }
+      ds = page_slot(p, tp, h, tr);
+      const int64_t ss = page_slot(p, fp, h, fr);
       dst = page_elem(p, tp, h, tr) * size;
       src = page_elem(p, fp, h, fr) * size;
+      mass = p.mass[ss];
+      if (a.order_out) order = p.order[ss];
+      if (p.k_scale) ks = p.k_scale[ss], vs = p.v_scale[ss];
     }
-    constexpr int kFlight = 8;
+    constexpr int kFlight = 4;
     for (int j0 = 0; j0 < cnt; j0 += kAtOnce * kFlight) {
       uint4 x[kFlight];
 #pragma unroll
@@ -453,6 +457,11 @@ __global__ void __launch_bounds__(kMvThreads) evict_move_kernel(const __grid_con
         const int64_t to = __shfl_sync(0xffffffffu, dst, j & 31);
         if (j < cnt) *reinterpret_cast<uint4*>(kv + to) = x[f];
       }
+    }
+    if (lane < cnt) {
+      a.mass_out[ds] = mass;
+      if (a.order_out) a.order_out[ds] = order;
+      if (p.k_scale) p.k_scale[ds] = ks, p.v_scale[ds] = vs;
     }
   }
 }
@@ -515,10 +524,9 @@ int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
 
 template <int RB>
 int launch_move(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
-  // two waves of eight CTAs to an SM over all (sequence, KV head) pairs, which
-  // walk over their moves
+  // four waves over all (sequence, KV head) pairs, which walk over their moves
   const int64_t units = (int64_t)a.pages.h_kv * a.pages.num_seqs;
-  const int64_t x = std::min<int64_t>((pl.half + kMvThreads - 1) / kMvThreads, (16LL * pl.sms + units - 1) / units);
+  const int64_t x = std::min<int64_t>((pl.half + kMvThreads - 1) / kMvThreads, (4LL * kMvCtas * pl.sms + units - 1) / units);
   return launch_pdl(evict_move_kernel<RB>, dim3((unsigned)x, a.pages.h_kv, a.pages.num_seqs), dim3(kMvThreads), 0, s,
                     a) == cudaSuccess
              ? AIRCACHE_OK
