@@ -55,6 +55,7 @@ struct Before {
 };
 
 constexpr int kBinBits = 8, kBins = 1 << kBinBits;
+constexpr int kNear = 4096;
 
 struct EvShared {
   uint32_t hist[4][kBins];
@@ -63,6 +64,7 @@ struct EvShared {
   uint32_t scan[kEvWarps], scan2[kEvWarps], scan3[kEvWarps];
   uint32_t least, most, safe, bad;  // this CTA's least and largest key, protected rows, bad pages
   uint32_t bin, above;
+  uint32_t near_count, near[kNear];  // the keys in the part of the range that the first histogram left
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -80,9 +82,11 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 
 // R CTAs (a cluster) per (sequence, KV head).  What they tell each other is read
 // by one lane per CTA at once, or by loads that do not wait for one another: a
-// load from another CTA's shared memory takes several hundred cycles.
-template <int R>
-__global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_constant__ EvArgs a) {
+// load from another CTA's shared memory takes several hundred cycles.  F groups of four rows
+// load at once in a thread: eight with one CTA to an SM, four (and half the registers) with two
+// (2 x 128k with 8 and 4: 47 and 52 us; ragged, 192 CTAs: 42 and 39.5).
+template <int R, int F>
+__global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kernel(const __grid_constant__ EvArgs a) {
   extern __shared__ uint32_t ev_keys[];
   __shared__ EvShared sh;
   const Pages& p = a.pages;
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   auto peer = [&](const uint32_t* x, int r) { return CL ? ld_cluster_u32(cluster_map(smem_u32(x), r)) : *x; };
   pdl_trigger();
   for (int i = tid; i < 4 * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.bad = 0;
+  if (tid == 0) sh.bad = sh.near_count = 0;
   __syncthreads();
   pdl_wait();
 
@@ -121,8 +125,8 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
   const int new_len = cut ? keep : n;
 
   // ---- keys of the slice, their range and the protected rows.  Four rows a thread
-  // (a page holds a multiple of 16), four such groups in flight
-  constexpr int kFlight = 4;
+  // (a page holds a multiple of 16)
+  constexpr int kFlight = F;
   uint32_t least = kProtected, most = 0, safe = 0;
   for (int i0 = 4 * tid; i0 < mine; i0 += 4 * kFlight * kEvThreads) {
     int page[kFlight], at[kFlight];
@@ -214,13 +218,28 @@ __global__ void __launch_bounds__(kEvThreads) evict_select_kernel(const __grid_c
       shift = max(0, shift - kBinBits);
       // (no protected row, nor what fills the last group of four, lies in it)
       const uint32_t left = min(top > 31 ? 0xffffffffu : (1u << top) - 1, kProtected - 1 - prefix);
-      for (int i = 4 * tid; i < mine; i += 4 * kEvThreads) {
-        const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
-        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t off = key[j] - prefix;  // (a key below the range wraps past it)
+      // the second histogram sets the keys that it counts aside, and the later ones look at these alone,
+      // if there are not too many (many equal keys)
+      if (d > 1 && sh.near_count <= kNear) {
+        for (uint32_t i = tid; i < sh.near_count; i += kEvThreads) {
+          const uint32_t off = sh.near[i] - prefix;
           if (off <= left) atomicAdd(&sh.hist[d][off >> shift], 1u);
+        }
+      } else {
+        for (int i = 4 * tid; i < mine; i += 4 * kEvThreads) {
+          const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
+          const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t off = key[j] - prefix;  // (a key below the range wraps past it)
+            if (off <= left) {
+              atomicAdd(&sh.hist[d][off >> shift], 1u);
+              if (d == 1) {
+                const uint32_t at = atomicAdd(&sh.near_count, 1u);
+                if (at < kNear) sh.near[at] = key[j];
+              }
+            }
+          }
         }
       }
       sync_all();
@@ -486,11 +505,11 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   if (p->max_rows > AIRCACHE_MAX_EVICT_ROWS) return AIRCACHE_ERR_UNSUPPORTED;
   pl.sms = device_sms();
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;
-  // CTAs per (sequence, KV head): enough that the batch fills the SMs twice,
-  // but at least 2048 rows to a CTA (each rank costs every barrier and
-  // histogram sum), and as many as the keys need room
+  // CTAs per (sequence, KV head): as many as leave every CTA an SM of its own
+  // (16 x 16k with 128 CTAs 60.5 us, with 256 61.3), but at least 2048 rows to a CTA (each rank costs every
+  // barrier and histogram sum), and as many as the keys need room
   int ranks = 1;
-  while (ranks < kEvMaxCluster && (units * ranks * 2 <= 2LL * pl.sms) && p->max_rows > 2048LL * ranks) ranks *= 2;
+  while (ranks < kEvMaxCluster && units * ranks * 2 <= pl.sms && p->max_rows > 2048LL * ranks) ranks *= 2;
   while (p->max_rows > (int64_t)kEvSlice * ranks) ranks *= 2;
   pl.ranks = ranks;
   pl.row_bytes = p->pages->head_dim * (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2);
@@ -501,9 +520,9 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   return AIRCACHE_OK;
 }
 
-template <int R>
+template <int R, int F>
 int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
-  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<R>), (int)pl.smem) != cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<R, F>), (int)pl.smem) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(R, a.pages.h_kv, a.pages.num_seqs);
@@ -519,7 +538,13 @@ int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = R > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R, F>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
+}
+
+template <int R>
+int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
+  const int64_t ctas = (int64_t)R * a.pages.h_kv * a.pages.num_seqs;
+  return ctas <= pl.sms ? launch_select<R, 8>(pl, a, s) : launch_select<R, 4>(pl, a, s);
 }
 
 template <int RB>
