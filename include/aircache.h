@@ -537,7 +537,7 @@ AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t
  *           bf16, or int8 codes with one fp32 scale per row and KV head
  *           (row = scale * code, scale >= 0).
  *   table   device int32 [num_seqs], rows table_stride apart, max_pages used.
- *           Only the entries of a sequence's own rows are read.
+ *           Entries behind a sequence's own rows may hold anything.
  *   lens    device int32 [num_seqs]: rows of each sequence.
  *   k_scale, v_scale, mass (fp32), order (int32): [num_pages][h_kv][page_rows], dense.
  *   mass    optional: attention weight a row has been given so far by its KV
@@ -611,7 +611,9 @@ typedef struct aircache_pages {
  * row's head in fp32 and codes round(y / s), half away from zero (0 for a row
  * of zeros).  Without a cache cu_tokens may be NULL (no padding) and positions
  * must be given.
- * q_out may be q and k_out may be k (the same pointer and strides: in place).
+ * q_out may be q and k_out may be k (the same pointer and strides: in place);
+ * otherwise outputs do not overlap inputs, nor their own rows (strides of at
+ * least head_dim where there is more than one token or head).
  *
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; head_dim
  * 64 or 128; at least one of q, k; q_out with q; k_out or pages with k; v
@@ -720,9 +722,10 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  *
  * mass_out and order_out are pages->mass and pages->order (in place) or other
  * arrays of their shape and alignment, which then get the entries of all rows below
- * lens_out[s] and nothing else (of a sequence in error: some of its entries).  lens is read by every KV head and lens_out
- * must be another array (several layers are cut by the same lens before it
- * takes lens_out's values).
+ * lens_out[s] and nothing else (of a sequence in error: some of its entries).
+ * lens, keep and seen are read by every KV head, so lens_out must be an array
+ * of its own (several layers are cut by the same lens before it takes
+ * lens_out's values).
  *
  * max_rows bounds lens; it sizes the workspace and the launch, and is at most
  * AIRCACHE_MAX_EVICT_ROWS (else AIRCACHE_ERR_UNSUPPORTED).  A sequence with a

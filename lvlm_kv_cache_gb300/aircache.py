@@ -711,6 +711,8 @@ class PagedCache:
         if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
             raise ValueError("table is an int32 [S, max_pages] tensor with contiguous rows")
         S, max_pages = (int(x) for x in table.shape)
+        if S > 1 and table.stride(0) < max_pages:
+            raise ValueError("the table's rows must not overlap")
         _dense(lens, torch.int32, (S,), "lens")
         q8 = k.dtype == torch.int8
         if q8 != (k_scale is not None) or q8 != (v_scale is not None):
@@ -814,6 +816,8 @@ class RotateProblem:
 
 
 def aircache_rotate(prob: RotateProblem, status=None, stream=None):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status is an int32 tensor")
     if prob.empty:  # (tensors without storage)
         return
     s = _paged_stream(prob, status, stream)

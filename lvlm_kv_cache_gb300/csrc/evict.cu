@@ -497,7 +497,8 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   if (!p) return AIRCACHE_ERR_INVALID_ARG;
   const int rc = check_pages(p->pages, pl.pages);
   if (rc != AIRCACHE_OK) return rc;
-  if (!p->keep || !p->lens_out || p->lens_out == p->pages->lens || !p->pages->mass || !p->mass_out ||
+  if (!p->keep || !p->lens_out || p->lens_out == p->pages->lens || p->lens_out == p->keep ||
+      p->lens_out == p->seen || !p->pages->mass || !p->mass_out ||
       (!p->order_out) != (!p->pages->order) || (reinterpret_cast<uintptr_t>(p->mass_out) & 15) != 0 ||
       (reinterpret_cast<uintptr_t>(p->order_out) & 15) != 0 || p->sink < 0 || p->recent < 0 ||
       ((p->sink || p->recent) && !p->pages->order) || (p->recent && !p->seen) || p->max_rows < 1)

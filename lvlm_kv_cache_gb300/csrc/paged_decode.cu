@@ -611,6 +611,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       x += __shfl_xor_sync(0xffffffffu, x, 2);
       if (cq == 0) {
         float* w = mlw + (warp * kPdGroup + hA + 8 * b) * 3;
+        // (logits that are all NaN leave no reference: any other than "no rows" passes them on)
+        if (x != x && m[b] == -INFINITY) m[b] = 0.f;
         w[0] = m[b], w[1] = x, w[2] = Q8 ? n[b] : m[b];
       }
     }
@@ -679,15 +681,15 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
     constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
     auto finish = [&](int hh, float m, float l) {  // the head's log-sum-exp
-      if (a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-      if (a.mass_out) a.lse2[head0 + hh] = l > 0.f ? m + log2f(l) : INFINITY;
+      if (a.lse) a.lse[head0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      if (a.mass_out) a.lse2[head0 + hh] = l == 0.f ? INFINITY : m + log2f(l);
     };
     if (r.count == r.tiles) {
       for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
         const int hh = c / (D / 4), d = c % (D / 4) * 4;
         float m, l, n;
         joined(hh, m, l, n);
-        const float f = l > 0.f ? kUndo * fast_exp2(n - m) / l : 0.f;
+        const float f = l == 0.f ? 0.f : kUndo * fast_exp2(n - m) / l;
         __nv_bfloat162 x[2] = {__floats2bfloat162_rn(joined_o(hh, d) * f, joined_o(hh, d + 1) * f),
                                __floats2bfloat162_rn(joined_o(hh, d + 2) * f, joined_o(hh, d + 3) * f)};
         *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
@@ -767,10 +769,10 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
         m = m1;
         n = n1;
       }
-      const float f = l > 0.f ? undo * fast_exp2(n - m) / l : 0.f;
+      const float f = l == 0.f ? 0.f : undo * fast_exp2(n - m) / l;
       __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
       *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
-      if (d == 0 && a.lse) a.lse[head0 + hh] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (d == 0 && a.lse) a.lse[head0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
   }
   if (!MASS) return;
@@ -818,7 +820,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
         for (int off = width; off < 32; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
         l = m == -INFINITY ? 0.f : l * fast_exp2(m - m1);
         for (int off = width; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        lse = l > 0.f ? m1 + log2f(l) : INFINITY;
+        lse = l == 0.f ? INFINITY : m1 + log2f(l);
       }
     }
     float2 sum = make_float2(0.f, 0.f);
@@ -862,7 +864,7 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   if (rc != AIRCACHE_OK) return rc;
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
   if (p->h_q <= 0 || p->h_q % p->pages->h_kv != 0 || p->reserved0 != 0 || p->dtype != AIRCACHE_BF16 ||
-      !(p->scale > 0.f) || !std::isfinite(p->scale) || p->total_rows < 1 || p->total_rows > 0x7fff0000LL || !p->q ||
+      !(p->scale > 0.f) || !std::isfinite(1.4427f * p->scale) || p->total_rows < 1 || p->total_rows > 0x7fff0000LL || !p->q ||
       !p->out || !al16(p->q) || !al16(p->out) || p->q_stride_seq < 0 || p->q_stride_head < 0 ||
       p->q_stride_seq % 8 != 0 || p->q_stride_head % 8 != 0 || (p->mass_out && !p->pages->mass) ||
       (reinterpret_cast<uintptr_t>(p->lse) & 3) != 0 || !al16(p->mass_out))

@@ -369,6 +369,13 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
       (p->q_out && !strides(p->qo_stride_tok, p->qo_stride_head)) ||
       (p->k_out && !strides(p->ko_stride_tok, p->ko_stride_head)))
     return AIRCACHE_ERR_INVALID_ARG;
+  // rows of an output do not overlap
+  auto apart = [&](int64_t tok, int64_t head, int heads) {
+    return (p->num_tokens <= 1 || tok >= p->head_dim) && (heads <= 1 || head >= p->head_dim);
+  };
+  if ((p->q_out && !apart(p->qo_stride_tok, p->qo_stride_head, p->h_q)) ||
+      (p->k_out && !apart(p->ko_stride_tok, p->ko_stride_head, p->h_kv)))
+    return AIRCACHE_ERR_INVALID_ARG;
   // in place means the same rows, not shifted ones
   if ((p->q && p->q_out == p->q && (p->qo_stride_tok != p->q_stride_tok || p->qo_stride_head != p->q_stride_head)) ||
       (p->k_out && p->k_out == p->k &&

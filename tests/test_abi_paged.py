@@ -65,7 +65,8 @@ BAD_PAGES = [
     ("num_seqs", -1), ("num_seqs", 65536), ("h_kv", 0), ("head_dim", 96), ("kv_dtype", 0), ("kv_dtype", 2),
     ("page_rows", 8), ("page_rows", 24), ("page_rows", 8192), ("max_pages", 0), ("max_pages", 1 << 28),
     ("num_pages", 0), ("num_pages", 1 << 31), ("k", None), ("v", 0x200008), ("stride_page", 0), ("stride_row", 516),
-    ("stride_head", -128), ("table", None), ("table_stride", 9), ("lens", None), ("lens", 0x400002)]
+    ("stride_head", -128), ("table", None), ("table_stride", 9), ("lens", None), ("lens", 0x400002), ("mass", 0x500004),
+    ("order", 0x600008)]
 
 
 @pytest.mark.parametrize("field,value", BAD_PAGES)
@@ -107,7 +108,8 @@ def test_decode_workspace_and_mass(A):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(keep=None), -1), (dict(lens_out=None), -1), (dict(lens_out=0x400000), -1), (dict(mass_out=None), -1),
+    (dict(keep=None), -1), (dict(lens_out=None), -1), (dict(lens_out=0x400000), -1), (dict(lens_out=0x700000), -1), (dict(lens_out=0x710000), -1),
+    (dict(mass_out=0x500008), -1), (dict(mass_out=None), -1),
     (dict(order_out=None), -1), (dict(sink=-1), -1), (dict(recent=-1), -1), (dict(seen=None), -1),
     (dict(max_rows=0), -1), (dict(max_rows=393217), -2)])
 def test_bad_evict_rejected(A, over, code):
@@ -135,7 +137,7 @@ def test_evict_pages_and_workspace(A):
     dict(rotary_dim=-16), dict(turns=None), dict(axes=2), dict(axes=3), dict(axes=3, positions=0x1900000, section0=65),
     dict(axes=3, positions=0x1900000, section0=-1), dict(seen=None), dict(cu_tokens=None), dict(q=0x1000008),
     dict(k_stride_tok=4604), dict(qo_stride_head=-128), dict(q_out=0x1000000), dict(k_out=0x1100000),
-    dict(q_weight=0x1500002)])
+    dict(q_weight=0x1500002), dict(qo_stride_head=64), dict(ko_stride_tok=0), dict(qo_stride_tok=64)])
 def test_bad_rotate_rejected(A, over):
     p = rotate(A, **over)
     assert A.lib().aircache_rotate(ctypes.byref(p), None, None) == A.ERR_INVALID_ARG
@@ -165,6 +167,8 @@ def test_tensors_of_the_wrong_kind_are_refused(A):
         a.update(bad)
         with pytest.raises((ValueError, TypeError)):
             A.PagedCache(**a)
+    with pytest.raises(ValueError):  # one row of pages for every sequence
+        A.PagedCache(k, k.clone(), t.expand(3, 2), torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError):
         A.RotateProblem()
     with pytest.raises(ValueError):

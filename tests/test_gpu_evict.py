@@ -158,6 +158,19 @@ def test_largest_slices(A):
     check(A, cache, [60_000] + [2] * 39)
 
 
+def test_the_longest_sequence(A):
+    n = A.MAX_EVICT_ROWS - 5
+    cache = P.build(A, [n], 1, 64, 256, seed=12, order=False)
+    check(A, cache, [150_001], max_rows=A.MAX_EVICT_ROWS)
+
+
+def test_more_protected_rows_than_places(A):
+    # an order that no append makes: every row is "first"; the lowest rows stay
+    cache = P.build(A, [500, 40], 2, 64, 16, seed=13)
+    cache.order.zero_()
+    check(A, cache, [100, 10], sink=1)
+
+
 def test_again_after_appending(A):
     # an eviction leaves a cache that the next one can cut
     cache = P.build(A, [400, 90], 2, 64, 16, seed=9)

@@ -319,3 +319,28 @@ def test_elements_past_32_bits(A):
     big = A.PagedCache(k, v, table, small.lens)
     assert torch.equal(A.paged_decode(A.PagedDecodeProblem(q, big, total_rows=389)),
                        A.paged_decode(A.PagedDecodeProblem(q, small, total_rows=389)))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_nan_in_a_row_that_counts_is_not_hidden(A, int8):
+    # one sequence's keys (or their scales) are all NaN, another's one value; the third is clean
+    cache = P.build(A, [40, 300, 70], 2, 128, 16, seed=21, int8=int8)
+    q = queries(3, 6, 128, 21)
+    if int8:
+        cache.k_scale[cache.table[0, :3].long()] = float("nan")
+        cache.v_scale[cache.table[1, 9].long(), 0, 5] = float("nan")
+    else:
+        cache.k[cache.table[0, :3].long()] = float("nan")
+        cache.v[cache.table[1, 9].long(), 5, 0, 17] = float("nan")
+    prob = A.PagedDecodeProblem(q, cache, lse=True)
+    A.paged_decode(prob)
+    assert bool(torch.isnan(prob.out[0]).all()) and bool(torch.isnan(prob.lse[0]).all())
+    hit = torch.isnan(prob.out[1])
+    assert bool(hit[:3, 17].all()) and not bool(hit[3:].any())
+    assert bool(torch.isfinite(prob.out[2]).all()) and bool(torch.isfinite(prob.lse[1:]).all())
+    one = P.build(A, [70], 2, 128, 16, seed=21, int8=int8)  # the query itself
+    q1 = queries(1, 6, 128, 21)
+    q1[0, 2] = float("nan")
+    p1 = A.PagedDecodeProblem(q1, one, lse=True)
+    A.paged_decode(p1)
+    assert bool(torch.isnan(p1.out[0, 2]).all())
