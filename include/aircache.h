@@ -556,9 +556,10 @@ AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t
  * scales), page_rows a multiple of 16 in 16..4096, max_pages >= 1 with
  * max_pages * page_rows <= 2^31 - 2^16, 1 <= num_pages <= 2^31 - 1, table_stride >=
  * max_pages; k, v, the scales, mass and order 16-byte aligned, strides positive
- * multiples of 16 bytes.  Device-side, a length outside [0, max_pages * page_rows] or a page outside
- * [0, num_pages) sets AIRCACHE_ERR_DEVICE_BOUNDS; nothing is then read or
- * written through it (each entry point says what becomes of the sequence).
+ * multiples of 16 bytes.  Device-side, a length outside
+ * [0, max_pages * page_rows] or a page outside [0, num_pages) sets
+ * AIRCACHE_ERR_DEVICE_BOUNDS; nothing is then read or written through it (each
+ * entry point says what becomes of the sequence).
  */
 typedef struct aircache_pages {
     int32_t num_seqs;
@@ -607,9 +608,9 @@ typedef struct aircache_pages {
  * With a cache (pages != NULL), lens[s] counts the rows of s AFTER the append:
  * the n tokens of s become its rows lens[s]-n .. lens[s]-1, with mass 0 (if
  * the cache has mass) and order seen[s]-n .. seen[s]-1 (if it has order), where
- * seen[s] is the number of tokens appended to s so far, these n among them.  int8 caches get s = max |y| / 127 of the
- * row's head in fp32 and codes round(y / s), half away from zero (0 for a row
- * of zeros).  Without a cache cu_tokens may be NULL (no padding) and positions
+ * seen[s] is the number of tokens appended to s so far, these n among them.
+ * int8 caches get s = max |y| / 127 of the row's head in fp32 and codes
+ * round(y / s), half away from zero (0 for a row of zeros).  Without a cache cu_tokens may be NULL (no padding) and positions
  * must be given.
  * q_out may be q and k_out may be k (the same pointer and strides: in place);
  * otherwise outputs do not overlap inputs, nor their own rows (strides of at
@@ -683,8 +684,8 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  * length counts as 0, a bad page's rows count as not there.
  * Requirements: dtype AIRCACHE_BF16; h_q a multiple of h_kv (else
  * AIRCACHE_ERR_INVALID_ARG) with at most 16 query heads to a KV head (else
- * AIRCACHE_ERR_UNSUPPORTED); 1 <= total_rows <= 2^31 - 2^16; scale > 0 and finite; q 16-byte
- * aligned and its strides multiples of 8; out and mass_out 16-byte aligned, dense; mass_out
+ * AIRCACHE_ERR_UNSUPPORTED); 1 <= total_rows <= 2^31 - 2^16; scale > 0 and
+ * finite; q 16-byte aligned and its strides multiples of 8; out and mass_out 16-byte aligned, dense; mass_out
  * only with pages->mass.
  *
  * The workspace is caller-owned, 256-byte aligned, ZEROED ONCE before its first
@@ -713,11 +714,11 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
 /*
  * Eviction by accumulated attention weight: of the n = lens[s] rows of sequence
  * s, every KV head keeps keep[s] (all if n <= keep[s]): first its protected rows
- * (order < sink, or order >= seen[s] - recent), then those of largest mass, ties to
- * the lower row (a NaN counts as -inf).  Kept rows that lie at keep[s] or behind move, in ascending
- * order, into the vacated rows below keep[s], in ascending order, and take
- * their scales, mass and order along; every other row stays where it is, so as
- * few bytes as possible move.  lens_out[s] = min(n, keep[s]); pages past
+ * (order < sink, or order >= seen[s] - recent), then those of largest mass,
+ * ties to the lower row (a NaN counts as -inf).  Kept rows that lie at keep[s]
+ * or behind move, in ascending order, into the vacated rows below keep[s], in
+ * ascending order, and take their scales, mass and order along; every other
+ * row stays where it is, so as few bytes as possible move.  lens_out[s] = min(n, keep[s]); pages past
  * ceil(lens_out[s] / page_rows) are the caller's again.
  *
  * mass_out and order_out are pages->mass and pages->order (in place) or other
@@ -729,12 +730,12 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  *
  * max_rows bounds lens; it sizes the workspace and the launch, and is at most
  * AIRCACHE_MAX_EVICT_ROWS (else AIRCACHE_ERR_UNSUPPORTED).  A sequence with a
- * length outside [0, max_rows], a page out of bounds, keep[s] < 0, or n > keep[s] < sink + recent
- * sets AIRCACHE_ERR_DEVICE_BOUNDS and keeps its rows, mass and order
- * (lens_out[s] = lens[s]).
+ * length outside [0, max_rows], a page out of bounds, keep[s] < 0, or
+ * n > keep[s] < sink + recent sets AIRCACHE_ERR_DEVICE_BOUNDS and keeps its
+ * rows, mass and order (lens_out[s] = lens[s]).
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): mass; order when sink or recent
- * is not 0, seen when recent is not 0; order_out exactly with order; sink, recent >= 0.  Workspace as
- * for aircache_paged_decode.  Two kernels: one selects, one moves.
+ * is not 0, seen when recent is not 0; order_out exactly with order; sink,
+ * recent >= 0.  Workspace as for aircache_paged_decode.  Two kernels: one selects, one moves.
  */
 #define AIRCACHE_MAX_EVICT_ROWS 393216
 
