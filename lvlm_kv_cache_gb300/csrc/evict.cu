@@ -55,7 +55,7 @@ struct Before {
 };
 
 constexpr int kBinBits = 8, kBins = 1 << kBinBits;
-constexpr int kNear = 4096;
+constexpr int kNear = 256;  // keys that a warp can set aside
 
 struct EvShared {
   uint32_t hist[4][kBins];
@@ -64,7 +64,7 @@ struct EvShared {
   uint32_t scan[kEvWarps], scan2[kEvWarps], scan3[kEvWarps];
   uint32_t least, most, safe, bad;  // this CTA's least and largest key, protected rows, bad pages
   uint32_t bin, above;
-  uint32_t near_count, near[kNear];  // the keys in the part of the range that the first histogram left
+  uint32_t near[kEvWarps][kNear];  // the keys in the part of the range that the first histogram left
 };
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -103,11 +103,12 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   auto peer = [&](const uint32_t* x, int r) { return CL ? ld_cluster_u32(cluster_map(smem_u32(x), r)) : *x; };
   pdl_trigger();
   for (int i = tid; i < 4 * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.bad = sh.near_count = 0;
+  if (tid == 0) sh.bad = 0;
   __syncthreads();
   pdl_wait();
 
   const int len = p.lens[s], keep = a.keep[s];
+  const int32_t seen = a.recent ? a.seen[s] : 0;
   const bool sane = len >= 0 && len <= a.max_rows && len <= p.max_rows && keep >= 0 &&
                     (len <= keep || (int64_t)keep >= (int64_t)a.sink + a.recent);
   if (!sane && tid == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   const int per = ((n + R - 1) / R + 15) & ~15;
   const int lo = min(rank * per, n), mine = min(per, n - lo);  // this CTA's rows
   const int32_t* table = p.table + (int64_t)s * p.table_stride;
-  const int32_t fresh = a.seen && a.recent ? a.seen[s] - a.recent : 0x7fffffff;  // order from which rows are recent
+  const int32_t fresh = a.recent ? seen - a.recent : 0x7fffffff;  // order from which rows are recent
   const bool aged = a.sink | a.recent;
 
   // Where mass and order go to other arrays, every row below the new length is
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
 
   // ---- the threshold, and how many of the rows at it stay (`need`).  Protected
   // rows stay, unless there are more of them than places
-  uint32_t prefix = kProtected, need = keep;
+  uint32_t prefix = kProtected, need = keep, near = 0;
   if (go && safe < (uint32_t)keep) {
     need = keep - safe;
     prefix = least;  // where the range that is left begins
@@ -218,27 +219,35 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
       shift = max(0, shift - kBinBits);
       // (no protected row, nor what fills the last group of four, lies in it)
       const uint32_t left = min(top > 31 ? 0xffffffffu : (1u << top) - 1, kProtected - 1 - prefix);
-      // the second histogram sets the keys that it counts aside, and the later ones look at these alone,
-      // if there are not too many (many equal keys)
-      if (d > 1 && sh.near_count <= kNear) {
-        for (uint32_t i = tid; i < sh.near_count; i += kEvThreads) {
-          const uint32_t off = sh.near[i] - prefix;
+      // with the second histogram each warp sets the keys that it counts aside, and looks at these
+      // alone in the later ones, if they have room (they have not with many equal keys)
+      if (d > 1 && near <= kNear) {
+        for (uint32_t i = lane; i < near; i += 32) {
+          const uint32_t off = sh.near[warp][i] - prefix;
           if (off <= left) atomicAdd(&sh.hist[d][off >> shift], 1u);
         }
       } else {
-        for (int i = 4 * tid; i < mine; i += 4 * kEvThreads) {
-          const uint4 k4 = *reinterpret_cast<const uint4*>(ev_keys + i);
+        for (int i0 = 0; i0 < mine; i0 += 4 * kEvThreads) {
+          const int i = i0 + 4 * tid;
+          const uint4 k4 = i < mine ? *reinterpret_cast<const uint4*>(ev_keys + i)
+                                    : make_uint4(kProtected, kProtected, kProtected, kProtected);
           const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+          bool in[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t off = key[j] - prefix;  // (a key below the range wraps past it)
-            if (off <= left) {
-              atomicAdd(&sh.hist[d][off >> shift], 1u);
-              if (d == 1) {
-                const uint32_t at = atomicAdd(&sh.near_count, 1u);
-                if (at < kNear) sh.near[at] = key[j];
-              }
+            in[j] = off <= left;
+            if (in[j]) atomicAdd(&sh.hist[d][off >> shift], 1u);
+          }
+          if (d == 1 && __any_sync(0xffffffffu, in[0] || in[1] || in[2] || in[3])) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t hits = __ballot_sync(0xffffffffu, in[j]);
+              const uint32_t at = near + __popc(hits & ((1u << lane) - 1));
+              if (in[j] && at < kNear) sh.near[warp][at] = key[j];
+              near += __popc(hits);
             }
+            __syncwarp();
           }
         }
       }
@@ -354,22 +363,22 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
       const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
       const bool tied = key[0] == prefix || key[1] == prefix || key[2] == prefix || key[3] == prefix;
       if (i0 + 128 <= w1 && (lo + i0 + 128 <= keep || lo + i0 >= keep) && !__any_sync(0xffffffffu, tied)) {
-        // 128 rows on one side of keep and off the threshold: only lesser or only greater rows count
+        // 128 rows on one side of keep and off the threshold: only lesser or only greater rows
+        // count.  (Taken 32 rows at a time here; the vote above is past every lane's reads.)
         const bool high = lo + i0 >= keep;
-        uint32_t is[4], c = 0;
+        const uint32_t stay = min(at.ties, need);
+        uint32_t to = high ? holes + at.more + stay - mover0 : at.less + at.ties - stay - hole0;
+        uint32_t row_key[4], all = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c += is[j] = (key[j] > prefix) == high;
-        uint32_t incl = c;
+        for (int j = 0; j < 4; ++j) row_key[j] = ev_keys[i0 + 32 * j + lane];
+        __syncwarp();
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t t = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += t;
+        for (int j = 0; j < 4; ++j) {
+          const bool is = (row_key[j] > prefix) == high;
+          const uint32_t hits = __ballot_sync(0xffffffffu, is);
+          if (is) packed[to + all + __popc(hits & ((1u << lane) - 1))] = lo + i0 + 32 * j + lane;
+          all += __popc(hits);
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, incl, 31), stay = min(at.ties, need);
-        uint32_t* to = packed + incl - c + (high ? holes + at.more + stay - mover0 : at.less + at.ties - stay - hole0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (is[j]) *to++ = lo + i + j;
         if (high)
           at.more += all;
         else
