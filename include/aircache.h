@@ -624,7 +624,8 @@ typedef struct aircache_pages {
  * rotary_dim > 0); pointers 16-byte aligned, strides multiples of 8 elements.
  * A token whose row or page is out of bounds sets AIRCACHE_ERR_DEVICE_BOUNDS
  * in *status (optional device int32, not cleared by the call) and is not
- * appended; its q_out and k_out are written.  One kernel.
+ * appended; its q_out and k_out are written.  cu_tokens[num_seqs] > num_tokens
+ * sets it too.  One kernel.
  */
 typedef struct aircache_rotate_problem {
     int64_t num_tokens;   /* rows of q, k, v: 0..2^31-1 */

@@ -682,6 +682,22 @@ def _paged_stream(prob, ws, stream):
     return torch._C._cuda_getCurrentRawStream(prob.device.index) if stream is None else stream.cuda_stream
 
 
+def _on_stream(prob, stream, make):
+    """make() with its allocations and kernels on the stream that a call on `prob` will use."""
+    with torch.cuda.device(prob.device), torch.cuda.stream(stream):  # (None: the current stream)
+        return make()
+
+
+def _check_device(prob, word, stream, where):
+    """Waits for the call's stream and raises what the device recorded in `word`."""
+    if prob.empty:
+        return
+    with torch.cuda.device(prob.device):
+        st = aircache_get_error(word, stream)
+    if st != OK:
+        raise AirCacheError(st, where + " (device)")
+
+
 def _run_paged(fn, where, prob, *args):
     """fn(problem, *args) on the problem's device, whichever the current one is."""
     if torch._C._cuda_getDevice() == prob.device.index:
@@ -826,12 +842,10 @@ def aircache_rotate(prob: RotateProblem, status=None, stream=None):
 
 def rotate(prob: RotateProblem, stream=None, check=True):
     """One call; returns (q_out, k_out).  check=True reads the device status (synchronises)."""
-    st = torch.zeros(1, dtype=torch.int32, device=prob.device) if check else None
+    st = _on_stream(prob, stream, lambda: torch.zeros(1, dtype=torch.int32, device=prob.device)) if check else None
     aircache_rotate(prob, st, stream)
     if check:
-        code = aircache_get_error(st, stream)
-        if code != OK:
-            raise AirCacheError(code, "aircache_rotate (device)")
+        _check_device(prob, st, stream, "aircache_rotate")
     return prob.q_out, prob.k_out
 
 
@@ -853,8 +867,8 @@ class PagedDecodeProblem:
             raise ValueError("q must have the cache's sequences and head_dim")
         if out is None:
             out = torch.empty((S, h_q, d), dtype=torch.bfloat16, device=q.device)
-        if lse is True:
-            lse = torch.empty((S, h_q), dtype=torch.float32, device=q.device)
+        if isinstance(lse, bool):
+            lse = torch.empty((S, h_q), dtype=torch.float32, device=q.device) if lse else None
         _dense(out, torch.bfloat16, (S, h_q, d), "out")
         _dense(lse, torch.float32, (S, h_q), "lse")
         if accumulate and mass_out is None:
@@ -898,12 +912,10 @@ def aircache_paged_decode(prob: PagedDecodeProblem, ws, stream=None):
 
 def paged_decode(prob: PagedDecodeProblem, ws=None, stream=None, check=True):
     """One decode step; returns prob.out.  check=True reads the device error word (synchronises)."""
-    ws = prob.new_workspace() if ws is None else ws
+    ws = _on_stream(prob, stream, prob.new_workspace) if ws is None else ws
     aircache_paged_decode(prob, ws, stream)
     if check:
-        st = aircache_get_error(ws, stream)
-        if st != OK:
-            raise AirCacheError(st, "aircache_paged_decode (device)")
+        _check_device(prob, ws, stream, "aircache_paged_decode")
     return prob.out
 
 
@@ -961,10 +973,8 @@ def aircache_evict(prob: EvictProblem, ws, stream=None):
 
 def evict(prob: EvictProblem, ws=None, stream=None, check=True):
     """One eviction; returns prob.lens_out.  check=True reads the device error word (synchronises)."""
-    ws = prob.new_workspace() if ws is None else ws
+    ws = _on_stream(prob, stream, prob.new_workspace) if ws is None else ws
     aircache_evict(prob, ws, stream)
     if check:
-        st = aircache_get_error(ws, stream)
-        if st != OK:
-            raise AirCacheError(st, "aircache_evict (device)")
+        _check_device(prob, ws, stream, "aircache_evict")
     return prob.lens_out

@@ -9,10 +9,12 @@
 // D/8 lanes take one head's row, eight elements a lane, so a warp works on 2 (D =
 // 128) or 4 (D = 64) rows at once; it walks over the query, key and value heads
 // of ONE token, so that the token's sines and cosines are formed once, in the
-// registers of the lanes that need them, multiplied by the norm's weights, and the slot in
-// the cache is looked up once.  Both elements of a pair lie in one lane (half
-// style: four elements and the four half a rotation further), so a row costs no
-// shuffles but the norm's.  With few tokens a token's heads go to several warps.
+// registers of the lanes that need them, multiplied by the norm's weights, and
+// the slot in the cache is looked up once.  Both elements of a pair lie in one
+// lane (half style: four elements and the four half a rotation further), so a
+// row costs no shuffles but the norm's.  With few tokens a token's heads go to
+// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 3.3 us; 15,541 of them, the
+// keys also dense, in 57 us (303 MB read and written, 5.3 TB/s).
 //
 // The angle: position * (hi + lo) turns is reduced before it is rounded.  The
 // position splits into two parts of at most 20 bits (exact in fp32), each
@@ -254,7 +256,8 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
 }
 
 template <int D, bool Q8, bool INTER, int NB>
-__global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRotWarps) rotate_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRotWarps)
+    rotate_kernel(const __grid_constant__ RotArgs a) {
   constexpr int kLanes = D / 8;
   const int lane = threadIdx.x & 31, l = lane % kLanes;
   const int64_t w = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
@@ -290,6 +293,8 @@ __global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRo
   int s = 0, back = 0;
   x.order = 0;
   if (a.cu_tokens) {
+    if (w == 0 && lane == 0 && a.status && a.cu_tokens[a.num_seqs] > a.num_tokens)
+      set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);  // tokens that the batch does not have
     s = find_seq(a.cu_tokens, a.num_seqs, (int)t, lane);
     if (s < 0 || s >= a.num_seqs) return;  // padding
     back = a.cu_tokens[s + 1] - (int)t;

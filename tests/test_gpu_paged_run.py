@@ -137,3 +137,26 @@ def test_two_layers_on_two_streams_with_their_own_workspaces(A):
     for p, b, q, ws in zip(probs, before, qs, wss):
         verify(p, b, q)
         assert A.aircache_get_error(ws) == A.OK
+
+
+def test_calls_on_a_side_stream_without_a_workspace(A):
+    # the conveniences allocate and zero their workspace on the stream that the call uses
+    s = torch.cuda.Stream()
+    cache = P.build(A, [500, 33], 2, 64, 16, seed=50)
+    g = torch.Generator(device="cuda").manual_seed(51)
+    q = torch.randn((2, 6, 64), generator=g, device="cuda").to(torch.bfloat16)
+    before = P.host(cache)
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy * 1e-3  # keeps the current stream behind
+    prob = A.PagedDecodeProblem(q, cache, lse=True, accumulate=True)
+    A.paged_decode(prob, stream=s)
+    verify(prob, before, q)
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    keep, out = t([100, 20]), t([0, 0])
+    torch.cuda.synchronize()
+    st = P.state(cache)
+    want, new = expect(st, cache, [100, 20], None, 0, 0)
+    assert A.evict(A.EvictProblem(cache, keep, out), stream=s).tolist() == new
+    P.assert_same_state(want, P.state(cache))

@@ -193,9 +193,12 @@ def test_append(A, int8, page_rows, d, new, old):
             assert np.array_equal(want[name], after[name]), name  # nothing else was written
 
 
-def test_int8_values_are_coded_exactly(A):
+@pytest.mark.parametrize("size", [1.0, 1e30, 1e-36, 1e-38, 3e-40])
+def test_int8_values_are_coded_exactly(A, size):
     # values pass unrotated: scale and code are exact functions of the bf16 input, as aircache_quantize_int8's
+    # (down to scales that are subnormal, where 1/scale overflows and max/127 is a coarse rounding)
     cache, prob, (q, k, v, *_rest) = append_case(A, [200], [0], True, 32, seed=8)
+    v.copy_((v.double() * size).to(torch.bfloat16))
     A.rotate(prob)
     c = P.host(cache)
     x = v.float().cpu().numpy()
@@ -226,6 +229,23 @@ def test_out_of_bounds_is_reported_and_not_written(A):
     A.aircache_rotate(prob, st)
     with pytest.raises(A.AirCacheError):
         A.rotate(prob)
+
+
+def test_tokens_that_the_batch_does_not_have(A):
+    cache, prob, (q, k, v, w, f, cu, seen) = append_case(A, [3, 4], [0, 5], False, 16)
+    cu[2] = 9  # seven tokens are there
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    A.aircache_rotate(prob, st)
+    assert A.aircache_get_error(st) == A.ERR_DEVICE_BOUNDS
+
+
+def test_status_of_another_kind_is_refused(A):
+    q = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda")
+    prob = A.RotateProblem(q)
+    for bad in (torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            A.aircache_rotate(prob, bad)
 
 
 def test_plain_rows_into_pages(A):
