@@ -40,7 +40,7 @@
 // Measured (28 query and 4 KV heads of 128, calls back to back): 16 x 16,384
 // bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 us; 8 x 32,768 int8 rows 64 us
 // (277 MB); 32 heads of 64 over 55,113 rows 76 us (452 MB, 5.9 TB/s); one
-// sequence of 701 rows 8.3 us, two launches.
+// sequence of 701 rows 8.9 us, of 8,192 11.1 us, of 131,072 49 us; two launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -95,6 +95,7 @@ struct PdArgs {
   float* mass_out;
   int32_t* error;
   int32_t* tiles;    // tile count, for the mass kernel
+  int2* cut;         // [CTAs]: the unit that begins in the CTA and ends in another (-1: none), and its parts
   int2* unit;        // [S * h_kv]: the first CTA that has a part of it, and how many have one
   float* lse2;       // [S * h_q] base 2, of units that one CTA has whole
   float4* part_ml;   // [2 CTAs][g]: m, l, n of O
@@ -102,7 +103,7 @@ struct PdArgs {
   TileInfo* info;    // [tiles]
   float* logits;     // [tiles][g][64], base 2
   int64_t total_rows;
-  int h_q, group;
+  int h_q, group, ctas;
   float scale_log2;
 };
 
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
 
   // ---- consumers
   const int hA = lane >> 2, cq = lane & 3;  // S: heads hA and hA + 8, rows 2cq, 2cq + 1 of each eight
+  if (tid == 0) a.cut[blockIdx.x] = make_int2(-1, 0);  // (until a run says otherwise)
   // sequences without rows: out = 0, lse = -inf
   for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
@@ -691,7 +693,9 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     };
     if (tid == 0 && r.first == 0) {
       const int c0 = (int)(r.unit / sh.per);
-      a.unit[r.s * p.h_kv + r.h] = make_int2(c0, (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1);
+      const int parts = (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1;
+      a.unit[r.s * p.h_kv + r.h] = make_int2(c0, parts);
+      if (parts > 1) a.cut[blockIdx.x] = make_int2(r.s * p.h_kv + r.h, parts);
     }
     const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
     constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
@@ -728,75 +732,134 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   }
 }
 
-// After the attention.  Joins the parts of the units that several CTAs shared: a
-// unit to a CTA, four columns a thread.  MASS: also turns the stored logits into
-// weights and adds them to the rows' mass: a warp takes a run of tiles, a lane two
-// rows of each; it forms its unit's log-sum-exps from the parts itself, which costs less
-// than a third launch that waits for the join (16 x 16k: 103 us, and 107 with that launch).
+// The parts j0, j0 + step, .. of one unit, head hh and four columns, N of them in flight.
+struct Joined {
+  float m, l, n;
+  float4 o;
+  __device__ __forceinline__ void rescale(float m1, float n1) {
+    l *= m == -INFINITY ? 0.f : fast_exp2(m - m1);
+    const float f = m == -INFINITY ? 0.f : fast_exp2(n - n1);
+    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+    m = m1;
+    n = n1;
+  }
+  __device__ __forceinline__ void add(const float4& x, const float4& y) {  // (m, l, n) and O, under the references
+    if (x.x == -INFINITY) return;  // (a part without rows)
+    l += x.y * fast_exp2(x.x - m);
+    const float f = fast_exp2(x.z - n);
+    o.x += f * y.x;
+    o.y += f * y.y;
+    o.z += f * y.z;
+    o.w += f * y.w;
+  }
+};
+// CTA c's part of a unit lies in slot 2c when the unit began before c, in 2c + 1 when it began in c.
+__device__ __forceinline__ int64_t part_slot(int c0, int j) { return 2 * (int64_t)(c0 + j) + (j == 0); }
+template <int D, int N>
+__device__ __forceinline__ Joined join_parts(const PdArgs& a, int c0, int parts, int hh, int d, int first, int step) {
+  Joined r = {-INFINITY, 0.f, -INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int j0 = first; j0 < parts; j0 += step * N) {
+    float4 x[N], y[N];
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+      const int64_t j = part_slot(c0, min(j0 + f * step, parts - 1)) * a.group + hh;
+      x[f] = a.part_ml[j];
+      y[f] = *reinterpret_cast<const float4*>(a.part_o + j * D + d);
+    }
+    float m1 = r.m, n1 = r.n;
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+      if (j0 + f * step >= parts) x[f].x = x[f].z = -INFINITY;
+      m1 = fmaxf(m1, x[f].x);
+      n1 = fmaxf(n1, x[f].z);
+    }
+    r.rescale(m1, n1);
+#pragma unroll
+    for (int f = 0; f < N; ++f) r.add(x[f], y[f]);
+  }
+  return r;
+}
+template <int D>
+__device__ __forceinline__ void write_joined(const PdArgs& a, const Joined& r, int unit, int hh, int d, float undo) {
+  const float f = r.l == 0.f ? 0.f : undo * fast_exp2(r.n - r.m) / r.l;
+  const __nv_bfloat162 x[2] = {__floats2bfloat162_rn(r.o.x * f, r.o.y * f), __floats2bfloat162_rn(r.o.z * f, r.o.w * f)};
+  const int64_t head = (int64_t)unit * a.group + hh;  // (s h_kv + h) g + hh = s h_q + h g + hh
+  *reinterpret_cast<uint2*>(a.out + head * D + d) = *reinterpret_cast<const uint2*>(x);
+  if (d == 0 && a.lse) a.lse[head] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * 0.69314718055994531f;
+}
+
+// After the attention.  Joins the parts of the units that several CTAs shared.
+// Of up to kPfMany parts: a unit to a CTA, a thread to all parts of its four
+// columns, one round trip or two.  Of more (few units, then): a query head to a
+// CTA, whose threads also share the parts (one sequence of 8,192 rows, 76 parts
+// to a KV head: 11.1 us for the step, 18.1 with a thread to all parts; 48
+// sequences of 2,000: 30 us, 35 with a head to a CTA).
+// MASS: also turns the stored logits into weights and adds them to the rows'
+// mass: a warp takes a run of tiles, a lane two rows of each; it forms its unit's
+// log-sum-exps from the parts itself, which costs less than a third launch that
+// waits for the join (16 x 16k: 103 us, and 107 with that launch).
 constexpr int kPfThreads = 256;
+constexpr int kPfMany = 16;
+constexpr int kPfHeads = 16;  // heads of units in many parts that one CTA looks at
 template <int D, bool MASS>
 __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(const __grid_constant__ PdArgs a,
                                                                                 float undo) {
+  constexpr int kCols = D / 4, kGroups = kPfThreads / kCols;
+  __shared__ float4 part_o[kGroups][kCols];
+  __shared__ float3 part_ml[kGroups];
   pdl_trigger();
   pdl_wait();
   const Pages& p = a.pages;
   const int tid = threadIdx.x, lane = tid & 31, g = a.group;
-  const int units = p.num_seqs * p.h_kv;
-  auto slot_of = [](int c0, int j) { return 2 * (int64_t)(c0 + j) + (j == 0); };
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int2 un = a.unit[u];  // its first CTA, its parts
-    if (un.y < 2) continue;
-    const int64_t head0 = (int64_t)u * g;  // (s h_kv + h) g = s h_q + h g
-    for (int c = tid; c < g * (D / 4); c += kPfThreads) {
-      const int hh = c / (D / 4), d = c % (D / 4) * 4;
-      constexpr int kFlight = MASS ? 4 : 8;  // parts whose loads are in flight
-      float m = -INFINITY, n = -INFINITY, l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j0 = 0; j0 < un.y; j0 += kFlight) {
-        float4 x[kFlight], y[kFlight];
+  // this warp's tiles of the mass: the first one's logits and place come to L1 while the join is dealt out
+  int t0 = 0, t1 = 0;
+  if (MASS) {
+    const int total = *a.tiles, warps = gridDim.x * (kPfThreads / 32), each = (total + warps - 1) / warps;
+    t0 = min((int)(blockIdx.x * (kPfThreads / 32) + (tid >> 5)) * each, total);
+    t1 = min(t0 + each, total);
+    const char* lg = reinterpret_cast<const char*>(a.logits + (int64_t)t0 * g * kPdRows);
+    if (t0 < t1 && lane < 2 * g) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(lg + 128 * lane));
+    if (t0 < t1 && lane == 0) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(a.info + t0));
+  }
+  // the unit that begins in CTA c = blockIdx.x, if it is cut; and heads of units in many parts, dealt out apart
+  // (every warp finds out by itself: nothing to wait for but the loads)
+  const int2 cut = blockIdx.x < (unsigned)a.ctas ? a.cut[blockIdx.x] : make_int2(-1, 0);
+  const uint32_t my_head = blockIdx.x + (uint32_t)lane * gridDim.x;
+  const bool heavy = lane < kPfHeads && my_head < (uint32_t)(a.ctas * g) && a.cut[my_head / g].y > kPfMany;
+  uint32_t heads = __ballot_sync(0xffffffffu, heavy);
+  if (cut.y > 1 && cut.y <= kPfMany) {
+    for (int c = tid; c < g * kCols; c += kPfThreads) {
+      const int hh = c / kCols, d = c % kCols * 4;
+      write_joined<D>(a, join_parts<D, MASS ? 4 : 8>(a, blockIdx.x, cut.y, hh, d, 0, 1), cut.x, hh, d, undo);
+    }
+  }
+  const int col = tid % kCols, grp = tid / kCols;
+  for (; heads; heads &= heads - 1) {
+    const uint32_t i = blockIdx.x + (uint32_t)(__ffs(heads) - 1) * gridDim.x;
+    const int c0 = (int)(i / g), hh = (int)(i % g);
+    const int2 t = a.cut[c0];
+    const Joined r = join_parts<D, 4>(a, c0, t.y, hh, 4 * col, grp, kGroups);
+    __syncthreads();  // the last head's parts are read
+    part_o[grp][col] = r.o;
+    if (col == 0) part_ml[grp] = make_float3(r.m, r.l, r.n);
+    __syncthreads();
+    if (grp == 0) {
+      Joined all = {-INFINITY, 0.f, -INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-          const int64_t j = slot_of(un.x, min(j0 + f, un.y - 1)) * g + hh;
-          x[f] = a.part_ml[j];
-          y[f] = *reinterpret_cast<const float4*>(a.part_o + j * D + d);
-        }
-        float m1 = m, n1 = n;
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-          if (j0 + f >= un.y) x[f].x = x[f].z = -INFINITY;  // (a part without rows has them so)
-          m1 = fmaxf(m1, x[f].x);
-          n1 = fmaxf(n1, x[f].z);
-        }
-        if (m1 == -INFINITY) continue;
-        l *= fast_exp2(m - m1);
-        float k = fast_exp2(n - n1);
-        acc.x *= k, acc.y *= k, acc.z *= k, acc.w *= k;
-#pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-          if (x[f].x == -INFINITY) continue;
-          l += x[f].y * fast_exp2(x[f].x - m1);
-          k = fast_exp2(x[f].z - n1);
-          acc.x += k * y[f].x;
-          acc.y += k * y[f].y;
-          acc.z += k * y[f].z;
-          acc.w += k * y[f].w;
-        }
-        m = m1;
-        n = n1;
+      for (int q = 0; q < kGroups; ++q) {
+        all.m = fmaxf(all.m, part_ml[q].x);
+        all.n = fmaxf(all.n, part_ml[q].z);
       }
-      const float f = l == 0.f ? 0.f : undo * fast_exp2(n - m) / l;
-      __nv_bfloat162 x[2] = {__floats2bfloat162_rn(acc.x * f, acc.y * f), __floats2bfloat162_rn(acc.z * f, acc.w * f)};
-      *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
-      if (d == 0 && a.lse) a.lse[head0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q)
+        all.add(make_float4(part_ml[q].x, part_ml[q].y, part_ml[q].z, 0.f), part_o[q][col]);
+      write_joined<D>(a, all, t.x, hh, 4 * col, undo);
     }
   }
   if (!MASS) return;
-  const int total = *a.tiles, warps = gridDim.x * (kPfThreads / 32);
-  const int each = (total + warps - 1) / warps, w = blockIdx.x * (kPfThreads / 32) + (tid >> 5);
-  const int t1 = min((w + 1) * each, total);
   int now = -1;
   float lse = INFINITY;  // lane hh: of query head hh of unit `now`
-  for (int t = w * each; t < t1; ++t) {
+  for (int t = t0; t < t1; ++t) {
     // (the logits' place goes by the tile alone: they load while the rest is looked up)
     const float* lg = a.logits + (int64_t)t * g * kPdRows + 2 * lane;
     float2 v[8];
@@ -822,7 +885,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
           float2 ml[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f)
-            ml[f] = *reinterpret_cast<const float2*>(a.part_ml + slot_of(un.x, min(j0 + f * subs, un.y - 1)) * g + hh);
+            ml[f] = *reinterpret_cast<const float2*>(a.part_ml + part_slot(un.x, min(j0 + f * subs, un.y - 1)) * g + hh);
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
             if (j0 + f * subs >= un.y || ml[f].x == -INFINITY) continue;
@@ -868,7 +931,7 @@ struct PdPlan {
   bool q8;
   int d, g, grid, sms;
   int64_t tiles;  // bound of the tile list
-  size_t lse_off, ml_off, o_off, info_off, lg_off, total;
+  size_t unit_off, lse_off, ml_off, o_off, info_off, lg_off, total;
 };
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -893,7 +956,8 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
   if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
   pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)ctas_per_sm(pl.q8, pl.g) * pl.sms, pl.tiles));
-  pl.lse_off = kPdHeader + up256(sizeof(int2) * (size_t)units);
+  pl.unit_off = kPdHeader + up256(sizeof(int2) * (size_t)pl.grid);
+  pl.lse_off = pl.unit_off + up256(sizeof(int2) * (size_t)units);
   pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
   pl.o_off = pl.ml_off + up256(sizeof(float4) * 2 * (size_t)pl.grid * pl.g);
   pl.info_off = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.g * pl.d);
@@ -949,9 +1013,11 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8, HB>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  const int64_t units = (int64_t)pl.pages.num_seqs * pl.pages.h_kv;
-  const int64_t work = a.mass_out ? std::max(units, (pl.tiles + kPfThreads / 32 - 1) / (kPfThreads / 32)) : units;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(work, (a.mass_out ? 4LL : 3LL) * pl.sms));
+  // As many CTAs as the attention has (a cut unit begins in one of them; so each looks at one unit and
+  // g heads), or with the mass as many as the SMs hold and its tiles need
+  static_assert(kPfHeads >= kPdGroup, "g heads for each CTA of the attention");
+  cfg.gridDim = dim3((unsigned)std::max<int64_t>(
+      pl.grid, a.mass_out ? std::min<int64_t>((pl.tiles + kPfThreads / 32 - 1) / (kPfThreads / 32), 4LL * pl.sms) : 0));
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = 0;
   const float undo = Q8 ? 1.f / kP16 : 1.f;
@@ -996,7 +1062,8 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   a.mass_out = p->mass_out;
   a.error = reinterpret_cast<int32_t*>(w);
   a.tiles = reinterpret_cast<int32_t*>(w + 64);
-  a.unit = reinterpret_cast<int2*>(w + kPdHeader);
+  a.cut = reinterpret_cast<int2*>(w + kPdHeader);
+  a.unit = reinterpret_cast<int2*>(w + pl.unit_off);
   a.lse2 = reinterpret_cast<float*>(w + pl.lse_off);
   a.part_ml = reinterpret_cast<float4*>(w + pl.ml_off);
   a.part_o = reinterpret_cast<float*>(w + pl.o_off);
@@ -1005,6 +1072,7 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   a.total_rows = p->total_rows;
   a.h_q = p->h_q;
   a.group = pl.g;
+  a.ctas = pl.grid;
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pl.q8) return pl.d == 128 ? launch_pd<128, true>(pl, a, s) : launch_pd<64, true>(pl, a, s);
