@@ -305,27 +305,36 @@ __global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRo
   if (a.has_pages && last > a.h_q) {
     const int len = a.pages.lens[s], i = len - back;
     if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
-      x.page = a.pages.table[s * a.pages.table_stride + i / a.pages.page_rows];
-      x.row = i % a.pages.page_rows;
+      const int nth = a.pages.max_rows < (1 << 24) ? page_of(a.pages, i, x.row) : i / a.pages.page_rows;
+      x.row = i - nth * a.pages.page_rows;
+      x.page = a.pages.table[s * a.pages.table_stride + nth];
       if (!page_ok(a.pages, x.page)) x.page = -1;
     }
     if (x.page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
   }
 
   // ---- its angles
+  // the lanes of the warp's other rows need the same ones: each forms its share, and they are exchanged
+  constexpr int kMine = 4 * kLanes / 32;
+  const int grp = lane / kLanes;
+  float sn[kMine], cs[kMine];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x.cs[e] = 1.f, x.sn[e] = 0.f;
-  if (x.turned && first < a.h_q + a.h_kv) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 4 * l + e;
+  for (int q = 0; q < kMine; ++q) {
+    sn[q] = 0.f, cs[q] = 1.f;
+    if (x.turned && first < a.h_q + a.h_kv) {
+      const int i = 4 * l + grp * kMine + q;
       int pos = x.order;
       if (a.positions) {
         const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
         pos = a.positions[axis * a.num_tokens + t];
       }
-      turn(pos, a.turns[i], x.sn[e], x.cs[e]);
+      turn(pos, a.turns[i], sn[q], cs[q]);
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x.sn[e] = __shfl_sync(0xffffffffu, sn[e % kMine], (e / kMine) * kLanes + l);
+    x.cs[e] = __shfl_sync(0xffffffffu, cs[e % kMine], (e / kMine) * kLanes + l);
   }
   if (first < q_end) rows_of_token<D, Q8, INTER, 0>(a, x, t, first, q_end, lane, r);
   if (max(first, a.h_q) < k_end) {
@@ -426,11 +435,12 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   a.sec1 = p->section1;
   a.has_pages = p->pages != nullptr;
   a.eps = p->eps;
-  // A warp takes a whole token where that makes enough warps for the GPU (16 to an
-  // SM); with fewer tokens it takes as few rows as it has at once
+  // A warp takes a whole token where that makes enough warps for the GPU (32 to an
+  // SM); with fewer tokens fewer of a token's rows (1,000 tokens of 28 + 4 heads: 7.6 us, and
+  // 9.1 with 16 warps to an SM or with 64)
   const int sms = device_sms();
   const int at_once = p->head_dim == 128 ? 2 : 4;
-  const int64_t want = std::max<int64_t>(1, 16LL * sms / p->num_tokens);
+  const int64_t want = std::max<int64_t>(1, 32LL * sms / p->num_tokens);
   a.per = (int)std::max<int64_t>(at_once, (a.heads + want - 1) / want);
   a.per = (a.per + at_once - 1) / at_once * at_once;
   a.shares = (a.heads + a.per - 1) / a.per;
