@@ -160,3 +160,57 @@ def test_calls_on_a_side_stream_without_a_workspace(A):
     want, new = expect(st, cache, [100, 20], None, 0, 0)
     assert A.evict(A.EvictProblem(cache, keep, out), stream=s).tolist() == new
     P.assert_same_state(want, P.state(cache))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_captured_step_equals_the_eager_one(A, int8):
+    # append, attend with mass and evict as one graph on a side stream, replayed with new projections and lengths,
+    # against the same calls made one by one on a copy of the cache: the same bits
+    S, h_q, h_kv, d, page_rows = 5, 10, 2, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(60)
+    qkv = torch.randn((S, (h_q + 2 * h_kv) * d), generator=g, device="cuda").to(torch.bfloat16)
+    f = 1e4 ** (-np.arange(0, d, 2) / d)
+    turns = A.rotation_table(torch.tensor(f)).cuda()
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+
+    def world():
+        cache = P.build(A, [300, 41, 17, 90, 64], h_kv, d, page_rows, seed=61, int8=int8)
+        w = dict(cache=cache, qkv=qkv.clone(), seen=t([400, 41, 20, 95, 64]), keep=t([250, 50, 16, 88, 63]),
+                 out=t([0] * S))
+        q = w["qkv"][:, :h_q * d].view(S, h_q, d)
+        k = w["qkv"][:, h_q * d:(h_q + h_kv) * d].view(S, h_kv, d)
+        v = w["qkv"][:, (h_q + h_kv) * d:].view(S, h_kv, d)
+        w["rot"] = A.RotateProblem(q, k, v, cache=cache, cu_tokens=cu, seen=w["seen"], turns=turns)
+        w["dec"] = A.PagedDecodeProblem(w["rot"].q_out, cache, lse=True, accumulate=True)
+        w["ev"] = A.EvictProblem(cache, w["keep"], w["out"], seen=w["seen"], sink=1, recent=4)
+        w["ws_d"], w["ws_e"], w["st"] = w["dec"].new_workspace(), w["ev"].new_workspace(), t([0])
+        return w
+
+    def step(w):
+        A.aircache_rotate(w["rot"], w["st"])
+        A.aircache_paged_decode(w["dec"], w["ws_d"])
+        A.aircache_evict(w["ev"], w["ws_e"])
+
+    a, b = world(), world()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(b)
+    for i in range(3):
+        lens = [300 - 9 * i, 41 + i, 17, 90 - 30 * i, 64]
+        new = torch.randn(qkv.shape, generator=g, device="cuda").to(torch.bfloat16)
+        for w in (a, b):
+            w["qkv"].copy_(new)
+            w["cache"].lens.copy_(t(lens))
+        torch.cuda.synchronize()
+        step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        P.assert_same_state(P.state(a["cache"]), P.state(b["cache"]))
+        for x, y in ((a["dec"].out, b["dec"].out), (a["dec"].lse, b["dec"].lse), (a["out"], b["out"]),
+                     (a["rot"].q_out, b["rot"].q_out)):
+            assert np.array_equal(P.bits(x), P.bits(y))
+        for w in (a, b):
+            assert [A.aircache_get_error(w[n]) for n in ("st", "ws_d", "ws_e")] == [A.OK] * 3
