@@ -619,8 +619,8 @@ typedef struct aircache_pages {
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; head_dim
  * 64 or 128; at least one of q, k; q_out with q; k_out or pages with k; v
  * exactly with pages; rotary_dim 0 or a multiple of 16 up to head_dim, turns
- * when it is not 0; axes 1 or 3, sections >= 0 with a sum of rotary_dim/2 when
- * axes is 3; eps >= 0; seen when pages has order or positions is NULL (with
+ * when it is not 0; axes 1 or 3, sections >= 0 with a sum of at most rotary_dim/2
+ * when axes is 3; eps >= 0; seen when pages has order or positions is NULL (with
  * rotary_dim > 0); pointers 16-byte aligned, strides multiples of 8 elements.
  * A token whose row or page is out of bounds sets AIRCACHE_ERR_DEVICE_BOUNDS
  * in *status (optional device int32, not cleared by the call) and is not
@@ -669,7 +669,10 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  *   lse[s][h] = log sum_j exp(scale * q[s][h] . k_j)        (optional)
  *   mass_out[row j][KV head] = mass[..] + the sum of w_j over the KV head's
  *   query heads                                              (optional)
- * A sequence without rows gets out = 0 and lse = -inf.  out is bf16, lse fp32
+ * A sequence without rows gets out = 0 and lse = -inf, and so does a query all
+ * of whose logits lie below fp32's range (single ones weigh nothing); a NaN, an
+ * infinite key or value or a logit above the range makes what it meets NaN or
+ * infinite.  out is bf16, lse fp32
  * dense [num_seqs][h_q]; mass_out is pages->mass itself (in place) or another
  * array of its shape, where only the slots of attended rows are written.
  *

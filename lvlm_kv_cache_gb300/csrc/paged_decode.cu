@@ -45,6 +45,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -431,10 +432,11 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
 #pragma unroll
       for (int b = 0; b < HB; ++b) o[t][b][0] = o[t][b][1] = o[t][b][2] = o[t][b][3] = 0.f;
     // of head hA + 8b: the sum's reference and this lane's part of the sum; O's reference (the
-    // same, but for int8 rows)
+    // same, but for int8 rows).  Before any row: fp32's lowest, not -inf, against which a
+    // logit under fp32's range would weigh NaN where it weighs nothing
     float m[HB], l[HB], n[HB];
 #pragma unroll
-    for (int b = 0; b < HB; ++b) m[b] = -INFINITY, l[b] = 0.f, n[b] = Q8 ? -1e30f : -INFINITY;
+    for (int b = 0; b < HB; ++b) m[b] = n[b] = -FLT_MAX, l[b] = 0.f;
     static_assert(kP16 == 16384.f, "2^14, as the weights' exponent takes it");
     constexpr float kSlack = 8.f, kSlack16 = 1.f;  // (f16 weights carry 2^14: 2^15 is the most they may reach)
 
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           for (int b = 0; b < HB; ++b) {
             float x = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], 1));
             x = fmaxf(m[b], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)));
-            float f = fast_exp2(m[b] - x);  // (from -inf: 0)
+            float f = fast_exp2(m[b] - x);
             l[b] *= f;
             m[b] = x;
             if (Q8) {
@@ -628,8 +630,6 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       x += __shfl_xor_sync(0xffffffffu, x, 2);
       if (cq == 0) {
         float* w = mlw + (warp * kPdGroup + hA + 8 * b) * 3;
-        // (logits that are all NaN leave no reference: any other than "no rows" passes them on)
-        if (x != x && m[b] == -INFINITY) m[b] = 0.f;
         w[0] = m[b], w[1] = x, w[2] = Q8 ? n[b] : m[b];
       }
     }
@@ -643,10 +643,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         n = fmaxf(n, mlw[(w * kPdGroup + hh) * 3 + 2]);
       }
 #pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) {
-        const float x = mlw[(w * kPdGroup + hh) * 3];
-        if (x != -INFINITY) l += mlw[(w * kPdGroup + hh) * 3 + 1] * fast_exp2(x - m);
-      }
+      for (int w = 0; w < kPdWarps; ++w)
+        l += mlw[(w * kPdGroup + hh) * 3 + 1] * fast_exp2(mlw[(w * kPdGroup + hh) * 3] - m);
     };
     // head hh's column d lies at d ^ 8 (hh / 2 mod 4): a warp's stores then fall into 32 banks
     auto place = [](int hh, int d) { return hh * D + (d ^ ((hh >> 1 & 3) << 3)); };
@@ -659,8 +657,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           const int hh = 8 * b + 2 * cq + e;
           float mm, ll, nn;
           joined(hh, mm, ll, nn);
-          const float x = mlw[(warp * kPdGroup + hh) * 3 + 2];
-          c[b][e] = x == -INFINITY ? 0.f : fast_exp2(x - nn);
+          c[b][e] = fast_exp2(mlw[(warp * kPdGroup + hh) * 3 + 2] - nn);
         }
       auto put = [&](auto q, bool first) {
         constexpr int quarter = decltype(q)::value;
@@ -744,7 +741,7 @@ struct Joined {
     n = n1;
   }
   __device__ __forceinline__ void add(const float4& x, const float4& y) {  // (m, l, n) and O, under the references
-    if (x.x == -INFINITY) return;  // (a part without rows)
+    if (x.x == -INFINITY) return;  // (a place without a part)
     l += x.y * fast_exp2(x.x - m);
     const float f = fast_exp2(x.z - n);
     o.x += f * y.x;
@@ -888,7 +885,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
             ml[f] = *reinterpret_cast<const float2*>(a.part_ml + part_slot(un.x, min(j0 + f * subs, un.y - 1)) * g + hh);
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            if (j0 + f * subs >= un.y || ml[f].x == -INFINITY) continue;
+            if (j0 + f * subs >= un.y) continue;
             const float m1 = fmaxf(m, ml[f].x);
             l = l * fast_exp2(m - m1) + ml[f].y * fast_exp2(ml[f].x - m1);
             m = m1;

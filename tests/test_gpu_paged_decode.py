@@ -344,3 +344,48 @@ def test_nan_in_a_row_that_counts_is_not_hidden(A, int8):
     p1 = A.PagedDecodeProblem(q1, one, lse=True)
     A.paged_decode(p1)
     assert bool(torch.isnan(p1.out[0, 2]).all())
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_logits_below_fp32_weigh_nothing(A, int8):
+    # finite keys whose product with one of the queries is under fp32's range, in all of a warp's first rows, in the
+    # last ones, and in every row of the second sequence; the group's other queries do not see that element
+    cache = P.build(A, [600, 20], 1, 128, 16, seed=22, int8=int8)
+    q = queries(2, 6, 128, 22)
+    q[:, :, 7] = 0.0
+    q[:, 2] = 0.0
+    q[:, 2, 7] = 100.0
+    lowest = torch.cat([torch.arange(16), torch.arange(64, 97), torch.arange(560, 600)])
+    for s, rows in ((0, lowest), (1, torch.arange(20))):
+        pg, r = cache.table[s, (rows // 16).cuda()].long(), (rows % 16).cuda()
+        cache.k[pg, r] = 0
+        cache.k[pg, r, 0, 7] = -127 if int8 else -3e38
+        if int8:
+            cache.k_scale[pg, 0, r] = 1e36
+    before = P.host(cache)
+    prob = A.PagedDecodeProblem(q, cache, lse=True, accumulate=True)
+    A.paged_decode(prob)
+    # (the oracle's weights of those rows are 0: exp of less than -1e38)
+    out, lse, w, _, spread = O.decode(q.double().cpu().numpy(), before, 128 ** -0.5)
+    seen = np.setdiff1d(np.arange(600), lowest.numpy())
+    pg, r = (x[seen] for x in O.slots(before, 0))
+    k = before["k"][pg, r, 0].astype(np.float64) * (before["k_scale"][pg, 0, r][:, None] if int8 else 1)
+    size = np.abs(k) @ np.abs(q[0].double().cpu().numpy()).T * 128 ** -0.5
+    dx = 128 * 2.0 ** -24 * size.max(0)
+    tol = ((2.0 ** -11 if int8 else 2.0 ** -16) + 2 * dx[:, None] + 2.0 ** -18) * spread[0] + HALF * np.abs(out[0])
+    if int8:
+        tol += 600 * 127 * 2.0 ** -39 * before["v_scale"].max()
+    assert np.all(np.abs(prob.out[0].double().cpu().numpy() - out[0]) <= tol)
+    assert np.all(np.abs(prob.lse[0].double().cpu().numpy() - lse[0]) <= dx + 2.0 ** -20 * (1 + np.abs(lse[0])))
+    # no row of the second sequence has a logit in range: none weighs anything for that query
+    assert bool((prob.out[1, 2] == 0).all()) and bool(torch.isneginf(prob.lse[1, 2]))
+    assert bool(torch.isfinite(prob.out[1]).all()) and bool(torch.isfinite(prob.lse[1, [0, 1, 3, 4, 5]]).all())
+    for s, weight in ((0, w[0][0]), (1, None)):
+        pg, r = O.slots(before, s)
+        got = prob.mass_out.double().cpu().numpy()[pg, 0, r] - before["mass"][pg, 0, r]
+        if weight is None:  # (five queries that see equal keys)
+            weight = np.full(20, 5 / 20)
+            rel = 2.0 ** -20
+        else:
+            rel = 2 * dx.max() + 2.0 ** -20
+        assert np.all(np.abs(got - weight) <= rel * weight + 2.0 ** -23 * (1 + weight + 6))
