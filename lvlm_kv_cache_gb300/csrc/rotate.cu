@@ -13,8 +13,8 @@
 // the slot in the cache is looked up once.  Both elements of a pair lie in one
 // lane (half style: four elements and the four half a rotation further), so a
 // row costs no shuffles but the norm's.  With few tokens a token's heads go to
-// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 3.3 us; 15,541 of them, the
-// keys also dense, in 57 us (303 MB read and written, 5.3 TB/s).
+// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 3.1 us; 15,541 of them, the
+// keys also dense, in 54 us (303 MB read and written, 5.6 TB/s).
 //
 // The angle: position * (hi + lo) turns is reduced before it is rounded.  The
 // position splits into two parts of at most 20 bits (exact in fp32), each
@@ -30,13 +30,15 @@
 namespace aircache {
 namespace {
 
-constexpr int kRotWarps = 4;
-
+// A CTA is one warp: the next token starts as soon as one is done (15,541 tokens: 53.7 us, and 56.9
+// with four warps to a CTA, 56.4 with two).
 // NB: rows a lane group works on at a time, while as many load.  Two, with 32 warps
-// to an SM, where there are tokens enough (15,541 tokens of 28 + 4 heads of 128: 58 us, and
-// 64 with four); four, with 24 warps, where a warp has to keep its own loads in flight
-// (3,447 tokens of 32 + 32 heads of 64: 17.7 us, and 20.7 with two).
-constexpr int kRotFew = 24;  // warps to an SM
+// to an SM (15,541 tokens of 28 + 4 heads of 128: 53.7 us, and 61.3 with four); four, with 24 warps,
+// where whole tokens do not fill those, so that a warp has to keep more loads of its own in flight
+// (3,447 tokens of 32 + 32 heads of 64: 17.1 us, and 19.2 with two).
+constexpr int kRotMany = 32, kRotFew = 24;  // warps to an SM
+// (The bounds on the kernels' registers: as 32 CTAs of 32 threads for NB = 2 and, though it is launched
+// with 32 threads, as 6 of 128 for NB = 4; the other way round 55.6 and 18.2 us.)
 
 struct RotArgs {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -256,15 +258,14 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
 }
 
 template <int D, bool Q8, bool INTER, int NB>
-__global__ void __launch_bounds__(kRotWarps * 32, (NB == 2 ? 32 : kRotFew) / kRotWarps)
+__global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotFew / 4)
     rotate_kernel(const __grid_constant__ RotArgs a) {
   constexpr int kLanes = D / 8;
-  const int lane = threadIdx.x & 31, l = lane % kLanes;
-  const int64_t w = (int64_t)blockIdx.x * kRotWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x, l = lane % kLanes;
+  const int64_t w = blockIdx.x;
   const int64_t t = w / a.shares;  // neighbouring warps share a token's heads
   pdl_trigger();
   pdl_wait();
-  if (t >= a.num_tokens) return;
   const int first = (int)(w % a.shares) * a.per, last = min(first + a.per, a.heads);
   const int q_end = min(last, a.h_q), k_end = min(last, a.h_q + a.h_kv);
 
@@ -435,19 +436,30 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   a.sec1 = p->section1;
   a.has_pages = p->pages != nullptr;
   a.eps = p->eps;
-  // A warp takes a whole token where that makes enough warps for the GPU (32 to an
-  // SM); with fewer tokens fewer of a token's rows (1,000 tokens of 28 + 4 heads: 7.6 us, and
-  // 9.1 with 16 warps to an SM or with 64)
+  // How many warps share a token's heads.  A warp's time is about that of its rows' steps and three
+  // more (the token's place and angles), the SMs hold kRotMany warps at once, and starting
+  // them takes a step for every ten to an SM.  (5,000 tokens of 32 + 32 heads of 64: 29 us with one
+  // warp to a token, 26 with the two that this gives, 24 with three; 3,000 of 32 + 32 heads of
+  // 128: 34, and 28 with its three; 200 of 28 + 4: 7.0, and 4.4 with its nine)
   const int sms = device_sms();
   const int at_once = p->head_dim == 128 ? 2 : 4;
-  const int64_t want = std::max<int64_t>(1, 32LL * sms / p->num_tokens);
-  a.per = (int)std::max<int64_t>(at_once, (a.heads + want - 1) / want);
-  a.per = (a.per + at_once - 1) / at_once * at_once;
+  const int steps = (a.heads + at_once - 1) / at_once;
+  const int64_t slots = (int64_t)kRotMany * sms;
+  int64_t least = INT64_MAX;
+  int best = steps;
+  const int shares_max = p->num_tokens >= 8 * slots ? 1 : std::min(steps, 17);
+  for (int i = 1; i <= shares_max; ++i) {
+    const int n = i == 17 ? 1 : (steps + i - 1) / i;  // (16 shares at most, or a step to each)
+    const int64_t warps = p->num_tokens * ((steps + n - 1) / n);
+    const int64_t cost = 10LL * sms * ((warps + slots - 1) / slots) * (n + 3) + warps;
+    if (cost < least) least = cost, best = n;
+  }
+  a.per = best * at_once;
   a.shares = (a.heads + a.per - 1) / a.per;
-  const dim3 grid((unsigned)((p->num_tokens * a.shares + kRotWarps - 1) / kRotWarps));
-  const dim3 block(kRotWarps * 32);
+  const int64_t warps = p->num_tokens * a.shares;
+  const bool few = a.shares == 1 && p->num_tokens <= (int64_t)kRotFew * sms;
+  const dim3 grid((unsigned)warps), block(32);  // (many tokens have one share: 2^31 - 1 at most)
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool few = p->num_tokens * a.shares <= (int64_t)kRotFew * sms;
   void (*kernel)(RotArgs) = p->head_dim == 128 ? rotate_pick<128>(q8, p->interleaved != 0, few)
                                                : rotate_pick<64>(q8, p->interleaved != 0, few);
   return launch_pdl(kernel, grid, block, 0, s, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
