@@ -63,7 +63,7 @@ struct EvShared {
   Before sum;
   uint32_t scan[kEvWarps], scan2[kEvWarps], scan3[kEvWarps];
   uint32_t least, most, safe, bad;  // this CTA's least and largest key, protected rows, bad pages
-  uint32_t bin, above;
+  uint32_t bin, above, in_bin;
   uint32_t near[kEvWarps][kNear];  // the keys in the part of the range that the first histogram left
 };
 
@@ -276,10 +276,17 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
       if (tid < kBins && above < need && above + c >= need) {
         sh.bin = kBins - 1 - tid;
         sh.above = above;
+        sh.in_bin = c;
       }
       __syncthreads();
       prefix += sh.bin << shift;
       need -= sh.above;
+      // all of the part's rows stay: it need not be divided further, and no row is at the threshold
+      if (sh.in_bin == need) {
+        prefix -= 1;
+        need = 0;
+        break;
+      }
     }
   }
 
