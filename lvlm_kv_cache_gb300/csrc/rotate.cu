@@ -13,8 +13,8 @@
 // the slot in the cache is looked up once.  Both elements of a pair lie in one
 // lane (half style: four elements and the four half a rotation further), so a
 // row costs no shuffles but the norm's.  With few tokens a token's heads go to
-// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 3.1 us; 15,541 of them, the
-// keys also dense, in 54 us (303 MB read and written, 5.6 TB/s).
+// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 2.7 us; 15,541 of them, the
+// keys also dense, in 52 us (303 MB read and written, 5.8 TB/s).
 //
 // The angle: position * (hi + lo) turns is reduced before it is rounded.  The
 // position splits into two parts of at most 20 bits (exact in fp32), each
@@ -290,8 +290,27 @@ __global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotF
   else
     load_rows<D, false>(r, from, a.src_head[kind], first - kind0, from_end, x.e0, x.e1, lane);
 
-  // ---- the token's sequence, order and slot
-  int s = 0, back = 0;
+  // ---- the token's positions, sequence, order and slot.  What is loaded here is used as late as
+  // may be, the place in the cache behind the queries (15,541 tokens: 53.5 us with each lookup waited for)
+  constexpr int kMine = 4 * kLanes / 32;
+  const int grp = lane / kLanes;
+  const bool turns = x.turned && first < a.h_q + a.h_kv;
+  float2 turn_of[kMine];
+  int pos[kMine];
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    const int i = 4 * l + grp * kMine + q;
+    turn_of[q] = make_float2(0.f, 0.f);
+    pos[q] = 0;
+    if (turns) {
+      turn_of[q] = a.turns[i];
+      if (a.positions) {
+        const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
+        pos[q] = a.positions[axis * a.num_tokens + t];
+      }
+    }
+  }
+  int s = 0, back = 0, len = 0;
   x.order = 0;
   if (a.cu_tokens) {
     if (w == 0 && lane == 0 && a.status && a.cu_tokens[a.num_seqs] > a.num_tokens)
@@ -300,44 +319,38 @@ __global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotF
     if (s < 0 || s >= a.num_seqs) return;  // padding
     back = a.cu_tokens[s + 1] - (int)t;
     if (a.seen) x.order = a.seen[s] - back;
-  }
-  x.page = -1;
-  x.row = 0;
-  if (a.has_pages && last > a.h_q) {
-    const int len = a.pages.lens[s], i = len - back;
-    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
-      const int nth = a.pages.max_rows < (1 << 24) ? page_of(a.pages, i, x.row) : i / a.pages.page_rows;
-      x.row = i - nth * a.pages.page_rows;
-      x.page = a.pages.table[s * a.pages.table_stride + nth];
-      if (!page_ok(a.pages, x.page)) x.page = -1;
-    }
-    if (x.page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
+    if (a.has_pages) len = a.pages.lens[s];
   }
 
   // ---- its angles
   // the lanes of the warp's other rows need the same ones: each forms its share, and they are exchanged
-  constexpr int kMine = 4 * kLanes / 32;
-  const int grp = lane / kLanes;
   float sn[kMine], cs[kMine];
 #pragma unroll
   for (int q = 0; q < kMine; ++q) {
     sn[q] = 0.f, cs[q] = 1.f;
-    if (x.turned && first < a.h_q + a.h_kv) {
-      const int i = 4 * l + grp * kMine + q;
-      int pos = x.order;
-      if (a.positions) {
-        const int axis = a.axes == 1 ? 0 : i < a.sec0 ? 0 : i < a.sec0 + a.sec1 ? 1 : 2;
-        pos = a.positions[axis * a.num_tokens + t];
-      }
-      turn(pos, a.turns[i], sn[q], cs[q]);
-    }
+    if (turns) turn(a.positions ? pos[q] : x.order, turn_of[q], sn[q], cs[q]);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     x.sn[e] = __shfl_sync(0xffffffffu, sn[e % kMine], (e / kMine) * kLanes + l);
     x.cs[e] = __shfl_sync(0xffffffffu, cs[e % kMine], (e / kMine) * kLanes + l);
   }
+  x.page = -1;
+  x.row = 0;
+  const bool appends = a.has_pages && last > a.h_q;
+  if (appends) {
+    const int i = len - back;
+    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
+      const int nth = a.pages.max_rows < (1 << 24) ? page_of(a.pages, i, x.row) : i / a.pages.page_rows;
+      x.row = i - nth * a.pages.page_rows;
+      x.page = a.pages.table[s * a.pages.table_stride + nth];
+    }
+  }
   if (first < q_end) rows_of_token<D, Q8, INTER, 0>(a, x, t, first, q_end, lane, r);
+  if (appends) {
+    if (!page_ok(a.pages, x.page)) x.page = -1;
+    if (x.page < 0 && lane == 0 && a.status) set_error(a.status, AIRCACHE_ERR_DEVICE_BOUNDS);
+  }
   if (max(first, a.h_q) < k_end) {
     const int from = max(first, a.h_q) - a.h_q, to = k_end - a.h_q;
     if (kind < 1) load_rows<D, INTER>(r, a.src[1] + t * a.src_tok[1], a.src_head[1], from, to, x.e0, x.e1, lane);
