@@ -107,6 +107,10 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   __syncthreads();
   pdl_wait();
 
+  // the table's row comes to L1 while the length is waited for
+  const int32_t* table = p.table + (int64_t)s * p.table_stride;
+  for (int64_t i = 32LL * tid; i * p.page_rows < min(a.max_rows, p.max_rows); i += 32 * kEvThreads)
+    asm volatile("prefetch.global.L1 [%0];\n" ::"l"(table + i));
   const int len = p.lens[s], keep = a.keep[s];
   const int32_t seen = a.recent ? a.seen[s] : 0;
   const bool sane = len >= 0 && len <= a.max_rows && len <= p.max_rows && keep >= 0 &&
@@ -116,7 +120,6 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   const bool cut = sane && n > keep;
   const int per = ((n + R - 1) / R + 15) & ~15;
   const int lo = min(rank * per, n), mine = min(per, n - lo);  // this CTA's rows
-  const int32_t* table = p.table + (int64_t)s * p.table_stride;
   const int32_t fresh = a.recent ? seen - a.recent : 0x7fffffff;  // order from which rows are recent
   const bool aged = a.sink | a.recent;
 
