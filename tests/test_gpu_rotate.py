@@ -281,3 +281,29 @@ def test_batches_without_sequences(A):
     cache = A.PagedCache(pages, pages.clone(), e(0, 3), e(0), mass=e(2, 2, 16, dt=torch.float32))
     assert A.paged_decode(A.PagedDecodeProblem(e(0, 4, 64, dt=torch.bfloat16), cache)).shape == (0, 4, 64)
     assert A.evict(A.EvictProblem(cache, e(0), e(0))).shape == (0,)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("new,d,h_q,h_kv", [((2, 1, 3), 128, 33, 2), ((9, 300, 91), 64, 40, 3), ((700, 1, 1200), 128, 28, 4),
+                                            ((2600, 7, 900), 64, 32, 32), ((3000, 60, 2500), 128, 6, 1),
+                                            ((39000, 5, 1), 64, 2, 1)])
+def test_the_split_of_the_work_changes_nothing(A, new, d, h_q, h_kv, int8):
+    # one batch against its sequences one by one: other numbers of warps to a token, the same bits
+    T, lens = sum(new), [n + 5 for n in new]
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn((T, h_q + 2 * h_kv, d), generator=g, device="cuda").to(torch.bfloat16)
+    q, k, v = x.split([h_q, h_kv, h_kv], dim=1)
+    w = (1 + 0.3 * torch.randn((2, d), generator=g, device="cuda")).to(torch.bfloat16)
+    turns = A.rotation_table(torch.tensor(freqs(d))).cuda()
+    i32 = lambda *xs: torch.tensor(xs, dtype=torch.int32, device="cuda")  # noqa: E731
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    whole, parts = (P.build(A, lens, h_kv, d, 32, seed=32, int8=int8) for _ in range(2))
+    kw = dict(turns=turns, q_weight=w[0], k_weight=w[1])
+    qo, _ = A.rotate(A.RotateProblem(q, k, v, cache=whole, cu_tokens=i32(*cu), seen=i32(*lens), **kw))
+    for s, n in enumerate(new):
+        at = slice(cu[s], cu[s + 1])
+        one = A.PagedCache(parts.k, parts.v, parts.table[s:s + 1], parts.lens[s:s + 1].clone(), k_scale=parts.k_scale,
+                           v_scale=parts.v_scale, mass=parts.mass, order=parts.order)
+        qs, _ = A.rotate(A.RotateProblem(q[at], k[at], v[at], cache=one, cu_tokens=i32(0, n), seen=i32(lens[s]), **kw))
+        assert np.array_equal(P.bits(qs), P.bits(qo[at]))
+    P.assert_same_state(P.state(whole), P.state(parts))
