@@ -680,7 +680,10 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  * of 64-row tiles of the batch's (sequence, KV head) list, whatever the lengths,
  * and a second kernel joins the parts of each (sequence, KV head), in a fixed
  * order.  With mass_out it also turns the logits, which the first then leaves in
- * the workspace, into weights.
+ * the workspace, into weights.  Where the table and total_rows allow only short
+ * sequences (some thousand rows, fewer in a large batch), a cluster of CTAs
+ * takes each (sequence, KV head) instead and the call is one kernel: give the table's
+ * real width and a close total_rows.
  *
  * total_rows bounds the sum of lens; it sizes the grid and the workspace.  A
  * larger sum sets AIRCACHE_ERR_CAPACITY and nothing is computed.  A sequence

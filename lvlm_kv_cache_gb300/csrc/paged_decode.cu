@@ -25,6 +25,11 @@
 // last one cost 8 us at the end of a 16 x 16k step, more than the launch, which
 // starts while the first kernel runs.)
 //
+// Short sequences need neither the list nor the second kernel: a cluster of one to
+// eight CTAs takes a (sequence, KV head), an equal part of its tiles each, and they
+// join their parts, form the log-sum-exps and add to the mass themselves, through
+// each other's shared memory (one of 701 rows: 7.0 us, 8.9 by the list).
+//
 // int8 rows carry a scale each.  The key's multiplies the logit.  The value's
 // joins the weight before it is rounded to f16: the weights of O are
 // exp2(x_j + log2 s_j) against their own reference, and the sum l keeps its own.
@@ -40,7 +45,7 @@
 // Measured (28 query and 4 KV heads of 128, calls back to back): 16 x 16,384
 // bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 us; 8 x 32,768 int8 rows 64 us
 // (277 MB); 32 heads of 64 over 55,113 rows 76 us (452 MB, 5.9 TB/s); one
-// sequence of 701 rows 8.9 us, of 8,192 11.1 us, of 131,072 49 us; two launches.
+// sequence of 8,192 rows 11.1 us, of 131,072 49 us; of 701, in one launch, 7.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -60,6 +65,7 @@ constexpr int kPdRows = 64;   // rows of a tile
 constexpr int kPdWarps = 4;   // consumer warps, 16 rows each
 constexpr int kPdThreads = (kPdWarps + 1) * 32;
 constexpr int kPdGroup = 16;  // query heads of a KV head, at most
+constexpr int kPdRanks = 8;     // CTAs of a cluster, at most
 constexpr int kPdHeader = 256;  // workspace: error word, then the tile count of the last call
 
 // HB: blocks of eight query heads.
@@ -73,7 +79,8 @@ struct PdCfg {
   static constexpr int kCtas = HB == 1 ? 3 : 2;               // to an SM, for the registers
   static constexpr int kScratch = 8 * HB * D * 4;             // the warps' joined O
   static constexpr int kScales = Q8 ? kStages * 2 * kPdRows * 4 : 0;
-  static constexpr int kMl = kPdWarps * kPdGroup * 3 * 4;     // (m, l, n) of each warp and head
+  static constexpr int kMl = (kPdWarps + 1) * kPdGroup * 3 * 4 + kPdGroup * 4;  // (m, l, n) of each warp and
+                                                              // head, of the CTA, and the heads' log-sum-exps
   static constexpr int kSmem = 1024 + kRing + kScratch + kScales + kMl + kStages * (8 + 8 + 4) + 448;
   static_assert(kSmem <= (Q8 && HB == 1 ? 75 : 113) * 1024, "CTAs per SM, as ctas_per_sm() says");
 };
@@ -104,7 +111,7 @@ struct PdArgs {
   TileInfo* info;    // [tiles]
   float* logits;     // [tiles][g][64], base 2
   int64_t total_rows;
-  int h_q, group, ctas;
+  int h_q, group, ctas, ranks;  // ranks: CTAs to a unit (kernels of short sequences)
   float scale_log2;
 };
 
@@ -253,7 +260,58 @@ __device__ __forceinline__ Share make_share(const PdArgs& a, ShareScratch* sc) {
   return sh;
 }
 
-template <int D, bool Q8, int HB>
+// Short sequences: `ranks` CTAs (a cluster) to a unit, with an equal part of its tiles each.
+__device__ __forceinline__ Share make_unit(const PdArgs& a, ShareScratch* sc) {
+  const Pages& p = a.pages;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int unit = blockIdx.x / a.ranks, rank = blockIdx.x % a.ranks;
+  Share sh;
+  Run& r = sh.run;
+  r.s = unit / p.h_kv;
+  r.h = unit % p.h_kv;
+  r.len = rows_of(p, r.s);
+  r.tiles = (r.len + kPdRows - 1) / kPdRows;
+  r.unit = 0;
+  sh.per = (r.tiles + a.ranks - 1) / a.ranks;
+  r.first = min(rank * sh.per, r.tiles);
+  r.count = min(sh.per, r.tiles - r.first);
+  uint32_t tiles = 0;  // of the sequences before
+  int64_t rows = 0;
+  for (int s = tid; s < p.num_seqs; s += kPdThreads) {
+    const int n = rows_of(p, s);
+    if (n != p.lens[s] && blockIdx.x == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+    rows += n;
+    if (s < r.s) tiles += (n + kPdRows - 1) / kPdRows;
+  }
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, off);
+  if (lane == 0) sc->tiles[warp] = tiles, sc->rows[warp] = rows;
+  __syncthreads();
+  int64_t all = 0;
+  tiles = 0;
+#pragma unroll
+  for (int w = 0; w < kPdThreads / 32; ++w) all += sc->rows[w], tiles += sc->tiles[w];
+  r.at = tiles * p.h_kv + r.h * r.tiles + r.first;
+  sh.lo = 0;
+  sh.hi = r.tiles > 0;
+  sh.tiles = 0;
+  if (all > a.total_rows) {
+    if (blockIdx.x == 0 && tid == 0) set_error(a.error, AIRCACHE_ERR_CAPACITY);
+    sh.tiles = -1;
+    sh.hi = 0;
+  }
+  return sh;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// SHORT: a cluster to a unit, and no second kernel.
+template <int D, bool Q8, int HB, bool SHORT>
 __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap,
                                                                   const __grid_constant__ PdArgs a) {
@@ -263,6 +321,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   float* scratch = reinterpret_cast<float*>(ring + C::kRing);               // [8 HB][D], swizzled
   float* scales = reinterpret_cast<float*>(ring + C::kRing + C::kScratch);  // [stages][K, V][64]
   float* mlw = reinterpret_cast<float*>(ring + C::kRing + C::kScratch + C::kScales);  // [4][16][3]
+  float* part = mlw + kPdWarps * kPdGroup * 3;  // [16][3]
+  float* lse2 = part + kPdGroup * 3;            // [16]
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(mlw) + C::kMl);
   uint64_t* empty = full + C::kStages;
   ShareScratch* share = reinterpret_cast<ShareScratch*>(empty + C::kStages);
@@ -284,8 +344,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   pdl_wait();
-  const Share sh = make_share(a, share);  // (its barriers publish the mbarriers too)
-  if (blockIdx.x == 0 && tid == 0) *a.tiles = max(sh.tiles, 0);
+  const Share sh = SHORT ? make_unit(a, share) : make_share(a, share);  // (its barriers publish the mbarriers too)
+  if (!SHORT && blockIdx.x == 0 && tid == 0) *a.tiles = max(sh.tiles, 0);
   Run r = sh.run;
 
   if (warp == kPdWarps) {
@@ -295,7 +355,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     int st = 0;
     uint32_t phase = 0, filled = 0;
     bool alive = true;
-    for (bool more = sh.lo < sh.hi; more && alive; more = next_run(p, r, sh.lo, sh.hi)) {
+    for (bool more = sh.lo < sh.hi; more && alive; more = !SHORT && next_run(p, r, sh.lo, sh.hi)) {
       const int32_t* table = p.table + (int64_t)r.s * p.table_stride;
       int page = -1;
       for (uint32_t i = 0; i < r.count; ++i) {
@@ -345,7 +405,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
                      (lane >= 12 ? p.v_scale : p.k_scale) + slot, 64, &full[st]);
           }
         }
-        if (a.mass_out) {
+        if (!SHORT && a.mass_out) {
           const uint32_t t = r.at + i;
           if (lane < 4) a.info[t].page[lane] = pg;
           if (lane == 4) *reinterpret_cast<int4*>(&a.info[t]) = make_int4(r.s, r.h, r.first + i, 0);
@@ -354,25 +414,30 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         if (++st == C::kStages) st = 0, phase ^= 1;
       }
     }
+    if (SHORT && sh.lo < sh.hi) {  // (the consumers' barriers are the whole cluster's)
+      __syncwarp();
+      cluster_sync_all();
+      cluster_sync_all();
+    }
     return;
   }
 
   // ---- consumers
   const int hA = lane >> 2, cq = lane & 3;  // S: heads hA and hA + 8, rows 2cq, 2cq + 1 of each eight
-  if (tid == 0) a.cut[blockIdx.x] = make_int2(-1, 0);  // (until a run says otherwise)
+  if (!SHORT && tid == 0) a.cut[blockIdx.x] = make_int2(-1, 0);  // (until a run says otherwise)
   // sequences without rows: out = 0, lse = -inf
   for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
     for (int i = tid; i < a.h_q * D / 8; i += kPdWarps * 32)
       *reinterpret_cast<uint4*>(a.out + (int64_t)s * a.h_q * D + i * 8) = make_uint4(0, 0, 0, 0);
     for (int i = tid; i < a.h_q && a.lse; i += kPdWarps * 32) a.lse[(int64_t)s * a.h_q + i] = -INFINITY;
-    for (int i = tid; i < p.h_kv; i += kPdWarps * 32) a.unit[s * p.h_kv + i] = make_int2(0, 0);
+    for (int i = tid; i < p.h_kv && !SHORT; i += kPdWarps * 32) a.unit[s * p.h_kv + i] = make_int2(0, 0);
   }
   int st = 0;
   uint32_t phase = 0;
   bool alive = true;
-  for (bool more = sh.lo < sh.hi; more; more = next_run(p, r, sh.lo, sh.hi)) {
-    if (r.count == 0) continue;
+  for (bool more = sh.lo < sh.hi; more; more = !SHORT && next_run(p, r, sh.lo, sh.hi)) {
+    if (!SHORT && r.count == 0) continue;
     // ---- the group's queries as A fragments (heads at or past g: zeros)
     uint32_t qa[D / 16][2 * HB];
 #pragma unroll
@@ -688,14 +753,95 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       const int rem = d % (D / 8);
       return scratch[place(hh, Q8 ? 16 * (rem >> 1) + d / (D / 8) + 8 * (rem & 1) : d)];
     };
+    const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
+    constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
+    if constexpr (SHORT) {
+      if (tid < g) {
+        float m, l, n;
+        joined(tid, m, l, n);
+        part[tid * 3] = m, part[tid * 3 + 1] = l, part[tid * 3 + 2] = n;
+      }
+      cluster_sync_all();
+      const int rank = blockIdx.x % a.ranks;
+      constexpr int kRanks = kPdRanks;
+      // the ranks' references and sums of head hh: the common ones
+      auto heads = [&](int hh, float m[kRanks], float l[kRanks], float n[kRanks], float& mm, float& ll, float& nn) {
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j) {
+          const uint32_t at = cluster_map(smem_u32(part + hh * 3), min(j, a.ranks - 1));
+          m[j] = ld_cluster_f32(at);
+          l[j] = ld_cluster_f32(at + 4);
+          n[j] = ld_cluster_f32(at + 8);
+        }
+        mm = nn = -FLT_MAX;
+        ll = 0.f;
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j) mm = fmaxf(mm, m[j]), nn = fmaxf(nn, n[j]);
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j)
+          if (j < a.ranks) ll += l[j] * fast_exp2(m[j] - mm);
+      };
+      // four columns to a thread, the ranks in turn
+      for (int c = rank + a.ranks * tid; c < g * (D / 4); c += a.ranks * kPdWarps * 32) {
+        const int hh = c / (D / 4), d = c % (D / 4) * 4;
+        float m[kRanks], l[kRanks], n[kRanks], mm, ll, nn, x[kRanks][4];
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int rem = (d + e) % (D / 8);
+            const int at = place(hh, Q8 ? 16 * (rem >> 1) + (d + e) / (D / 8) + 8 * (rem & 1) : d + e);
+            x[j][e] = j < a.ranks ? ld_cluster_f32(cluster_map(smem_u32(scratch + at), j)) : 0.f;
+          }
+        heads(hh, m, l, n, mm, ll, nn);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j) {
+          const float f = fast_exp2(n[j] - nn);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] += j < a.ranks ? f * x[j][e] : 0.f;
+        }
+        const float f = ll == 0.f ? 0.f : kUndo * fast_exp2(nn - mm) / ll;
+        const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(y[0] * f, y[1] * f), __floats2bfloat162_rn(y[2] * f, y[3] * f)};
+        *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(w);
+        if (d == 0 && a.lse) a.lse[head0 + hh] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+      }
+      if (a.mass_out) {
+        const int hh = tid - 3 * 32;
+        if (hh >= 0 && hh < g) {
+          float m[kRanks], l[kRanks], n[kRanks], mm, ll, nn;
+          heads(hh, m, l, n, mm, ll, nn);
+          lse2[hh] = ll == 0.f ? INFINITY : mm + log2f(ll);
+        }
+        named_bar_sync(1, kPdWarps * 32);  // (and the CTA's logits are written)
+        for (int i = tid; i < (int)r.count * kPdRows; i += kPdWarps * 32) {
+          const int row = r.first * kPdRows + i;
+          if (row >= r.len) break;
+          const int page = p.table[(int64_t)r.s * p.table_stride + row / p.page_rows];
+          if (!page_ok(p, page)) continue;
+          const int64_t slot = page_slot(p, page, r.h, row % p.page_rows);
+          const float* lg = a.logits + (int64_t)(r.at + i / kPdRows) * g * kPdRows + i % kPdRows;
+          float sum = 0.f, x[8];
+          const float old = p.mass[slot];
+          for (int q0 = 0; q0 < g; q0 += 8) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = q0 + q < g ? lg[(q0 + q) * kPdRows] : -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (q0 + q < g) sum += fast_exp2(x[q] - lse2[q0 + q]);
+          }
+          a.mass_out[slot] = old + sum;
+        }
+      }
+      cluster_sync_all();  // shared memory stays readable until every rank is done
+      return;
+    }
     if (tid == 0 && r.first == 0) {
       const int c0 = (int)(r.unit / sh.per);
       const int parts = (int)((r.unit + r.tiles - 1) / sh.per) - c0 + 1;
       a.unit[r.s * p.h_kv + r.h] = make_int2(c0, parts);
       if (parts > 1) a.cut[blockIdx.x] = make_int2(r.s * p.h_kv + r.h, parts);
     }
-    const int64_t head0 = (int64_t)r.s * a.h_q + (int64_t)r.h * g;
-    constexpr float kUndo = Q8 ? 1.f / kP16 : 1.f;
     auto finish = [&](int hh, float m, float l) {  // the head's log-sum-exp
       if (a.lse) a.lse[head0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
       if (a.mass_out) a.lse2[head0 + hh] = l == 0.f ? INFINITY : m + log2f(l);
@@ -926,7 +1072,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
 struct PdPlan {
   Pages pages;
   bool q8;
-  int d, g, grid, sms;
+  int d, g, grid, sms, ranks;  // ranks: CTAs to a unit of short sequences (0: the list)
   int64_t tiles;  // bound of the tile list
   size_t unit_off, lse_off, ml_off, o_off, info_off, lg_off, total;
 };
@@ -953,6 +1099,18 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
   pl.tiles = (p->total_rows / kPdRows + p->pages->num_seqs) * p->pages->h_kv;
   if (pl.tiles + (int64_t)kPdEnd * units > 0x7fffffffLL) return AIRCACHE_ERR_UNSUPPORTED;
   pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)ctas_per_sm(pl.q8, pl.g) * pl.sms, pl.tiles));
+  // Short sequences: the number of CTAs to a unit by the time of a call, in seventieths of a tile's
+  // (0.57 us; int8 rows and mass cost twice that): its CTAs' tiles, what clusters of 4 and 8 add, and one for each
+  // CTA.  Up to ten tiles' worth that beats the list and its second kernel (701 rows of 4 KV heads: 7.0 us
+  // with 4 CTAs to each, 7.7 with 8, 8.2 with 2, 11.6 with 1, 8.9 by the list; 24 x 600: 11.1 and 13.2; but 4,000
+  // rows: 11.3 and 9.8)
+  pl.ranks = 0;
+  const int64_t longest = (std::min<int64_t>(pl.pages.max_rows, p->total_rows) + kPdRows - 1) / kPdRows;  // tiles
+  int64_t least = 701;
+  for (int r = 1; r <= kPdRanks && units * r <= (int64_t)ctas_per_sm(pl.q8, pl.g) * pl.sms; r *= 2) {
+    const int64_t cost = (pl.q8 || p->mass_out ? 140 : 70) * ((longest + r - 1) / r) + (r == 8 ? 224 : r == 4 ? 56 : 0) + units * r;
+    if (cost < least) least = cost, pl.ranks = r;
+  }
   pl.unit_off = kPdHeader + up256(sizeof(int2) * (size_t)pl.grid);
   pl.lse_off = pl.unit_off + up256(sizeof(int2) * (size_t)units);
   pl.ml_off = pl.lse_off + up256(sizeof(float) * (size_t)p->pages->num_seqs * p->h_q);
@@ -997,19 +1155,25 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!encode_pages(&km, pl.pages.k, pl) || !encode_pages(&vm, pl.pages.v, pl)) return AIRCACHE_ERR_UNSUPPORTED;
   constexpr int smem = PdCfg<D, Q8, HB>::kSmem;
-  if (allow_smem(reinterpret_cast<const void*>(&paged_decode_kernel<D, Q8, HB>), smem) != cudaSuccess)
-    return AIRCACHE_ERR_CUDA;
+  const auto kernel = pl.ranks > 0 ? &paged_decode_kernel<D, Q8, HB, true> : &paged_decode_kernel<D, Q8, HB, false>;
+  if (allow_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.grid);
+  cfg.gridDim = dim3(pl.ranks > 0 ? pl.ranks * pl.pages.num_seqs * pl.pages.h_kv : pl.grid);
   cfg.blockDim = dim3(kPdThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = std::max(pl.ranks, 1);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = pl.ranks > 0 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (pl.ranks > 0) return AIRCACHE_OK;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_decode_kernel<D, Q8, HB>, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   // As many CTAs as the attention has (a cut unit begins in one of them; so each looks at one unit and
   // g heads), or with the mass as many as the SMs hold and its tiles need
   static_assert(kPfHeads >= kPdGroup, "g heads for each CTA of the attention");
@@ -1070,6 +1234,7 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   a.h_q = p->h_q;
   a.group = pl.g;
   a.ctas = pl.grid;
+  a.ranks = pl.ranks;
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pl.q8) return pl.d == 128 ? launch_pd<128, true>(pl, a, s) : launch_pd<64, true>(pl, a, s);

@@ -389,3 +389,86 @@ def test_logits_below_fp32_weigh_nothing(A, int8):
         else:
             rel = 2 * dx.max() + 2.0 ** -20
         assert np.all(np.abs(got - weight) <= rel * weight + 2.0 ** -23 * (1 + weight + 6))
+
+
+# The calls above are short by the table and the bound: a cluster to a (sequence, KV head), one kernel.  These
+# run the same rows so (tight) and as a list of tiles with a second kernel (wide: a table and a bound for far more).
+def both_ways(A, lens, h_q, h_kv, d, page_rows, seed, **kw):
+    for wide in (False, True):
+        cache = P.build(A, lens, h_kv, d, page_rows, seed=seed, max_pages=80000 // page_rows if wide else None, **kw)
+        yield wide, cache, lambda q, **k: A.PagedDecodeProblem(q, cache, total_rows=80000 if wide else max(1, sum(lens)), **k)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,h_q,h_kv,d,page_rows", [
+    ([300], 7, 1, 128, 16), ([2048, 0], 28, 4, 128, 64), ([2048], 16, 1, 64, 32), ([1000], 9, 1, 128, 48),
+    ([130] * 16, 28, 4, 128, 16), ([64] * 40, 8, 4, 64, 64), ([1] * 30, 10, 2, 128, 16),
+    ([700, 3, 0, 64, 65], 32, 32, 64, 16), ([15, 0, 640, 321, 1], 12, 6, 128, 256), (LENS, 28, 4, 128, 48),
+    (LENS, 16, 16, 64, 16)])
+def test_short_and_long_forms(A, lens, h_q, h_kv, d, page_rows, int8):
+    q = queries(len(lens), h_q, d, 41)
+    for wide, cache, make in both_ways(A, lens, h_q, h_kv, d, page_rows, 41, int8=int8, fill=float("nan")):
+        before = P.host(cache)
+        for mass in (True, False):
+            prob = make(q, lse=True, accumulate=mass)
+            A.paged_decode(prob)
+            verify(prob, before, q)
+
+
+def test_bounds_in_both_forms(A):
+    lens, q = [100, 200, 70], queries(3, 8, 128, 42)
+    for wide, cache, make in both_ways(A, lens, 8, 2, 128, 16, 42):
+        before = P.host(cache)
+        prob = make(q, lse=True, accumulate=True)
+        # a page out of range: its 16 rows count as not there, and what is reported is that
+        cache.table[1, 3] = cache.num_pages
+        ws = prob.new_workspace()
+        A.aircache_paged_decode(prob, ws)
+        with pytest.raises(A.AirCacheError) as e:
+            A.paged_decode(prob, ws)
+        assert e.value.status == A.ERR_DEVICE_BOUNDS
+        cache.mass.copy_(torch.as_tensor(before["mass"]))
+        A.aircache_paged_decode(prob, ws)
+        rest = np.setdiff1d(np.arange(200), np.arange(48, 64))
+        c = {n: before[n] for n in before}
+        pg, r = O.slots(before, 1)
+        sub = dict(k=c["k"][pg, r][rest][:, None], v=c["v"][pg, r][rest][:, None], k_scale=None, v_scale=None,
+                   mass=None, order=None, table=np.arange(len(rest))[None], lens=np.array([len(rest)]))
+        out, lse, w, size, spread = O.decode(q[1:2].double().cpu().numpy(), sub, 128 ** -0.5)
+        dx = 128 * 2.0 ** -24 * size
+        tol = (2.0 ** -16 + 2 * dx[..., None] + 2.0 ** -18) * spread + HALF * np.abs(out)
+        assert np.all(np.abs(prob.out[1:2].double().cpu().numpy() - out) <= tol)
+        gm = prob.mass_out.double().cpu().numpy()[pg, :, r] - before["mass"][pg, :, r]
+        assert np.all(gm[48:64] == 0)
+        assert np.all(np.abs(gm[rest] - w[0].T) <= (2 * dx.max() + 2.0 ** -20) * w[0].T + 2.0 ** -23 * 6)
+        cache.table[1, 3] = torch.as_tensor(before["table"][1, 3])
+        # a bad length counts as 0
+        cache.lens[1] = -5
+        ws = prob.new_workspace()
+        A.aircache_paged_decode(prob, ws)
+        with pytest.raises(A.AirCacheError):
+            A.paged_decode(prob, ws)
+        assert not prob.out[1].any() and bool(torch.isneginf(prob.lse[1]).all())
+        cache.lens[1] = 200
+        # more rows than the bound: nothing is computed
+        small = A.PagedDecodeProblem(q, cache, lse=True, total_rows=369 if not wide else 80000)
+        if wide:
+            cache.lens[2] = cache.max_pages * 16
+        small.out.fill_(7.0)
+        with pytest.raises(A.AirCacheError) as e:
+            A.paged_decode(small)
+        assert e.value.status == A.ERR_CAPACITY
+        assert bool((small.out == 7.0).all())
+
+
+def test_nan_is_not_hidden_by_the_list(A):
+    lens, q = [40, 300, 70], queries(3, 6, 128, 43)
+    for wide, cache, make in both_ways(A, lens, 6, 2, 128, 16, 43):
+        cache.k[cache.table[0, :3].long()] = float("nan")
+        cache.v[cache.table[1, 9].long(), 5, 0, 17] = float("nan")
+        prob = make(q, lse=True)
+        A.paged_decode(prob)
+        assert bool(torch.isnan(prob.out[0]).all()) and bool(torch.isnan(prob.lse[0]).all())
+        hit = torch.isnan(prob.out[1])
+        assert bool(hit[:3, 17].all()) and not bool(hit[3:].any())
+        assert bool(torch.isfinite(prob.out[2]).all()) and bool(torch.isfinite(prob.lse[1:]).all())
