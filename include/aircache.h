@@ -742,7 +742,8 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  * rows, mass and order (lens_out[s] = lens[s]).
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): mass; order when sink or recent
  * is not 0, seen when recent is not 0; order_out exactly with order; sink,
- * recent >= 0.  Workspace as for aircache_paged_decode.  Two kernels: one selects, one moves.
+ * recent >= 0.  Workspace as for aircache_paged_decode.  Two kernels, one that selects and one that moves; one
+ * does both where max_rows is small (some thousand): give a close one.
  */
 #define AIRCACHE_MAX_EVICT_ROWS 393216
 

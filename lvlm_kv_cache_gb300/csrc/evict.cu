@@ -18,7 +18,7 @@
 // and movers in order.  Bound by the
 // chain of barriers and scans: 8 bytes a row are read.
 // move: CTAs over all SMs copy the listed rows, 32 moves to a warp at a time.
-// Bound by HBM.
+// Bound by HBM.  Few rows are moved by the CTAs that selected them, in one kernel.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -31,6 +31,11 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvMaxCluster = 8;
 constexpr int kMvThreads = 256, kMvCtas = 4;  // of the moves: threads of a CTA, CTAs to an SM
 constexpr int kEvSlice = AIRCACHE_MAX_EVICT_ROWS / kEvMaxCluster;  // keys of one CTA, at most
+// Rows of one CTA, at most, for it to move them too, in one kernel; twice as many where it has a (sequence, KV
+// head) for itself (one of 1,088: 7.2 us, and 8.3 with the second kernel; 8 x 4,000, in clusters of 2:
+// 18.4 and 21.1; 48 x 4,000 int8: 29.8 and 34.2; but 16 x 8,000, in clusters of 2: 36.2 and 33.8, and 48 of up
+// to 9,000 int8: 39.8 and 38.4)
+constexpr int kEvShort = 2048;
 constexpr int kEvHeader = 256;                                     // workspace: error word
 constexpr uint32_t kProtected = 0xffffffffu;
 
@@ -80,12 +85,70 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+// RB: 16-byte pieces of a row of one KV head.  What a warp waits for is hidden
+// by other warps, so few registers count for more than many loads of one warp
+// (16 x 16k to half: 73 us with eight row loads in flight and 24 warps to an SM,
+// 61 with four and 32), and nothing is stored before every load of the 32 moves' scales, mass
+// and order and the first rows' has been issued.
+template <int RB>
+__device__ __forceinline__ void move_rows(const EvArgs& a, int s, int h, int moves, int first, int warps) {
+  const Pages& p = a.pages;
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.table + (int64_t)s * p.table_stride;
+  const int32_t* list = a.lists + ((int64_t)s * p.h_kv + h) * 2 * a.half;
+  constexpr int kAtOnce = 32 / (2 * RB);  // moves of one warp instruction
+  const int piece = lane % RB, sub = lane / (2 * RB);
+  uint8_t* const kv = ((lane / RB) & 1 ? p.v : p.k) + 16 * piece;
+  const int size = p.k_scale ? 1 : 2;
+  for (int m0 = 32 * first; m0 < moves; m0 += 32 * warps) {
+    int64_t src = 0, dst = 0, ds = 0;
+    const int cnt = min(32, moves - m0);
+    float mass = 0.f, ks = 0.f, vs = 0.f;
+    int32_t order = 0;
+    if (lane < cnt) {
+      const int to = list[m0 + lane], from = list[a.half + m0 + lane];
+      int tr, fr;
+      const int tx = page_of(p, to, tr), fx = page_of(p, from, fr);
+      const int tp = table[tx], fp = table[fx];
+      ds = page_slot(p, tp, h, tr);
+      const int64_t ss = page_slot(p, fp, h, fr);
+      dst = page_elem(p, tp, h, tr) * size;
+      src = page_elem(p, fp, h, fr) * size;
+      mass = p.mass[ss];
+      if (a.order_out) order = p.order[ss];
+      if (p.k_scale) ks = p.k_scale[ss], vs = p.v_scale[ss];
+    }
+    constexpr int kFlight = 4;
+    for (int j0 = 0; j0 < cnt; j0 += kAtOnce * kFlight) {
+      uint4 x[kFlight];
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        const int j = j0 + f * kAtOnce + sub;
+        const int64_t from = __shfl_sync(0xffffffffu, src, j & 31);
+        if (j < cnt) x[f] = *reinterpret_cast<const uint4*>(kv + from);
+      }
+#pragma unroll
+      for (int f = 0; f < kFlight; ++f) {
+        const int j = j0 + f * kAtOnce + sub;
+        const int64_t to = __shfl_sync(0xffffffffu, dst, j & 31);
+        if (j < cnt) *reinterpret_cast<uint4*>(kv + to) = x[f];
+      }
+    }
+    if (lane < cnt) {
+      a.mass_out[ds] = mass;
+      if (a.order_out) a.order_out[ds] = order;
+      if (p.k_scale) p.k_scale[ds] = ks, p.v_scale[ds] = vs;
+    }
+  }
+}
+
 // R CTAs (a cluster) per (sequence, KV head).  What they tell each other is read
 // by one lane per CTA at once, or by loads that do not wait for one another: a
 // load from another CTA's shared memory takes several hundred cycles.  F groups of four rows
 // load at once in a thread: eight with one CTA to an SM, four (and half the registers) with two
 // (2 x 128k with 8 and 4: 47 and 52 us; ragged, 192 CTAs: 42 and 39.5).
-template <int R, int F>
+// RB: the CTA also moves the rows (0: another kernel does).
+template <int R, int F, int RB>
 __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kernel(const __grid_constant__ EvArgs a) {
   extern __shared__ uint32_t ev_keys[];
   __shared__ EvShared sh;
@@ -432,8 +495,14 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
       for (uint32_t e = lane; e < holes; e += 32) list[hole0 + e] = packed[e];
       for (uint32_t e = lane; e < movers; e += 32) list[a.half + mover0 - stay_low + e] = packed[holes + e];
     }
-    if (tid == 0 && rank == 0) a.moves[(int64_t)s * p.h_kv + h] = keep > 0 ? less + ties_low - stay_low : 0;
-  } else if (tid == 0 && rank == 0) {
+    const int moves = keep > 0 ? less + ties_low - stay_low : 0;
+    if constexpr (RB > 0) {
+      sync_all();  // the lists are written
+      move_rows<RB>(a, s, h, moves, rank * kEvWarps + warp, R * kEvWarps);
+    } else if (tid == 0 && rank == 0) {
+      a.moves[(int64_t)s * p.h_kv + h] = moves;
+    }
+  } else if (RB == 0 && tid == 0 && rank == 0) {
     a.moves[(int64_t)s * p.h_kv + h] = 0;
   }
   if (tid == 0 && rank == 0 && h == 0) a.lens_out[s] = go ? keep : len;
@@ -441,67 +510,13 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   if (CL) cluster_sync_all();  // shared memory stays readable until every rank is done
 }
 
-// RB: 16-byte pieces of a row of one KV head.  What a warp waits for is hidden
-// by other warps, so few registers count for more than many loads of one warp
-// (16 x 16k to half: 73 us with eight row loads in flight and 24 warps to an SM,
-// 61 with four and 32), and nothing is stored before every load of the 32 moves' scales, mass
-// and order and the first rows' has been issued.
 template <int RB>
 __global__ void __launch_bounds__(kMvThreads, kMvCtas) evict_move_kernel(const __grid_constant__ EvArgs a) {
   pdl_trigger();
   pdl_wait();
-  const Pages& p = a.pages;
-  const int lane = threadIdx.x & 31;
   const int h = blockIdx.y, s = blockIdx.z;
-  const int64_t unit = (int64_t)s * p.h_kv + h;
-  const int moves = a.moves[unit];
-  const int32_t* table = p.table + (int64_t)s * p.table_stride;
-  const int32_t* list = a.lists + unit * 2 * a.half;
-  constexpr int kAtOnce = 32 / (2 * RB);  // moves of one warp instruction
-  const int piece = lane % RB, sub = lane / (2 * RB);
-  uint8_t* const kv = ((lane / RB) & 1 ? p.v : p.k) + 16 * piece;
-  const int size = p.k_scale ? 1 : 2;
-  for (int m0 = 32 * (blockIdx.x * (kMvThreads / 32) + (threadIdx.x >> 5)); m0 < moves;
-       m0 += 32 * gridDim.x * (kMvThreads / 32)) {
-    int64_t src = 0, dst = 0, ds = 0;
-    const int cnt = min(32, moves - m0);
-    float mass = 0.f, ks = 0.f, vs = 0.f;
-    int32_t order = 0;
-    if (lane < cnt) {
-      const int to = list[m0 + lane], from = list[a.half + m0 + lane];
-      int tr, fr;
-      const int tx = page_of(p, to, tr), fx = page_of(p, from, fr);
-      const int tp = table[tx], fp = table[fx];
-      ds = page_slot(p, tp, h, tr);
-      const int64_t ss = page_slot(p, fp, h, fr);
-      dst = page_elem(p, tp, h, tr) * size;
-      src = page_elem(p, fp, h, fr) * size;
-      mass = p.mass[ss];
-      if (a.order_out) order = p.order[ss];
-      if (p.k_scale) ks = p.k_scale[ss], vs = p.v_scale[ss];
-    }
-    constexpr int kFlight = 4;
-    for (int j0 = 0; j0 < cnt; j0 += kAtOnce * kFlight) {
-      uint4 x[kFlight];
-#pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        const int j = j0 + f * kAtOnce + sub;
-        const int64_t from = __shfl_sync(0xffffffffu, src, j & 31);
-        if (j < cnt) x[f] = *reinterpret_cast<const uint4*>(kv + from);
-      }
-#pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        const int j = j0 + f * kAtOnce + sub;
-        const int64_t to = __shfl_sync(0xffffffffu, dst, j & 31);
-        if (j < cnt) *reinterpret_cast<uint4*>(kv + to) = x[f];
-      }
-    }
-    if (lane < cnt) {
-      a.mass_out[ds] = mass;
-      if (a.order_out) a.order_out[ds] = order;
-      if (p.k_scale) p.k_scale[ds] = ks, p.v_scale[ds] = vs;
-    }
-  }
+  const int moves = a.moves[(int64_t)s * a.pages.h_kv + h];
+  move_rows<RB>(a, s, h, moves, blockIdx.x * (kMvThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kMvThreads / 32));
 }
 
 // ------------------------------------------------------------------ host
@@ -540,9 +555,9 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   return AIRCACHE_OK;
 }
 
-template <int R, int F>
+template <int R, int F, int RB>
 int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
-  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<R, F>), (int)pl.smem) != cudaSuccess)
+  if (allow_smem(reinterpret_cast<const void*>(&evict_select_kernel<R, F, RB>), (int)pl.smem) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(R, a.pages.h_kv, a.pages.num_seqs);
@@ -558,13 +573,23 @@ int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = R > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R, F>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<R, F, RB>, a) == cudaSuccess ? AIRCACHE_OK : AIRCACHE_ERR_CUDA;
 }
 
-template <int R>
+template <int R, int RB>
 int launch_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
   const int64_t ctas = (int64_t)R * a.pages.h_kv * a.pages.num_seqs;
-  return ctas <= pl.sms ? launch_select<R, 8>(pl, a, s) : launch_select<R, 4>(pl, a, s);
+  return ctas <= pl.sms ? launch_select<R, 8, RB>(pl, a, s) : launch_select<R, 4, RB>(pl, a, s);
+}
+
+template <int RB>
+int pick_select(const EvPlan& pl, const EvArgs& a, cudaStream_t s) {
+  switch (pl.ranks) {
+    case 1: return launch_select<1, RB>(pl, a, s);
+    case 2: return launch_select<2, RB>(pl, a, s);
+    case 4: return launch_select<4, RB>(pl, a, s);
+    default: return launch_select<8, RB>(pl, a, s);
+  }
 }
 
 template <int RB>
@@ -612,10 +637,14 @@ int aircache_evict(const aircache_evict_problem* p, void* ws, size_t ws_bytes, v
   a.sink = p->sink;
   a.recent = p->recent;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sel = pl.ranks == 1   ? launch_select<1>(pl, a, s)
-                  : pl.ranks == 2 ? launch_select<2>(pl, a, s)
-                  : pl.ranks == 4 ? launch_select<4>(pl, a, s)
-                                  : launch_select<8>(pl, a, s);
+  if (p->max_rows <= kEvShort * std::max<int64_t>(pl.ranks, 2)) {
+    switch (pl.row_bytes) {
+      case 256: return pick_select<16>(pl, a, s);
+      case 128: return pick_select<8>(pl, a, s);
+      default: return pick_select<4>(pl, a, s);
+    }
+  }
+  const int sel = pick_select<0>(pl, a, s);
   if (sel != AIRCACHE_OK) return sel;
   switch (pl.row_bytes) {
     case 256: return launch_move<16>(pl, a, s);

@@ -228,3 +228,15 @@ def test_lengths_past_max_rows(A):
     with pytest.raises(A.AirCacheError):
         A.evict(prob)
     assert prob.lens_out.tolist() == [100, 30]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("max_rows", [0, 60_000])
+@pytest.mark.parametrize("lens,keep,h_kv,d", [
+    (LENS, [4, 10, 8, 12, 16, 40, 99, 150, 200], 3, 128), ([3001, 700], [1500, 650], 2, 64),
+    ([5003, 8000], [5002, 300], 2, 128), ([16003], [9000], 3, 64), ([400] * 50, [200] * 50, 4, 64)])
+def test_moves_by_the_selecting_ctas_and_by_others(A, lens, keep, h_kv, d, max_rows, in_place, int8):
+    # a close bound: one kernel, of one to eight CTAs to a (sequence, KV head); a far one: two kernels
+    cache = P.build(A, lens, h_kv, d, 16, seed=33, int8=int8)
+    check(A, cache, keep, seen=lens, sink=2, recent=2, max_rows=max_rows, in_place=in_place)
