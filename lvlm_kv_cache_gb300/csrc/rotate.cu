@@ -459,9 +459,9 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   const int steps = (a.heads + at_once - 1) / at_once;
   const int64_t slots = (int64_t)kRotMany * sms;
   int64_t least = INT64_MAX;
-  int best = steps;
-  const int shares_max = p->num_tokens >= 8 * slots ? 1 : std::min(steps, 17);
-  for (int i = 1; i <= shares_max; ++i) {
+  int best = p->num_tokens >= 8 * slots ? steps : 1;
+  const bool ask = best == 1 && p->num_tokens * steps > 20LL * sms;  // (below, a step to a warp costs least)
+  for (int i = 1; ask && i <= std::min(steps, 17); ++i) {
     const int n = i == 17 ? 1 : (steps + i - 1) / i;  // (16 shares at most, or a step to each)
     const int64_t warps = p->num_tokens * ((steps + n - 1) / n);
     const int64_t cost = 10LL * sms * ((warps + slots - 1) / slots) * (n + 3) + warps;
