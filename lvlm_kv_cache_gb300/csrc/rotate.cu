@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotF
   x.row = 0;
   const bool appends = a.has_pages && last > a.h_q;
   if (appends) {
-    const int i = len - back;
-    if (back >= 1 && i >= 0 && len <= a.pages.max_rows) {
+    if (back >= 1 && len >= back && len <= a.pages.max_rows) {
+      const int i = len - back;  // (formed only here: a length near int32's lowest would wrap to a row)
       const int nth = a.pages.max_rows < (1 << 24) ? page_of(a.pages, i, x.row) : i / a.pages.page_rows;
       x.row = i - nth * a.pages.page_rows;
       x.page = a.pages.table[s * a.pages.table_stride + nth];

@@ -1,0 +1,59 @@
+"""The paged cache's operators, and the int8 storage they share their codes with, at the
+ends of their ranges: infinities and NaN, sizes far apart, orders and lengths at int32's
+ends, first calls from several threads, bounds that are left to their defaults.
+
+Results are exact or go by the tolerances that test_gpu_paged_decode.py derives."""
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import paged_utils as P
+import test_gpu_paged_decode as D
+from conftest import ROOT
+from oracle import paged as O
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def A():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from lvlm_kv_cache_gb300 import build
+
+    build.build()
+    from lvlm_kv_cache_gb300 import aircache
+
+    aircache.lib()
+    return aircache
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def normal(*shape, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("length", [-1, -2, -5, -(2 ** 31), -(2 ** 31) + 1, -(2 ** 31) + 4, 2 ** 31 - 1])
+def test_rotation_reads_nothing_through_a_length_out_of_bounds(A, length):
+    n = [3, 5]
+    cache = P.build(A, [20, 5], 2, 64, 16, seed=51)
+    cache.lens[0] = length
+    k = normal(8, 2, 64, seed=52)
+    before = P.state(cache)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    A.aircache_rotate(A.RotateProblem(None, k, k.clone(), cache=cache, cu_tokens=i32(0, 3, 8), seen=i32(3, 5)), st)
+    assert A.aircache_get_error(st) == A.ERR_DEVICE_BOUNDS
+    after = P.state(cache)
+    own = int(cache.table[1, 0])
+    for name in before:  # sequence 1's five rows are its page's; nothing else is written
+        rest = [i for i in range(cache.num_pages) if i != own]
+        assert np.array_equal(before[name][rest], after[name][rest]), name
+    assert np.array_equal(after["k"][own][:5], P.bits(k[3:]))
