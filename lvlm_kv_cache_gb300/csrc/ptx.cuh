@@ -100,9 +100,11 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
 
 // Thread-block clusters: every thread of every CTA of the cluster arrives
 // (release) and waits (acquire), so shared-memory writes made before the
-// barrier are visible to the whole cluster after it.  Called uniformly by all
-// threads (.aligned).
+// barrier are visible to the whole cluster after it.  Called by all threads; the
+// lanes of a warp may come from loops and branches of their own, and meet here
+// first, because the .aligned form counts a warp once.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 

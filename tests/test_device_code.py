@@ -1,0 +1,33 @@
+"""Rules of the device code that no result on a GPU shows until they are broken at the wrong
+moment: read from the sources, without a GPU."""
+import os
+import re
+
+from conftest import ROOT
+
+CSRC = os.path.join(ROOT, "lvlm_kv_cache_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(text, head):
+    """The braces' contents behind the first `head`."""
+    at = text.index("{", text.index(head))
+    depth, i = 1, at + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+    return text[at + 1:i - 1]
+
+
+def test_warps_meet_before_a_cluster_barrier():
+    # barrier.cluster.*.aligned is undefined for a warp whose lanes have not reconverged
+    for name in sorted(os.listdir(CSRC)):
+        if name != "ptx.cuh":
+            assert "barrier.cluster" not in source(name), name
+    text = source("ptx.cuh")
+    assert text.count("barrier.cluster.arrive") == 1
+    assert body(text, "void cluster_sync_all()").strip().startswith("__syncwarp();")
