@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         const int pg = __shfl_sync(0xffffffffu, page, (i & 7) * 4 + piece);
         const uint32_t mask = __ballot_sync(0xffffffffu, pg >= 0) & 15u;
         if (filled >= C::kStages) {
-          if (!mbar_wait(&empty[st], phase ^ 1)) {
+          if (!mbar_wait_warp(&empty[st], phase ^ 1)) {
             set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
             alive = false;
             break;
@@ -414,8 +414,10 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         if (++st == C::kStages) st = 0, phase ^= 1;
       }
     }
+    // every copy has landed before the CTA's shared memory is another's (consumers whose wait ran out left some behind)
+    for (uint32_t f = filled > C::kStages ? filled - C::kStages : 0; f < filled; ++f)
+      (void)mbar_wait_warp(&full[f % C::kStages], (f / C::kStages) & 1);
     if (SHORT && sh.lo < sh.hi) {  // (the consumers' barriers are the whole cluster's)
-      __syncwarp();
       cluster_sync_all();
       cluster_sync_all();
     }
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     constexpr float kSlack = 8.f, kSlack16 = 1.f;  // (f16 weights carry 2^14: 2^15 is the most they may reach)
 
     for (uint32_t i = 0; i < r.count && alive; ++i) {
-      if (!mbar_wait(&full[st], phase)) {
+      if (!mbar_wait_warp(&full[st], phase)) {
         if (lane == 0) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
         alive = false;
         break;

@@ -53,6 +53,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, long l
   return true;
 }
 
+// mbar_wait by a whole warp, whose lanes get one answer: false where any lane's time
+// ran out.  (Lanes that gave up alone would leave the others to wait for them in the
+// next vote or shuffle.)
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, long long limit = kWaitCycles) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
+}
+
 // Bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) from
 // global to this CTA's shared memory; completion is counted on `bar`.
 // Bulk copy shared -> global (a bulk group), the group commit, and the waits

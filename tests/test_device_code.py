@@ -31,3 +31,10 @@ def test_warps_meet_before_a_cluster_barrier():
     text = source("ptx.cuh")
     assert text.count("barrier.cluster.arrive") == 1
     assert body(text, "void cluster_sync_all()").strip().startswith("__syncwarp();")
+
+
+def test_waits_of_the_paged_decode_end_for_whole_warps_and_after_its_copies():
+    text = source("paged_decode.cu")
+    assert "mbar_wait(" not in text and "__all_sync" in body(source("ptx.cuh"), "bool mbar_wait_warp(")
+    producer = body(text, "if (warp == kPdWarps) {")
+    assert producer.rindex("mbar_wait_warp(&full[") > producer.rindex("tma_load_5d(")
