@@ -555,8 +555,8 @@ AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t
  * head_dim 64 or 128, kv_dtype AIRCACHE_BF16 or AIRCACHE_INT8 (with both
  * scales), page_rows a multiple of 16 in 16..4096, max_pages >= 1 with
  * max_pages * page_rows <= 2^31 - 2^16, 1 <= num_pages <= 2^31 - 1, table_stride >=
- * max_pages; k, v, the scales, mass and order 16-byte aligned, strides positive
- * multiples of 16 bytes.  Device-side, a length outside
+ * max_pages; k, v, the scales, mass and order 16-byte aligned, other integers
+ * here and in the calls below 4-byte, strides positive multiples of 16 bytes.  Device-side, a length outside
  * [0, max_pages * page_rows] or a page outside [0, num_pages) sets
  * AIRCACHE_ERR_DEVICE_BOUNDS; nothing is then read or written through it (each
  * entry point says what becomes of the sequence).
@@ -621,7 +621,7 @@ typedef struct aircache_pages {
  * exactly with pages; rotary_dim 0 or a multiple of 16 up to head_dim, turns
  * when it is not 0; axes 1 or 3, sections >= 0 with a sum of at most rotary_dim/2
  * when axes is 3; eps >= 0; seen when pages has order or positions is NULL (with
- * rotary_dim > 0); pointers 16-byte aligned, strides multiples of 8 elements.
+ * rotary_dim > 0); pointers 16-byte aligned (those of integers 4-byte), strides multiples of 8 elements.
  * A token whose row or page is out of bounds sets AIRCACHE_ERR_DEVICE_BOUNDS
  * in *status (optional device int32, not cleared by the call) and is not
  * appended; its q_out and k_out are written.  cu_tokens[num_seqs] > num_tokens

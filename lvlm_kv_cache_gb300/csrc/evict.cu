@@ -537,6 +537,8 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
       (reinterpret_cast<uintptr_t>(p->order_out) & 15) != 0 || p->sink < 0 || p->recent < 0 ||
       ((p->sink || p->recent) && !p->pages->order) || (p->recent && !p->seen) || p->max_rows < 1)
     return AIRCACHE_ERR_INVALID_ARG;
+  auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
+  if (!al4(p->keep) || !al4(p->seen) || !al4(p->lens_out)) return AIRCACHE_ERR_INVALID_ARG;
   if (p->max_rows > AIRCACHE_MAX_EVICT_ROWS) return AIRCACHE_ERR_UNSUPPORTED;
   pl.sms = device_sms();
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;

@@ -391,6 +391,8 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
       (p->axes != 1 && p->axes != 3) || (p->axes == 3 && (p->section0 < 0 || p->section1 < 0 ||
        (int64_t)p->section0 + p->section1 > p->rotary_dim / 2 || !p->positions)))
     return AIRCACHE_ERR_INVALID_ARG;
+  auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
+  if (!al4(p->positions) || !al4(p->cu_tokens) || !al4(p->seen) || !al4(status)) return AIRCACHE_ERR_INVALID_ARG;
   if (!al16(p->q) || !al16(p->k) || !al16(p->v) || !al16(p->q_out) || !al16(p->k_out) || !al16(p->q_weight) ||
       !al16(p->k_weight) || !al16(p->turns) || (p->q && !strides(p->q_stride_tok, p->q_stride_head)) ||
       (p->k && !strides(p->k_stride_tok, p->k_stride_head)) || (p->v && !strides(p->v_stride_tok, p->v_stride_head)) ||
