@@ -150,7 +150,7 @@ __device__ __forceinline__ void move_rows(const EvArgs& a, int s, int h, int mov
 // RB: the CTA also moves the rows (0: another kernel does).
 template <int R, int F, int RB>
 __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kernel(const __grid_constant__ EvArgs a) {
-  extern __shared__ uint32_t ev_keys[];
+  extern __shared__ __align__(16) uint32_t ev_keys[];  // (read four at a time)
   __shared__ EvShared sh;
   const Pages& p = a.pages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

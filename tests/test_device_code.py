@@ -38,3 +38,12 @@ def test_waits_of_the_paged_decode_end_for_whole_warps_and_after_its_copies():
     assert "mbar_wait(" not in text and "__all_sync" in body(source("ptx.cuh"), "bool mbar_wait_warp(")
     producer = body(text, "if (warp == kPdWarps) {")
     assert producer.rindex("mbar_wait_warp(&full[") > producer.rindex("tma_load_5d(")
+
+
+def test_shared_memory_that_is_read_in_pieces_is_aligned_for_them():
+    # dynamic shared memory that is cast to 16-byte vectors says so itself, whatever static arrays lie before it
+    for name in ("evict.cu", "elite.cu", "compact.cu"):
+        text = source(name)
+        assert "uint4*" in text or "float4*" in text
+        for decl in re.findall(r"extern __shared__[^;]*;", text):
+            assert re.search(r"__align__\((16|32|64|128|1024)\)|alignas\((16|32|64|128|1024)\)|uint4|float4", decl), (name, decl)
