@@ -63,7 +63,14 @@ __device__ __forceinline__ void ldsm_x4(uint32_t r[4], uint32_t addr) {
 
 // ------------------------------------------------------------------ host
 
+// The encoder refuses threads without a context, and a thread has none before its first CUDA call
+// that needs one: the encoder's callers get their device's here.
 inline PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() {
+  static thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    bound = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+  }
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static bool tried = false;
   if (!tried) {

@@ -57,3 +57,35 @@ def test_rotation_reads_nothing_through_a_length_out_of_bounds(A, length):
         rest = [i for i in range(cache.num_pages) if i != own]
         assert np.array_equal(before[name][rest], after[name][rest]), name
     assert np.array_equal(after["k"][own][:5], P.bits(k[3:]))
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_the_first_cuda_call_of_a_thread(A, dense):
+    # a thread that has no CUDA context yet: the call binds its device's
+    import threading
+
+    q, k, v = normal(2, 4, 128, seed=53), normal(100, 2, 128, seed=54), normal(100, 2, 128, seed=55)
+    if dense:
+        prob = A.DecodeProblem(q, k, v, offsets=torch.tensor([0, 60, 100], device="cuda"))
+        call = A.aircache_decode
+    else:
+        prob = A.PagedDecodeProblem(q, P.build(A, [70, 33], 2, 128, 16, seed=56))
+        call = A.aircache_paged_decode
+    ws = prob.new_workspace()
+    call(prob, ws)
+    want = prob.out.clone()
+    prob.out.zero_()
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run():
+        try:
+            call(prob, ws)
+        except A.AirCacheError as e:
+            wrong.append(str(e))
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not wrong and torch.equal(prob.out, want)
