@@ -47,3 +47,12 @@ def test_shared_memory_that_is_read_in_pieces_is_aligned_for_them():
         assert "uint4*" in text or "float4*" in text
         for decl in re.findall(r"extern __shared__[^;]*;", text):
             assert re.search(r"__align__\((16|32|64|128|1024)\)|alignas\((16|32|64|128|1024)\)|uint4|float4", decl), (name, decl)
+
+
+def test_host_code_keeps_nothing_that_two_threads_could_set_at_once():
+    # a function's static is constant, one to a thread, or of a type that threads may share
+    plain = r"^ +static (?!const\b|constexpr\b|thread_local\b|std::mutex\b|std::once_flag\b|std::atomic<|__device__)[^()]*;"
+    guarded = {"budget.cu": "std::call_once(", "api.cu": "std::lock_guard<std::mutex> lock(mu);"}
+    for name in sorted(os.listdir(CSRC)):
+        found = re.findall(plain, source(name), re.M)
+        assert not found or guarded.get(name, "nothing") in source(name), (name, found)

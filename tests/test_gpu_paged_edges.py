@@ -89,3 +89,39 @@ def test_the_first_cuda_call_of_a_thread(A, dense):
     t.join()
     torch.cuda.synchronize()
     assert not wrong and torch.equal(prob.out, want)
+
+
+def test_first_calls_from_several_threads(A):
+    # a fresh process whose threads make their first call at once: each gets the answer of a call alone
+    code = """
+import sys, threading
+sys.path[:0] = [%r, %r + "/tests"]
+import torch
+import paged_utils as P
+from lvlm_kv_cache_gb300 import aircache as A
+lens, n = [70, 33], 16
+jobs = []
+for i in range(n):
+    cache = P.build(A, lens, 2, 128, 16, seed=45)
+    q = torch.randn((2, 4, 128), generator=torch.Generator().manual_seed(46)).to(torch.bfloat16).cuda()
+    prob = A.PagedDecodeProblem(q, cache)
+    jobs.append((prob, prob.new_workspace(), torch.cuda.Stream()))
+torch.cuda.synchronize()
+gate, wrong = threading.Barrier(n), []
+def call(prob, ws, stream):
+    try:
+        gate.wait()
+        A.aircache_paged_decode(prob, ws, stream)
+    except Exception as e:
+        wrong.append(str(e))
+threads = [threading.Thread(target=call, args=j) for j in jobs]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not wrong, wrong
+assert all(torch.equal(j[0].out, jobs[0][0].out) for j in jobs)
+print("same")
+""" % (ROOT, ROOT)
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+        assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
