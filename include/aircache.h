@@ -484,6 +484,8 @@ AIRCACHE_API int aircache_decode_splits(const aircache_decode_problem* p);
  *   s = max |x| / 127 in fp32 over the unit's rows and the head's head_dim values;
  *   q = clip(round(x / s), -127, 127), x / s in fp32 (correctly rounded),
  *       round half away from zero; a head whose values are all 0 has s = 0, q = 0.
+ *       A head with an infinity has s = inf and q = 0 throughout, which read as
+ *       NaN; a value that is NaN has q = 0.
  * The units of aircache_compress's arena are its (layer, request) pairs:
  * offsets = out_offsets, num_units = L*B.
  *

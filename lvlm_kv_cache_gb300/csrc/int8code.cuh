@@ -14,11 +14,16 @@ namespace aircache {
 // 4e-5 of a half-integer the correctly rounded division and roundf decide.
 // |t| < 127.5 there, so no clip is needed.  A subnormal s can overflow 1/s and
 // is itself a coarse rounding of max / 127: those quotients (t infinite or NaN,
-// which fails the comparison below) are divided and clipped.
+// which fails the comparison below) are divided and clipped.  What has no quotient
+// (a NaN, or an infinity under the infinite scale that it makes) has the code 0,
+// which under that scale stands for NaN: clipped, it would be minus the largest value.
 __device__ __forceinline__ int code(float x, float s, float rs) {
   const float t = x * rs;
   const float rt = rintf(t);
-  if (!(fabsf(t - rt) <= 0.5f - 4e-5f)) return (int)fminf(fmaxf(roundf(__fdiv_rn(x, s)), -127.f), 127.f);
+  if (!(fabsf(t - rt) <= 0.5f - 4e-5f)) {
+    const float q = roundf(__fdiv_rn(x, s));
+    return q == q ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;
+  }
   return (int)rt;
 }
 

@@ -125,3 +125,40 @@ print("same")
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
         assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_quantized_infinities_are_not_numbers(A, oracle, d):
+    # a head with an infinity has the scale inf and codes of 0, which stand for NaN: no infinity changes its sign
+    k, v = normal(600, 3, d, seed=1), normal(600, 3, d, seed=2)
+    clean = A.quantize_int8(k, v, torch.tensor([0, 100, 350, 600], device="cuda"))
+    k[5, 0, 7], k[5, 0, 8], k[120, 1, 0], v[599, 2, d - 1] = INF, -INF, INF, -INF
+    k8, v8, ks, vs = A.quantize_int8(k, v, torch.tensor([0, 100, 350, 600], device="cuda"))
+    hit = [(k8, ks, 0, slice(0, 100), 0), (k8, ks, 1, slice(100, 350), 1), (v8, vs, 2, slice(350, 600), 2)]
+    for codes, scale, u, rows, h in hit:
+        assert float(scale[u, h]) == INF and not bool(codes[rows, h].any())
+    for codes, scale, was, was_scale, at in ((k8, ks, clean[0], clean[2], hit[:2]), (v8, vs, clean[1], clean[3], hit[2:])):
+        same, same_scale = torch.ones_like(codes, dtype=torch.bool), torch.ones_like(scale, dtype=torch.bool)
+        for _, _, u, rows, h in at:
+            same[rows, h] = False
+            same_scale[u, h] = False
+        assert torch.equal(codes[same], was[same]) and torch.equal(scale[same_scale], was_scale[same_scale])
+
+
+def test_quantized_nan_has_the_code_0(A):
+    k = normal(64, 2, 64, seed=3)
+    k[4, 0, 5] = NAN
+    k8, _, _, _ = A.quantize_int8(k, k.clone(), torch.tensor([0, 64], device="cuda"))
+    assert int(k8[4, 0, 5]) == 0
+
+
+@pytest.mark.parametrize("size", [1e-36, 1e-38, 3e-40])
+def test_quantized_subnormal_scales(A, size):
+    k = (normal(200, 2, 128, seed=4).double() * size).to(torch.bfloat16)
+    k8, _, ks, _ = A.quantize_int8(k, k.clone(), torch.tensor([0, 200], device="cuda"))
+    x = k.float().cpu().numpy()
+    s = (np.abs(x).max((0, 2)) / np.float32(127)).astype(np.float32)
+    assert np.array_equal(ks[0].cpu().numpy(), s)
+    t = (x / s[None, :, None]).astype(np.float64)
+    want = np.clip(np.copysign(np.floor(np.abs(t) + 0.5), t), -127, 127)
+    assert np.array_equal(k8.cpu().numpy().astype(np.float64), want)
