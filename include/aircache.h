@@ -612,7 +612,10 @@ typedef struct aircache_pages {
  * the cache has mass) and order seen[s]-n .. seen[s]-1 (if it has order), where
  * seen[s] is the number of tokens appended to s so far, these n among them.
  * int8 caches get s = max |y| / 127 of the row's head in fp32 and codes
- * round(y / s), half away from zero (0 for a row of zeros).  Without a cache cu_tokens may be NULL (no padding) and positions
+ * round(y / s), half away from zero (0 for a row of zeros).  A row's head with a
+ * NaN gets the scale NaN, one with an infinity the scale inf, and both codes of
+ * 0, which read as NaN throughout: attention over the row gives NaN, as bf16
+ * rows do.  Without a cache cu_tokens may be NULL (no padding) and positions
  * must be given.
  * q_out may be q and k_out may be k (the same pointer and strides: in place);
  * otherwise outputs do not overlap inputs, nor their own rows (strides of at

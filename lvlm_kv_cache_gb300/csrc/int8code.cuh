@@ -6,6 +6,13 @@
 
 namespace aircache {
 
+// The larger value, or NaN where one of them is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // clip(round(x / s)) with x / s correctly rounded, s > 0, |x| <= 127 s.
 // The quotient is first taken as t = x * (1/s) (both correctly rounded:
 // within 1.6e-5 of the exact quotient, and the correctly rounded quotient is

@@ -206,11 +206,11 @@ __device__ __forceinline__ void rows_of_token(const RotArgs& a, const Lane& x, i
       }
       float sc = 0.f;
       if constexpr (Q8 && KIND > 0) {
-        float m = 0.f;
+        float m = 0.f;  // (NaN from any of them stays, and the scale says so)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
 #pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int off = kLanes / 2; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
         sc = __fdiv_rn(m, 127.f);
       }
       if (j >= last) continue;

@@ -162,3 +162,45 @@ def test_quantized_subnormal_scales(A, size):
     t = (x / s[None, :, None]).astype(np.float64)
     want = np.clip(np.copysign(np.floor(np.abs(t) + 0.5), t), -127, 127)
     assert np.array_equal(k8.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("d,inter", [(128, False), (64, True)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_rows_with_nan_or_infinity_are_appended_as_such(A, d, inter, norm):
+    # an int8 row that holds a NaN or an infinity reads as NaN throughout: its scale is NaN or infinite and its codes
+    # are 0.  All other rows are as if there were none
+    n, h_q, h_kv = 40, 4, 2
+    q, k, v = normal(n, h_q, d, seed=5), normal(n, h_kv, d, seed=6), normal(n, h_kv, d, seed=7)
+    f = 1e4 ** (-np.arange(0, d // 2, 2) / (d // 2))
+    turns = A.rotation_table(torch.tensor(f)).cuda()
+    w = (1 + 0.3 * normal(d, seed=8).float()).to(torch.bfloat16) if norm else None
+
+    def append(k, v):
+        cache = P.build(A, [n], h_kv, d, 16, seed=9, int8=True)
+        A.rotate(A.RotateProblem(q, k, v, cache=cache, cu_tokens=i32(0, n), seen=i32(n), turns=turns, k_weight=w,
+                                 interleaved=inter))
+        return cache
+
+    clean = P.host(append(k, v))
+    bad = {0: [(3, 0, 1, NAN), (3, 1, d - 1, NAN), (9, 0, 0, INF), (10, 0, d - 2, -INF), (17, 1, 5, INF), (17, 1, 6, -INF),
+               (39, 1, d // 4, NAN), (39, 1, 2, INF)],
+           1: [(0, 0, 0, NAN), (3, 1, d - 1, INF), (8, 0, 63, -INF), (9, 1, 4, INF), (9, 1, 5, -INF), (38, 0, 2, NAN),
+               (38, 0, 9, -INF)]}
+    for x, at in ((k, bad[0]), (v, bad[1])):
+        for t, h, e, y in at:
+            x[t, h, e] = y
+    cache = append(k, v)
+    got = P.host(cache)
+    pg, r = O.slots(got, 0)
+    for name, x, at in (("k", k, bad[0]), ("v", v, bad[1])):
+        hit = np.zeros((n, h_kv), bool)
+        hit[[t for t, *_ in at], [h for _, h, *_ in at]] = True
+        codes, scale = got[name][pg, r], got[name + "_scale"][pg, :, r]
+        assert not np.isfinite(scale[hit]).any() and not codes[hit].any()
+        nan_in = np.isnan(x.float().cpu().numpy()).any(-1)
+        assert np.isnan(scale[nan_in]).all()
+        assert np.array_equal(codes[~hit], clean[name][pg, r][~hit])
+        assert np.array_equal(scale[~hit], clean[name + "_scale"][pg, :, r][~hit])
+    # and the attention over them does not hide them: keys' heads first (all of a head's queries), then values'
+    out = A.paged_decode(A.PagedDecodeProblem(q[:1], cache))
+    assert bool(torch.isnan(out).all())
