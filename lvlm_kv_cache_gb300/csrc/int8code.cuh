@@ -6,10 +6,15 @@
 
 namespace aircache {
 
-// The larger value, or NaN where one of them is (fmaxf would drop it).
+// The larger and the smaller value, or NaN where one of them is (fmaxf and fminf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b) {
   float m;
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(m) : "f"(a), "f"(b));
   return m;
 }
 
@@ -28,8 +33,7 @@ __device__ __forceinline__ int code(float x, float s, float rs) {
   const float t = x * rs;
   const float rt = rintf(t);
   if (!(fabsf(t - rt) <= 0.5f - 4e-5f)) {
-    const float q = roundf(__fdiv_rn(x, s));
-    return q == q ? (int)fminf(fmaxf(q, -127.f), 127.f) : 0;
+    return __float2int_rz(min_nan(max_nan(roundf(__fdiv_rn(x, s)), -127.f), 127.f));  // (of NaN: 0)
   }
   return (int)rt;
 }
