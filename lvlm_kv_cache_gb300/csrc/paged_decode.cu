@@ -462,35 +462,40 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         qa[kk][HB + b] = x.y;
       }
     }
-    float kmult = a.scale_log2;
-    if constexpr (Q8) {
-      // Q enters the f16 product times the power of two that puts the group's
-      // largest |q| in [2^14, 2^15): exact, and undone in the logit's multiplier
-      float mx = 0.f;
+    float kmult[HB];  // of head hA + 8b
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
+    for (int b = 0; b < HB; ++b) {
+      kmult[b] = a.scale_log2;
+      if constexpr (Q8) {
+        // Q enters the f16 product times the power of two that puts its head's largest |q| in
+        // [2^14, 2^15): exact, and undone in the logit's multiplier.  Each head by its own, so that none
+        // pushes another's values out of f16's range
+        float mx = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2 * HB; ++j) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
-          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int j = b; j < 2 * HB; j += HB) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
+            mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float qscale = 1.f;
+        if (mx > 0.f && mx < INFINITY) {
+          int ex;
+          (void)frexpf(mx, &ex);
+          qscale = ldexpf(1.f, min(15 - ex, 120));
         }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      float qscale = 1.f;
-      if (mx > 0.f && mx < INFINITY) {
-        int ex;
-        (void)frexpf(mx, &ex);
-        qscale = ldexpf(1.f, min(15 - ex, 120));
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int j = b; j < 2 * HB; j += HB) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
+            const __half2 hq = __floats2half2_rn(f.x * qscale, f.y * qscale);
+            qa[kk][j] = *reinterpret_cast<const uint32_t*>(&hq);
+          }
+        kmult[b] /= qscale;
       }
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-        for (int j = 0; j < 2 * HB; ++j) {
-          const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&qa[kk][j]));
-          const __half2 hq = __floats2half2_rn(f.x * qscale, f.y * qscale);
-          qa[kk][j] = *reinterpret_cast<const uint32_t*>(&hq);
-        }
-      kmult /= qscale;
     }
     // o[t][b]: columns 16t + hA and + 8 (rows of the product), heads 8b + 2cq and + 1
     float o[D / 16][HB][4];
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         uint8_t* kt = ring + st * C::kStageBytes + warp * C::kPiece;
         uint8_t* vt = kt + C::kTile;
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        float ks[4] = {1.f, 1.f, 1.f, 1.f}, lv[4] = {0.f, 0.f, 0.f, 0.f};  // rows 2cq, 2cq+1, 2cq+8, 2cq+9
+        float ks[HB][4], lv[4] = {0.f, 0.f, 0.f, 0.f};  // rows 2cq, 2cq+1, 2cq+8, 2cq+9
         auto qk = [&](int t, int kk, uint32_t b0, uint32_t b1) {
           const uint32_t af[4] = {qa[kk][0], HB == 2 ? qa[kk][1] : 0u, qa[kk][HB], HB == 2 ? qa[kk][3] : 0u};
           mma16816<Q8>(sc[t], af, b0, b1);
@@ -528,7 +533,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int row = 2 * cq + (j & 1) + 8 * (j >> 1);
-            ks[j] = kmult * sk[row];
+#pragma unroll
+            for (int b = 0; b < HB; ++b) ks[b][j] = kmult[b] * sk[row];
             lv[j] = row < valid ? __log2f(sk[kPdRows + row]) : 0.f;  // (past the end a scale may be anything)
           }
 #pragma unroll
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           for (int j = 0; j < 4; ++j) {
             float& x = sc[j >> 1][2 * b + (j & 1)];
             const bool in = 8 * (j >> 1) + 2 * cq + (j & 1) < valid;
-            x = in ? x * (Q8 ? ks[j] : kmult) : -INFINITY;
+            x = in ? x * (Q8 ? ks[b][j] : kmult[b]) : -INFINITY;
             top[b] = fmaxf(top[b], x);
             if (Q8) ytop[b] = fmaxf(ytop[b], x + lv[j]);
           }

@@ -204,3 +204,24 @@ def test_rows_with_nan_or_infinity_are_appended_as_such(A, d, inter, norm):
     # and the attention over them does not hide them: keys' heads first (all of a head's queries), then values'
     out = A.paged_decode(A.PagedDecodeProblem(q[:1], cache))
     assert bool(torch.isnan(out).all())
+
+
+@pytest.mark.parametrize("h_q,h_kv", [(7, 1), (16, 1)])
+@pytest.mark.parametrize("big", [2.0 ** 40, 2.0 ** 70, INF])
+def test_a_large_query_leaves_its_groups_others_alone(A, h_q, h_kv, big):
+    # int8 rows: queries enter the product in 16 bits, each head under a power of two of its own
+    for wide, cache, prob in D.both_ways(A, [70, 901], h_q, h_kv, 128, 16, 41, int8=True):
+        q = D.queries(2, h_q, 128, 42)
+        q[:, 1] *= 1e-3
+        small, before = q.clone(), P.host(cache)
+        q[:, 0] = INF if big == INF else q[:, 0] * big
+        small[:, 0] = 0.0
+        p = prob(q, lse=True, accumulate=big != INF)
+        A.paged_decode(p)
+        if big == INF:  # head 0 is NaN; the others' results by the definition
+            assert bool(torch.isnan(p.out[:, 0]).all())
+            p.out[:, 0] = torch.stack([x.mean(0) for x in (torch.tensor(O.rows(before, "v", s, 0)) for s in range(2))])
+            p.lse[:, 0] = torch.log(cache.lens.float())
+            D.verify(p, before, small)
+        else:
+            D.verify(p, before, q)
