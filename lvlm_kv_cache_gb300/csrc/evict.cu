@@ -20,6 +20,7 @@
 // move: CTAs over all SMs copy the listed rows, 32 moves to a warp at a time.
 // Bound by HBM.  Few rows are moved by the CTAs that selected them, in one kernel.
 #include <algorithm>
+#include <climits>
 
 #include "pages.cuh"
 
@@ -183,7 +184,11 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
   const bool cut = sane && n > keep;
   const int per = ((n + R - 1) / R + 15) & ~15;
   const int lo = min(rank * per, n), mine = min(per, n - lo);  // this CTA's rows
-  const int32_t fresh = a.recent ? seen - a.recent : 0x7fffffff;  // order from which rows are recent
+  // protected are orders under `first` and over `last`: of all where seen - recent is below int32, and without
+  // recent rows no order is over `last`
+  const bool all_recent = a.recent && seen <= INT_MIN + a.recent;
+  const int32_t first = all_recent ? INT_MAX : a.sink;
+  const int32_t last = !a.recent ? INT_MAX : all_recent ? INT_MAX - 1 : seen - a.recent - 1;
   const bool aged = a.sink | a.recent;
 
   // Where mass and order go to other arrays, every row below the new length is
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool in = i + j < mine;
-        key[j] = !in || (aged && (oo[j] < a.sink || oo[j] >= fresh)) ? kProtected : mass_key(mm[j]);
+        key[j] = !in || (aged && (oo[j] < first || oo[j] > last)) ? kProtected : mass_key(mm[j]);
         least = min(least, key[j]);
         most = max(most, key[j] + 1);  // (a protected row wraps to 0)
         safe += in && key[j] == kProtected;

@@ -225,3 +225,15 @@ def test_a_large_query_leaves_its_groups_others_alone(A, h_q, h_kv, big):
             D.verify(p, before, small)
         else:
             D.verify(p, before, q)
+
+
+def test_protected_orders_at_the_ends_of_int32(A):
+    import test_gpu_evict as E
+
+    # without recent rows no order is too new, the largest among them
+    cache = P.build(A, [300, 40], 2, 64, 16, seed=43)
+    cache.order[cache.order % 3 == 1] = 2 ** 31 - 1
+    E.check(A, cache, [100, 20], sink=2)
+    # seen - recent below int32: every order is at or behind it
+    cache = P.build(A, [300, 40], 2, 64, 16, seed=44)
+    E.check(A, cache, [100, 20], seen=[-(2 ** 31) + 3, 40], recent=7)
