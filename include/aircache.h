@@ -618,8 +618,9 @@ typedef struct aircache_pages {
  * rows do.  Without a cache cu_tokens may be NULL (no padding) and positions
  * must be given.
  * q_out may be q and k_out may be k (the same pointer and strides: in place);
- * otherwise outputs do not overlap inputs, nor their own rows (strides of at
- * least head_dim where there is more than one token or head).
+ * otherwise outputs do not overlap inputs, nor one another (the cache's k and v
+ * among them), nor their own rows (strides of at least head_dim where there is
+ * more than one token or head, and no token's row of a head on another's).
  *
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; head_dim
  * 64 or 128; at least one of q, k; q_out with q; k_out or pages with k; v

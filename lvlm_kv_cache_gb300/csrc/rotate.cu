@@ -399,12 +399,24 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
       (p->q_out && !strides(p->qo_stride_tok, p->qo_stride_head)) ||
       (p->k_out && !strides(p->ko_stride_tok, p->ko_stride_head)))
     return AIRCACHE_ERR_INVALID_ARG;
-  // rows of an output do not overlap
+  // rows of an output do not overlap: neither along a token's heads nor along the tokens, and where one axis does
+  // not lie within the other's step, no head's row meets an earlier head's of another token
   auto apart = [&](int64_t tok, int64_t head, int heads) {
-    return (p->num_tokens <= 1 || tok >= p->head_dim) && (heads <= 1 || head >= p->head_dim);
+    const int64_t d = p->head_dim, tokens = p->num_tokens;
+    if ((tokens > 1 && tok < d) || (heads > 1 && head < d)) return false;
+    if (tokens <= 1 || heads <= 1 || head <= (tok - d) / (heads - 1) || tok <= (head - d) / (tokens - 1)) return true;
+    for (int64_t h = 1; h < heads; ++h) {
+      const int64_t t = h * head / tok, past = h * head % tok;
+      if ((t < tokens && past < d) || (t + 1 < tokens && tok - past < d)) return false;
+    }
+    return true;
   };
   if ((p->q_out && !apart(p->qo_stride_tok, p->qo_stride_head, p->h_q)) ||
       (p->k_out && !apart(p->ko_stride_tok, p->ko_stride_head, p->h_kv)))
+    return AIRCACHE_ERR_INVALID_ARG;
+  // an output lies on no other input or output (k's and v's rows of the cache are outputs too)
+  if ((p->q_out && (p->q_out == p->k || p->q_out == p->v || p->q_out == p->k_out)) ||
+      (p->k_out && (p->k_out == p->q || p->k_out == p->v)) || (p->pages && p->pages->k == p->pages->v))
     return AIRCACHE_ERR_INVALID_ARG;
   // in place means the same rows, not shifted ones
   if ((p->q && p->q_out == p->q && (p->qo_stride_tok != p->q_stride_tok || p->qo_stride_head != p->q_stride_head)) ||

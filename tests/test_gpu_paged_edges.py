@@ -237,3 +237,15 @@ def test_protected_orders_at_the_ends_of_int32(A):
     # seen - recent below int32: every order is at or behind it
     cache = P.build(A, [300, 40], 2, 64, 16, seed=44)
     E.check(A, cache, [100, 20], seen=[-(2 ** 31) + 3, 40], recent=7)
+
+
+@pytest.mark.parametrize("T,h,tok,head", [(9, 5, 64, 9 * 64), (9, 5, 7 * 64, 64), (2, 2, 128, 192), (3, 2, 128, 5 * 64)])
+def test_outputs_of_any_layout_without_overlap(A, T, h, tok, head):
+    q = normal(T, h, 64, seed=57)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    turns = A.rotation_table([1e4 ** (-i / 64) for i in range(0, 64, 2)]).cuda()
+    want, _ = A.rotate(A.RotateProblem(q, positions=pos, turns=turns))
+    buf = torch.zeros(T * tok + h * head, dtype=torch.bfloat16, device="cuda")
+    out = buf.as_strided((T, h, 64), (tok, head, 1))
+    A.rotate(A.RotateProblem(q, q_out=out, positions=pos, turns=turns))
+    assert torch.equal(out, want)

@@ -32,3 +32,23 @@ def test_eviction_refuses_integers_off_their_alignment(A, field, by):
     p = T.evict(A, **{field: 0x1900000 + by})
     assert A.lib().aircache_evict(ctypes.byref(p), T.WS, 1 << 40, None) == A.ERR_INVALID_ARG
     assert A.lib().aircache_evict_workspace_size(ctypes.byref(p)) == 0
+
+
+# Ten tokens: of 28 query heads and 4 key heads of 128.  The first two lay rows of different tokens and heads onto one
+# another (token 1's head 0 on token 0's head 1; token 3's head 0 on token 0's head 2), the third by half a row.
+@pytest.mark.parametrize("over", [
+    dict(qo_stride_tok=128, qo_stride_head=128), dict(ko_stride_tok=256, ko_stride_head=384),
+    dict(qo_stride_tok=192, qo_stride_head=128), dict(ko_stride_tok=192, ko_stride_head=256)])
+def test_rotation_refuses_outputs_whose_own_rows_overlap(A, over):
+    assert A.lib().aircache_rotate(ctypes.byref(T.rotate(A, **over)), None, None) == A.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [
+    dict(q_out=0x1100000), dict(q_out=0x1200000), dict(k_out=0x1000000), dict(k_out=0x1200000), dict(q_out=0x1400000)])
+def test_rotation_refuses_outputs_on_other_inputs(A, over):
+    assert A.lib().aircache_rotate(ctypes.byref(T.rotate(A, **over)), None, None) == A.ERR_INVALID_ARG
+
+
+def test_rotation_refuses_keys_and_values_in_one_place(A):
+    p = T.rotate(A, T.pages(A, v=0x100000))
+    assert A.lib().aircache_rotate(ctypes.byref(p), None, None) == A.ERR_INVALID_ARG
