@@ -680,7 +680,7 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  * infinite key or value or a logit above the range makes what it meets NaN or
  * infinite.  out is bf16, lse fp32
  * dense [num_seqs][h_q]; mass_out is pages->mass itself (in place) or another
- * array of its shape, where only the slots of attended rows are written.
+ * array of its shape apart from it, where only the slots of attended rows are written.
  *
  * The work is split by rows, not by sequences: every CTA takes the same number
  * of 64-row tiles of the batch's (sequence, KV head) list, whatever the lengths,
@@ -735,7 +735,7 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  * ceil(lens_out[s] / page_rows) are the caller's again.
  *
  * mass_out and order_out are pages->mass and pages->order (in place) or other
- * arrays of their shape and alignment, which then get the entries of all rows below
+ * arrays of their shape and alignment apart from them, which then get the entries of all rows below
  * lens_out[s] and nothing else (of a sequence in error: some of its entries).
  * lens, keep and seen are read by every KV head, so lens_out must be an array
  * of its own (several layers are cut by the same lens before it takes

@@ -536,14 +536,22 @@ int ev_plan(const aircache_evict_problem* p, EvPlan& pl) {
   if (!p) return AIRCACHE_ERR_INVALID_ARG;
   const int rc = check_pages(p->pages, pl.pages);
   if (rc != AIRCACHE_OK) return rc;
-  if (!p->keep || !p->lens_out || p->lens_out == p->pages->lens || p->lens_out == p->keep ||
-      p->lens_out == p->seen || !p->pages->mass || !p->mass_out ||
+  if (!p->keep || !p->lens_out || !p->pages->mass || !p->mass_out ||
       (!p->order_out) != (!p->pages->order) || (reinterpret_cast<uintptr_t>(p->mass_out) & 15) != 0 ||
       (reinterpret_cast<uintptr_t>(p->order_out) & 15) != 0 || p->sink < 0 || p->recent < 0 ||
       ((p->sink || p->recent) && !p->pages->order) || (p->recent && !p->seen) || p->max_rows < 1)
     return AIRCACHE_ERR_INVALID_ARG;
   auto al4 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; };
   if (!al4(p->keep) || !al4(p->seen) || !al4(p->lens_out)) return AIRCACHE_ERR_INVALID_ARG;
+  // lens_out is an array of its own; mass_out and order_out are the cache's, or lie apart from them and each other
+  const size_t lens_bytes = 4 * (size_t)p->pages->num_seqs, slots = slot_bytes(pl.pages);
+  for (const int32_t* x : {p->pages->lens, p->keep, p->seen})
+    if (x == p->lens_out || arrays_meet(p->lens_out, lens_bytes, x, lens_bytes)) return AIRCACHE_ERR_INVALID_ARG;
+  auto meet = [&](const void* x, const void* y) { return arrays_meet(x, slots, y, slots); };
+  if ((p->mass_out != p->pages->mass && meet(p->mass_out, p->pages->mass)) ||
+      (p->order_out != p->pages->order && meet(p->order_out, p->pages->order)) || meet(p->mass_out, p->order_out) ||
+      meet(p->mass_out, p->pages->order) || meet(p->pages->mass, p->order_out))
+    return AIRCACHE_ERR_INVALID_ARG;
   if (p->max_rows > AIRCACHE_MAX_EVICT_ROWS) return AIRCACHE_ERR_UNSUPPORTED;
   pl.sms = device_sms();
   const int64_t units = (int64_t)p->pages->num_seqs * p->pages->h_kv;

@@ -1096,6 +1096,8 @@ int pd_plan(const aircache_paged_decode_problem* p, PdPlan& pl) {
       !(p->scale > 0.f) || !std::isfinite(1.4427f * p->scale) || p->total_rows < 1 || p->total_rows > 0x7fff0000LL || !p->q ||
       !p->out || !al16(p->q) || !al16(p->out) || p->q_stride_seq < 0 || p->q_stride_head < 0 ||
       p->q_stride_seq % 8 != 0 || p->q_stride_head % 8 != 0 || (p->mass_out && !p->pages->mass) ||
+      (p->mass_out != p->pages->mass &&
+       arrays_meet(p->mass_out, slot_bytes(pl.pages), p->pages->mass, slot_bytes(pl.pages))) ||
       (reinterpret_cast<uintptr_t>(p->lse) & 3) != 0 || !al16(p->mass_out))
     return AIRCACHE_ERR_INVALID_ARG;
   pl.g = p->h_q / p->pages->h_kv;

@@ -85,4 +85,12 @@ inline int check_pages(const aircache_pages* p, Pages& d) {
   return AIRCACHE_OK;
 }
 
+// Host: whether two arrays of `bytes` and `other` bytes share any.
+inline bool arrays_meet(const void* x, size_t bytes, const void* y, size_t other) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return x && y && a < b + other && b < a + bytes;
+}
+// Host: the bytes of an array of the mass's and the order's shape.
+inline size_t slot_bytes(const Pages& p) { return 4 * (size_t)p.num_pages * p.h_kv * p.page_rows; }
+
 }  // namespace aircache
