@@ -926,7 +926,8 @@ class EvictProblem:
     cache.lens itself; seen: int32 [S], tokens appended so far (needed with
     recent); sink, recent: the first and the newest tokens, always kept;
     mass_out, order_out: other arrays than the cache's (None: in place);
-    max_rows: a bound of cache.lens (0: the table's capacity)."""
+    max_rows: a bound of cache.lens (0: the table's capacity, or the longest that
+    an eviction takes, MAX_EVICT_ROWS, if it is less)."""
 
     def __init__(self, cache, keep, lens_out, seen=None, sink=0, recent=0, mass_out=None, order_out=None, max_rows=0):
         S = cache.num_seqs
@@ -947,7 +948,7 @@ class EvictProblem:
         self.c = EvictProblemStruct(
             pages=ctypes.pointer(cache.c), keep=adr(keep), seen=adr(seen), lens_out=adr(lens_out),
             mass_out=adr(mass_out), order_out=adr(order_out), sink=int(sink), recent=int(recent),
-            max_rows=int(max_rows) or cache.max_pages * cache.page_rows)
+            max_rows=int(max_rows) or min(cache.max_pages * cache.page_rows, MAX_EVICT_ROWS))
         self.ref = ctypes.byref(self.c)
 
     def workspace_size(self) -> int:

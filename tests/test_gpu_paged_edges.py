@@ -249,3 +249,15 @@ def test_outputs_of_any_layout_without_overlap(A, T, h, tok, head):
     out = buf.as_strided((T, h, 64), (tok, head, 1))
     A.rotate(A.RotateProblem(q, q_out=out, positions=pos, turns=turns))
     assert torch.equal(out, want)
+
+
+def test_eviction_without_a_bound_takes_tables_of_any_width(A):
+    # 30,000 pages of 16 rows to a sequence: more than the longest eviction, though none is that long
+    lens = [100, 60]
+    tight, wide = (P.build(A, lens, 2, 64, 16, seed=47, max_pages=m) for m in (7, 30000))
+    outs = []
+    for cache in (tight, wide):
+        prob = A.EvictProblem(cache, i32(50, 30), i32(0, 0), seen=i32(*lens), sink=1, recent=4)
+        outs.append(A.evict(prob).tolist())
+    assert outs == [[50, 30]] * 2
+    P.assert_same_state(P.state(tight), P.state(wide))
