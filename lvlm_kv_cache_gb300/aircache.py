@@ -894,8 +894,8 @@ class PagedDecodeProblem:
             return 256
         with torch.cuda.device(self.device):
             n = lib().aircache_paged_decode_workspace_size(self.ref)
-        if n == 0:
-            raise AirCacheError(ERR_INVALID_ARG, "aircache_paged_decode_workspace_size")
+            if n == 0:  # (the call itself names the reason, before it looks at a workspace)
+                raise AirCacheError(lib().aircache_paged_decode(self.ref, None, 0, None), "aircache_paged_decode_workspace_size")
         return int(n)
 
     def new_workspace(self) -> torch.Tensor:
@@ -956,8 +956,8 @@ class EvictProblem:
             return 256
         with torch.cuda.device(self.device):
             n = lib().aircache_evict_workspace_size(self.ref)
-        if n == 0:
-            raise AirCacheError(ERR_INVALID_ARG, "aircache_evict_workspace_size")
+            if n == 0:  # (the call itself names the reason, before it looks at a workspace)
+                raise AirCacheError(lib().aircache_evict(self.ref, None, 0, None), "aircache_evict_workspace_size")
         return int(n)
 
     def new_workspace(self) -> torch.Tensor:

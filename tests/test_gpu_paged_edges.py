@@ -261,3 +261,16 @@ def test_eviction_without_a_bound_takes_tables_of_any_width(A):
         outs.append(A.evict(prob).tolist())
     assert outs == [[50, 30]] * 2
     P.assert_same_state(P.state(tight), P.state(wide))
+
+
+def test_sizes_of_refused_problems_name_the_reason(A):
+    cache = P.build(A, [100], 2, 64, 16, seed=48)
+    with pytest.raises(A.AirCacheError) as e:
+        A.EvictProblem(cache, i32(50), i32(0), max_rows=A.MAX_EVICT_ROWS + 1).workspace_size()
+    assert e.value.status == A.ERR_UNSUPPORTED
+    with pytest.raises(A.AirCacheError) as e:
+        A.PagedDecodeProblem(normal(1, 2 * 17, 64), cache).workspace_size()
+    assert e.value.status == A.ERR_UNSUPPORTED
+    with pytest.raises(A.AirCacheError) as e:
+        A.EvictProblem(cache, i32(50), i32(0), sink=-1).workspace_size()
+    assert e.value.status == A.ERR_INVALID_ARG
