@@ -885,7 +885,7 @@ class PagedDecodeProblem:
         adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self.c = PagedDecodeProblemStruct(
             pages=ctypes.pointer(cache.c), h_q=h_q, dtype=BF16, scale=float(d ** -0.5 if scale is None else scale),
-            reserved0=0, total_rows=max(1, int(total_rows)), q=adr(q), q_stride_seq=q.stride(0),
+            reserved0=0, total_rows=int(total_rows), q=adr(q), q_stride_seq=q.stride(0),
             q_stride_head=q.stride(1), out=adr(out), lse=adr(lse), mass_out=adr(mass_out))
         self.ref = ctypes.byref(self.c)
 

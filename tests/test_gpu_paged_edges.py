@@ -274,3 +274,11 @@ def test_sizes_of_refused_problems_name_the_reason(A):
     with pytest.raises(A.AirCacheError) as e:
         A.EvictProblem(cache, i32(50), i32(0), sink=-1).workspace_size()
     assert e.value.status == A.ERR_INVALID_ARG
+
+
+def test_a_negative_bound_of_the_rows_is_refused(A):
+    cache = P.build(A, [100], 2, 64, 16, seed=49)
+    q = normal(1, 4, 64, seed=50)
+    with pytest.raises(A.AirCacheError) as e:
+        A.paged_decode(A.PagedDecodeProblem(q, cache, total_rows=-5), check=False)
+    assert e.value.status == A.ERR_INVALID_ARG
