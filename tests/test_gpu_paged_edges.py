@@ -282,3 +282,28 @@ def test_a_negative_bound_of_the_rows_is_refused(A):
     with pytest.raises(A.AirCacheError) as e:
         A.paged_decode(A.PagedDecodeProblem(q, cache, total_rows=-5), check=False)
     assert e.value.status == A.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("what", ["mass", "moves"])
+def test_smoke_sees_a_wrong_mass_and_wrong_moves(A, monkeypatch, what):
+    import __graft_entry__ as g
+
+    if what == "mass":
+        right = O.decode
+
+        def decode(q, c, scale):
+            out, lse, w, size, spread = right(q, c, scale)
+            w[1][0, 3] += 1e-3  # one row of one KV head
+            return out, lse, w, size, spread
+
+        monkeypatch.setattr(O, "decode", decode)
+    else:
+        rule = O.evict_moves
+
+        def moves(*a):  # the last move's row goes one further
+            kept, to = rule(*a)
+            return kept, to[:-1] + [(to[-1][0], to[-1][1] + 1)]
+
+        monkeypatch.setattr(O, "evict_moves", moves)
+    with pytest.raises(AssertionError):
+        g.smoke()
