@@ -678,7 +678,10 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  * A sequence without rows gets out = 0 and lse = -inf, and so does a query all
  * of whose logits lie below fp32's range (single ones weigh nothing); a NaN, an
  * infinite key or value or a logit above the range makes what it meets NaN or
- * infinite.  out is bf16, lse fp32
+ * infinite.  Logits, sums, lse and mass are fp32.  The weights that meet V are
+ * held in 16 bits (a sum of two bf16) for bf16 rows and in 11 (one f16, with the
+ * value's scale) for int8 rows, so that out may differ in its last bit from a
+ * form that holds 24.  out is bf16, lse fp32
  * dense [num_seqs][h_q]; mass_out is pages->mass itself (in place) or another
  * array of its shape apart from it, where only the slots of attended rows are written.
  *
@@ -703,7 +706,8 @@ AIRCACHE_API int aircache_rotate(const aircache_rotate_problem* p, int32_t* stat
  *
  * The workspace is caller-owned, 256-byte aligned, ZEROED ONCE before its first
  * use and left ready for the next call, as aircache_decode's; a device error
- * stays recorded until the caller zeroes it.
+ * stays recorded until the caller zeroes it.  Calls that may run at the same
+ * time (on two streams, or in two graphs replayed at once) need one each.
  */
 typedef struct aircache_paged_decode_problem {
     const aircache_pages* pages;  /* HOST */
@@ -731,7 +735,10 @@ AIRCACHE_API int aircache_paged_decode(const aircache_paged_decode_problem* p, v
  * ties to the lower row (a NaN counts as -inf).  Kept rows that lie at keep[s]
  * or behind move, in ascending order, into the vacated rows below keep[s], in
  * ascending order, and take their scales, mass and order along; every other
- * row stays where it is, so as few bytes as possible move.  lens_out[s] = min(n, keep[s]); pages past
+ * row stays where it is, so as few bytes as possible move.  (aircache_rotate
+ * appends rows with mass 0, and only aircache_paged_decode adds to it: before an
+ * eviction right after a prompt the caller fills mass, or all unprotected rows
+ * tie and the lowest stay.)  lens_out[s] = min(n, keep[s]); pages past
  * ceil(lens_out[s] / page_rows) are the caller's again.
  *
  * mass_out and order_out are pages->mass and pages->order (in place) or other

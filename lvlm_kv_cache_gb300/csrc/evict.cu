@@ -33,9 +33,8 @@ constexpr int kEvMaxCluster = 8;
 constexpr int kMvThreads = 256, kMvCtas = 4;  // of the moves: threads of a CTA, CTAs to an SM
 constexpr int kEvSlice = AIRCACHE_MAX_EVICT_ROWS / kEvMaxCluster;  // keys of one CTA, at most
 // Rows of one CTA, at most, for it to move them too, in one kernel; twice as many where it has a (sequence, KV
-// head) for itself (one of 1,088: 7.2 us, and 8.3 with the second kernel; 8 x 4,000, in clusters of 2:
-// 18.4 and 21.1; 48 x 4,000 int8: 29.8 and 34.2; but 16 x 8,000, in clusters of 2: 36.2 and 33.8, and 48 of up
-// to 9,000 int8: 39.8 and 38.4)
+// head) for itself (with the second kernel one of 1,088 takes 15 % longer, 8 x 4,000, in clusters of 2, 15 %, 48 x
+// 4,000 int8 15 %; but 16 x 8,000, in clusters of 2, 7 % less, and 48 of up to 9,000 int8 4 % less)
 constexpr int kEvShort = 2048;
 constexpr int kEvHeader = 256;                                     // workspace: error word
 constexpr uint32_t kProtected = 0xffffffffu;
@@ -88,8 +87,8 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 
 // RB: 16-byte pieces of a row of one KV head.  What a warp waits for is hidden
 // by other warps, so few registers count for more than many loads of one warp
-// (16 x 16k to half: 73 us with eight row loads in flight and 24 warps to an SM,
-// 61 with four and 32), and nothing is stored before every load of the 32 moves' scales, mass
+// (16 x 16k to half: 61 us with four row loads in flight and 32 warps to an SM,
+// 73 with eight and 24), and nothing is stored before every load of the 32 moves' scales, mass
 // and order and the first rows' has been issued.
 template <int RB>
 __device__ __forceinline__ void move_rows(const EvArgs& a, int s, int h, int moves, int first, int warps) {
@@ -147,7 +146,7 @@ __device__ __forceinline__ void move_rows(const EvArgs& a, int s, int h, int mov
 // by one lane per CTA at once, or by loads that do not wait for one another: a
 // load from another CTA's shared memory takes several hundred cycles.  F groups of four rows
 // load at once in a thread: eight with one CTA to an SM, four (and half the registers) with two
-// (2 x 128k with 8 and 4: 47 and 52 us; ragged, 192 CTAs: 42 and 39.5).
+// (2 x 128k: 46 us, 10 % longer with four; ragged, 192 CTAs: 39 us, 6 % longer with eight).
 // RB: the CTA also moves the rows (0: another kernel does).
 template <int R, int F, int RB>
 __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kernel(const __grid_constant__ EvArgs a) {

@@ -28,7 +28,7 @@
 // Short sequences need neither the list nor the second kernel: a cluster of one to
 // eight CTAs takes a (sequence, KV head), an equal part of its tiles each, and they
 // join their parts, form the log-sum-exps and add to the mass themselves, through
-// each other's shared memory (one of 701 rows: 7.0 us, 8.9 by the list).
+// each other's shared memory (one of 701 rows: 7.2 us, a quarter longer by the list).
 //
 // int8 rows carry a scale each.  The key's multiplies the logit.  The value's
 // joins the weight before it is rounded to f16: the weights of O are
@@ -38,14 +38,16 @@
 //
 // The product with V takes 16-bit weights: bf16 ones as a sum of two (what
 // rounding takes away goes through a second product, which costs no time beside
-// the bytes: 16 x 16k 103.6 us with and without), f16 ones (int8 rows) rounded
-// once, to 2^-12.  Maximum, sum, O and the joins are fp32, and out is rounded
+// the bytes), f16 ones (int8 rows) rounded once, to 2^-12, because these rows are
+// bound by instructions and a second product is more of them.  Maximum, sum, O and the joins are fp32, and out is rounded
 // once, to bf16.
 //
 // Measured (28 query and 4 KV heads of 128, calls back to back): 16 x 16,384
-// bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 us; 8 x 32,768 int8 rows 64 us
-// (277 MB); 32 heads of 64 over 55,113 rows 76 us (452 MB, 5.9 TB/s); one
-// sequence of 8,192 rows 11.1 us, of 131,072 49 us; of 701, in one launch, 7.0 us.
+// bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 to 105 us; 8 x 32,768 int8 rows
+// 65 us (277 MB), with mass 75; 32 heads of 64 over 55,113 rows 74 to 88 us (452 MB,
+// 5.1 to 6.1 TB/s: it goes by the box and by where the tensors lie); one sequence of
+// 8,192 rows 11 us, of 131,072 49 us; of 701, in one launch, 7.2 us; 16 x 16,384 of
+// one KV head to 16 query heads 33 us, int8 30.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -116,7 +118,7 @@ struct PdArgs {
 };
 
 // Keys and values pass through L2 once: they are to go first, so that the stored logits stay for the
-// mass (16 x 16k with mass: 107.5 us without the policy, 104.6 with; 64-wide heads: 80.6 and 76.5).
+// mass (without the policy 16 x 16k with mass takes 3 % longer, 64-wide heads 5 %).
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int a, int b, int c, int d, int e,
                                             uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -138,7 +140,7 @@ __device__ __forceinline__ int rows_of(const Pages& p, int s) {
 // falls to (merging the warps, writing, joining, the next queries).  CTA c
 // takes the places c * per .. c * per + per - 1, so the parts of a unit go to
 // consecutive CTAs and only its first and its last run can be a part.  (48 ragged
-// sequences with mass: 94 us with 4 places, 101 with none, 96 with 2 or 16.)
+// sequences with mass: 7 % longer than with 4 places with none, 2 % with 2 or 16.)
 constexpr uint32_t kPdEnd = 4;
 
 // A run of tiles of one unit: what a CTA does at a time.
@@ -943,12 +945,12 @@ __device__ __forceinline__ void write_joined(const PdArgs& a, const Joined& r, i
 // Of up to kPfMany parts: a unit to a CTA, a thread to all parts of its four
 // columns, one round trip or two.  Of more (few units, then): a query head to a
 // CTA, whose threads also share the parts (one sequence of 8,192 rows, 76 parts
-// to a KV head: 11.1 us for the step, 18.1 with a thread to all parts; 48
+// to a KV head: 11 us for the step, 18 with a thread to all parts; 48
 // sequences of 2,000: 30 us, 35 with a head to a CTA).
 // MASS: also turns the stored logits into weights and adds them to the rows'
 // mass: a warp takes a run of tiles, a lane two rows of each; it forms its unit's
 // log-sum-exps from the parts itself, which costs less than a third launch that
-// waits for the join (16 x 16k: 103 us, and 107 with that launch).
+// waits for the join (16 x 16k: 4 % longer with that launch).
 constexpr int kPfThreads = 256;
 constexpr int kPfMany = 16;
 constexpr int kPfHeads = 16;  // heads of units in many parts that one CTA looks at

@@ -13,8 +13,9 @@
 // the slot in the cache is looked up once.  Both elements of a pair lie in one
 // lane (half style: four elements and the four half a rotation further), so a
 // row costs no shuffles but the norm's.  With few tokens a token's heads go to
-// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 2.7 us; 15,541 of them, the
-// keys also dense, in 52 us (303 MB read and written, 5.8 TB/s).
+// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 2.7 us within a graph (a call by
+// itself takes the host 3.9); 15,541 of them, the keys also dense, in 53 us (303 MB read and
+// written, 5.8 TB/s), and into an int8 cache, without those, in 61.
 //
 // The angle: position * (hi + lo) turns is reduced before it is rounded.  The
 // position splits into two parts of at most 20 bits (exact in fp32), each
@@ -30,15 +31,15 @@
 namespace aircache {
 namespace {
 
-// A CTA is one warp: the next token starts as soon as one is done (15,541 tokens: 53.7 us, and 56.9
-// with four warps to a CTA, 56.4 with two).
+// A CTA is one warp: the next token starts as soon as one is done (15,541 tokens: 6 % longer with
+// four warps to a CTA, 5 % with two).
 // NB: rows a lane group works on at a time, while as many load.  Two, with 32 warps
-// to an SM (15,541 tokens of 28 + 4 heads of 128: 53.7 us, and 61.3 with four); four, with 24 warps,
+// to an SM (15,541 tokens of 28 + 4 heads of 128: 14 % longer with four); four, with 24 warps,
 // where whole tokens do not fill those, so that a warp has to keep more loads of its own in flight
-// (3,447 tokens of 32 + 32 heads of 64: 17.1 us, and 19.2 with two).
+// (3,447 tokens of 32 + 32 heads of 64: 12 % longer with two).
 constexpr int kRotMany = 32, kRotFew = 24;  // warps to an SM
 // (The bounds on the kernels' registers: as 32 CTAs of 32 threads for NB = 2 and, though it is launched
-// with 32 threads, as 6 of 128 for NB = 4; the other way round 55.6 and 18.2 us.)
+// with 32 threads, as 6 of 128 for NB = 4; the other way round 4 and 6 % longer.)
 
 struct RotArgs {
   const __nv_bfloat16* src[3];  // q, k, v
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotF
     load_rows<D, false>(r, from, a.src_head[kind], first - kind0, from_end, x.e0, x.e1, lane);
 
   // ---- the token's positions, sequence, order and slot.  What is loaded here is used as late as
-  // may be, the place in the cache behind the queries (15,541 tokens: 53.5 us with each lookup waited for)
+  // may be, the place in the cache behind the queries (15,541 tokens: 2.5 % longer with each lookup waited for)
   constexpr int kMine = 4 * kLanes / 32;
   const int grp = lane / kLanes;
   const bool turns = x.turned && first < a.h_q + a.h_kv;
@@ -465,9 +466,10 @@ extern "C" int aircache_rotate(const aircache_rotate_problem* p, int32_t* status
   a.eps = p->eps;
   // How many warps share a token's heads.  A warp's time is about that of its rows' steps and three
   // more (the token's place and angles), the SMs hold kRotMany warps at once, and starting
-  // them takes a step for every ten to an SM.  (5,000 tokens of 32 + 32 heads of 64: 29 us with one
-  // warp to a token, 26 with the two that this gives, 24 with three; 3,000 of 32 + 32 heads of
-  // 128: 34, and 28 with its three; 200 of 28 + 4: 7.0, and 4.4 with its nine)
+  // them takes a step for every ten to an SM: a rough model, which need not find the best number.  (5,000
+  // tokens of 32 + 32 heads of 64: 29 us with one warp to a token and 26 with the two that it gives, though
+  // 24 with three; 3,000 of 32 + 32 heads of 128: 34, and 28 with its three; 200 of 28 + 4: 7.0, and 4.4
+  // with its nine)
   const int sms = device_sms();
   const int at_once = p->head_dim == 128 ? 2 : 4;
   const int steps = (a.heads + at_once - 1) / at_once;
