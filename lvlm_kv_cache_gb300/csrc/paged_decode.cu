@@ -306,12 +306,6 @@ __device__ __forceinline__ Share make_unit(const PdArgs& a, ShareScratch* sc) {
   return sh;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // SHORT: a cluster to a unit, and no second kernel.
 template <int D, bool Q8, int HB, bool SHORT>
 __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
