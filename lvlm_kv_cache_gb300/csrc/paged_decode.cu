@@ -45,7 +45,7 @@
 // Measured (28 query and 4 KV heads of 128, calls back to back): 16 x 16,384
 // bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 to 105 us; 8 x 32,768 int8 rows
 // 65 us (277 MB), with mass 75; 32 heads of 64 over 55,113 rows 74 to 88 us (452 MB,
-// 5.1 to 6.1 TB/s: it goes by the box and by where the tensors lie); one sequence of
+// 5.1 to 6.1 TB/s, by the machine); one sequence of
 // 8,192 rows 11 us, of 131,072 49 us; of 701, in one launch, 7.2 us; 16 x 16,384 of
 // one KV head to 16 query heads 33 us, int8 30.
 #include <cuda_bf16.h>
