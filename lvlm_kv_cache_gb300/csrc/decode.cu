@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
   const int split = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
   const int g = a.group;
 
-  pdl_trigger();  // the next kernel on the stream may launch; it waits for this one before using its output
   if (warp == kDecWarps && lane == 0) {
     // ---- producer lane: this CTA's slice of the sequence's rows, then the
     // first tiles right away (the queries load meanwhile)
@@ -205,6 +204,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
   // kernel on the stream is done: it may have written q; everything below
   // comes after this wait in every thread but the producer's early reads)
   pdl_wait();
+  pdl_trigger();
   for (int c = tid; c < kDecMaxGroup * (D / 8); c += kDecThreads) {
     const int hh = c / (D / 8), ch = c % (D / 8);
     uint4 val = make_uint4(0, 0, 0, 0);

@@ -164,11 +164,11 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
       __syncthreads();
   };
   auto peer = [&](const uint32_t* x, int r) { return CL ? ld_cluster_u32(cluster_map(smem_u32(x), r)) : *x; };
-  pdl_trigger();
   for (int i = tid; i < 4 * kBins; i += kEvThreads) (&sh.hist[0][0])[i] = 0;
   if (tid == 0) sh.bad = 0;
   __syncthreads();
   pdl_wait();
+  pdl_trigger();
 
   // the table's row comes to L1 while the length is waited for
   const int32_t* table = p.table + (int64_t)s * p.table_stride;
@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(kEvThreads, F == 4 ? 2 : 1) evict_select_kerne
 
 template <int RB>
 __global__ void __launch_bounds__(kMvThreads, kMvCtas) evict_move_kernel(const __grid_constant__ EvArgs a) {
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int h = blockIdx.y, s = blockIdx.z;
   const int moves = a.moves[(int64_t)s * a.pages.h_kv + h];
   move_rows<RB>(a, s, h, moves, blockIdx.x * (kMvThreads / 32) + (threadIdx.x >> 5), gridDim.x * (kMvThreads / 32));

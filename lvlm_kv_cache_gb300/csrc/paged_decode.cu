@@ -327,7 +327,6 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = a.group;
   const Pages& p = a.pages;
-  pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -340,6 +339,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
   pdl_wait();
+  pdl_trigger();
   const Share sh = SHORT ? make_unit(a, share) : make_share(a, share);  // (its barriers publish the mbarriers too)
   if (!SHORT && blockIdx.x == 0 && tid == 0) *a.tiles = max(sh.tiles, 0);
   Run r = sh.run;
@@ -954,8 +954,8 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
   constexpr int kCols = D / 4, kGroups = kPfThreads / kCols;
   __shared__ float4 part_o[kGroups][kCols];
   __shared__ float3 part_ml[kGroups];
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const Pages& p = a.pages;
   const int tid = threadIdx.x, lane = tid & 31, g = a.group;
   // this warp's tiles of the mass: the first one's logits and place come to L1 while the join is dealt out

@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(NB == 2 ? 32 : 128, NB == 2 ? kRotMany : kRotF
   const int lane = threadIdx.x, l = lane % kLanes;
   const int64_t w = blockIdx.x;
   const int64_t t = w / a.shares;  // neighbouring warps share a token's heads
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();
   const int first = (int)(w % a.shares) * a.per, last = min(first + a.per, a.heads);
   const int q_end = min(last, a.h_q), k_end = min(last, a.h_q + a.h_kv);
 

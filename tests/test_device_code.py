@@ -56,3 +56,15 @@ def test_host_code_keeps_nothing_that_two_threads_could_set_at_once():
     for name in sorted(os.listdir(CSRC)):
         found = re.findall(plain, source(name), re.M)
         assert not found or guarded.get(name, "nothing") in source(name), (name, found)
+
+
+def test_kernels_let_the_next_one_start_behind_their_own_wait():
+    # a decode with AIRCACHE_DECODE_EARLY_CACHE reads its rows when the kernel before it lets it start: that kernel's
+    # predecessors, which may write the rows, have then to be complete
+    for name in ("rotate.cu", "paged_decode.cu", "evict.cu", "decode.cu"):
+        text = source(name)
+        kernels = text.split("__global__")[1:]
+        assert kernels, name
+        for k in kernels:
+            if "pdl_trigger();" in k:
+                assert -1 < k.rindex("pdl_wait();") < k.index("pdl_trigger();"), name

@@ -307,3 +307,47 @@ def test_smoke_sees_a_wrong_mass_and_wrong_moves(A, monkeypatch, what):
         monkeypatch.setattr(O, "evict_moves", moves)
     with pytest.raises(AssertionError):
         g.smoke()
+
+
+def test_early_decode_behind_a_kernel_that_does_not_write_its_rows(A):
+    # two layers' rows are rotated into dense arenas; the kernel just before each early decode writes neither its
+    # ranges nor its rows: a rotation of queries, and the decode of the layer before
+    n, h, d = 20000, 4, 128
+    ks, vs = (normal(2, n, h, d, seed=60 + i) for i in range(2))
+    q = normal(2, 28, d, seed=62)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    turns = A.rotation_table([1e4 ** (-i / d) for i in range(0, d, 2)]).cuda()
+    arena, q_rot = torch.zeros_like(ks), torch.zeros_like(q)
+    offs = torch.tensor([0, 500, n], device="cuda")
+    write = [A.RotateProblem(None, ks[i], k_out=arena[i], positions=pos, turns=turns) for i in range(2)]
+    turn_q = A.RotateProblem(q, q_out=q_rot, positions=i32(499, n - 1), turns=turns)
+    steps = [A.DecodeProblem(q_rot, arena[i], vs[i], offsets=offs, early_cache=True) for i in range(2)]
+    ws = [p.new_workspace() for p in steps]
+
+    def run(apart):
+        arena.zero_()
+        q_rot.zero_()
+        torch.cuda.synchronize()
+        for call in (lambda: A.aircache_rotate(write[0]), lambda: A.aircache_rotate(write[1]),
+                     lambda: A.aircache_rotate(turn_q), lambda: A.aircache_decode(steps[0], ws[0]),
+                     lambda: A.aircache_decode(steps[1], ws[1])):
+            call()
+            if apart:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [p.out.clone() for p in steps]
+
+    want = run(True)
+    for _ in range(20):
+        got = run(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # the rows of layer 1 are written while layer 0 is decoded
+    A.aircache_rotate(turn_q)
+    for _ in range(20):
+        arena[1].zero_()
+        torch.cuda.synchronize()
+        A.aircache_rotate(write[1])
+        A.aircache_decode(steps[0], ws[0])
+        A.aircache_decode(steps[1], ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(steps[1].out, want[1])
