@@ -28,7 +28,7 @@
 // Short sequences need neither the list nor the second kernel: a cluster of one to
 // eight CTAs takes a (sequence, KV head), an equal part of its tiles each, and they
 // join their parts, form the log-sum-exps and add to the mass themselves, through
-// each other's shared memory (one of 701 rows: 7.2 us, a quarter longer by the list).
+// each other's shared memory (one of 701 rows: 7.3 us, a quarter longer by the list).
 //
 // int8 rows carry a scale each.  The key's multiplies the logit.  The value's
 // joins the weight before it is rounded to f16: the weights of O are
@@ -46,7 +46,7 @@
 // bf16 rows 87 us (537 MB, 6.2 TB/s), with mass 102 to 105 us; 8 x 32,768 int8 rows
 // 65 us (277 MB), with mass 75; 32 heads of 64 over 55,113 rows 74 to 88 us (452 MB,
 // 5.1 to 6.1 TB/s, by the machine); one sequence of
-// 8,192 rows 11 us, of 131,072 49 us; of 701, in one launch, 7.2 us; 16 x 16,384 of
+// 8,192 rows 11 us, of 131,072 49 us; of 701, in one launch, 7.3 us; 16 x 16,384 of
 // one KV head to 16 query heads 33 us, int8 30.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

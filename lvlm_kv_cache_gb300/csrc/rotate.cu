@@ -13,7 +13,7 @@
 // the slot in the cache is looked up once.  Both elements of a pair lie in one
 // lane (half style: four elements and the four half a rotation further), so a
 // row costs no shuffles but the norm's.  With few tokens a token's heads go to
-// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 2.7 us within a graph (a call by
+// several warps.  Measured: 8 tokens of 28 + 4 heads of 128 in 2.8 us within a graph (a call by
 // itself takes the host 3.9); 15,541 of them, the keys also dense, in 53 us (303 MB read and
 // written, 5.8 TB/s), and into an int8 cache, without those, in 61.
 //
