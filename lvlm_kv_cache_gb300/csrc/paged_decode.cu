@@ -373,6 +373,16 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           if (!mbar_wait_warp(&empty[st], phase ^ 1)) {
             set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
             alive = false;
+            if (!SHORT && a.mass_out) {
+              // the tiles from here on are not there: the mass kernel would find another call's pages in their place
+              do {
+                for (; i < r.count; ++i) {
+                  if (lane < 4) a.info[r.at + i].page[lane] = -1;
+                  if (lane == 4) *reinterpret_cast<int4*>(&a.info[r.at + i]) = make_int4(r.s, r.h, r.first + i, 0);
+                }
+                i = 0;
+              } while (next_run(p, r, sh.lo, sh.hi));
+            }
             break;
           }
         }

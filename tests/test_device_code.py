@@ -68,3 +68,12 @@ def test_kernels_let_the_next_one_start_behind_their_own_wait():
         for k in kernels:
             if "pdl_trigger();" in k:
                 assert -1 < k.rindex("pdl_wait();") < k.index("pdl_trigger();"), name
+
+
+def test_every_tile_of_the_paged_decode_is_noted():
+    # the mass kernel takes each tile's pages from the workspace: a producer whose wait ran out notes the tiles that it
+    # does not copy as not there, or another call's pages would be found in their place
+    producer = body(source("paged_decode.cu"), "if (warp == kPdWarps) {")
+    gave_up = body(producer, "if (!mbar_wait_warp(&empty")
+    assert ".page[lane] = -1;" in gave_up and "while (next_run(" in gave_up
+    assert producer.count("break;") == gave_up.count("break;") == 1
