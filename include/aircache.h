@@ -775,6 +775,72 @@ typedef struct aircache_evict_problem {
 AIRCACHE_API size_t aircache_evict_workspace_size(const aircache_evict_problem* p);
 AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Attention of several query tokens of each sequence over its paged rows: new
+ * tokens that continue a cached sequence (a question behind a cached image
+ * prompt, a chunk of a prompt, drafted tokens), and text tokens over an
+ * encoder's states (cross attention; the states appended by aircache_rotate
+ * with rotary_dim 0).  For token t, the i-th of the n tokens of sequence s, query
+ * head h (KV head h / (h_q / h_kv)) and the rows j < lens[s] that it sees
+ *   out[t][h] = sum_j w_j v_j,  w_j = softmax_j(scale * q[t][h] . k_j)
+ *   lse[t][h] = log sum_j exp(scale * q[t][h] . k_j)        (optional)
+ * A token sees all rows of its sequence, with `causal` those below
+ * lens[s] - n + i + 1: the tokens' own rows are appended (aircache_rotate) and
+ * each sees the rows before its own and its own.  (Earlier rows may lie in any
+ * order, as after an eviction.)  row_begin and row_end, where given, narrow that
+ * to row_begin[t] <= j < row_end[t] (any integers): a text token sees the images
+ * before it, or its latest image, or a window of the last rows.
+ * A token that sees no row gets out = 0 and lse = -inf, and so does a query all
+ * of whose logits lie below fp32's range; a NaN, an infinite key or value or a
+ * logit above the range makes what sees it NaN or infinite, and nothing else.
+ * Logits, sums and lse are fp32; the weights that meet V are rounded once, to
+ * bf16.  out is bf16, lse fp32 dense [num_tokens][h_q].
+ *
+ * Tokens cu_tokens[s] .. cu_tokens[s+1]-1 belong to sequence s (a sequence may
+ * have none); tokens at or behind cu_tokens[num_seqs] are padding, whose outputs
+ * are left as they are.  Sequences may share pages: nothing is written to them.
+ *
+ * Device-side, AIRCACHE_ERR_DEVICE_BOUNDS is set by a length out of bounds (the
+ * sequence then has no rows), a decreasing cu_tokens, one below 0 or above
+ * num_tokens (the sequence then has no tokens, and its outputs are left as they
+ * are), fewer rows than tokens with `causal`, and a page out of bounds (its rows
+ * read as zeros).
+ *
+ * The work is split by rows and tokens, whatever the lengths; a second kernel
+ * joins what several CTAs did, in a fixed order (a third one before them where
+ * row_begin or row_end is given).
+ * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; h_q a
+ * multiple of h_kv (with at most 16 query heads to a KV head, else
+ * AIRCACHE_ERR_UNSUPPORTED); scale > 0 and finite; q and out 16-byte aligned,
+ * integers and lse 4-byte; strides positive multiples of 8 elements, those of out such
+ * that no two of its rows meet; out apart from q, lse and the cache (from the
+ * whole range that each spans).  Workspace as for aircache_paged_decode.
+ */
+typedef struct aircache_paged_attend_problem {
+    const aircache_pages* pages;  /* HOST */
+    int64_t num_tokens;    /* rows of q and out: 0..2^31 - 2^16 */
+    int32_t h_q;
+    int32_t dtype;
+    int32_t causal;        /* 0 or 1 */
+    int32_t reserved0;     /* 0 */
+    float scale;
+    float reserved1;       /* 0 */
+    const int32_t* cu_tokens;  /* device [num_seqs + 1], non-decreasing, from 0 */
+    const int32_t* row_begin;  /* optional, device [num_tokens] */
+    const int32_t* row_end;    /* optional, device [num_tokens] */
+    const void* q;         /* [num_tokens][h_q][head_dim] */
+    int64_t q_stride_tok;
+    int64_t q_stride_head;
+    void* out;             /* [num_tokens][h_q][head_dim] bf16 */
+    int64_t out_stride_tok;
+    int64_t out_stride_head;
+    float* lse;            /* optional */
+} aircache_paged_attend_problem;
+
+AIRCACHE_API size_t aircache_paged_attend_workspace_size(const aircache_paged_attend_problem* p);
+AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -155,6 +155,18 @@ class EvictProblemStruct(ctypes.Structure):
     ]
 
 
+class PagedAttendProblemStruct(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.POINTER(PagesStruct)), ("num_tokens", ctypes.c_int64), ("h_q", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("reserved1", ctypes.c_float),
+        ("cu_tokens", ctypes.c_void_p), ("row_begin", ctypes.c_void_p), ("row_end", ctypes.c_void_p),
+        ("q", ctypes.c_void_p), ("q_stride_tok", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_stride_tok", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 def lib():
     """The loaded CUDA library (raises if it was not built)."""
     global _lib
@@ -221,6 +233,11 @@ def lib():
         L.aircache_evict_workspace_size.restype = sz
         L.aircache_evict.argtypes = [EV, vp, sz, vp]
         L.aircache_evict.restype = i32
+        PA = ctypes.POINTER(PagedAttendProblemStruct)
+        L.aircache_paged_attend_workspace_size.argtypes = [PA]
+        L.aircache_paged_attend_workspace_size.restype = sz
+        L.aircache_paged_attend.argtypes = [PA, vp, sz, vp]
+        L.aircache_paged_attend.restype = i32
         _lib = L
     return _lib
 
@@ -979,3 +996,73 @@ def evict(prob: EvictProblem, ws=None, stream=None, check=True):
     if check:
         _check_device(prob, ws, stream, "aircache_evict")
     return prob.lens_out
+
+
+class PagedAttendProblem:
+    """Attention of several tokens of each sequence over a PagedCache (see
+    aircache_paged_attend in the header).
+
+    q: [T, H_q, D] bf16; cu_tokens: int32 [S + 1], the tokens of each sequence;
+    out: bf16 [T, H_q, D] (allocated when None); lse: True (allocated) or an fp32
+    [T, H_q] tensor; scale: the logits' factor (None: 1 / sqrt(D)).  A token sees
+    all rows of its sequence; causal: the tokens' own rows are the cache's last
+    and each sees those up to its own; row_begin, row_end: int32 [T], only rows
+    of [row_begin, row_end) (either may be None)."""
+
+    def __init__(self, q, cache, cu_tokens, out=None, lse=None, scale=None, causal=False, row_begin=None, row_end=None):
+        if q.dim() != 3 or q.dtype != torch.bfloat16 or q.stride(2) != 1:
+            raise ValueError("q is bf16 [T, H_q, D], head_dim contiguous")
+        T, h_q, d = (int(x) for x in q.shape)
+        if d != cache.d:
+            raise ValueError("q must have the cache's head_dim")
+        _dense(cu_tokens, torch.int32, (cache.num_seqs + 1,), "cu_tokens")
+        if out is None:
+            out = torch.empty((T, h_q, d), dtype=torch.bfloat16, device=q.device)
+        if out.dtype != torch.bfloat16 or out.shape != q.shape or out.stride(2) != 1:
+            raise ValueError("out is bf16 of q's shape, head_dim contiguous")
+        if isinstance(lse, bool):
+            lse = torch.empty((T, h_q), dtype=torch.float32, device=q.device) if lse else None
+        _dense(lse, torch.float32, (T, h_q), "lse")
+        for t, name in ((row_begin, "row_begin"), (row_end, "row_end")):
+            _dense(t, torch.int32, (T,), name)
+        self.device = _same_device(q, cu_tokens, out, lse, row_begin, row_end, cache.k)
+        self.keep = (q, cache, cu_tokens, row_begin, row_end)
+        self.empty = T == 0 or cache.num_seqs == 0
+        self.out, self.lse = out, lse
+        adr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = PagedAttendProblemStruct(
+            pages=ctypes.pointer(cache.c), num_tokens=T, h_q=h_q, dtype=BF16, causal=1 if causal else 0, reserved0=0,
+            scale=float(d ** -0.5 if scale is None else scale), reserved1=0.0, cu_tokens=adr(cu_tokens),
+            row_begin=adr(row_begin), row_end=adr(row_end), q=adr(q), q_stride_tok=q.stride(0),
+            q_stride_head=q.stride(1), out=adr(out), out_stride_tok=out.stride(0), out_stride_head=out.stride(1),
+            lse=adr(lse))
+        self.ref = ctypes.byref(self.c)
+
+    def workspace_size(self) -> int:
+        if self.empty:
+            return 256
+        with torch.cuda.device(self.device):
+            n = lib().aircache_paged_attend_workspace_size(self.ref)
+            if n == 0:  # (the call itself names the reason, before it looks at a workspace)
+                raise AirCacheError(lib().aircache_paged_attend(self.ref, None, 0, None), "aircache_paged_attend_workspace_size")
+        return int(n)
+
+    def new_workspace(self) -> torch.Tensor:
+        """A zeroed workspace (zeroed once; every call leaves it ready for the next)."""
+        return torch.zeros(self.workspace_size(), dtype=torch.uint8, device=self.device)
+
+
+def aircache_paged_attend(prob: PagedAttendProblem, ws, stream=None):
+    if prob.empty:
+        return
+    s = _paged_stream(prob, ws, stream)
+    _run_paged(lib().aircache_paged_attend, "aircache_paged_attend", prob, ws.data_ptr(), ws.numel(), s)
+
+
+def paged_attend(prob: PagedAttendProblem, ws=None, stream=None, check=True):
+    """One call; returns prob.out.  check=True reads the device error word (synchronises)."""
+    ws = _on_stream(prob, stream, prob.new_workspace) if ws is None else ws
+    aircache_paged_attend(prob, ws, stream)
+    if check:
+        _check_device(prob, ws, stream, "aircache_paged_attend")
+    return prob.out

@@ -1,0 +1,34 @@
+// Attention of several query tokens over paged rows (paged_attend.cu), as the shared-prefix decode
+// (shared_decode.cu) takes part in it.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "pages.cuh"
+
+namespace aircache {
+
+// Results kept in fp32 for a later join, of [token][query head]: the output [..][head_dim], and the log-sum-exp in
+// base 2 (-inf: the token saw no row, and its output is 0).
+struct AttendPart {
+  float* out;
+  float* lse2;
+};
+
+struct AttendPlan {
+  Pages pages;
+  bool q8;
+  int d, g, h_q;
+  int tok_tile;   // tokens of a stream's 128 query rows
+  int slots;      // bound of the batch's units for one KV head
+  int grid, rows_cap;
+  size_t cut_off, range_off, ml_off, o_off, total;
+};
+
+// Checks a problem and lays out its workspace.  `part`: the results go to fp32 arrays and p->out is not looked at.
+int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& pl);
+// Enqueues it; `ws` holds pl.total bytes, `error` the device error word.
+int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AttendPart& part, uint8_t* ws,
+                  int32_t* error, cudaStream_t s);
+
+}  // namespace aircache

@@ -1,0 +1,1042 @@
+// Attention of several query tokens of each sequence over its paged rows (aircache_paged_attend).
+//
+//   x_j = scale q . k_j for the rows j that the token sees,  o = sum_j exp(x_j - m) v_j / l,  l = sum_j exp(x_j - m).
+//
+// 4 D operations for each (token, query head, row): bound by the matrix units where a sequence has many tokens, by HBM
+// where it has few.  The query heads of a KV head are packed: 128 query rows are floor(128 / g) tokens with their g
+// heads, so that one tile of keys and values serves them all.
+//
+// A unit of work is a KV head and up to two such query tiles ("streams") of one sequence, over the 128-row key tiles
+// that any of its tokens sees.  With more tokens than a tile holds, the streams are two query tiles that take the same
+// keys in turn (wide); with fewer, they are one query tile whose key tiles go to the streams alternately (narrow), and
+// their results are joined at the end.  Either way one stream's softmax runs while the tensor cores work for the other.
+// The units lie on a line, each with its key tiles and some places for its end, and every CTA takes an equal run of it
+// (one CTA to an SM, persistent): ragged batches and long rows leave no SM idle.  Units that a run's border cuts leave
+// their parts in the workspace, and a second kernel joins them in the order of the CTAs.
+//
+// In a CTA: two groups of four softmax warps, one to a stream; a warp issues the MMAs (one thread), one the copies of
+// keys and values (TMA, boxes of as many rows as divide a page and 128, into a ring of tiles), one brings queries and
+// clears the value rows behind the sequence's last (a weight of 0 times whatever a page holds there could be NaN).
+// S = Q K^T goes to a TMEM buffer per stream; a softmax thread owns a row of it (its TMEM lane), takes it to registers
+// whole, and writes the weights as bf16 over the buffer's first half, from where the next MMA takes them as its A
+// operand: O += P V accumulates in TMEM.  The reference of the exponentials moves only when a row's maximum passes it by
+// 2^8; then O is rescaled in place, which nothing else touches in between because a thread's MMAs run in order.
+//
+// Weights that meet V are rounded once to bf16 (2^-9 of each weight, independent of one another: an output's error is
+// that of its own rounding to bf16 or less).  Logits, maximum, sum, O, parts and the joins are fp32.
+//
+// A weight of 0 does not hide a NaN or an infinity in V from a matrix product: a row whose output is not finite while
+// its sum is gets formed again, by a warp over the rows that it sees (repair_row).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstring>
+
+#include "attend.cuh"
+#include "tmap.cuh"
+#include "umma.cuh"
+
+namespace aircache {
+namespace {
+
+constexpr int kAtKeys = 128;                  // rows of a key tile
+constexpr int kAtRows = 128;                  // query rows of a stream (TMEM lanes)
+constexpr int kAtMma = 8, kAtLoad = 9, kAtAux = 10;  // behind the eight softmax warps: MMA issue, keys and values,
+                                                     // queries and tails (warp 11 fills their warpgroup)
+constexpr int kAtThreads = 12 * 32;
+// Registers of a thread: 168 at launch; the softmax threads, which hold a row of 128 logits, take what the others give
+constexpr int kAtRegsSoft = 208, kAtRegsOther = 80;
+static_assert(256 * kAtRegsSoft + 128 * kAtRegsOther <= kAtThreads * 168, "within the launch's own registers");
+constexpr uint32_t kAtEnd = 2;                // places of the line for a unit's end
+constexpr float kAtSlack = 8.f;               // base-2 powers that a maximum may pass its reference by
+constexpr uint32_t kAtS = 0, kAtO = 256;      // TMEM columns: S of stream i at 128 i, O at 256 + 128 i
+constexpr int kAtGroup = 16;                  // query heads of a KV head, at most
+constexpr int kAtHeader = 256;                // workspace: error word
+constexpr long long kAtLong = 4 * kWaitCycles;  // waits that stand behind another warp's
+
+template <int D>
+struct AtCfg {
+  static constexpr int kSlab = kAtKeys * 128;       // [128 rows][64 bf16]
+  static constexpr int kTile = kSlab * (D / 64);
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kOffQ = 0;                   // two query tiles
+  static constexpr int kOffRing = 2 * kTile;
+  static constexpr int kOffCtl = kOffRing + kStages * kTile;
+};
+
+struct AtArgs {
+  Pages pages;
+  const int32_t* cu;
+  const int32_t* row_begin;
+  const int32_t* row_end;
+  const __nv_bfloat16* q;
+  int64_t q_stride_tok, q_stride_head;
+  __nv_bfloat16* out;
+  int64_t out_stride_tok, out_stride_head;
+  float* lse;
+  AttendPart part;
+  int32_t* error;
+  int4* cut;        // [CTAs]: the unit that begins in the CTA and ends in another: slot, KV head, first CTA, parts
+  int2* range;      // [slots]: the key tiles that a unit's tokens see (with row_begin or row_end)
+  float2* part_ml;  // [2 CTAs][rows_cap]
+  float* part_o;    // [2 CTAs][rows_cap][D]
+  int64_t num_tokens;
+  int slots, group, tok_tile, h_q, causal, ctas, rows_cap, box;
+  float scale_log2;
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is M rows (lanes) of 16-bit elements, two to a column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int a, int b, int c, int d, int e,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(smem_u32(bar))
+      : "memory");
+}
+// Two fp32 multiply-adds and additions in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------ the line of units
+
+// Tokens of a unit for one KV head, and the key tiles that any of them sees.
+struct AtUnit {
+  int s, tok0, ntok, n;  // sequence, first token of it, tokens, the sequence's tokens
+  int rows, t0, c;       // its rows, first key tile, key tiles
+  int64_t token0;        // the batch's token of tok0
+};
+// Units of sequence s start at slot cu[s] / (2 tok_tile) + s: never less than the units before it, so that a slot's
+// sequence is found without a sum over the batch, and at most num_seqs slots are empty.
+__device__ __forceinline__ int slot_base(const AtArgs& a, int s) {
+  const int c = min(max(a.cu[s], 0), (int)a.num_tokens);
+  return c / (2 * a.tok_tile) + s;
+}
+__device__ __forceinline__ int find_seq(const AtArgs& a, int slot) {
+  int lo = 0, hi = a.pages.num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (slot_base(a, mid) <= slot)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+// Rows [lo, hi) that token i (of the sequence; `token` of the batch) sees.
+__device__ __forceinline__ void token_rows(const AtArgs& a, int rows, int n, int i, int64_t token, int& lo, int& hi) {
+  lo = 0;
+  hi = a.causal ? max(rows - n + i + 1, 0) : rows;
+  if (a.row_begin) lo = max(lo, a.row_begin[token]);
+  if (a.row_end) hi = min(hi, a.row_end[token]);
+  if (hi <= lo) lo = hi = 0;
+}
+// The unit of `slot` in sequence s; ntok = 0 when there is none.  LISTED: its key tiles are in a.range.
+template <bool LISTED = true>
+__device__ __forceinline__ AtUnit unit_of(const AtArgs& a, int s, int slot) {
+  AtUnit u;
+  u.s = s;
+  const int c0 = a.cu[s], c1 = a.cu[s + 1];
+  u.n = c0 >= 0 && c1 >= c0 && c1 <= a.num_tokens ? c1 - c0 : 0;
+  const int len = a.pages.lens[s];
+  u.rows = len >= 0 && len <= a.pages.max_rows ? len : 0;
+  const int64_t first = (int64_t)(slot - slot_base(a, s)) * (2 * a.tok_tile);
+  const bool in = first >= 0 && first < u.n;
+  u.tok0 = in ? (int)first : 0;
+  u.ntok = in ? min(2 * a.tok_tile, u.n - u.tok0) : 0;
+  u.token0 = (int64_t)c0 + u.tok0;
+  u.t0 = u.c = 0;
+  if (in) {
+    if (LISTED && a.range) {
+      const int2 r = a.range[slot];
+      u.t0 = r.x;
+      u.c = r.y - r.x;
+    } else {
+      const int hi = a.causal ? max(u.rows - u.n + u.tok0 + u.ntok, 0) : u.rows;
+      u.c = (int)(((int64_t)hi + kAtKeys - 1) / kAtKeys);
+    }
+  }
+  return u;
+}
+
+// A CTA's places of the line, and the walk over the units in them.
+struct AtRun {
+  uint64_t per, lo, hi, at;  // places of a CTA, its own, the unit's first
+  int slot, h;
+  AtUnit u;
+  int first, count;          // the CTA's key tiles of the unit, from u.t0 on
+};
+__device__ __forceinline__ void clip(AtRun& r) {
+  const uint64_t from = max(r.at, r.lo), to = min(r.at + r.u.c, r.hi);
+  r.first = (int)(min(from, r.at + r.u.c) - r.at);
+  r.count = to > from ? (int)(to - from) : 0;
+}
+__device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r) {
+  r.at += r.u.c + kAtEnd;
+  if (r.at >= r.hi) return false;
+  if (++r.h == a.pages.h_kv) {
+    r.h = 0;
+    do {
+      if (++r.slot >= a.slots) return false;
+      while (r.u.s + 1 < a.pages.num_seqs && slot_base(a, r.u.s + 1) <= r.slot) ++r.u.s;
+      r.u = unit_of(a, r.u.s, r.slot);
+    } while (r.u.ntok == 0);
+  }
+  clip(r);
+  return true;
+}
+// A unit that fits one query tile takes its key tiles alternately with both streams.
+__device__ __forceinline__ bool narrow(const AtArgs& a, const AtUnit& u) { return u.ntok <= a.tok_tile; }
+// Key tiles of stream i in a run.
+__device__ __forceinline__ int stream_tiles(bool nar, int count, int i) { return nar ? (count + 1 - i) / 2 : count; }
+
+struct AtScratch {
+  uint64_t sum[kAtThreads / 32];
+  AtRun run;
+};
+struct AtCtl {
+  uint64_t full[10], empty[10];
+  uint64_t tail[10];  // of a stage that holds values to be cleared in part: its copies have landed
+  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], mlfull, mlfree, done;
+  uint32_t tmem;
+  float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
+  AtScratch scratch;
+};
+// By all threads of the CTA; false if the CTA has no place.
+__device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (a.slots + kAtThreads - 1) / kAtThreads;
+  const int s0 = min(tid * each, a.slots), s1 = min(s0 + each, a.slots);
+  uint64_t mine = 0;
+  int seq0 = 0;
+  if (s0 < s1) {
+    int s = seq0 = find_seq(a, s0);
+    for (int i = s0; i < s1; ++i) {
+      while (s + 1 < a.pages.num_seqs && slot_base(a, s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, s, i);
+      if (u.ntok) mine += (uint64_t)(u.c + kAtEnd) * a.pages.h_kv;
+    }
+  }
+  uint64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sc->sum[warp] = incl;
+  __syncthreads();
+  uint64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAtThreads / 32; ++w) {
+    if (w < warp) before += sc->sum[w];
+    total += sc->sum[w];
+  }
+  const uint64_t per = max((uint64_t)1, (total + gridDim.x - 1) / gridDim.x);
+  const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
+  if (lo < hi && lo >= before && lo < before + mine) {
+    uint64_t at = before;
+    int s = seq0;
+    for (int i = s0; i < s1; ++i) {
+      while (s + 1 < a.pages.num_seqs && slot_base(a, s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, s, i);
+      if (!u.ntok) continue;
+      const uint64_t wide = u.c + kAtEnd;
+      if (lo < at + wide * a.pages.h_kv) {
+        AtRun x;
+        x.per = per;
+        x.lo = lo;
+        x.hi = hi;
+        x.slot = i;
+        x.h = (int)((lo - at) / wide);
+        x.at = at + x.h * wide;
+        x.u = u;
+        clip(x);
+        sc->run = x;
+        break;
+      }
+      at += wide * a.pages.h_kv;
+    }
+  }
+  __syncthreads();
+  if (lo < hi) r = sc->run;
+  return lo < hi;
+}
+
+// ------------------------------------------------------------------ results
+
+// The output of one row whose sum is finite and whose values are not: over the rows that it sees, without those that a
+// matrix product multiplies by 0.  By a warp; lane holds D / 32 columns.
+template <int D>
+__device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t token, int head, int lo, int hi, float m,
+                                        float l, float y[D / 32]) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const Pages& p = a.pages;
+  const __nv_bfloat16* q = a.q + token * a.q_stride_tok + (int64_t)head * a.q_stride_head + lane * E;
+  float qv[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q[e]), y[e] = 0.f;
+  for (int j = lo; j < hi; ++j) {
+    const int page = p.table[(int64_t)s * p.table_stride + j / p.page_rows];
+    float x = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+    if (page_ok(p, page)) {
+      const int64_t at = page_elem(p, page, h, j % p.page_rows) + lane * E;
+      const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at;
+      const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x), v[e] = __bfloat162float(vv[e]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    const float w = fast_exp2(fmaf(x, a.scale_log2, -m));
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = fmaf(w, v[e], y[e]);
+  }
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] *= inv;
+}
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
+
+// The log-sum-exp of a row.
+__device__ __forceinline__ void write_lse(const AtArgs& a, int64_t token, int head, float m, float l) {
+  const float x = l == 0.f ? -INFINITY : m + log2f(l);
+  if (a.part.lse2) a.part.lse2[token * a.h_q + head] = x;
+  if (a.lse) a.lse[token * a.h_q + head] = x * 0.69314718055994531f;
+}
+// E consecutive columns of a row.
+template <int D, int E>
+__device__ __forceinline__ void write_out(const AtArgs& a, int64_t token, int head, int col, const float* y) {
+  if (a.part.out) {
+    float* to = a.part.out + (token * a.h_q + head) * D + col;
+    if constexpr (E == 2) {
+      *reinterpret_cast<float2*>(to) = make_float2(y[0], y[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+    }
+    return;
+  }
+  __nv_bfloat16* to = a.out + token * a.out_stride_tok + (int64_t)head * a.out_stride_head + col;
+  if constexpr (E == 2) {
+    *reinterpret_cast<uint32_t*>(to) = pack2(y[0], y[1]);
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; e += 8)
+      *reinterpret_cast<uint4*>(to + e) = make_uint4(pack2(y[e], y[e + 1]), pack2(y[e + 2], y[e + 3]),
+                                                     pack2(y[e + 4], y[e + 5]), pack2(y[e + 6], y[e + 7]));
+  }
+}
+
+// ------------------------------------------------------------------ the attention
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __grid_constant__ CUtensorMap qmap,
+                                                                     const __grid_constant__ CUtensorMap kmap,
+                                                                     const __grid_constant__ CUtensorMap vmap,
+                                                                     const __grid_constant__ AtArgs a) {
+  using C = AtCfg<D>;
+  extern __shared__ uint8_t at_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
+  AtCtl* ctl = reinterpret_cast<AtCtl*>(sm + C::kOffCtl);
+  const uint32_t base = smem_u32(sm);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Pages& p = a.pages;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->tail[i], 1);
+    }
+    mbar_init(&ctl->qfull, 1);
+    mbar_init(&ctl->qempty, 1);
+    mbar_init(&ctl->mlfull, 4);
+    mbar_init(&ctl->mlfree, 4);
+    mbar_init(&ctl->done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->sfull[i], 1);
+      mbar_init(&ctl->pfull[i], 4);
+      mbar_init(&ctl->ofull[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kAtMma) {
+    __syncwarp();
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == kAtLoad && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) {  // what the batch's description says that cannot be
+    bool bad = tid == 0 && a.cu[0] < 0;
+    for (int s = tid; s < p.num_seqs; s += kAtThreads) {
+      const int c0 = a.cu[s], c1 = a.cu[s + 1], len = p.lens[s];
+      bad |= c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
+    }
+    if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+  }
+  tc_fence_before();
+  AtRun r;
+  const bool any = make_run(a, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  if (warp >= kAtMma)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kAtRegsOther));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kAtRegsSoft));
+
+  if (warp == kAtLoad) {
+    // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
+    // and the odd chunks: the next chunk's are looked up while this one is copied
+    const int boxes = kAtKeys / a.box, per_chunk = 32 / boxes;  // boxes of a tile, tiles of a chunk
+    uint32_t n = 0;                                             // ring entries so far
+    bool ok = true;
+    for (bool more = any; more && ok; more = next_unit(a, r)) {
+      if (r.count == 0) continue;
+      const bool nar = narrow(a, r.u);
+      const int32_t* table = p.table + (int64_t)r.u.s * p.table_stride;
+      const int tile0 = r.u.t0 + r.first;
+      auto look = [&](int chunk) {
+        const int64_t row = ((int64_t)tile0 + (int64_t)chunk * per_chunk) * kAtKeys + (int64_t)lane * a.box;
+        if (row >= r.u.rows || row >= (int64_t)(tile0 + r.count) * kAtKeys) return -1;
+        const int page = table[(int)row / p.page_rows];
+        if (page_ok(p, page)) return page;
+        set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+        return (int)p.num_pages;  // (behind the tensor: its rows arrive as zeros)
+      };
+      int even = look(0), odd = look(1);
+      for (int pos = 0; pos < 2 * r.count && ok; ++pos, ++n) {
+        bool val;
+        int j;  // the key tile within the run
+        if (!nar) {
+          val = pos & 1;
+          j = pos >> 1;
+        } else if (pos == 2 * r.count - 1) {
+          val = true;
+          j = r.count - 1;
+        } else {
+          val = pos > 0 && !(pos & 1);
+          j = val ? pos / 2 - 1 : (pos + 1) / 2;
+        }
+        const int chunk = j / per_chunk, in_chunk = j - chunk * per_chunk;
+        if (val && in_chunk == 0 && chunk > 0) {  // keys are at most two tiles ahead of values, a chunk four or more
+          if (chunk & 1)
+            even = look(chunk + 1);
+          else
+            odd = look(chunk + 1);
+        }
+        const uint32_t st = n % C::kStages;
+        if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
+        if (!ok) break;
+        const int slabs = D / 64;
+        const int box = lane / slabs, slab = lane % slabs;
+        const int page = __shfl_sync(0xffffffffu, chunk & 1 ? odd : even, (in_chunk * boxes + box) & 31);
+        const int row0 = (tile0 + j) * kAtKeys;
+        const bool mine = lane < boxes * slabs && page >= 0;
+        const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine));
+        // values behind the last row are cleared by another warp, which then says that the tile is there
+        const bool tail = val && (int64_t)row0 + kAtKeys > r.u.rows;
+        uint64_t* bar = tail ? &ctl->tail[st] : &ctl->full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(a.box * 128));
+        __syncwarp();
+        if (mine) {
+          fence_proxy_async_smem();
+          tma_load_5d(base + C::kOffRing + st * C::kTile + slab * C::kSlab + box * a.box * 128, val ? &vmap : &kmap, 0,
+                      (row0 + box * a.box) % p.page_rows, slab, r.h, page, bar);
+        }
+      }
+    }
+    if (!ok) {
+      set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      // the copies in flight land before the CTA's shared memory is another's
+      for (uint32_t f = n > C::kStages ? n - C::kStages : 0; f < n; ++f)
+        (void)mbar_wait_warp(&ctl->full[f % C::kStages], (f / C::kStages) & 1);
+    }
+  } else if (warp == kAtAux) {
+    // ---- queries, and the values behind a sequence's last row
+    uint32_t units = 0, tails = 0, n = 0;  // tails: bit st is the parity of tail[st]
+    bool ok = true;
+    for (bool more = any; more && ok; more = next_unit(a, r)) {
+      if (r.count == 0) continue;
+      const bool nar = narrow(a, r.u);
+      if (units > 0) ok = mbar_wait_warp(&ctl->qempty, (units - 1) & 1, kAtLong);
+      if (!ok) break;
+      if (lane == 0) {
+        const int streams = nar ? 1 : 2;
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&ctl->qfull, (uint32_t)(streams * (D / 64) * a.tok_tile * a.group * 128));
+        for (int i = 0; i < streams; ++i)
+          for (int sl = 0; sl < D / 64; ++sl)
+            tma_load_4d(base + C::kOffQ + i * C::kTile + sl * C::kSlab, &qmap, 0, sl, r.h * a.group,
+                        (int)r.u.token0 + i * a.tok_tile, &ctl->qfull);
+      }
+      __syncwarp();
+      ++units;
+      const int64_t last = (int64_t)(r.u.t0 + r.first + r.count) * kAtKeys;
+      if (last > r.u.rows) {
+        const uint32_t st = (n + 2 * r.count - 1) % C::kStages;  // a run's last entry
+        ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
+        if (!ok) break;
+        tails ^= 1u << st;
+        uint8_t* tile = sm + C::kOffRing + st * C::kTile;
+        const int valid = r.u.rows - (int)(last - kAtKeys);
+        for (int i = valid * (D / 8) + lane; i < kAtKeys * (D / 8); i += 32) {
+          const int row = i / (D / 8), rest = i % (D / 8);
+          *reinterpret_cast<uint4*>(tile + (rest >> 3) * C::kSlab + row * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[st]);
+      }
+      n += 2 * r.count;
+    }
+    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+    if (units > 0) (void)mbar_wait_warp(&ctl->qfull, (units - 1) & 1);  // (landed)
+  } else if (warp == kAtMma) {
+    if (lane == 0) {
+      // ---- turn k: stream k & 1 gets O += P V for its (k >> 1)-th tile, then S for its next
+      constexpr uint32_t id_s = umma_idesc_bf16(kAtRows, kAtKeys);
+      constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
+      uint32_t units = 0, n = 0, p_it[2] = {0, 0};
+      bool ok = true;
+      for (bool more = any; more && ok; more = next_unit(a, r)) {
+        if (r.count == 0) continue;
+        const bool nar = narrow(a, r.u);
+        const int turns = nar ? r.count : 2 * r.count;
+        ok = mbar_wait(&ctl->qfull, units & 1, kAtLong);
+        if (!ok) break;
+        ++units;
+        auto logits = [&](int k) {
+          const int i = k & 1, j = nar ? k : k >> 1;
+          const uint32_t e = n + (nar ? (j == 0 ? 0 : 2 * j - 1) : 2 * j);
+          const uint32_t st = e % C::kStages;
+          if (!mbar_wait(&ctl->full[st], (e / C::kStages) & 1, kAtLong)) return false;
+          tc_fence_after();
+          const uint32_t qb = base + C::kOffQ + (nar ? 0 : i * C::kTile), kb = base + C::kOffRing + st * C::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::kSlab + (kk & 3) * 32;
+            umma_bf16(tmem + kAtS + 128 * i, umma_desc_sw128(qb + off), umma_desc_sw128(kb + off), id_s, kk > 0);
+          }
+          umma_commit(&ctl->sfull[i]);
+          if (nar || i == 1) umma_commit(&ctl->empty[st]);
+          if (k == turns - 1) umma_commit(&ctl->qempty);
+          return true;
+        };
+        ok = logits(0);
+        if (ok && turns > 1) ok = logits(1);
+        for (int k = 0; k < turns && ok; ++k) {
+          const int i = k & 1, j = nar ? k : k >> 1;
+          const uint32_t e = n + (nar ? min(2 * j + 2, 2 * r.count - 1) : 2 * j + 1);
+          const uint32_t st = e % C::kStages;
+          ok = mbar_wait(&ctl->pfull[i], p_it[i] & 1, kAtLong) && mbar_wait(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
+          if (!ok) break;
+          ++p_it[i];
+          tc_fence_after();
+          const uint32_t vb = base + C::kOffRing + st * C::kTile;
+#pragma unroll
+          for (int kk = 0; kk < kAtKeys / 16; ++kk)
+            umma_bf16_ts(tmem + kAtO + 128 * i, tmem + kAtS + 128 * i + 8 * kk,
+                         umma_desc_sw128_mn(vb + kk * 16 * 128, C::kSlab, 1024), id_o, k >= 2 || kk > 0);
+          if (nar || i == 1) umma_commit(&ctl->empty[st]);
+          if (k + 2 >= turns) umma_commit(&ctl->ofull[i]);
+          if (k + 2 < turns) ok = logits(k + 2);
+        }
+        n += 2 * r.count;
+      }
+      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
+      (void)mbar_wait(&ctl->done, 0);
+    }
+  } else if (warp < kAtMma) {
+    // ---- softmax: stream i, query row `row` (its TMEM lane)
+    const int i = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = tl + kAtS + 128 * i;
+    if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (until a run says otherwise)
+    const int tok = row / a.group, hh = row - tok * a.group;
+    uint32_t it_s = 0, it_o = 0, joins = 0;
+    bool ok = true;
+    for (bool more = any; more && ok; more = next_unit(a, r)) {
+      const bool nar = narrow(a, r.u);
+      const int my_tok = nar ? tok : tok + i * a.tok_tile;  // of the unit
+      const bool valid = tok < a.tok_tile && my_tok < r.u.ntok;
+      const int64_t token = r.u.token0 + my_tok;
+      const int head = r.h * a.group + hh;
+      if (r.count == 0) {
+        if (r.u.c == 0 && r.at >= r.lo && valid && (!nar || i == 0)) {  // nothing to see
+          const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int c = 0; c < D; c += 8) write_out<D, 8>(a, token, head, c, zero);
+          write_lse(a, token, head, 0.f, 0.f);
+        }
+        continue;
+      }
+      // rows without a query see every key, so that they mask nothing; what they get is not read
+      int lo = 0, hi = INT32_MAX;
+      if (valid) token_rows(a, r.u.rows, r.u.n, r.u.tok0 + my_tok, token, lo, hi);
+      const bool idle = !__any_sync(0xffffffffu, valid);
+      const int tiles = stream_tiles(nar, r.count, i);
+      float m = -FLT_MAX;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int it = 0; it < tiles; ++it) {
+        if (!mbar_wait_warp(&ctl->sfull[i], it_s & 1, kAtLong)) {
+          ok = false;
+          break;
+        }
+        ++it_s;
+        tc_fence_after();
+        if (!idle) {
+          const int k0 = (r.u.t0 + r.first + (nar ? 2 * it + i : it)) * kAtKeys;
+          float v[kAtKeys];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v + 32 * c);
+          tmem_wait_ld();
+          if (!__all_sync(0xffffffffu, lo <= k0 && hi - k0 >= kAtKeys)) {
+            const int from = lo - k0;
+            const uint32_t wide = (uint32_t)(hi - lo);
+#pragma unroll
+            for (int c = 0; c < kAtKeys; ++c)
+              if ((uint32_t)(c - from) >= wide) v[c] = -INFINITY;
+          }
+          float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int c = 4; c < kAtKeys; c += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+          if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
+            const float to = fmaxf(m, mx), f = fast_exp2(m - to);
+            m = to;
+            sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
+            if (it > 0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld16(tl + kAtO + 128 * i + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= f;
+                tmem_st16(tl + kAtO + 128 * i + c, o);
+              }
+            }
+          }
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-m, -m);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float2 x = fma2(make_float2(v[64 * half + 2 * c], v[64 * half + 2 * c + 1]), scale2, ref2);
+              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+              sum[c & 1] = add2(sum[c & 1], e);
+              w[c] = pack2(e.x, e.y);
+            }
+            tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->pfull[i]);
+      }
+      if (!ok) break;
+      float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (tiles > 0) {
+        if (!mbar_wait_warp(&ctl->ofull[i], it_o & 1, kAtLong)) {
+          ok = false;
+          break;
+        }
+        ++it_o;
+        tc_fence_after();
+      }
+      // ---- the run's result
+      const bool both = nar && r.count > 1;  // the streams' results are joined, by the first
+      float f0 = 1.f, f1 = 0.f;
+      if (both && i == 1) {
+        ctl->ml[row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->mlfull);
+        ok = mbar_wait_warp(&ctl->mlfree, joins & 1, kAtLong);
+        if (!ok) break;
+        ++joins;
+        tc_fence_after();
+      } else if (both) {
+        ok = mbar_wait_warp(&ctl->mlfull, joins & 1, kAtLong);
+        if (!ok) break;
+        ++joins;
+        tc_fence_after();
+        const float2 o = ctl->ml[row];
+        const float to = fmaxf(m, o.x);
+        f0 = fast_exp2(m - to);
+        f1 = fast_exp2(o.x - to);
+        l = l * f0 + o.y * f1;
+        m = to;
+      }
+      if ((!nar || i == 0) && !idle) {
+        const bool cut = r.count < r.u.c;
+        // a CTA's part of a unit that began before it goes to slot 2 x CTA, of one that begins in it to the next
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (r.first == 0 ? 1 : 0)) * a.rows_cap + my_tok * a.group + hh;
+        const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const bool none = !cut && l == 0.f;
+        bool bad = false;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tl + kAtO + 128 * i + c, o);
+          tmem_wait_ld();
+          if (both) {
+            float o1[32];
+            tmem_ld32(tl + kAtO + 128 + c, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            o[e] = none ? 0.f : o[e] * inv;
+            bad |= !finite(o[e]);
+          }
+          if (!valid) continue;
+          if (cut) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(a.part_o + slot * D + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else {
+            write_out<D, 32>(a, token, head, c, o);
+          }
+        }
+        if (valid && cut) a.part_ml[slot] = make_float2(m, l);
+        if (valid && !cut) write_lse(a, token, head, m, l);
+        if (!cut) {
+          uint32_t rows = __ballot_sync(0xffffffffu, valid && bad && finite(l));
+          while (rows) {
+            const int from = __ffs(rows) - 1;
+            rows &= rows - 1;
+            float y[D / 32];
+            const int64_t t = __shfl_sync(0xffffffffu, token, from);
+            const int hd = __shfl_sync(0xffffffffu, head, from);
+            repair_row<D>(a, r.u.s, r.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
+                          __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), y);
+            write_out<D, D / 32>(a, t, hd, lane * (D / 32), y);
+          }
+        }
+      }
+      if (tid == 0 && r.first == 0) {
+        const int c0 = (int)(r.at / r.per);
+        const int parts = (int)((r.at + r.u.c - 1) / r.per) - c0 + 1;
+        if (parts > 1) a.cut[blockIdx.x] = make_int4(r.slot, r.h, c0, parts);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (both && i == 0 && lane == 0) mbar_arrive(&ctl->mlfree);  // the second stream's O and sums are read
+    }
+    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kAtMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The key tiles that each unit's tokens see, where tokens have ranges of their own.  A warp to a slot.
+constexpr int kArThreads = 128;
+__global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_constant__ AtArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int slot = blockIdx.x * (kArThreads / 32) + (threadIdx.x >> 5);
+  if (slot >= a.slots) return;
+  const AtUnit u = unit_of<false>(a, find_seq(a, slot), slot);
+  int from = INT32_MAX, to = 0;
+  for (int i = lane; i < u.ntok; i += 32) {
+    int lo, hi;
+    token_rows(a, u.rows, u.n, u.tok0 + i, u.token0 + i, lo, hi);
+    if (hi > lo) from = min(from, lo), to = max(to, hi);
+  }
+  from = __reduce_min_sync(0xffffffffu, from);
+  to = __reduce_max_sync(0xffffffffu, to);
+  if (lane == 0) a.range[slot] = to > 0 ? make_int2(from / kAtKeys, (to - 1) / kAtKeys + 1) : make_int2(0, 0);
+}
+
+// Joins the parts of the units that several CTAs shared, a warp to a row.
+constexpr int kAfThreads = 256;
+constexpr int kAfSplit = 8;  // CTAs to a unit
+template <int D>
+__global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_constant__ AtArgs a) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int4 cut = a.cut[blockIdx.x / kAfSplit];
+  if (cut.w < 2) return;
+  const int lane = threadIdx.x & 31;
+  const AtUnit u = unit_of(a, find_seq(a, cut.x), cut.x);
+  for (int rho = (blockIdx.x % kAfSplit) * (kAfThreads / 32) + (threadIdx.x >> 5); rho < u.ntok * a.group;
+       rho += kAfSplit * (kAfThreads / 32)) {
+    float m = -FLT_MAX, l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    constexpr int N = 4;
+    for (int j0 = 0; j0 < cut.w; j0 += N) {
+      float2 ml[N];
+      float x[N][E];
+#pragma unroll
+      for (int f = 0; f < N; ++f) {
+        const int j = min(j0 + f, cut.w - 1);
+        const int64_t at = (2 * (int64_t)(cut.z + j) + (j == 0 ? 1 : 0)) * a.rows_cap + rho;
+        ml[f] = a.part_ml[at];
+        const float* from = a.part_o + at * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(from);
+          x[f][0] = y.x, x[f][1] = y.y, x[f][2] = y.z, x[f][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(from);
+          x[f][0] = y.x, x[f][1] = y.y;
+        }
+      }
+      float to = m;
+#pragma unroll
+      for (int f = 0; f < N; ++f) to = fmaxf(to, ml[f].x);
+      const float f0 = fast_exp2(m - to);
+      m = to;
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f0;
+#pragma unroll
+      for (int f = 0; f < N; ++f) {
+        if (j0 + f >= cut.w) continue;
+        const float w = fast_exp2(ml[f].x - m);
+        l = fmaf(ml[f].y, w, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[f][e], w, o[e]);
+      }
+    }
+    const int my_tok = rho / a.group, head = cut.y * a.group + rho % a.group;
+    const int64_t token = u.token0 + my_tok;
+    const float inv = 1.f / l;
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] = l == 0.f ? 0.f : o[e] * inv;
+      bad |= !finite(o[e]);
+    }
+    if (__any_sync(0xffffffffu, bad) && finite(l)) {
+      int lo, hi;
+      token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
+      repair_row<D>(a, u.s, cut.y, token, head, lo, hi, m, l, o);
+    }
+    write_out<D, E>(a, token, head, lane * E, o);
+    if (lane == 0) write_lse(a, token, head, m, l);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline bool al16(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; }
+inline bool al4(const void* x) { return (reinterpret_cast<uintptr_t>(x) & 3) == 0; }
+
+int box_rows(int page_rows) {  // the largest power of two up to 128 that divides a page
+  int b = kAtKeys;
+  while (page_rows % b) b /= 2;
+  return b;
+}
+
+// Boxes of as many rows of one page and KV head, one 128-byte slab of them.
+bool encode_kv(CUtensorMap* m, const void* base, const AttendPlan& pl) {
+  auto enc = tma_encoder();
+  if (!enc) return false;
+  const Pages& p = pl.pages;
+  cuuint64_t dims[5] = {64, (cuuint64_t)p.page_rows, (cuuint64_t)pl.d / 64, (cuuint64_t)p.h_kv, (cuuint64_t)p.num_pages};
+  cuuint64_t strides[4] = {(cuuint64_t)p.stride_row * 2, 128, (cuuint64_t)p.stride_head * 2, (cuuint64_t)p.stride_page * 2};
+  cuuint32_t box[5] = {64, (cuuint32_t)box_rows(p.page_rows), 1, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             pl.d == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Boxes of a KV head's query heads of tok_tile tokens, one 128-byte slab of them: packed rows, head by head.
+bool encode_q(CUtensorMap* m, const aircache_paged_attend_problem* p, const AttendPlan& pl) {
+  auto enc = tma_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {64, (cuuint64_t)pl.d / 64, (cuuint64_t)p->h_q, (cuuint64_t)p->num_tokens};
+  cuuint64_t strides[3] = {128, (cuuint64_t)(p->h_q > 1 ? p->q_stride_head : pl.d) * 2,
+                           (cuuint64_t)(p->num_tokens > 1 ? p->q_stride_tok : (int64_t)p->h_q * pl.d) * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)pl.g, (cuuint32_t)pl.tok_tile}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p->q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AtArgs& a, cudaStream_t s) {
+  CUtensorMap qm, km, vm;
+  if (!encode_q(&qm, p, pl) || !encode_kv(&km, pl.pages.k, pl) || !encode_kv(&vm, pl.pages.v, pl))
+    return AIRCACHE_ERR_UNSUPPORTED;
+  constexpr int smem = AtCfg<D>::kOffCtl + (int)sizeof(AtCtl) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+  if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (a.range && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
+                            dim3(kArThreads), 0, s, a) != cudaSuccess)
+    return AIRCACHE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.grid);
+  cfg.blockDim = dim3(kAtThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  return launch_pdl(attend_finish_kernel<D>, dim3(pl.grid * kAfSplit), dim3(kAfThreads), 0, s, a) == cudaSuccess
+             ? AIRCACHE_OK
+             : AIRCACHE_ERR_CUDA;
+}
+
+}  // namespace
+
+int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& pl) {
+  if (!p) return AIRCACHE_ERR_INVALID_ARG;
+  const int rc = check_pages(p->pages, pl.pages);
+  if (rc != AIRCACHE_OK) return rc;
+  const int d = p->pages->head_dim;
+  if (p->num_tokens < 0 || p->num_tokens > 0x7fff0000LL || p->h_q <= 0 || p->h_q % p->pages->h_kv != 0 || p->dtype != AIRCACHE_BF16 ||
+      (p->causal != 0 && p->causal != 1) || p->reserved0 != 0 || p->reserved1 != 0.f || !(p->scale > 0.f) || !std::isfinite(1.4427f * p->scale) ||
+      !p->q || !al16(p->q) || p->q_stride_tok % 8 != 0 || p->q_stride_head % 8 != 0 ||
+      (p->num_tokens > 1 && p->q_stride_tok <= 0) || (p->h_q > 1 && p->q_stride_head <= 0) || !p->cu_tokens ||
+      !al4(p->cu_tokens) || !al4(p->row_begin) || !al4(p->row_end) || !al4(p->lse))
+    return AIRCACHE_ERR_INVALID_ARG;
+  if (!part) {
+    // outputs: rows apart from one another and from the queries
+    const int64_t st = p->out_stride_tok, sh = p->out_stride_head;
+    if (!p->out || !al16(p->out) || st % 8 != 0 || sh % 8 != 0) return AIRCACHE_ERR_INVALID_ARG;
+    const bool many_t = p->num_tokens > 1, many_h = p->h_q > 1;
+    if ((many_t && st < d) || (many_h && sh < d)) return AIRCACHE_ERR_INVALID_ARG;
+    if (many_t && many_h) {
+      const int64_t heads = (p->h_q - 1) * sh + d, toks = (p->num_tokens - 1) * st + d;
+      if (st < heads && sh < toks) return AIRCACHE_ERR_INVALID_ARG;
+    }
+    auto bytes = [&](int64_t stride_t, int64_t stride_h) {
+      return (size_t)2 * ((p->num_tokens > 0 ? p->num_tokens - 1 : 0) * stride_t + (p->h_q - 1) * stride_h + d);
+    };
+    const size_t nq = bytes(many_t ? p->q_stride_tok : 0, many_h ? p->q_stride_head : 0);
+    const size_t no = bytes(many_t ? st : 0, many_h ? sh : 0), nl = 4 * (size_t)p->num_tokens * p->h_q;
+    const size_t nk = 2 * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;  // (to the last page, at least)
+    if (arrays_meet(p->out, no, p->q, nq) || arrays_meet(p->out, no, pl.pages.k, nk) ||
+        arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq))
+      return AIRCACHE_ERR_INVALID_ARG;
+  }
+  pl.d = d;
+  pl.h_q = p->h_q;
+  pl.g = p->h_q / p->pages->h_kv;
+  pl.q8 = p->pages->kv_dtype == AIRCACHE_INT8;
+  if (pl.g > kAtGroup || pl.q8) return AIRCACHE_ERR_UNSUPPORTED;
+  pl.tok_tile = kAtRows / pl.g;
+  pl.slots = (int)(p->num_tokens / (2 * pl.tok_tile)) + p->pages->num_seqs;
+  pl.grid = device_sms();
+  pl.rows_cap = (int)std::min<int64_t>(2 * pl.tok_tile, std::max<int64_t>(p->num_tokens, 1)) * pl.g;
+  pl.cut_off = kAtHeader;
+  pl.range_off = pl.cut_off + up256(sizeof(int4) * (size_t)pl.grid);
+  pl.ml_off = pl.range_off + (p->row_begin || p->row_end ? up256(sizeof(int2) * (size_t)pl.slots) : 0);
+  pl.o_off = pl.ml_off + up256(sizeof(float2) * 2 * (size_t)pl.grid * pl.rows_cap);
+  pl.total = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.rows_cap * pl.d);
+  return AIRCACHE_OK;
+}
+
+int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AttendPart& part, uint8_t* ws,
+                  int32_t* error, cudaStream_t s) {
+  AtArgs a;
+  a.pages = pl.pages;
+  a.cu = p->cu_tokens;
+  a.row_begin = p->row_begin;
+  a.row_end = p->row_end;
+  a.q = static_cast<const __nv_bfloat16*>(p->q);
+  a.q_stride_tok = p->q_stride_tok;
+  a.q_stride_head = p->q_stride_head;
+  a.out = static_cast<__nv_bfloat16*>(p->out);
+  a.out_stride_tok = p->out_stride_tok;
+  a.out_stride_head = p->out_stride_head;
+  a.lse = p->lse;
+  a.part = part;
+  a.error = error;
+  a.cut = reinterpret_cast<int4*>(ws + pl.cut_off);
+  a.range = p->row_begin || p->row_end ? reinterpret_cast<int2*>(ws + pl.range_off) : nullptr;
+  a.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + pl.o_off);
+  a.num_tokens = p->num_tokens;
+  a.slots = pl.slots;
+  a.group = pl.g;
+  a.tok_tile = pl.tok_tile;
+  a.h_q = p->h_q;
+  a.causal = p->causal;
+  a.ctas = pl.grid;
+  a.rows_cap = pl.rows_cap;
+  a.box = box_rows(pl.pages.page_rows);
+  a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
+  return pl.d == 128 ? launch_at<128>(p, pl, a, s) : launch_at<64>(p, pl, a, s);
+}
+
+}  // namespace aircache
+
+using namespace aircache;
+
+extern "C" {
+
+size_t aircache_paged_attend_workspace_size(const aircache_paged_attend_problem* p) {
+  AttendPlan pl;
+  return attend_plan(p, false, pl) == AIRCACHE_OK ? pl.total : 0;
+}
+
+int aircache_paged_attend(const aircache_paged_attend_problem* p, void* ws, size_t ws_bytes, void* stream) {
+  AttendPlan pl;
+  const int rc = attend_plan(p, false, pl);
+  if (rc != AIRCACHE_OK) return rc;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) != 0) return AIRCACHE_ERR_INVALID_ARG;
+  if (ws_bytes < pl.total) return AIRCACHE_ERR_WORKSPACE;
+  if (p->pages->num_seqs == 0 || p->num_tokens == 0) return AIRCACHE_OK;
+  return attend_launch(p, pl, AttendPart{nullptr, nullptr}, static_cast<uint8_t*>(ws), static_cast<int32_t*>(ws),
+                       static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

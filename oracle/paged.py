@@ -56,6 +56,38 @@ def decode(q, c, scale):
     return out, lse, w_all, size, spread
 
 
+def attend(q, cu, c, scale, causal=False, begin=None, end=None):
+    """(out [T, H_q, D], lse [T, H_q], logits' sizes [T, H_q], sum_j w_j |v_j| [T, H_q, D]); rows of tokens behind the
+    last sequence are NaN.  A masked row takes no part at all."""
+    T, h_q, d = q.shape
+    g = h_q // c["k"].shape[2]
+    out, spread = np.full((T, h_q, d), np.nan), np.zeros((T, h_q, d))
+    lse, size = np.full((T, h_q), np.nan), np.zeros((T, h_q))
+    for s in range(len(cu) - 1):
+        n, R = int(cu[s + 1] - cu[s]), int(c["lens"][s])
+        for j in range(h_q):
+            if n == 0:
+                continue
+            k, v = rows(c, "k", s, j // g), rows(c, "v", s, j // g)
+            for i in range(n):
+                t = int(cu[s]) + i
+                lo, hi = 0, max(R - n + i + 1, 0) if causal else R
+                if begin is not None:
+                    lo = max(lo, int(begin[t]))
+                if end is not None:
+                    hi = min(hi, int(end[t]))
+                out[t, j], lse[t, j] = 0.0, -np.inf
+                if hi <= lo:
+                    continue
+                x = (k[lo:hi] @ q[t, j]) * scale
+                size[t, j] = (np.abs(k[lo:hi]) @ np.abs(q[t, j])).max() * scale
+                e = np.exp(x - x.max())
+                lse[t, j] = x.max() + np.log(e.sum())
+                w = e / e.sum()
+                out[t, j], spread[t, j] = w @ v[lo:hi], w @ np.abs(v[lo:hi])
+    return out, lse, size, spread
+
+
 def largest_weighted_scale(q, c, scale):
     """int8 values: max_j w_j s_j of each sequence and query head [S, H_q], s_j the value's scale."""
     S, h_q, _ = q.shape
