@@ -841,6 +841,41 @@ AIRCACHE_API size_t aircache_paged_attend_workspace_size(const aircache_paged_at
 AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, void* ws, size_t ws_bytes,
                                        void* stream);
 
+/*
+ * One decode step of a batch whose sequences share prefixes (a system prompt, an
+ * image or a video that many conversations are about), each prefix's rows read
+ * once for all of them.  Sequences cu_seqs[i] .. cu_seqs[i+1]-1 continue prefix i:
+ * each attends over the rows of that prefix (rows 0 .. prefix->lens[i]-1 of the
+ * prefix's own pages) and over its own rows (own.pages), as one softmax; the
+ * results are those of aircache_paged_decode over both.  Sequences at or behind
+ * cu_seqs[number of prefixes] have only their own rows; a prefix may have no
+ * rows, and a sequence none of its own.
+ * own: the step over the own rows, all of it as aircache_paged_decode takes it
+ * (total_rows bounds the own rows only); with mass_out, the mass of the own rows
+ * grows by their weights in the joint softmax.  The prefixes' mass is neither
+ * read nor written.  Own rows and prefixes may be of different kv_dtype and
+ * page_rows, and their pages of one pool; prefixes need not be in different pages.
+ * The weights of the prefixes' rows are rounded as aircache_paged_attend's.
+ *
+ * Device-side, AIRCACHE_ERR_DEVICE_BOUNDS is also set by a prefix's length or
+ * page out of bounds (it then counts as empty; a bad page's rows read as zeros) and
+ * by a cu_seqs that decreases or leaves [0, num_seqs] (results of the sequences
+ * concerned are then undefined).
+ * Requirements beside those of own (else AIRCACHE_ERR_INVALID_ARG): prefix of
+ * own.pages's h_kv and head_dim; cu_seqs 4-byte aligned; own's q strides positive
+ * (where there is more than one sequence or head).  Workspace as for
+ * aircache_paged_decode.  Two kernels before those of aircache_paged_decode.
+ */
+typedef struct aircache_shared_decode_problem {
+    aircache_paged_decode_problem own;
+    const aircache_pages* prefix;  /* HOST; its num_seqs: the number of prefixes */
+    const int32_t* cu_seqs;        /* device [prefix->num_seqs + 1], non-decreasing, from 0 */
+} aircache_shared_decode_problem;
+
+AIRCACHE_API size_t aircache_shared_decode_workspace_size(const aircache_shared_decode_problem* p);
+AIRCACHE_API int aircache_shared_decode(const aircache_shared_decode_problem* p, void* ws, size_t ws_bytes,
+                                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -167,6 +167,12 @@ class PagedAttendProblemStruct(ctypes.Structure):
     ]
 
 
+class SharedDecodeProblemStruct(ctypes.Structure):
+    _fields_ = [
+        ("own", PagedDecodeProblemStruct), ("prefix", ctypes.POINTER(PagesStruct)), ("cu_seqs", ctypes.c_void_p),
+    ]
+
+
 def lib():
     """The loaded CUDA library (raises if it was not built)."""
     global _lib
@@ -238,6 +244,11 @@ def lib():
         L.aircache_paged_attend_workspace_size.restype = sz
         L.aircache_paged_attend.argtypes = [PA, vp, sz, vp]
         L.aircache_paged_attend.restype = i32
+        SD = ctypes.POINTER(SharedDecodeProblemStruct)
+        L.aircache_shared_decode_workspace_size.argtypes = [SD]
+        L.aircache_shared_decode_workspace_size.restype = sz
+        L.aircache_shared_decode.argtypes = [SD, vp, sz, vp]
+        L.aircache_shared_decode.restype = i32
         _lib = L
     return _lib
 
@@ -1065,4 +1076,49 @@ def paged_attend(prob: PagedAttendProblem, ws=None, stream=None, check=True):
     aircache_paged_attend(prob, ws, stream)
     if check:
         _check_device(prob, ws, stream, "aircache_paged_attend")
+    return prob.out
+
+
+class SharedDecodeProblem(PagedDecodeProblem):
+    """One decode step of sequences that share prefixes (see aircache_shared_decode
+    in the header): a PagedDecodeProblem over the sequences' own rows, q and cache,
+    with prefix, a PagedCache of the prefixes, and cu_seqs: int32 [prefixes + 1],
+    sequences cu_seqs[i] .. cu_seqs[i + 1] - 1 continue prefix i.  total_rows
+    bounds the own rows."""
+
+    def __init__(self, q, cache, prefix, cu_seqs, out=None, lse=None, scale=None, accumulate=False, mass_out=None,
+                 total_rows=0):
+        super().__init__(q, cache, out=out, lse=lse, scale=scale, accumulate=accumulate, mass_out=mass_out,
+                         total_rows=total_rows)
+        if prefix.d != cache.d or prefix.h_kv != cache.h_kv:
+            raise ValueError("prefix must have the cache's KV heads and head_dim")
+        _dense(cu_seqs, torch.int32, (prefix.num_seqs + 1,), "cu_seqs")
+        self.device = _same_device(q, cache.k, prefix.k, cu_seqs)
+        self.keep += (prefix, cu_seqs)
+        self.c = SharedDecodeProblemStruct(own=self.c, prefix=ctypes.pointer(prefix.c), cu_seqs=cu_seqs.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    def workspace_size(self) -> int:
+        if self.empty:
+            return 256
+        with torch.cuda.device(self.device):
+            n = lib().aircache_shared_decode_workspace_size(self.ref)
+            if n == 0:  # (the call itself names the reason, before it looks at a workspace)
+                raise AirCacheError(lib().aircache_shared_decode(self.ref, None, 0, None), "aircache_shared_decode_workspace_size")
+        return int(n)
+
+
+def aircache_shared_decode(prob: SharedDecodeProblem, ws, stream=None):
+    if prob.empty:
+        return
+    s = _paged_stream(prob, ws, stream)
+    _run_paged(lib().aircache_shared_decode, "aircache_shared_decode", prob, ws.data_ptr(), ws.numel(), s)
+
+
+def shared_decode(prob: SharedDecodeProblem, ws=None, stream=None, check=True):
+    """One decode step; returns prob.out.  check=True reads the device error word (synchronises)."""
+    ws = _on_stream(prob, stream, prob.new_workspace) if ws is None else ws
+    aircache_shared_decode(prob, ws, stream)
+    if check:
+        _check_device(prob, ws, stream, "aircache_shared_decode")
     return prob.out

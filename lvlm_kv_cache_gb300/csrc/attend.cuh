@@ -31,4 +31,16 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
 int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AttendPart& part, uint8_t* ws,
                   int32_t* error, cudaStream_t s);
 
+// A result over other rows that a decode step joins with its own: fp32 outputs [S][h_q][head_dim] and log-sum-exps in
+// base 2 [S][h_q], of the first *num sequences (out == nullptr: of none).
+struct DecodePrior {
+  const float* out;
+  const float* lse2;
+  const int32_t* num;  // device
+};
+// aircache_paged_decode, joined with a prior result; and the workspace it takes (AIRCACHE_OK, or why not).
+int paged_decode_run(const aircache_paged_decode_problem* p, const DecodePrior& prior, void* ws, size_t ws_bytes,
+                     void* stream);
+int paged_decode_size(const aircache_paged_decode_problem* p, size_t& bytes);
+
 }  // namespace aircache

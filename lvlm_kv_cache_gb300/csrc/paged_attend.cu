@@ -35,6 +35,7 @@
 #include <cstring>
 
 #include "attend.cuh"
+#include "rowmma.cuh"
 #include "tmap.cuh"
 #include "umma.cuh"
 
@@ -44,11 +45,7 @@ namespace {
 constexpr int kAtKeys = 128;                  // rows of a key tile
 constexpr int kAtRows = 128;                  // query rows of a stream (TMEM lanes)
 constexpr int kAtMma = 8, kAtLoad = 9, kAtAux = 10;  // behind the eight softmax warps: MMA issue, keys and values,
-                                                     // queries and tails (warp 11 fills their warpgroup)
-constexpr int kAtThreads = 12 * 32;
-// Registers of a thread: 168 at launch; the softmax threads, which hold a row of 128 logits, take what the others give
-constexpr int kAtRegsSoft = 208, kAtRegsOther = 80;
-static_assert(256 * kAtRegsSoft + 128 * kAtRegsOther <= kAtThreads * 168, "within the launch's own registers");
+constexpr int kAtWiden = 12;                         // queries and tails; from 12 on four that widen int8 codes
 constexpr uint32_t kAtEnd = 2;                // places of the line for a unit's end
 constexpr float kAtSlack = 8.f;               // base-2 powers that a maximum may pass its reference by
 constexpr uint32_t kAtS = 0, kAtO = 256;      // TMEM columns: S of stream i at 128 i, O at 256 + 128 i
@@ -56,14 +53,21 @@ constexpr int kAtGroup = 16;                  // query heads of a KV head, at mo
 constexpr int kAtHeader = 256;                // workspace: error word
 constexpr long long kAtLong = 4 * kWaitCycles;  // waits that stand behind another warp's
 
-template <int D>
+template <int D, bool Q8>
 struct AtCfg {
+  static constexpr int kThreads = Q8 ? 512 : 352;
   static constexpr int kSlab = kAtKeys * 128;       // [128 rows][64 bf16]
   static constexpr int kTile = kSlab * (D / 64);
-  static constexpr int kStages = D == 128 ? 5 : 10;
-  static constexpr int kOffQ = 0;                   // two query tiles
+  static constexpr int kStages = (Q8 ? 3 : 5) * 128 / D;       // tiles of the ring
+  static constexpr int kCodeTile = kAtKeys * D;                // int8 rows: tiles of codes before them,
+  static constexpr int kCodeStages = Q8 ? (D == 128 ? 3 : 8) : 0;
+  static constexpr int kScaleStages = Q8 ? 4 : 0;              // and the scales of a key tile's keys and values
+  static constexpr int kWeights = Q8 ? 64 : 0;                 // column of S that the weights start at
+  static constexpr int kOffQ = 0;                              // two query tiles
   static constexpr int kOffRing = 2 * kTile;
-  static constexpr int kOffCtl = kOffRing + kStages * kTile;
+  static constexpr int kOffCodes = kOffRing + kStages * kTile;
+  static constexpr int kOffScales = kOffCodes + kCodeStages * kCodeTile;
+  static constexpr int kOffCtl = kOffScales + kScaleStages * 2 * kAtKeys * 4;
 };
 
 struct AtArgs {
@@ -118,6 +122,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=l"(reinterpret_cast<uint64_t&>(r))
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return r;
+}
+// Arrives `n` times.
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+// Two int8 codes (the bytes that `sel` picks) as two bf16, exactly: the low seven bits in the mantissa of 128 are
+// 128 + (c mod 128), and 128 is taken away again, or 256 where the sign bit is set.
+__device__ __forceinline__ uint32_t widen2_bf16(uint32_t c4, uint32_t sel) {
+  const uint32_t t = __byte_perm(c4, 0x43434343u, sel);
+  const uint32_t x = t & 0xff7fff7fu, y = (t & 0x00800080u) | 0x43004300u;
+  const __nv_bfloat162 r = __hsub2(reinterpret_cast<const __nv_bfloat162&>(x), reinterpret_cast<const __nv_bfloat162&>(y));
+  return reinterpret_cast<const uint32_t&>(r);
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -217,22 +233,45 @@ __device__ __forceinline__ bool narrow(const AtArgs& a, const AtUnit& u) { retur
 // Key tiles of stream i in a run.
 __device__ __forceinline__ int stream_tiles(bool nar, int count, int i) { return nar ? (count + 1 - i) / 2 : count; }
 
+// Ring entry pos of a run: whether it is a tile of values, and which of the run's tiles.  Wide: K0 V0 K1 V1 ..; narrow:
+// K0 K1 V0 K2 V1 .. (the streams' first logits come before the first weights).
+__device__ __forceinline__ bool entry_of(bool nar, int count, int pos, int& j) {
+  bool val;
+  if (!nar) {
+    val = pos & 1;
+    j = pos >> 1;
+  } else if (pos == 2 * count - 1) {
+    val = true;
+    j = count - 1;
+  } else {
+    val = pos > 0 && !(pos & 1);
+    j = val ? pos / 2 - 1 : (pos + 1) / 2;
+  }
+  return val;
+}
+
 struct AtScratch {
-  uint64_t sum[kAtThreads / 32];
+  uint64_t sum[16];
   AtRun run;
 };
+template <int D, bool Q8>
 struct AtCtl {
-  uint64_t full[10], empty[10];
-  uint64_t tail[10];  // of a stage that holds values to be cleared in part: its copies have landed
+  using C = AtCfg<D, Q8>;
+  static constexpr int kCodes = Q8 ? C::kCodeStages : 1, kScales = Q8 ? C::kScaleStages : 1;
+  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t tail[C::kStages];  // of a stage that holds values to be cleared in part: its copies have landed
+  uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scempty[kScales];
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], mlfull, mlfree, done;
   uint32_t tmem;
   float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
   AtScratch scratch;
 };
 // By all threads of the CTA; false if the CTA has no place.
+template <int THREADS>
 __device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
+  static_assert(THREADS <= 512, "warps' sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (a.slots + kAtThreads - 1) / kAtThreads;
+  const int each = (a.slots + THREADS - 1) / THREADS;
   const int s0 = min(tid * each, a.slots), s1 = min(s0 + each, a.slots);
   uint64_t mine = 0;
   int seq0 = 0;
@@ -254,7 +293,7 @@ __device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
   __syncthreads();
   uint64_t before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kAtThreads / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += sc->sum[w];
     total += sc->sum[w];
   }
@@ -361,23 +400,32 @@ __device__ __forceinline__ void write_out(const AtArgs& a, int64_t token, int he
 
 // ------------------------------------------------------------------ the attention
 
-template <int D>
-__global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __grid_constant__ CUtensorMap qmap,
+template <int D, bool Q8>
+__global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                      const __grid_constant__ CUtensorMap kmap,
                                                                      const __grid_constant__ CUtensorMap vmap,
                                                                      const __grid_constant__ AtArgs a) {
-  using C = AtCfg<D>;
+  using C = AtCfg<D, Q8>;
+  using Ctl = AtCtl<D, Q8>;
   extern __shared__ uint8_t at_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
-  AtCtl* ctl = reinterpret_cast<AtCtl*>(sm + C::kOffCtl);
+  Ctl* ctl = reinterpret_cast<Ctl*>(sm + C::kOffCtl);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Pages& p = a.pages;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->full[i], Q8 ? 4 : 1);
       mbar_init(&ctl->empty[i], 1);
       mbar_init(&ctl->tail[i], 1);
+    }
+    for (int i = 0; i < C::kCodeStages; ++i) {
+      mbar_init(&ctl->cfull[i], 1);
+      mbar_init(&ctl->cempty[i], 4);
+    }
+    for (int i = 0; i < C::kScaleStages; ++i) {
+      mbar_init(&ctl->scfull[i], 1);
+      mbar_init(&ctl->scempty[i], 8);
     }
     mbar_init(&ctl->qfull, 1);
     mbar_init(&ctl->qempty, 1);
@@ -405,7 +453,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
   pdl_trigger();
   if (blockIdx.x == 0) {  // what the batch's description says that cannot be
     bool bad = tid == 0 && a.cu[0] < 0;
-    for (int s = tid; s < p.num_seqs; s += kAtThreads) {
+    for (int s = tid; s < p.num_seqs; s += C::kThreads) {
       const int c0 = a.cu[s], c1 = a.cu[s + 1], len = p.lens[s];
       bad |= c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
     }
@@ -413,19 +461,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
   }
   tc_fence_before();
   AtRun r;
-  const bool any = make_run(a, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+  const bool any = make_run<C::kThreads>(a, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  if (warp >= kAtMma)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kAtRegsOther));
-  else
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kAtRegsSoft));
 
   if (warp == kAtLoad) {
     // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
     // and the odd chunks: the next chunk's are looked up while this one is copied
     const int boxes = kAtKeys / a.box, per_chunk = 32 / boxes;  // boxes of a tile, tiles of a chunk
-    uint32_t n = 0;                                             // ring entries so far
+    uint32_t n = 0, tiles = 0;  // entries and key tiles so far
     bool ok = true;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
       if (r.count == 0) continue;
@@ -441,19 +485,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
         return (int)p.num_pages;  // (behind the tensor: its rows arrive as zeros)
       };
       int even = look(0), odd = look(1);
-      for (int pos = 0; pos < 2 * r.count && ok; ++pos, ++n) {
-        bool val;
+      for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
         int j;  // the key tile within the run
-        if (!nar) {
-          val = pos & 1;
-          j = pos >> 1;
-        } else if (pos == 2 * r.count - 1) {
-          val = true;
-          j = r.count - 1;
-        } else {
-          val = pos > 0 && !(pos & 1);
-          j = val ? pos / 2 - 1 : (pos + 1) / 2;
-        }
+        const bool val = entry_of(nar, r.count, pos, j);
         const int chunk = j / per_chunk, in_chunk = j - chunk * per_chunk;
         if (val && in_chunk == 0 && chunk > 0) {  // keys are at most two tiles ahead of values, a chunk four or more
           if (chunk & 1)
@@ -461,32 +495,65 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
           else
             odd = look(chunk + 1);
         }
-        const uint32_t st = n % C::kStages;
-        if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
-        if (!ok) break;
-        const int slabs = D / 64;
-        const int box = lane / slabs, slab = lane % slabs;
-        const int page = __shfl_sync(0xffffffffu, chunk & 1 ? odd : even, (in_chunk * boxes + box) & 31);
         const int row0 = (tile0 + j) * kAtKeys;
-        const bool mine = lane < boxes * slabs && page >= 0;
-        const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine));
-        // values behind the last row are cleared by another warp, which then says that the tile is there
-        const bool tail = val && (int64_t)row0 + kAtKeys > r.u.rows;
-        uint64_t* bar = tail ? &ctl->tail[st] : &ctl->full[st];
-        if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(a.box * 128));
-        __syncwarp();
-        if (mine) {
+        const int pages = chunk & 1 ? odd : even;
+        if constexpr (Q8) {
+          // codes to their own ring, from where they are widened into the tiles' one; with a tile's keys its scales
+          const uint32_t st = n % C::kCodeStages;
+          if (n >= C::kCodeStages) ok = mbar_wait_warp(&ctl->cempty[st], (n / C::kCodeStages + 1) & 1, kAtLong);
+          const uint32_t sc = (tiles + j) % C::kScaleStages, turn = (tiles + j) / C::kScaleStages;
+          if (ok && !val && turn > 0) ok = mbar_wait_warp(&ctl->scempty[sc], (turn + 1) & 1, kAtLong);
+          if (!ok) break;
+          const int page = __shfl_sync(0xffffffffu, pages, (in_chunk * boxes + lane % boxes) & 31);
+          const int at = (row0 + lane % boxes * a.box) % p.page_rows;
+          const bool mine = lane < boxes && page >= 0;
+          const bool scale = !val && lane < 2 * boxes && page >= 0, there = scale && page < p.num_pages;
+          const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine)), scales = __popc(__ballot_sync(0xffffffffu, there));
+          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 2 + lane / boxes) * kAtKeys + lane % boxes * a.box;
+          if (scale && !there)  // (of a page out of bounds)
+            for (int e = 0; e < a.box; ++e) to[e] = 0.f;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&ctl->cfull[st], count * (uint32_t)(a.box * D));
+            if (!val) mbar_arrive_expect_tx(&ctl->scfull[sc], scales * (uint32_t)(a.box * 4));
+          }
+          __syncwarp();
           fence_proxy_async_smem();
-          tma_load_5d(base + C::kOffRing + st * C::kTile + slab * C::kSlab + box * a.box * 128, val ? &vmap : &kmap, 0,
-                      (row0 + box * a.box) % p.page_rows, slab, r.h, page, bar);
+          if (mine)
+            tma_load_4d(base + C::kOffCodes + st * C::kCodeTile + lane * a.box * D, val ? &vmap : &kmap, 0, at, r.h, page,
+                        &ctl->cfull[st]);
+          if (there)
+            bulk_g2s(to, (lane < boxes ? p.k_scale : p.v_scale) + page_slot(p, page, r.h, at), a.box * 4, &ctl->scfull[sc]);
+        } else {
+          const uint32_t st = n % C::kStages;
+          if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
+          if (!ok) break;
+          const int slabs = D / 64;
+          const int box = lane / slabs, slab = lane % slabs;
+          const int page = __shfl_sync(0xffffffffu, pages, (in_chunk * boxes + box) & 31);
+          const bool mine = lane < boxes * slabs && page >= 0;
+          const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine));
+          // values behind the last row are cleared by another warp, which then says that the tile is there
+          const bool tail = val && (int64_t)row0 + kAtKeys > r.u.rows;
+          uint64_t* bar = tail ? &ctl->tail[st] : &ctl->full[st];
+          if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(a.box * 128));
+          __syncwarp();
+          if (mine) {
+            fence_proxy_async_smem();
+            tma_load_5d(base + C::kOffRing + st * C::kTile + slab * C::kSlab + box * a.box * 128, val ? &vmap : &kmap, 0,
+                        (row0 + box * a.box) % p.page_rows, slab, r.h, page, bar);
+          }
         }
       }
+      tiles += r.count;
     }
     if (!ok) {
-      set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
       // the copies in flight land before the CTA's shared memory is another's
-      for (uint32_t f = n > C::kStages ? n - C::kStages : 0; f < n; ++f)
-        (void)mbar_wait_warp(&ctl->full[f % C::kStages], (f / C::kStages) & 1);
+      set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      constexpr uint32_t kRing = Q8 ? C::kCodeStages : C::kStages;
+      uint64_t* bars = Q8 ? ctl->cfull : ctl->full;
+      for (uint32_t f = n > kRing ? n - kRing : 0; f < n; ++f) (void)mbar_wait_warp(&bars[f % kRing], (f / kRing) & 1);
+      for (uint32_t f = 0; Q8 && f < C::kScaleStages && f <= tiles; ++f) (void)mbar_wait_warp(&ctl->scfull[f], 0);
     }
   } else if (warp == kAtAux) {
     // ---- queries, and the values behind a sequence's last row
@@ -509,7 +576,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
       __syncwarp();
       ++units;
       const int64_t last = (int64_t)(r.u.t0 + r.first + r.count) * kAtKeys;
-      if (last > r.u.rows) {
+      if (!Q8 && last > r.u.rows) {
         const uint32_t st = (n + 2 * r.count - 1) % C::kStages;  // a run's last entry
         ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
         if (!ok) break;
@@ -572,7 +639,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
           const uint32_t vb = base + C::kOffRing + st * C::kTile;
 #pragma unroll
           for (int kk = 0; kk < kAtKeys / 16; ++kk)
-            umma_bf16_ts(tmem + kAtO + 128 * i, tmem + kAtS + 128 * i + 8 * kk,
+            umma_bf16_ts(tmem + kAtO + 128 * i, tmem + kAtS + 128 * i + C::kWeights + 8 * kk,
                          umma_desc_sw128_mn(vb + kk * 16 * 128, C::kSlab, 1024), id_o, k >= 2 || kk > 0);
           if (nar || i == 1) umma_commit(&ctl->empty[st]);
           if (k + 2 >= turns) umma_commit(&ctl->ofull[i]);
@@ -584,14 +651,53 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
       umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
       (void)mbar_wait(&ctl->done, 0);
     }
+  } else if (Q8 && warp >= kAtWiden) {
+    // ---- int8 codes become bf16 tiles, a row to a thread; value rows behind the sequence's last are zeros
+    uint32_t n = 0;
+    bool ok = true;
+    const int row = tid - kAtWiden * 32;
+    for (bool more = any; more && ok; more = next_unit(a, r)) {
+      if (r.count == 0) continue;
+      const bool nar = narrow(a, r.u);
+      for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
+        int j;
+        const bool val = entry_of(nar, r.count, pos, j);
+        const uint32_t cs = n % (Q8 ? C::kCodeStages : 1), st = n % C::kStages;
+        ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
+        if (ok && n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
+        if (!ok) break;
+        const uint8_t* from = sm + C::kOffCodes + cs * C::kCodeTile;
+        uint8_t* to = sm + C::kOffRing + st * C::kTile + row * 128;
+        const bool zero = val && (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint4 x = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * c));
+          if (zero) x = make_uint4(0, 0, 0, 0);
+          uint8_t* slab = to + (c >> 2) * C::kSlab;
+          *reinterpret_cast<uint4*>(slab + (((2 * c) & 7) ^ (row & 7)) * 16) =
+              make_uint4(widen2_bf16(x.x, 0x4140u), widen2_bf16(x.x, 0x4342u), widen2_bf16(x.y, 0x4140u),
+                         widen2_bf16(x.y, 0x4342u));
+          *reinterpret_cast<uint4*>(slab + (((2 * c + 1) & 7) ^ (row & 7)) * 16) =
+              make_uint4(widen2_bf16(x.z, 0x4140u), widen2_bf16(x.z, 0x4342u), widen2_bf16(x.w, 0x4140u),
+                         widen2_bf16(x.w, 0x4342u));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->full[st]);
+          mbar_arrive(&ctl->cempty[cs]);
+        }
+      }
+    }
+    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
   } else if (warp < kAtMma) {
     // ---- softmax: stream i, query row `row` (its TMEM lane)
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = tl + kAtS + 128 * i;
+    const uint32_t ts = tl + kAtS + 128 * i, tp = ts + AtCfg<D, Q8>::kWeights;  // logits; the weights over them
     if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (until a run says otherwise)
     const int tok = row / a.group, hh = row - tok * a.group;
-    uint32_t it_s = 0, it_o = 0, joins = 0;
+    uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
     bool ok = true;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
       const bool nar = narrow(a, r.u);
@@ -621,61 +727,131 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
         }
         ++it_s;
         tc_fence_after();
+        const int j = nar ? 2 * it + i : it;
+        const int k0 = (r.u.t0 + r.first + j) * kAtKeys;
+        const uint32_t sc = Q8 ? (tiles0 + j) % (Q8 ? C::kScaleStages : 1) : 0;
+        if constexpr (Q8) {
+          ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles0 + j) / C::kScaleStages) & 1, kAtLong);
+          if (!ok) break;
+        }
         if (!idle) {
-          const int k0 = (r.u.t0 + r.first + (nar ? 2 * it + i : it)) * kAtKeys;
-          float v[kAtKeys];
+          const bool masked = !__all_sync(0xffffffffu, lo <= k0 && hi - k0 >= kAtKeys);
+          const int from = lo - k0;
+          const uint32_t wide = (uint32_t)(hi - lo);
+          const float* ks = reinterpret_cast<const float*>(sm + C::kOffScales) + sc * 2 * kAtKeys;
+          // moves the reference to a maximum that passes it by more than the slack
+          auto refer = [&](float top) {
+            const float mx = top * a.scale_log2;
+            if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
+              const float to = fmaxf(m, mx), f = fast_exp2(m - to);
+              m = to;
+              sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
+              if (it > 0) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v + 32 * c);
-          tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, lo <= k0 && hi - k0 >= kAtKeys)) {
-            const int from = lo - k0;
-            const uint32_t wide = (uint32_t)(hi - lo);
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(tl + kAtO + 128 * i + c, o);
+                  tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kAtKeys; ++c)
-              if ((uint32_t)(c - from) >= wide) v[c] = -INFINITY;
-          }
-          float top[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-          for (int c = 4; c < kAtKeys; c += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-          if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
-            const float to = fmaxf(m, mx), f = fast_exp2(m - to);
-            m = to;
-            sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
-            if (it > 0) {
-#pragma unroll
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tmem_ld16(tl + kAtO + 128 * i + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] *= f;
-                tmem_st16(tl + kAtO + 128 * i + c, o);
+                  for (int e = 0; e < 16; ++e) o[e] *= f;
+                  tmem_st16(tl + kAtO + 128 * i + c, o);
+                }
               }
             }
-          }
-          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), ref2 = make_float2(-m, -m);
+          };
+          const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+          if constexpr (!Q8) {
+            float v[kAtKeys];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[32];
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v + 32 * c);
+            tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float2 x = fma2(make_float2(v[64 * half + 2 * c], v[64 * half + 2 * c + 1]), scale2, ref2);
-              const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              sum[c & 1] = add2(sum[c & 1], e);
-              w[c] = pack2(e.x, e.y);
+              for (int c = 0; c < kAtKeys; ++c)
+                if ((uint32_t)(c - from) >= wide) v[c] = -INFINITY;
             }
-            tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
+            float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int c = 4; c < kAtKeys; c += 4)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
+            refer(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const float2 ref2 = make_float2(-m, -m);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const float2 x = fma2(make_float2(v[64 * half + 2 * c], v[64 * half + 2 * c + 1]), scale2, ref2);
+                const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                sum[c & 1] = add2(sum[c & 1], e);
+                w[c] = pack2(e.x, e.y);
+              }
+              tmem_st32(tp + 32 * half, reinterpret_cast<const float*>(w));
+            }
+          } else {
+            // 32 logits at a time, twice (128 registers a thread); the last 32 stay from the first pass to the second,
+            // which goes backwards and writes the weights from the buffer's end on
+            float v[32];
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto logits = [&](int c) {
+              tmem_ld32(ts + 32 * c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * c + e);
+                v[e] *= k4.x, v[e + 1] *= k4.y, v[e + 2] *= k4.z, v[e + 3] *= k4.w;
+              }
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if ((uint32_t)(32 * c + e - from) >= wide) v[e] = -INFINITY;
+              }
+            };
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              logits(c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[e]);
+            }
+            refer(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const float2 ref2 = make_float2(-m, -m);
+#pragma unroll 1
+            for (int c = 3; c >= 0; --c) {
+              if (c < 3) logits(c);
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float2 x = fma2(make_float2(v[e], v[e + 1]), scale2, ref2);
+                const float2 y = fma2(make_float2(v[e + 2], v[e + 3]), scale2, ref2);
+                const float4 z = make_float4(fast_exp2(x.x), fast_exp2(x.y), fast_exp2(y.x), fast_exp2(y.y));
+                sum[0] = add2(sum[0], make_float2(z.x, z.y));
+                sum[1] = add2(sum[1], make_float2(z.z, z.w));
+                const float4 v4 = *reinterpret_cast<const float4*>(ks + kAtKeys + 32 * c + e);
+                float u[4] = {z.x * v4.x, z.y * v4.y, z.z * v4.z, z.w * v4.w};
+                if (masked) {  // (a scale may be anything there)
+#pragma unroll
+                  for (int f = 0; f < 4; ++f)
+                    if ((uint32_t)(32 * c + e + f - from) >= wide) u[f] = 0.f;
+                }
+                w[e / 2] = pack2(u[0], u[1]);
+                w[e / 2 + 1] = pack2(u[2], u[3]);
+              }
+              tmem_st16(tp + 16 * c, reinterpret_cast<const float*>(w));
+            }
           }
           tmem_wait_st();
           tc_fence_before();
+        }
+        if constexpr (Q8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(&ctl->scempty[sc], nar ? 2 : 1);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->pfull[i]);
       }
       if (!ok) break;
+      tiles0 += r.count;
       float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (tiles > 0) {
         if (!mbar_wait_warp(&ctl->ofull[i], it_o & 1, kAtLong)) {
@@ -745,7 +921,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) paged_attend_kernel(const __gri
         if (valid && cut) a.part_ml[slot] = make_float2(m, l);
         if (valid && !cut) write_lse(a, token, head, m, l);
         if (!cut) {
-          uint32_t rows = __ballot_sync(0xffffffffu, valid && bad && finite(l));
+          uint32_t rows = Q8 ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
           while (rows) {
             const int from = __ffs(rows) - 1;
             rows &= rows - 1;
@@ -859,7 +1035,7 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
       o[e] = l == 0.f ? 0.f : o[e] * inv;
       bad |= !finite(o[e]);
     }
-    if (__any_sync(0xffffffffu, bad) && finite(l)) {
+    if (!a.pages.k_scale && __any_sync(0xffffffffu, bad) && finite(l)) {
       int lo, hi;
       token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
       repair_row<D>(a, u.s, cut.y, token, head, lo, hi, m, l, o);
@@ -881,11 +1057,20 @@ int box_rows(int page_rows) {  // the largest power of two up to 128 that divide
   return b;
 }
 
-// Boxes of as many rows of one page and KV head, one 128-byte slab of them.
+// Boxes of as many rows of one page and KV head, one 128-byte slab of them (int8 rows: whole).
 bool encode_kv(CUtensorMap* m, const void* base, const AttendPlan& pl) {
   auto enc = tma_encoder();
   if (!enc) return false;
   const Pages& p = pl.pages;
+  if (pl.q8) {
+    cuuint64_t dims[4] = {(cuuint64_t)pl.d, (cuuint64_t)p.page_rows, (cuuint64_t)p.h_kv, (cuuint64_t)p.num_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)p.stride_row, (cuuint64_t)p.stride_head, (cuuint64_t)p.stride_page};
+    cuuint32_t box[4] = {(cuuint32_t)pl.d, (cuuint32_t)box_rows(p.page_rows), 1, 1}, es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, pl.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               pl.d == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   cuuint64_t dims[5] = {64, (cuuint64_t)p.page_rows, (cuuint64_t)pl.d / 64, (cuuint64_t)p.h_kv, (cuuint64_t)p.num_pages};
   cuuint64_t strides[4] = {(cuuint64_t)p.stride_row * 2, 128, (cuuint64_t)p.stride_head * 2, (cuuint64_t)p.stride_page * 2};
   cuuint32_t box[5] = {64, (cuuint32_t)box_rows(p.page_rows), 1, 1, 1}, es[5] = {1, 1, 1, 1, 1};
@@ -907,20 +1092,21 @@ bool encode_q(CUtensorMap* m, const aircache_paged_attend_problem* p, const Atte
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool Q8>
 int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AtArgs& a, cudaStream_t s) {
+  using C = AtCfg<D, Q8>;
   CUtensorMap qm, km, vm;
   if (!encode_q(&qm, p, pl) || !encode_kv(&km, pl.pages.k, pl) || !encode_kv(&vm, pl.pages.v, pl))
     return AIRCACHE_ERR_UNSUPPORTED;
-  constexpr int smem = AtCfg<D>::kOffCtl + (int)sizeof(AtCtl) + 1024;
+  constexpr int smem = C::kOffCtl + (int)sizeof(AtCtl<D, Q8>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   if (a.range && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
                             dim3(kArThreads), 0, s, a) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid);
-  cfg.blockDim = dim3(kAtThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -928,7 +1114,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   return launch_pdl(attend_finish_kernel<D>, dim3(pl.grid * kAfSplit), dim3(kAfThreads), 0, s, a) == cudaSuccess
              ? AIRCACHE_OK
              : AIRCACHE_ERR_CUDA;
@@ -962,7 +1148,7 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
     };
     const size_t nq = bytes(many_t ? p->q_stride_tok : 0, many_h ? p->q_stride_head : 0);
     const size_t no = bytes(many_t ? st : 0, many_h ? sh : 0), nl = 4 * (size_t)p->num_tokens * p->h_q;
-    const size_t nk = 2 * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;  // (to the last page, at least)
+    const size_t nk = (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2) * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;  // (to the last page, at least)
     if (arrays_meet(p->out, no, p->q, nq) || arrays_meet(p->out, no, pl.pages.k, nk) ||
         arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq))
       return AIRCACHE_ERR_INVALID_ARG;
@@ -971,7 +1157,7 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
   pl.h_q = p->h_q;
   pl.g = p->h_q / p->pages->h_kv;
   pl.q8 = p->pages->kv_dtype == AIRCACHE_INT8;
-  if (pl.g > kAtGroup || pl.q8) return AIRCACHE_ERR_UNSUPPORTED;
+  if (pl.g > kAtGroup) return AIRCACHE_ERR_UNSUPPORTED;
   pl.tok_tile = kAtRows / pl.g;
   pl.slots = (int)(p->num_tokens / (2 * pl.tok_tile)) + p->pages->num_seqs;
   pl.grid = device_sms();
@@ -1014,7 +1200,8 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.rows_cap = pl.rows_cap;
   a.box = box_rows(pl.pages.page_rows);
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
-  return pl.d == 128 ? launch_at<128>(p, pl, a, s) : launch_at<64>(p, pl, a, s);
+  if (pl.q8) return pl.d == 128 ? launch_at<128, true>(p, pl, a, s) : launch_at<64, true>(p, pl, a, s);
+  return pl.d == 128 ? launch_at<128, false>(p, pl, a, s) : launch_at<64, false>(p, pl, a, s);
 }
 
 }  // namespace aircache

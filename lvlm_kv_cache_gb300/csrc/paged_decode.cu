@@ -56,6 +56,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "attend.cuh"
 #include "pages.cuh"
 #include "rowmma.cuh"
 #include "tmap.cuh"
@@ -90,6 +91,12 @@ struct PdCfg {
 // by the instructions that widen them: a third CTA gives them more warps to issue from.
 constexpr int ctas_per_sm(bool q8, int group) { return q8 && group <= 8 ? 3 : 2; }
 
+// A query head's result under the reference m and the sum l next to what it joins: factors of the two, and the
+// log-sum-exp in base 2 (-inf: no rows).
+struct Joint {
+  float own, prior, lse2;
+};
+
 // What the mass kernel needs of a tile: its place, and its pieces' pages (-1: not there).
 struct TileInfo {
   int s, h, i, pad;
@@ -108,6 +115,7 @@ struct PdArgs {
   int2* cut;         // [CTAs]: the unit that begins in the CTA and ends in another (-1: none), and its parts
   int2* unit;        // [S * h_kv]: the first CTA that has a part of it, and how many have one
   float* lse2;       // [S * h_q] base 2, of units that one CTA has whole
+  DecodePrior prior; // a result over other rows that each sequence's joins
   float4* part_ml;   // [2 CTAs][g]: m, l, n of O
   float* part_o;     // [2 CTAs][g][D]
   TileInfo* info;    // [tiles]
@@ -132,6 +140,58 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ int rows_of(const Pages& p, int s) {
   const int n = p.lens[s];
   return n >= 0 && n <= p.max_rows ? n : 0;
+}
+
+// `head` of the batch's S * h_q.  Without a prior result there is nothing to form (own = 1).
+__device__ __forceinline__ Joint joint(const PdArgs& a, int64_t head, float m, float l) {
+  Joint j = {1.f, 0.f, l == 0.f ? -INFINITY : m + log2f(l)};
+  if (head < (int64_t)*a.prior.num * a.h_q) {
+    const float p = a.prior.lse2[head];
+    if (p != -INFINITY) {
+      const float top = fmaxf(j.lse2, p);  // (a NaN stays one in the factor of its own)
+      const float x = fast_exp2(j.lse2 - top), y = fast_exp2(p - top), z = x + y;
+      j.own = x / z;
+      j.prior = y / z;
+      j.lse2 = top + log2f(z);
+    }
+  }
+  return j;
+}
+// Four columns of a head's output: y times f is the result over its own rows.
+template <int D>
+__device__ __forceinline__ float4 join_prior(const PdArgs& a, const Joint& j, int64_t head, int d, float4 y) {
+  y.x *= j.own, y.y *= j.own, y.z *= j.own, y.w *= j.own;
+  if (j.prior != 0.f) {
+    const float4 p = *reinterpret_cast<const float4*>(a.prior.out + head * D + d);
+    y.x = fmaf(p.x, j.prior, y.x);
+    y.y = fmaf(p.y, j.prior, y.y);
+    y.z = fmaf(p.z, j.prior, y.z);
+    y.w = fmaf(p.w, j.prior, y.w);
+  }
+  return y;
+}
+// Writes four columns, and with the first of them the log-sum-exp.  f: what makes y the result over the own rows.
+template <int D>
+__device__ __forceinline__ void write_columns(const PdArgs& a, int64_t head, int d, float4 y, float f, float m, float l,
+                                              bool lse2 = false) {
+  y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+  float top = 0.f;
+  if (a.prior.out) {
+    const Joint j = joint(a, head, m, l);
+    y = join_prior<D>(a, j, head, d, y);
+    top = j.lse2;
+  } else if (d == 0) {
+    top = l == 0.f ? -INFINITY : m + log2f(l);
+  }
+  const __nv_bfloat162 x[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+  *reinterpret_cast<uint2*>(a.out + head * D + d) = *reinterpret_cast<const uint2*>(x);
+  if (d == 0 && a.lse) a.lse[head] = top * 0.69314718055994531f;
+  if (d == 0 && lse2) a.lse2[head] = top == -INFINITY ? INFINITY : top;
+}
+// The log-sum-exp that turns a head's logits into weights (inf: none has one).
+__device__ __forceinline__ float mass_lse2(const PdArgs& a, int64_t head, float m, float l) {
+  const float x = a.prior.out ? joint(a, head, m, l).lse2 : l == 0.f ? -INFINITY : m + log2f(l);
+  return x == -INFINITY ? INFINITY : x;
 }
 
 // How the batch's tiles are dealt out: the units (the sequences' KV heads) lie
@@ -436,9 +496,8 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   // sequences without rows: out = 0, lse = -inf
   for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
-    for (int i = tid; i < a.h_q * D / 8; i += kPdWarps * 32)
-      *reinterpret_cast<uint4*>(a.out + (int64_t)s * a.h_q * D + i * 8) = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < a.h_q && a.lse; i += kPdWarps * 32) a.lse[(int64_t)s * a.h_q + i] = -INFINITY;
+    for (int i = tid; i < a.h_q * (D / 4); i += kPdWarps * 32)
+      write_columns<D>(a, (int64_t)s * a.h_q + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
     for (int i = tid; i < p.h_kv && !SHORT; i += kPdWarps * 32) a.unit[s * p.h_kv + i] = make_int2(0, 0);
   }
   int st = 0;
@@ -816,16 +875,14 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           for (int e = 0; e < 4; ++e) y[e] += j < a.ranks ? f * x[j][e] : 0.f;
         }
         const float f = ll == 0.f ? 0.f : kUndo * fast_exp2(nn - mm) / ll;
-        const __nv_bfloat162 w[2] = {__floats2bfloat162_rn(y[0] * f, y[1] * f), __floats2bfloat162_rn(y[2] * f, y[3] * f)};
-        *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(w);
-        if (d == 0 && a.lse) a.lse[head0 + hh] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+        write_columns<D>(a, head0 + hh, d, make_float4(y[0], y[1], y[2], y[3]), f, mm, ll);
       }
       if (a.mass_out) {
         const int hh = tid - 3 * 32;
         if (hh >= 0 && hh < g) {
           float m[kRanks], l[kRanks], n[kRanks], mm, ll, nn;
           heads(hh, m, l, n, mm, ll, nn);
-          lse2[hh] = ll == 0.f ? INFINITY : mm + log2f(ll);
+          lse2[hh] = mass_lse2(a, head0 + hh, mm, ll);
         }
         named_bar_sync(1, kPdWarps * 32);  // (and the CTA's logits are written)
         for (int i = tid; i < (int)r.count * kPdRows; i += kPdWarps * 32) {
@@ -856,20 +913,15 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       a.unit[r.s * p.h_kv + r.h] = make_int2(c0, parts);
       if (parts > 1) a.cut[blockIdx.x] = make_int2(r.s * p.h_kv + r.h, parts);
     }
-    auto finish = [&](int hh, float m, float l) {  // the head's log-sum-exp
-      if (a.lse) a.lse[head0 + hh] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-      if (a.mass_out) a.lse2[head0 + hh] = l == 0.f ? INFINITY : m + log2f(l);
-    };
     if (r.count == r.tiles) {
       for (int c = tid; c < g * (D / 4); c += kPdWarps * 32) {
         const int hh = c / (D / 4), d = c % (D / 4) * 4;
         float m, l, n;
         joined(hh, m, l, n);
         const float f = l == 0.f ? 0.f : kUndo * fast_exp2(n - m) / l;
-        __nv_bfloat162 x[2] = {__floats2bfloat162_rn(joined_o(hh, d) * f, joined_o(hh, d + 1) * f),
-                               __floats2bfloat162_rn(joined_o(hh, d + 2) * f, joined_o(hh, d + 3) * f)};
-        *reinterpret_cast<uint2*>(a.out + (head0 + hh) * D + d) = *reinterpret_cast<const uint2*>(x);
-        if (d == 0) finish(hh, m, l);
+        write_columns<D>(a, head0 + hh, d,
+                         make_float4(joined_o(hh, d), joined_o(hh, d + 1), joined_o(hh, d + 2), joined_o(hh, d + 3)), f, m,
+                         l, a.mass_out != nullptr);
       }
       continue;
     }
@@ -939,10 +991,7 @@ __device__ __forceinline__ Joined join_parts(const PdArgs& a, int c0, int parts,
 template <int D>
 __device__ __forceinline__ void write_joined(const PdArgs& a, const Joined& r, int unit, int hh, int d, float undo) {
   const float f = r.l == 0.f ? 0.f : undo * fast_exp2(r.n - r.m) / r.l;
-  const __nv_bfloat162 x[2] = {__floats2bfloat162_rn(r.o.x * f, r.o.y * f), __floats2bfloat162_rn(r.o.z * f, r.o.w * f)};
-  const int64_t head = (int64_t)unit * a.group + hh;  // (s h_kv + h) g + hh = s h_q + h g + hh
-  *reinterpret_cast<uint2*>(a.out + head * D + d) = *reinterpret_cast<const uint2*>(x);
-  if (d == 0 && a.lse) a.lse[head] = r.l == 0.f ? -INFINITY : (r.m + log2f(r.l)) * 0.69314718055994531f;
+  write_columns<D>(a, (int64_t)unit * a.group + hh, d, r.o, f, r.m, r.l);  // (s h_kv + h) g + hh = s h_q + h g + hh
 }
 
 // After the attention.  Joins the parts of the units that several CTAs shared.
@@ -1055,7 +1104,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
         for (int off = width; off < 32; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
         l = m == -INFINITY ? 0.f : l * fast_exp2(m - m1);
         for (int off = width; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        lse = l == 0.f ? INFINITY : m1 + log2f(l);
+        lse = mass_lse2(a, (int64_t)u * g + hh, m1, l);
       }
     }
     float2 sum = make_float2(0.f, 0.f);
@@ -1210,18 +1259,9 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
-}  // namespace aircache
 
-using namespace aircache;
-
-extern "C" {
-
-size_t aircache_paged_decode_workspace_size(const aircache_paged_decode_problem* p) {
-  PdPlan pl;
-  return pd_plan(p, pl) == AIRCACHE_OK ? pl.total : 0;
-}
-
-int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size_t ws_bytes, void* stream) {
+int paged_decode_run(const aircache_paged_decode_problem* p, const DecodePrior& prior, void* ws, size_t ws_bytes,
+                     void* stream) {
   PdPlan pl;
   const int rc = pd_plan(p, pl);
   if (rc != AIRCACHE_OK) return rc;
@@ -1246,6 +1286,7 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   a.part_o = reinterpret_cast<float*>(w + pl.o_off);
   a.info = reinterpret_cast<TileInfo*>(w + pl.info_off);
   a.logits = reinterpret_cast<float*>(w + pl.lg_off);
+  a.prior = prior;
   a.total_rows = p->total_rows;
   a.h_q = p->h_q;
   a.group = pl.g;
@@ -1255,6 +1296,28 @@ int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pl.q8) return pl.d == 128 ? launch_pd<128, true>(pl, a, s) : launch_pd<64, true>(pl, a, s);
   return pl.d == 128 ? launch_pd<128, false>(pl, a, s) : launch_pd<64, false>(pl, a, s);
+}
+
+int paged_decode_size(const aircache_paged_decode_problem* p, size_t& bytes) {
+  PdPlan pl;
+  const int rc = pd_plan(p, pl);
+  bytes = pl.total;
+  return rc;
+}
+
+}  // namespace aircache
+
+using namespace aircache;
+
+extern "C" {
+
+size_t aircache_paged_decode_workspace_size(const aircache_paged_decode_problem* p) {
+  PdPlan pl;
+  return pd_plan(p, pl) == AIRCACHE_OK ? pl.total : 0;
+}
+
+int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size_t ws_bytes, void* stream) {
+  return paged_decode_run(p, DecodePrior{nullptr, nullptr, nullptr}, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

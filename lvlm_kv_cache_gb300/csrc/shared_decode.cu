@@ -1,0 +1,82 @@
+// One decode step of a batch whose sequences share prefixes (aircache_shared_decode).
+//
+// Softmax over a prefix's rows and a sequence's own, put together from the two halves:
+//   o = (2^{L_p} o_p + 2^{L_o} o_o) / (2^{L_p} + 2^{L_o}),  L = log2 sum 2^x.
+// A prefix's rows are read once for all sequences that share it: their queries are the tokens of one attention
+// without a mask over the prefix (paged_attend.cu; 128 query rows to a tile of keys, where the decode kernel reads
+// every row again for each sequence), whose fp32 results the decode step over the own rows (paged_decode.cu) joins
+// where it writes its outputs, log-sum-exps and mass.
+#include "attend.cuh"
+
+namespace aircache {
+namespace {
+
+struct SdPlan {
+  aircache_paged_attend_problem at;
+  AttendPlan attend;
+  size_t attend_off, out_off, lse_off, total;
+};
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int sd_plan(const aircache_shared_decode_problem* p, SdPlan& pl) {
+  if (!p || !p->prefix) return AIRCACHE_ERR_INVALID_ARG;
+  size_t own = 0;
+  int rc = paged_decode_size(&p->own, own);
+  if (rc != AIRCACHE_OK) return rc;
+  const aircache_pages* o = p->own.pages;
+  if (p->prefix->h_kv != o->h_kv || p->prefix->head_dim != o->head_dim) return AIRCACHE_ERR_INVALID_ARG;
+  pl.attend_off = up256(own);
+  pl.total = pl.attend_off;
+  if (p->prefix->num_seqs == 0) return AIRCACHE_OK;  // (its arrays have no elements, and need no address)
+  pl.at = aircache_paged_attend_problem{};
+  pl.at.pages = p->prefix;
+  pl.at.num_tokens = o->num_seqs;
+  pl.at.h_q = p->own.h_q;
+  pl.at.dtype = p->own.dtype;
+  pl.at.scale = p->own.scale;
+  pl.at.cu_tokens = p->cu_seqs;
+  pl.at.q = p->own.q;
+  pl.at.q_stride_tok = p->own.q_stride_seq;
+  pl.at.q_stride_head = p->own.q_stride_head;
+  rc = attend_plan(&pl.at, true, pl.attend);
+  if (rc != AIRCACHE_OK) return rc;
+  const size_t heads = (size_t)o->num_seqs * p->own.h_q;
+  pl.out_off = pl.attend_off + pl.attend.total;
+  pl.lse_off = pl.out_off + up256(sizeof(float) * heads * o->head_dim);
+  pl.total = pl.lse_off + up256(sizeof(float) * heads);
+  return AIRCACHE_OK;
+}
+
+}  // namespace
+}  // namespace aircache
+
+using namespace aircache;
+
+extern "C" {
+
+size_t aircache_shared_decode_workspace_size(const aircache_shared_decode_problem* p) {
+  SdPlan pl;
+  return sd_plan(p, pl) == AIRCACHE_OK ? pl.total : 0;
+}
+
+int aircache_shared_decode(const aircache_shared_decode_problem* p, void* ws, size_t ws_bytes, void* stream) {
+  SdPlan pl;
+  int rc = sd_plan(p, pl);
+  if (rc != AIRCACHE_OK) return rc;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) != 0) return AIRCACHE_ERR_INVALID_ARG;
+  if (ws_bytes < pl.total) return AIRCACHE_ERR_WORKSPACE;
+  if (p->own.pages->num_seqs == 0) return AIRCACHE_OK;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  DecodePrior prior = {nullptr, nullptr, nullptr};
+  if (p->prefix->num_seqs > 0) {
+    const AttendPart part = {reinterpret_cast<float*>(w + pl.out_off), reinterpret_cast<float*>(w + pl.lse_off)};
+    rc = attend_launch(&pl.at, pl.attend, part, w + pl.attend_off, reinterpret_cast<int32_t*>(w),
+                       static_cast<cudaStream_t>(stream));
+    if (rc != AIRCACHE_OK) return rc;
+    prior = {part.out, part.lse2, p->cu_seqs + p->prefix->num_seqs};
+  }
+  return paged_decode_run(&p->own, prior, ws, pl.attend_off, stream);
+}
+
+}  // extern "C"

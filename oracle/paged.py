@@ -88,6 +88,37 @@ def attend(q, cu, c, scale, causal=False, begin=None, end=None):
     return out, lse, size, spread
 
 
+def shared_decode(q, c, prefix, cu, scale):
+    """decode() over each sequence's prefix (cu: the first sequence of each, and of none) and its own rows: (out, lse,
+    weight of each own row [S][H][n], logits' sizes, sum_j w_j |v_j|, the same over the prefix's rows alone)."""
+    S, h_q, d = q.shape
+    h = c["k"].shape[2]
+    g = h_q // h
+    out, lse = np.zeros((S, h_q, d)), np.full((S, h_q), -np.inf)
+    spread, far, size, w_all = np.zeros((S, h_q, d)), np.zeros((S, h_q, d)), np.zeros((S, h_q)), []
+    for s in range(S):
+        i = int(np.searchsorted(cu, s, side="right")) - 1
+        n = int(c["lens"][s])
+        w_s = np.zeros((h, n))
+        for j in range(h_q):
+            k, v = rows(c, "k", s, j // g), rows(c, "v", s, j // g)
+            if i < len(cu) - 1:
+                k = np.concatenate([rows(prefix, "k", i, j // g), k])
+                v = np.concatenate([rows(prefix, "v", i, j // g), v])
+            if len(k) == 0:
+                continue
+            x = (k @ q[s, j]) * scale
+            size[s, j] = (np.abs(k) @ np.abs(q[s, j])).max() * scale
+            e = np.exp(x - x.max())
+            lse[s, j] = x.max() + np.log(e.sum())
+            w = e / e.sum()
+            p = len(k) - n
+            out[s, j], spread[s, j], far[s, j] = w @ v, w @ np.abs(v), w[:p] @ np.abs(v[:p])
+            w_s[j // g] += w[p:]
+        w_all.append(w_s)
+    return out, lse, w_all, size, spread, far
+
+
 def largest_weighted_scale(q, c, scale):
     """int8 values: max_j w_j s_j of each sequence and query head [S, H_q], s_j the value's scale."""
     S, h_q, _ = q.shape

@@ -85,9 +85,303 @@ NEW = [1, 2, 0, 17, 18, 19, 36, 37, 5, 73]
 OLD = [0, 126, 40, 111, 0, 128, 300, 91, 1000, 55]
 
 
+@pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("d", [128, 64])
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("page_rows", [16, 48, 64, 256])
-def test_ragged(A, page_rows, causal, d):
+def test_ragged(A, page_rows, causal, d, int8):
     lens = [a + b for a, b in zip(NEW, OLD)]
-    case(A, NEW, lens, 28, 4, d, page_rows, seed=d + page_rows, causal=causal)
+    case(A, NEW, lens, 28, 4, d, page_rows, seed=d + page_rows, causal=causal, int8=int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (16, 1), (9, 1), (8, 8), (10, 2), (24, 3)])
+def test_heads(A, h_q, h_kv, int8):
+    case(A, [130, 1, 0, 14, 3], [140, 5, 9, 300, 257], h_q, h_kv, 128, 32, seed=h_q, causal=True, int8=int8)
+    case(A, [5, 129, 1], [200, 0, 128], h_q, h_kv, 64, 32, seed=h_q, int8=int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_one_sequence_is_joined_from_many_parts(A, int8):
+    case(A, [3], [20011], 28, 4, 128, 64, seed=3, causal=True, int8=int8)
+    case(A, [40, 1], [9000, 1], 4, 1, 64, 16, seed=4, int8=int8)
+    case(A, [260], [3000], 2, 1, 128, 256, seed=4, causal=True, int8=int8)
+
+
+def test_many_short_sequences(A):
+    g = np.random.default_rng(5)
+    new = g.integers(0, 4, 700)
+    case(A, new.tolist(), (new + g.integers(0, 40, 700)).tolist(), 4, 2, 64, 16, seed=5, causal=True)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_slots_behind_the_last_row_hold_anything(A, int8):
+    # NaN rows (bf16) or NaN scales (int8) behind the end, in a tile's middle and in its own page
+    for causal in (True, False):
+        case(A, [1, 17, 20, 50], [1, 17, 70, 250], 8, 2, 128, 64, seed=6, int8=int8, fill=float("nan"), causal=causal)
+        case(A, [1, 17, 20, 50], [129, 17, 383, 513], 8, 8, 64, 16, seed=6, int8=int8, fill=float("inf"), causal=causal)
+
+
+@pytest.mark.parametrize("fused,wide", [(True, 0), (False, 3), (True, 1)])
+def test_strides(A, fused, wide):
+    for d, int8 in ((128, False), (64, True), (64, False)):
+        case(A, [33, 7, 64], [33, 100, 64], 6, 2, d, 32, seed=7, fused=fused, wide=wide, int8=int8, causal=True)
+    # views of one projection, every second head, a transposed output
+    T, h_q, d = 45, 6, 128
+    q = queries(T, 2 * h_q + 3, d, 8)[:, 1:1 + 2 * h_q:2]
+    cache = P.build(A, [40, 90, 64], 3, d, 16, seed=8)
+    out = torch.full((h_q + 1, T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    o = out[:h_q].transpose(0, 1)
+    prob = A.PagedAttendProblem(q, cache, i32([0, 20, 40, 45]), out=o, causal=True)
+    A.paged_attend(prob)
+    verify(o, None, q, [0, 20, 40, 45], P.host(cache), causal=True)
+    assert torch.all(out[h_q] == 7.0)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+def test_ranges(A, causal, int8):
+    g = np.random.default_rng(11)
+    new, lens = [60, 1, 130, 0, 20], [700, 40, 1000, 30, 20]
+    T = sum(new)
+    begin, end = g.integers(-50, 900, T), g.integers(-50, 1100, T)
+    begin[:20], end[:20] = 130, 120                      # nothing at all
+    begin[61:100], end[61:100] = -2 ** 31, 2 ** 31 - 1   # everything
+    begin[150:], end[150:] = 255, 257                    # two rows across tiles
+    for b, e in ((begin, end), (begin, None), (None, end)):
+        case(A, new, lens, 14, 2, 128, 32, seed=12, causal=causal, int8=int8, begin=b, end=e)
+    case(A, new, lens, 4, 4, 64, 16, seed=13, causal=causal, int8=int8, begin=begin, end=end)
+
+
+def test_a_window_over_the_last_rows(A):
+    new, lens = [100, 300], [900, 300]
+    hi = np.concatenate([R - n + 1 + np.arange(n) for n, R in zip(new, lens)])
+    case(A, new, lens, 28, 4, 128, 64, seed=14, causal=True, begin=hi - 100)
+
+
+def test_tokens_that_see_nothing(A):
+    case(A, [5, 40], [0, 0], 28, 4, 128, 16, seed=15)
+    case(A, [5, 40, 3], [70, 300, 0], 28, 4, 128, 16, seed=15, end=[0] * 48)
+    # some rows of a tile only, with NaN where nobody looks
+    case(A, [30], [300], 28, 4, 128, 16, seed=15, begin=[400] * 10 + [128] * 10 + [0] * 10, fill=float("nan"))
+
+
+# A later token's key and value are nobody's but its own (and those behind it): bf16 rows of NaN and infinities
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("h_q,h_kv,n,R,d", [(28, 4, 50, 170, 128), (8, 8, 200, 2600, 64), (14, 2, 9, 6000, 128), (2, 2, 140, 140, 128)])
+def test_masked_rows_that_are_not_finite(A, value, h_q, h_kv, n, R, d):
+    cache = P.build(A, [R, R], h_kv, d, 32, seed=16, mass=False, order=False)
+    q = queries(2 * n, h_q, d, 16)
+    cu = [0, n, 2 * n]
+    at = R - n + n // 2  # the row of token n // 2
+    clean = P.host(cache)
+    pg = cache.table[0].long()
+    for name in ("k", "v"):
+        t = getattr(cache, name)
+        t[pg[at // 32], at % 32] = value
+        t[pg[(R - 1) // 32], (R - 1) % 32, :, ::3] = value
+    prob = A.PagedAttendProblem(q, cache, i32(cu), lse=True, causal=True)
+    A.paged_attend(prob)
+    want, want_lse, size, spread = O.attend(q.double().cpu().numpy(), cu, clean, d ** -0.5, True)
+    got = prob.out.double().cpu().numpy()
+    tol = (HALF + 2.0 ** -12) * spread + HALF * np.abs(want)
+    free = np.r_[0:n // 2, n:2 * n]  # the tokens before it, and the other sequence
+    assert np.all(np.isfinite(got[free])) and np.all(np.abs(got - want)[free] <= tol[free])
+    assert not np.isfinite(got[n // 2:n]).any()  # its key has given every logit sum a NaN, an infinity or a zero weight
+    assert np.all(np.abs(prob.lse.double().cpu().numpy() - want_lse)[free] < 1e-3)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_stay_in_their_column(A, value):
+    n, R, d = 40, 300, 128
+    cache = P.build(A, [R], 2, d, 32, seed=17, mass=False, order=False)
+    q = queries(n, 14, d, 17, 0.2)
+    clean = P.host(cache)
+    at = R - n + 11
+    cache.v[cache.table[0, at // 32].long(), at % 32, 1, 5] = value
+    prob = A.PagedAttendProblem(q, cache, i32([0, n]), causal=True)
+    A.paged_attend(prob)
+    want, _, size, spread = O.attend(q.double().cpu().numpy(), [0, n], clean, d ** -0.5, True)
+    got = prob.out.double().cpu().numpy()
+    hit = np.zeros(got.shape, bool)
+    hit[11:, 7:, 5] = True
+    assert np.all(np.isnan(got[hit]) if np.isnan(value) else got[hit] == value)
+    tol = (HALF + 2.0 ** -12) * spread + HALF * np.abs(want)
+    assert np.all(np.abs(got - want)[~hit] <= tol[~hit])
+
+
+def test_int8_scales_that_are_not_finite(A):
+    n, R = 40, 300
+    cache = P.build(A, [R, R], 2, 128, 32, seed=18, mass=False, order=False, int8=True)
+    q = queries(2 * n, 14, 128, 18)
+    clean = P.host(cache)
+    at = R - n + 11
+    for t in (cache.k_scale, cache.v_scale):
+        t[cache.table[0, at // 32].long(), 1, at % 32] = float("nan")
+    cache.k[cache.table[0, at // 32].long(), at % 32, 1] = 0
+    prob = A.PagedAttendProblem(q, cache, i32([0, n, 2 * n]), causal=True)
+    A.paged_attend(prob)
+    want, _, _, spread = O.attend(q.double().cpu().numpy(), [0, n, 2 * n], clean, 128 ** -0.5, True)
+    got = prob.out.double().cpu().numpy()
+    hit = np.zeros(got.shape, bool)
+    hit[11:n, 7:] = True
+    assert np.all(np.isnan(got[hit]))
+    tol = (HALF + 2.0 ** -12) * spread + HALF * np.abs(want)
+    assert np.all(np.abs(got - want)[~hit] <= tol[~hit])
+
+
+def test_far_apart_logits(A):
+    # a few rows have all the weight, the reference moves with almost every tile; and the smallest scales
+    case(A, [50, 3], [900, 2000], 14, 2, 128, 64, seed=19, q_scale=60.0, causal=True)
+    case(A, [50, 3], [900, 2000], 14, 2, 128, 64, seed=19, scale=1e-30)
+    cache = P.build(A, [600], 2, 128, 64, seed=20, mass=False, order=False)
+    q = queries(30, 14, 128, 20)
+    r = torch.arange(600, device="cuda")
+    k = cache.k[cache.table[0].long()[r // 64], r % 64]
+    cache.k[cache.table[0].long()[r // 64], r % 64] = (k * (1 + r[:, None, None] / 20)).to(torch.bfloat16)
+    prob = A.PagedAttendProblem(q, cache, i32([0, 30]), lse=True)
+    A.paged_attend(prob)
+    verify(prob.out, prob.lse, q, [0, 30], P.host(cache))
+
+
+def test_logits_under_the_range_weigh_nothing(A):
+    cache = P.build(A, [200, 200], 2, 128, 16, seed=21, mass=False, order=False)
+    q = torch.full((60, 14, 128), 3e38, dtype=torch.bfloat16, device="cuda")
+    pg = cache.table.long()
+    r = torch.arange(200, device="cuda")
+    cache.k[pg[0][r // 16], r % 16] = -1.0
+    cache.k[pg[1][r // 16], r % 16] = -1.0
+    cache.k[pg[1, 3], 7] = 0.0  # one row of the second sequence has the logit 0
+    prob = A.PagedAttendProblem(q, cache, i32([0, 30, 60]), lse=True)
+    A.paged_attend(prob)
+    assert torch.all(prob.out[:30] == 0) and torch.all(torch.isneginf(prob.lse[:30]))
+    v = cache.v[pg[1, 3], 7].repeat_interleave(7, 0)
+    assert torch.equal(prob.out[30:], v.expand(30, -1, -1)) and torch.all(prob.lse[30:] == 0)
+
+
+# ------------------------------------------------------------------ use
+
+def test_the_same_call_gives_the_same_bits(A):
+    lens, new = [5000, 700, 1], [40, 300, 1]
+    cache = P.build(A, lens, 4, 128, 64, seed=22, mass=False, order=False)
+    q = queries(sum(new), 28, 128, 22)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]).tolist())
+    prob = A.PagedAttendProblem(q, cache, cu, lse=True, causal=True)
+    ws = prob.new_workspace()
+    A.paged_attend(prob, ws)
+    first = P.bits(prob.out), P.bits(prob.lse)
+    for _ in range(5):
+        prob.out.zero_()
+        A.paged_attend(prob, ws)
+        assert np.array_equal(first[0], P.bits(prob.out)) and np.array_equal(first[1], P.bits(prob.lse))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_captured_calls_follow_their_inputs(A, int8):
+    # one workspace, lengths and queries that change between replays, on another stream than the default
+    S, h_q, h_kv, d, page_rows = 4, 14, 2, 128, 16
+    cache = P.build(A, [400, 300, 200, 100], h_kv, d, page_rows, seed=23, int8=int8, mass=False, order=False)
+    q = queries(100, h_q, d, 23)
+    cu = i32([0, 10, 10, 60, 90])
+    prob = A.PagedAttendProblem(q, cache, cu, lse=True, causal=True)
+    ws = prob.new_workspace()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        A.aircache_paged_attend(prob, ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            A.aircache_paged_attend(prob, ws)
+            A.aircache_paged_attend(prob, ws)
+    torch.cuda.synchronize()
+    for turn, (lens, c) in enumerate([((400, 300, 200, 100), (0, 10, 10, 60, 90)), ((17, 0, 50, 99), (0, 0, 0, 50, 100)),
+                                      ((399, 1, 128, 16), (0, 99, 100, 100, 100))]):
+        cache.lens.copy_(i32(list(lens)))
+        cu.copy_(i32(list(c)))
+        q.copy_(queries(100, h_q, d, 30 + turn))
+        graph.replay()
+        torch.cuda.synchronize()
+        verify(prob.out, prob.lse, q, c, P.host(cache), causal=True)
+        assert A.aircache_get_error(ws) == A.OK
+
+
+def test_two_calls_at_once(A):
+    probs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        cache = P.build(A, [3000, 50], 4, 128, 64, seed=24 + i, mass=False, order=False)
+        q = queries(120, 28, 128, 24 + i)
+        probs.append((A.PagedAttendProblem(q, cache, i32([0, 100, 120]), lse=True), cache, q))
+    torch.cuda.synchronize()
+    works = [p.new_workspace() for p, _, _ in probs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (p, _, _), ws, s in zip(probs, works, streams):
+            A.aircache_paged_attend(p, ws, s)
+    torch.cuda.synchronize()
+    for p, cache, q in probs:
+        verify(p.out, p.lse, q, [0, 100, 120], P.host(cache))
+
+
+def test_sequences_may_share_pages(A):
+    cache = P.build(A, [200, 200], 2, 128, 16, seed=26, mass=False, order=False)
+    cache.table[1].copy_(cache.table[0])
+    q = queries(40, 14, 128, 26)
+    prob = A.PagedAttendProblem(q, cache, i32([0, 15, 40]))
+    A.paged_attend(prob)
+    verify(prob.out, None, q, [0, 15, 40], P.host(cache))
+
+
+# ------------------------------------------------------------------ what the device refuses
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_bad_pages_and_lengths(A, int8):
+    for change in ("page", "negative page", "long", "negative", "short"):
+        cache = P.build(A, [200, 100, 50], 2, 128, 16, seed=27, int8=int8, mass=False, order=False)
+        good = P.host(cache)
+        q = queries(60, 14, 128, 27)
+        if change == "page":
+            cache.table[1, 3] = cache.num_pages
+        elif change == "negative page":
+            cache.table[1, 3] = -1
+        else:
+            cache.lens[1] = {"long": 4000, "negative": -5, "short": 7}[change]
+        out = torch.full((60, 14, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        prob = A.PagedAttendProblem(q, cache, i32([0, 20, 40, 60]), out=out, causal=True)
+        ws = prob.new_workspace()
+        with pytest.raises(A.AirCacheError) as e:
+            A.paged_attend(prob, ws)
+        assert e.value.status == A.ERR_DEVICE_BOUNDS
+        want = O.attend(q.double().cpu().numpy(), [0, 20, 40, 60], good, 128 ** -0.5, True)
+        got = out.double().cpu().numpy()
+        rest = np.r_[0:20, 40:60]
+        assert np.all(np.abs(got - want[0])[rest] <= ((HALF + 2.0 ** -12) * want[3] + HALF * np.abs(want[0]))[rest])
+        if change in ("long", "negative"):
+            assert torch.all(out[20:40] == 0)
+        ws.zero_()
+        cache.table.copy_(torch.from_numpy(good["table"]).cuda())
+        cache.lens.copy_(i32([200, 100, 50]))
+        A.paged_attend(prob, ws)  # (the workspace is as good as new)
+        verify(out, None, q, [0, 20, 40, 60], good, causal=True)
+
+
+@pytest.mark.parametrize("cu", [[0, 30, 20, 60], [0, 20, 40, 61], [-1, 20, 40, 60], [0, 20, 2 ** 31 - 1, 60], [0, -2 ** 31, 40, 60],
+                                [60, 60, 0, 60]])
+def test_bad_token_offsets(A, cu):
+    cache = P.build(A, [200, 100, 50], 2, 128, 16, seed=28, mass=False, order=False)
+    q = queries(60, 14, 128, 28)
+    big = torch.full((80, 14, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    prob = A.PagedAttendProblem(q, cache, i32(cu), out=big[10:70])
+    with pytest.raises(A.AirCacheError) as e:
+        A.paged_attend(prob)
+    assert e.value.status == A.ERR_DEVICE_BOUNDS
+    assert torch.all(big[:10] == 7.0) and torch.all(big[70:] == 7.0)
+
+
+def test_no_tokens_and_no_sequences(A):
+    cache = P.build(A, [20, 10], 2, 128, 16, seed=29, mass=False, order=False)
+    prob = A.PagedAttendProblem(torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda"), cache, i32([0, 0, 0]))
+    assert A.paged_attend(prob).shape == (0, 4, 128)
+    out = torch.full((3, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    prob = A.PagedAttendProblem(queries(3, 4, 128), cache, i32([0, 0, 0]), out=out)
+    A.paged_attend(prob)
+    assert torch.all(out == 7.0)
