@@ -44,18 +44,24 @@ namespace {
 
 constexpr int kAtKeys = 128;                  // rows of a key tile
 constexpr int kAtRows = 128;                  // query rows of a stream (TMEM lanes)
-constexpr int kAtMma = 8, kAtLoad = 9, kAtAux = 10;  // behind the eight softmax warps: MMA issue, keys and values,
-constexpr int kAtWiden = 12;                         // queries and tails; from 12 on four that widen int8 codes
+// Behind the eight softmax warps: the streams' MMA issue (8 and 9), keys and values, queries and tails; from 12 on
+// four that widen int8 codes
+constexpr int kAtMma = 8, kAtLoad = 10, kAtAux = 11, kAtWiden = 12;
 constexpr uint32_t kAtEnd = 2;                // places of the line for a unit's end
 constexpr float kAtSlack = 8.f;               // base-2 powers that a maximum may pass its reference by
 constexpr uint32_t kAtS = 0, kAtO = 256;      // TMEM columns: S of stream i at 128 i, O at 256 + 128 i
 constexpr int kAtGroup = 16;                  // query heads of a KV head, at most
+constexpr int kAtStaged = 4096;               // sequences whose lengths and offsets go through shared memory
+constexpr int kAtRanged = 48;                 // units up to which every CTA finds their ranges
 constexpr int kAtHeader = 256;                // workspace: error word
 constexpr long long kAtLong = 4 * kWaitCycles;  // waits that stand behind another warp's
 
 template <int D, bool Q8>
 struct AtCfg {
-  static constexpr int kThreads = Q8 ? 512 : 352;
+  static constexpr int kThreads = Q8 ? 512 : 384;
+  // registers of a thread: what the other warps give, the softmax warps, which hold a row of 128 logits, take
+  static constexpr int kRegs = Q8 ? 128 : 168, kRegsSoft = Q8 ? 160 : 200, kRegsOther = Q8 ? 96 : 104;
+  static_assert(256 * kRegsSoft + (kThreads - 256) * kRegsOther <= kThreads * kRegs, "within the launch's own");
   static constexpr int kSlab = kAtKeys * 128;       // [128 rows][64 bf16]
   static constexpr int kTile = kSlab * (D / 64);
   static constexpr int kStages = (Q8 ? 3 : 5) * 128 / D;       // tiles of the ring
@@ -70,6 +76,13 @@ struct AtCfg {
   static constexpr int kOffCtl = kOffScales + kScaleStages * 2 * kAtKeys * 4;
 };
 
+// A unit whose parts are to be joined (parts < 2: none): of CTAs c0 .. c0 + parts - 1.
+struct alignas(16) AtCut {
+  int parts, c0, h, ntok;
+  int64_t token0;
+  int slot, pad;
+};
+
 struct AtArgs {
   Pages pages;
   const int32_t* cu;
@@ -82,12 +95,12 @@ struct AtArgs {
   float* lse;
   AttendPart part;
   int32_t* error;
-  int4* cut;        // [CTAs]: the unit that begins in the CTA and ends in another: slot, KV head, first CTA, parts
+  AtCut* cut;       // [CTAs]: the unit that begins in the CTA and ends in another
   int2* range;      // [slots]: the key tiles that a unit's tokens see (with row_begin or row_end)
   float2* part_ml;  // [2 CTAs][rows_cap]
   float* part_o;    // [2 CTAs][rows_cap][D]
   int64_t num_tokens;
-  int slots, group, tok_tile, h_q, causal, ctas, rows_cap, box;
+  int slots, group, tok_tile, h_q, causal, ranged, rows_cap, box;  // ranged: a kernel has filled `range`
   float scale_log2;
 };
 
@@ -123,6 +136,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return r;
 }
+// True for one lane of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // Arrives `n` times.
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
@@ -151,15 +170,20 @@ struct AtUnit {
 };
 // Units of sequence s start at slot cu[s] / (2 tok_tile) + s: never less than the units before it, so that a slot's
 // sequence is found without a sum over the batch, and at most num_seqs slots are empty.
-__device__ __forceinline__ int slot_base(const AtArgs& a, int s) {
-  const int c = min(max(a.cu[s], 0), (int)a.num_tokens);
+struct AtSeqs {
+  const int32_t* cu;
+  const int32_t* lens;
+};
+__device__ __forceinline__ AtSeqs seqs_of(const AtArgs& a) { return {a.cu, a.pages.lens}; }
+__device__ __forceinline__ int slot_base(const AtArgs& a, const AtSeqs& q, int s) {
+  const int c = min(max(q.cu[s], 0), (int)a.num_tokens);
   return c / (2 * a.tok_tile) + s;
 }
-__device__ __forceinline__ int find_seq(const AtArgs& a, int slot) {
+__device__ __forceinline__ int find_seq(const AtArgs& a, const AtSeqs& q, int slot) {
   int lo = 0, hi = a.pages.num_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (slot_base(a, mid) <= slot)
+    if (slot_base(a, q, mid) <= slot)
       lo = mid;
     else
       hi = mid - 1;
@@ -176,14 +200,14 @@ __device__ __forceinline__ void token_rows(const AtArgs& a, int rows, int n, int
 }
 // The unit of `slot` in sequence s; ntok = 0 when there is none.  LISTED: its key tiles are in a.range.
 template <bool LISTED = true>
-__device__ __forceinline__ AtUnit unit_of(const AtArgs& a, int s, int slot) {
+__device__ __forceinline__ AtUnit unit_of(const AtArgs& a, const AtSeqs& q, int s, int slot) {
   AtUnit u;
   u.s = s;
-  const int c0 = a.cu[s], c1 = a.cu[s + 1];
+  const int c0 = q.cu[s], c1 = q.cu[s + 1];
   u.n = c0 >= 0 && c1 >= c0 && c1 <= a.num_tokens ? c1 - c0 : 0;
-  const int len = a.pages.lens[s];
+  const int len = q.lens[s];
   u.rows = len >= 0 && len <= a.pages.max_rows ? len : 0;
-  const int64_t first = (int64_t)(slot - slot_base(a, s)) * (2 * a.tok_tile);
+  const int64_t first = (int64_t)(slot - slot_base(a, q, s)) * (2 * a.tok_tile);
   const bool in = first >= 0 && first < u.n;
   u.tok0 = in ? (int)first : 0;
   u.ntok = in ? min(2 * a.tok_tile, u.n - u.tok0) : 0;
@@ -202,9 +226,23 @@ __device__ __forceinline__ AtUnit unit_of(const AtArgs& a, int s, int slot) {
   return u;
 }
 
+// A unit's key tiles by its tokens' own ranges, by a warp.
+__device__ __forceinline__ void find_range(const AtArgs& a, const AtSeqs& q, int slot) {
+  const AtUnit u = unit_of<false>(a, q, find_seq(a, q, slot), slot);
+  int from = INT32_MAX, to = 0;
+  for (int i = threadIdx.x & 31; i < u.ntok; i += 32) {
+    int lo, hi;
+    token_rows(a, u.rows, u.n, u.tok0 + i, u.token0 + i, lo, hi);
+    if (hi > lo) from = min(from, lo), to = max(to, hi);
+  }
+  from = __reduce_min_sync(0xffffffffu, from);
+  to = __reduce_max_sync(0xffffffffu, to);
+  if ((threadIdx.x & 31) == 0) a.range[slot] = to > 0 ? make_int2(from / kAtKeys, (to - 1) / kAtKeys + 1) : make_int2(0, 0);
+}
+
 // A CTA's places of the line, and the walk over the units in them.
 struct AtRun {
-  uint64_t per, lo, hi, at;  // places of a CTA, its own, the unit's first
+  uint64_t hi, lo, at;       // the CTA's places, the unit's first
   int slot, h;
   AtUnit u;
   int first, count;          // the CTA's key tiles of the unit, from u.t0 on
@@ -221,8 +259,9 @@ __device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r) {
     r.h = 0;
     do {
       if (++r.slot >= a.slots) return false;
-      while (r.u.s + 1 < a.pages.num_seqs && slot_base(a, r.u.s + 1) <= r.slot) ++r.u.s;
-      r.u = unit_of(a, r.u.s, r.slot);
+      int s = r.u.s;
+      while (s + 1 < a.pages.num_seqs && slot_base(a, seqs_of(a), s + 1) <= r.slot) ++s;
+      r.u = unit_of(a, seqs_of(a), s, r.slot);
     } while (r.u.ntok == 0);
   }
   clip(r);
@@ -253,6 +292,7 @@ __device__ __forceinline__ bool entry_of(bool nar, int count, int pos, int& j) {
 struct AtScratch {
   uint64_t sum[16];
   AtRun run;
+  uint64_t per;  // places of a CTA
 };
 template <int D, bool Q8>
 struct AtCtl {
@@ -261,14 +301,19 @@ struct AtCtl {
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t tail[C::kStages];  // of a stage that holds values to be cleared in part: its copies have landed
   uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scempty[kScales];
-  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2], mlfull, mlfree, done;
+  uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done;
   uint32_t tmem;
   float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
   AtScratch scratch;
+  AtRun run[C::kThreads / 32];  // each warp's place: read seldom, not worth registers
 };
+// (64-bit division takes many times a 32-bit one's time, and is seldom needed)
+__device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
+  return ((x | y) >> 32) == 0 ? (uint32_t)x / (uint32_t)y : x / y;
+}
 // By all threads of the CTA; false if the CTA has no place.
 template <int THREADS>
-__device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
+__device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun& r) {
   static_assert(THREADS <= 512, "warps' sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.slots + THREADS - 1) / THREADS;
@@ -276,10 +321,10 @@ __device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
   uint64_t mine = 0;
   int seq0 = 0;
   if (s0 < s1) {
-    int s = seq0 = find_seq(a, s0);
+    int s = seq0 = find_seq(a, q, s0);
     for (int i = s0; i < s1; ++i) {
-      while (s + 1 < a.pages.num_seqs && slot_base(a, s + 1) <= i) ++s;
-      const AtUnit u = unit_of(a, s, i);
+      while (s + 1 < a.pages.num_seqs && slot_base(a, q, s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, q, s, i);
       if (u.ntok) mine += (uint64_t)(u.c + kAtEnd) * a.pages.h_kv;
     }
   }
@@ -297,23 +342,23 @@ __device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
     if (w < warp) before += sc->sum[w];
     total += sc->sum[w];
   }
-  const uint64_t per = max((uint64_t)1, (total + gridDim.x - 1) / gridDim.x);
+  const uint64_t per = max((uint64_t)1, quotient(total + gridDim.x - 1, gridDim.x));
   const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
+  if (tid == 0) sc->per = per;
   if (lo < hi && lo >= before && lo < before + mine) {
     uint64_t at = before;
     int s = seq0;
     for (int i = s0; i < s1; ++i) {
-      while (s + 1 < a.pages.num_seqs && slot_base(a, s + 1) <= i) ++s;
-      const AtUnit u = unit_of(a, s, i);
+      while (s + 1 < a.pages.num_seqs && slot_base(a, q, s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, q, s, i);
       if (!u.ntok) continue;
       const uint64_t wide = u.c + kAtEnd;
       if (lo < at + wide * a.pages.h_kv) {
         AtRun x;
-        x.per = per;
         x.lo = lo;
         x.hi = hi;
         x.slot = i;
-        x.h = (int)((lo - at) / wide);
+        x.h = (int)quotient(lo - at, wide);
         x.at = at + x.h * wide;
         x.u = u;
         clip(x);
@@ -325,34 +370,40 @@ __device__ bool make_run(const AtArgs& a, AtScratch* sc, AtRun& r) {
   }
   __syncthreads();
   if (lo < hi) r = sc->run;
+  __syncwarp();
   return lo < hi;
 }
 
 // ------------------------------------------------------------------ results
 
-// The output of one row whose sum is finite and whose values are not: over the rows that it sees, without those that a
-// matrix product multiplies by 0.  By a warp; lane holds D / 32 columns.
-template <int D>
+// E columns from `col` on (of each lane; none where col is D) of one row whose sum is finite and whose values are not:
+// over the rows that it sees, without those that a matrix product multiplies by 0.  By a warp.
+template <int D, int E>
 __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t token, int head, int lo, int hi, float m,
-                                        float l, float y[D / 32]) {
-  constexpr int E = D / 32;
+                                        float l, int col, float y[E]) {
+  constexpr int Q = D / 32;
   const int lane = threadIdx.x & 31;
   const Pages& p = a.pages;
-  const __nv_bfloat16* q = a.q + token * a.q_stride_tok + (int64_t)head * a.q_stride_head + lane * E;
-  float qv[E];
+  const __nv_bfloat16* q = a.q + token * a.q_stride_tok + (int64_t)head * a.q_stride_head + lane * Q;
+  float qv[Q];
 #pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = __bfloat162float(q[e]), y[e] = 0.f;
+  for (int e = 0; e < Q; ++e) qv[e] = __bfloat162float(q[e]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
   for (int j = lo; j < hi; ++j) {
     const int page = p.table[(int64_t)s * p.table_stride + j / p.page_rows];
     float x = 0.f, v[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = 0.f;
     if (page_ok(p, page)) {
-      const int64_t at = page_elem(p, page, h, j % p.page_rows) + lane * E;
-      const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at;
+      const int64_t at = page_elem(p, page, h, j % p.page_rows);
+      const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
       const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
 #pragma unroll
-      for (int e = 0; e < E; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x), v[e] = __bfloat162float(vv[e]);
+      for (int e = 0; e < Q; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (col + e < D) v[e] = __bfloat162float(vv[col + e]);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -366,6 +417,10 @@ __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t t
 }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
+// A CTA's part of a unit that began before it lies in slot 2 x CTA, of one that begins in it in the next.  A slot holds
+// [D / 4][rows_cap] pieces of four columns, so that a warp's rows are next to one another.
+__device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * (int64_t)cta + (begins ? 1 : 0); }
+
 // The log-sum-exp of a row.
 __device__ __forceinline__ void write_lse(const AtArgs& a, int64_t token, int head, float m, float l) {
   const float x = l == 0.f ? -INFINITY : m + log2f(l);
@@ -377,7 +432,9 @@ template <int D, int E>
 __device__ __forceinline__ void write_out(const AtArgs& a, int64_t token, int head, int col, const float* y) {
   if (a.part.out) {
     float* to = a.part.out + (token * a.h_q + head) * D + col;
-    if constexpr (E == 2) {
+    if constexpr (E == 1) {
+      *to = y[0];
+    } else if constexpr (E == 2) {
       *reinterpret_cast<float2*>(to) = make_float2(y[0], y[1]);
     } else {
 #pragma unroll
@@ -386,7 +443,9 @@ __device__ __forceinline__ void write_out(const AtArgs& a, int64_t token, int he
     return;
   }
   __nv_bfloat16* to = a.out + token * a.out_stride_tok + (int64_t)head * a.out_stride_head + col;
-  if constexpr (E == 2) {
+  if constexpr (E == 1) {
+    *to = __float2bfloat16_rn(y[0]);
+  } else if constexpr (E == 2) {
     *reinterpret_cast<uint32_t*>(to) = pack2(y[0], y[1]);
   } else if constexpr (E == 4) {
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
@@ -407,8 +466,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
                                                                      const __grid_constant__ AtArgs a) {
   using C = AtCfg<D, Q8>;
   using Ctl = AtCtl<D, Q8>;
-  extern __shared__ uint8_t at_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(at_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   Ctl* ctl = reinterpret_cast<Ctl*>(sm + C::kOffCtl);
   const uint32_t base = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -416,7 +474,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&ctl->full[i], Q8 ? 4 : 1);
-      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->empty[i], 2);
       mbar_init(&ctl->tail[i], 1);
     }
     for (int i = 0; i < C::kCodeStages; ++i) {
@@ -428,12 +486,14 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       mbar_init(&ctl->scempty[i], 8);
     }
     mbar_init(&ctl->qfull, 1);
-    mbar_init(&ctl->qempty, 1);
+    mbar_init(&ctl->qempty, 2);
     mbar_init(&ctl->mlfull, 4);
     mbar_init(&ctl->mlfree, 4);
-    mbar_init(&ctl->done, 1);
+    mbar_init(&ctl->done, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->sfull[i], 1);
+      mbar_init(&ctl->turn[i], 1);
+      mbar_init(&ctl->phalf[i], 4);
       mbar_init(&ctl->pfull[i], 4);
       mbar_init(&ctl->ofull[i], 1);
     }
@@ -451,20 +511,38 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   }
   pdl_wait();
   pdl_trigger();
+  // lengths and token offsets lie where the tiles will until the CTA has found its place: searches go to shared memory
+  AtSeqs seqs = seqs_of(a);
+  if (p.num_seqs <= kAtStaged) {
+    int32_t* lens = reinterpret_cast<int32_t*>(sm);
+    int32_t* cu = lens + kAtStaged;
+    for (int s = tid; s <= p.num_seqs; s += C::kThreads) {
+      cu[s] = a.cu[s];
+      if (s < p.num_seqs) lens[s] = p.lens[s];
+    }
+    seqs = {cu, lens};
+    __syncthreads();
+  }
   if (blockIdx.x == 0) {  // what the batch's description says that cannot be
-    bool bad = tid == 0 && a.cu[0] < 0;
+    bool bad = tid == 0 && seqs.cu[0] < 0;
     for (int s = tid; s < p.num_seqs; s += C::kThreads) {
-      const int c0 = a.cu[s], c1 = a.cu[s + 1], len = p.lens[s];
+      const int c0 = seqs.cu[s], c1 = seqs.cu[s + 1], len = seqs.lens[s];
       bad |= c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
     }
     if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
   }
+  if (a.range && !a.ranged) {  // few units: each CTA finds what their tokens see by itself (all write the same)
+    for (int slot = warp; slot < a.slots; slot += C::kThreads / 32) find_range(a, seqs, slot);
+    __syncthreads();
+  }
   tc_fence_before();
-  AtRun r;
-  const bool any = make_run<C::kThreads>(a, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+  AtRun& r = ctl->run[warp];
+  const bool any = make_run<C::kThreads>(a, seqs, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
+  if (warp >= kAtMma) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOther));
   if (warp == kAtLoad) {
     // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
     // and the odd chunks: the next chunk's are looked up while this one is copied
@@ -595,62 +673,118 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     }
     if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
     if (units > 0) (void)mbar_wait_warp(&ctl->qfull, (units - 1) & 1);  // (landed)
-  } else if (warp == kAtMma) {
-    if (lane == 0) {
-      // ---- turn k: stream k & 1 gets O += P V for its (k >> 1)-th tile, then S for its next
-      constexpr uint32_t id_s = umma_idesc_bf16(kAtRows, kAtKeys);
-      constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
-      uint32_t units = 0, n = 0, p_it[2] = {0, 0};
-      bool ok = true;
-      for (bool more = any; more && ok; more = next_unit(a, r)) {
-        if (r.count == 0) continue;
-        const bool nar = narrow(a, r.u);
-        const int turns = nar ? r.count : 2 * r.count;
-        ok = mbar_wait(&ctl->qfull, units & 1, kAtLong);
-        if (!ok) break;
-        ++units;
-        auto logits = [&](int k) {
-          const int i = k & 1, j = nar ? k : k >> 1;
-          const uint32_t e = n + (nar ? (j == 0 ? 0 : 2 * j - 1) : 2 * j);
-          const uint32_t st = e % C::kStages;
-          if (!mbar_wait(&ctl->full[st], (e / C::kStages) & 1, kAtLong)) return false;
-          tc_fence_after();
-          const uint32_t qb = base + C::kOffQ + (nar ? 0 : i * C::kTile), kb = base + C::kOffRing + st * C::kTile;
+  } else if (warp == kAtMma || warp == kAtMma + 1) {
+    // ---- the MMAs of stream i: S of its first tile; then, tile by tile, O += P V and S of the next.  The whole warp
+    // walks along, with values that the compiler knows to be one for all lanes, and one lane issues: MMAs take their
+    // operands from uniform registers (a chunk of a 130,000-row prompt took a fifth longer with one lane alone in a
+    // branch).  Each stream has a warp of its own, which hides the waits between one's MMAs behind the other's
+    constexpr uint32_t id_s = umma_idesc_bf16(kAtRows, kAtKeys);
+    constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
+    const int i = __shfl_sync(0xffffffffu, warp - kAtMma, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts + C::kWeights;
+    const bool one = elect_one();
+    uint32_t units = 0, n = 0, p_it = 0, turns = 0;
+    bool ok = true;
+    // the streams issue in turns: one's burst of MMAs would otherwise slow the other's, and both softmaxes wait for both
+    auto my_turn = [&] { return (i == 0 && turns == 0) || mbar_wait_warp(&ctl->turn[i], (turns - (i == 0)) & 1, kAtLong); };
+    auto pass = [&] {
+      if (one) mbar_arrive(&ctl->turn[1 - i]);
+    };
+    for (bool more = any; more && ok; more = next_unit(a, r)) {
+      const int count = __shfl_sync(0xffffffffu, r.count, 0);
+      if (count == 0) continue;
+      const bool nar = __shfl_sync(0xffffffffu, (int)narrow(a, r.u), 0);
+      const int tiles = stream_tiles(nar, count, i);
+      ok = mbar_wait_warp(&ctl->qfull, units & 1, kAtLong);
+      if (!ok) break;
+      ++units;
+      const uint64_t qd = umma_desc_sw128(base + C::kOffQ + (nar ? 0 : i * C::kTile));
+      auto entry = [&](uint32_t pos, uint32_t& st) {  // waits for a tile
+        const uint32_t e = n + pos;
+        st = e % C::kStages;
+        return mbar_wait_warp(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
+      };
+      auto release = [&](uint32_t st) {  // (by both streams, or by the one that has it)
+        umma_commit(&ctl->empty[st]);
+        if (nar) umma_commit(&ctl->empty[st]);
+      };
+      auto key_entry = [&](int it) { return nar ? max(2 * (2 * it + i) - 1, 0) : 2 * it; };
+      auto logits = [&](int it, uint32_t st) {
+        const uint64_t kd = umma_desc_sw128(base + C::kOffRing + st * C::kTile);
+        if (one) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kSlab + (kk & 3) * 32;
-            umma_bf16(tmem + kAtS + 128 * i, umma_desc_sw128(qb + off), umma_desc_sw128(kb + off), id_s, kk > 0);
+            const uint32_t off = ((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4;  // (of the address field)
+            umma_bf16(ts, qd + off, kd + off, id_s, kk > 0);
+            if (kk == D / 16 - 3) mbar_arrive(&ctl->turn[1 - i]);  // (what is left covers the other's waking up)
           }
           umma_commit(&ctl->sfull[i]);
-          if (nar || i == 1) umma_commit(&ctl->empty[st]);
-          if (k == turns - 1) umma_commit(&ctl->qempty);
-          return true;
-        };
-        ok = logits(0);
-        if (ok && turns > 1) ok = logits(1);
-        for (int k = 0; k < turns && ok; ++k) {
-          const int i = k & 1, j = nar ? k : k >> 1;
-          const uint32_t e = n + (nar ? min(2 * j + 2, 2 * r.count - 1) : 2 * j + 1);
-          const uint32_t st = e % C::kStages;
-          ok = mbar_wait(&ctl->pfull[i], p_it[i] & 1, kAtLong) && mbar_wait(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
-          if (!ok) break;
-          ++p_it[i];
-          tc_fence_after();
-          const uint32_t vb = base + C::kOffRing + st * C::kTile;
-#pragma unroll
-          for (int kk = 0; kk < kAtKeys / 16; ++kk)
-            umma_bf16_ts(tmem + kAtO + 128 * i, tmem + kAtS + 128 * i + C::kWeights + 8 * kk,
-                         umma_desc_sw128_mn(vb + kk * 16 * 128, C::kSlab, 1024), id_o, k >= 2 || kk > 0);
-          if (nar || i == 1) umma_commit(&ctl->empty[st]);
-          if (k + 2 >= turns) umma_commit(&ctl->ofull[i]);
-          if (k + 2 < turns) ok = logits(k + 2);
+          release(st);
+          if (it == tiles - 1) umma_commit(&ctl->qempty);
         }
-        n += 2 * r.count;
+        __syncwarp();
+      };
+      uint32_t ks = 0, vs = 0;
+      if (tiles > 0) {
+        ok = entry(key_entry(0), ks);
+        if (!ok) break;
+        tc_fence_after();
+        ok = my_turn();
+        if (!ok) break;
+        ++turns;
+        logits(0, ks);
+      } else {
+        ok = my_turn();
+        if (!ok) break;
+        ++turns;
+        pass();
+        if (one) mbar_arrive(&ctl->qempty);
       }
-      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-      umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
-      (void)mbar_wait(&ctl->done, 0);
+      for (int it = 0; it < tiles; ++it) {
+        // (what the tiles' waits cost is over before the weights come)
+        ok = entry(nar ? min(2 * (2 * it + i) + 2, 2 * count - 1) : 2 * it + 1, vs) &&
+             (it + 1 == tiles || entry(key_entry(it + 1), ks)) &&
+             mbar_wait_warp(&ctl->phalf[i], p_it & 1, kAtLong) && my_turn();
+        if (!ok) break;
+        ++turns;
+        tc_fence_after();
+        const uint64_t vd = umma_desc_sw128_mn(base + C::kOffRing + vs * C::kTile, C::kSlab, 1024);
+        auto weigh = [&](int half, bool first) {
+#pragma unroll
+          for (int kk = 0; kk < kAtKeys / 32; ++kk) {
+            const int at = half * (kAtKeys / 32) + kk;
+            umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0);
+          }
+        };
+        constexpr int kFirst = Q8 ? 1 : 0;  // the half of the weights that comes first
+        if (one) weigh(kFirst, true);
+        __syncwarp();
+        ok = mbar_wait_warp(&ctl->pfull[i], p_it & 1, kAtLong);
+        if (!ok) break;
+        ++p_it;
+        tc_fence_after();
+        if (one) {
+          weigh(1 - kFirst, false);
+          release(vs);
+          if (it + 1 == tiles) umma_commit(&ctl->ofull[i]);
+        }
+        __syncwarp();
+        if (it + 1 < tiles)
+          logits(it + 1, ks);
+        else
+          pass();
+      }
+      if (ok && nar && i == 1 && tiles < stream_tiles(nar, count, 0)) {  // (a turn for each of the first stream's)
+        ok = my_turn();
+        ++turns;
+        pass();
+      }
+      n += 2 * count;
     }
+    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+    if (one) umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
+    (void)mbar_wait_warp(&ctl->done, 0);
   } else if (Q8 && warp >= kAtWiden) {
     // ---- int8 codes become bf16 tiles, a row to a thread; value rows behind the sequence's last are zeros
     uint32_t n = 0;
@@ -690,12 +824,14 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       }
     }
     if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-  } else if (warp < kAtMma) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoft));
     // ---- softmax: stream i, query row `row` (its TMEM lane)
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + kAtS + 128 * i, tp = ts + AtCfg<D, Q8>::kWeights;  // logits; the weights over them
-    if (tid == 0) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);  // (until a run says otherwise)
+    if (tid == 0) a.cut[blockIdx.x].parts = 0;  // (until a run says otherwise)
     const int tok = row / a.group, hh = row - tok * a.group;
     uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
     bool ok = true;
@@ -760,6 +896,12 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             }
           };
           const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+          auto half_done = [&] {  // the first half of the weights is in place: its product can begin
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->phalf[i]);
+          };
           if constexpr (!Q8) {
             float v[kAtKeys];
 #pragma unroll
@@ -770,11 +912,13 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
               for (int c = 0; c < kAtKeys; ++c)
                 if ((uint32_t)(c - from) >= wide) v[c] = -INFINITY;
             }
-            float top[4] = {v[0], v[1], v[2], v[3]};
+            float top[4];
 #pragma unroll
-            for (int c = 4; c < kAtKeys; c += 4)
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(v[e], v[4 + e]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
+            for (int c = 8; c < kAtKeys; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], v[c + e]), v[c + 4 + e]);
             refer(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
             const float2 ref2 = make_float2(-m, -m);
 #pragma unroll
@@ -788,6 +932,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
                 w[c] = pack2(e.x, e.y);
               }
               tmem_st32(tp + 32 * half, reinterpret_cast<const float*>(w));
+              if (half == 0) half_done();
             }
           } else {
             // 32 logits at a time, twice (128 registers a thread); the last 32 stay from the first pass to the second,
@@ -838,10 +983,13 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
                 w[e / 2 + 1] = pack2(u[2], u[3]);
               }
               tmem_st16(tp + 16 * c, reinterpret_cast<const float*>(w));
+              if (c == 2) half_done();
             }
           }
           tmem_wait_st();
           tc_fence_before();
+        } else if (lane == 0) {
+          mbar_arrive(&ctl->phalf[i]);
         }
         if constexpr (Q8) {
           __syncwarp();
@@ -887,8 +1035,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       }
       if ((!nar || i == 0) && !idle) {
         const bool cut = r.count < r.u.c;
-        // a CTA's part of a unit that began before it goes to slot 2 x CTA, of one that begins in it to the next
-        const int64_t slot = (2 * (int64_t)blockIdx.x + (r.first == 0 ? 1 : 0)) * a.rows_cap + my_tok * a.group + hh;
+        const int64_t slot = part_slot(blockIdx.x, r.first == 0) * a.rows_cap;
+        const int rho = my_tok * a.group + hh;
         const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
         const bool none = !cut && l == 0.f;
         bool bad = false;
@@ -896,7 +1044,6 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         for (int c = 0; c < D; c += 32) {
           float o[32];
           tmem_ld32(tl + kAtO + 128 * i + c, o);
-          tmem_wait_ld();
           if (both) {
             float o1[32];
             tmem_ld32(tl + kAtO + 128 + c, o1);
@@ -904,6 +1051,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
           }
+          tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             o[e] = none ? 0.f : o[e] * inv;
@@ -911,33 +1059,34 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           }
           if (!valid) continue;
           if (cut) {
+            float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + (int64_t)(c / 4) * a.rows_cap + rho;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(a.part_o + slot * D + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 4) to[(int64_t)(e / 4) * a.rows_cap] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           } else {
             write_out<D, 32>(a, token, head, c, o);
           }
         }
-        if (valid && cut) a.part_ml[slot] = make_float2(m, l);
+        if (valid && cut) a.part_ml[slot + rho] = make_float2(m, l);
         if (valid && !cut) write_lse(a, token, head, m, l);
-        if (!cut) {
-          uint32_t rows = Q8 ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
+        if (!cut && !Q8) {
+          uint32_t rows = __ballot_sync(0xffffffffu, valid && bad && finite(l));
           while (rows) {
             const int from = __ffs(rows) - 1;
             rows &= rows - 1;
             float y[D / 32];
             const int64_t t = __shfl_sync(0xffffffffu, token, from);
-            const int hd = __shfl_sync(0xffffffffu, head, from);
-            repair_row<D>(a, r.u.s, r.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
-                          __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), y);
-            write_out<D, D / 32>(a, t, hd, lane * (D / 32), y);
+            const int hd = __shfl_sync(0xffffffffu, head, from), col = lane * (D / 32);
+            repair_row<D, D / 32>(a, r.u.s, r.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
+                                  __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), col, y);
+            write_out<D, D / 32>(a, t, hd, col, y);
           }
         }
       }
       if (tid == 0 && r.first == 0) {
-        const int c0 = (int)(r.at / r.per);
-        const int parts = (int)((r.at + r.u.c - 1) / r.per) - c0 + 1;
-        if (parts > 1) a.cut[blockIdx.x] = make_int4(r.slot, r.h, c0, parts);
+        const uint64_t per = ctl->scratch.per;
+        const int c0 = (int)quotient(r.at, per);
+        const int parts = (int)quotient(r.at + r.u.c - 1, per) - c0 + 1;
+        if (parts > 1) a.cut[blockIdx.x] = AtCut{parts, c0, r.h, r.u.ntok, r.u.token0, r.slot, 0};
       }
       tc_fence_before();
       __syncwarp();
@@ -954,80 +1103,67 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   }
 }
 
-// The key tiles that each unit's tokens see, where tokens have ranges of their own.  A warp to a slot.
+// The key tiles that each unit's tokens see, where tokens have ranges of their own.
 constexpr int kArThreads = 128;
 __global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_constant__ AtArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
   const int slot = blockIdx.x * (kArThreads / 32) + (threadIdx.x >> 5);
-  if (slot >= a.slots) return;
-  const AtUnit u = unit_of<false>(a, find_seq(a, slot), slot);
-  int from = INT32_MAX, to = 0;
-  for (int i = lane; i < u.ntok; i += 32) {
-    int lo, hi;
-    token_rows(a, u.rows, u.n, u.tok0 + i, u.token0 + i, lo, hi);
-    if (hi > lo) from = min(from, lo), to = max(to, hi);
-  }
-  from = __reduce_min_sync(0xffffffffu, from);
-  to = __reduce_max_sync(0xffffffffu, to);
-  if (lane == 0) a.range[slot] = to > 0 ? make_int2(from / kAtKeys, (to - 1) / kAtKeys + 1) : make_int2(0, 0);
+  if (slot < a.slots) find_range(a, seqs_of(a), slot);
 }
 
-// Joins the parts of the units that several CTAs shared, a warp to a row.
+// Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and eight columns of them, a
+// row to a lane, eight parts in flight.
 constexpr int kAfThreads = 256;
 constexpr int kAfSplit = 8;  // CTAs to a unit
 template <int D>
 __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_constant__ AtArgs a) {
-  constexpr int E = D / 32;
+  constexpr int E = 8, N = 8;
   pdl_wait();
   pdl_trigger();
-  const int4 cut = a.cut[blockIdx.x / kAfSplit];
-  if (cut.w < 2) return;
+  const AtCut cut = a.cut[blockIdx.x / kAfSplit];
+  if (cut.parts < 2) return;
   const int lane = threadIdx.x & 31;
-  const AtUnit u = unit_of(a, find_seq(a, cut.x), cut.x);
-  for (int rho = (blockIdx.x % kAfSplit) * (kAfThreads / 32) + (threadIdx.x >> 5); rho < u.ntok * a.group;
-       rho += kAfSplit * (kAfThreads / 32)) {
+  const int rows = cut.ntok * a.group, blocks = (rows + 31) / 32;
+  for (int item = (blockIdx.x % kAfSplit) * (kAfThreads / 32) + (threadIdx.x >> 5); item < blocks * (D / E);
+       item += kAfSplit * (kAfThreads / 32)) {
+    const int col = item % (D / E) * E, rho = min(item / (D / E) * 32 + lane, rows - 1);
+    const bool valid = item / (D / E) * 32 + lane < rows;
     float m = -FLT_MAX, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    constexpr int N = 4;
-    for (int j0 = 0; j0 < cut.w; j0 += N) {
+    for (int j0 = 0; j0 < cut.parts; j0 += N) {
       float2 ml[N];
-      float x[N][E];
+      float4 x[N][2];
 #pragma unroll
       for (int f = 0; f < N; ++f) {
-        const int j = min(j0 + f, cut.w - 1);
-        const int64_t at = (2 * (int64_t)(cut.z + j) + (j == 0 ? 1 : 0)) * a.rows_cap + rho;
-        ml[f] = a.part_ml[at];
-        const float* from = a.part_o + at * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(from);
-          x[f][0] = y.x, x[f][1] = y.y, x[f][2] = y.z, x[f][3] = y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(from);
-          x[f][0] = y.x, x[f][1] = y.y;
-        }
+        const int j = min(j0 + f, cut.parts - 1);
+        const int64_t slot = part_slot(cut.c0 + j, j == 0) * a.rows_cap;
+        ml[f] = a.part_ml[slot + rho];
+        const float4* from = reinterpret_cast<const float4*>(a.part_o + slot * D) + (int64_t)(col / 4) * a.rows_cap + rho;
+        x[f][0] = from[0];
+        x[f][1] = from[a.rows_cap];
       }
-      float to = m;
+      float up = m;
 #pragma unroll
-      for (int f = 0; f < N; ++f) to = fmaxf(to, ml[f].x);
-      const float f0 = fast_exp2(m - to);
-      m = to;
+      for (int f = 0; f < N; ++f) up = fmaxf(up, ml[f].x);
+      const float f0 = fast_exp2(m - up);
+      m = up;
       l *= f0;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] *= f0;
 #pragma unroll
       for (int f = 0; f < N; ++f) {
-        if (j0 + f >= cut.w) continue;
+        if (j0 + f >= cut.parts) continue;
         const float w = fast_exp2(ml[f].x - m);
         l = fmaf(ml[f].y, w, l);
+        const float* y = reinterpret_cast<const float*>(x[f]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x[f][e], w, o[e]);
+        for (int e = 0; e < E; ++e) o[e] = fmaf(y[e], w, o[e]);
       }
     }
-    const int my_tok = rho / a.group, head = cut.y * a.group + rho % a.group;
-    const int64_t token = u.token0 + my_tok;
+    const int my_tok = rho / a.group, head = cut.h * a.group + rho % a.group;
+    const int64_t token = cut.token0 + my_tok;
     const float inv = 1.f / l;
     bool bad = false;
 #pragma unroll
@@ -1035,13 +1171,23 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
       o[e] = l == 0.f ? 0.f : o[e] * inv;
       bad |= !finite(o[e]);
     }
-    if (!a.pages.k_scale && __any_sync(0xffffffffu, bad) && finite(l)) {
-      int lo, hi;
-      token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
-      repair_row<D>(a, u.s, cut.y, token, head, lo, hi, m, l, o);
+    if (valid) write_out<D, E>(a, token, head, col, o);
+    if (valid && col == 0) write_lse(a, token, head, m, l);
+    uint32_t wrong = a.pages.k_scale ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
+    if (!wrong) continue;
+    const AtUnit u = unit_of(a, seqs_of(a), find_seq(a, seqs_of(a), cut.slot), cut.slot);
+    int lo, hi;
+    token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
+    while (wrong) {
+      const int from = __ffs(wrong) - 1;
+      wrong &= wrong - 1;
+      float y[1];
+      const int64_t t = __shfl_sync(0xffffffffu, token, from);
+      const int hd = __shfl_sync(0xffffffffu, head, from), c = lane < E ? col + lane : D;
+      repair_row<D, 1>(a, u.s, cut.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
+                       __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), c, y);
+      if (lane < E) write_out<D, 1>(a, t, hd, c, y);
     }
-    write_out<D, E>(a, token, head, lane * E, o);
-    if (lane == 0) write_lse(a, token, head, m, l);
   }
 }
 
@@ -1098,12 +1244,17 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   CUtensorMap qm, km, vm;
   if (!encode_q(&qm, p, pl) || !encode_kv(&km, pl.pages.k, pl) || !encode_kv(&vm, pl.pages.v, pl))
     return AIRCACHE_ERR_UNSUPPORTED;
-  constexpr int smem = C::kOffCtl + (int)sizeof(AtCtl<D, Q8>) + 1024;
+  constexpr int smem = C::kOffCtl + (int)sizeof(AtCtl<D, Q8>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  if (a.range && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
+  if (a.range && a.ranged && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
                             dim3(kArThreads), 0, s, a) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
+  static const int regs = [] {  // what the warps share out between them is what the launch brings
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>)) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs < C::kRegs) return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid);
   cfg.blockDim = dim3(C::kThreads);
@@ -1163,7 +1314,7 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
   pl.grid = device_sms();
   pl.rows_cap = (int)std::min<int64_t>(2 * pl.tok_tile, std::max<int64_t>(p->num_tokens, 1)) * pl.g;
   pl.cut_off = kAtHeader;
-  pl.range_off = pl.cut_off + up256(sizeof(int4) * (size_t)pl.grid);
+  pl.range_off = pl.cut_off + up256(sizeof(AtCut) * (size_t)pl.grid);
   pl.ml_off = pl.range_off + (p->row_begin || p->row_end ? up256(sizeof(int2) * (size_t)pl.slots) : 0);
   pl.o_off = pl.ml_off + up256(sizeof(float2) * 2 * (size_t)pl.grid * pl.rows_cap);
   pl.total = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.rows_cap * pl.d);
@@ -1186,7 +1337,7 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.lse = p->lse;
   a.part = part;
   a.error = error;
-  a.cut = reinterpret_cast<int4*>(ws + pl.cut_off);
+  a.cut = reinterpret_cast<AtCut*>(ws + pl.cut_off);
   a.range = p->row_begin || p->row_end ? reinterpret_cast<int2*>(ws + pl.range_off) : nullptr;
   a.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + pl.o_off);
@@ -1196,7 +1347,7 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.tok_tile = pl.tok_tile;
   a.h_q = p->h_q;
   a.causal = p->causal;
-  a.ctas = pl.grid;
+  a.ranged = pl.slots > kAtRanged;
   a.rows_cap = pl.rows_cap;
   a.box = box_rows(pl.pages.page_rows);
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
