@@ -33,6 +33,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "attend.cuh"
 #include "rowmma.cuh"
@@ -45,7 +46,7 @@ namespace {
 constexpr int kAtKeys = 128;                  // rows of a key tile
 constexpr int kAtRows = 128;                  // query rows of a stream (TMEM lanes)
 // Behind the eight softmax warps: the streams' MMA issue (8 and 9), keys and values, queries and tails; from 12 on
-// four that widen int8 codes
+// eight that widen int8 codes
 constexpr int kAtMma = 8, kAtLoad = 10, kAtAux = 11, kAtWiden = 12;
 constexpr uint32_t kAtEnd = 2;                // places of the line for a unit's end
 constexpr float kAtSlack = 8.f;               // base-2 powers that a maximum may pass its reference by
@@ -58,9 +59,9 @@ constexpr long long kAtLong = 4 * kWaitCycles;  // waits that stand behind anoth
 
 template <int D, bool Q8>
 struct AtCfg {
-  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kThreads = Q8 ? 640 : 384;
   // registers of a thread: what the other warps give, the softmax warps, which hold a row of 128 logits, take
-  static constexpr int kRegs = Q8 ? 128 : 168, kRegsSoft = Q8 ? 160 : 200, kRegsOther = Q8 ? 96 : 104;
+  static constexpr int kRegs = Q8 ? 96 : 168, kRegsSoft = Q8 ? 144 : 200, kRegsOther = Q8 ? 64 : 104;
   static_assert(256 * kRegsSoft + (kThreads - 256) * kRegsOther <= kThreads * kRegs, "within the launch's own");
   static constexpr int kSlab = kAtKeys * 128;       // [128 rows][64 bf16]
   static constexpr int kTile = kSlab * (D / 64);
@@ -68,7 +69,6 @@ struct AtCfg {
   static constexpr int kCodeTile = kAtKeys * D;                // int8 rows: tiles of codes before them,
   static constexpr int kCodeStages = Q8 ? (D == 128 ? 3 : 8) : 0;
   static constexpr int kScaleStages = Q8 ? 4 : 0;              // and the scales of a key tile's keys and values
-  static constexpr int kWeights = Q8 ? 64 : 0;                 // column of S that the weights start at
   static constexpr int kOffQ = 0;                              // two query tiles
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffCodes = kOffRing + kStages * kTile;
@@ -136,11 +136,28 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return r;
 }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 // True for one lane of the warp, always the same.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+// Logits of 32 keys from `at` on: those outside [from, from + wide) become -inf.  By a warp, each lane its own row's.
+__device__ __forceinline__ void mask32(float v[32], int from, uint32_t wide, int at) {
+  const int lo = min(max(from - at, 0), 32);
+  const int hi = (int)min(max((int64_t)from + wide - at, (int64_t)0), (int64_t)32);
+  const uint32_t in = (uint32_t)(((1ull << hi) - 1) & ~((1ull << lo) - 1));
+  if (__all_sync(0xffffffffu, in == 0xffffffffu)) return;
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = in >> c & 1 ? v[c] : -INFINITY;
 }
 // Arrives `n` times.
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
@@ -290,7 +307,7 @@ __device__ __forceinline__ bool entry_of(bool nar, int count, int pos, int& j) {
 }
 
 struct AtScratch {
-  uint64_t sum[16];
+  uint64_t sum[24];
   AtRun run;
   uint64_t per;  // places of a CTA
 };
@@ -300,9 +317,10 @@ struct AtCtl {
   static constexpr int kCodes = Q8 ? C::kCodeStages : 1, kScales = Q8 ? C::kScaleStages : 1;
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t tail[C::kStages];  // of a stage that holds values to be cleared in part: its copies have landed
-  uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scempty[kScales];
+  uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scready[kScales], scempty[kScales];
   uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done;
   uint32_t tmem;
+  uint8_t vbad[kScales][kAtKeys];  // int8 values whose scale is not finite
   float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
   AtScratch scratch;
   AtRun run[C::kThreads / 32];  // each warp's place: read seldom, not worth registers
@@ -314,7 +332,7 @@ __device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
 // By all threads of the CTA; false if the CTA has no place.
 template <int THREADS>
 __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun& r) {
-  static_assert(THREADS <= 512, "warps' sums");
+  static_assert(THREADS <= 768, "warps' sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.slots + THREADS - 1) / THREADS;
   const int s0 = min(tid * each, a.slots), s1 = min(s0 + each, a.slots);
@@ -397,13 +415,25 @@ __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t t
     for (int e = 0; e < E; ++e) v[e] = 0.f;
     if (page_ok(p, page)) {
       const int64_t at = page_elem(p, page, h, j % p.page_rows);
-      const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
-      const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
+      if (p.k_scale) {
+        const int64_t slot = page_slot(p, page, h, j % p.page_rows);
+        const int8_t* k = reinterpret_cast<const int8_t*>(p.k) + at + lane * Q;
+        const int8_t* vv = reinterpret_cast<const int8_t*>(p.v) + at;
 #pragma unroll
-      for (int e = 0; e < Q; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x);
+        for (int e = 0; e < Q; ++e) x = fmaf(qv[e], (float)k[e], x);
+        x *= p.k_scale[slot];
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (col + e < D) v[e] = __bfloat162float(vv[col + e]);
+        for (int e = 0; e < E; ++e)
+          if (col + e < D) v[e] = (float)vv[col + e] * p.v_scale[slot];
+      } else {
+        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
+        const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
+#pragma unroll
+        for (int e = 0; e < Q; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (col + e < D) v[e] = __bfloat162float(vv[col + e]);
+      }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -415,7 +445,6 @@ __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t t
 #pragma unroll
   for (int e = 0; e < E; ++e) y[e] *= inv;
 }
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= FLT_MAX; }
 
 // A CTA's part of a unit that began before it lies in slot 2 x CTA, of one that begins in it in the next.  A slot holds
 // [D / 4][rows_cap] pieces of four columns, so that a warp's rows are next to one another.
@@ -473,16 +502,17 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   const Pages& p = a.pages;
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&ctl->full[i], Q8 ? 4 : 1);
+      mbar_init(&ctl->full[i], Q8 ? 8 : 1);
       mbar_init(&ctl->empty[i], 2);
       mbar_init(&ctl->tail[i], 1);
     }
     for (int i = 0; i < C::kCodeStages; ++i) {
       mbar_init(&ctl->cfull[i], 1);
-      mbar_init(&ctl->cempty[i], 4);
+      mbar_init(&ctl->cempty[i], 8);
     }
     for (int i = 0; i < C::kScaleStages; ++i) {
       mbar_init(&ctl->scfull[i], 1);
+      mbar_init(&ctl->scready[i], 8);
       mbar_init(&ctl->scempty[i], 8);
     }
     mbar_init(&ctl->qfull, 1);
@@ -682,7 +712,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
     const int i = __shfl_sync(0xffffffffu, warp - kAtMma, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts + C::kWeights;
+    const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts;
     const bool one = elect_one();
     uint32_t units = 0, n = 0, p_it = 0, turns = 0;
     bool ok = true;
@@ -757,15 +787,14 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0);
           }
         };
-        constexpr int kFirst = Q8 ? 1 : 0;  // the half of the weights that comes first
-        if (one) weigh(kFirst, true);
+        if (one) weigh(0, true);
         __syncwarp();
         ok = mbar_wait_warp(&ctl->pfull[i], p_it & 1, kAtLong);
         if (!ok) break;
         ++p_it;
         tc_fence_after();
         if (one) {
-          weigh(1 - kFirst, false);
+          weigh(1, false);
           release(vs);
           if (it + 1 == tiles) umma_commit(&ctl->ofull[i]);
         }
@@ -786,10 +815,11 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     if (one) umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
     (void)mbar_wait_warp(&ctl->done, 0);
   } else if (Q8 && warp >= kAtWiden) {
-    // ---- int8 codes become bf16 tiles, a row to a thread; value rows behind the sequence's last are zeros
+    // ---- int8 codes become bf16 tiles, half a row to a thread; value rows behind the sequence's last are zeros
     uint32_t n = 0;
     bool ok = true;
-    const int row = tid - kAtWiden * 32;
+    const int row = (tid - kAtWiden * 32) & 127, half = (tid - kAtWiden * 32) >> 7;
+    uint32_t tiles = 0;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
       if (r.count == 0) continue;
       const bool nar = narrow(a, r.u);
@@ -800,28 +830,53 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
         if (ok && n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
         if (!ok) break;
+        const uint32_t sc = (tiles + j) % (Q8 ? C::kScaleStages : 1);
+        const bool behind = (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
+        if (!val) {
+          // a key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
+          // weight of 0 makes of that is mended as bf16 rows' is
+          ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles + j) / (Q8 ? C::kScaleStages : 1)) & 1, kAtLong);
+          if (!ok) break;
+          float* scale = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 2 + half) * kAtKeys + row;
+          if (half == 0) {
+            *scale *= a.scale_log2;
+          } else {
+            const float x = behind ? 0.f : *scale;
+            *scale = finite(x) ? x : 1.f;
+            ctl->vbad[sc][row] = !finite(x);
+          }
+        }
         const uint8_t* from = sm + C::kOffCodes + cs * C::kCodeTile;
         uint8_t* to = sm + C::kOffRing + st * C::kTile + row * 128;
-        const bool zero = val && (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
+        const bool zero = val && behind, bad = val && ctl->vbad[sc][row];
+        uint4 x[D / 32];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint4 x = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * c));
-          if (zero) x = make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < D / 32; ++q)
+          x[q] = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * (half * (D / 32) + q)));
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          const int c = half * (D / 32) + q;
+          uint4 lo = make_uint4(widen2_bf16(x[q].x, 0x4140u), widen2_bf16(x[q].x, 0x4342u), widen2_bf16(x[q].y, 0x4140u),
+                                widen2_bf16(x[q].y, 0x4342u));
+          uint4 hi = make_uint4(widen2_bf16(x[q].z, 0x4140u), widen2_bf16(x[q].z, 0x4342u), widen2_bf16(x[q].w, 0x4140u),
+                                widen2_bf16(x[q].w, 0x4342u));
+          if (zero || bad) {
+            const uint32_t u = bad ? 0x7fc07fc0u : 0u;
+            lo = hi = make_uint4(u, u, u, u);
+          }
           uint8_t* slab = to + (c >> 2) * C::kSlab;
-          *reinterpret_cast<uint4*>(slab + (((2 * c) & 7) ^ (row & 7)) * 16) =
-              make_uint4(widen2_bf16(x.x, 0x4140u), widen2_bf16(x.x, 0x4342u), widen2_bf16(x.y, 0x4140u),
-                         widen2_bf16(x.y, 0x4342u));
-          *reinterpret_cast<uint4*>(slab + (((2 * c + 1) & 7) ^ (row & 7)) * 16) =
-              make_uint4(widen2_bf16(x.z, 0x4140u), widen2_bf16(x.z, 0x4342u), widen2_bf16(x.w, 0x4140u),
-                         widen2_bf16(x.w, 0x4342u));
+          *reinterpret_cast<uint4*>(slab + (((2 * c) & 7) ^ (row & 7)) * 16) = lo;
+          *reinterpret_cast<uint4*>(slab + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
+          if (!val) mbar_arrive(&ctl->scready[sc]);
           mbar_arrive(&ctl->full[st]);
           mbar_arrive(&ctl->cempty[cs]);
         }
       }
+      tiles += r.count;
     }
     if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
   }
@@ -830,7 +885,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     // ---- softmax: stream i, query row `row` (its TMEM lane)
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = tl + kAtS + 128 * i, tp = ts + AtCfg<D, Q8>::kWeights;  // logits; the weights over them
+    const uint32_t ts = tl + kAtS + 128 * i, tp = ts;  // logits; the weights over them
     if (tid == 0) a.cut[blockIdx.x].parts = 0;  // (until a run says otherwise)
     const int tok = row / a.group, hh = row - tok * a.group;
     uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
@@ -867,7 +922,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         const int k0 = (r.u.t0 + r.first + j) * kAtKeys;
         const uint32_t sc = Q8 ? (tiles0 + j) % (Q8 ? C::kScaleStages : 1) : 0;
         if constexpr (Q8) {
-          ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles0 + j) / C::kScaleStages) & 1, kAtLong);
+          ok = mbar_wait_warp(&ctl->scready[sc], ((tiles0 + j) / C::kScaleStages) & 1, kAtLong);
           if (!ok) break;
         }
         if (!idle) {
@@ -877,7 +932,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           const float* ks = reinterpret_cast<const float*>(sm + C::kOffScales) + sc * 2 * kAtKeys;
           // moves the reference to a maximum that passes it by more than the slack
           auto refer = [&](float top) {
-            const float mx = top * a.scale_log2;
+            const float mx = Q8 ? top : top * a.scale_log2;
             if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
               const float to = fmaxf(m, mx), f = fast_exp2(m - to);
               m = to;
@@ -909,8 +964,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             tmem_wait_ld();
             if (masked) {
 #pragma unroll
-              for (int c = 0; c < kAtKeys; ++c)
-                if ((uint32_t)(c - from) >= wide) v[c] = -INFINITY;
+              for (int h = 0; h < kAtKeys; h += 32) mask32(v + h, from, wide, h);
             }
             float top[4];
 #pragma unroll
@@ -935,55 +989,59 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
               if (half == 0) half_done();
             }
           } else {
-            // 32 logits at a time, twice (128 registers a thread); the last 32 stay from the first pass to the second,
-            // which goes backwards and writes the weights from the buffer's end on
-            float v[32];
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            auto logits = [&](int c) {
-              tmem_ld32(ts + 32 * c, v);
+            // 64 at a time (144 registers a thread): the logits get the key's scale and their mask and go back to where
+            // they were, then come again as weights, which get the value's scale
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int h = 0; h < kAtKeys; h += 64) {
+              float v[64];
+              tmem_ld32(ts + h, v);
+              tmem_ld32(ts + h + 32, v + 32);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * c + e);
-                v[e] *= k4.x, v[e + 1] *= k4.y, v[e + 2] *= k4.z, v[e + 3] *= k4.w;
+              for (int e = 0; e < 64; e += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(ks + h + e);
+                const float2 x = mul2(make_float2(v[e], v[e + 1]), make_float2(k4.x, k4.y));
+                const float2 y = mul2(make_float2(v[e + 2], v[e + 3]), make_float2(k4.z, k4.w));
+                v[e] = x.x, v[e + 1] = x.y, v[e + 2] = y.x, v[e + 3] = y.y;
               }
               if (masked) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if ((uint32_t)(32 * c + e - from) >= wide) v[e] = -INFINITY;
+                mask32(v, from, wide, h);
+                mask32(v + 32, from, wide, h + 32);
               }
-            };
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              logits(c);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], v[e]);
+              for (int e = 0; e < 64; e += 4) {
+                top[0] = fmaxf(fmaxf(top[0], v[e]), v[e + 1]);
+                top[1] = fmaxf(fmaxf(top[1], v[e + 2]), v[e + 3]);
+              }
+              tmem_st32(ts + h, v);
+              tmem_st32(ts + h + 32, v + 32);
             }
-            refer(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            refer(fmaxf(top[0], top[1]));
+            tmem_wait_st();
             const float2 ref2 = make_float2(-m, -m);
 #pragma unroll 1
-            for (int c = 3; c >= 0; --c) {
-              if (c < 3) logits(c);
-              uint32_t w[16];
+            for (int h = 0; h < kAtKeys; h += 64) {
+              float v[64];
+              tmem_ld32(ts + h, v);
+              tmem_ld32(ts + h + 32, v + 32);
+              tmem_wait_ld();
+              uint32_t w[32];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float2 x = fma2(make_float2(v[e], v[e + 1]), scale2, ref2);
-                const float2 y = fma2(make_float2(v[e + 2], v[e + 3]), scale2, ref2);
-                const float4 z = make_float4(fast_exp2(x.x), fast_exp2(x.y), fast_exp2(y.x), fast_exp2(y.y));
-                sum[0] = add2(sum[0], make_float2(z.x, z.y));
-                sum[1] = add2(sum[1], make_float2(z.z, z.w));
-                const float4 v4 = *reinterpret_cast<const float4*>(ks + kAtKeys + 32 * c + e);
-                float u[4] = {z.x * v4.x, z.y * v4.y, z.z * v4.z, z.w * v4.w};
-                if (masked) {  // (a scale may be anything there)
-#pragma unroll
-                  for (int f = 0; f < 4; ++f)
-                    if ((uint32_t)(32 * c + e + f - from) >= wide) u[f] = 0.f;
-                }
-                w[e / 2] = pack2(u[0], u[1]);
-                w[e / 2 + 1] = pack2(u[2], u[3]);
+              for (int e = 0; e < 64; e += 4) {
+                const float4 v4 = *reinterpret_cast<const float4*>(ks + kAtKeys + h + e);
+                float2 x = add2(make_float2(v[e], v[e + 1]), ref2), y = add2(make_float2(v[e + 2], v[e + 3]), ref2);
+                x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                sum[0] = add2(sum[0], x);
+                sum[1] = add2(sum[1], y);
+                x = mul2(x, make_float2(v4.x, v4.y));
+                y = mul2(y, make_float2(v4.z, v4.w));
+                w[e / 2] = pack2(x.x, x.y);
+                w[e / 2 + 1] = pack2(y.x, y.y);
               }
-              tmem_st16(tp + 16 * c, reinterpret_cast<const float*>(w));
-              if (c == 2) half_done();
+              tmem_st32(tp + h / 2, reinterpret_cast<const float*>(w));
+              if (h == 0) half_done();
             }
           }
           tmem_wait_st();
@@ -1068,7 +1126,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         }
         if (valid && cut) a.part_ml[slot + rho] = make_float2(m, l);
         if (valid && !cut) write_lse(a, token, head, m, l);
-        if (!cut && !Q8) {
+        if (!cut) {
           uint32_t rows = __ballot_sync(0xffffffffu, valid && bad && finite(l));
           while (rows) {
             const int from = __ffs(rows) - 1;
@@ -1173,7 +1231,7 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
     }
     if (valid) write_out<D, E>(a, token, head, col, o);
     if (valid && col == 0) write_lse(a, token, head, m, l);
-    uint32_t wrong = a.pages.k_scale ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
+    uint32_t wrong = __ballot_sync(0xffffffffu, valid && bad && finite(l));
     if (!wrong) continue;
     const AtUnit u = unit_of(a, seqs_of(a), find_seq(a, seqs_of(a), cut.slot), cut.slot);
     int lo, hi;
