@@ -53,7 +53,6 @@ constexpr float kAtSlack = 8.f;               // base-2 powers that a maximum ma
 constexpr uint32_t kAtS = 0, kAtO = 256;      // TMEM columns: S of stream i at 128 i, O at 256 + 128 i
 constexpr int kAtGroup = 16;                  // query heads of a KV head, at most
 constexpr int kAtStaged = 4096;               // sequences whose lengths and offsets go through shared memory
-constexpr int kAtRanged = 48;                 // units up to which every CTA finds their ranges
 constexpr int kAtHeader = 256;                // workspace: error word
 constexpr long long kAtLong = 4 * kWaitCycles;  // waits that stand behind another warp's
 
@@ -100,7 +99,8 @@ struct AtArgs {
   float2* part_ml;  // [2 CTAs][rows_cap]
   float* part_o;    // [2 CTAs][rows_cap][D]
   int64_t num_tokens;
-  int slots, group, tok_tile, h_q, causal, ranged, rows_cap, box;  // ranged: a kernel has filled `range`
+  int slots, group, tok_tile, h_q, causal, ranged, rows_cap, box, ctas;  // ranged: a kernel has filled `range`; otherwise
+                                                                   // every CTA does, with the same
   float scale_log2;
 };
 
@@ -192,15 +192,14 @@ struct AtSeqs {
   const int32_t* lens;
 };
 __device__ __forceinline__ AtSeqs seqs_of(const AtArgs& a) { return {a.cu, a.pages.lens}; }
-__device__ __forceinline__ int slot_base(const AtArgs& a, const AtSeqs& q, int s) {
-  const int c = min(max(q.cu[s], 0), (int)a.num_tokens);
-  return c / (2 * a.tok_tile) + s;
+__device__ __forceinline__ int slot_base(const AtArgs& a, int c0, int s) {
+  return min(max(c0, 0), (int)a.num_tokens) / (2 * a.tok_tile) + s;
 }
 __device__ __forceinline__ int find_seq(const AtArgs& a, const AtSeqs& q, int slot) {
   int lo = 0, hi = a.pages.num_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (slot_base(a, q, mid) <= slot)
+    if (slot_base(a, q.cu[mid], mid) <= slot)
       lo = mid;
     else
       hi = mid - 1;
@@ -215,24 +214,22 @@ __device__ __forceinline__ void token_rows(const AtArgs& a, int rows, int n, int
   if (a.row_end) hi = min(hi, a.row_end[token]);
   if (hi <= lo) lo = hi = 0;
 }
-// The unit of `slot` in sequence s; ntok = 0 when there is none.  LISTED: its key tiles are in a.range.
-template <bool LISTED = true>
-__device__ __forceinline__ AtUnit unit_of(const AtArgs& a, const AtSeqs& q, int s, int slot) {
+// The unit of `slot` in sequence s, whose tokens are c0 .. c1 - 1 and whose rows len; ntok = 0 when there is none.
+// range: where the units' key tiles are listed, if tokens have ranges of their own.
+__device__ __forceinline__ AtUnit make_unit(const AtArgs& a, int s, int slot, int c0, int c1, int len, const int2* range) {
   AtUnit u;
   u.s = s;
-  const int c0 = q.cu[s], c1 = q.cu[s + 1];
   u.n = c0 >= 0 && c1 >= c0 && c1 <= a.num_tokens ? c1 - c0 : 0;
-  const int len = q.lens[s];
   u.rows = len >= 0 && len <= a.pages.max_rows ? len : 0;
-  const int64_t first = (int64_t)(slot - slot_base(a, q, s)) * (2 * a.tok_tile);
+  const int64_t first = (int64_t)(slot - slot_base(a, c0, s)) * (2 * a.tok_tile);
   const bool in = first >= 0 && first < u.n;
   u.tok0 = in ? (int)first : 0;
   u.ntok = in ? min(2 * a.tok_tile, u.n - u.tok0) : 0;
   u.token0 = (int64_t)c0 + u.tok0;
   u.t0 = u.c = 0;
   if (in) {
-    if (LISTED && a.range) {
-      const int2 r = a.range[slot];
+    if (range) {
+      const int2 r = range[slot];
       u.t0 = r.x;
       u.c = r.y - r.x;
     } else {
@@ -242,10 +239,13 @@ __device__ __forceinline__ AtUnit unit_of(const AtArgs& a, const AtSeqs& q, int 
   }
   return u;
 }
+__device__ __forceinline__ AtUnit unit_of(const AtArgs& a, const AtSeqs& q, int s, int slot, const int2* range) {
+  return make_unit(a, s, slot, q.cu[s], q.cu[s + 1], q.lens[s], range);
+}
 
 // A unit's key tiles by its tokens' own ranges, by a warp.
 __device__ __forceinline__ void find_range(const AtArgs& a, const AtSeqs& q, int slot) {
-  const AtUnit u = unit_of<false>(a, q, find_seq(a, q, slot), slot);
+  const AtUnit u = unit_of(a, q, find_seq(a, q, slot), slot, nullptr);
   int from = INT32_MAX, to = 0;
   for (int i = threadIdx.x & 31; i < u.ntok; i += 32) {
     int lo, hi;
@@ -277,8 +277,8 @@ __device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r) {
     do {
       if (++r.slot >= a.slots) return false;
       int s = r.u.s;
-      while (s + 1 < a.pages.num_seqs && slot_base(a, seqs_of(a), s + 1) <= r.slot) ++s;
-      r.u = unit_of(a, seqs_of(a), s, r.slot);
+      while (s + 1 < a.pages.num_seqs && slot_base(a, a.cu[s + 1], s + 1) <= r.slot) ++s;
+      r.u = unit_of(a, seqs_of(a), s, r.slot, a.range);
     } while (r.u.ntok == 0);
   }
   clip(r);
@@ -329,6 +329,46 @@ struct AtCtl {
 __device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
   return ((x | y) >> 32) == 0 ? (uint32_t)x / (uint32_t)y : x / y;
 }
+// At most 32 slots: every warp finds the CTA's place by itself, a slot to a lane.  Lane s has the offsets c0, c1 of sequence
+// s and its length.
+__device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, int len, AtScratch* sc, AtRun& r) {
+  const int lane = threadIdx.x & 31;
+  const int base = lane < a.pages.num_seqs ? slot_base(a, c0, lane) : INT32_MAX;
+  int s = 0;  // the last sequence that starts at the lane's slot or before
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1) {
+    const int x = __shfl_sync(0xffffffffu, base, s + step);
+    if (x <= lane) s += step;
+  }
+  const int u0 = __shfl_sync(0xffffffffu, c0, s), u1 = __shfl_sync(0xffffffffu, c1, s), ul = __shfl_sync(0xffffffffu, len, s);
+  AtUnit u;
+  u.ntok = 0;
+  if (lane < a.slots) u = make_unit(a, s, lane, u0, u1, ul, a.range);
+  const uint64_t wide = u.c + kAtEnd, mine = u.ntok ? wide * a.pages.h_kv : 0;
+  uint64_t incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
+  const uint64_t per = max((uint64_t)1, quotient(total + gridDim.x - 1, gridDim.x));
+  const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
+  if (threadIdx.x == 0) sc->per = per;
+  if (lo < hi && lo >= incl - mine && lo < incl) {
+    AtRun x;
+    x.lo = lo;
+    x.hi = hi;
+    x.slot = lane;
+    x.h = (int)quotient(lo - (incl - mine), wide);
+    x.at = incl - mine + x.h * wide;
+    x.u = u;
+    clip(x);
+    r = x;
+  }
+  __syncwarp();
+  return lo < hi;
+}
 // By all threads of the CTA; false if the CTA has no place.
 template <int THREADS>
 __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun& r) {
@@ -341,8 +381,8 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
   if (s0 < s1) {
     int s = seq0 = find_seq(a, q, s0);
     for (int i = s0; i < s1; ++i) {
-      while (s + 1 < a.pages.num_seqs && slot_base(a, q, s + 1) <= i) ++s;
-      const AtUnit u = unit_of(a, q, s, i);
+      while (s + 1 < a.pages.num_seqs && slot_base(a, q.cu[s + 1], s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, q, s, i, a.range);
       if (u.ntok) mine += (uint64_t)(u.c + kAtEnd) * a.pages.h_kv;
     }
   }
@@ -367,8 +407,8 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
     uint64_t at = before;
     int s = seq0;
     for (int i = s0; i < s1; ++i) {
-      while (s + 1 < a.pages.num_seqs && slot_base(a, q, s + 1) <= i) ++s;
-      const AtUnit u = unit_of(a, q, s, i);
+      while (s + 1 < a.pages.num_seqs && slot_base(a, q.cu[s + 1], s + 1) <= i) ++s;
+      const AtUnit u = unit_of(a, q, s, i, a.range);
       if (!u.ntok) continue;
       const uint64_t wide = u.c + kAtEnd;
       if (lo < at + wide * a.pages.h_kv) {
@@ -541,33 +581,40 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   }
   pdl_wait();
   pdl_trigger();
-  // lengths and token offsets lie where the tiles will until the CTA has found its place: searches go to shared memory
-  AtSeqs seqs = seqs_of(a);
-  if (p.num_seqs <= kAtStaged) {
-    int32_t* lens = reinterpret_cast<int32_t*>(sm);
-    int32_t* cu = lens + kAtStaged;
-    for (int s = tid; s <= p.num_seqs; s += C::kThreads) {
-      cu[s] = a.cu[s];
-      if (s < p.num_seqs) lens[s] = p.lens[s];
-    }
-    seqs = {cu, lens};
-    __syncthreads();
-  }
-  if (blockIdx.x == 0) {  // what the batch's description says that cannot be
-    bool bad = tid == 0 && seqs.cu[0] < 0;
-    for (int s = tid; s < p.num_seqs; s += C::kThreads) {
-      const int c0 = seqs.cu[s], c1 = seqs.cu[s + 1], len = seqs.lens[s];
-      bad |= c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
-    }
-    if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
-  }
-  if (a.range && !a.ranged) {  // few units: each CTA finds what their tokens see by itself (all write the same)
-    for (int slot = warp; slot < a.slots; slot += C::kThreads / 32) find_range(a, seqs, slot);
-    __syncthreads();
-  }
-  tc_fence_before();
   AtRun& r = ctl->run[warp];
-  const bool any = make_run<C::kThreads>(a, seqs, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+  bool any;
+  auto wrong = [&](int c0, int c1, int len) {  // what a batch's description says that cannot be
+    return c0 < 0 || c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
+  };
+  tc_fence_before();
+  if (a.slots <= 32) {
+    const bool in = lane < p.num_seqs;
+    const int c0 = in ? a.cu[lane] : 0, c1 = in ? a.cu[lane + 1] : 0, len = in ? p.lens[lane] : 0;
+    if (blockIdx.x == 0 && warp == 0 && in && wrong(c0, c1, len)) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+    if (a.range && !a.ranged)
+      for (int slot = warp; slot < a.slots; slot += C::kThreads / 32) find_range(a, seqs_of(a), slot);
+    __syncthreads();  // (publishes the mbarriers and TMEM too)
+    any = make_run_small(a, c0, c1, len, &ctl->scratch, r);
+  } else {
+    // lengths and token offsets lie where the tiles will until the CTA has found its place: searches go to shared memory
+    AtSeqs seqs = seqs_of(a);
+    if (p.num_seqs <= kAtStaged) {
+      int32_t* lens = reinterpret_cast<int32_t*>(sm);
+      int32_t* cu = lens + kAtStaged;
+      for (int s = tid; s <= p.num_seqs; s += C::kThreads) {
+        cu[s] = a.cu[s];
+        if (s < p.num_seqs) lens[s] = p.lens[s];
+      }
+      seqs = {cu, lens};
+      __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+      bool bad = false;
+      for (int s = tid; s < p.num_seqs; s += C::kThreads) bad |= wrong(seqs.cu[s], seqs.cu[s + 1], seqs.lens[s]);
+      if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+    }
+    any = make_run<C::kThreads>(a, seqs, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+  }
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
@@ -1096,34 +1143,38 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         const int64_t slot = part_slot(blockIdx.x, r.first == 0) * a.rows_cap;
         const int rho = my_tok * a.group + hh;
         const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        const bool none = !cut && l == 0.f;
-        bool bad = false;
+        float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + rho;
+        float not_finite = 0.f;  // (0 times what is not finite is NaN)
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(tl + kAtO + 128 * i + c, o);
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tmem_ld16(tl + kAtO + 128 * i + c, o);
           if (both) {
-            float o1[32];
-            tmem_ld32(tl + kAtO + 128 + c, o1);
+            float o1[16];
+            tmem_ld16(tl + kAtO + 128 + c, o1);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+            for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + o1[e] * f1;
           }
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            o[e] = none ? 0.f : o[e] * inv;
-            bad |= !finite(o[e]);
+          for (int e = 0; e < 16; ++e) {
+            o[e] *= inv;
+            not_finite = fmaf(o[e], 0.f, not_finite);
           }
           if (!valid) continue;
           if (cut) {
-            float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + (int64_t)(c / 4) * a.rows_cap + rho;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) to[(int64_t)(e / 4) * a.rows_cap] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; e += 4, to += a.rows_cap) *to = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           } else {
-            write_out<D, 32>(a, token, head, c, o);
+            if (l == 0.f) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = 0.f;
+            }
+            write_out<D, 16>(a, token, head, c, o);
           }
         }
+        const bool bad = not_finite != 0.f && l != 0.f;
         if (valid && cut) a.part_ml[slot + rho] = make_float2(m, l);
         if (valid && !cut) write_lse(a, token, head, m, l);
         if (!cut) {
@@ -1173,18 +1224,34 @@ __global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_c
 // Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and eight columns of them, a
 // row to a lane, eight parts in flight.
 constexpr int kAfThreads = 256;
-constexpr int kAfSplit = 8;  // CTAs to a unit
+constexpr int kAfCtas = 4;  // CTAs to an SM
 template <int D>
 __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_constant__ AtArgs a) {
   constexpr int E = 8, N = 8;
   pdl_wait();
   pdl_trigger();
-  const AtCut cut = a.cut[blockIdx.x / kAfSplit];
-  if (cut.parts < 2) return;
-  const int lane = threadIdx.x & 31;
-  const int rows = cut.ntok * a.group, blocks = (rows + 31) / 32;
-  for (int item = (blockIdx.x % kAfSplit) * (kAfThreads / 32) + (threadIdx.x >> 5); item < blocks * (D / E);
-       item += kAfSplit * (kAfThreads / 32)) {
+  // the cut units' items, a unit to a thread; ends[c]: those up to the unit that begins in CTA c
+  __shared__ int ends[kAfThreads], sums[kAfThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const AtCut* mine = a.cut + tid;
+  int incl = tid < a.ctas && mine->parts > 1 ? (mine->ntok * a.group + 31) / 32 * (D / E) : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) sums[tid >> 5] = incl;
+  __syncthreads();
+  for (int w = 0; w < (tid >> 5); ++w) incl += sums[w];
+  ends[tid] = incl;
+  __syncthreads();
+  for (int all = ends[kAfThreads - 1], i = blockIdx.x + gridDim.x * (tid >> 5); i < all; i += gridDim.x * (kAfThreads / 32)) {
+    int unit = 0;  // the first whose end is past i
+#pragma unroll
+    for (int step = kAfThreads / 2; step > 0; step >>= 1)
+      if (ends[unit + step - 1] <= i) unit += step;
+    const AtCut cut = a.cut[unit];
+    const int item = i - (unit ? ends[unit - 1] : 0), rows = cut.ntok * a.group;
     const int col = item % (D / E) * E, rho = min(item / (D / E) * 32 + lane, rows - 1);
     const bool valid = item / (D / E) * 32 + lane < rows;
     float m = -FLT_MAX, l = 0.f, o[E];
@@ -1233,7 +1300,7 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
     if (valid && col == 0) write_lse(a, token, head, m, l);
     uint32_t wrong = __ballot_sync(0xffffffffu, valid && bad && finite(l));
     if (!wrong) continue;
-    const AtUnit u = unit_of(a, seqs_of(a), find_seq(a, seqs_of(a), cut.slot), cut.slot);
+    const AtUnit u = unit_of(a, seqs_of(a), find_seq(a, seqs_of(a), cut.slot), cut.slot, a.range);
     int lo, hi;
     token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
     while (wrong) {
@@ -1324,7 +1391,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  return launch_pdl(attend_finish_kernel<D>, dim3(pl.grid * kAfSplit), dim3(kAfThreads), 0, s, a) == cudaSuccess
+  return launch_pdl(attend_finish_kernel<D>, dim3(pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
              ? AIRCACHE_OK
              : AIRCACHE_ERR_CUDA;
 }
@@ -1369,7 +1436,7 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
   if (pl.g > kAtGroup) return AIRCACHE_ERR_UNSUPPORTED;
   pl.tok_tile = kAtRows / pl.g;
   pl.slots = (int)(p->num_tokens / (2 * pl.tok_tile)) + p->pages->num_seqs;
-  pl.grid = device_sms();
+  pl.grid = std::min(device_sms(), kAfThreads);
   pl.rows_cap = (int)std::min<int64_t>(2 * pl.tok_tile, std::max<int64_t>(p->num_tokens, 1)) * pl.g;
   pl.cut_off = kAtHeader;
   pl.range_off = pl.cut_off + up256(sizeof(AtCut) * (size_t)pl.grid);
@@ -1405,7 +1472,8 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.tok_tile = pl.tok_tile;
   a.h_q = p->h_q;
   a.causal = p->causal;
-  a.ranged = pl.slots > kAtRanged;
+  a.ranged = pl.slots > 32;
+  a.ctas = pl.grid;
   a.rows_cap = pl.rows_cap;
   a.box = box_rows(pl.pages.page_rows);
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
