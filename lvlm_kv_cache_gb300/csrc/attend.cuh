@@ -31,6 +31,9 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
 int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AttendPart& part, uint8_t* ws,
                   int32_t* error, cudaStream_t s);
 
+// griddepcontrol.wait where a kernel has already begun to work: the kernel before has completed.
+__device__ __forceinline__ void prior_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
 // A result over other rows that a decode step joins with its own: fp32 outputs [S][h_q][head_dim] and log-sum-exps in
 // base 2 [S][h_q], of the first *num sequences (out == nullptr: of none).
 struct DecodePrior {

@@ -1224,12 +1224,14 @@ __global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_c
 // Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and eight columns of them, a
 // row to a lane, eight parts in flight.
 constexpr int kAfThreads = 256;
-constexpr int kAfCtas = 4;  // CTAs to an SM
+constexpr int kAfCtas = 4;  // CTAs to an SM (one, where the next kernel is to start beside them)
 template <int D>
 __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_constant__ AtArgs a) {
   constexpr int E = 8, N = 8;
+  // (results that are a part of another call's: its next kernel is the call's own, and waits for them where it needs them)
+  if (a.part.out) pdl_trigger();
   pdl_wait();
-  pdl_trigger();
+  if (!a.part.out) pdl_trigger();
   // the cut units' items, a unit to a thread; ends[c]: those up to the unit that begins in CTA c
   __shared__ int ends[kAfThreads], sums[kAfThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1391,7 +1393,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  return launch_pdl(attend_finish_kernel<D>, dim3(pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
+  return launch_pdl(attend_finish_kernel<D>, dim3(a.part.out ? pl.grid : pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
              ? AIRCACHE_OK
              : AIRCACHE_ERR_CUDA;
 }

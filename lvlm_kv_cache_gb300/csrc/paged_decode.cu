@@ -144,6 +144,7 @@ __device__ __forceinline__ int rows_of(const Pages& p, int s) {
 
 // `head` of the batch's S * h_q.  Without a prior result there is nothing to form (own = 1).
 __device__ __forceinline__ Joint joint(const PdArgs& a, int64_t head, float m, float l) {
+  prior_wait();
   Joint j = {1.f, 0.f, l == 0.f ? -INFINITY : m + log2f(l)};
   if (head < (int64_t)*a.prior.num * a.h_q) {
     const float p = a.prior.lse2[head];
@@ -398,8 +399,12 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
   }
-  pdl_wait();
-  pdl_trigger();
+  // With a prior result the kernel before is the one that makes it, and writes nothing else that is read here: the rows
+  // are read while it runs, and what joins waits for it (prior_wait), as the kernel's end does.  The kernel behind may
+  // start early only if it is this call's own, the join of the list's parts
+  const bool late = a.prior.out != nullptr;
+  if (!late) pdl_wait();
+  if (!late || !SHORT) pdl_trigger();
   const Share sh = SHORT ? make_unit(a, share) : make_share(a, share);  // (its barriers publish the mbarriers too)
   if (!SHORT && blockIdx.x == 0 && tid == 0) *a.tiles = max(sh.tiles, 0);
   Run r = sh.run;
@@ -487,6 +492,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       cluster_sync_all();
       cluster_sync_all();
     }
+    if (late) prior_wait();
     return;
   }
 
@@ -905,6 +911,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         }
       }
       cluster_sync_all();  // shared memory stays readable until every rank is done
+      if (late) prior_wait();
       return;
     }
     if (tid == 0 && r.first == 0) {
@@ -939,6 +946,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
       }
     }
   }
+  if (late) prior_wait();
 }
 
 // The parts j0, j0 + step, .. of one unit, head hh and four columns, N of them in flight.
