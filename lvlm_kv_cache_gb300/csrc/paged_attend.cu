@@ -66,13 +66,16 @@ struct AtCfg {
   static constexpr int kTile = kSlab * (D / 64);
   static constexpr int kStages = (Q8 ? 3 : 5) * 128 / D;       // tiles of the ring
   static constexpr int kCodeTile = kAtKeys * D;                // int8 rows: tiles of codes before them,
-  static constexpr int kCodeStages = Q8 ? (D == 128 ? 3 : 8) : 0;
-  static constexpr int kScaleStages = Q8 ? 4 : 0;              // and the scales of a key tile's keys and values
+  static constexpr int kCodeStages = Q8 ? (D == 128 ? 3 : 5) : 0;
+  static constexpr int kScaleStages = Q8 ? 4 : 0;              // and the scales of a tile's keys and values: as they
+                                                               // come, then as the softmax takes them
+  // (a tile's values are widened before its stage of scales can be another's: five entries or more lie between)
+  static_assert(kCodeStages <= 5);
   static constexpr int kOffQ = 0;                              // two query tiles
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffCodes = kOffRing + kStages * kTile;
   static constexpr int kOffScales = kOffCodes + kCodeStages * kCodeTile;
-  static constexpr int kOffCtl = kOffScales + kScaleStages * 2 * kAtKeys * 4;
+  static constexpr int kOffCtl = kOffScales + kScaleStages * 4 * kAtKeys * 4;
 };
 
 // A unit whose parts are to be joined (parts < 2: none): of CTAs c0 .. c0 + parts - 1.
@@ -320,7 +323,6 @@ struct AtCtl {
   uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scready[kScales], scempty[kScales];
   uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done;
   uint32_t tmem;
-  uint8_t vbad[kScales][kAtKeys];  // int8 values whose scale is not finite
   float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
   AtScratch scratch;
   AtRun run[C::kThreads / 32];  // each warp's place: read seldom, not worth registers
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           const bool mine = lane < boxes && page >= 0;
           const bool scale = !val && lane < 2 * boxes && page >= 0, there = scale && page < p.num_pages;
           const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine)), scales = __popc(__ballot_sync(0xffffffffu, there));
-          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 2 + lane / boxes) * kAtKeys + lane % boxes * a.box;
+          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 4 + lane / boxes) * kAtKeys + lane % boxes * a.box;
           if (scale && !there)  // (of a page out of bounds)
             for (int e = 0; e < a.box; ++e) to[e] = 0.f;
           __syncwarp();
@@ -863,10 +865,10 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     (void)mbar_wait_warp(&ctl->done, 0);
   } else if (Q8 && warp >= kAtWiden) {
     // ---- int8 codes become bf16 tiles, half a row to a thread; value rows behind the sequence's last are zeros
-    uint32_t n = 0;
+    uint32_t n = 0, tiles = 0;
     bool ok = true;
-    const int row = (tid - kAtWiden * 32) & 127, half = (tid - kAtWiden * 32) >> 7;
-    uint32_t tiles = 0;
+    const int row = (tid - kAtWiden * 32) & 127;
+    const int half = (tid - kAtWiden * 32) >> 7;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
       if (r.count == 0) continue;
       const bool nar = narrow(a, r.u);
@@ -874,32 +876,30 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         int j;
         const bool val = entry_of(nar, r.count, pos, j);
         const uint32_t cs = n % (Q8 ? C::kCodeStages : 1), st = n % C::kStages;
-        ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
-        if (ok && n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
-        if (!ok) break;
         const uint32_t sc = (tiles + j) % (Q8 ? C::kScaleStages : 1);
         const bool behind = (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
+        float* scales = reinterpret_cast<float*>(sm + C::kOffScales) + sc * 4 * kAtKeys + row;
         if (!val) {
-          // a key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
+          // A key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
           // weight of 0 makes of that is mended as bf16 rows' is
           ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles + j) / (Q8 ? C::kScaleStages : 1)) & 1, kAtLong);
           if (!ok) break;
-          float* scale = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 2 + half) * kAtKeys + row;
-          if (half == 0) {
-            *scale *= a.scale_log2;
-          } else {
-            const float x = behind ? 0.f : *scale;
-            *scale = finite(x) ? x : 1.f;
-            ctl->vbad[sc][row] = !finite(x);
-          }
+          const float x = scales[half * kAtKeys];
+          scales[(2 + half) * kAtKeys] = half == 0 ? x * a.scale_log2 : behind ? 0.f : finite(x) ? x : 1.f;
         }
+        const bool zero = val && behind, bad = val && !behind && !finite(scales[kAtKeys]);
+        ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
+        if (!ok) break;
         const uint8_t* from = sm + C::kOffCodes + cs * C::kCodeTile;
         uint8_t* to = sm + C::kOffRing + st * C::kTile + row * 128;
-        const bool zero = val && behind, bad = val && ctl->vbad[sc][row];
         uint4 x[D / 32];
 #pragma unroll
         for (int q = 0; q < D / 32; ++q)
           x[q] = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * (half * (D / 32) + q)));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->cempty[cs]);
+        if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
+        if (!ok) break;
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
           const int c = half * (D / 32) + q;
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           uint4 hi = make_uint4(widen2_bf16(x[q].z, 0x4140u), widen2_bf16(x[q].z, 0x4342u), widen2_bf16(x[q].w, 0x4140u),
                                 widen2_bf16(x[q].w, 0x4342u));
           if (zero || bad) {
-            const uint32_t u = bad ? 0x7fc07fc0u : 0u;
+            const uint32_t u = zero ? 0u : 0x7fc07fc0u;
             lo = hi = make_uint4(u, u, u, u);
           }
           uint8_t* slab = to + (c >> 2) * C::kSlab;
@@ -920,7 +920,6 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         if (lane == 0) {
           if (!val) mbar_arrive(&ctl->scready[sc]);
           mbar_arrive(&ctl->full[st]);
-          mbar_arrive(&ctl->cempty[cs]);
         }
       }
       tiles += r.count;
@@ -976,7 +975,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           const bool masked = !__all_sync(0xffffffffu, lo <= k0 && hi - k0 >= kAtKeys);
           const int from = lo - k0;
           const uint32_t wide = (uint32_t)(hi - lo);
-          const float* ks = reinterpret_cast<const float*>(sm + C::kOffScales) + sc * 2 * kAtKeys;
+          const float* ks = reinterpret_cast<const float*>(sm + C::kOffScales) + (sc * 4 + 2) * kAtKeys;
           // moves the reference to a maximum that passes it by more than the slack
           auto refer = [&](float top) {
             const float mx = Q8 ? top : top * a.scale_log2;
