@@ -60,7 +60,7 @@ template <int D, bool Q8>
 struct AtCfg {
   static constexpr int kThreads = Q8 ? 640 : 384;
   // registers of a thread: what the other warps give, the softmax warps, which hold a row of 128 logits, take
-  static constexpr int kRegs = Q8 ? 96 : 168, kRegsSoft = Q8 ? 144 : 200, kRegsOther = Q8 ? 64 : 104;
+  static constexpr int kRegs = Q8 ? 96 : 168, kRegsSoft = Q8 ? 144 : 208, kRegsOther = Q8 ? 64 : 88;
   static_assert(256 * kRegsSoft + (kThreads - 256) * kRegsOther <= kThreads * kRegs, "within the launch's own");
   static constexpr int kSlab = kAtKeys * 128;       // [128 rows][64 bf16]
   static constexpr int kTile = kSlab * (D / 64);
@@ -85,6 +85,13 @@ struct alignas(16) AtCut {
   int slot, pad;
 };
 
+// x / d for x < 2^31 and 1 <= d <= 256: M = ceil(2^40 / d) is off by less than d / 2^40 of 1 / d, and x d < 2^39.
+struct AtDivisor {
+  uint64_t m;
+  __host__ __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> 40); }
+};
+inline AtDivisor divisor(int d) { return {((1ull << 40) + d - 1) / d}; }
+
 struct AtArgs {
   Pages pages;
   const int32_t* cu;
@@ -102,8 +109,11 @@ struct AtArgs {
   float2* part_ml;  // [2 CTAs][rows_cap]
   float* part_o;    // [2 CTAs][rows_cap][D]
   int64_t num_tokens;
-  int slots, group, tok_tile, h_q, causal, ranged, rows_cap, box, ctas;  // ranged: a kernel has filled `range`; otherwise
-                                                                   // every CTA does, with the same
+  AtDivisor by_unit, by_page, by_group;  // by 2 tok_tile, page_rows / 16, group
+  int slots, group, tok_tile, h_q, causal, rows_cap, ctas;
+  int box_shift;  // boxes of 2^box_shift rows
+  int ranged;     // a kernel has filled `range`; otherwise every CTA does, with the same
+  int few;        // every CTA's warps place the batch by themselves: at most 32 units to a KV head, fewer than 2^31 places
   float scale_log2;
 };
 
@@ -196,7 +206,7 @@ struct AtSeqs {
 };
 __device__ __forceinline__ AtSeqs seqs_of(const AtArgs& a) { return {a.cu, a.pages.lens}; }
 __device__ __forceinline__ int slot_base(const AtArgs& a, int c0, int s) {
-  return min(max(c0, 0), (int)a.num_tokens) / (2 * a.tok_tile) + s;
+  return a.by_unit.quotient(min(max(c0, 0), (int)a.num_tokens)) + s;
 }
 __device__ __forceinline__ int find_seq(const AtArgs& a, const AtSeqs& q, int slot) {
   int lo = 0, hi = a.pages.num_seqs - 1;
@@ -331,7 +341,7 @@ struct AtCtl {
 __device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
   return ((x | y) >> 32) == 0 ? (uint32_t)x / (uint32_t)y : x / y;
 }
-// At most 32 slots: every warp finds the CTA's place by itself, a slot to a lane.  Lane s has the offsets c0, c1 of sequence
+// Few units: every warp finds the CTA's place by itself, a slot to a lane.  Lane s has the offsets c0, c1 of sequence
 // s and its length.
 __device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, int len, AtScratch* sc, AtRun& r) {
   const int lane = threadIdx.x & 31;
@@ -346,23 +356,23 @@ __device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, 
   AtUnit u;
   u.ntok = 0;
   if (lane < a.slots) u = make_unit(a, s, lane, u0, u1, ul, a.range);
-  const uint64_t wide = u.c + kAtEnd, mine = u.ntok ? wide * a.pages.h_kv : 0;
-  uint64_t incl = mine;
+  const uint32_t wide = u.c + kAtEnd, mine = u.ntok ? wide * a.pages.h_kv : 0;
+  uint32_t incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += x;
   }
-  const uint64_t total = __shfl_sync(0xffffffffu, incl, 31);
-  const uint64_t per = max((uint64_t)1, quotient(total + gridDim.x - 1, gridDim.x));
-  const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
+  const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
+  const uint32_t per = max(2u, (total + gridDim.x - 1) / gridDim.x);  // (a narrow unit's streams take a tile each)
+  const uint32_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
   if (threadIdx.x == 0) sc->per = per;
   if (lo < hi && lo >= incl - mine && lo < incl) {
     AtRun x;
     x.lo = lo;
     x.hi = hi;
     x.slot = lane;
-    x.h = (int)quotient(lo - (incl - mine), wide);
+    x.h = (int)((lo - (incl - mine)) / wide);
     x.at = incl - mine + x.h * wide;
     x.u = u;
     clip(x);
@@ -402,7 +412,7 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
     if (w < warp) before += sc->sum[w];
     total += sc->sum[w];
   }
-  const uint64_t per = max((uint64_t)1, quotient(total + gridDim.x - 1, gridDim.x));
+  const uint64_t per = max((uint64_t)2, quotient(total + gridDim.x - 1, gridDim.x));
   const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
   if (tid == 0) sc->per = per;
   if (lo < hi && lo >= before && lo < before + mine) {
@@ -589,7 +599,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     return c0 < 0 || c1 < c0 || c1 > a.num_tokens || len < 0 || len > p.max_rows || (a.causal && len < c1 - c0);
   };
   tc_fence_before();
-  if (a.slots <= 32) {
+  if (a.few) {
     const bool in = lane < p.num_seqs;
     const int c0 = in ? a.cu[lane] : 0, c1 = in ? a.cu[lane + 1] : 0, len = in ? p.lens[lane] : 0;
     if (blockIdx.x == 0 && warp == 0 && in && wrong(c0, c1, len)) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
@@ -624,36 +634,48 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOther));
   if (warp == kAtLoad) {
     // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
-    // and the odd chunks: the next chunk's are looked up while this one is copied
-    const int boxes = kAtKeys / a.box, per_chunk = 32 / boxes;  // boxes of a tile, tiles of a chunk
+    // and the odd chunks: the next chunk's are looked up while this one is copied.  The copies are issued in turn by one
+    // lane (issued by a lane each they took four times as long, as their operands are the warp's)
+    const int box_shift = a.box_shift, box = 1 << box_shift;
+    const int boxes_shift = 7 - box_shift, per_shift = 5 - boxes_shift;  // boxes of a tile, tiles of a chunk
+    static_assert(kAtKeys == 128);
+    const bool one = elect_one();
     uint32_t n = 0, tiles = 0;  // entries and key tiles so far
     bool ok = true;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
-      if (r.count == 0) continue;
+      const int count = r.count;
+      if (count == 0) continue;
       const bool nar = narrow(a, r.u);
       const int32_t* table = p.table + (int64_t)r.u.s * p.table_stride;
-      const int tile0 = r.u.t0 + r.first;
-      auto look = [&](int chunk) {
-        const int64_t row = ((int64_t)tile0 + (int64_t)chunk * per_chunk) * kAtKeys + (int64_t)lane * a.box;
-        if (row >= r.u.rows || row >= (int64_t)(tile0 + r.count) * kAtKeys) return -1;
-        const int page = table[(int)row / p.page_rows];
-        if (page_ok(p, page)) return page;
-        set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
-        return (int)p.num_pages;  // (behind the tensor: its rows arrive as zeros)
+      const int tile0 = r.u.t0 + r.first, rows = r.u.rows, h = r.h;
+      struct Place {
+        int page, row;  // of a box; -1: none
       };
-      int even = look(0), odd = look(1);
-      for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
+      auto look = [&](int chunk) -> Place {
+        const int64_t row = ((int64_t)tile0 + ((int64_t)chunk << per_shift)) * kAtKeys + ((int64_t)lane << box_shift);
+        if (row >= rows || row >= (int64_t)(tile0 + count) * kAtKeys) return {-1, 0};
+        const int at = a.by_page.quotient((int)row >> 4);
+        const int page = table[at];
+        if (page_ok(p, page)) return {page, (int)row - at * p.page_rows};
+        set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+        return {(int)p.num_pages, 0};  // (behind the tensor: its rows arrive as zeros)
+      };
+      Place even = look(0), odd = look(1);
+      for (int pos = 0; pos < 2 * count; ++pos, ++n) {
         int j;  // the key tile within the run
-        const bool val = entry_of(nar, r.count, pos, j);
-        const int chunk = j / per_chunk, in_chunk = j - chunk * per_chunk;
+        const bool val = entry_of(nar, count, pos, j);
+        const int chunk = j >> per_shift, in_chunk = j - (chunk << per_shift);
         if (val && in_chunk == 0 && chunk > 0) {  // keys are at most two tiles ahead of values, a chunk four or more
           if (chunk & 1)
             even = look(chunk + 1);
           else
             odd = look(chunk + 1);
         }
-        const int row0 = (tile0 + j) * kAtKeys;
-        const int pages = chunk & 1 ? odd : even;
+        const int left = rows - (tile0 + j) * kAtKeys;                     // rows from the tile's first on
+        const int boxes = (min(left, kAtKeys) + box - 1) >> box_shift;     // that hold any
+        const Place mine = chunk & 1 ? odd : even;
+        const int lane0 = in_chunk << boxes_shift;
+        const CUtensorMap* map = val ? &vmap : &kmap;
         if constexpr (Q8) {
           // codes to their own ring, from where they are widened into the tiles' one; with a tile's keys its scales
           const uint32_t st = n % C::kCodeStages;
@@ -661,48 +683,49 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           const uint32_t sc = (tiles + j) % C::kScaleStages, turn = (tiles + j) / C::kScaleStages;
           if (ok && !val && turn > 0) ok = mbar_wait_warp(&ctl->scempty[sc], (turn + 1) & 1, kAtLong);
           if (!ok) break;
-          const int page = __shfl_sync(0xffffffffu, pages, (in_chunk * boxes + lane % boxes) & 31);
-          const int at = (row0 + lane % boxes * a.box) % p.page_rows;
-          const bool mine = lane < boxes && page >= 0;
-          const bool scale = !val && lane < 2 * boxes && page >= 0, there = scale && page < p.num_pages;
-          const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine)), scales = __popc(__ballot_sync(0xffffffffu, there));
-          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 4 + lane / boxes) * kAtKeys + lane % boxes * a.box;
+          // a lane to each box of codes, and of the keys' and of the values' scales
+          const int b = lane & ((1 << boxes_shift) - 1);
+          const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b), row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
+          const bool codes = lane < (1 << boxes_shift) && b < boxes;
+          const bool scale = !val && lane < (2 << boxes_shift) && b < boxes, there = scale && page < p.num_pages;
+          const uint32_t scales = __popc(__ballot_sync(0xffffffffu, there));
+          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 4 + (lane >> boxes_shift)) * kAtKeys + (b << box_shift);
           if (scale && !there)  // (of a page out of bounds)
-            for (int e = 0; e < a.box; ++e) to[e] = 0.f;
+            for (int e = 0; e < box; ++e) to[e] = 0.f;
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl->cfull[st], count * (uint32_t)(a.box * D));
-            if (!val) mbar_arrive_expect_tx(&ctl->scfull[sc], scales * (uint32_t)(a.box * 4));
+          if (one) {
+            mbar_arrive_expect_tx(&ctl->cfull[st], (uint32_t)((boxes << box_shift) * D));
+            if (!val) mbar_arrive_expect_tx(&ctl->scfull[sc], scales << (box_shift + 2));
           }
           __syncwarp();
           fence_proxy_async_smem();
-          if (mine)
-            tma_load_4d(base + C::kOffCodes + st * C::kCodeTile + lane * a.box * D, val ? &vmap : &kmap, 0, at, r.h, page,
-                        &ctl->cfull[st]);
+          if (codes)
+            tma_load_4d(base + C::kOffCodes + st * C::kCodeTile + ((b * D) << box_shift), map, 0, row, h, page, &ctl->cfull[st]);
           if (there)
-            bulk_g2s(to, (lane < boxes ? p.k_scale : p.v_scale) + page_slot(p, page, r.h, at), a.box * 4, &ctl->scfull[sc]);
+            bulk_g2s(to, (codes ? p.k_scale : p.v_scale) + page_slot(p, page, h, row), 4 << box_shift, &ctl->scfull[sc]);
         } else {
           const uint32_t st = n % C::kStages;
           if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
           if (!ok) break;
-          const int slabs = D / 64;
-          const int box = lane / slabs, slab = lane % slabs;
-          const int page = __shfl_sync(0xffffffffu, pages, (in_chunk * boxes + box) & 31);
-          const bool mine = lane < boxes * slabs && page >= 0;
-          const uint32_t count = __popc(__ballot_sync(0xffffffffu, mine));
           // values behind the last row are cleared by another warp, which then says that the tile is there
-          const bool tail = val && (int64_t)row0 + kAtKeys > r.u.rows;
-          uint64_t* bar = tail ? &ctl->tail[st] : &ctl->full[st];
-          if (lane == 0) mbar_arrive_expect_tx(bar, count * (uint32_t)(a.box * 128));
-          __syncwarp();
-          if (mine) {
+          uint64_t* bar = val && left < kAtKeys ? &ctl->tail[st] : &ctl->full[st];
+          if (one) {
+            mbar_arrive_expect_tx(bar, (uint32_t)((boxes << box_shift) * 2 * D));
             fence_proxy_async_smem();
-            tma_load_5d(base + C::kOffRing + st * C::kTile + slab * C::kSlab + box * a.box * 128, val ? &vmap : &kmap, 0,
-                        (row0 + box * a.box) % p.page_rows, slab, r.h, page, bar);
           }
+          const uint32_t dst = base + C::kOffRing + st * C::kTile;
+          for (int b = 0; b < boxes; ++b) {
+            const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b), row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
+            if (one) {
+#pragma unroll
+              for (int slab = 0; slab < D / 64; ++slab)
+                tma_load_5d(dst + slab * C::kSlab + ((b * 128) << box_shift), map, 0, row, slab, h, page, bar);
+            }
+          }
+          __syncwarp();
         }
       }
-      tiles += r.count;
+      tiles += count;
     }
     if (!ok) {
       // the copies in flight land before the CTA's shared memory is another's
@@ -933,7 +956,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = tl + kAtS + 128 * i, tp = ts;  // logits; the weights over them
     if (tid == 0) a.cut[blockIdx.x].parts = 0;  // (until a run says otherwise)
-    const int tok = row / a.group, hh = row - tok * a.group;
+    const int tok = a.by_group.quotient(row), hh = row - tok * a.group;
     uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
     bool ok = true;
     for (bool more = any; more && ok; more = next_unit(a, r)) {
@@ -979,7 +1002,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           // moves the reference to a maximum that passes it by more than the slack
           auto refer = [&](float top) {
             const float mx = Q8 ? top : top * a.scale_log2;
-            if (__any_sync(0xffffffffu, mx > m + kAtSlack)) {
+            if (__any_sync(0xffffffffu, valid && mx > m + kAtSlack)) {  // (what lies in rows without a query has no say)
               const float to = fmaxf(m, mx), f = fast_exp2(m - to);
               m = to;
               sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
@@ -1143,7 +1166,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         const int rho = my_tok * a.group + hh;
         const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
         float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + rho;
-        float not_finite = 0.f;  // (0 times what is not finite is NaN)
+        float not_finite[4] = {0.f, 0.f, 0.f, 0.f};  // (0 times what is not finite is NaN)
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float o[16];
@@ -1159,7 +1182,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             o[e] *= inv;
-            not_finite = fmaf(o[e], 0.f, not_finite);
+            not_finite[e & 3] = fmaf(o[e], 0.f, not_finite[e & 3]);
           }
           if (!valid) continue;
           if (cut) {
@@ -1173,7 +1196,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             write_out<D, 16>(a, token, head, c, o);
           }
         }
-        const bool bad = not_finite != 0.f && l != 0.f;
+        const bool bad = (not_finite[0] + not_finite[1]) + (not_finite[2] + not_finite[3]) != 0.f && l != 0.f;
         if (valid && cut) a.part_ml[slot + rho] = make_float2(m, l);
         if (valid && !cut) write_lse(a, token, head, m, l);
         if (!cut) {
@@ -1473,10 +1496,16 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.tok_tile = pl.tok_tile;
   a.h_q = p->h_q;
   a.causal = p->causal;
-  a.ranged = pl.slots > 32;
+  // (places: tiles of a unit and its end, for each of 32 slots and every KV head)
+  a.few = pl.slots <= 32 && (int64_t)32 * pl.pages.h_kv * (pl.pages.max_rows / kAtKeys + 1 + kAtEnd) < (1ll << 31);
+  a.ranged = !a.few;
+  a.by_unit = divisor(2 * pl.tok_tile);
+  a.by_page = divisor(pl.pages.page_rows / 16);
+  a.by_group = divisor(pl.g);
   a.ctas = pl.grid;
   a.rows_cap = pl.rows_cap;
-  a.box = box_rows(pl.pages.page_rows);
+  a.box_shift = 0;
+  while ((1 << a.box_shift) < box_rows(pl.pages.page_rows)) ++a.box_shift;
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
   if (pl.q8) return pl.d == 128 ? launch_at<128, true>(p, pl, a, s) : launch_at<64, true>(p, pl, a, s);
   return pl.d == 128 ? launch_at<128, false>(p, pl, a, s) : launch_at<64, false>(p, pl, a, s);
