@@ -77,3 +77,42 @@ def test_every_tile_of_the_paged_decode_is_noted():
     gave_up = body(producer, "if (!mbar_wait_warp(&empty")
     assert ".page[lane] = -1;" in gave_up and "while (next_run(" in gave_up
     assert producer.count("break;") == gave_up.count("break;") == 1
+
+
+def test_paged_attention_lets_the_next_kernel_start_behind_its_own_wait():
+    # (its join may let one start before, where that is the same call's: results that are a part of another's)
+    kernels = source("paged_attend.cu").split("__global__")[1:]
+    assert len(kernels) == 3
+    for k in kernels:
+        waits, starts = k.index("pdl_wait();"), [m.start() for m in re.finditer(r"pdl_trigger\(\);", k)]
+        early = [s for s in starts if s < waits]
+        assert starts and max(starts) > waits
+        assert [k[s - 19:s].strip() for s in early] == ["if (a.part.out)"] * len(early)
+    text = source("shared_decode.cu")
+    assert text.index("attend_launch(&pl.at") < text.rindex("paged_decode_run(&p->own, prior")
+
+
+def test_a_decode_that_starts_early_waits_before_it_ends_and_before_it_joins():
+    text = source("paged_decode.cu")
+    kernel = text[text.index("paged_decode_kernel(const"):text.index("struct Joined {")]
+    assert kernel.count("if (late) prior_wait();") == kernel.count("return;") + 1  # at each way out
+    assert body(text, "Joint joint(").strip().startswith("prior_wait();")
+    assert "if (!late) pdl_wait();" in kernel and "if (!late || !SHORT) pdl_trigger();" in kernel
+
+
+def test_waits_of_the_paged_attention_end_for_whole_warps():
+    text = source("paged_attend.cu")
+    assert "mbar_wait(" not in text and "named_bar_sync" not in text and "bar.sync" not in text
+    # each wait's answer is looked at, but for those that let copies and products end
+    for line in text.split("\n"):
+        if "mbar_wait_warp(" in line and "(void)" not in line:
+            assert re.search(r"ok = |&& |return |if \(!", line) or "mbar_wait_warp(&ctl->turn" in line, line
+
+
+def test_registers_that_the_paged_attention_shares_out():
+    # what setmaxnreg adds up to may not pass what the launch brings, or it waits for ever: stated in the source, and the
+    # launch compares the built kernel's registers with it
+    text = source("paged_attend.cu")
+    assert "256 * kRegsSoft + (kThreads - 256) * kRegsOther <= kThreads * kRegs" in text
+    assert "if (regs < C::kRegs) return AIRCACHE_ERR_CUDA;" in text
+    assert text.count("setmaxnreg") == 2

@@ -277,6 +277,30 @@ def test_the_same_call_gives_the_same_bits(A):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("h_q,h_kv,new,lens", [(28, 4, [40, 300, 1], [5000, 700, 1]), (9, 1, [3, 17], [6000, 130]),
+                                               (8, 8, [70, 129], [2000, 3000])])
+def test_what_another_call_left_has_no_say(A, h_q, h_kv, new, lens, int8):
+    # between two runs of a call another one leaves large queries and keys wherever the first has rows without a query
+    # and slots without a row
+    d = 128
+    cache = P.build(A, lens, h_kv, d, 64, seed=22, mass=False, order=False, int8=int8)
+    q = queries(sum(new), h_q, d, 22)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]).tolist())
+    prob = A.PagedAttendProblem(q, cache, cu, lse=True, causal=True)
+    ws = prob.new_workspace()
+    other = P.build(A, [20000], h_kv, d, 64, seed=23, mass=False, order=False, int8=int8)
+    loud = [A.PagedAttendProblem(queries(300, h_q, d, 24 + i, scale), other, i32([0, 300]))
+            for i, scale in enumerate((1e-3, 1e2, 1e4))]
+    A.paged_attend(prob, ws)
+    first = P.bits(prob.out), P.bits(prob.lse)
+    for turn in range(6):
+        A.paged_attend(loud[turn % 3])
+        prob.out.zero_()
+        A.paged_attend(prob, ws)
+        assert np.array_equal(first[0], P.bits(prob.out)) and np.array_equal(first[1], P.bits(prob.lse))
+
+
+@pytest.mark.parametrize("int8", [False, True])
 def test_captured_calls_follow_their_inputs(A, int8):
     # one workspace, lengths and queries that change between replays, on another stream than the default
     S, h_q, h_kv, d, page_rows = 4, 14, 2, 128, 16
