@@ -447,7 +447,9 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
 // ------------------------------------------------------------------ results
 
 // E columns from `col` on (of each lane; none where col is D) of one row whose sum is finite and whose values are not:
-// over the rows that it sees, without those that a matrix product multiplies by 0.  By a warp.
+// over the rows that it sees, without those that a matrix product multiplies by 0, and with weights of 1 at most, whose
+// products do not pass fp32's range before they are divided by the sum.  By a warp, kRepair rows in flight.
+constexpr int kRepair = 8;
 template <int D, int E>
 __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t token, int head, int lo, int hi, float m,
                                         float l, int col, float y[E]) {
@@ -455,49 +457,58 @@ __device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t t
   const int lane = threadIdx.x & 31;
   const Pages& p = a.pages;
   const __nv_bfloat16* q = a.q + token * a.q_stride_tok + (int64_t)head * a.q_stride_head + lane * Q;
+  const int32_t* table = p.table + (int64_t)s * p.table_stride;
+  const float lse2 = m + log2f(l);
   float qv[Q];
 #pragma unroll
   for (int e = 0; e < Q; ++e) qv[e] = __bfloat162float(q[e]);
 #pragma unroll
   for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    const int page = p.table[(int64_t)s * p.table_stride + j / p.page_rows];
-    float x = 0.f, v[E];
+  for (int j0 = lo; j0 < hi; j0 += kRepair) {
+    float x[kRepair], v[kRepair][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
-    if (page_ok(p, page)) {
-      const int64_t at = page_elem(p, page, h, j % p.page_rows);
-      if (p.k_scale) {
-        const int64_t slot = page_slot(p, page, h, j % p.page_rows);
-        const int8_t* k = reinterpret_cast<const int8_t*>(p.k) + at + lane * Q;
-        const int8_t* vv = reinterpret_cast<const int8_t*>(p.v) + at;
+    for (int f = 0; f < kRepair; ++f) {
+      const int j = min(j0 + f, hi - 1), at_page = a.by_page.quotient(j >> 4), in_page = j - at_page * p.page_rows;
+      const int page = table[at_page];
+      x[f] = 0.f;
 #pragma unroll
-        for (int e = 0; e < Q; ++e) x = fmaf(qv[e], (float)k[e], x);
-        x *= p.k_scale[slot];
+      for (int e = 0; e < E; ++e) v[f][e] = 0.f;
+      if (page_ok(p, page)) {
+        const int64_t at = page_elem(p, page, h, in_page);
+        if (p.k_scale) {
+          const int64_t slot = page_slot(p, page, h, in_page);
+          const int8_t* k = reinterpret_cast<const int8_t*>(p.k) + at + lane * Q;
+          const int8_t* vv = reinterpret_cast<const int8_t*>(p.v) + at;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (col + e < D) v[e] = (float)vv[col + e] * p.v_scale[slot];
-      } else {
-        const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
-        const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
+          for (int e = 0; e < Q; ++e) x[f] = fmaf(qv[e], (float)k[e], x[f]);
+          x[f] *= p.k_scale[slot];
 #pragma unroll
-        for (int e = 0; e < Q; ++e) x = fmaf(qv[e], __bfloat162float(k[e]), x);
+          for (int e = 0; e < E; ++e)
+            if (col + e < D) v[f][e] = (float)vv[col + e] * p.v_scale[slot];
+        } else {
+          const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
+          const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (col + e < D) v[e] = __bfloat162float(vv[col + e]);
+          for (int e = 0; e < Q; ++e) x[f] = fmaf(qv[e], __bfloat162float(k[e]), x[f]);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (col + e < D) v[f][e] = __bfloat162float(vv[col + e]);
+        }
       }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    const float w = fast_exp2(fmaf(x, a.scale_log2, -m));
+    for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = fmaf(w, v[e], y[e]);
+      for (int f = 0; f < kRepair; ++f) x[f] += __shfl_xor_sync(0xffffffffu, x[f], off);
+#pragma unroll
+    for (int f = 0; f < kRepair; ++f) {
+      if (j0 + f >= hi) continue;
+      const float w = fast_exp2(fmaf(x[f], a.scale_log2, -lse2));
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = fmaf(w, v[f][e], y[e]);
+    }
   }
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] *= inv;
 }
-
 // A CTA's part of a unit that began before it lies in slot 2 x CTA, of one that begins in it in the next.  A slot holds
 // [D / 4][rows_cap] pieces of four columns, so that a warp's rows are next to one another.
 __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * (int64_t)cta + (begins ? 1 : 0); }

@@ -122,6 +122,36 @@ def test_slots_behind_the_last_row_hold_anything(A, int8):
         case(A, [1, 17, 20, 50], [129, 17, 383, 513], 8, 8, 64, 16, seed=6, int8=int8, fill=float("inf"), causal=causal)
 
 
+def test_many_sequences(A):
+    # more than one CTA stages in shared memory, most of them without tokens
+    g = np.random.default_rng(30)
+    new = np.where(g.random(6000) < 0.1, g.integers(1, 4, 6000), 0)
+    case(A, new.tolist(), (new + g.integers(0, 20, 6000)).tolist(), 2, 1, 64, 16, seed=30, causal=True)
+
+
+def test_pages_of_many_rows(A):
+    for page_rows, int8 in ((4096, False), (2048, True), (112, False), (4080, True)):
+        case(A, [20, 3], [5000, 4097], 4, 2, 128, page_rows, seed=31, causal=True, int8=int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_offsets_past_32_bits(A, int8):
+    # pages so far apart that elements (and, int8, bytes) of the last are past 2^32 from the first
+    d, h, page_rows, n, R = 128, 2, 64, 30, 300
+    small = P.build(A, [R], h, d, page_rows, seed=32, mass=False, order=False, int8=int8)
+    apart, pages_n = 1 << 30, small.num_pages
+    k = torch.empty(apart * (pages_n - 1) + page_rows * h * d, dtype=small.k.dtype, device="cuda")
+    v = torch.empty_like(k)
+    far = [x.as_strided(small.k.shape, (apart, h * d, d, 1)) for x in (k, v)]
+    far[0].copy_(small.k)
+    far[1].copy_(small.v)
+    cache = A.PagedCache(far[0], far[1], small.table, small.lens, k_scale=small.k_scale, v_scale=small.v_scale)
+    q = queries(n, 8, d, 32)
+    prob = A.PagedAttendProblem(q, cache, i32([0, n]), lse=True, causal=True)
+    A.paged_attend(prob)
+    verify(prob.out, prob.lse, q, [0, n], P.host(small), causal=True)
+
+
 @pytest.mark.parametrize("fused,wide", [(True, 0), (False, 3), (True, 1)])
 def test_strides(A, fused, wide):
     for d, int8 in ((128, False), (64, True), (64, False)):
@@ -228,6 +258,23 @@ def test_int8_scales_that_are_not_finite(A):
     assert np.all(np.isnan(got[hit]))
     tol = (HALF + 2.0 ** -12) * spread + HALF * np.abs(want)
     assert np.all(np.abs(got - want)[~hit] <= tol[~hit])
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_values_near_the_end_of_the_range(A, int8):
+    # the unnormalised sum passes fp32's range, the output does not
+    cache = P.build(A, [300, 4000], 2, 128, 32, seed=18, mass=False, order=False, int8=int8)
+    q = queries(40, 14, 128, 18, 0.3)
+    if int8:
+        cache.v.fill_(100)
+        cache.v_scale.fill_(3e36)
+    else:
+        cache.v.fill_(3e38)
+    prob = A.PagedAttendProblem(q, cache, i32([0, 20, 40]), causal=True)
+    A.paged_attend(prob)
+    got = prob.out.double()
+    want = 3e38 if int8 else float(torch.tensor(3e38, dtype=torch.bfloat16))
+    assert float((got / want - 1).abs().max()) <= 3 * HALF  # (weights and their sum, and the output)
 
 
 def test_far_apart_logits(A):
