@@ -172,12 +172,12 @@ __device__ __forceinline__ float4 join_prior(const PdArgs& a, const Joint& j, in
   return y;
 }
 // Writes four columns, and with the first of them the log-sum-exp.  f: what makes y the result over the own rows.
-template <int D>
+template <int D, bool PRIOR>
 __device__ __forceinline__ void write_columns(const PdArgs& a, int64_t head, int d, float4 y, float f, float m, float l,
                                               bool lse2 = false) {
   y.x *= f, y.y *= f, y.z *= f, y.w *= f;
   float top = 0.f;
-  if (a.prior.out) {
+  if (PRIOR) {
     const Joint j = joint(a, head, m, l);
     y = join_prior<D>(a, j, head, d, y);
     top = j.lse2;
@@ -190,8 +190,9 @@ __device__ __forceinline__ void write_columns(const PdArgs& a, int64_t head, int
   if (d == 0 && lse2) a.lse2[head] = top == -INFINITY ? INFINITY : top;
 }
 // The log-sum-exp that turns a head's logits into weights (inf: none has one).
+template <bool PRIOR>
 __device__ __forceinline__ float mass_lse2(const PdArgs& a, int64_t head, float m, float l) {
-  const float x = a.prior.out ? joint(a, head, m, l).lse2 : l == 0.f ? -INFINITY : m + log2f(l);
+  const float x = PRIOR ? joint(a, head, m, l).lse2 : l == 0.f ? -INFINITY : m + log2f(l);
   return x == -INFINITY ? INFINITY : x;
 }
 
@@ -367,8 +368,8 @@ __device__ __forceinline__ Share make_unit(const PdArgs& a, ShareScratch* sc) {
   return sh;
 }
 
-// SHORT: a cluster to a unit, and no second kernel.
-template <int D, bool Q8, int HB, bool SHORT>
+// SHORT: a cluster to a unit, and no second kernel.  PRIOR: the results are joined with those over other rows.
+template <int D, bool Q8, int HB, bool SHORT, bool PRIOR>
 __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                                   const __grid_constant__ CUtensorMap vmap,
                                                                   const __grid_constant__ PdArgs a) {
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   // With a prior result the kernel before is the one that makes it, and writes nothing else that is read here: the rows
   // are read while it runs, and what joins waits for it (prior_wait), as the kernel's end does.  The kernel behind may
   // start early only if it is this call's own, the join of the list's parts
-  const bool late = a.prior.out != nullptr;
+  constexpr bool late = PRIOR;
   if (!late) pdl_wait();
   if (!late || !SHORT) pdl_trigger();
   const Share sh = SHORT ? make_unit(a, share) : make_share(a, share);  // (its barriers publish the mbarriers too)
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
   for (int s = blockIdx.x; s < p.num_seqs && sh.tiles >= 0; s += gridDim.x) {
     if (rows_of(p, s) != 0) continue;
     for (int i = tid; i < a.h_q * (D / 4); i += kPdWarps * 32)
-      write_columns<D>(a, (int64_t)s * a.h_q + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
+      write_columns<D, PRIOR>(a, (int64_t)s * a.h_q + i / (D / 4), i % (D / 4) * 4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f, 0.f, 0.f);
     for (int i = tid; i < p.h_kv && !SHORT; i += kPdWarps * 32) a.unit[s * p.h_kv + i] = make_int2(0, 0);
   }
   int st = 0;
@@ -881,14 +882,14 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
           for (int e = 0; e < 4; ++e) y[e] += j < a.ranks ? f * x[j][e] : 0.f;
         }
         const float f = ll == 0.f ? 0.f : kUndo * fast_exp2(nn - mm) / ll;
-        write_columns<D>(a, head0 + hh, d, make_float4(y[0], y[1], y[2], y[3]), f, mm, ll);
+        write_columns<D, PRIOR>(a, head0 + hh, d, make_float4(y[0], y[1], y[2], y[3]), f, mm, ll);
       }
       if (a.mass_out) {
         const int hh = tid - 3 * 32;
         if (hh >= 0 && hh < g) {
           float m[kRanks], l[kRanks], n[kRanks], mm, ll, nn;
           heads(hh, m, l, n, mm, ll, nn);
-          lse2[hh] = mass_lse2(a, head0 + hh, mm, ll);
+          lse2[hh] = mass_lse2<PRIOR>(a, head0 + hh, mm, ll);
         }
         named_bar_sync(1, kPdWarps * 32);  // (and the CTA's logits are written)
         for (int i = tid; i < (int)r.count * kPdRows; i += kPdWarps * 32) {
@@ -926,7 +927,7 @@ __global__ void __launch_bounds__(kPdThreads, PdCfg<D, Q8, HB>::kCtas) paged_dec
         float m, l, n;
         joined(hh, m, l, n);
         const float f = l == 0.f ? 0.f : kUndo * fast_exp2(n - m) / l;
-        write_columns<D>(a, head0 + hh, d,
+        write_columns<D, PRIOR>(a, head0 + hh, d,
                          make_float4(joined_o(hh, d), joined_o(hh, d + 1), joined_o(hh, d + 2), joined_o(hh, d + 3)), f, m,
                          l, a.mass_out != nullptr);
       }
@@ -996,10 +997,10 @@ __device__ __forceinline__ Joined join_parts(const PdArgs& a, int c0, int parts,
   }
   return r;
 }
-template <int D>
+template <int D, bool PRIOR>
 __device__ __forceinline__ void write_joined(const PdArgs& a, const Joined& r, int unit, int hh, int d, float undo) {
   const float f = r.l == 0.f ? 0.f : undo * fast_exp2(r.n - r.m) / r.l;
-  write_columns<D>(a, (int64_t)unit * a.group + hh, d, r.o, f, r.m, r.l);  // (s h_kv + h) g + hh = s h_q + h g + hh
+  write_columns<D, PRIOR>(a, (int64_t)unit * a.group + hh, d, r.o, f, r.m, r.l);  // (s h_kv + h) g + hh = s h_q + h g + hh
 }
 
 // After the attention.  Joins the parts of the units that several CTAs shared.
@@ -1015,7 +1016,7 @@ __device__ __forceinline__ void write_joined(const PdArgs& a, const Joined& r, i
 constexpr int kPfThreads = 256;
 constexpr int kPfMany = 16;
 constexpr int kPfHeads = 16;  // heads of units in many parts that one CTA looks at
-template <int D, bool MASS>
+template <int D, bool MASS, bool PRIOR>
 __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(const __grid_constant__ PdArgs a,
                                                                                 float undo) {
   constexpr int kCols = D / 4, kGroups = kPfThreads / kCols;
@@ -1044,7 +1045,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
   if (cut.y > 1 && cut.y <= kPfMany) {
     for (int c = tid; c < g * kCols; c += kPfThreads) {
       const int hh = c / kCols, d = c % kCols * 4;
-      write_joined<D>(a, join_parts<D, MASS ? 4 : 8>(a, blockIdx.x, cut.y, hh, d, 0, 1), cut.x, hh, d, undo);
+      write_joined<D, PRIOR>(a, join_parts<D, MASS ? 4 : 8>(a, blockIdx.x, cut.y, hh, d, 0, 1), cut.x, hh, d, undo);
     }
   }
   const int col = tid % kCols, grp = tid / kCols;
@@ -1067,7 +1068,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
 #pragma unroll
       for (int q = 0; q < kGroups; ++q)
         all.add(make_float4(part_ml[q].x, part_ml[q].y, part_ml[q].z, 0.f), part_o[q][col]);
-      write_joined<D>(a, all, t.x, hh, 4 * col, undo);
+      write_joined<D, PRIOR>(a, all, t.x, hh, 4 * col, undo);
     }
   }
   if (!MASS) return;
@@ -1112,7 +1113,7 @@ __global__ void __launch_bounds__(kPfThreads, MASS ? 4 : 3) paged_finish_kernel(
         for (int off = width; off < 32; off <<= 1) m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, off));
         l = m == -INFINITY ? 0.f : l * fast_exp2(m - m1);
         for (int off = width; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        lse = mass_lse2(a, (int64_t)u * g + hh, m1, l);
+        lse = mass_lse2<PRIOR>(a, (int64_t)u * g + hh, m1, l);
       }
     }
     float2 sum = make_float2(0.f, 0.f);
@@ -1223,12 +1224,12 @@ bool encode_pages(CUtensorMap* m, const void* base, const PdPlan& pl) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8, int HB>
+template <int D, bool Q8, int HB, bool PRIOR>
 int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   CUtensorMap km, vm;
   if (!encode_pages(&km, pl.pages.k, pl) || !encode_pages(&vm, pl.pages.v, pl)) return AIRCACHE_ERR_UNSUPPORTED;
   constexpr int smem = PdCfg<D, Q8, HB>::kSmem;
-  const auto kernel = pl.ranks > 0 ? &paged_decode_kernel<D, Q8, HB, true> : &paged_decode_kernel<D, Q8, HB, false>;
+  const auto kernel = pl.ranks > 0 ? &paged_decode_kernel<D, Q8, HB, true, PRIOR> : &paged_decode_kernel<D, Q8, HB, false, PRIOR>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.ranks > 0 ? pl.ranks * pl.pages.num_seqs * pl.pages.h_kv : pl.grid);
@@ -1255,7 +1256,7 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(kPfThreads);
   cfg.dynamicSmemBytes = 0;
   const float undo = Q8 ? 1.f / kP16 : 1.f;
-  if (cudaLaunchKernelEx(&cfg, a.mass_out ? paged_finish_kernel<D, true> : paged_finish_kernel<D, false>, a, undo) !=
+  if (cudaLaunchKernelEx(&cfg, a.mass_out ? paged_finish_kernel<D, true, PRIOR> : paged_finish_kernel<D, false, PRIOR>, a, undo) !=
       cudaSuccess)
     return AIRCACHE_ERR_CUDA;
   return AIRCACHE_OK;
@@ -1263,7 +1264,8 @@ int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
 
 template <int D, bool Q8>
 int launch_pd(const PdPlan& pl, const PdArgs& a, cudaStream_t s) {
-  return pl.g <= 8 ? launch_pd<D, Q8, 1>(pl, a, s) : launch_pd<D, Q8, 2>(pl, a, s);
+  if (a.prior.out) return pl.g <= 8 ? launch_pd<D, Q8, 1, true>(pl, a, s) : launch_pd<D, Q8, 2, true>(pl, a, s);
+  return pl.g <= 8 ? launch_pd<D, Q8, 1, false>(pl, a, s) : launch_pd<D, Q8, 2, false>(pl, a, s);
 }
 
 }  // namespace
