@@ -109,7 +109,7 @@ struct AtArgs {
   float2* part_ml;  // [2 CTAs][rows_cap]
   float* part_o;    // [2 CTAs][rows_cap][D]
   int64_t num_tokens;
-  AtDivisor by_unit, by_page, by_group;  // by 2 tok_tile, page_rows / 16, group
+  AtDivisor by_unit, by_page, by_group, by_cta;  // by 2 tok_tile, page_rows / 16, group, ctas
   int slots, group, tok_tile, h_q, causal, rows_cap, ctas;
   int box_shift;  // boxes of 2^box_shift rows
   int ranged;     // a kernel has filled `range`; otherwise every CTA does, with the same
@@ -196,7 +196,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 struct AtUnit {
   int s, tok0, ntok, n;  // sequence, first token of it, tokens, the sequence's tokens
   int rows, t0, c;       // its rows, first key tile, key tiles
-  int64_t token0;        // the batch's token of tok0
+  int token0;            // the batch's token of tok0
 };
 // Units of sequence s start at slot cu[s] / (2 tok_tile) + s: never less than the units before it, so that a slot's
 // sequence is found without a sum over the batch, and at most num_seqs slots are empty.
@@ -238,7 +238,7 @@ __device__ __forceinline__ AtUnit make_unit(const AtArgs& a, int s, int slot, in
   const bool in = first >= 0 && first < u.n;
   u.tok0 = in ? (int)first : 0;
   u.ntok = in ? min(2 * a.tok_tile, u.n - u.tok0) : 0;
-  u.token0 = (int64_t)c0 + u.tok0;
+  u.token0 = in ? c0 + u.tok0 : 0;
   u.t0 = u.c = 0;
   if (in) {
     if (range) {
@@ -272,19 +272,19 @@ __device__ __forceinline__ void find_range(const AtArgs& a, const AtSeqs& q, int
 
 // A CTA's places of the line, and the walk over the units in them.
 struct AtRun {
-  uint64_t hi, lo, at;       // the CTA's places, the unit's first
+  uint64_t at;               // the unit's first place
   int slot, h;
   AtUnit u;
   int first, count;          // the CTA's key tiles of the unit, from u.t0 on
 };
-__device__ __forceinline__ void clip(AtRun& r) {
-  const uint64_t from = max(r.at, r.lo), to = min(r.at + r.u.c, r.hi);
+__device__ __forceinline__ void clip(AtRun& r, uint64_t per) {  // per: places of a CTA
+  const uint64_t lo = per * blockIdx.x, from = max(r.at, lo), to = min(r.at + r.u.c, lo + per);
   r.first = (int)(min(from, r.at + r.u.c) - r.at);
   r.count = to > from ? (int)(to - from) : 0;
 }
-__device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r) {
+__device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r, uint64_t per) {
   r.at += r.u.c + kAtEnd;
-  if (r.at >= r.hi) return false;
+  if (r.at >= per * (blockIdx.x + 1)) return false;
   if (++r.h == a.pages.h_kv) {
     r.h = 0;
     do {
@@ -294,7 +294,7 @@ __device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r) {
       r.u = unit_of(a, seqs_of(a), s, r.slot, a.range);
     } while (r.u.ntok == 0);
   }
-  clip(r);
+  clip(r, per);
   return true;
 }
 // A unit that fits one query tile takes its key tiles alternately with both streams.
@@ -322,7 +322,6 @@ __device__ __forceinline__ bool entry_of(bool nar, int count, int pos, int& j) {
 struct AtScratch {
   uint64_t sum[24];
   AtRun run;
-  uint64_t per;  // places of a CTA
 };
 template <int D, bool Q8>
 struct AtCtl {
@@ -333,8 +332,8 @@ struct AtCtl {
   uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scready[kScales], scempty[kScales];
   uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done;
   uint32_t tmem;
-  float2 ml[kAtRows];  // narrow units: the second stream's reference and sum of each row
-  AtScratch scratch;
+  alignas(16) float2 ml[2][kAtRows];  // narrow units: the streams' references and sums of each row
+  uint64_t per;        // places of a CTA
   AtRun run[C::kThreads / 32];  // each warp's place: read seldom, not worth registers
 };
 // (64-bit division takes many times a 32-bit one's time, and is seldom needed)
@@ -343,7 +342,7 @@ __device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t y) {
 }
 // Few units: every warp finds the CTA's place by itself, a slot to a lane.  Lane s has the offsets c0, c1 of sequence
 // s and its length.
-__device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, int len, AtScratch* sc, AtRun& r) {
+__device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, int len, uint64_t& share, AtRun& r) {
   const int lane = threadIdx.x & 31;
   const int base = lane < a.pages.num_seqs ? slot_base(a, c0, lane) : INT32_MAX;
   int s = 0;  // the last sequence that starts at the lane's slot or before
@@ -364,18 +363,16 @@ __device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, 
     if (lane >= off) incl += x;
   }
   const uint32_t total = __shfl_sync(0xffffffffu, incl, 31);
-  const uint32_t per = max(2u, (total + gridDim.x - 1) / gridDim.x);  // (a narrow unit's streams take a tile each)
+  const uint32_t per = max(2u, (uint32_t)a.by_cta.quotient(total + a.ctas - 1));  // (a narrow unit's streams take a tile each)
   const uint32_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
-  if (threadIdx.x == 0) sc->per = per;
+  if (lane == 0) share = per;  // (every warp the same)
   if (lo < hi && lo >= incl - mine && lo < incl) {
     AtRun x;
-    x.lo = lo;
-    x.hi = hi;
     x.slot = lane;
     x.h = (int)((lo - (incl - mine)) / wide);
     x.at = incl - mine + x.h * wide;
     x.u = u;
-    clip(x);
+    clip(x, per);
     r = x;
   }
   __syncwarp();
@@ -383,7 +380,7 @@ __device__ __forceinline__ bool make_run_small(const AtArgs& a, int c0, int c1, 
 }
 // By all threads of the CTA; false if the CTA has no place.
 template <int THREADS>
-__device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun& r) {
+__device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, uint64_t& share, AtRun& r) {
   static_assert(THREADS <= 768, "warps' sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (a.slots + THREADS - 1) / THREADS;
@@ -414,7 +411,7 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
   }
   const uint64_t per = max((uint64_t)2, quotient(total + gridDim.x - 1, gridDim.x));
   const uint64_t lo = min(per * blockIdx.x, total), hi = min(lo + per, total);
-  if (tid == 0) sc->per = per;
+  if (tid == 0) share = per;
   if (lo < hi && lo >= before && lo < before + mine) {
     uint64_t at = before;
     int s = seq0;
@@ -425,13 +422,11 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
       const uint64_t wide = u.c + kAtEnd;
       if (lo < at + wide * a.pages.h_kv) {
         AtRun x;
-        x.lo = lo;
-        x.hi = hi;
         x.slot = i;
         x.h = (int)quotient(lo - at, wide);
         x.at = at + x.h * wide;
         x.u = u;
-        clip(x);
+        clip(x, per);
         sc->run = x;
         break;
       }
@@ -440,7 +435,7 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, AtRun&
   }
   __syncthreads();
   if (lo < hi) r = sc->run;
-  __syncwarp();
+  __syncthreads();  // (what lies in `sc`'s place may come)
   return lo < hi;
 }
 
@@ -580,8 +575,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     }
     mbar_init(&ctl->qfull, 1);
     mbar_init(&ctl->qempty, 2);
-    mbar_init(&ctl->mlfull, 4);
-    mbar_init(&ctl->mlfree, 4);
+    mbar_init(&ctl->mlfull, 8);
+    mbar_init(&ctl->mlfree, 8);
     mbar_init(&ctl->done, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->sfull[i], 1);
@@ -617,7 +612,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     if (a.range && !a.ranged)
       for (int slot = warp; slot < a.slots; slot += C::kThreads / 32) find_range(a, seqs_of(a), slot);
     __syncthreads();  // (publishes the mbarriers and TMEM too)
-    any = make_run_small(a, c0, c1, len, &ctl->scratch, r);
+    any = make_run_small(a, c0, c1, len, ctl->per, r);
   } else {
     // lengths and token offsets lie where the tiles will until the CTA has found its place: searches go to shared memory
     AtSeqs seqs = seqs_of(a);
@@ -636,7 +631,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       for (int s = tid; s < p.num_seqs; s += C::kThreads) bad |= wrong(seqs.cu[s], seqs.cu[s + 1], seqs.lens[s]);
       if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
     }
-    any = make_run<C::kThreads>(a, seqs, &ctl->scratch, r);  // (its barriers publish the mbarriers and TMEM too)
+    any = make_run<C::kThreads>(a, seqs, reinterpret_cast<AtScratch*>(ctl->ml), ctl->per, r);  // (its barriers publish the mbarriers and TMEM too)
   }
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
@@ -653,7 +648,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     const bool one = elect_one();
     uint32_t n = 0, tiles = 0;  // entries and key tiles so far
     bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r)) {
+    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
       const int count = r.count;
       if (count == 0) continue;
       const bool nar = narrow(a, r.u);
@@ -750,7 +745,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     // ---- queries, and the values behind a sequence's last row
     uint32_t units = 0, tails = 0, n = 0;  // tails: bit st is the parity of tail[st]
     bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r)) {
+    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
       if (r.count == 0) continue;
       const bool nar = narrow(a, r.u);
       if (units > 0) ok = mbar_wait_warp(&ctl->qempty, (units - 1) & 1, kAtLong);
@@ -762,7 +757,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         for (int i = 0; i < streams; ++i)
           for (int sl = 0; sl < D / 64; ++sl)
             tma_load_4d(base + C::kOffQ + i * C::kTile + sl * C::kSlab, &qmap, 0, sl, r.h * a.group,
-                        (int)r.u.token0 + i * a.tok_tile, &ctl->qfull);
+                        r.u.token0 + i * a.tok_tile, &ctl->qfull);
       }
       __syncwarp();
       ++units;
@@ -804,7 +799,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     auto pass = [&] {
       if (one) mbar_arrive(&ctl->turn[1 - i]);
     };
-    for (bool more = any; more && ok; more = next_unit(a, r)) {
+    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
       const int count = __shfl_sync(0xffffffffu, r.count, 0);
       if (count == 0) continue;
       const bool nar = __shfl_sync(0xffffffffu, (int)narrow(a, r.u), 0);
@@ -903,7 +898,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     bool ok = true;
     const int row = (tid - kAtWiden * 32) & 127;
     const int half = (tid - kAtWiden * 32) >> 7;
-    for (bool more = any; more && ok; more = next_unit(a, r)) {
+    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
       if (r.count == 0) continue;
       const bool nar = narrow(a, r.u);
       for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
@@ -970,14 +965,14 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     const int tok = a.by_group.quotient(row), hh = row - tok * a.group;
     uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
     bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r)) {
+    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
       const bool nar = narrow(a, r.u);
       const int my_tok = nar ? tok : tok + i * a.tok_tile;  // of the unit
       const bool valid = tok < a.tok_tile && my_tok < r.u.ntok;
-      const int64_t token = r.u.token0 + my_tok;
+      const int64_t token = (int64_t)r.u.token0 + my_tok;
       const int head = r.h * a.group + hh;
       if (r.count == 0) {
-        if (r.u.c == 0 && r.at >= r.lo && valid && (!nar || i == 0)) {  // nothing to see
+        if (r.u.c == 0 && r.at >= ctl->per * blockIdx.x && valid && (!nar || i == 0)) {  // nothing to see
           const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
           for (int c = 0; c < D; c += 8) write_out<D, 8>(a, token, head, c, zero);
           write_lse(a, token, head, 0.f, 0.f);
@@ -1147,92 +1142,105 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         ++it_o;
         tc_fence_after();
       }
-      // ---- the run's result
-      const bool both = nar && r.count > 1;  // the streams' results are joined, by the first
-      float f0 = 1.f, f1 = 0.f;
-      if (both && i == 1) {
-        ctl->ml[row] = make_float2(m, l);
+      // ---- the run's result: O of stream 0 times f0 and that of stream 1 times f1, over columns c0 .. c1 - 1.  A narrow
+      // unit's streams join theirs, each half the columns
+      const bool other = nar && r.count > 1;  // the second stream has any
+      float f0 = i == 0 || nar ? 1.f : 0.f, f1 = 1.f - f0;
+      const int c0 = nar ? i * (D / 2) : 0, c1 = nar ? c0 + D / 2 : D;
+      if (nar) {
+        ctl->ml[i][row] = make_float2(m, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->mlfull);
-        ok = mbar_wait_warp(&ctl->mlfree, joins & 1, kAtLong);
-        if (!ok) break;
-        ++joins;
-        tc_fence_after();
-      } else if (both) {
         ok = mbar_wait_warp(&ctl->mlfull, joins & 1, kAtLong);
         if (!ok) break;
-        ++joins;
         tc_fence_after();
-        const float2 o = ctl->ml[row];
-        const float to = fmaxf(m, o.x);
-        f0 = fast_exp2(m - to);
-        f1 = fast_exp2(o.x - to);
-        l = l * f0 + o.y * f1;
-        m = to;
+        const float2 x = ctl->ml[0][row], y = ctl->ml[1][row];
+        m = fmaxf(x.x, y.x);
+        f0 = fast_exp2(x.x - m);
+        f1 = fast_exp2(y.x - m);
+        l = x.y * f0 + y.y * f1;
       }
-      if ((!nar || i == 0) && !idle) {
+      if (!idle) {
         const bool cut = r.count < r.u.c;
         const int64_t slot = part_slot(blockIdx.x, r.first == 0) * a.rows_cap;
         const int rho = my_tok * a.group + hh;
-        const float inv = cut ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + rho;
-        float not_finite[4] = {0.f, 0.f, 0.f, 0.f};  // (0 times what is not finite is NaN)
+        if (!cut) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        const float2 f02 = make_float2(f0, f0), f12 = make_float2(f1, f1), zero2 = make_float2(0.f, 0.f);
+        float4* to = reinterpret_cast<float4*>(a.part_o + slot * D) + (int64_t)(c0 / 4) * a.rows_cap + rho;
+        float2 not_finite[2] = {zero2, zero2};  // (0 times what is not finite is NaN)
 #pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(tl + kAtO + 128 * i + c, o);
-          if (both) {
-            float o1[16];
-            tmem_ld16(tl + kAtO + 128 + c, o1);
+        for (int c = c0; c < c1; c += 16) {
+          float2 o[8];
+          tmem_ld16(tl + kAtO + (nar ? 0 : 128 * i) + c, reinterpret_cast<float*>(o));
+          if (other) {
+            float2 x[8];
+            tmem_ld16(tl + kAtO + 128 + c, reinterpret_cast<float*>(x));
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + o1[e] * f1;
-          }
-          tmem_wait_ld();
+            for (int e = 0; e < 8; ++e) o[e] = fma2(x[e], f12, mul2(o[e], f02));
+          } else {
+            const float2 f = nar || i == 0 ? f02 : f12;
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            o[e] *= inv;
-            not_finite[e & 3] = fmaf(o[e], 0.f, not_finite[e & 3]);
+            for (int e = 0; e < 8; ++e) o[e] = mul2(o[e], f);
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) not_finite[e & 1] = fma2(o[e], zero2, not_finite[e & 1]);
           if (!valid) continue;
           if (cut) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4, to += a.rows_cap) *to = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 8; e += 2, to += a.rows_cap) *to = make_float4(o[e].x, o[e].y, o[e + 1].x, o[e + 1].y);
           } else {
             if (l == 0.f) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = 0.f;
+              for (int e = 0; e < 8; ++e) o[e] = zero2;
             }
-            write_out<D, 16>(a, token, head, c, o);
+            write_out<D, 16>(a, token, head, c, reinterpret_cast<const float*>(o));
           }
         }
-        const bool bad = (not_finite[0] + not_finite[1]) + (not_finite[2] + not_finite[3]) != 0.f && l != 0.f;
-        if (valid && cut) a.part_ml[slot + rho] = make_float2(m, l);
-        if (valid && !cut) write_lse(a, token, head, m, l);
-        if (!cut) {
-          uint32_t rows = __ballot_sync(0xffffffffu, valid && bad && finite(l));
-          while (rows) {
-            const int from = __ffs(rows) - 1;
-            rows &= rows - 1;
-            float y[D / 32];
-            const int64_t t = __shfl_sync(0xffffffffu, token, from);
-            const int hd = __shfl_sync(0xffffffffu, head, from), col = lane * (D / 32);
-            repair_row<D, D / 32>(a, r.u.s, r.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
-                                  __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), col, y);
-            write_out<D, D / 32>(a, t, hd, col, y);
+        not_finite[0] = add2(not_finite[0], not_finite[1]);
+        const bool bad = not_finite[0].x + not_finite[0].y != 0.f && l != 0.f;
+        if (valid && c0 == 0) {
+          if (cut)
+            a.part_ml[slot + rho] = make_float2(m, l);
+          else
+            write_lse(a, token, head, m, l);
+        }
+        uint32_t rows = cut ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
+        while (rows) {
+          const int from = __ffs(rows) - 1;
+          rows &= rows - 1;
+          const int64_t t = __shfl_sync(0xffffffffu, token, from);
+          const int hd = __shfl_sync(0xffffffffu, head, from), first = __shfl_sync(0xffffffffu, lo, from);
+          const int end = __shfl_sync(0xffffffffu, hi, from);
+          const float top = __shfl_sync(0xffffffffu, m, from), all = __shfl_sync(0xffffffffu, l, from);
+          for (int c = c0; c < c1; c += D / 2) {
+            float y[D / 64];
+            const int col = c + lane * (D / 64);
+            repair_row<D, D / 64>(a, r.u.s, r.h, t, hd, first, end, top, all, col, y);
+            write_out<D, D / 64>(a, t, hd, col, y);
           }
         }
       }
       if (tid == 0 && r.first == 0) {
-        const uint64_t per = ctl->scratch.per;
-        const int c0 = (int)quotient(r.at, per);
-        const int parts = (int)quotient(r.at + r.u.c - 1, per) - c0 + 1;
-        if (parts > 1) a.cut[blockIdx.x] = AtCut{parts, c0, r.h, r.u.ntok, r.u.token0, r.slot, 0};
+        const uint64_t per = ctl->per;
+        const int cta = (int)quotient(r.at, per), parts = (int)quotient(r.at + r.u.c - 1, per) - cta + 1;
+        if (parts > 1) a.cut[blockIdx.x] = AtCut{parts, cta, r.h, r.u.ntok, r.u.token0, r.slot, 0};
       }
       tc_fence_before();
-      __syncwarp();
-      if (both && i == 0 && lane == 0) mbar_arrive(&ctl->mlfree);  // the second stream's O and sums are read
+      if (nar) {  // (either stream's O is both's to read)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->mlfree);
+        ok = mbar_wait_warp(&ctl->mlfree, joins & 1, kAtLong);
+        if (!ok) break;
+        ++joins;
+        tc_fence_after();
+      }
     }
     if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
   }
@@ -1508,11 +1516,12 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.h_q = p->h_q;
   a.causal = p->causal;
   // (places: tiles of a unit and its end, for each of 32 slots and every KV head)
-  a.few = pl.slots <= 32 && (int64_t)32 * pl.pages.h_kv * (pl.pages.max_rows / kAtKeys + 1 + kAtEnd) < (1ll << 31);
+  a.few = pl.slots <= 32 && (int64_t)32 * pl.pages.h_kv * (pl.pages.max_rows / kAtKeys + 1 + kAtEnd) < (1ll << 31) - pl.grid;
   a.ranged = !a.few;
   a.by_unit = divisor(2 * pl.tok_tile);
   a.by_page = divisor(pl.pages.page_rows / 16);
   a.by_group = divisor(pl.g);
+  a.by_cta = divisor(pl.grid);
   a.ctas = pl.grid;
   a.rows_cap = pl.rows_cap;
   a.box_shift = 0;
