@@ -14,19 +14,42 @@
 // (one CTA to an SM, persistent): ragged batches and long rows leave no SM idle.  Units that a run's border cuts leave
 // their parts in the workspace, and a second kernel joins them in the order of the CTAs.
 //
-// In a CTA: two groups of four softmax warps, one to a stream; a warp issues the MMAs (one thread), one the copies of
-// keys and values (TMA, boxes of as many rows as divide a page and 128, into a ring of tiles), one brings queries and
-// clears the value rows behind the sequence's last (a weight of 0 times whatever a page holds there could be NaN).
-// S = Q K^T goes to a TMEM buffer per stream; a softmax thread owns a row of it (its TMEM lane), takes it to registers
-// whole, and writes the weights as bf16 over the buffer's first half, from where the next MMA takes them as its A
-// operand: O += P V accumulates in TMEM.  The reference of the exponentials moves only when a row's maximum passes it by
-// 2^8; then O is rescaled in place, which nothing else touches in between because a thread's MMAs run in order.
+// In a CTA: two groups of four softmax warps, one to a stream; a warp to each stream's MMAs; one that copies keys and
+// values (TMA, boxes of as many rows as divide a page and 128, into a ring of tiles); one that brings queries and clears
+// the value rows behind the sequence's last (a weight of 0 times whatever a page holds there could be NaN).  S = Q K^T
+// goes to a TMEM buffer per stream; a softmax thread owns a row of it (its TMEM lane), takes it to registers whole, and
+// writes the weights as bf16 over the buffer's first half, from where the next MMA takes them as its A operand: O += P V
+// accumulates in TMEM.  The product begins when half of the weights are there.  The reference of the exponentials moves
+// only when a row's maximum passes it by 2^8; then O is rescaled in place, which nothing else touches in between because
+// a thread's MMAs run in order.  The streams' bursts of MMAs take turns: side by side each would take twice as long, and
+// both softmaxes would wait for both.
 //
-// Weights that meet V are rounded once to bf16 (2^-9 of each weight, independent of one another: an output's error is
-// that of its own rounding to bf16 or less).  Logits, maximum, sum, O, parts and the joins are fp32.
+// What the loop is bound by, at 128-wide heads: 2,048 cycles of the tensor cores for a tile of keys and two streams, 1,190
+// of the exponentials (4.6 cycles to a warp's), and the chain of a stream: its softmax (1,350 cycles alone, 2,100 beside
+// the other's), half of P V, S and the waits between them.  A tile takes 3,000 cycles (tensor pipe 65 to 67 % active).
+// Steps that it took (1,000 tokens over 130,000 rows, 28 to 4 heads): one lane of a warp that issues both streams' MMAs
+// 1,634 us; operands in the warp's uniform registers 1,372; a warp to each stream, and turns, 1,299; a run's description
+// out of the softmax threads' registers, and 200 of those, 1,192 (1,210 to 1,440 by the machine).  Not kept: 16 softmax
+// warps with half a row each, which meet for every maximum (1,718 of 1,304 then); exponentials under the old reference
+// beside the search of the maximum (1,211 of 1,205); one softmax at a time (1,519 of 1,404); turns for the first half's
+// MMAs alone (1,370 of 1,205).
+//
+// int8 rows: eight more warps widen the codes, exactly, into the bf16 tiles.  The softmax threads multiply logits by the
+// keys' scales and weights by the values', which takes 64 logits at a time, twice (3,900 cycles to a tile); these rows are
+// bound by instructions (issue 49 %, tensor pipe 24 %).
+//
+// Weights that meet V are rounded once to bf16 (at most 2^-8 of each weight, independent of one another; the error of an
+// output against 64 bits goes from 0.0017 of its norm, its own rounding to bf16, to 0.0023).  A second product with what
+// rounding takes away, as the decode kernel's, would be half as much again for the tensor cores.  Logits, maximum, sum, O,
+// parts and the joins are fp32.
 //
 // A weight of 0 does not hide a NaN or an infinity in V from a matrix product: a row whose output is not finite while
 // its sum is gets formed again, by a warp over the rows that it sees (repair_row).
+//
+// Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
+// 576 to 9,000 rows 577 to 625 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 153 to 169 us; one
+// token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats 16
+// to 17 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -631,330 +654,335 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       for (int s = tid; s < p.num_seqs; s += C::kThreads) bad |= wrong(seqs.cu[s], seqs.cu[s + 1], seqs.lens[s]);
       if (bad) set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
     }
-    any = make_run<C::kThreads>(a, seqs, reinterpret_cast<AtScratch*>(ctl->ml), ctl->per, r);  // (its barriers publish the mbarriers and TMEM too)
+    // (its barriers publish the mbarriers and TMEM too)
+    any = make_run<C::kThreads>(a, seqs, reinterpret_cast<AtScratch*>(ctl->ml), ctl->per, r);
   }
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
   if (warp >= kAtMma) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOther));
-  if (warp == kAtLoad) {
-    // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
-    // and the odd chunks: the next chunk's are looked up while this one is copied.  The copies are issued in turn by one
-    // lane (issued by a lane each they took four times as long, as their operands are the warp's)
-    const int box_shift = a.box_shift, box = 1 << box_shift;
-    const int boxes_shift = 7 - box_shift, per_shift = 5 - boxes_shift;  // boxes of a tile, tiles of a chunk
-    static_assert(kAtKeys == 128);
-    const bool one = elect_one();
-    uint32_t n = 0, tiles = 0;  // entries and key tiles so far
-    bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
-      const int count = r.count;
-      if (count == 0) continue;
-      const bool nar = narrow(a, r.u);
-      const int32_t* table = p.table + (int64_t)r.u.s * p.table_stride;
-      const int tile0 = r.u.t0 + r.first, rows = r.u.rows, h = r.h;
-      struct Place {
-        int page, row;  // of a box; -1: none
-      };
-      auto look = [&](int chunk) -> Place {
-        const int64_t row = ((int64_t)tile0 + ((int64_t)chunk << per_shift)) * kAtKeys + ((int64_t)lane << box_shift);
-        if (row >= rows || row >= (int64_t)(tile0 + count) * kAtKeys) return {-1, 0};
-        const int at = a.by_page.quotient((int)row >> 4);
-        const int page = table[at];
-        if (page_ok(p, page)) return {page, (int)row - at * p.page_rows};
-        set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
-        return {(int)p.num_pages, 0};  // (behind the tensor: its rows arrive as zeros)
-      };
-      Place even = look(0), odd = look(1);
-      for (int pos = 0; pos < 2 * count; ++pos, ++n) {
-        int j;  // the key tile within the run
-        const bool val = entry_of(nar, count, pos, j);
-        const int chunk = j >> per_shift, in_chunk = j - (chunk << per_shift);
-        if (val && in_chunk == 0 && chunk > 0) {  // keys are at most two tiles ahead of values, a chunk four or more
-          if (chunk & 1)
-            even = look(chunk + 1);
-          else
-            odd = look(chunk + 1);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOther));
+    if (warp == kAtLoad) {
+      // ---- keys and values.  Lane b holds the page of the b-th box of a chunk of 32 boxes (4 to 32 tiles), of the even
+      // and the odd chunks: the next chunk's are looked up while this one is copied.  The copies are issued in turn by one
+      // lane (issued by a lane each they took four times as long, as their operands are the warp's)
+      const int box_shift = a.box_shift, box = 1 << box_shift;
+      const int boxes_shift = 7 - box_shift, per_shift = 5 - boxes_shift;  // boxes of a tile, tiles of a chunk
+      static_assert(kAtKeys == 128);
+      const bool one = elect_one();
+      uint32_t n = 0, tiles = 0;  // entries and key tiles so far
+      bool ok = true;
+      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+        const int count = r.count;
+        if (count == 0) continue;
+        const bool nar = narrow(a, r.u);
+        const int32_t* table = p.table + (int64_t)r.u.s * p.table_stride;
+        const int tile0 = r.u.t0 + r.first, rows = r.u.rows, h = r.h;
+        struct Place {
+          int page, row;  // of a box; -1: none
+        };
+        auto look = [&](int chunk) -> Place {
+          const int64_t row = ((int64_t)tile0 + ((int64_t)chunk << per_shift)) * kAtKeys + ((int64_t)lane << box_shift);
+          if (row >= rows || row >= (int64_t)(tile0 + count) * kAtKeys) return {-1, 0};
+          const int at = a.by_page.quotient((int)row >> 4);
+          const int page = table[at];
+          if (page_ok(p, page)) return {page, (int)row - at * p.page_rows};
+          set_error(a.error, AIRCACHE_ERR_DEVICE_BOUNDS);
+          return {(int)p.num_pages, 0};  // (behind the tensor: its rows arrive as zeros)
+        };
+        Place even = look(0), odd = look(1);
+        for (int pos = 0; pos < 2 * count; ++pos, ++n) {
+          int j;  // the key tile within the run
+          const bool val = entry_of(nar, count, pos, j);
+          const int chunk = j >> per_shift, in_chunk = j - (chunk << per_shift);
+          if (val && in_chunk == 0 && chunk > 0) {  // keys are at most two tiles ahead of values, a chunk four or more
+            if (chunk & 1)
+              even = look(chunk + 1);
+            else
+              odd = look(chunk + 1);
+          }
+          const int left = rows - (tile0 + j) * kAtKeys;                     // rows from the tile's first on
+          const int boxes = (min(left, kAtKeys) + box - 1) >> box_shift;     // that hold any
+          const Place mine = chunk & 1 ? odd : even;
+          const int lane0 = in_chunk << boxes_shift;
+          const CUtensorMap* map = val ? &vmap : &kmap;
+          if constexpr (Q8) {
+            // codes to their own ring, from where they are widened into the tiles' one; with a tile's keys its scales
+            const uint32_t st = n % C::kCodeStages;
+            if (n >= C::kCodeStages) ok = mbar_wait_warp(&ctl->cempty[st], (n / C::kCodeStages + 1) & 1, kAtLong);
+            const uint32_t sc = (tiles + j) % C::kScaleStages, turn = (tiles + j) / C::kScaleStages;
+            if (ok && !val && turn > 0) ok = mbar_wait_warp(&ctl->scempty[sc], (turn + 1) & 1, kAtLong);
+            if (!ok) break;
+            // a lane to each box of codes, and of the keys' and of the values' scales
+            const int b = lane & ((1 << boxes_shift) - 1);
+            const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b);
+            const int row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
+            const bool codes = lane < (1 << boxes_shift) && b < boxes;
+            const bool scale = !val && lane < (2 << boxes_shift) && b < boxes, there = scale && page < p.num_pages;
+            const uint32_t scales = __popc(__ballot_sync(0xffffffffu, there));
+            float* to =
+                  reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 4 + (lane >> boxes_shift)) * kAtKeys + (b << box_shift);
+            if (scale && !there)  // (of a page out of bounds)
+              for (int e = 0; e < box; ++e) to[e] = 0.f;
+            __syncwarp();
+            if (one) {
+              mbar_arrive_expect_tx(&ctl->cfull[st], (uint32_t)((boxes << box_shift) * D));
+              if (!val) mbar_arrive_expect_tx(&ctl->scfull[sc], scales << (box_shift + 2));
+            }
+            __syncwarp();
+            fence_proxy_async_smem();
+            if (codes)
+              tma_load_4d(base + C::kOffCodes + st * C::kCodeTile + ((b * D) << box_shift), map, 0, row, h, page,
+                          &ctl->cfull[st]);
+            if (there)
+              bulk_g2s(to, (codes ? p.k_scale : p.v_scale) + page_slot(p, page, h, row), 4 << box_shift, &ctl->scfull[sc]);
+          } else {
+            const uint32_t st = n % C::kStages;
+            if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
+            if (!ok) break;
+            // values behind the last row are cleared by another warp, which then says that the tile is there
+            uint64_t* bar = val && left < kAtKeys ? &ctl->tail[st] : &ctl->full[st];
+            if (one) {
+              mbar_arrive_expect_tx(bar, (uint32_t)((boxes << box_shift) * 2 * D));
+              fence_proxy_async_smem();
+            }
+            const uint32_t dst = base + C::kOffRing + st * C::kTile;
+            for (int b = 0; b < boxes; ++b) {
+              const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b);
+              const int row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
+              if (one) {
+#pragma unroll
+                for (int slab = 0; slab < D / 64; ++slab)
+                  tma_load_5d(dst + slab * C::kSlab + ((b * 128) << box_shift), map, 0, row, slab, h, page, bar);
+              }
+            }
+            __syncwarp();
+          }
         }
-        const int left = rows - (tile0 + j) * kAtKeys;                     // rows from the tile's first on
-        const int boxes = (min(left, kAtKeys) + box - 1) >> box_shift;     // that hold any
-        const Place mine = chunk & 1 ? odd : even;
-        const int lane0 = in_chunk << boxes_shift;
-        const CUtensorMap* map = val ? &vmap : &kmap;
-        if constexpr (Q8) {
-          // codes to their own ring, from where they are widened into the tiles' one; with a tile's keys its scales
-          const uint32_t st = n % C::kCodeStages;
-          if (n >= C::kCodeStages) ok = mbar_wait_warp(&ctl->cempty[st], (n / C::kCodeStages + 1) & 1, kAtLong);
-          const uint32_t sc = (tiles + j) % C::kScaleStages, turn = (tiles + j) / C::kScaleStages;
-          if (ok && !val && turn > 0) ok = mbar_wait_warp(&ctl->scempty[sc], (turn + 1) & 1, kAtLong);
+        tiles += count;
+      }
+      if (!ok) {
+        // the copies in flight land before the CTA's shared memory is another's
+        set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+        constexpr uint32_t kRing = Q8 ? C::kCodeStages : C::kStages;
+        uint64_t* bars = Q8 ? ctl->cfull : ctl->full;
+        for (uint32_t f = n > kRing ? n - kRing : 0; f < n; ++f) (void)mbar_wait_warp(&bars[f % kRing], (f / kRing) & 1);
+        for (uint32_t f = 0; Q8 && f < C::kScaleStages && f <= tiles; ++f) (void)mbar_wait_warp(&ctl->scfull[f], 0);
+      }
+    } else if (warp == kAtAux) {
+      // ---- queries, and the values behind a sequence's last row
+      uint32_t units = 0, tails = 0, n = 0;  // tails: bit st is the parity of tail[st]
+      bool ok = true;
+      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+        if (r.count == 0) continue;
+        const bool nar = narrow(a, r.u);
+        if (units > 0) ok = mbar_wait_warp(&ctl->qempty, (units - 1) & 1, kAtLong);
+        if (!ok) break;
+        if (lane == 0) {
+          const int streams = nar ? 1 : 2;
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(&ctl->qfull, (uint32_t)(streams * (D / 64) * a.tok_tile * a.group * 128));
+          for (int i = 0; i < streams; ++i)
+            for (int sl = 0; sl < D / 64; ++sl)
+              tma_load_4d(base + C::kOffQ + i * C::kTile + sl * C::kSlab, &qmap, 0, sl, r.h * a.group,
+                          r.u.token0 + i * a.tok_tile, &ctl->qfull);
+        }
+        __syncwarp();
+        ++units;
+        const int64_t last = (int64_t)(r.u.t0 + r.first + r.count) * kAtKeys;
+        if (!Q8 && last > r.u.rows) {
+          const uint32_t st = (n + 2 * r.count - 1) % C::kStages;  // a run's last entry
+          ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
           if (!ok) break;
-          // a lane to each box of codes, and of the keys' and of the values' scales
-          const int b = lane & ((1 << boxes_shift) - 1);
-          const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b), row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
-          const bool codes = lane < (1 << boxes_shift) && b < boxes;
-          const bool scale = !val && lane < (2 << boxes_shift) && b < boxes, there = scale && page < p.num_pages;
-          const uint32_t scales = __popc(__ballot_sync(0xffffffffu, there));
-          float* to = reinterpret_cast<float*>(sm + C::kOffScales) + (sc * 4 + (lane >> boxes_shift)) * kAtKeys + (b << box_shift);
-          if (scale && !there)  // (of a page out of bounds)
-            for (int e = 0; e < box; ++e) to[e] = 0.f;
+          tails ^= 1u << st;
+          uint8_t* tile = sm + C::kOffRing + st * C::kTile;
+          const int valid = r.u.rows - (int)(last - kAtKeys);
+          for (int i = valid * (D / 8) + lane; i < kAtKeys * (D / 8); i += 32) {
+            const int row = i / (D / 8), rest = i % (D / 8);
+            *reinterpret_cast<uint4*>(tile + (rest >> 3) * C::kSlab + row * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->full[st]);
+        }
+        n += 2 * r.count;
+      }
+      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      if (units > 0) (void)mbar_wait_warp(&ctl->qfull, (units - 1) & 1);  // (landed)
+    } else if (warp == kAtMma || warp == kAtMma + 1) {
+      // ---- the MMAs of stream i: S of its first tile; then, tile by tile, O += P V and S of the next.  The whole warp
+      // walks along, with values that the compiler knows to be one for all lanes, and one lane issues: MMAs take their
+      // operands from uniform registers (a chunk of a 130,000-row prompt took a fifth longer with one lane alone in a
+      // branch).  Each stream has a warp of its own, which hides the waits between one's MMAs behind the other's
+      constexpr uint32_t id_s = umma_idesc_bf16(kAtRows, kAtKeys);
+      constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
+      const int i = __shfl_sync(0xffffffffu, warp - kAtMma, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts;
+      const bool one = elect_one();
+      uint32_t units = 0, n = 0, p_it = 0, turns = 0;
+      bool ok = true;
+      // the streams issue in turns: one's burst of MMAs would otherwise slow the other's, and both softmaxes wait for both
+      auto my_turn = [&] { return (i == 0 && turns == 0) || mbar_wait_warp(&ctl->turn[i], (turns - (i == 0)) & 1, kAtLong); };
+      auto pass = [&] {
+        if (one) mbar_arrive(&ctl->turn[1 - i]);
+      };
+      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+        const int count = __shfl_sync(0xffffffffu, r.count, 0);
+        if (count == 0) continue;
+        const bool nar = __shfl_sync(0xffffffffu, (int)narrow(a, r.u), 0);
+        const int tiles = stream_tiles(nar, count, i);
+        ok = mbar_wait_warp(&ctl->qfull, units & 1, kAtLong);
+        if (!ok) break;
+        ++units;
+        const uint64_t qd = umma_desc_sw128(base + C::kOffQ + (nar ? 0 : i * C::kTile));
+        auto entry = [&](uint32_t pos, uint32_t& st) {  // waits for a tile
+          const uint32_t e = n + pos;
+          st = e % C::kStages;
+          return mbar_wait_warp(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
+        };
+        auto release = [&](uint32_t st) {  // (by both streams, or by the one that has it)
+          umma_commit(&ctl->empty[st]);
+          if (nar) umma_commit(&ctl->empty[st]);
+        };
+        auto key_entry = [&](int it) { return nar ? max(2 * (2 * it + i) - 1, 0) : 2 * it; };
+        auto logits = [&](int it, uint32_t st) {
+          const uint64_t kd = umma_desc_sw128(base + C::kOffRing + st * C::kTile);
           if (one) {
-            mbar_arrive_expect_tx(&ctl->cfull[st], (uint32_t)((boxes << box_shift) * D));
-            if (!val) mbar_arrive_expect_tx(&ctl->scfull[sc], scales << (box_shift + 2));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4;  // (of the address field)
+              umma_bf16(ts, qd + off, kd + off, id_s, kk > 0);
+              if (kk == D / 16 - 3) mbar_arrive(&ctl->turn[1 - i]);  // (what is left covers the other's waking up)
+            }
+            umma_commit(&ctl->sfull[i]);
+            release(st);
+            if (it == tiles - 1) umma_commit(&ctl->qempty);
           }
           __syncwarp();
-          fence_proxy_async_smem();
-          if (codes)
-            tma_load_4d(base + C::kOffCodes + st * C::kCodeTile + ((b * D) << box_shift), map, 0, row, h, page, &ctl->cfull[st]);
-          if (there)
-            bulk_g2s(to, (codes ? p.k_scale : p.v_scale) + page_slot(p, page, h, row), 4 << box_shift, &ctl->scfull[sc]);
+        };
+        uint32_t ks = 0, vs = 0;
+        if (tiles > 0) {
+          ok = entry(key_entry(0), ks);
+          if (!ok) break;
+          tc_fence_after();
+          ok = my_turn();
+          if (!ok) break;
+          ++turns;
+          logits(0, ks);
         } else {
-          const uint32_t st = n % C::kStages;
+          ok = my_turn();
+          if (!ok) break;
+          ++turns;
+          pass();
+          if (one) mbar_arrive(&ctl->qempty);
+        }
+        for (int it = 0; it < tiles; ++it) {
+          // (what the tiles' waits cost is over before the weights come)
+          ok = entry(nar ? min(2 * (2 * it + i) + 2, 2 * count - 1) : 2 * it + 1, vs) &&
+               (it + 1 == tiles || entry(key_entry(it + 1), ks)) &&
+               mbar_wait_warp(&ctl->phalf[i], p_it & 1, kAtLong) && my_turn();
+          if (!ok) break;
+          ++turns;
+          tc_fence_after();
+          const uint64_t vd = umma_desc_sw128_mn(base + C::kOffRing + vs * C::kTile, C::kSlab, 1024);
+          auto weigh = [&](int half, bool first) {
+#pragma unroll
+            for (int kk = 0; kk < kAtKeys / 32; ++kk) {
+              const int at = half * (kAtKeys / 32) + kk;
+              umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0);
+            }
+          };
+          if (one) weigh(0, true);
+          __syncwarp();
+          ok = mbar_wait_warp(&ctl->pfull[i], p_it & 1, kAtLong);
+          if (!ok) break;
+          ++p_it;
+          tc_fence_after();
+          if (one) {
+            weigh(1, false);
+            release(vs);
+            if (it + 1 == tiles) umma_commit(&ctl->ofull[i]);
+          }
+          __syncwarp();
+          if (it + 1 < tiles)
+            logits(it + 1, ks);
+          else
+            pass();
+        }
+        if (ok && nar && i == 1 && tiles < stream_tiles(nar, count, 0)) {  // (a turn for each of the first stream's)
+          ok = my_turn();
+          ++turns;
+          pass();
+        }
+        n += 2 * count;
+      }
+      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      if (one) umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
+      (void)mbar_wait_warp(&ctl->done, 0);
+    } else if (Q8 && warp >= kAtWiden) {
+      // ---- int8 codes become bf16 tiles, half a row to a thread; value rows behind the sequence's last are zeros
+      uint32_t n = 0, tiles = 0;
+      bool ok = true;
+      const int row = (tid - kAtWiden * 32) & 127;
+      const int half = (tid - kAtWiden * 32) >> 7;
+      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+        if (r.count == 0) continue;
+        const bool nar = narrow(a, r.u);
+        for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
+          int j;
+          const bool val = entry_of(nar, r.count, pos, j);
+          const uint32_t cs = n % (Q8 ? C::kCodeStages : 1), st = n % C::kStages;
+          const uint32_t sc = (tiles + j) % (Q8 ? C::kScaleStages : 1);
+          const bool behind = (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
+          float* scales = reinterpret_cast<float*>(sm + C::kOffScales) + sc * 4 * kAtKeys + row;
+          if (!val) {
+            // A key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
+            // weight of 0 makes of that is mended as bf16 rows' is
+            ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles + j) / (Q8 ? C::kScaleStages : 1)) & 1, kAtLong);
+            if (!ok) break;
+            const float x = scales[half * kAtKeys];
+            scales[(2 + half) * kAtKeys] = half == 0 ? x * a.scale_log2 : behind ? 0.f : finite(x) ? x : 1.f;
+          }
+          const bool zero = val && behind, bad = val && !behind && !finite(scales[kAtKeys]);
+          ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
+          if (!ok) break;
+          const uint8_t* from = sm + C::kOffCodes + cs * C::kCodeTile;
+          uint8_t* to = sm + C::kOffRing + st * C::kTile + row * 128;
+          uint4 x[D / 32];
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q)
+            x[q] = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * (half * (D / 32) + q)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->cempty[cs]);
           if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
           if (!ok) break;
-          // values behind the last row are cleared by another warp, which then says that the tile is there
-          uint64_t* bar = val && left < kAtKeys ? &ctl->tail[st] : &ctl->full[st];
-          if (one) {
-            mbar_arrive_expect_tx(bar, (uint32_t)((boxes << box_shift) * 2 * D));
-            fence_proxy_async_smem();
-          }
-          const uint32_t dst = base + C::kOffRing + st * C::kTile;
-          for (int b = 0; b < boxes; ++b) {
-            const int page = __shfl_sync(0xffffffffu, mine.page, lane0 + b), row = __shfl_sync(0xffffffffu, mine.row, lane0 + b);
-            if (one) {
 #pragma unroll
-              for (int slab = 0; slab < D / 64; ++slab)
-                tma_load_5d(dst + slab * C::kSlab + ((b * 128) << box_shift), map, 0, row, slab, h, page, bar);
+          for (int q = 0; q < D / 32; ++q) {
+            const int c = half * (D / 32) + q;
+            uint4 lo = make_uint4(widen2_bf16(x[q].x, 0x4140u), widen2_bf16(x[q].x, 0x4342u), widen2_bf16(x[q].y, 0x4140u),
+                                  widen2_bf16(x[q].y, 0x4342u));
+            uint4 hi = make_uint4(widen2_bf16(x[q].z, 0x4140u), widen2_bf16(x[q].z, 0x4342u), widen2_bf16(x[q].w, 0x4140u),
+                                  widen2_bf16(x[q].w, 0x4342u));
+            if (zero || bad) {
+              const uint32_t u = zero ? 0u : 0x7fc07fc0u;
+              lo = hi = make_uint4(u, u, u, u);
             }
+            uint8_t* slab = to + (c >> 2) * C::kSlab;
+            *reinterpret_cast<uint4*>(slab + (((2 * c) & 7) ^ (row & 7)) * 16) = lo;
+            *reinterpret_cast<uint4*>(slab + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = hi;
           }
+          fence_proxy_async_smem();
           __syncwarp();
-        }
-      }
-      tiles += count;
-    }
-    if (!ok) {
-      // the copies in flight land before the CTA's shared memory is another's
-      set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-      constexpr uint32_t kRing = Q8 ? C::kCodeStages : C::kStages;
-      uint64_t* bars = Q8 ? ctl->cfull : ctl->full;
-      for (uint32_t f = n > kRing ? n - kRing : 0; f < n; ++f) (void)mbar_wait_warp(&bars[f % kRing], (f / kRing) & 1);
-      for (uint32_t f = 0; Q8 && f < C::kScaleStages && f <= tiles; ++f) (void)mbar_wait_warp(&ctl->scfull[f], 0);
-    }
-  } else if (warp == kAtAux) {
-    // ---- queries, and the values behind a sequence's last row
-    uint32_t units = 0, tails = 0, n = 0;  // tails: bit st is the parity of tail[st]
-    bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
-      if (r.count == 0) continue;
-      const bool nar = narrow(a, r.u);
-      if (units > 0) ok = mbar_wait_warp(&ctl->qempty, (units - 1) & 1, kAtLong);
-      if (!ok) break;
-      if (lane == 0) {
-        const int streams = nar ? 1 : 2;
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(&ctl->qfull, (uint32_t)(streams * (D / 64) * a.tok_tile * a.group * 128));
-        for (int i = 0; i < streams; ++i)
-          for (int sl = 0; sl < D / 64; ++sl)
-            tma_load_4d(base + C::kOffQ + i * C::kTile + sl * C::kSlab, &qmap, 0, sl, r.h * a.group,
-                        r.u.token0 + i * a.tok_tile, &ctl->qfull);
-      }
-      __syncwarp();
-      ++units;
-      const int64_t last = (int64_t)(r.u.t0 + r.first + r.count) * kAtKeys;
-      if (!Q8 && last > r.u.rows) {
-        const uint32_t st = (n + 2 * r.count - 1) % C::kStages;  // a run's last entry
-        ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
-        if (!ok) break;
-        tails ^= 1u << st;
-        uint8_t* tile = sm + C::kOffRing + st * C::kTile;
-        const int valid = r.u.rows - (int)(last - kAtKeys);
-        for (int i = valid * (D / 8) + lane; i < kAtKeys * (D / 8); i += 32) {
-          const int row = i / (D / 8), rest = i % (D / 8);
-          *reinterpret_cast<uint4*>(tile + (rest >> 3) * C::kSlab + row * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->full[st]);
-      }
-      n += 2 * r.count;
-    }
-    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-    if (units > 0) (void)mbar_wait_warp(&ctl->qfull, (units - 1) & 1);  // (landed)
-  } else if (warp == kAtMma || warp == kAtMma + 1) {
-    // ---- the MMAs of stream i: S of its first tile; then, tile by tile, O += P V and S of the next.  The whole warp
-    // walks along, with values that the compiler knows to be one for all lanes, and one lane issues: MMAs take their
-    // operands from uniform registers (a chunk of a 130,000-row prompt took a fifth longer with one lane alone in a
-    // branch).  Each stream has a warp of its own, which hides the waits between one's MMAs behind the other's
-    constexpr uint32_t id_s = umma_idesc_bf16(kAtRows, kAtKeys);
-    constexpr uint32_t id_o = umma_idesc_bf16_bmn(kAtRows, D);
-    const int i = __shfl_sync(0xffffffffu, warp - kAtMma, 0);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts;
-    const bool one = elect_one();
-    uint32_t units = 0, n = 0, p_it = 0, turns = 0;
-    bool ok = true;
-    // the streams issue in turns: one's burst of MMAs would otherwise slow the other's, and both softmaxes wait for both
-    auto my_turn = [&] { return (i == 0 && turns == 0) || mbar_wait_warp(&ctl->turn[i], (turns - (i == 0)) & 1, kAtLong); };
-    auto pass = [&] {
-      if (one) mbar_arrive(&ctl->turn[1 - i]);
-    };
-    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
-      const int count = __shfl_sync(0xffffffffu, r.count, 0);
-      if (count == 0) continue;
-      const bool nar = __shfl_sync(0xffffffffu, (int)narrow(a, r.u), 0);
-      const int tiles = stream_tiles(nar, count, i);
-      ok = mbar_wait_warp(&ctl->qfull, units & 1, kAtLong);
-      if (!ok) break;
-      ++units;
-      const uint64_t qd = umma_desc_sw128(base + C::kOffQ + (nar ? 0 : i * C::kTile));
-      auto entry = [&](uint32_t pos, uint32_t& st) {  // waits for a tile
-        const uint32_t e = n + pos;
-        st = e % C::kStages;
-        return mbar_wait_warp(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
-      };
-      auto release = [&](uint32_t st) {  // (by both streams, or by the one that has it)
-        umma_commit(&ctl->empty[st]);
-        if (nar) umma_commit(&ctl->empty[st]);
-      };
-      auto key_entry = [&](int it) { return nar ? max(2 * (2 * it + i) - 1, 0) : 2 * it; };
-      auto logits = [&](int it, uint32_t st) {
-        const uint64_t kd = umma_desc_sw128(base + C::kOffRing + st * C::kTile);
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::kSlab + (kk & 3) * 32) >> 4;  // (of the address field)
-            umma_bf16(ts, qd + off, kd + off, id_s, kk > 0);
-            if (kk == D / 16 - 3) mbar_arrive(&ctl->turn[1 - i]);  // (what is left covers the other's waking up)
+          if (lane == 0) {
+            if (!val) mbar_arrive(&ctl->scready[sc]);
+            mbar_arrive(&ctl->full[st]);
           }
-          umma_commit(&ctl->sfull[i]);
-          release(st);
-          if (it == tiles - 1) umma_commit(&ctl->qempty);
         }
-        __syncwarp();
-      };
-      uint32_t ks = 0, vs = 0;
-      if (tiles > 0) {
-        ok = entry(key_entry(0), ks);
-        if (!ok) break;
-        tc_fence_after();
-        ok = my_turn();
-        if (!ok) break;
-        ++turns;
-        logits(0, ks);
-      } else {
-        ok = my_turn();
-        if (!ok) break;
-        ++turns;
-        pass();
-        if (one) mbar_arrive(&ctl->qempty);
+        tiles += r.count;
       }
-      for (int it = 0; it < tiles; ++it) {
-        // (what the tiles' waits cost is over before the weights come)
-        ok = entry(nar ? min(2 * (2 * it + i) + 2, 2 * count - 1) : 2 * it + 1, vs) &&
-             (it + 1 == tiles || entry(key_entry(it + 1), ks)) &&
-             mbar_wait_warp(&ctl->phalf[i], p_it & 1, kAtLong) && my_turn();
-        if (!ok) break;
-        ++turns;
-        tc_fence_after();
-        const uint64_t vd = umma_desc_sw128_mn(base + C::kOffRing + vs * C::kTile, C::kSlab, 1024);
-        auto weigh = [&](int half, bool first) {
-#pragma unroll
-          for (int kk = 0; kk < kAtKeys / 32; ++kk) {
-            const int at = half * (kAtKeys / 32) + kk;
-            umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0);
-          }
-        };
-        if (one) weigh(0, true);
-        __syncwarp();
-        ok = mbar_wait_warp(&ctl->pfull[i], p_it & 1, kAtLong);
-        if (!ok) break;
-        ++p_it;
-        tc_fence_after();
-        if (one) {
-          weigh(1, false);
-          release(vs);
-          if (it + 1 == tiles) umma_commit(&ctl->ofull[i]);
-        }
-        __syncwarp();
-        if (it + 1 < tiles)
-          logits(it + 1, ks);
-        else
-          pass();
-      }
-      if (ok && nar && i == 1 && tiles < stream_tiles(nar, count, 0)) {  // (a turn for each of the first stream's)
-        ok = my_turn();
-        ++turns;
-        pass();
-      }
-      n += 2 * count;
+      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
     }
-    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-    if (one) umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
-    (void)mbar_wait_warp(&ctl->done, 0);
-  } else if (Q8 && warp >= kAtWiden) {
-    // ---- int8 codes become bf16 tiles, half a row to a thread; value rows behind the sequence's last are zeros
-    uint32_t n = 0, tiles = 0;
-    bool ok = true;
-    const int row = (tid - kAtWiden * 32) & 127;
-    const int half = (tid - kAtWiden * 32) >> 7;
-    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
-      if (r.count == 0) continue;
-      const bool nar = narrow(a, r.u);
-      for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
-        int j;
-        const bool val = entry_of(nar, r.count, pos, j);
-        const uint32_t cs = n % (Q8 ? C::kCodeStages : 1), st = n % C::kStages;
-        const uint32_t sc = (tiles + j) % (Q8 ? C::kScaleStages : 1);
-        const bool behind = (int64_t)(r.u.t0 + r.first + j) * kAtKeys + row >= r.u.rows;
-        float* scales = reinterpret_cast<float*>(sm + C::kOffScales) + sc * 4 * kAtKeys + row;
-        if (!val) {
-          // A key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
-          // weight of 0 makes of that is mended as bf16 rows' is
-          ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles + j) / (Q8 ? C::kScaleStages : 1)) & 1, kAtLong);
-          if (!ok) break;
-          const float x = scales[half * kAtKeys];
-          scales[(2 + half) * kAtKeys] = half == 0 ? x * a.scale_log2 : behind ? 0.f : finite(x) ? x : 1.f;
-        }
-        const bool zero = val && behind, bad = val && !behind && !finite(scales[kAtKeys]);
-        ok = mbar_wait_warp(&ctl->cfull[cs], (n / (Q8 ? C::kCodeStages : 1)) & 1, kAtLong);
-        if (!ok) break;
-        const uint8_t* from = sm + C::kOffCodes + cs * C::kCodeTile;
-        uint8_t* to = sm + C::kOffRing + st * C::kTile + row * 128;
-        uint4 x[D / 32];
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q)
-          x[q] = *reinterpret_cast<const uint4*>(from + swz8<D>(row * D + 16 * (half * (D / 32) + q)));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->cempty[cs]);
-        if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
-        if (!ok) break;
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          const int c = half * (D / 32) + q;
-          uint4 lo = make_uint4(widen2_bf16(x[q].x, 0x4140u), widen2_bf16(x[q].x, 0x4342u), widen2_bf16(x[q].y, 0x4140u),
-                                widen2_bf16(x[q].y, 0x4342u));
-          uint4 hi = make_uint4(widen2_bf16(x[q].z, 0x4140u), widen2_bf16(x[q].z, 0x4342u), widen2_bf16(x[q].w, 0x4140u),
-                                widen2_bf16(x[q].w, 0x4342u));
-          if (zero || bad) {
-            const uint32_t u = zero ? 0u : 0x7fc07fc0u;
-            lo = hi = make_uint4(u, u, u, u);
-          }
-          uint8_t* slab = to + (c >> 2) * C::kSlab;
-          *reinterpret_cast<uint4*>(slab + (((2 * c) & 7) ^ (row & 7)) * 16) = lo;
-          *reinterpret_cast<uint4*>(slab + (((2 * c + 1) & 7) ^ (row & 7)) * 16) = hi;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (!val) mbar_arrive(&ctl->scready[sc]);
-          mbar_arrive(&ctl->full[st]);
-        }
-      }
-      tiles += r.count;
-    }
-    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoft));
     // ---- softmax: stream i, query row `row` (its TMEM lane)
@@ -1446,8 +1474,9 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
   const int rc = check_pages(p->pages, pl.pages);
   if (rc != AIRCACHE_OK) return rc;
   const int d = p->pages->head_dim;
-  if (p->num_tokens < 0 || p->num_tokens > 0x7fff0000LL || p->h_q <= 0 || p->h_q % p->pages->h_kv != 0 || p->dtype != AIRCACHE_BF16 ||
-      (p->causal != 0 && p->causal != 1) || p->reserved0 != 0 || p->reserved1 != 0.f || !(p->scale > 0.f) || !std::isfinite(1.4427f * p->scale) ||
+  if (p->num_tokens < 0 || p->num_tokens > 0x7fff0000LL || p->h_q <= 0 || p->h_q % p->pages->h_kv != 0 ||
+      p->dtype != AIRCACHE_BF16 || (p->causal != 0 && p->causal != 1) || p->reserved0 != 0 || p->reserved1 != 0.f ||
+      !(p->scale > 0.f) || !std::isfinite(1.4427f * p->scale) ||
       !p->q || !al16(p->q) || p->q_stride_tok % 8 != 0 || p->q_stride_head % 8 != 0 ||
       (p->num_tokens > 1 && p->q_stride_tok <= 0) || (p->h_q > 1 && p->q_stride_head <= 0) || !p->cu_tokens ||
       !al4(p->cu_tokens) || !al4(p->row_begin) || !al4(p->row_end) || !al4(p->lse))
@@ -1467,7 +1496,8 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
     };
     const size_t nq = bytes(many_t ? p->q_stride_tok : 0, many_h ? p->q_stride_head : 0);
     const size_t no = bytes(many_t ? st : 0, many_h ? sh : 0), nl = 4 * (size_t)p->num_tokens * p->h_q;
-    const size_t nk = (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2) * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;  // (to the last page, at least)
+    // (keys and values to the last page, at least)
+    const size_t nk = (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2) * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;
     if (arrays_meet(p->out, no, p->q, nq) || arrays_meet(p->out, no, pl.pages.k, nk) ||
         arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq))
       return AIRCACHE_ERR_INVALID_ARG;
