@@ -108,12 +108,18 @@ struct alignas(16) AtCut {
   int slot, pad;
 };
 
-// x / d for x < 2^31 and 1 <= d <= 256: M = ceil(2^40 / d) is off by less than d / 2^40 of 1 / d, and x d < 2^39.
+// x / d for 0 <= x < 2^31 and 1 <= d <= 2^30: with 2^(L-1) < d <= 2^L, M = ceil(2^(31 + L) / d) <= 2^32 - 1 and
+// M d - 2^(31 + L) < d, so that x M / 2^(31 + L) passes x / d by less than 1 / d.
 struct AtDivisor {
-  uint64_t m;
-  __host__ __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> 40); }
+  uint32_t m;
+  int shift;
+  __host__ __device__ __forceinline__ int quotient(int x) const { return (int)(((uint64_t)(uint32_t)x * m) >> shift); }
 };
-inline AtDivisor divisor(int d) { return {((1ull << 40) + d - 1) / d}; }
+inline AtDivisor divisor(int d) {
+  int shift = 31;
+  while ((1ll << (shift - 31)) < d) ++shift;
+  return {(uint32_t)(((1ull << shift) + d - 1) / d), shift};
+}
 
 struct AtArgs {
   Pages pages;

@@ -2,6 +2,7 @@
 moment: read from the sources, without a GPU."""
 import os
 import re
+import subprocess
 
 from conftest import ROOT
 
@@ -116,3 +117,34 @@ def test_registers_that_the_paged_attention_shares_out():
     assert "256 * kRegsSoft + (kThreads - 256) * kRegsOther <= kThreads * kRegs" in text
     assert "if (regs < C::kRegs) return AIRCACHE_ERR_CUDA;" in text
     assert text.count("setmaxnreg") == 2
+
+
+def test_division_by_a_constant_holds_over_its_range(tmp_path):
+    # rows of a sequence (of 16, to its pages) run up to 2^31: a product that passes 64 bits would name another page
+    with open(os.path.join(CSRC, "paged_attend.cu")) as f:
+        text = f.read()
+    at = text.index("struct AtDivisor {")
+    code = text[at:text.index("struct AtArgs {", at)]
+    main = """
+#include <cstdint>
+#include <cstdio>
+#define __host__
+#define __device__
+#define __forceinline__ inline
+%s
+int main() {
+  long bad = 0;
+  for (int d = 1; d <= 304; ++d) {
+    const AtDivisor by = divisor(d);
+    auto check = [&](int64_t x) { bad += x >= 0 && x < (1ll << 31) && by.quotient((int)x) != x / d; };
+    for (int64_t x = 0; x < 3000; ++x) check(x), check((1ll << 31) - 1 - x);
+    for (int b = 10; b < 31; ++b)
+      for (int64_t k = -40; k <= 40; ++k) check((1ll << b) + k), check(((1ll << b) / d + k) * d), check(((1ll << b) / d + k) * d - 1);
+  }
+  printf("%%ld\\n", bad);
+}
+""" % code
+    src, exe = tmp_path / "divide.cpp", tmp_path / "divide"
+    src.write_text(main)
+    subprocess.run(["g++", "-O1", "-std=c++17", str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.strip() == "0"

@@ -152,6 +152,22 @@ def test_offsets_past_32_bits(A, int8):
     verify(prob.out, prob.lse, q, [0, n], P.host(small), causal=True)
 
 
+@pytest.mark.parametrize("int8", [False, True])
+def test_rows_past_two_to_the_28(A, int8):
+    # a table of more than 2^24 pages (the same 64 of them again and again), of which the tokens see a window
+    d, h, page_rows, n, pages_n = 64, 1, 16, 9, 64
+    at, R = (1 << 28) + 5, (1 << 28) + 700
+    small = P.build(A, [page_rows * pages_n], h, d, page_rows, seed=34, mass=False, order=False, int8=int8)
+    table = small.table[0].repeat(R // (page_rows * pages_n) + 1).reshape(1, -1)
+    cache = A.PagedCache(small.k, small.v, table, i32([R]), k_scale=small.k_scale, v_scale=small.v_scale)
+    q = queries(n, 4, d, 34)
+    begin, end = [at + 10 * i for i in range(n)], [at + 10 * i + 300 for i in range(n)]
+    prob = A.PagedAttendProblem(q, cache, i32([0, n]), lse=True, row_begin=i32(begin), row_end=i32(end))
+    A.paged_attend(prob)
+    base = at // (page_rows * pages_n) * page_rows * pages_n  # (the window lies within one round of the pages)
+    verify(prob.out, prob.lse, q, [0, n], P.host(small), begin=[x - base for x in begin], end=[x - base for x in end])
+
+
 @pytest.mark.parametrize("fused,wide", [(True, 0), (False, 3), (True, 1)])
 def test_strides(A, fused, wide):
     for d, int8 in ((128, False), (64, True), (64, False)):
