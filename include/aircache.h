@@ -803,8 +803,8 @@ AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_
  * Device-side, AIRCACHE_ERR_DEVICE_BOUNDS is set by a length out of bounds (the
  * sequence then has no rows), a decreasing cu_tokens, one below 0 or above
  * num_tokens (the sequence then has no tokens, and its outputs are left as they
- * are), fewer rows than tokens with `causal`, and a page out of bounds (its rows
- * read as zeros).
+ * are; where offsets are out of order others' may be undefined too), fewer rows
+ * than tokens with `causal`, and a page out of bounds (its rows read as zeros).
  *
  * The work is split by rows and tokens, whatever the lengths; a second kernel
  * joins what several CTAs did, in a fixed order (a third one before them where

@@ -1263,7 +1263,9 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       }
       if (tid == 0 && r.first == 0) {
         const uint64_t per = ctl->per;
-        const int cta = (int)quotient(r.at, per), parts = (int)quotient(r.at + r.u.c - 1, per) - cta + 1;
+        // (offsets out of order, an error, give every CTA a line of its own: no part of a unit lies behind the last CTA)
+        const int cta = (int)quotient(r.at, per);
+        const int parts = (int)min(quotient(r.at + r.u.c - 1, per), (uint64_t)a.ctas - 1) - cta + 1;
         if (parts > 1) a.cut[blockIdx.x] = AtCut{parts, cta, r.h, r.u.ntok, r.u.token0, r.slot, 0};
       }
       tc_fence_before();

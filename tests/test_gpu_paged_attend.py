@@ -464,6 +464,22 @@ def test_bad_token_offsets(A, cu):
     assert torch.all(big[:10] == 7.0) and torch.all(big[70:] == 7.0)
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("few", [True, False])
+def test_offsets_out_of_order_over_many_rows(A, few, int8):
+    # the units that CTAs find then differ from CTA to CTA: all of them are cut, none has parts behind the last CTA
+    S, T = (4, 60) if few else (40, 2000)
+    cache = P.build(A, [9000, 20, 9000, 9000] + [3000] * (S - 4), 2, 128, 64, seed=35, mass=False, order=False, int8=int8)
+    q = queries(T, 32, 128, 35)
+    for cu in ([0, T, 0] + [T] * (S - 2), [0, T // 2, T // 4, T] + [0] * (S - 4) + [T], [T, 0] * (S // 2) + [T]):
+        big = torch.full((T + 20, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        prob = A.PagedAttendProblem(q, cache, i32(cu), out=big[10:T + 10])
+        with pytest.raises(A.AirCacheError) as e:
+            A.paged_attend(prob)
+        assert e.value.status == A.ERR_DEVICE_BOUNDS
+        assert torch.all(big[:10] == 7.0) and torch.all(big[T + 10:] == 7.0)
+
+
 def test_no_tokens_and_no_sequences(A):
     cache = P.build(A, [20, 10], 2, 128, 16, seed=29, mass=False, order=False)
     prob = A.PagedAttendProblem(torch.empty((0, 4, 128), dtype=torch.bfloat16, device="cuda"), cache, i32([0, 0, 0]))
