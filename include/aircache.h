@@ -847,9 +847,9 @@ AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, v
  * once for all of them.  Sequences cu_seqs[i] .. cu_seqs[i+1]-1 continue prefix i:
  * each attends over the rows of that prefix (rows 0 .. prefix->lens[i]-1 of the
  * prefix's own pages) and over its own rows (own.pages), as one softmax; the
- * results are those of aircache_paged_decode over both.  Sequences at or behind
- * cu_seqs[number of prefixes] have only their own rows; a prefix may have no
- * rows, and a sequence none of its own.
+ * results are those of aircache_paged_decode over both.  Sequences before
+ * cu_seqs[0], and at or behind cu_seqs[number of prefixes], have only their own
+ * rows; a prefix may have no rows, and a sequence none of its own.
  * own: the step over the own rows, all of it as aircache_paged_decode takes it
  * (total_rows bounds the own rows only); with mass_out, the mass of the own rows
  * grows by their weights in the joint softmax.  The prefixes' mass is neither
@@ -869,7 +869,7 @@ AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, v
 typedef struct aircache_shared_decode_problem {
     aircache_paged_decode_problem own;
     const aircache_pages* prefix;  /* HOST; its num_seqs: the number of prefixes */
-    const int32_t* cu_seqs;        /* device [prefix->num_seqs + 1], non-decreasing, from 0 */
+    const int32_t* cu_seqs;        /* device [prefix->num_seqs + 1], non-decreasing */
 } aircache_shared_decode_problem;
 
 AIRCACHE_API size_t aircache_shared_decode_workspace_size(const aircache_shared_decode_problem* p);

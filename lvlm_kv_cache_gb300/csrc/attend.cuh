@@ -35,11 +35,11 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
 __device__ __forceinline__ void prior_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // A result over other rows that a decode step joins with its own: fp32 outputs [S][h_q][head_dim] and log-sum-exps in
-// base 2 [S][h_q], of the first *num sequences (out == nullptr: of none).
+// base 2 [S][h_q], of sequences *from .. *num - 1 (out == nullptr: of none).
 struct DecodePrior {
   const float* out;
   const float* lse2;
-  const int32_t* num;  // device
+  const int32_t *from, *num;  // device
 };
 // aircache_paged_decode, joined with a prior result; and the workspace it takes (AIRCACHE_OK, or why not).
 int paged_decode_run(const aircache_paged_decode_problem* p, const DecodePrior& prior, void* ws, size_t ws_bytes,

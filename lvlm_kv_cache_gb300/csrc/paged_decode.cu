@@ -146,7 +146,7 @@ __device__ __forceinline__ int rows_of(const Pages& p, int s) {
 __device__ __forceinline__ Joint joint(const PdArgs& a, int64_t head, float m, float l) {
   prior_wait();
   Joint j = {1.f, 0.f, l == 0.f ? -INFINITY : m + log2f(l)};
-  if (head < (int64_t)*a.prior.num * a.h_q) {
+  if (head >= (int64_t)*a.prior.from * a.h_q && head < (int64_t)*a.prior.num * a.h_q) {
     const float p = a.prior.lse2[head];
     if (p != -INFINITY) {
       const float top = fmaxf(j.lse2, p);  // (a NaN stays one in the factor of its own)
@@ -1327,7 +1327,7 @@ size_t aircache_paged_decode_workspace_size(const aircache_paged_decode_problem*
 }
 
 int aircache_paged_decode(const aircache_paged_decode_problem* p, void* ws, size_t ws_bytes, void* stream) {
-  return paged_decode_run(p, DecodePrior{nullptr, nullptr, nullptr}, ws, ws_bytes, stream);
+  return paged_decode_run(p, DecodePrior{nullptr, nullptr, nullptr, nullptr}, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

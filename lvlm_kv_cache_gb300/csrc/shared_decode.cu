@@ -76,13 +76,13 @@ int aircache_shared_decode(const aircache_shared_decode_problem* p, void* ws, si
   if (ws_bytes < pl.total) return AIRCACHE_ERR_WORKSPACE;
   if (p->own.pages->num_seqs == 0) return AIRCACHE_OK;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  DecodePrior prior = {nullptr, nullptr, nullptr};
+  DecodePrior prior = {nullptr, nullptr, nullptr, nullptr};
   if (p->prefix->num_seqs > 0) {
     const AttendPart part = {reinterpret_cast<float*>(w + pl.out_off), reinterpret_cast<float*>(w + pl.lse_off)};
     rc = attend_launch(&pl.at, pl.attend, part, w + pl.attend_off, reinterpret_cast<int32_t*>(w),
                        static_cast<cudaStream_t>(stream));
     if (rc != AIRCACHE_OK) return rc;
-    prior = {part.out, part.lse2, p->cu_seqs + p->prefix->num_seqs};
+    prior = {part.out, part.lse2, p->cu_seqs, p->cu_seqs + p->prefix->num_seqs};
   }
   return paged_decode_run(&p->own, prior, ws, pl.attend_off, stream);
 }

@@ -89,7 +89,7 @@ def attend(q, cu, c, scale, causal=False, begin=None, end=None):
 
 
 def shared_decode(q, c, prefix, cu, scale):
-    """decode() over each sequence's prefix (cu: the first sequence of each, and of none) and its own rows: (out, lse,
+    """decode() over each sequence's prefix (cu: the first sequence of each, and the first behind them) and its own rows: (out, lse,
     weight of each own row [S][H][n], logits' sizes, sum_j w_j |v_j|, the same over the prefix's rows alone)."""
     S, h_q, d = q.shape
     h = c["k"].shape[2]
@@ -102,7 +102,7 @@ def shared_decode(q, c, prefix, cu, scale):
         w_s = np.zeros((h, n))
         for j in range(h_q):
             k, v = rows(c, "k", s, j // g), rows(c, "v", s, j // g)
-            if i < len(cu) - 1:
+            if 0 <= i < len(cu) - 1:
                 k = np.concatenate([rows(prefix, "k", i, j // g), k])
                 v = np.concatenate([rows(prefix, "v", i, j // g), v])
             if len(k) == 0:

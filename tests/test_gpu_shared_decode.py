@@ -49,13 +49,13 @@ def verify(prob, q, c, prefix, cu, mass_before=None):
 
 
 def case(A, groups, prefix, lens, h_q, h_kv, d, page_rows=16, p_page=32, seed=0, int8=False, p_int8=None, mass=False,  # noqa: F811
-         q_scale=1.5, fill=None, **kw):
-    """groups: members of each prefix; sequences behind them have none."""
+         q_scale=1.5, fill=None, first=0, **kw):
+    """groups: members of each prefix, from sequence `first` on; those before and behind them have none."""
     S = len(lens)
     cache = P.build(A, lens, h_kv, d, page_rows, seed=seed, int8=int8, mass=mass, order=False, fill=fill)
     pre = P.build(A, prefix, h_kv, d, p_page, seed=seed + 100, int8=int8 if p_int8 is None else p_int8, mass=False,
                   order=False, fill=fill)
-    cu = np.concatenate([[0], np.cumsum(groups)])
+    cu = first + np.concatenate([[0], np.cumsum(groups)])
     q = queries(S, h_q, d, seed, q_scale)
     before, p_before, p_state = P.host(cache), P.host(pre), P.state(pre)
     prob = A.SharedDecodeProblem(q, cache, pre, i32(cu.tolist()), lse=True, accumulate=mass, **kw)
@@ -73,6 +73,15 @@ def test_groups(A, d, mass, int8):  # noqa: F811
     lens = [0, 5, 64, 700, 1, 33, 0, 128, 90, 300, 0, 17]
     case(A, [3, 0, 1, 5], [300, 50, 0, 129], lens, 28, 4, d, seed=d, int8=int8, mass=mass)
     case(A, [3, 0, 1, 8], [128, 1, 17, 2000], lens, 8, 8, d, seed=d, int8=int8, mass=mass)
+
+
+@pytest.mark.parametrize("mass", [False, True])
+@pytest.mark.parametrize("last", [700, 9000])
+def test_sequences_before_the_first_group(A, last, mass):  # noqa: F811
+    # (twice: the second call's workspace holds what other sequences got in the first)
+    lens = [40, 0, 300, 5, 90, 64, last]
+    for first in (0, 3):
+        case(A, [2, 1], [200, 130], lens, 14, 2, 128, seed=8, mass=mass, first=first)
 
 
 @pytest.mark.parametrize("int8,p_int8", [(False, True), (True, False)])
