@@ -1507,7 +1507,8 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
     // (keys and values to the last page, at least)
     const size_t nk = (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2) * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;
     if (arrays_meet(p->out, no, p->q, nq) || arrays_meet(p->out, no, pl.pages.k, nk) ||
-        arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq))
+        arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq) ||
+        arrays_meet(p->lse, nl, pl.pages.k, nk) || arrays_meet(p->lse, nl, pl.pages.v, nk))
       return AIRCACHE_ERR_INVALID_ARG;
   }
   pl.d = d;

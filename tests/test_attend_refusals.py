@@ -77,7 +77,8 @@ def test_bad_attend(A, over, code):
     dict(out_stride_tok=256, out_stride_head=1280),                     # rows of out that meet
     dict(out=0x1000000), dict(out=0x1000100), dict(out=0x1000000 - 256),  # out and q
     dict(out=0x100000), dict(out=0x200010), dict(out=0x100000 + 49 * 16 * 512 * 2 - 16),  # out and the cache
-    dict(lse=0x1100000), dict(lse=0x1100000 + 9 * 7168 + 27 * 256), dict(lse=0x1000010)])  # lse and out, q
+    dict(lse=0x1100000), dict(lse=0x1100000 + 9 * 7168 + 27 * 256), dict(lse=0x1000010),  # lse and out, q
+    dict(lse=0x100000), dict(lse=0x200010)])                            # lse and the cache
 def test_attend_refuses_outputs_that_lie_on_something(A, over):
     assert attend_status(A, attend(A, **over)) == A.ERR_INVALID_ARG
 
