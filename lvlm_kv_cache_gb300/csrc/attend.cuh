@@ -22,7 +22,7 @@ struct AttendPlan {
   int tok_tile;   // tokens of a stream's 128 query rows
   int slots;      // bound of the batch's units for one KV head
   int grid, rows_cap;
-  size_t cut_off, range_off, ml_off, o_off, total;
+  size_t cut_off, start_off, range_off, ml_off, o_off, total;
 };
 
 // Checks a problem and lays out its workspace.  `part`: the results go to fp32 arrays and p->out is not looked at.

@@ -43,8 +43,11 @@
 // rounding takes away, as the decode kernel's, would be half as much again for the tensor cores.  Logits, maximum, sum, O,
 // parts and the joins are fp32.
 //
-// A weight of 0 does not hide a NaN or an infinity in V from a matrix product: a row whose output is not finite while
-// its sum is gets formed again, by a warp over the rows that it sees (repair_row).
+// A weight of 0 does not hide a NaN or an infinity in V from a matrix product.  A CTA that finds an output that is not
+// finite while its sum is walks over its units a second time: values that are not finite are cleared before the product
+// and added to the outputs of the rows that see them, and the weights are 2^-40 of what they were (sums of large values
+// may have passed fp32's range).  Ragged questions of which every sequence holds a NaN take 2.4 ms instead of 0.6; row by
+// row, a warp to an output row, they took 1,600 to 2,500 ms.
 //
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
 // 576 to 9,000 rows 577 to 625 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 153 to 169 us; one
@@ -121,6 +124,7 @@ inline AtDivisor divisor(int d) {
   return {(uint32_t)(((1ull << shift) + d - 1) / d), shift};
 }
 
+struct AtRun;
 struct AtArgs {
   Pages pages;
   const int32_t* cu;
@@ -134,6 +138,7 @@ struct AtArgs {
   AttendPart part;
   int32_t* error;
   AtCut* cut;       // [CTAs]: the unit that begins in the CTA and ends in another
+  AtRun* start;      // [CTAs]: where each begins
   int2* range;      // [slots]: the key tiles that a unit's tokens see (with row_begin or row_end)
   float2* part_ml;  // [2 CTAs][rows_cap]
   float* part_o;    // [2 CTAs][rows_cap][D]
@@ -311,20 +316,27 @@ __device__ __forceinline__ void clip(AtRun& r, uint64_t per) {  // per: places o
   r.first = (int)(min(from, r.at + r.u.c) - r.at);
   r.count = to > from ? (int)(to - from) : 0;
 }
+// (`r` is the warp's: every lane reads it before any writes the same over it)
 __device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r, uint64_t per) {
-  r.at += r.u.c + kAtEnd;
-  if (r.at >= per * (blockIdx.x + 1)) return false;
-  if (++r.h == a.pages.h_kv) {
-    r.h = 0;
+  __syncwarp();
+  AtRun x = r;
+  __syncwarp();
+  x.at += x.u.c + kAtEnd;
+  bool more = x.at < per * (blockIdx.x + 1);
+  if (more && ++x.h == a.pages.h_kv) {
+    x.h = 0;
     do {
-      if (++r.slot >= a.slots) return false;
-      int s = r.u.s;
-      while (s + 1 < a.pages.num_seqs && slot_base(a, a.cu[s + 1], s + 1) <= r.slot) ++s;
-      r.u = unit_of(a, seqs_of(a), s, r.slot, a.range);
-    } while (r.u.ntok == 0);
+      more = ++x.slot < a.slots;
+      if (!more) break;
+      int s = x.u.s;
+      while (s + 1 < a.pages.num_seqs && slot_base(a, a.cu[s + 1], s + 1) <= x.slot) ++s;
+      x.u = unit_of(a, seqs_of(a), s, x.slot, a.range);
+    } while (x.u.ntok == 0);
   }
-  clip(r, per);
-  return true;
+  if (more) clip(x, per);
+  r = x;
+  __syncwarp();
+  return more;
 }
 // A unit that fits one query tile takes its key tiles alternately with both streams.
 __device__ __forceinline__ bool narrow(const AtArgs& a, const AtUnit& u) { return u.ntok <= a.tok_tile; }
@@ -359,8 +371,10 @@ struct AtCtl {
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t tail[C::kStages];  // of a stage that holds values to be cleared in part: its copies have landed
   uint64_t cfull[kCodes], cempty[kCodes], scfull[kScales], scready[kScales], scempty[kScales];
-  uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done;
+  uint64_t qfull, qempty, turn[2], sfull[2], phalf[2], pfull[2], ofull[2], mlfull, mlfree, done, again;
   uint32_t tmem;
+  uint32_t odd[C::kStages];  // second walk: bit q: rows 4 q .. 4 q + 3 of a stage's values hold any that is not finite
+  int bad, stop;             // a row wants the second walk; a warp has given up
   alignas(16) float2 ml[2][kAtRows];  // narrow units: the streams' references and sums of each row
   uint64_t per;        // places of a CTA
   AtRun run[C::kThreads / 32];  // each warp's place: read seldom, not worth registers
@@ -470,69 +484,6 @@ __device__ bool make_run(const AtArgs& a, const AtSeqs& q, AtScratch* sc, uint64
 
 // ------------------------------------------------------------------ results
 
-// E columns from `col` on (of each lane; none where col is D) of one row whose sum is finite and whose values are not:
-// over the rows that it sees, without those that a matrix product multiplies by 0, and with weights of 1 at most, whose
-// products do not pass fp32's range before they are divided by the sum.  By a warp, kRepair rows in flight.
-constexpr int kRepair = 8;
-template <int D, int E>
-__device__ __noinline__ void repair_row(const AtArgs& a, int s, int h, int64_t token, int head, int lo, int hi, float m,
-                                        float l, int col, float y[E]) {
-  constexpr int Q = D / 32;
-  const int lane = threadIdx.x & 31;
-  const Pages& p = a.pages;
-  const __nv_bfloat16* q = a.q + token * a.q_stride_tok + (int64_t)head * a.q_stride_head + lane * Q;
-  const int32_t* table = p.table + (int64_t)s * p.table_stride;
-  const float lse2 = m + log2f(l);
-  float qv[Q];
-#pragma unroll
-  for (int e = 0; e < Q; ++e) qv[e] = __bfloat162float(q[e]);
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int j0 = lo; j0 < hi; j0 += kRepair) {
-    float x[kRepair], v[kRepair][E];
-#pragma unroll
-    for (int f = 0; f < kRepair; ++f) {
-      const int j = min(j0 + f, hi - 1), at_page = a.by_page.quotient(j >> 4), in_page = j - at_page * p.page_rows;
-      const int page = table[at_page];
-      x[f] = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[f][e] = 0.f;
-      if (page_ok(p, page)) {
-        const int64_t at = page_elem(p, page, h, in_page);
-        if (p.k_scale) {
-          const int64_t slot = page_slot(p, page, h, in_page);
-          const int8_t* k = reinterpret_cast<const int8_t*>(p.k) + at + lane * Q;
-          const int8_t* vv = reinterpret_cast<const int8_t*>(p.v) + at;
-#pragma unroll
-          for (int e = 0; e < Q; ++e) x[f] = fmaf(qv[e], (float)k[e], x[f]);
-          x[f] *= p.k_scale[slot];
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (col + e < D) v[f][e] = (float)vv[col + e] * p.v_scale[slot];
-        } else {
-          const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(p.k) + at + lane * Q;
-          const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(p.v) + at;
-#pragma unroll
-          for (int e = 0; e < Q; ++e) x[f] = fmaf(qv[e], __bfloat162float(k[e]), x[f]);
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            if (col + e < D) v[f][e] = __bfloat162float(vv[col + e]);
-        }
-      }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int f = 0; f < kRepair; ++f) x[f] += __shfl_xor_sync(0xffffffffu, x[f], off);
-#pragma unroll
-    for (int f = 0; f < kRepair; ++f) {
-      if (j0 + f >= hi) continue;
-      const float w = fast_exp2(fmaf(x[f], a.scale_log2, -lse2));
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = fmaf(w, v[f][e], y[e]);
-    }
-  }
-}
 // A CTA's part of a unit that began before it lies in slot 2 x CTA, of one that begins in it in the next.  A slot holds
 // [D / 4][rows_cap] pieces of four columns, so that a warp's rows are next to one another.
 __device__ __forceinline__ int64_t part_slot(int cta, bool begins) { return 2 * (int64_t)cta + (begins ? 1 : 0); }
@@ -548,32 +499,48 @@ template <int D, int E>
 __device__ __forceinline__ void write_out(const AtArgs& a, int64_t token, int head, int col, const float* y) {
   if (a.part.out) {
     float* to = a.part.out + (token * a.h_q + head) * D + col;
-    if constexpr (E == 1) {
-      *to = y[0];
-    } else if constexpr (E == 2) {
-      *reinterpret_cast<float2*>(to) = make_float2(y[0], y[1]);
-    } else {
 #pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-    }
+    for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
     return;
   }
   __nv_bfloat16* to = a.out + token * a.out_stride_tok + (int64_t)head * a.out_stride_head + col;
-  if constexpr (E == 1) {
-    *to = __float2bfloat16_rn(y[0]);
-  } else if constexpr (E == 2) {
-    *reinterpret_cast<uint32_t*>(to) = pack2(y[0], y[1]);
-  } else if constexpr (E == 4) {
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-  } else {
 #pragma unroll
-    for (int e = 0; e < E; e += 8)
-      *reinterpret_cast<uint4*>(to + e) = make_uint4(pack2(y[e], y[e + 1]), pack2(y[e + 2], y[e + 3]),
-                                                     pack2(y[e + 4], y[e + 5]), pack2(y[e + 6], y[e + 7]));
-  }
+  for (int e = 0; e < E; e += 8)
+    *reinterpret_cast<uint4*>(to + e) = make_uint4(pack2(y[e], y[e + 1]), pack2(y[e + 2], y[e + 3]),
+                                                   pack2(y[e + 4], y[e + 5]), pack2(y[e + 6], y[e + 7]));
 }
 
 // ------------------------------------------------------------------ the attention
+
+// Adds the values of row `at` that are not finite (int8: NaN, where the scale is not) to O in a warp's TMEM lanes, of the
+// query rows that see it.
+template <int D, bool Q8>
+__device__ __forceinline__ void add_odd(const AtArgs& a, int s, int h, int at, bool sees, uint32_t o_cols) {
+  const Pages& p = a.pages;
+  const int at_page = a.by_page.quotient(at >> 4), in_page = at - at_page * p.page_rows;
+  const int page = (p.table + (int64_t)s * p.table_stride)[at_page];
+  if (!__all_sync(0xffffffffu, page_ok(p, page))) return;
+  const float scale = Q8 ? p.v_scale[page_slot(p, page, h, in_page)] : 0.f;
+  const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(p.v) + (Q8 ? 0 : page_elem(p, page, h, in_page));
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float x[16], o[16];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      x[e] = Q8 ? (finite(scale) ? 0.f : NAN) : __bfloat162float(v[c + e]);
+      any |= !finite(x[e]);
+    }
+    if (!__any_sync(0xffffffffu, any)) continue;
+    tmem_ld16(o_cols + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (sees && !finite(x[e])) o[e] += x[e];
+    tmem_st16(o_cols + c, o);
+    tmem_wait_st();
+  }
+}
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -607,6 +574,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     mbar_init(&ctl->mlfull, 8);
     mbar_init(&ctl->mlfree, 8);
     mbar_init(&ctl->done, 2);
+    mbar_init(&ctl->again, C::kThreads / 32);
+    ctl->bad = ctl->stop = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->sfull[i], 1);
       mbar_init(&ctl->turn[i], 1);
@@ -665,7 +634,27 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
   }
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-
+  if (any && tid == 0) a.start[blockIdx.x] = r;
+  __syncwarp();
+  // A warp's next unit.  Behind the last one all warps meet, and walk over the units a second time, with `clean` set, if
+  // any row of the first walk wants it
+  auto onward = [&](bool& clean) {
+    if (next_unit(a, r, ctl->per)) return true;
+    if (clean) return false;
+    if (lane == 0) mbar_arrive(&ctl->again);
+    if (!mbar_wait_warp(&ctl->again, 0, kAtLong) || !ctl->bad || ctl->stop) return false;
+    r = a.start[blockIdx.x];
+    __syncwarp();
+    return clean = true;
+  };
+  auto give_up = [&](bool clean) {
+    set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+    if (lane == 0 && !clean) {
+      ctl->stop = 1;
+      mbar_arrive(&ctl->again);
+    }
+    __syncwarp();
+  };
   if (warp >= kAtMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOther));
     if (warp == kAtLoad) {
@@ -677,8 +666,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       static_assert(kAtKeys == 128);
       const bool one = elect_one();
       uint32_t n = 0, tiles = 0;  // entries and key tiles so far
-      bool ok = true;
-      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+      bool ok = true, clean = false;
+      for (bool more = any; more && ok; more = ok && onward(clean)) {
         const int count = r.count;
         if (count == 0) continue;
         const bool nar = narrow(a, r.u);
@@ -746,8 +735,9 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             const uint32_t st = n % C::kStages;
             if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
             if (!ok) break;
-            // values behind the last row are cleared by another warp, which then says that the tile is there
-            uint64_t* bar = val && left < kAtKeys ? &ctl->tail[st] : &ctl->full[st];
+            // values behind the last row (in a second walk all that are not finite) are cleared by another warp, which
+            // then says that the tile is there
+            uint64_t* bar = val && (clean || left < kAtKeys) ? &ctl->tail[st] : &ctl->full[st];
             if (one) {
               mbar_arrive_expect_tx(bar, (uint32_t)((boxes << box_shift) * 2 * D));
               fence_proxy_async_smem();
@@ -769,7 +759,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       }
       if (!ok) {
         // the copies in flight land before the CTA's shared memory is another's
-        set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+        give_up(clean);
         constexpr uint32_t kRing = Q8 ? C::kCodeStages : C::kStages;
         uint64_t* bars = Q8 ? ctl->cfull : ctl->full;
         for (uint32_t f = n > kRing ? n - kRing : 0; f < n; ++f) (void)mbar_wait_warp(&bars[f % kRing], (f / kRing) & 1);
@@ -778,8 +768,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     } else if (warp == kAtAux) {
       // ---- queries, and the values behind a sequence's last row
       uint32_t units = 0, tails = 0, n = 0;  // tails: bit st is the parity of tail[st]
-      bool ok = true;
-      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+      bool ok = true, clean = false;
+      for (bool more = any; more && ok; more = ok && onward(clean)) {
         if (r.count == 0) continue;
         const bool nar = narrow(a, r.u);
         if (units > 0) ok = mbar_wait_warp(&ctl->qempty, (units - 1) & 1, kAtLong);
@@ -796,7 +786,41 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         __syncwarp();
         ++units;
         const int64_t last = (int64_t)(r.u.t0 + r.first + r.count) * kAtKeys;
-        if (!Q8 && last > r.u.rows) {
+        for (int pos = 0; !Q8 && clean && pos < 2 * r.count; ++pos) {
+          int j;
+          if (!entry_of(nar, r.count, pos, j)) continue;
+          const uint32_t st = (n + pos) % C::kStages;
+          ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
+          if (!ok) break;
+          tails ^= 1u << st;
+          uint8_t* tile = sm + C::kOffRing + st * C::kTile;
+          const int valid = min(r.u.rows - (r.u.t0 + r.first + j) * kAtKeys, kAtKeys);
+          uint32_t odd = 0;
+          for (int i = lane; i < kAtKeys * (D / 8); i += 32) {
+            const int row = i / (D / 8), rest = i % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(tile + (rest >> 3) * C::kSlab + row * 128 + (rest & 7) * 16);
+            uint4 x = *at;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            bool any_odd = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // (all ones in the exponent)
+              const uint32_t lo = (w[e] & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+              const uint32_t hi = (w[e] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u;
+              any_odd |= (lo | hi) != 0;
+              w[e] &= ~(lo | hi);
+            }
+            const bool behind = row >= valid;
+            if (behind || any_odd) *at = behind ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+            if (any_odd && !behind) odd |= 1u << (row >> 2);
+          }
+          odd = __reduce_or_sync(0xffffffffu, odd);
+          if (lane == 0) ctl->odd[st] = odd;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->full[st]);
+        }
+        if (!ok) break;
+        if (!Q8 && !clean && last > r.u.rows) {
           const uint32_t st = (n + 2 * r.count - 1) % C::kStages;  // a run's last entry
           ok = mbar_wait_warp(&ctl->tail[st], (tails >> st) & 1, kAtLong);
           if (!ok) break;
@@ -813,7 +837,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         }
         n += 2 * r.count;
       }
-      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      if (!ok) give_up(clean);
       if (units > 0) (void)mbar_wait_warp(&ctl->qfull, (units - 1) & 1);  // (landed)
     } else if (warp == kAtMma || warp == kAtMma + 1) {
       // ---- the MMAs of stream i: S of its first tile; then, tile by tile, O += P V and S of the next.  The whole warp
@@ -827,13 +851,13 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       const uint32_t ts = tm + kAtS + 128 * i, to = tm + kAtO + 128 * i, tp = ts;
       const bool one = elect_one();
       uint32_t units = 0, n = 0, p_it = 0, turns = 0;
-      bool ok = true;
+      bool ok = true, clean = false;
       // the streams issue in turns: one's burst of MMAs would otherwise slow the other's, and both softmaxes wait for both
       auto my_turn = [&] { return (i == 0 && turns == 0) || mbar_wait_warp(&ctl->turn[i], (turns - (i == 0)) & 1, kAtLong); };
       auto pass = [&] {
         if (one) mbar_arrive(&ctl->turn[1 - i]);
       };
-      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+      for (bool more = any; more && ok; more = ok && onward(clean)) {
         const int count = __shfl_sync(0xffffffffu, r.count, 0);
         if (count == 0) continue;
         const bool nar = __shfl_sync(0xffffffffu, (int)narrow(a, r.u), 0);
@@ -896,7 +920,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
 #pragma unroll
             for (int kk = 0; kk < kAtKeys / 32; ++kk) {
               const int at = half * (kAtKeys / 32) + kk;
-              umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0);
+              umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0 || clean);
             }
           };
           if (one) weigh(0, true);
@@ -923,16 +947,16 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         }
         n += 2 * count;
       }
-      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      if (!ok) give_up(clean);
       if (one) umma_commit(&ctl->done);  // nothing of the tensor cores' is left behind
       (void)mbar_wait_warp(&ctl->done, 0);
     } else if (Q8 && warp >= kAtWiden) {
       // ---- int8 codes become bf16 tiles, half a row to a thread; value rows behind the sequence's last are zeros
       uint32_t n = 0, tiles = 0;
-      bool ok = true;
+      bool ok = true, clean = false;
       const int row = (tid - kAtWiden * 32) & 127;
       const int half = (tid - kAtWiden * 32) >> 7;
-      for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+      for (bool more = any; more && ok; more = ok && onward(clean)) {
         if (r.count == 0) continue;
         const bool nar = narrow(a, r.u);
         for (int pos = 0; pos < 2 * r.count; ++pos, ++n) {
@@ -944,7 +968,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           float* scales = reinterpret_cast<float*>(sm + C::kOffScales) + sc * 4 * kAtKeys + row;
           if (!val) {
             // A key's scale takes the logits' factor along.  A value's that is not finite makes its row one of NaN: what a
-            // weight of 0 makes of that is mended as bf16 rows' is
+            // weight of 0 makes of that is mended as bf16 rows' is, by a second walk
             ok = mbar_wait_warp(&ctl->scfull[sc], ((tiles + j) / (Q8 ? C::kScaleStages : 1)) & 1, kAtLong);
             if (!ok) break;
             const float x = scales[half * kAtKeys];
@@ -963,6 +987,11 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           if (lane == 0) mbar_arrive(&ctl->cempty[cs]);
           if (n >= C::kStages) ok = mbar_wait_warp(&ctl->empty[st], (n / C::kStages + 1) & 1, kAtLong);
           if (!ok) break;
+          if (clean && val) {
+            uint32_t quads = __ballot_sync(0xffffffffu, bad), byte = 0;
+            for (int q = 0; q < 8; ++q) byte |= (quads >> (4 * q) & 15) ? 1u << q : 0u;
+            if (half == 0 && lane == 0) reinterpret_cast<uint8_t*>(&ctl->odd[st])[row >> 5] = (uint8_t)byte;
+          }
 #pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             const int c = half * (D / 32) + q;
@@ -971,7 +1000,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             uint4 hi = make_uint4(widen2_bf16(x[q].z, 0x4140u), widen2_bf16(x[q].z, 0x4342u), widen2_bf16(x[q].w, 0x4140u),
                                   widen2_bf16(x[q].w, 0x4342u));
             if (zero || bad) {
-              const uint32_t u = zero ? 0u : 0x7fc07fc0u;
+              const uint32_t u = zero || clean ? 0u : 0x7fc07fc0u;
               lo = hi = make_uint4(u, u, u, u);
             }
             uint8_t* slab = to + (c >> 2) * C::kSlab;
@@ -987,7 +1016,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         }
         tiles += r.count;
       }
-      if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      if (!ok) give_up(clean);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoft));
@@ -998,8 +1027,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     if (tid == 0) a.cut[blockIdx.x].parts = 0;  // (until a run says otherwise)
     const int tok = a.by_group.quotient(row), hh = row - tok * a.group;
     uint32_t it_s = 0, it_o = 0, joins = 0, tiles0 = 0;
-    bool ok = true;
-    for (bool more = any; more && ok; more = next_unit(a, r, ctl->per)) {
+    bool ok = true, clean = false;
+    for (bool more = any; more && ok; more = ok && onward(clean)) {
       const bool nar = narrow(a, r.u);
       const int my_tok = nar ? tok : tok + i * a.tok_tile;  // of the unit
       const bool valid = tok < a.tok_tile && my_tok < r.u.ntok;
@@ -1034,6 +1063,24 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           ok = mbar_wait_warp(&ctl->scready[sc], ((tiles0 + j) / C::kScaleStages) & 1, kAtLong);
           if (!ok) break;
         }
+        if (clean) {
+          // second walk: the tile's values that are not finite are zeros by now, and go to O here, to the rows that see them
+          const uint32_t e = 2 * tiles0 + (nar ? min(2 * j + 2, 2 * r.count - 1) : 2 * j + 1), st = e % C::kStages;
+          ok = mbar_wait_warp(&ctl->full[st], (e / C::kStages) & 1, kAtLong);
+          if (!ok) break;
+          if (it == 0) {
+            const float zero[16] = {};
+            for (int c = 0; c < D; c += 16) tmem_st16(tl + kAtO + 128 * i + c, zero);
+          }
+          for (uint32_t odd = ctl->odd[st]; odd; odd &= odd - 1)
+            for (int f = 0; f < 4; ++f) {
+              const int at = k0 + 4 * (__ffs(odd) - 1) + f;
+              const bool sees = valid && at >= lo && at < hi;
+              if (__any_sync(0xffffffffu, sees)) add_odd<D, Q8>(a, r.u.s, r.h, at, sees, tl + kAtO + 128 * i);
+            }
+          tmem_wait_st();
+          __syncwarp();
+        }
         if (!idle) {
           const bool masked = !__all_sync(0xffffffffu, lo <= k0 && hi - k0 >= kAtKeys);
           const int from = lo - k0;
@@ -1041,7 +1088,8 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           const float* ks = reinterpret_cast<const float*>(sm + C::kOffScales) + (sc * 4 + 2) * kAtKeys;
           // moves the reference to a maximum that passes it by more than the slack
           auto refer = [&](float top) {
-            const float mx = Q8 ? top : top * a.scale_log2;
+            // (a second walk's weights are 2^-40 of what they were)
+            const float mx = (Q8 ? top : top * a.scale_log2) + (clean ? 40.f : 0.f);
             if (__any_sync(0xffffffffu, valid && mx > m + kAtSlack)) {  // (what lies in rows without a query has no say)
               const float to = fmaxf(m, mx), f = fast_exp2(m - to);
               m = to;
@@ -1245,21 +1293,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           else
             write_lse(a, token, head, m, l);
         }
-        uint32_t rows = cut ? 0 : __ballot_sync(0xffffffffu, valid && bad && finite(l));
-        while (rows) {
-          const int from = __ffs(rows) - 1;
-          rows &= rows - 1;
-          const int64_t t = __shfl_sync(0xffffffffu, token, from);
-          const int hd = __shfl_sync(0xffffffffu, head, from), first = __shfl_sync(0xffffffffu, lo, from);
-          const int end = __shfl_sync(0xffffffffu, hi, from);
-          const float top = __shfl_sync(0xffffffffu, m, from), all = __shfl_sync(0xffffffffu, l, from);
-          for (int c = c0; c < c1; c += D / 2) {
-            float y[D / 64];
-            const int col = c + lane * (D / 64);
-            repair_row<D, D / 64>(a, r.u.s, r.h, t, hd, first, end, top, all, col, y);
-            write_out<D, D / 64>(a, t, hd, col, y);
-          }
-        }
+        if (valid && bad && finite(l)) ctl->bad = 1;
       }
       if (tid == 0 && r.first == 0) {
         const uint64_t per = ctl->per;
@@ -1278,7 +1312,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
         tc_fence_after();
       }
     }
-    if (!ok) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+    if (!ok) give_up(clean);
   }
   __syncwarp();
   tc_fence_before();
@@ -1375,23 +1409,20 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
       o[e] = l == 0.f ? 0.f : o[e] * inv;
       bad |= !finite(o[e]);
     }
+    if (bad && finite(l)) {  // sums of finite parts may pass fp32's range before they are divided
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+      for (int j = 0; j < cut.parts; ++j) {
+        const int64_t slot = part_slot(cut.c0 + j, j == 0) * a.rows_cap;
+        const float w = fast_exp2(a.part_ml[slot + rho].x - m) * inv;
+        const float4* from = reinterpret_cast<const float4*>(a.part_o + slot * D) + (int64_t)(col / 4) * a.rows_cap + rho;
+        const float4 x[2] = {from[0], from[a.rows_cap]};
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(reinterpret_cast<const float*>(x)[e], w, o[e]);
+      }
+    }
     if (valid) write_out<D, E>(a, token, head, col, o);
     if (valid && col == 0) write_lse(a, token, head, m, l);
-    uint32_t wrong = __ballot_sync(0xffffffffu, valid && bad && finite(l));
-    if (!wrong) continue;
-    const AtUnit u = unit_of(a, seqs_of(a), find_seq(a, seqs_of(a), cut.slot), cut.slot, a.range);
-    int lo, hi;
-    token_rows(a, u.rows, u.n, u.tok0 + my_tok, token, lo, hi);
-    while (wrong) {
-      const int from = __ffs(wrong) - 1;
-      wrong &= wrong - 1;
-      float y[1];
-      const int64_t t = __shfl_sync(0xffffffffu, token, from);
-      const int hd = __shfl_sync(0xffffffffu, head, from), c = lane < E ? col + lane : D;
-      repair_row<D, 1>(a, u.s, cut.h, t, hd, __shfl_sync(0xffffffffu, lo, from), __shfl_sync(0xffffffffu, hi, from),
-                       __shfl_sync(0xffffffffu, m, from), __shfl_sync(0xffffffffu, l, from), c, y);
-      if (lane < E) write_out<D, 1>(a, t, hd, c, y);
-    }
   }
 }
 
@@ -1521,7 +1552,8 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
   pl.grid = std::min(device_sms(), kAfThreads);
   pl.rows_cap = (int)std::min<int64_t>(2 * pl.tok_tile, std::max<int64_t>(p->num_tokens, 1)) * pl.g;
   pl.cut_off = kAtHeader;
-  pl.range_off = pl.cut_off + up256(sizeof(AtCut) * (size_t)pl.grid);
+  pl.start_off = pl.cut_off + up256(sizeof(AtCut) * (size_t)pl.grid);
+  pl.range_off = pl.start_off + up256(sizeof(AtRun) * (size_t)pl.grid);
   pl.ml_off = pl.range_off + (p->row_begin || p->row_end ? up256(sizeof(int2) * (size_t)pl.slots) : 0);
   pl.o_off = pl.ml_off + up256(sizeof(float2) * 2 * (size_t)pl.grid * pl.rows_cap);
   pl.total = pl.o_off + up256(sizeof(float) * 2 * (size_t)pl.grid * pl.rows_cap * pl.d);
@@ -1545,6 +1577,7 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.part = part;
   a.error = error;
   a.cut = reinterpret_cast<AtCut*>(ws + pl.cut_off);
+  a.start = reinterpret_cast<AtRun*>(ws + pl.start_off);
   a.range = p->row_begin || p->row_end ? reinterpret_cast<int2*>(ws + pl.range_off) : nullptr;
   a.part_ml = reinterpret_cast<float2*>(ws + pl.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + pl.o_off);

@@ -256,6 +256,43 @@ def test_values_that_are_not_finite_stay_in_their_column(A, value):
     assert np.all(np.abs(got - want)[~hit] <= tol[~hit])
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("where", ["all see it", "the last token sees it", "everywhere"])
+@pytest.mark.parametrize("lens", [[6000, 700], [300] * 40])
+def test_values_that_are_not_finite_cost_little(A, lens, where, int8):
+    # units in many parts and whole ones; what has to be formed again is formed by tiles as before: a few times as long
+    new = [200 if len(lens) == 2 else 9] * len(lens)
+    cache = P.build(A, lens, 4, 128, 64, seed=36, mass=False, order=False, int8=int8)
+    q = queries(sum(new), 28, 128, 36)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    good = P.host(cache)
+    want, _, size, spread = O.attend(q.double().cpu().numpy(), cu, good, 128 ** -0.5, True)
+    nan = torch.zeros(sum(new), dtype=torch.bool)
+    for s, n in enumerate(lens):
+        at = torch.arange(n, device="cuda") if where == "everywhere" else torch.tensor([70 if where == "all see it" else n - 1], device="cuda")
+        pg = cache.table[s].long()[at // 64]
+        if int8:
+            cache.v_scale[pg, 2, at % 64] = float("nan")
+        else:
+            cache.v[pg, at % 64, 2] = float("nan")
+        nan[int(cu[s + 1]) - 1 if where == "the last token sees it" else int(cu[s]):int(cu[s + 1])] = True
+    prob = A.PagedAttendProblem(q, cache, i32(cu.tolist()), causal=True)
+    ws = prob.new_workspace()
+    A.paged_attend(prob, ws)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    A.aircache_paged_attend(prob, ws)
+    end.record()
+    end.synchronize()
+    got = prob.out.double().cpu().numpy()
+    hit = nan[:, None].numpy() & (np.arange(28) // 7 == 2)[None]
+    assert np.all(np.isnan(got[hit]))
+    tol = (HALF + 2 * 128 * 2.0 ** -24 * size[..., None] + 2.0 ** -18) * spread + HALF * np.abs(want) + 1e-30  # (as in verify: the last, a weight
+    # under 2^-126, fp32's smallest, may be 0: at most 6,000 of them times values under 2^7 are 2^-106)
+    assert np.all(np.abs(got - want)[~hit] <= tol[~hit])
+    assert begin.elapsed_time(end) < 20  # ms (row by row it would be hundreds; by tiles it is a fraction of one)
+
+
 def test_int8_scales_that_are_not_finite(A):
     n, R = 40, 300
     cache = P.build(A, [R, R], 2, 128, 32, seed=18, mass=False, order=False, int8=True)
