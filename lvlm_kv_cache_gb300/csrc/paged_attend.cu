@@ -316,27 +316,30 @@ __device__ __forceinline__ void clip(AtRun& r, uint64_t per) {  // per: places o
   r.first = (int)(min(from, r.at + r.u.c) - r.at);
   r.count = to > from ? (int)(to - from) : 0;
 }
-// (`r` is the warp's: every lane reads it before any writes the same over it)
+// (`r` is the warp's: every lane reads before any writes the same over it)
 __device__ __forceinline__ bool next_unit(const AtArgs& a, AtRun& r, uint64_t per) {
   __syncwarp();
-  AtRun x = r;
+  const uint64_t at = r.at + r.u.c + kAtEnd;
+  const int h = r.h + 1, s0 = r.u.s;
+  int slot = r.slot;
   __syncwarp();
-  x.at += x.u.c + kAtEnd;
-  bool more = x.at < per * (blockIdx.x + 1);
-  if (more && ++x.h == a.pages.h_kv) {
-    x.h = 0;
+  if (at >= per * (blockIdx.x + 1)) return false;
+  if (h == a.pages.h_kv) {
+    AtUnit u;
+    int s = s0;
     do {
-      more = ++x.slot < a.slots;
-      if (!more) break;
-      int s = x.u.s;
-      while (s + 1 < a.pages.num_seqs && slot_base(a, a.cu[s + 1], s + 1) <= x.slot) ++s;
-      x.u = unit_of(a, seqs_of(a), s, x.slot, a.range);
-    } while (x.u.ntok == 0);
+      if (++slot >= a.slots) return false;
+      while (s + 1 < a.pages.num_seqs && slot_base(a, a.cu[s + 1], s + 1) <= slot) ++s;
+      u = unit_of(a, seqs_of(a), s, slot, a.range);
+    } while (u.ntok == 0);
+    r.u = u;
+    r.slot = slot;
   }
-  if (more) clip(x, per);
-  r = x;
+  r.h = h == a.pages.h_kv ? 0 : h;
+  r.at = at;
+  clip(r, per);
   __syncwarp();
-  return more;
+  return true;
 }
 // A unit that fits one query tile takes its key tiles alternately with both streams.
 __device__ __forceinline__ bool narrow(const AtArgs& a, const AtUnit& u) { return u.ntok <= a.tok_tile; }
