@@ -36,7 +36,7 @@
 //
 // int8 rows: eight more warps widen the codes, exactly, into the bf16 tiles.  The softmax threads multiply logits by the
 // keys' scales and weights by the values', which takes 64 logits at a time, twice (3,900 cycles to a tile); these rows are
-// bound by instructions (issue 49 %, tensor pipe 24 %).
+// bound by instructions (issue 47 %, tensor pipe 23 %).
 //
 // Weights that meet V are rounded once to bf16 (at most 2^-8 of each weight, independent of one another; the error of an
 // output against 64 bits goes from 0.0017 of its norm, its own rounding to bf16, to 0.0023).  A second product with what
@@ -50,7 +50,7 @@
 // row, a warp to an output row, they took 1,600 to 2,500 ms.
 //
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
-// 576 to 9,000 rows 577 to 625 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 153 to 169 us; one
+// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 157 to 167 us; one
 // token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats 16
 // to 17 us.
 #include <cuda_bf16.h>
