@@ -50,9 +50,9 @@
 // row, a warp to an output row, they took 1,600 to 2,500 ms.
 //
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
-// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 157 to 167 us; one
-// token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats 16
-// to 17 us.
+// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 152 us; one
+// token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats 15
+// us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1335,13 +1335,14 @@ __global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_c
   if (slot < a.slots) find_range(a, seqs_of(a), slot);
 }
 
-// Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and eight columns of them, a
-// row to a lane, eight parts in flight.
+// Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and E columns of them, a row
+// to a lane, N parts in flight.
 constexpr int kAfThreads = 256;
-constexpr int kAfCtas = 4;  // CTAs to an SM (one, where the next kernel is to start beside them)
-template <int D>
+// As many CTAs as an SM holds at once (four: four drafts of eight chats 16.7 us instead of 14.7), or one, where the next
+// kernel is to start beside them.
+constexpr int kAfCtas = 2;
+template <int D, int E, int N>
 __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_constant__ AtArgs a) {
-  constexpr int E = 8, N = 8;
   // (results that are a part of another call's: its next kernel is the call's own, and waits for them where it needs them)
   if (a.part.out) pdl_trigger();
   pdl_wait();
@@ -1375,15 +1376,15 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     for (int j0 = 0; j0 < cut.parts; j0 += N) {
       float2 ml[N];
-      float4 x[N][2];
+      float4 x[N][E / 4];
 #pragma unroll
       for (int f = 0; f < N; ++f) {
         const int j = min(j0 + f, cut.parts - 1);
         const int64_t slot = part_slot(cut.c0 + j, j == 0) * a.rows_cap;
         ml[f] = a.part_ml[slot + rho];
         const float4* from = reinterpret_cast<const float4*>(a.part_o + slot * D) + (int64_t)(col / 4) * a.rows_cap + rho;
-        x[f][0] = from[0];
-        x[f][1] = from[a.rows_cap];
+#pragma unroll
+        for (int e = 0; e < E / 4; ++e) x[f][e] = from[(int64_t)e * a.rows_cap];
       }
       float up = m;
 #pragma unroll
@@ -1419,9 +1420,14 @@ __global__ void __launch_bounds__(kAfThreads) attend_finish_kernel(const __grid_
         const int64_t slot = part_slot(cut.c0 + j, j == 0) * a.rows_cap;
         const float w = fast_exp2(a.part_ml[slot + rho].x - m) * inv;
         const float4* from = reinterpret_cast<const float4*>(a.part_o + slot * D) + (int64_t)(col / 4) * a.rows_cap + rho;
-        const float4 x[2] = {from[0], from[a.rows_cap]};
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(reinterpret_cast<const float*>(x)[e], w, o[e]);
+        for (int e = 0; e < E / 4; ++e) {
+          const float4 x = from[(int64_t)e * a.rows_cap];
+          o[4 * e] = fmaf(x.x, w, o[4 * e]);
+          o[4 * e + 1] = fmaf(x.y, w, o[4 * e + 1]);
+          o[4 * e + 2] = fmaf(x.z, w, o[4 * e + 2]);
+          o[4 * e + 3] = fmaf(x.w, w, o[4 * e + 3]);
+        }
       }
     }
     if (valid) write_out<D, E>(a, token, head, col, o);
@@ -1504,7 +1510,13 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
-  return launch_pdl(attend_finish_kernel<D>, dim3(a.part.out ? pl.grid : pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
+  // Few units (at most half as many as CTAs) have many parts each, of which many are in flight; with more, few parts, it is
+  // the pieces of work that are many, and larger.  (4 x 256 tokens over 12,544 rows, 128 units: 156 us with 8 columns and
+  // 8 parts, 152 with 16 and 3; four drafts of eight chats, 32 units: 14.7 and 15.6; 24 chats behind a prefix of
+  // 131,072, 4 units: 75 and 79)
+  const bool many = 2 * (int64_t)pl.slots * pl.pages.h_kv > pl.grid;
+  const auto join = many ? &attend_finish_kernel<D, 16, 3> : &attend_finish_kernel<D, 8, 8>;
+  return launch_pdl(join, dim3(a.part.out ? pl.grid : pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
              ? AIRCACHE_OK
              : AIRCACHE_ERR_CUDA;
 }
