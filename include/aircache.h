@@ -808,7 +808,7 @@ AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_
  *
  * The work is split by rows and tokens, whatever the lengths; a second kernel
  * joins what several CTAs did, in a fixed order (a third one before them where
- * row_begin or row_end is given).
+ * row_begin or row_end is given for many tokens).
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): dtype AIRCACHE_BF16; h_q a
  * multiple of h_kv (with at most 16 query heads to a KV head, else
  * AIRCACHE_ERR_UNSUPPORTED); scale > 0 and finite; q and out 16-byte aligned,

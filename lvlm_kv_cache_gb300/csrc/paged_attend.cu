@@ -50,9 +50,9 @@
 // row, a warp to an output row, they took 1,600 to 2,500 ms.
 //
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
-// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 152 us; one
-// token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats 15
-// us.
+// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 152 to 162 us;
+// one token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats
+// 15 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
