@@ -1074,6 +1074,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           if (it == 0) {
             const float zero[16] = {};
             for (int c = 0; c < D; c += 16) tmem_st16(tl + kAtO + 128 * i + c, zero);
+            tmem_wait_st();  // (add_odd reads these columns)
           }
           for (uint32_t odd = ctl->odd[st]; odd; odd &= odd - 1)
             for (int f = 0; f < 4; ++f) {

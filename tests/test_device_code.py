@@ -148,3 +148,15 @@ int main() {
     src.write_text(main)
     subprocess.run(["g++", "-O1", "-std=c++17", str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.strip() == "0"
+
+
+def test_the_second_walk_waits_for_the_columns_that_it_clears():
+    # tcgen05.ld is ordered behind an earlier tcgen05.st of the same columns by tcgen05.wait::st alone
+    text = source("paged_attend.cu")
+    walk = body(text, "if (clean) {")
+    cleared = body(walk, "if (it == 0) {")
+    assert cleared.index("tmem_st16(") < cleared.index("tmem_wait_st();")
+    assert walk.index("tmem_wait_st();") < walk.index("add_odd<")
+    # and what adds to them leaves them ready for the next that does
+    add = body(text, "void add_odd(")
+    assert add.index("tmem_st16(") < add.rindex("tmem_wait_st();")
