@@ -540,6 +540,7 @@ __device__ __forceinline__ void add_odd(const AtArgs& a, int s, int h, int at, b
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       if (sees && !finite(x[e])) o[e] += x[e];
+    __syncwarp();
     tmem_st16(o_cols + c, o);
     tmem_wait_st();
   }
@@ -1117,6 +1118,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->phalf[i]);
+            __syncwarp();
           };
           if constexpr (!Q8) {
             float v[kAtKeys];
@@ -1277,17 +1279,17 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) not_finite[e & 1] = fma2(o[e], zero2, not_finite[e & 1]);
-          if (!valid) continue;
-          if (cut) {
+          if (valid && cut) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2, to += a.rows_cap) *to = make_float4(o[e].x, o[e].y, o[e + 1].x, o[e + 1].y);
-          } else {
+          } else if (valid) {
             if (l == 0.f) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) o[e] = zero2;
             }
             write_out<D, 16>(a, token, head, c, reinterpret_cast<const float*>(o));
           }
+          __syncwarp();  // (tcgen05.ld and .st want the warp's lanes together)
         }
         not_finite[0] = add2(not_finite[0], not_finite[1]);
         const bool bad = not_finite[0].x + not_finite[0].y != 0.f && l != 0.f;

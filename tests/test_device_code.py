@@ -160,3 +160,14 @@ def test_the_second_walk_waits_for_the_columns_that_it_clears():
     # and what adds to them leaves them ready for the next that does
     add = body(text, "void add_odd(")
     assert add.index("tmem_st16(") < add.rindex("tmem_wait_st();")
+
+
+def test_lanes_meet_before_the_paged_attention_moves_tensor_memory():
+    # tcgen05.ld and .st are .sync.aligned: what lets a warp's lanes part in front of one is followed by __syncwarp
+    text = source("paged_attend.cu")
+    result = text[text.index("for (int c = c0; c < c1; c += 16) {"):]
+    loop = body(result, "for (int c = c0; c < c1; c += 16) {")
+    assert "continue;" not in loop and loop.strip().endswith("__syncwarp();")
+    assert body(text, "auto half_done = [&] {").strip().endswith("__syncwarp();")
+    add = body(text, "void add_odd(")
+    assert add.index("if (sees &&") < add.index("__syncwarp();") < add.index("tmem_st16(")
