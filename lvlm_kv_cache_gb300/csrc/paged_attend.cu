@@ -206,6 +206,13 @@ __device__ __forceinline__ void mask32(float v[32], int from, uint32_t wide, int
 #pragma unroll
   for (int c = 0; c < 32; ++c) v[c] = in >> c & 1 ? v[c] : -INFINITY;
 }
+// Arrives where `on` says so, without a branch: the lanes stay together.
+__device__ __forceinline__ void mbar_arrive_if(bool on, uint64_t* bar) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(
+                   smem_u32(bar)),
+               "r"((uint32_t)on)
+               : "memory");
+}
 // Arrives `n` times.
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
@@ -1117,8 +1124,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->phalf[i]);
-            __syncwarp();
+            mbar_arrive_if(lane == 0, &ctl->phalf[i]);
           };
           if constexpr (!Q8) {
             float v[kAtKeys];

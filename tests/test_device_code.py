@@ -163,11 +163,14 @@ def test_the_second_walk_waits_for_the_columns_that_it_clears():
 
 
 def test_lanes_meet_before_the_paged_attention_moves_tensor_memory():
-    # tcgen05.ld and .st are .sync.aligned: what lets a warp's lanes part in front of one is followed by __syncwarp
+    # tcgen05.ld and .st are .sync.aligned: what lets a warp's lanes part in front of one is followed by __syncwarp, or
+    # is an instruction under a predicate instead of a branch
     text = source("paged_attend.cu")
     result = text[text.index("for (int c = c0; c < c1; c += 16) {"):]
     loop = body(result, "for (int c = c0; c < c1; c += 16) {")
     assert "continue;" not in loop and loop.strip().endswith("__syncwarp();")
-    assert body(text, "auto half_done = [&] {").strip().endswith("__syncwarp();")
+    half_done = body(text, "auto half_done = [&] {")
+    assert "if (" not in half_done and "mbar_arrive_if(lane == 0," in half_done
+    assert "@p mbarrier.arrive" in body(text, "void mbar_arrive_if(")
     add = body(text, "void add_odd(")
     assert add.index("if (sees &&") < add.index("__syncwarp();") < add.index("tmem_st16(")
