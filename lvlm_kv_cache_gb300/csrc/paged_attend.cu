@@ -1257,6 +1257,10 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
       }
       if (!idle) {
         const bool cut = r.count < r.u.c;
+        // A row that sees none of the run's keys has the result 0 whatever their values are: a weight of 0 times one that is
+        // not finite has made its O NaN, which a join would take along
+        const int row0 = (r.u.t0 + r.first) * kAtKeys;
+        const bool blind = hi <= row0 || lo - row0 >= r.count * kAtKeys;
         const int64_t slot = part_slot(blockIdx.x, r.first == 0) * a.rows_cap;
         const int rho = my_tok * a.group + hh;
         if (!cut) {
@@ -1285,20 +1289,21 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) not_finite[e & 1] = fma2(o[e], zero2, not_finite[e & 1]);
+          if (blind || (!cut && l == 0.f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = zero2;
+          }
           if (valid && cut) {
 #pragma unroll
             for (int e = 0; e < 8; e += 2, to += a.rows_cap) *to = make_float4(o[e].x, o[e].y, o[e + 1].x, o[e + 1].y);
           } else if (valid) {
-            if (l == 0.f) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = zero2;
-            }
             write_out<D, 16>(a, token, head, c, reinterpret_cast<const float*>(o));
           }
           __syncwarp();  // (tcgen05.ld and .st want the warp's lanes together)
         }
         not_finite[0] = add2(not_finite[0], not_finite[1]);
-        const bool bad = not_finite[0].x + not_finite[0].y != 0.f && l != 0.f;
+        // (a part without a sum, whose logits are all minus infinity, is of a row that others may have given one)
+        const bool bad = not_finite[0].x + not_finite[0].y != 0.f && !blind && (cut || l != 0.f);
         if (valid && c0 == 0) {
           if (cut)
             a.part_ml[slot + rho] = make_float2(m, l);
