@@ -92,7 +92,8 @@ struct PdCfg {
 constexpr int ctas_per_sm(bool q8, int group) { return q8 && group <= 8 ? 3 : 2; }
 
 // A query head's result under the reference m and the sum l next to what it joins: factors of the two, and the
-// log-sum-exp in base 2 (-inf: no rows).
+// log-sum-exp in base 2 (-inf: no rows).  prior < 0: there is no prior result.  (One whose factor is 0 takes part: 0
+// times what is not finite is NaN, as for a row whose weight is 0.)
 struct Joint {
   float own, prior, lse2;
 };
@@ -145,7 +146,7 @@ __device__ __forceinline__ int rows_of(const Pages& p, int s) {
 // `head` of the batch's S * h_q.  Without a prior result there is nothing to form (own = 1).
 __device__ __forceinline__ Joint joint(const PdArgs& a, int64_t head, float m, float l) {
   prior_wait();
-  Joint j = {1.f, 0.f, l == 0.f ? -INFINITY : m + log2f(l)};
+  Joint j = {1.f, -1.f, l == 0.f ? -INFINITY : m + log2f(l)};
   if (head >= (int64_t)*a.prior.from * a.h_q && head < (int64_t)*a.prior.num * a.h_q) {
     const float p = a.prior.lse2[head];
     if (p != -INFINITY) {
@@ -162,7 +163,7 @@ __device__ __forceinline__ Joint joint(const PdArgs& a, int64_t head, float m, f
 template <int D>
 __device__ __forceinline__ float4 join_prior(const PdArgs& a, const Joint& j, int64_t head, int d, float4 y) {
   y.x *= j.own, y.y *= j.own, y.z *= j.own, y.w *= j.own;
-  if (j.prior != 0.f) {
+  if (!(j.prior < 0.f)) {
     const float4 p = *reinterpret_cast<const float4*>(a.prior.out + head * D + d);
     y.x = fmaf(p.x, j.prior, y.x);
     y.y = fmaf(p.y, j.prior, y.y);
