@@ -813,8 +813,9 @@ AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_
  * multiple of h_kv (with at most 16 query heads to a KV head, else
  * AIRCACHE_ERR_UNSUPPORTED); scale > 0 and finite; q and out 16-byte aligned,
  * integers and lse 4-byte; strides positive multiples of 8 elements, those of out such
- * that no two of its rows meet; out and lse apart from one another, q and the
- * cache (from the whole range that each spans).  Workspace as for aircache_paged_decode.
+ * that no two of its rows meet; out and lse apart from one another, q, the call's
+ * integers and the cache's keys, values, scales, table and lengths (from the whole range
+ * that each spans, its last page's rows among it).  Workspace as for aircache_paged_decode.
  */
 typedef struct aircache_paged_attend_problem {
     const aircache_pages* pages;  /* HOST */

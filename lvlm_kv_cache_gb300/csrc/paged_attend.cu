@@ -1556,19 +1556,19 @@ int attend_plan(const aircache_paged_attend_problem* p, bool part, AttendPlan& p
     const bool many_t = p->num_tokens > 1, many_h = p->h_q > 1;
     if ((many_t && st < d) || (many_h && sh < d)) return AIRCACHE_ERR_INVALID_ARG;
     if (many_t && many_h) {
-      const int64_t heads = (p->h_q - 1) * sh + d, toks = (p->num_tokens - 1) * st + d;
+      const __int128 heads = (__int128)(p->h_q - 1) * sh + d, toks = (__int128)(p->num_tokens - 1) * st + d;
       if (st < heads && sh < toks) return AIRCACHE_ERR_INVALID_ARG;
     }
-    auto bytes = [&](int64_t stride_t, int64_t stride_h) {
-      return (size_t)2 * ((p->num_tokens > 0 ? p->num_tokens - 1 : 0) * stride_t + (p->h_q - 1) * stride_h + d);
+    // (without a token nothing is written)
+    const int64_t T = p->num_tokens, H = p->h_q;
+    const size_t nq = span_bytes(p->q, {{T, p->q_stride_tok}, {H, p->q_stride_head}}, d, 2);
+    const size_t no = span_bytes(p->out, {{T, st}, {H, sh}}, d, 2), nl = p->lse ? span_bytes(p->lse, {{T, H}}, H, 4) : 0;
+    auto meets = [&](const void* x, size_t n) {
+      return arrays_meet(x, n, p->q, nq) || meets_cache(p->pages, pl.pages, x, n) ||
+             arrays_meet(x, n, p->cu_tokens, 4 * ((size_t)p->pages->num_seqs + 1)) ||
+             arrays_meet(x, n, p->row_begin, 4 * (size_t)T) || arrays_meet(x, n, p->row_end, 4 * (size_t)T);
     };
-    const size_t nq = bytes(many_t ? p->q_stride_tok : 0, many_h ? p->q_stride_head : 0);
-    const size_t no = bytes(many_t ? st : 0, many_h ? sh : 0), nl = 4 * (size_t)p->num_tokens * p->h_q;
-    // (keys and values to the last page, at least)
-    const size_t nk = (p->pages->kv_dtype == AIRCACHE_INT8 ? 1 : 2) * (size_t)(pl.pages.num_pages - 1) * pl.pages.stride_page;
-    if (arrays_meet(p->out, no, p->q, nq) || arrays_meet(p->out, no, pl.pages.k, nk) ||
-        arrays_meet(p->out, no, pl.pages.v, nk) || arrays_meet(p->lse, nl, p->out, no) || arrays_meet(p->lse, nl, p->q, nq) ||
-        arrays_meet(p->lse, nl, pl.pages.k, nk) || arrays_meet(p->lse, nl, pl.pages.v, nk))
+    if (T > 0 && (meets(p->out, no) || meets(p->lse, nl) || arrays_meet(p->lse, nl, p->out, no)))
       return AIRCACHE_ERR_INVALID_ARG;
   }
   pl.d = d;

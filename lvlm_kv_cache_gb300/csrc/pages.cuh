@@ -4,6 +4,9 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "internal.cuh"
 #include "ptx.cuh"
 
@@ -88,7 +91,34 @@ inline int check_pages(const aircache_pages* p, Pages& d) {
 // Host: whether two arrays of `bytes` and `other` bytes share any.
 inline bool arrays_meet(const void* x, size_t bytes, const void* y, size_t other) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  return x && y && a < b + other && b < a + bytes;
+  return x && y && bytes > 0 && other > 0 && a < b + other && b < a + bytes;
+}
+// Host: the bytes from an array's first element to the end of its last, `count` of each axis `stride` elements apart;
+// as many as addresses go on for where that passes them.
+struct Axis {
+  int64_t count, stride;
+};
+inline size_t span_bytes(const void* base, std::initializer_list<Axis> axes, int64_t inner, size_t size) {
+  unsigned __int128 n = inner;
+  for (const Axis& a : axes) {
+    if (a.count <= 0) return 0;
+    if (a.count > 1) n += (unsigned __int128)(a.count - 1) * (uint64_t)a.stride;
+  }
+  return (size_t)std::min<unsigned __int128>(n * size, SIZE_MAX - reinterpret_cast<uintptr_t>(base));
+}
+// Host: whether an array shares any byte with what the cache's keys, values, scales, table or lengths span.
+inline bool meets_cache(const aircache_pages* p, const Pages& d, const void* x, size_t bytes) {
+  const bool q8 = p->kv_dtype == AIRCACHE_INT8;
+  auto rows = [&](const void* base) {
+    return span_bytes(base, {{d.num_pages, d.stride_page}, {d.page_rows, d.stride_row}, {d.h_kv, d.stride_head}},
+                      p->head_dim, q8 ? 1 : 2);
+  };
+  const int64_t slots = (int64_t)d.h_kv * d.page_rows;
+  auto scales = [&](const void* base) { return span_bytes(base, {{d.num_pages, slots}}, slots, 4); };
+  return arrays_meet(x, bytes, d.k, rows(d.k)) || arrays_meet(x, bytes, d.v, rows(d.v)) ||
+         arrays_meet(x, bytes, d.k_scale, scales(d.k_scale)) || arrays_meet(x, bytes, d.v_scale, scales(d.v_scale)) ||
+         arrays_meet(x, bytes, d.table, span_bytes(d.table, {{d.num_seqs, d.table_stride}}, p->max_pages, 4)) ||
+         arrays_meet(x, bytes, d.lens, 4 * (size_t)d.num_seqs);
 }
 // Host: the bytes of an array of the mass's and the order's shape.
 inline size_t slot_bytes(const Pages& p) { return 4 * (size_t)p.num_pages * p.h_kv * p.page_rows; }
