@@ -27,6 +27,36 @@ struct SdPlan {
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Whether an output lies on another, or on what the step reads.  (mass_out may be the own rows' mass, and lie on the
+// prefixes', which may be of the same pool: they are neither read nor written.)
+bool outputs_meet(const aircache_shared_decode_problem* p) {
+  const aircache_paged_decode_problem& o = p->own;
+  Pages own, prefix;
+  const bool shared = p->prefix->num_seqs > 0 && check_pages(p->prefix, prefix) == AIRCACHE_OK;
+  if (check_pages(o.pages, own) != AIRCACHE_OK || own.num_seqs == 0) return false;
+  const int64_t S = own.num_seqs, H = o.h_q, d = o.pages->head_dim;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } outs[3] = {{o.out, span_bytes(o.out, {{S, H * d}}, H * d, 2)},
+               {o.lse, span_bytes(o.lse, {{S, H}}, H, 4)},
+               {o.mass_out, o.mass_out ? slot_bytes(own) : 0}};
+  const size_t nq = span_bytes(o.q, {{S, o.q_stride_seq}, {H, o.q_stride_head}}, d, 2);
+  for (int i = 0; i < 3; ++i) {
+    const void* x = outs[i].at;
+    const size_t n = outs[i].bytes;
+    if (!x) continue;
+    for (int j = 0; j < i; ++j)
+      if (arrays_meet(x, n, outs[j].at, outs[j].bytes)) return true;
+    if (arrays_meet(x, n, o.q, nq) || meets_cache(o.pages, own, x, n) ||
+        (shared && (meets_cache(p->prefix, prefix, x, n) ||
+                    arrays_meet(x, n, p->cu_seqs, 4 * ((size_t)prefix.num_seqs + 1)))) ||
+        (i < 2 && o.mass_out && arrays_meet(x, n, own.mass, slot_bytes(own))))
+      return true;
+  }
+  return false;
+}
+
 int sd_plan(const aircache_shared_decode_problem* p, SdPlan& pl) {
   if (!p || !p->prefix) return AIRCACHE_ERR_INVALID_ARG;
   size_t own = 0;
@@ -36,6 +66,7 @@ int sd_plan(const aircache_shared_decode_problem* p, SdPlan& pl) {
   if (p->prefix->h_kv != o->h_kv || p->prefix->head_dim != o->head_dim) return AIRCACHE_ERR_INVALID_ARG;
   pl.attend_off = up256(own);
   pl.total = pl.attend_off;
+  if (outputs_meet(p)) return AIRCACHE_ERR_INVALID_ARG;
   if (p->prefix->num_seqs == 0) return AIRCACHE_OK;  // (its arrays have no elements, and need no address)
   pl.at = aircache_paged_attend_problem{};
   pl.at.pages = p->prefix;
