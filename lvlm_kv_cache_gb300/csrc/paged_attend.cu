@@ -653,7 +653,9 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     if (next_unit(a, r, ctl->per)) return true;
     if (clean) return false;
     if (lane == 0) mbar_arrive(&ctl->again);
-    if (!mbar_wait_warp(&ctl->again, 0, kAtLong) || !ctl->bad || ctl->stop) return false;
+    const bool met = mbar_wait_warp(&ctl->again, 0, kAtLong);
+    if (!met) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+    if (!met || !ctl->bad || ctl->stop) return false;
     r = a.start[blockIdx.x];
     __syncwarp();
     return clean = true;

@@ -174,3 +174,10 @@ def test_lanes_meet_before_the_paged_attention_moves_tensor_memory():
     assert "@p mbarrier.arrive" in body(text, "void mbar_arrive_if(")
     add = body(text, "void add_odd(")
     assert add.index("if (sees &&") < add.index("__syncwarp();") < add.index("tmem_st16(")
+
+
+def test_a_warp_that_the_others_do_not_meet_says_so():
+    # without the second walk outputs are left as the first made them: that is an error, not a result
+    onward = body(source("paged_attend.cu"), "auto onward = [&](bool& clean) {")
+    assert "if (!met) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);" in onward
+    assert onward.index("set_error") < onward.index("return false;", onward.index("met ="))
