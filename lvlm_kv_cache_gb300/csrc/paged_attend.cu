@@ -56,6 +56,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstring>
@@ -1510,10 +1511,15 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   if (a.range && a.ranged && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
                             dim3(kArThreads), 0, s, a) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
-  static const int regs = [] {  // what the warps share out between them is what the launch brings
+  static std::atomic<int> known{0};  // registers that the built kernel has; what a failed query says is not kept
+  int regs = known.load(std::memory_order_relaxed);
+  if (regs == 0) {
     cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>)) == cudaSuccess ? f.numRegs : 0;
-  }();
+    if (cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>)) != cudaSuccess)
+      return AIRCACHE_ERR_CUDA;
+    known.store(regs = f.numRegs, std::memory_order_relaxed);
+  }
+  // (what the warps share out between them is what the launch brings)
   if (regs < C::kRegs) return AIRCACHE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pl.grid);

@@ -181,3 +181,11 @@ def test_a_warp_that_the_others_do_not_meet_says_so():
     onward = body(source("paged_attend.cu"), "auto onward = [&](bool& clean) {")
     assert "if (!met) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);" in onward
     assert onward.index("set_error") < onward.index("return false;", onward.index("met ="))
+
+
+def test_a_failed_query_of_a_kernel_is_asked_again():
+    # a static that takes its value from the first call alone would refuse every later one
+    text = source("paged_attend.cu")
+    assert "static const int regs" not in text
+    query = body(text, "if (regs == 0) {")
+    assert query.index("return AIRCACHE_ERR_CUDA;") < query.index("known.store(")
