@@ -654,9 +654,11 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
     if (next_unit(a, r, ctl->per)) return true;
     if (clean) return false;
     if (lane == 0) mbar_arrive(&ctl->again);
-    const bool met = mbar_wait_warp(&ctl->again, 0, kAtLong);
-    if (!met) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
-    if (!met || !ctl->bad || ctl->stop) return false;
+    if (!mbar_wait_warp(&ctl->again, 0, kAtLong)) {
+      set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+    if (!ctl->bad || ctl->stop) return false;
     r = a.start[blockIdx.x];
     __syncwarp();
     return clean = true;

@@ -179,8 +179,7 @@ def test_lanes_meet_before_the_paged_attention_moves_tensor_memory():
 def test_a_warp_that_the_others_do_not_meet_says_so():
     # without the second walk outputs are left as the first made them: that is an error, not a result
     onward = body(source("paged_attend.cu"), "auto onward = [&](bool& clean) {")
-    assert "if (!met) set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);" in onward
-    assert onward.index("set_error") < onward.index("return false;", onward.index("met ="))
+    assert "set_error(a.error, AIRCACHE_ERR_DEVICE_TIMEOUT);" in body(onward, "if (!mbar_wait_warp(&ctl->again")
 
 
 def test_a_failed_query_of_a_kernel_is_asked_again():
