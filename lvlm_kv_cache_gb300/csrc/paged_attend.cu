@@ -131,8 +131,6 @@ struct AtArgs {
   const int32_t* cu;
   const int32_t* row_begin;
   const int32_t* row_end;
-  const __nv_bfloat16* q;
-  int64_t q_stride_tok, q_stride_head;
   __nv_bfloat16* out;
   int64_t out_stride_tok, out_stride_head;
   float* lse;
@@ -1606,9 +1604,6 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.cu = p->cu_tokens;
   a.row_begin = p->row_begin;
   a.row_end = p->row_end;
-  a.q = static_cast<const __nv_bfloat16*>(p->q);
-  a.q_stride_tok = p->q_stride_tok;
-  a.q_stride_head = p->q_stride_head;
   a.out = static_cast<__nv_bfloat16*>(p->out);
   a.out_stride_tok = p->out_stride_tok;
   a.out_stride_head = p->out_stride_head;
