@@ -794,7 +794,9 @@ AIRCACHE_API int aircache_evict(const aircache_evict_problem* p, void* ws, size_
  * of whose logits lie below fp32's range; a NaN, an infinite key or value or a
  * logit above the range makes what sees it NaN or infinite, and nothing else.
  * Logits, sums and lse are fp32; the weights that meet V are rounded once, to
- * bf16.  out is bf16, lse fp32 dense [num_tokens][h_q].
+ * bf16 (int8 rows' with the value's scale), 2^-8 of each at most: out may differ by
+ * that of sum_j w_j |v_j| from a form that holds 24 bits, and usually does by about as
+ * much as its own rounding to bf16.  out is bf16, lse fp32 dense [num_tokens][h_q].
  *
  * Tokens cu_tokens[s] .. cu_tokens[s+1]-1 belong to sequence s (a sequence may
  * have none); tokens at or behind cu_tokens[num_seqs] are padding, whose outputs
@@ -856,7 +858,8 @@ AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, v
  * grows by their weights in the joint softmax.  The prefixes' mass is neither
  * read nor written.  Own rows and prefixes may be of different kv_dtype and
  * page_rows, and their pages of one pool; prefixes need not be in different pages.
- * The weights of the prefixes' rows are rounded as aircache_paged_attend's.
+ * The weights of the prefixes' rows that meet V are held in 16 bits (a sum of two bf16),
+ * whatever their kv_dtype.
  *
  * Device-side, AIRCACHE_ERR_DEVICE_BOUNDS is also set by a prefix's length or
  * page out of bounds (it then counts as empty; a bad page's rows read as zeros) and

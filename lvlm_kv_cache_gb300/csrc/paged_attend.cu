@@ -39,9 +39,11 @@
 // bound by instructions (issue 47 %, tensor pipe 23 %).
 //
 // Weights that meet V are rounded once to bf16 (at most 2^-8 of each weight, independent of one another; the error of an
-// output against 64 bits goes from 0.0017 of its norm, its own rounding to bf16, to 0.0023).  A second product with what
-// rounding takes away, as the decode kernel's, would be half as much again for the tensor cores.  Logits, maximum, sum, O,
-// parts and the joins are fp32.
+// output against 64 bits goes from 0.0017 of its norm, its own rounding to bf16, to 0.0023).  For the prefixes of a shared
+// decode (FINE) they are a sum of two bf16, 16 bits, as in the decode step that it stands in for (error 0.0017): what the
+// first leaves takes the rest of S's columns and a second product.  That is half as much again of P V for the tensor
+// cores: 4 x 256 tokens over 12,544 rows would take 205 us instead of 161, a chunk of 1,000 tokens over 130,000 rows 1,895
+// instead of 1,440.  Logits, maximum, sum, O, parts and the joins are fp32.
 //
 // A weight of 0 does not hide a NaN or an infinity in V from a matrix product.  A CTA that finds an output that is not
 // finite while its sum is walks over its units a second time: values that are not finite are cleared before the product
@@ -228,6 +230,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// What is left of two weights when the bf16 pair `w` has been taken away, as bf16 again.
+__device__ __forceinline__ uint32_t rest2(float2 e, uint32_t w) {
+  const float2 r = fma2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), make_float2(-1.f, -1.f), e);
+  return pack2(r.x, r.y);
 }
 
 // ------------------------------------------------------------------ the line of units
@@ -552,7 +560,8 @@ __device__ __forceinline__ void add_odd(const AtArgs& a, int s, int h, int at, b
   }
 }
 
-template <int D, bool Q8>
+// FINE: weights meet V as a sum of two bf16, those of 64 keys in 32 columns each.
+template <int D, bool Q8, bool FINE>
 __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel(const __grid_constant__ CUtensorMap qmap,
                                                                      const __grid_constant__ CUtensorMap kmap,
                                                                      const __grid_constant__ CUtensorMap vmap,
@@ -934,7 +943,9 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
 #pragma unroll
             for (int kk = 0; kk < kAtKeys / 32; ++kk) {
               const int at = half * (kAtKeys / 32) + kk;
-              umma_bf16_ts(to, tp + 8 * at, vd + (at * 16 * 128 >> 4), id_o, !first || it > 0 || kk > 0 || clean);
+              umma_bf16_ts(to, tp + (FINE ? 64 * half + 8 * kk : 8 * at), vd + (at * 16 * 128 >> 4), id_o,
+                           !first || it > 0 || kk > 0 || clean);
+              if constexpr (FINE) umma_bf16_ts(to, tp + 64 * half + 32 + 8 * kk, vd + (at * 16 * 128 >> 4), id_o, 1);
             }
           };
           if (one) weigh(0, true);
@@ -1149,15 +1160,17 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
             const float2 ref2 = make_float2(-m, -m);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t w[32];
+              uint32_t w[32], z[FINE ? 32 : 1];
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
                 const float2 x = fma2(make_float2(v[64 * half + 2 * c], v[64 * half + 2 * c + 1]), scale2, ref2);
                 const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                 sum[c & 1] = add2(sum[c & 1], e);
                 w[c] = pack2(e.x, e.y);
+                if constexpr (FINE) z[c] = rest2(e, w[c]);
               }
-              tmem_st32(tp + 32 * half, reinterpret_cast<const float*>(w));
+              tmem_st32(tp + (FINE ? 64 : 32) * half, reinterpret_cast<const float*>(w));
+              if constexpr (FINE) tmem_st32(tp + 64 * half + 32, reinterpret_cast<const float*>(z));
               if (half == 0) half_done();
             }
           } else {
@@ -1198,7 +1211,7 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
               tmem_ld32(ts + h, v);
               tmem_ld32(ts + h + 32, v + 32);
               tmem_wait_ld();
-              uint32_t w[32];
+              uint32_t w[32], z[FINE ? 32 : 1];
 #pragma unroll
               for (int e = 0; e < 64; e += 4) {
                 const float4 v4 = *reinterpret_cast<const float4*>(ks + kAtKeys + h + e);
@@ -1211,8 +1224,10 @@ __global__ void __launch_bounds__(AtCfg<D, Q8>::kThreads, 1) paged_attend_kernel
                 y = mul2(y, make_float2(v4.z, v4.w));
                 w[e / 2] = pack2(x.x, x.y);
                 w[e / 2 + 1] = pack2(y.x, y.y);
+                if constexpr (FINE) z[e / 2] = rest2(x, w[e / 2]), z[e / 2 + 1] = rest2(y, w[e / 2 + 1]);
               }
-              tmem_st32(tp + h / 2, reinterpret_cast<const float*>(w));
+              tmem_st32(tp + (FINE ? h : h / 2), reinterpret_cast<const float*>(w));
+              if constexpr (FINE) tmem_st32(tp + h + 32, reinterpret_cast<const float*>(z));
               if (h == 0) half_done();
             }
           }
@@ -1499,7 +1514,7 @@ bool encode_q(CUtensorMap* m, const aircache_paged_attend_problem* p, const Atte
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, bool FINE>
 int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AtArgs& a, cudaStream_t s) {
   using C = AtCfg<D, Q8>;
   CUtensorMap qm, km, vm;
@@ -1507,7 +1522,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
     return AIRCACHE_ERR_UNSUPPORTED;
   constexpr int smem = C::kOffCtl + (int)sizeof(AtCtl<D, Q8>);
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-  if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (allow_smem(reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8, FINE>), smem) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   if (a.range && a.ranged && launch_pdl(attend_range_kernel, dim3((a.slots + kArThreads / 32 - 1) / (kArThreads / 32)),
                             dim3(kArThreads), 0, s, a) != cudaSuccess)
     return AIRCACHE_ERR_CUDA;
@@ -1515,7 +1530,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   int regs = known.load(std::memory_order_relaxed);
   if (regs == 0) {
     cudaFuncAttributes f;
-    if (cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8>)) != cudaSuccess)
+    if (cudaFuncGetAttributes(&f, reinterpret_cast<const void*>(&paged_attend_kernel<D, Q8, FINE>)) != cudaSuccess)
       return AIRCACHE_ERR_CUDA;
     known.store(regs = f.numRegs, std::memory_order_relaxed);
   }
@@ -1531,7 +1546,7 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8, FINE>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   // Few units (at most half as many as CTAs) have many parts each, of which many are in flight; with more, few parts, it is
   // the pieces of work that are many, and larger.  (4 x 256 tokens over 12,544 rows, 128 units: 156 us with 8 columns and
   // 8 parts, 152 with 16 and 3; four drafts of eight chats, 32 units: 14.7 and 15.6; 24 chats behind a prefix of
@@ -1541,6 +1556,12 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   return launch_pdl(join, dim3(a.part.out ? pl.grid : pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess
              ? AIRCACHE_OK
              : AIRCACHE_ERR_CUDA;
+}
+
+template <bool FINE>
+int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, const AtArgs& a, cudaStream_t s) {
+  if (pl.q8) return pl.d == 128 ? launch_at<128, true, FINE>(p, pl, a, s) : launch_at<64, true, FINE>(p, pl, a, s);
+  return pl.d == 128 ? launch_at<128, false, FINE>(p, pl, a, s) : launch_at<64, false, FINE>(p, pl, a, s);
 }
 
 }  // namespace
@@ -1633,8 +1654,8 @@ int attend_launch(const aircache_paged_attend_problem* p, const AttendPlan& pl, 
   a.box_shift = 0;
   while ((1 << a.box_shift) < box_rows(pl.pages.page_rows)) ++a.box_shift;
   a.scale_log2 = (float)(1.4426950408889634 * (double)p->scale);
-  if (pl.q8) return pl.d == 128 ? launch_at<128, true>(p, pl, a, s) : launch_at<64, true>(p, pl, a, s);
-  return pl.d == 128 ? launch_at<128, false>(p, pl, a, s) : launch_at<64, false>(p, pl, a, s);
+  if (part.out) return launch_at<true>(p, pl, a, s);
+  return launch_at<false>(p, pl, a, s);
 }
 
 }  // namespace aircache

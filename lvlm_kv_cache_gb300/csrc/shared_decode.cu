@@ -8,12 +8,15 @@
 // where it writes its outputs, log-sum-exps and mass.
 //
 // Bound by HBM in the decode step, by launches and the chain of loads between four kernels in small calls.  The prefix
-// is not left to run beside the own rows: with half of the SMs to each, 64 sequences took 61 to 72 us instead of 60, as
+// is not left to run beside the own rows: with half of the SMs to each, 64 sequences took up to a fifth longer, as
 // the decode step wants all of them.  Its kernels start early instead (programmatic launch), and only its joins wait.
 //
+// The weights of a prefix's rows hold 16 bits, as the decode step's own (a sum of two bf16; one alone would take 17, 60 and
+// 75 us below, and leave outputs 0.0019 to 0.0025 of their norm from the decode step's instead of 0.0002).
+//
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 8 sequences with up to 64 own rows behind one
-// prefix of 2,048 17 us; 64 with 100 to 2,000 behind one of 16,384 60 us (163 MB, 24 us at the copy rate; 27 of the 60 in
-// the prefix); 24 with up to 256 behind one of 131,072 (275 MB, 41 us) 75 us.
+// prefix of 2,048 18 us; 64 with 100 to 2,000 behind one of 16,384 64 us (163 MB, 24 us at the copy
+// rate); 24 with up to 256 behind one of 131,072 (275 MB, 41 us) 87 us.
 #include "attend.cuh"
 
 namespace aircache {

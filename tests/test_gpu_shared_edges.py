@@ -1,11 +1,14 @@
-"""aircache_shared_decode where one half of the softmax has all of the weight, and in a workspace that other calls used.
+"""aircache_shared_decode where one half of the softmax has all of the weight, in a workspace that other calls used, and
+the bits that its weights hold.
 
-Tolerances: as in test_gpu_shared_decode.py."""
+Tolerances: as in test_gpu_shared_decode.py, and in the last test without what that one allows for weights of the
+prefixes' rows in bf16: they are a sum of two bf16, the second of what the first leaves, 2^-8 of 2^-8 of each weight."""
 import numpy as np
 import pytest
 import torch
 
 import paged_utils as P
+from oracle import paged as O
 from test_gpu_paged_attend import A, i32, queries  # noqa: F401
 from test_gpu_shared_decode import verify
 
@@ -67,3 +70,25 @@ def test_what_other_groups_left_in_the_workspace_has_no_say(A, last, mass):  # n
         alone = make(good, cu)
         A.shared_decode(alone)
         assert np.array_equal(P.bits(prob.out), P.bits(alone.out)) and np.array_equal(P.bits(prob.lse), P.bits(alone.lse))
+
+
+@pytest.mark.parametrize("int8,p_int8", [(False, False), (True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("q_scale", [0.2, 1.5])
+def test_weights_of_a_prefix_hold_the_bits_of_a_decode_step(A, q_scale, d, int8, p_int8):  # noqa: F811
+    # many rows of like weight and values of either sign: the output is small beside sum w |v|, and so is its own rounding
+    lens, prefix, cu = [0, 5, 70, 0, 300, 0], [3000, 140, 0], [0, 3, 5, 6]
+    cache = P.build(A, lens, 2, d, 16, seed=53, mass=False, order=False, int8=int8)
+    pre = P.build(A, prefix, 2, d, 64, seed=54, mass=False, order=False, int8=p_int8)
+    q = queries(6, 14, d, 53, q_scale / (10 if p_int8 else 1))
+    prob = A.SharedDecodeProblem(q, cache, pre, i32(cu), lse=True)
+    A.shared_decode(prob)
+    qd, c = q.double().cpu().numpy(), P.host(cache)
+    out, _, _, size, spread, far = O.shared_decode(qd, c, P.host(pre), cu, d ** -0.5)
+    dx = d * 2.0 ** -24 * size
+    own = 2.0 ** -11 if int8 else 2.0 ** -16
+    tol = (2 * dx[..., None] + 2.0 ** -16) * spread + 2.0 ** -16 * far + own * (spread - far) + 2.0 ** -8 * np.abs(out) + 1e-30
+    if int8:  # (f16 under a power of two: as in test_gpu_shared_decode.py)
+        tol += (c["lens"][:, None] * 127 * 2.0 ** -39 * O.largest_weighted_scale(qd, c, d ** -0.5))[..., None]
+    ratio = np.abs(prob.out.double().cpu().numpy() - out) / tol
+    assert np.all(ratio <= 1), f"worst {ratio.max():.2f}"
