@@ -27,16 +27,15 @@
 // What the loop is bound by, at 128-wide heads: 2,048 cycles of the tensor cores for a tile of keys and two streams, 1,190
 // of the exponentials (4.6 cycles to a warp's), and the chain of a stream: its softmax (1,350 cycles alone, 2,100 beside
 // the other's), half of P V, S and the waits between them.  A tile takes 3,000 cycles (tensor pipe 65 to 67 % active).
-// Steps that it took (1,000 tokens over 130,000 rows, 28 to 4 heads): one lane of a warp that issues both streams' MMAs
-// 1,634 us; operands in the warp's uniform registers 1,372; a warp to each stream, and turns, 1,299; a run's description
-// out of the softmax threads' registers, and 200 of those, 1,192 (1,210 to 1,440 by the machine).  Not kept: 16 softmax
-// warps with half a row each, which meet for every maximum (1,718 of 1,304 then); exponentials under the old reference
-// beside the search of the maximum (1,211 of 1,205); one softmax at a time (1,519 of 1,404); turns for the first half's
-// MMAs alone (1,370 of 1,205).
+// Why it is built so (1,000 tokens over 130,000 rows, 28 to 4 heads, each beside what it replaced on one machine): MMA
+// operands in a warp's uniform registers take a sixth less time than one lane's branch, a warp to each stream's MMAs and
+// turns 5 % less, a run's description out of the softmax threads' registers 8 %; sixteen softmax warps with half a row
+// each, which meet for every maximum, took a third more.
 //
 // int8 rows: eight more warps widen the codes, exactly, into the bf16 tiles.  The softmax threads multiply logits by the
-// keys' scales and weights by the values', which takes 64 logits at a time, twice (3,900 cycles to a tile); these rows are
-// bound by instructions (issue 47 %, tensor pipe 23 %).
+// keys' scales and weights by the values', which takes 64 logits at a time, twice (3,900 cycles to a tile).  Neither issue
+// slots (44 to 47 %), the tensor pipe (13 to 23 %) nor DRAM (7 to 12 %) are at a limit; the loop is 40 % of the time, and
+// how starts, ends of units and waits share the rest is not measured.
 //
 // Weights that meet V are rounded once to bf16 (at most 2^-8 of each weight, independent of one another; the error of an
 // output against 64 bits goes from 0.0017 of its norm, its own rounding to bf16, to 0.0023).  For the prefixes of a shared
@@ -48,13 +47,14 @@
 // A weight of 0 does not hide a NaN or an infinity in V from a matrix product.  A CTA that finds an output that is not
 // finite while its sum is walks over its units a second time: values that are not finite are cleared before the product
 // and added to the outputs of the rows that see them, and the weights are 2^-40 of what they were (sums of large values
-// may have passed fp32's range).  Ragged questions of which every sequence holds a NaN take 2.4 ms instead of 0.6; row by
-// row, a warp to an output row, they took 1,600 to 2,500 ms.
+// may have passed fp32's range; logits minus a reference near 40 are then rounded at 2^-19, weights under 2^-86 are 0).  A
+// row that sees none of the run's keys wants no second walk: its part is zeros.  Ragged questions of which every sequence
+// holds a NaN take 2.4 ms instead of 0.6; row by row, a warp to an output row, they took a thousand times that.
 //
-// Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 16 ragged questions of up to 1,024 tokens behind
-// 576 to 9,000 rows 574 to 630 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 4 x 256 tokens over 12,544 rows 152 to 162 us;
-// one token of each of 16 sequences over 16,384 rows 97 us (5.6 TB/s; the decode kernel 87); four drafts of eight chats
-// 15 us.
+// Measured (28 query and 4 KV heads of 128, bf16, calls back to back, on several machines): 16 ragged questions of up to
+// 1,024 tokens behind 576 to 9,000 rows 574 to 631 us (737 GFLOP, 1.2 to 1.3 PFLOP/s); 1,000 tokens over 130,000 rows 1,235
+// to 1,472 us; 4 x 256 tokens over 12,544 rows 152 to 164 us; one token of each of 16 sequences over 16,384 rows 97 us (5.6
+// TB/s; the decode kernel 87); four drafts of eight chats 14 to 15 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1370,7 +1370,7 @@ __global__ void __launch_bounds__(kArThreads) attend_range_kernel(const __grid_c
 // Joins the parts of the units that several CTAs shared, in their order: a warp to 32 rows and E columns of them, a row
 // to a lane, N parts in flight.
 constexpr int kAfThreads = 256;
-// As many CTAs as an SM holds at once (four: four drafts of eight chats 16.7 us instead of 14.7), or one, where the next
+// As many CTAs as an SM holds at once (four of them: four drafts of eight chats took 14 % more), or one, where the next
 // kernel is to start beside them.
 constexpr int kAfCtas = 2;
 template <int D, int E, int N>
@@ -1548,9 +1548,9 @@ int launch_at(const aircache_paged_attend_problem* p, const AttendPlan& pl, cons
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, paged_attend_kernel<D, Q8, FINE>, qm, km, vm, a) != cudaSuccess) return AIRCACHE_ERR_CUDA;
   // Few units (at most half as many as CTAs) have many parts each, of which many are in flight; with more, few parts, it is
-  // the pieces of work that are many, and larger.  (4 x 256 tokens over 12,544 rows, 128 units: 156 us with 8 columns and
-  // 8 parts, 152 with 16 and 3; four drafts of eight chats, 32 units: 14.7 and 15.6; 24 chats behind a prefix of
-  // 131,072, 4 units: 75 and 79)
+  // the pieces of work that are many, and larger.  (4 x 256 tokens over 12,544 rows, 128 units: 8 columns and 8 parts take 3 %
+  // more than 16 and 3; four drafts of eight chats, 32 units: 6 % less; 24 chats behind a prefix of 131,072, 4 units: 5 %
+  // less)
   const bool many = 2 * (int64_t)pl.slots * pl.pages.h_kv > pl.grid;
   const auto join = many ? &attend_finish_kernel<D, 16, 3> : &attend_finish_kernel<D, 8, 8>;
   return launch_pdl(join, dim3(a.part.out ? pl.grid : pl.grid * kAfCtas), dim3(kAfThreads), 0, s, a) == cudaSuccess

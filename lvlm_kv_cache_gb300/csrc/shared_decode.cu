@@ -7,9 +7,10 @@
 // every row again for each sequence), whose fp32 results the decode step over the own rows (paged_decode.cu) joins
 // where it writes its outputs, log-sum-exps and mass.
 //
-// Bound by HBM in the decode step, by launches and the chain of loads between four kernels in small calls.  The prefix
-// is not left to run beside the own rows: with half of the SMs to each, 64 sequences took up to a fifth longer, as
-// the decode step wants all of them.  Its kernels start early instead (programmatic launch), and only its joins wait.
+// Bound by HBM in the decode step, by launches and the chain of loads between its three or four kernels in small
+// calls.  The prefix is not left to run beside the own rows: with half of the SMs to each, 64 sequences took up to a
+// fifth longer, as the decode step wants all of them.  Its kernels start early instead (programmatic launch), and only
+// its joins wait.
 //
 // The weights of a prefix's rows hold 16 bits, as the decode step's own (a sum of two bf16; one alone would take 17, 60 and
 // 75 us below, and leave outputs 0.0019 to 0.0025 of their norm from the decode step's instead of 0.0002).
