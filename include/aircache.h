@@ -868,8 +868,9 @@ AIRCACHE_API int aircache_paged_attend(const aircache_paged_attend_problem* p, v
  * Requirements beside those of own (else AIRCACHE_ERR_INVALID_ARG): prefix of
  * own.pages's h_kv and head_dim; cu_seqs 4-byte aligned; own's q strides positive
  * (where there is more than one sequence or head); out, lse and mass_out apart from one
- * another, q, cu_seqs and the keys, values, scales, table and lengths of either cache
- * (mass_out may be the own rows' mass itself, as for aircache_paged_decode).  Workspace as for
+ * another, q, cu_seqs and the keys, values, scales, table and lengths of either cache, and
+ * with mass_out out and lse from the own rows' mass (mass_out may be that itself, as for
+ * aircache_paged_decode).  Workspace as for
  * aircache_paged_decode.  Two kernels before those of aircache_paged_decode.
  */
 typedef struct aircache_shared_decode_problem {

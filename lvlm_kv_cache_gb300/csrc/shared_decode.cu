@@ -12,8 +12,8 @@
 // fifth longer, as the decode step wants all of them.  Its kernels start early instead (programmatic launch), and only
 // its joins wait.
 //
-// The weights of a prefix's rows hold 16 bits, as the decode step's own (a sum of two bf16; one alone would take 17, 60 and
-// 75 us below, and leave outputs 0.0019 to 0.0025 of their norm from the decode step's instead of 0.0002).
+// The weights of a prefix's rows hold 16 bits, as the decode step's own (a sum of two bf16; one alone would take 17, 61 and
+// 76 us below, and leave outputs 0.0019 to 0.0025 of their norm from a form that holds 24 bits instead of 0.0002).
 //
 // Measured (28 query and 4 KV heads of 128, bf16, calls back to back): 8 sequences with up to 64 own rows behind one
 // prefix of 2,048 18 us; 64 with 100 to 2,000 behind one of 16,384 64 us (163 MB, 24 us at the copy
