@@ -550,9 +550,10 @@ AIRCACHE_API int aircache_quantize_int8(const aircache_quant_problem* p, int32_t
  * Attention does not depend on the order of the rows, and keys are stored
  * rotated, so no other operation needs their positions.
  *
- * Two sequences may share pages (a common prefix) as long as only
- * aircache_paged_decode without mass_out reads them; a page that a call writes
- * to (appended rows, mass, eviction) belongs to one sequence.
+ * Two sequences may share pages (a common prefix) as long as calls only read them
+ * (aircache_paged_decode without mass_out, aircache_paged_attend, the prefixes of
+ * aircache_shared_decode); a page that a call writes to (appended rows, mass, eviction)
+ * belongs to one sequence.
  * Requirements (else AIRCACHE_ERR_INVALID_ARG): 0 <= num_seqs <= 65535,
  * head_dim 64 or 128, kv_dtype AIRCACHE_BF16 or AIRCACHE_INT8 (with both
  * scales), page_rows a multiple of 16 in 16..4096, max_pages >= 1 with
