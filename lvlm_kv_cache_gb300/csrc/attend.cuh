@@ -10,6 +10,7 @@ namespace aircache {
 
 // Results kept in fp32 for a later join, of [token][query head]: the output [..][head_dim], and the log-sum-exp in
 // base 2 (-inf: the token saw no row, and its output is 0).
+// Their weights meet V in 16 bits, as those of the decode step that joins them.
 struct AttendPart {
   float* out;
   float* lse2;
